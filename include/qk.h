@@ -68,9 +68,13 @@ typedef enum {
     QK_ERR_TIMEOUT = 6,     /* a bounded device wait ran out (from qk_device_error)     */
     QK_ERR_WORKSPACE = 7,   /* workspace NULL, misaligned or smaller than required      */
     QK_ERR_TOO_LARGE = 8,   /* a size exceeds what the kernels support (see each call)  */
-    QK_ERR_BAD_INDEX = 9    /* an index read from device memory was out of range        */
+    QK_ERR_BAD_INDEX = 9,   /* an index read from device memory was out of range        */
                             /* (from qk_device_error; see qmatvec_experts_*)             */
+    QK_ERR_TYPE = 10        /* an element type is none of qk_dtype                       */
 } qk_status;
+
+/* Element types of the attention operators' queries, keys, values and outputs. */
+typedef enum { QK_F32 = 0, QK_F16 = 1, QK_BF16 = 2 } qk_dtype;
 
 #define QK_MAX_BATCH 8
 
@@ -291,6 +295,176 @@ size_t qgemm_q4_k_workspace_bytes(int64_t M, int64_t N, int64_t K);
 #define QK_NOALLOC_SCRATCH_BYTES (8u << 20)
 int qgemm_q4_k_noalloc(const void *w, int64_t row_offset, int64_t N, int64_t K, const float *x, int64_t M,
                        float *y, int64_t ldy, qk_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Attention operators: what a decode step or a prompt chunk does between its
+ * QKV product and its output product (the rope and attention steps of the
+ * decode loop, nurllama 0.18.1 API reference, kernels.nu `lk_rope`,
+ * `lk_attn`; QK-norm, rotation and cache store in one kernel and split
+ * decode attention, loom-port-llm SKILL.md, "Kernel inventory").  The
+ * key/value cache is held in 4 bits.
+ *
+ * Rotation table: fp32 [n_pos][rot/2][2], (cos, sin) of each position's
+ * angles; qk_rope_table fills one.  rot (even, <= head_dim) channels at the
+ * start of a head rotate, the others pass.  Pair i of a head is channels
+ * (i, i + rot/2), or (2i, 2i + 1) with interleaved != 0 (the two layouts of
+ * nurllama's `rope_neox` and `rope`), and (a, b) becomes
+ * (a*cos - b*sin, a*sin + b*cos).  rot == 0: no rotation (table may be NULL).
+ *
+ * Norm: n_j = x_j * weight_j / sqrt(mean_j(x_j^2) + eps) over a head's
+ * channels, before the rotation; weight NULL: no norm.
+ *
+ * The arithmetic is fp32 whatever the element types, with one rounding to
+ * the output's type.
+ */
+
+/*
+ * Fills table[p][i] = amplitude * (cos, sin)(p * f_i) for p < n_pos,
+ * i < rot/2.  f_i is the angle of one position:
+ *   e_i = base^(-2i/rot) / freq_factors[i]   (freq_factors NULL: 1)
+ *   f_i = e_i * freq_scale                   where orig_ctx == 0, else
+ *   f_i = e_i * (freq_scale * (1 - m_i) + m_i),
+ *   m_i = 1 - clamp((i - lo) / max(hi - lo, 0.001), 0, 1),
+ *   lo = max(0, floor(dim(beta_fast))), hi = min(rot - 1, ceil(dim(beta_slow))),
+ *   dim(t) = rot * ln(orig_ctx / (2*pi*t)) / (2 * ln(base)):
+ * position interpolation (freq_scale = 1/s), per-frequency factors (the
+ * rope_freqs tensor of GGUF files) and the ramp between interpolated and
+ * kept frequencies of Peng et al., "YaRN", 2023 (its attention temperature
+ * goes into `amplitude`).  Angles are formed and reduced in 64 bits, so a
+ * table of any length is within 4e-7 * amplitude of the exact values.
+ *   table         device, 8-byte aligned; freq_factors device fp32 [rot/2] or NULL.
+ * QK_ERR_BAD_DIM: n_pos or rot <= 0, rot odd, base <= 1, freq_scale <= 0,
+ * orig_ctx < 0, or (with orig_ctx > 0) a beta <= 0.
+ */
+int qk_rope_table(float *table, int64_t n_pos, int rot, double base, double freq_scale, const float *freq_factors,
+                  int64_t orig_ctx, double beta_fast, double beta_slow, double amplitude, qk_stream_t stream);
+
+/*
+ * Norm and rotation of T rows of n_q_heads query heads followed by n_k_heads
+ * key heads of head_dim channels (as the QKV product writes them), in one
+ * pass: query heads use q_weight, key heads k_weight.
+ *   x, y        device, element types x_type / y_type, aligned to their
+ *               element; rows ldx / ldy elements apart (0: heads * head_dim).
+ *               y may be x (with the same stride and type).
+ *   head_dim    even, 2..512;  n_q_heads + n_k_heads >= 1.
+ *   weights     device fp32 [head_dim], 4-byte aligned, or NULL.
+ *   positions   device int32 [T]; the rows of a token whose position is
+ *               outside [0, n_pos) become NaN and qk_device_error() reports
+ *               QK_ERR_BAD_INDEX.  Not read when rot == 0 (may be NULL).
+ * T == 0 is a call that does nothing.
+ */
+int qk_norm_rope(const void *x, int64_t ldx, int x_type, int n_q_heads, int n_k_heads, int head_dim,
+                 const float *q_weight, const float *k_weight, float eps, const float *table, int64_t n_pos, int rot,
+                 int interleaved, const int32_t *positions, int64_t T, void *y, int64_t ldy, int y_type,
+                 qk_stream_t stream);
+
+/*
+ * A paged key/value cache in 4 bits, owned by the caller.  The device buffer
+ * is [n_pages][n_kv_heads][page_tokens / 16] blocks of 18 * head_dim bytes,
+ * 16-byte aligned: QK_KV_Q4_BYTES in all.  Slot s is token s % page_tokens
+ * of page s / page_tokens.
+ *   head_dim     64, 96, 128 or 256;  page_tokens a multiple of 16, 16..1024.
+ * A value is d * (n - 8): the scale d is fp16(m / -8), m the value of largest
+ * magnitude of 32 neighbouring channels (the positive one of a tie; |d| is
+ * held to 65504), and the nibble n = clamp(floor(x / d + 8.5), 0, 15), 8
+ * where d is 0.  A group that holds a NaN or an infinity gets a NaN scale.
+ *
+ * Block (16 tokens of one head; G = head_dim/32 scale groups, Gp = 4 where G
+ * is a multiple of 4 and else G):
+ *   key nibbles    [G/Gp][row 16][c 4][Gp] 32-bit words: nibble i of a word is
+ *                  channel 32*group + 8*c + i; row 8h + 2a + b is token 4a + 2h + b
+ *   value nibbles  [G/Gp][u 2][r 8][c 4][Gp] 32-bit words: nibble 4b + j of a
+ *                  word is channel 32*group + 4*r + j of token 4c + 2u + b
+ *   key scales     [token 16][G] fp16;   value scales [token 16][G] fp16
+ * so that the words a thread reads are the operand fragments of the tensor
+ * cores' products over the block.
+ */
+typedef struct {
+    void *pages;
+    int64_t n_pages;
+    int n_kv_heads, head_dim, page_tokens;
+} qk_kv_cache_q4;
+#define QK_KV_Q4_BYTES(n_pages, n_kv_heads, page_tokens, head_dim) \
+    ((int64_t)(n_pages) * (n_kv_heads) * ((page_tokens) / 16) * 18 * (head_dim))
+
+/*
+ * Norm and rotation of T tokens' queries and keys as qk_norm_rope, with the
+ * keys and values stored into the cache: token t goes to slots[t].
+ *   q, k, v     device rows of n_q_heads, cache->n_kv_heads and
+ *               cache->n_kv_heads heads, all of element type `type`, ldq, ldk,
+ *               ldv elements apart (0: packed); q may be NULL (then q_out is
+ *               not written).
+ *   slots       device int64 [T], 8-byte aligned.  A negative slot stores
+ *               nothing (a padded token; its q_out row is written).  A slot
+ *               beyond the cache stores nothing and reports QK_ERR_BAD_INDEX.
+ *               Two tokens of a call in one slot: either may be left there.
+ *   positions   as qk_norm_rope; a bad one makes the token's q_out NaN and
+ *               its stored key NaN.
+ *   q_out       device rows of n_q_heads heads of type q_out_type; may be q
+ *               (with the same stride and type).
+ */
+int qk_kv_append_q4(const qk_kv_cache_q4 *cache, const void *q, int64_t ldq, int n_q_heads, const void *k, int64_t ldk,
+                    const void *v, int64_t ldv, int type, const float *q_weight, const float *k_weight, float eps,
+                    const float *table, int64_t n_pos, int rot, int interleaved, const int32_t *positions,
+                    const int64_t *slots, int64_t T, void *q_out, int64_t ldqo, int q_out_type, qk_stream_t stream);
+
+/*
+ * Reads slots back as values: k[t], v[t] (rows of n_kv_heads heads of type
+ * `type`, ldk / ldv elements apart, 0: packed) are what the cache holds at
+ * slots[t]; k or v may be NULL.  Rows of a negative slot become 0, of a slot
+ * beyond the cache NaN (QK_ERR_BAD_INDEX from qk_device_error()).
+ */
+int qk_kv_read_q4(const qk_kv_cache_q4 *cache, const int64_t *slots, int64_t T, void *k, int64_t ldk, void *v,
+                  int64_t ldv, int type, qk_stream_t stream);
+
+/*
+ * Attention of T query rows over the cache, grouped heads (query head h
+ * reads key/value head h / (n_q_heads / n_kv_heads)):
+ *   out[t][h] = sum_j p_j * V_j,  p = softmax_j(scale * q[t][h] . K_j)
+ * over the keys j of the row's sequence with j <= pos, j < lens[b] and, with
+ * window > 0, j > pos - window; pos = lens[b] - n_b + i for query i of the
+ * sequence's n_b.  A row that sees no key is 0.
+ *   q, out      device rows of n_q_heads heads, ldq / ldo elements apart (0:
+ *               packed), element types q_type / out_type.
+ *   page_table  device int32 [B][ld_pages]: page page_table[b][j / page_tokens]
+ *               holds key j; max_pages (<= ld_pages; 0: ld_pages) entries a
+ *               row are readable, those past a sequence's length are not read.
+ *   lens        device int32 [B], the sequences' lengths, the new tokens'
+ *               keys among them; 0 is a sequence with no keys.
+ *   q_start     device int32 [B + 1]: sequence b's queries are rows
+ *               [q_start[b], q_start[b+1]), at most max_q of them.  NULL: each
+ *               has max_q, and T == B * max_q.
+ *   max_len     an upper bound of lens that the call's split of the keys is
+ *               sized by (0: max_pages * page_tokens).  Longer sequences are
+ *               computed all the same.
+ *   scale       finite.
+ *   workspace   NULL, or device scratch, 256-byte aligned, that was filled
+ *               with zeros once before its first use; every call leaves its
+ *               counters zero again.  Calls that may overlap on the GPU need
+ *               one each.  With one, the keys of long sequences are split
+ *               over more thread blocks, as far as workspace_bytes allow;
+ *               qk_attn_q4_workspace_bytes() gives what the call can use.
+ * A page outside [0, n_pages), a length above max_pages * page_tokens or
+ * below 0, or a q_start out of order, beyond T or with more than max_q rows
+ * reports QK_ERR_BAD_INDEX from qk_device_error() without any access out of
+ * range.  A bad page makes the sequence's rows that see its keys NaN (and
+ * may make its other rows NaN); a bad length or q_start makes every row of
+ * the sequence NaN, as far as q_start names rows inside [0, T).
+ * Accuracy: with fp32 queries every product is formed from the exact 4-bit
+ * values and 22-bit query and probability pieces and summed in fp32; with
+ * 16-bit queries probabilities (and for chunks also the cache's values) are
+ * rounded to fp16 (2^-11), sums and the softmax are fp32.
+ * T == 0 or B == 0 is a call that does nothing.
+ */
+int qk_attn_q4(const qk_kv_cache_q4 *cache, const void *q, int64_t ldq, int q_type, int n_q_heads,
+               const int32_t *page_table, int64_t ld_pages, int64_t max_pages, const int32_t *lens,
+               const int32_t *q_start, int64_t B, int64_t T, int64_t max_q, int64_t max_len, float scale,
+               int64_t window, void *out, int64_t ldo, int out_type, void *workspace, size_t workspace_bytes,
+               qk_stream_t stream);
+
+/* Workspace bytes that a qk_attn_q4 call of these sizes can make use of. */
+size_t qk_attn_q4_workspace_bytes(int64_t B, int n_q_heads, int n_kv_heads, int head_dim, int64_t max_q,
+                                  int64_t max_len);
 
 /*
  * Bytes of one row of a tensor with K columns: ceil(K/32)*34 (Q8_0),

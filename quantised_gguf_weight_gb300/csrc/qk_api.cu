@@ -132,6 +132,7 @@ int gemv_entry(int fmt, const void *w, int64_t row_offset, int64_t rows, int64_t
 namespace qk {
 int *library_error_word() { return error_word_ptr(); }
 uint64_t library_wait_limit_ns() { return g_wait_limit_ns.load(); }
+bool library_programmatic() { return g_programmatic.load() != 0; }
 bool strict_blocks_reject(int fmt, int64_t K)
 {
     const int64_t qk = fmt == kFmtQ80 ? 32 : 256;
@@ -353,6 +354,7 @@ const char *qk_status_string(int status)
     case QK_ERR_WORKSPACE: return "workspace missing, misaligned or too small";
     case QK_ERR_TOO_LARGE: return "size beyond what the kernels support";
     case QK_ERR_BAD_INDEX: return "an index read from device memory was out of range";
+    case QK_ERR_TYPE: return "unknown element type";
     default: return "unknown status";
     }
 }

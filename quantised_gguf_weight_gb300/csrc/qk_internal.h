@@ -5,6 +5,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include "../../include/qk.h"
+
 namespace qk {
 
 constexpr int kFmtQ80 = 0;
@@ -58,6 +60,8 @@ bool device_limits(int *sms, int *smem_optin);
 // The device error word of the current device and the bound of device waits.
 int *library_error_word();
 uint64_t library_wait_limit_ns();
+// Programmatic dependent launch is on (qk_set_programmatic_launch).
+bool library_programmatic();
 // Strict-blocks mode: true when it is on and K is not a whole number of the
 // format's blocks (32 columns for Q8_0, 256 for Q4_K and Q6_K).
 bool strict_blocks_reject(int fmt, int64_t K);
@@ -82,5 +86,8 @@ cudaError_t gemm_launch(int fmt, const uint8_t *w_rows, int64_t N, int64_t K, co
 cudaError_t gemm_q4k_launch(const uint8_t *w_rows, int64_t N, int64_t K, const float *x, int64_t M, float *y,
                             int64_t ldy, void *workspace, cudaStream_t st, int *err, uint64_t wait_ns, int skip_chunk,
                             bool *encode_failed);
+
+// The argument checks of a 4-bit key/value cache (a qk_status).
+int kv4_check_cache(const qk_kv_cache_q4 *c);
 
 }  // namespace qk

@@ -1,0 +1,571 @@
+// qk_rope.cu -- per-head RMS norm and position rotation, the append of keys
+// and values to the 4-bit cache with both on the way, the cache's read-back,
+// and the rotation tables.
+//
+// One warp takes one head of one token: lane l holds channels 4l..4l+3 (and
+// the same 128 further on, for larger heads).  The norm is a warp sum, the
+// partner of a half-layout pair is read back from the warp's row in shared
+// memory, and a 4-bit group of 32 channels is 8 neighbouring lanes, so its
+// scale is three shuffles.  All of it is bound by the bytes of the rows.
+#include <cfloat>
+#include <cmath>
+
+#include "qk_device.cuh"
+#include "qk_internal.h"
+#include "qk_kv4.cuh"
+
+namespace qk {
+namespace {
+
+constexpr int kRowWarps = 8;
+
+struct RowsArgs {
+    // heads [0, n_q) from q with q_weight, the next n_k from k with k_weight, the last n_v from v (append only)
+    const void *q, *k, *v;
+    void *q_out, *k_out;       // k_out: null in the append
+    int64_t ldq, ldk, ldv, ldqo, ldko;
+    int in_type, out_type;
+    int n_q, n_k, n_v, D;
+    const float *q_weight, *k_weight;
+    float eps;
+    const float2 *table;
+    int64_t n_pos;
+    int rot, interleaved;
+    const int32_t *positions;
+    int64_t T;
+    bool vec_in, vec_out;      // four elements at a time: rows and bases allow it
+    // append
+    uint8_t *pages;
+    int64_t n_slots;
+    int page_tokens;
+    const int64_t *slots;
+    int *err;
+};
+
+__device__ __forceinline__ void load4(const void *p, int64_t i, int type, float (&x)[4])
+{
+    if (type == QK_F32) {
+        const float4 f = *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
+        x[0] = f.x, x[1] = f.y, x[2] = f.z, x[3] = f.w;
+        return;
+    }
+    const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p) + i);
+    if (type == QK_F16) {
+        const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&w.x));
+        const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&w.y));
+        x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y;
+    } else {
+        x[0] = __uint_as_float(w.x << 16), x[1] = __uint_as_float(w.x & 0xFFFF0000u);
+        x[2] = __uint_as_float(w.y << 16), x[3] = __uint_as_float(w.y & 0xFFFF0000u);
+    }
+}
+
+__device__ __forceinline__ void store4(void *p, int64_t i, int type, const float (&x)[4])
+{
+    if (type == QK_F32) {
+        *reinterpret_cast<float4 *>(static_cast<float *>(p) + i) = make_float4(x[0], x[1], x[2], x[3]);
+        return;
+    }
+    uint2 w;
+    if (type == QK_F16) {
+        const __half2 a = __floats2half2_rn(x[0], x[1]), b = __floats2half2_rn(x[2], x[3]);
+        w.x = *reinterpret_cast<const uint32_t *>(&a), w.y = *reinterpret_cast<const uint32_t *>(&b);
+    } else {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
+        w.x = *reinterpret_cast<const uint32_t *>(&a), w.y = *reinterpret_cast<const uint32_t *>(&b);
+    }
+    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p) + i) = w;
+}
+
+// The row's norm and rotation in place.  Each product and sum is rounded on
+// its own (no contraction), so a 4-bit group's nibbles do not depend on how
+// the compiler fuses them.
+template <int NV>
+__device__ __forceinline__ void norm_rotate(float (&x)[NV][4], const RowsArgs &a, const float *weight, bool bad,
+                                            const float2 *cs, float *row, int lane)
+{
+    const int D = a.D;
+    if (weight) {
+        float s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s = fmaf(x[i][e], x[i][e], s);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+        const float r = __frsqrt_rn(__fadd_rn(__fdiv_rn(s, static_cast<float>(D)), a.eps));
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int ch = (i * 32 + lane) * 4 + e;
+                if (ch < D) x[i][e] = __fmul_rn(__fmul_rn(x[i][e], r), weight[ch]);
+            }
+    }
+    if (a.rot > 0 && !bad) {
+        if (a.interleaved) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; e += 2) {
+                    const int ch = (i * 32 + lane) * 4 + e;
+                    if (ch < a.rot) {
+                        const float2 t = cs[ch >> 1];
+                        const float u = x[i][e], w = x[i][e + 1];
+                        x[i][e] = __fsub_rn(__fmul_rn(u, t.x), __fmul_rn(w, t.y));
+                        x[i][e + 1] = __fadd_rn(__fmul_rn(u, t.y), __fmul_rn(w, t.x));
+                    }
+                }
+        } else {
+            const int half = a.rot >> 1;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int ch = (i * 32 + lane) * 4;
+                if (ch < a.rot) *reinterpret_cast<float4 *>(row + ch) = make_float4(x[i][0], x[i][1], x[i][2], x[i][3]);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int ch = (i * 32 + lane) * 4 + e;
+                    if (ch < half) {
+                        const float2 t = cs[ch];
+                        x[i][e] = __fsub_rn(__fmul_rn(x[i][e], t.x), __fmul_rn(row[ch + half], t.y));
+                    } else if (ch < a.rot) {
+                        const float2 t = cs[ch - half];
+                        x[i][e] = __fadd_rn(__fmul_rn(row[ch - half], t.y), __fmul_rn(x[i][e], t.x));
+                    }
+                }
+            __syncwarp();
+        }
+    }
+    if (bad)
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[i][e] = __int_as_float(0x7FC00000);
+}
+
+// Four channels of a head to the cache: the group's scale over its 8 lanes,
+// then the lane's four nibbles as two bytes.
+__device__ __forceinline__ void store_nibbles(uint8_t *block, int D, int t, int ch, bool active, const float (&x)[4],
+                                              bool is_key, int lane)
+{
+    float hi = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+    float lo = fminf(fminf(x[0], x[1]), fminf(x[2], x[3]));
+    bool odd = false;   // a NaN or an infinity
+#pragma unroll
+    for (int e = 0; e < 4; ++e) odd |= !(fabsf(x[e]) <= FLT_MAX);
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) {
+        hi = fmaxf(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, o));
+        lo = fminf(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
+    }
+    const uint32_t odd_lanes = __ballot_sync(0xFFFFFFFFu, odd);
+    if (!active) return;
+    const bool group_odd = (odd_lanes >> (lane & 24)) & 0xFFu;
+    const float m = hi >= -lo ? hi : lo;
+    const float want = fminf(fmaxf(m * -0.125f, -65504.0f), 65504.0f);
+    const __half dh = group_odd ? __ushort_as_half(0x7FFF) : __float2half_rn(want);
+    const float d = __half2float(dh);
+    uint32_t bits = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        float n = 8.0f;
+        if (d != 0.0f && !group_odd)
+            n = fminf(fmaxf(floorf(__fadd_rn(__fdiv_rn(x[e], d), 8.5f)), 0.0f), 15.0f);
+        bits |= static_cast<uint32_t>(n) << (4 * e);
+    }
+    const Kv4Place p = is_key ? kv4_key_place(D, t, ch) : kv4_value_place(D, t, ch);
+    *reinterpret_cast<uint16_t *>(block + p.byte + (p.nibble >> 1)) = static_cast<uint16_t>(bits);
+    if ((lane & 7) == 0) {
+        const int s = is_key ? kv4_key_scale(D, t, ch >> 5) : kv4_value_scale(D, t, ch >> 5);
+        *reinterpret_cast<__half *>(block + s) = dh;
+    }
+}
+
+template <int NV, bool APPEND>
+__global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const RowsArgs a)
+{
+    __shared__ __align__(16) float rows[kRowWarps][NV * 128];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int heads = a.n_q + a.n_k + a.n_v;
+    const int64_t item = static_cast<int64_t>(blockIdx.x) * kRowWarps + warp;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (item >= a.T * heads) return;
+    const int64_t t = item / heads;
+    const int h = static_cast<int>(item - t * heads);
+    const bool is_q = h < a.n_q, is_v = h >= a.n_q + a.n_k;
+    const int hk = is_q ? h : (is_v ? h - a.n_q - a.n_k : h - a.n_q);
+    const void *src = is_q ? a.q : (is_v ? a.v : a.k);
+    const int64_t at = t * (is_q ? a.ldq : (is_v ? a.ldv : a.ldk)) + static_cast<int64_t>(hk) * a.D;
+
+    bool bad = false;
+    const float2 *cs = a.table;
+    if (a.rot > 0 && !is_v) {
+        const int32_t p = a.positions[t];
+        bad = p < 0 || p >= a.n_pos;
+        cs += bad ? 0 : static_cast<int64_t>(p) * (a.rot >> 1);
+        if (bad && lane == 0) record_error(a.err, kErrBadIndex);
+    }
+    float x[NV][4];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int ch = (i * 32 + lane) * 4;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[i][e] = 0.0f;
+        if (a.vec_in) {
+            if (ch < a.D) load4(src, at + ch, a.in_type, x[i]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (ch + e < a.D) x[i][e] = load_as_float(src, at + ch + e, a.in_type);
+        }
+    }
+    if (!is_v) norm_rotate<NV>(x, a, is_q ? a.q_weight : a.k_weight, bad, cs, rows[warp], lane);
+    if (APPEND && !is_q) {
+        const int64_t slot = a.slots[t];
+        if (slot < 0) return;
+        if (slot >= a.n_slots) {
+            if (lane == 0) record_error(a.err, kErrBadIndex);
+            return;
+        }
+        const int64_t page = slot / a.page_tokens;
+        const int off = static_cast<int>(slot - page * a.page_tokens);
+        uint8_t *block = a.pages + ((page * a.n_k + hk) * (a.page_tokens / kBlockTokens) + off / kBlockTokens) *
+                                       static_cast<int64_t>(18 * a.D);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int ch = (i * 32 + lane) * 4;
+            store_nibbles(block, a.D, off % kBlockTokens, ch, ch < a.D, x[i], !is_v, lane);
+        }
+        return;
+    }
+    void *dst = is_q ? a.q_out : a.k_out;
+    const int64_t to = t * (is_q ? a.ldqo : a.ldko) + static_cast<int64_t>(hk) * a.D;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int ch = (i * 32 + lane) * 4;
+        if (a.vec_out) {
+            if (ch < a.D) store4(dst, to + ch, a.out_type, x[i]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (ch + e < a.D) store_float_as(dst, to + ch + e, a.out_type, x[i][e]);
+        }
+    }
+}
+
+struct ReadArgs {
+    const uint8_t *pages;
+    int64_t n_slots;
+    int n_kv, D, page_tokens;
+    const int64_t *slots;
+    int64_t T;
+    void *k, *v;
+    int64_t ldk, ldv;
+    int type;
+    bool vec;
+    int *err;
+};
+
+// One warp reads one head of one slot, keys or values.
+__global__ void __launch_bounds__(kRowWarps * 32) read_kernel(const ReadArgs a)
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int lane = threadIdx.x & 31;
+    const int heads = a.n_kv * ((a.k ? 1 : 0) + (a.v ? 1 : 0));
+    const int64_t item = static_cast<int64_t>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (item >= a.T * heads) return;
+    const int64_t t = item / heads;
+    int h = static_cast<int>(item - t * heads);
+    const bool is_key = a.k && h < a.n_kv;
+    if (a.k && !is_key) h -= a.n_kv;
+    void *dst = is_key ? a.k : a.v;
+    const int64_t to = t * (is_key ? a.ldk : a.ldv) + static_cast<int64_t>(h) * a.D;
+    const int64_t slot = a.slots[t];
+    const bool inside = slot >= 0 && slot < a.n_slots;
+    if (slot >= a.n_slots && lane == 0) record_error(a.err, kErrBadIndex);
+    const int64_t page = inside ? slot / a.page_tokens : 0;
+    const int off = inside ? static_cast<int>(slot - page * a.page_tokens) : 0;
+    const uint8_t *block = a.pages + ((page * a.n_kv + h) * (a.page_tokens / kBlockTokens) + off / kBlockTokens) *
+                                         static_cast<int64_t>(18 * a.D);
+    for (int ch = lane * 4; ch < a.D; ch += 128) {
+        float x[4];
+        if (inside) {
+            const int tk = off % kBlockTokens;
+            const Kv4Place p = is_key ? kv4_key_place(a.D, tk, ch) : kv4_value_place(a.D, tk, ch);
+            const uint32_t n = *reinterpret_cast<const uint16_t *>(block + p.byte + (p.nibble >> 1));
+            const int s = is_key ? kv4_key_scale(a.D, tk, ch >> 5) : kv4_value_scale(a.D, tk, ch >> 5);
+            const float d = __half2float(*reinterpret_cast<const __half *>(block + s));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = d * (static_cast<float>((n >> (4 * e)) & 15u) - 8.0f);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = slot < 0 ? 0.0f : __int_as_float(0x7FC00000);
+        }
+        if (a.vec) store4(dst, to + ch, a.type, x);
+        else
+#pragma unroll
+            for (int e = 0; e < 4; ++e) store_float_as(dst, to + ch + e, a.type, x[e]);
+    }
+}
+
+struct TableArgs {
+    float2 *table;
+    int64_t n_pos;
+    int half;
+    double base, freq_scale, lo, hi, amplitude;
+    bool ramp;
+    const float *factors;
+};
+
+// Angles p * f_i in 64 bits, reduced to [-pi, pi]; sine and cosine of the
+// fp32 part by CUDA's sincosf, the rest of the angle by the first-order term.
+__global__ void __launch_bounds__(256) table_kernel(const TableArgs a)
+{
+    extern __shared__ double freq[];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    for (int i = threadIdx.x; i < a.half; i += blockDim.x) {
+        double e = pow(a.base, -static_cast<double>(i) / a.half);
+        if (a.factors) e /= static_cast<double>(a.factors[i]);
+        double s = a.freq_scale;
+        if (a.ramp) {
+            const double m = 1.0 - fmin(fmax((i - a.lo) / fmax(a.hi - a.lo, 0.001), 0.0), 1.0);
+            s = s * (1.0 - m) + m;
+        }
+        freq[i] = e * s;
+    }
+    __syncthreads();
+    const int64_t n = a.n_pos * a.half;
+    const double two_pi = 6.283185307179586476925;
+    for (int64_t j = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; j < n;
+         j += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+        const int64_t p = j / a.half;
+        const double angle = static_cast<double>(p) * freq[j - p * a.half];
+        const double r = angle - rint(angle * (1.0 / two_pi)) * two_pi;
+        const float rh = static_cast<float>(r), rl = static_cast<float>(r - rh);
+        float s, c;
+        sincosf(rh, &s, &c);
+        const float amp = static_cast<float>(a.amplitude);
+        a.table[j] = make_float2(amp * fmaf(-rl, s, c), amp * fmaf(rl, c, s));
+    }
+}
+
+bool multiple(const void *p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+// Four elements at a time are possible: heads, rows and base on 4-element boundaries.
+bool vec_ok(const void *p, int64_t ld, int D, int type)
+{
+    return D % 4 == 0 && ld % 4 == 0 && multiple(p, type == QK_F32 ? 16 : 8);
+}
+
+int64_t blocks_for(int64_t items) { return (items + kRowWarps - 1) / kRowWarps; }
+
+template <class Args>
+cudaError_t launch(void (*kern)(const Args), int64_t grid, int threads, size_t smem, cudaStream_t st, const Args &a)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at = {};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = library_programmatic() ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kern, a);
+}
+
+template <bool APPEND>
+cudaError_t launch_rows(const RowsArgs &a, cudaStream_t st)
+{
+    const int64_t grid = blocks_for(a.T * (a.n_q + a.n_k + a.n_v));
+    if (a.D <= 128) return launch(rows_kernel<1, APPEND>, grid, kRowWarps * 32, 0, st, a);
+    if (a.D <= 256) return launch(rows_kernel<2, APPEND>, grid, kRowWarps * 32, 0, st, a);
+    if constexpr (!APPEND) return launch(rows_kernel<4, APPEND>, grid, kRowWarps * 32, 0, st, a);
+    return cudaErrorInvalidValue;
+}
+
+bool type_ok(int t) { return t == QK_F32 || t == QK_F16 || t == QK_BF16; }
+int size_of(int t) { return t == QK_F32 ? 4 : 2; }
+
+// Rotation arguments shared by the entry points.
+int check_rotation(const float *table, int64_t n_pos, int rot, int D, const int32_t *positions)
+{
+    if (rot < 0 || rot % 2 || rot > D) return QK_ERR_BAD_DIM;
+    if (rot > 0) {
+        if (!table || !positions) return QK_ERR_NULL;
+        if (n_pos <= 0) return QK_ERR_BAD_DIM;
+        if (!multiple(table, 8) || !multiple(positions, 4)) return QK_ERR_ALIGN;
+    }
+    return QK_OK;
+}
+
+}  // namespace
+
+int kv4_check_cache(const qk_kv_cache_q4 *c)
+{
+    if (!c || !c->pages) return QK_ERR_NULL;
+    if (c->n_pages <= 0 || c->n_kv_heads <= 0 || c->page_tokens <= 0 || c->page_tokens % kBlockTokens ||
+        c->page_tokens > 1024)
+        return QK_ERR_BAD_DIM;
+    if (c->head_dim != 64 && c->head_dim != 96 && c->head_dim != 128 && c->head_dim != 256) return QK_ERR_BAD_DIM;
+    if (c->n_kv_heads > 65535 || c->n_pages > INT32_MAX) return QK_ERR_TOO_LARGE;
+    if (!multiple(c->pages, 16)) return QK_ERR_ALIGN;
+    return QK_OK;
+}
+
+}  // namespace qk
+
+using namespace qk;
+
+extern "C" {
+
+int qk_rope_table(float *table, int64_t n_pos, int rot, double base, double freq_scale, const float *freq_factors,
+                  int64_t orig_ctx, double beta_fast, double beta_slow, double amplitude, qk_stream_t stream)
+{
+    if (!table) return QK_ERR_NULL;
+    if (n_pos <= 0 || rot <= 0 || rot % 2 || !(base > 1.0) || !(freq_scale > 0.0) || orig_ctx < 0) return QK_ERR_BAD_DIM;
+    if (orig_ctx > 0 && (!(beta_fast > 0.0) || !(beta_slow > 0.0))) return QK_ERR_BAD_DIM;
+    if (rot > 4096 || n_pos > INT64_MAX / 65536) return QK_ERR_TOO_LARGE;
+    if (!multiple(table, 8) || (freq_factors && !multiple(freq_factors, 4))) return QK_ERR_ALIGN;
+    TableArgs a{};
+    a.table = reinterpret_cast<float2 *>(table);
+    a.n_pos = n_pos;
+    a.half = rot / 2;
+    a.base = base, a.freq_scale = freq_scale, a.amplitude = amplitude;
+    a.factors = freq_factors;
+    a.ramp = orig_ctx > 0;
+    if (a.ramp) {
+        const auto dim = [&](double turns) {
+            return rot * std::log(static_cast<double>(orig_ctx) / (turns * 6.283185307179586476925)) /
+                   (2.0 * std::log(base));
+        };
+        a.lo = std::fmax(0.0, std::floor(dim(beta_fast)));
+        a.hi = std::fmin(rot - 1.0, std::ceil(dim(beta_slow)));
+    }
+    const int64_t want = (n_pos * a.half + 1023) / 1024;
+    return launch(table_kernel, want < 1216 ? want : 1216, 256, sizeof(double) * a.half,
+                  reinterpret_cast<cudaStream_t>(stream), a) == cudaSuccess ? QK_OK : QK_ERR_CUDA;
+}
+
+int qk_norm_rope(const void *x, int64_t ldx, int x_type, int n_q_heads, int n_k_heads, int head_dim,
+                 const float *q_weight, const float *k_weight, float eps, const float *table, int64_t n_pos, int rot,
+                 int interleaved, const int32_t *positions, int64_t T, void *y, int64_t ldy, int y_type,
+                 qk_stream_t stream)
+{
+    if (!type_ok(x_type) || !type_ok(y_type)) return QK_ERR_TYPE;
+    if (n_q_heads < 0 || n_k_heads < 0 || n_q_heads + static_cast<int64_t>(n_k_heads) < 1 || head_dim < 2 ||
+        head_dim > 512 || head_dim % 2 || T < 0)
+        return QK_ERR_BAD_DIM;
+    const int64_t heads = static_cast<int64_t>(n_q_heads) + n_k_heads;
+    if (heads > 65535) return QK_ERR_TOO_LARGE;
+    if (ldx == 0) ldx = heads * head_dim;
+    if (ldy == 0) ldy = heads * head_dim;
+    if (ldx < heads * head_dim || ldy < heads * head_dim) return QK_ERR_BAD_DIM;
+    if (x == y && x && (x_type != y_type || ldx != ldy)) return QK_ERR_BAD_DIM;
+    if (T == 0) return QK_OK;
+    if (!x || !y) return QK_ERR_NULL;
+    const int st = check_rotation(table, n_pos, rot, head_dim, positions);
+    if (st != QK_OK) return st;
+    if (!multiple(x, size_of(x_type)) || !multiple(y, size_of(y_type)) || !multiple(q_weight, 4) ||
+        !multiple(k_weight, 4))
+        return QK_ERR_ALIGN;
+    if (T > (static_cast<int64_t>(INT32_MAX) * kRowWarps) / heads) return QK_ERR_TOO_LARGE;
+    RowsArgs a{};
+    a.q = x, a.q_out = y;
+    a.k = static_cast<const char *>(x) + static_cast<int64_t>(n_q_heads) * head_dim * size_of(x_type);
+    a.k_out = static_cast<char *>(y) + static_cast<int64_t>(n_q_heads) * head_dim * size_of(y_type);
+    a.ldq = a.ldk = ldx, a.ldqo = a.ldko = ldy;
+    a.in_type = x_type, a.out_type = y_type;
+    a.n_q = n_q_heads, a.n_k = n_k_heads, a.D = head_dim;
+    a.q_weight = q_weight, a.k_weight = k_weight, a.eps = eps;
+    a.table = reinterpret_cast<const float2 *>(table), a.n_pos = n_pos, a.rot = rot, a.interleaved = interleaved;
+    a.positions = positions, a.T = T;
+    a.vec_in = vec_ok(x, ldx, head_dim, x_type), a.vec_out = vec_ok(y, ldy, head_dim, y_type);
+    a.err = library_error_word();
+    if (!a.err) return QK_ERR_CUDA;
+    return launch_rows<false>(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? QK_OK : QK_ERR_CUDA;
+}
+
+int qk_kv_append_q4(const qk_kv_cache_q4 *cache, const void *q, int64_t ldq, int n_q_heads, const void *k, int64_t ldk,
+                    const void *v, int64_t ldv, int type, const float *q_weight, const float *k_weight, float eps,
+                    const float *table, int64_t n_pos, int rot, int interleaved, const int32_t *positions,
+                    const int64_t *slots, int64_t T, void *q_out, int64_t ldqo, int q_out_type, qk_stream_t stream)
+{
+    int st = kv4_check_cache(cache);
+    if (st != QK_OK) return st;
+    if (!type_ok(type) || (q && !type_ok(q_out_type))) return QK_ERR_TYPE;
+    const int D = cache->head_dim, n_kv = cache->n_kv_heads;
+    if (!q) n_q_heads = 0;
+    if ((q && n_q_heads < 1) || T < 0) return QK_ERR_BAD_DIM;
+    if (n_q_heads > 65535) return QK_ERR_TOO_LARGE;
+    const int64_t wq = static_cast<int64_t>(n_q_heads) * D, wk = static_cast<int64_t>(n_kv) * D;
+    if (ldq == 0) ldq = wq;
+    if (ldqo == 0) ldqo = wq;
+    if (ldk == 0) ldk = wk;
+    if (ldv == 0) ldv = wk;
+    if (ldq < wq || ldqo < wq || ldk < wk || ldv < wk) return QK_ERR_BAD_DIM;
+    if (q && q == q_out && (type != q_out_type || ldq != ldqo)) return QK_ERR_BAD_DIM;
+    if (T == 0) return QK_OK;
+    if (!k || !v || !slots || (q && !q_out)) return QK_ERR_NULL;
+    st = check_rotation(table, n_pos, rot, D, positions);
+    if (st != QK_OK) return st;
+    if (!multiple(k, size_of(type)) || !multiple(v, size_of(type)) || !multiple(slots, 8) || !multiple(q_weight, 4) ||
+        !multiple(k_weight, 4) || (q && (!multiple(q, size_of(type)) || !multiple(q_out, size_of(q_out_type)))))
+        return QK_ERR_ALIGN;
+    const int64_t heads = static_cast<int64_t>(n_q_heads) + 2 * n_kv;
+    if (T > (static_cast<int64_t>(INT32_MAX) * kRowWarps) / heads) return QK_ERR_TOO_LARGE;
+    RowsArgs a{};
+    a.q = q, a.k = k, a.v = v, a.q_out = q_out;
+    a.ldq = ldq, a.ldk = ldk, a.ldv = ldv, a.ldqo = ldqo;
+    a.in_type = type, a.out_type = q_out_type;
+    a.n_q = n_q_heads, a.n_k = a.n_v = n_kv, a.D = D;
+    a.q_weight = q_weight, a.k_weight = k_weight, a.eps = eps;
+    a.table = reinterpret_cast<const float2 *>(table), a.n_pos = n_pos, a.rot = rot, a.interleaved = interleaved;
+    a.positions = positions, a.T = T;
+    a.vec_in = vec_ok(k, ldk, D, type) && vec_ok(v, ldv, D, type) && (!q || vec_ok(q, ldq, D, type));
+    a.vec_out = q && vec_ok(q_out, ldqo, D, q_out_type);
+    a.pages = static_cast<uint8_t *>(cache->pages);
+    a.n_slots = cache->n_pages * cache->page_tokens;
+    a.page_tokens = cache->page_tokens, a.slots = slots;
+    a.err = library_error_word();
+    if (!a.err) return QK_ERR_CUDA;
+    return launch_rows<true>(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? QK_OK : QK_ERR_CUDA;
+}
+
+int qk_kv_read_q4(const qk_kv_cache_q4 *cache, const int64_t *slots, int64_t T, void *k, int64_t ldk, void *v,
+                  int64_t ldv, int type, qk_stream_t stream)
+{
+    const int st = kv4_check_cache(cache);
+    if (st != QK_OK) return st;
+    if (!type_ok(type)) return QK_ERR_TYPE;
+    const int64_t w = static_cast<int64_t>(cache->n_kv_heads) * cache->head_dim;
+    if (ldk == 0) ldk = w;
+    if (ldv == 0) ldv = w;
+    if (T < 0 || ldk < w || ldv < w) return QK_ERR_BAD_DIM;
+    if (T == 0) return QK_OK;
+    if (!slots || (!k && !v)) return QK_ERR_NULL;
+    if (!multiple(slots, 8) || !multiple(k, size_of(type)) || !multiple(v, size_of(type))) return QK_ERR_ALIGN;
+    if (T > (static_cast<int64_t>(INT32_MAX) * kRowWarps) / (2 * cache->n_kv_heads)) return QK_ERR_TOO_LARGE;
+    ReadArgs a{};
+    a.pages = static_cast<const uint8_t *>(cache->pages);
+    a.n_slots = cache->n_pages * cache->page_tokens;
+    a.n_kv = cache->n_kv_heads, a.D = cache->head_dim, a.page_tokens = cache->page_tokens;
+    a.slots = slots, a.T = T, a.k = k, a.v = v, a.ldk = ldk, a.ldv = ldv, a.type = type;
+    a.vec = (!k || vec_ok(k, ldk, a.D, type)) && (!v || vec_ok(v, ldv, a.D, type));
+    a.err = library_error_word();
+    if (!a.err) return QK_ERR_CUDA;
+    const int64_t items = T * a.n_kv * ((k ? 1 : 0) + (v ? 1 : 0));
+    return launch(read_kernel, blocks_for(items), kRowWarps * 32, 0, reinterpret_cast<cudaStream_t>(stream), a) ==
+                   cudaSuccess
+               ? QK_OK
+               : QK_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -21,8 +21,9 @@ _lock = threading.Lock()
 QK_OK = 0
 STATUS = {0: "QK_OK", 1: "QK_ERR_NULL", 2: "QK_ERR_BAD_DIM", 3: "QK_ERR_ALIGN", 4: "QK_ERR_BATCH",
           5: "QK_ERR_CUDA", 6: "QK_ERR_TIMEOUT", 7: "QK_ERR_WORKSPACE", 8: "QK_ERR_TOO_LARGE",
-          9: "QK_ERR_BAD_INDEX"}
+          9: "QK_ERR_BAD_INDEX", 10: "QK_ERR_TYPE"}
 MAX_BATCH = 8
+DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}   # qk_dtype
 
 EXPORTS = ["qmatvec_q8_0", "qmatvec_q4_k", "qmatvec_q6_k", "qmatvec_swiglu_q8_0", "qmatvec_swiglu_q4_k",
            "qmatvec_swiglu_q6_k", "qmatvec_experts_q8_0", "qmatvec_experts_q4_k", "qmatvec_experts_q6_k",
@@ -30,7 +31,14 @@ EXPORTS = ["qmatvec_q8_0", "qmatvec_q4_k", "qmatvec_q6_k", "qmatvec_swiglu_q8_0"
            "qgemm_q8_0_acc", "qgemm_swiglu_q8_0", "qgemm_q4_k_workspace_bytes",
            "qgemm_q4_k_noalloc", "qk_row_bytes_q8_0", "qk_row_bytes_q4_k",
            "qk_status_string", "qk_device_error", "qk_set_wait_limit_ns", "qk_set_programmatic_launch",
-           "qk_set_strict_blocks", "qk_version"]
+           "qk_set_strict_blocks", "qk_version", "qk_rope_table", "qk_norm_rope", "qk_kv_append_q4",
+           "qk_kv_read_q4", "qk_attn_q4", "qk_attn_q4_workspace_bytes"]
+
+
+class _KVCacheQ4(ctypes.Structure):
+    """qk_kv_cache_q4 of include/qk.h."""
+    _fields_ = [("pages", ctypes.c_void_p), ("n_pages", ctypes.c_int64), ("n_kv_heads", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("page_tokens", ctypes.c_int)]
 
 
 class QKError(RuntimeError):
@@ -91,6 +99,19 @@ def load(path: str | None = None):
         lib.qk_set_programmatic_launch.restype = I
         lib.qk_set_strict_blocks.argtypes = [I]
         lib.qk_set_strict_blocks.restype = I
+        F, D = ctypes.c_float, ctypes.c_double
+        C = ctypes.POINTER(_KVCacheQ4)
+        lib.qk_rope_table.argtypes = [P, I64, I, D, D, P, I64, D, D, D, P]
+        lib.qk_norm_rope.argtypes = [P, I64, I, I, I, I, P, P, F, P, I64, I, I, P, I64, P, I64, I, P]
+        lib.qk_kv_append_q4.argtypes = [C, P, I64, I, P, I64, P, I64, I, P, P, F, P, I64, I, I, P, P, I64, P, I64,
+                                        I, P]
+        lib.qk_kv_read_q4.argtypes = [C, P, I64, P, I64, P, I64, I, P]
+        lib.qk_attn_q4.argtypes = [C, P, I64, I, I, P, I64, I64, P, P, I64, I64, I64, I64, F, I64, P, I64, I, P,
+                                   ctypes.c_size_t, P]
+        for name in ("qk_rope_table", "qk_norm_rope", "qk_kv_append_q4", "qk_kv_read_q4", "qk_attn_q4"):
+            getattr(lib, name).restype = I
+        lib.qk_attn_q4_workspace_bytes.argtypes = [I64, I, I, I, I64, I64]
+        lib.qk_attn_q4_workspace_bytes.restype = ctypes.c_size_t
         lib.qk_debug_skip_item.argtypes = [I64]
         lib.qk_debug_skip_item.restype = I64
         lib.qk_debug_gemv_plan.argtypes = [I, I64, I64, I, ctypes.POINTER(ctypes.c_int64), I]
@@ -342,6 +363,208 @@ def qgemm_swiglu(fmt: str, w: torch.Tensor, gate_offset: int, up_offset: int, F:
 
 def qgemm_swiglu_q4_k(w, gate_offset, up_offset, F, K, x, h=None, ldh=0, workspace=None, stream=None):
     return qgemm_swiglu("q4_k", w, gate_offset, up_offset, F, K, x, h, ldh, workspace, stream)
+
+
+# ---------------------------------------------------------------- attention operators
+
+def _rows(t, width: int, name: str, dtype=None) -> None:
+    """Rows of `width` elements of an element type the attention operators take, unit stride inside a row."""
+    _on_device(t, name, dtype)
+    if t.dtype not in DTYPES:
+        raise ValueError(f"{name} must be float32, float16 or bfloat16, not {t.dtype}")
+    if t.dim() != 2 or t.shape[1] != width or (width > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be rows of {width} elements with unit stride, got shape {tuple(t.shape)} "
+                         f"stride {t.stride()}")
+    if t.shape[0] > 1 and t.stride(0) < width:
+        raise ValueError(f"{name} rows are {t.stride(0)} elements apart, less than their {width}")
+
+
+def _ld(t, width: int) -> int:
+    """Row stride of a checked tensor (a single row has none)."""
+    return t.stride(0) if t.shape[0] > 1 else width
+
+
+def _vector(t, n: int, dtype, name: str):
+    """Pointer of a contiguous vector of at least n elements (None: null)."""
+    if t is None:
+        return None
+    _on_device(t, name, dtype)
+    if not t.is_contiguous() or t.numel() < n:
+        raise ValueError(f"{name} must be contiguous with at least {n} elements")
+    return t.data_ptr()
+
+
+def _table(table, positions, T: int, D: int):
+    """(table pointer, positions in it, rotating channels, positions pointer)."""
+    if table is None:
+        return None, 0, 0, None
+    _on_device(table, "table", torch.float32)
+    if table.dim() != 3 or table.shape[2] != 2 or not table.is_contiguous() or 2 * table.shape[1] > D:
+        raise ValueError(f"table must be contiguous [n_pos][rot/2][2] with rot <= {D}, got {tuple(table.shape)}")
+    if positions is None:
+        raise ValueError("positions are needed with a table")
+    return table.data_ptr(), table.shape[0], 2 * table.shape[1], _vector(positions, T, torch.int32, "positions")
+
+
+def _cache(cache) -> _KVCacheQ4:
+    _on_device(cache, "cache", torch.uint8)
+    if cache.dim() != 4 or not cache.is_contiguous() or cache.shape[3] % 18:
+        raise ValueError("cache must be a contiguous uint8 tensor [pages][kv heads][page_tokens/16][18*head_dim] "
+                         f"(kv_cache_q4), got shape {tuple(cache.shape)}")
+    n, h, b, s = cache.shape
+    return _KVCacheQ4(cache.data_ptr(), n, h, s // 18, 16 * b)
+
+
+def rope_table(n_pos: int, rot: int, base: float = 10000.0, freq_scale: float = 1.0,
+               freq_factors: torch.Tensor | None = None, orig_ctx: int = 0, beta_fast: float = 32.0,
+               beta_slow: float = 1.0, amplitude: float = 1.0, table: torch.Tensor | None = None,
+               stream=None) -> torch.Tensor:
+    """[n_pos][rot/2][2] fp32 (cos, sin) of the position angles; freq_scale interpolates positions, freq_factors
+    divides each frequency, orig_ctx > 0 ramps between kept and interpolated frequencies (see include/qk.h)."""
+    if table is None:
+        table = torch.empty((max(n_pos, 0), max(rot, 0) // 2, 2), dtype=torch.float32, device="cuda")
+    _vector(table, n_pos * (rot // 2) * 2, torch.float32, "table")
+    st = load().qk_rope_table(table.data_ptr(), n_pos, rot, base, freq_scale,
+                              _vector(freq_factors, rot // 2, torch.float32, "freq_factors"), orig_ctx, beta_fast,
+                              beta_slow, amplitude, _stream(stream))
+    _check(st, "qk_rope_table")
+    return table
+
+
+def norm_rope(x: torch.Tensor, n_q_heads: int, n_k_heads: int, head_dim: int, positions: torch.Tensor | None,
+              table: torch.Tensor | None, q_weight: torch.Tensor | None = None,
+              k_weight: torch.Tensor | None = None, eps: float = 1e-6, interleaved: bool = False,
+              y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """RMS norm of every head (a weight of None: no norm) and rotation of its first channels by the table's row of
+    the token's position, over rows of n_q_heads + n_k_heads heads.  y may be x."""
+    width = (n_q_heads + n_k_heads) * head_dim
+    _rows(x, width, "x")
+    T = x.shape[0]
+    if y is None:
+        y = torch.empty((T, width), dtype=x.dtype, device=x.device)
+    else:
+        _rows(y, width, "y")
+        if y.shape[0] < T:
+            raise ValueError(f"y has {y.shape[0]} rows, x {T}")
+    tp, n_pos, rot, pp = _table(table, positions, T, head_dim)
+    st = load().qk_norm_rope(x.data_ptr(), _ld(x, width), DTYPES[x.dtype], n_q_heads, n_k_heads, head_dim,
+                             _vector(q_weight, head_dim, torch.float32, "q_weight"),
+                             _vector(k_weight, head_dim, torch.float32, "k_weight"), eps, tp, n_pos, rot,
+                             1 if interleaved else 0, pp, T, y.data_ptr(), _ld(y, width), DTYPES[y.dtype],
+                             _stream(stream))
+    _check(st, "qk_norm_rope")
+    return y
+
+
+def kv_cache_q4(n_pages: int, n_kv_heads: int, page_tokens: int, head_dim: int, device=None) -> torch.Tensor:
+    """An empty 4-bit cache: uint8 [n_pages][n_kv_heads][page_tokens/16][18*head_dim] (blocks as in include/qk.h)."""
+    if page_tokens % 16 or page_tokens <= 0 or head_dim not in (64, 96, 128, 256):
+        raise ValueError("page_tokens must be a multiple of 16 and head_dim 64, 96, 128 or 256")
+    return torch.zeros((n_pages, n_kv_heads, page_tokens // 16, 18 * head_dim), dtype=torch.uint8,
+                       device=device or "cuda")
+
+
+def kv_append_q4(cache: torch.Tensor, q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor,
+                 positions: torch.Tensor | None, slots: torch.Tensor, table: torch.Tensor | None,
+                 q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None, eps: float = 1e-6,
+                 interleaved: bool = False, q_out: torch.Tensor | None = None, stream=None) -> torch.Tensor | None:
+    """Norm and rotation of T tokens' queries and keys, with keys and values stored into `cache` at `slots` (int64;
+    negative: not stored).  Returns the queries (rows of q's heads; q_out may be q), None without q."""
+    c = _cache(cache)
+    D, width = c.head_dim, c.n_kv_heads * c.head_dim
+    _rows(k, width, "k")
+    _rows(v, width, "v", k.dtype)
+    T = k.shape[0]
+    if v.shape[0] != T:
+        raise ValueError(f"k has {T} rows, v {v.shape[0]}")
+    sp = _vector(slots, T, torch.int64, "slots")
+    tp, n_pos, rot, pp = _table(table, positions, T, D)
+    wq = heads = 0
+    if q is not None:
+        wq = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 2 else 0
+        if wq == 0 or wq % D:
+            raise ValueError(f"q must be rows of heads of {D} channels")
+        _rows(q, wq, "q", k.dtype)
+        heads = wq // D
+        if q_out is None:
+            q_out = torch.empty((T, wq), dtype=q.dtype, device=q.device)
+        _rows(q_out, wq, "q_out")
+        if q.shape[0] != T or q_out.shape[0] < T:
+            raise ValueError(f"q has {q.shape[0]} and q_out {q_out.shape[0]} rows, k {T}")
+    st = load().qk_kv_append_q4(
+        ctypes.byref(c), q.data_ptr() if heads else None, _ld(q, wq) if heads else 0, heads, k.data_ptr(),
+        _ld(k, width), v.data_ptr(), _ld(v, width), DTYPES[k.dtype],
+        _vector(q_weight, D, torch.float32, "q_weight"), _vector(k_weight, D, torch.float32, "k_weight"), eps, tp,
+        n_pos, rot, 1 if interleaved else 0, pp, sp, T, q_out.data_ptr() if heads else None,
+        _ld(q_out, wq) if heads else 0, DTYPES[q_out.dtype] if heads else 0, _stream(stream))
+    _check(st, "qk_kv_append_q4")
+    return q_out if heads else None
+
+
+def kv_read_q4(cache: torch.Tensor, slots: torch.Tensor, dtype: torch.dtype = torch.float16,
+               stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """The keys and values that the cache holds at `slots`: two [T][kv heads * head_dim] tensors of `dtype`."""
+    c = _cache(cache)
+    if dtype not in DTYPES:
+        raise ValueError(f"dtype must be float32, float16 or bfloat16, not {dtype}")
+    T = slots.numel()
+    sp = _vector(slots, T, torch.int64, "slots")
+    kv = torch.empty((2, T, c.n_kv_heads * c.head_dim), dtype=dtype, device=cache.device)
+    st = load().qk_kv_read_q4(ctypes.byref(c), sp, T, kv[0].data_ptr(), 0, kv[1].data_ptr(), 0, DTYPES[dtype],
+                              _stream(stream))
+    _check(st, "qk_kv_read_q4")
+    return kv[0], kv[1]
+
+
+def attn_q4_workspace(B: int, n_q_heads: int, n_kv_heads: int, head_dim: int, max_q: int = 1, max_len: int = 0,
+                      device=None) -> torch.Tensor:
+    """Zeroed scratch for attn_q4 calls of these sizes (one for each stream that calls)."""
+    n = load().qk_attn_q4_workspace_bytes(B, n_q_heads, n_kv_heads, head_dim, max_q, max_len)
+    return torch.zeros(max(256, n), dtype=torch.uint8, device=device or "cuda")
+
+
+def attn_q4(cache: torch.Tensor, q: torch.Tensor, page_table: torch.Tensor, lens: torch.Tensor,
+            q_start: torch.Tensor | None = None, max_q: int = 1, max_len: int = 0, scale: float | None = None,
+            window: int = 0, out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+            stream=None) -> torch.Tensor:
+    """Attention of the rows of q [T][heads * head_dim] over the 4-bit cache: sequence b has lens[b] keys in the
+    pages page_table[b], and the rows q_start[b]..q_start[b+1] (None: max_q each) as its last positions.  scale
+    defaults to head_dim^-0.5; window > 0 lets a row see that many keys up to its own.  `workspace` (zeroed once,
+    attn_q4_workspace) lets long sequences spread over the GPU; without it they are not split."""
+    c = _cache(cache)
+    D = c.head_dim
+    width = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 2 else 0
+    if width == 0 or width % (D * c.n_kv_heads):
+        raise ValueError(f"q must be rows of a multiple of {c.n_kv_heads} heads of {D} channels")
+    _rows(q, width, "q")
+    T, B = q.shape[0], lens.numel()
+    lp = _vector(lens, B, torch.int32, "lens")
+    _on_device(page_table, "page_table", torch.int32)
+    if page_table.dim() != 2 or page_table.shape[0] < B or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        raise ValueError(f"page_table must be [{B}][pages] with unit stride, got {tuple(page_table.shape)}")
+    pages = page_table.shape[1]
+    ld = page_table.stride(0) if page_table.shape[0] > 1 else pages
+    if ld < pages:
+        raise ValueError(f"page_table rows are {ld} entries apart, less than their {pages}")
+    qs = _vector(q_start, B + 1, torch.int32, "q_start")
+    if out is None:
+        out = torch.empty((T, width), dtype=q.dtype, device=q.device)
+    else:
+        _rows(out, width, "out")
+        if out.shape[0] < T:
+            raise ValueError(f"out has {out.shape[0]} rows, q {T}")
+    wp, wb = None, 0
+    if workspace is not None:
+        _on_device(workspace, "workspace")
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+        wp, wb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    st = load().qk_attn_q4(ctypes.byref(c), q.data_ptr(), _ld(q, width), DTYPES[q.dtype], width // D,
+                           page_table.data_ptr(), ld, pages, lp, qs, B, T, max_q, max_len,
+                           D ** -0.5 if scale is None else scale, window, out.data_ptr(), _ld(out, width),
+                           DTYPES[out.dtype], wp, wb, _stream(stream))
+    _check(st, "qk_attn_q4")
+    return out
 
 
 def debug_gemm_skip_chunk(chunk: int) -> int:
