@@ -359,6 +359,21 @@ def test_attn_split_and_hints(qk):
         check_attn(qk, [2000, 77], [9, 1], 8, 2, 128, 16, seed=3, dtype="bf16", **kw)
 
 
+def test_attn_one_workspace_for_calls_of_all_shapes(qk):
+    """A workspace serves calls of other shapes in turn: none leaves anything where another's counters are."""
+    ws = torch.zeros(8 << 20, dtype=torch.uint8, device="cuda")
+    calls = []
+    for i, (lens, n, nq, nkv, D, dtype) in enumerate([([3000], 1, 8, 1, 128, "f32"), ([900] * 40, 1, 16, 8, 64, "bf16"),
+                                                      ([2500, 800], 5, 4, 2, 256, "f16"), ([5000], 1, 3, 3, 96, "f32")]):
+        cache, tab, _, _ = make_cache(i, lens, nkv, D, 64)
+        q = rand(i, len(lens) * n, nq * D, dtype=dtype)
+        args = (cache, q, tab, torch.tensor(lens, dtype=torch.int32).cuda(), None, n, max(lens))
+        calls.append((args, qk.attn_q4(*args, workspace=torch.zeros_like(ws))))
+    for _ in range(3):
+        for args, want in calls:
+            assert torch.equal(qk.attn_q4(*args, workspace=ws), want)
+
+
 @pytest.mark.parametrize("dtype,out", [("f32", "bf16"), ("f16", "f32"), ("bf16", "f16")])
 def test_attn_output_types(qk, dtype, out):
     check_attn(qk, [77, 130], [1, 40], 4, 2, 64, 16, dtype=dtype, out=out)
