@@ -39,6 +39,10 @@ constexpr int kWarps = 8;
 constexpr float kNoMax = -3.0e38f;
 constexpr float kTwo24 = 16777216.0f;
 
+// Thread blocks an SM holds: two (128 registers a thread), one where a head of 256 channels needs more.
+template <int G>
+constexpr int kBlocksPerSm = G <= 4 ? 2 : 1;
+
 // Forms of a row tile.
 constexpr int kTwoPiece = 0;    // 8 rows, fp32 queries
 constexpr int kOnePiece8 = 1;   // 8 rows, 16-bit queries
@@ -133,8 +137,7 @@ __device__ __forceinline__ uint32_t signed_nibbles(uint32_t w)
 template <int G, int MODE>
 struct State {
     static constexpr int NR = MODE == kOnePiece16 ? 2 : 1;       // rows of a lane: lane/4 (and + 8)
-    static constexpr bool kHalfTile = MODE == kOnePiece8;        // rows 8..15 hold nothing
-    float o[G][4][kHalfTile ? 2 : 4];                            // [group][n-tile j]: channels 32g + 4n + j
+    float o[G][4][4];                                            // [group][n-tile j]: channels 32g + 4n + j
     float m[NR], l[NR];
     float limit;                                                 // exponents above it leave fp16's range
     uint32_t scale_lim;                                          // largest value scale seen (fp16 bits, twice)
@@ -144,8 +147,7 @@ struct State {
 template <int G, int MODE>
 struct Query {
     static constexpr int NR = State<G, MODE>::NR;
-    static constexpr int NP = MODE == kOnePiece8 ? 1 : 2;        // rows 8..15: second pieces or second rows
-    float init[G][NP];                                           // -8 * 2^-24 * (the group's sum of q')
+    float init[G][2];                                            // -8 * 2^-24 * (the group's sum of q'), rows r, r + 8
     float to_log2[NR];                                           // score -> exponent
     int lo[NR], hi[NR];                                          // keys [lo, hi) of each row, from the tile's first block
 };
@@ -171,22 +173,15 @@ __device__ __forceinline__ void block16(State<G, MODE> &S, const Query<G, MODE> 
 #pragma unroll
         for (int gp = 0; gp < Gp; ++gp) {
             const int g = pl * Gp + gp;
-            uint32_t a[2][MODE == kOnePiece8 ? 2 : 4];
+            uint32_t a[2][4];
 #pragma unroll
-            for (int st = 0; st < 2; ++st)
-                lds(a[st], qfrag + ((g * 2 + st) * 32 + lane) * (MODE == kOnePiece8 ? 8 : 16));
+            for (int st = 0; st < 2; ++st) lds(a[st], qfrag + ((g * 2 + st) * 32 + lane) * 16);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const uint32_t w = kw[h][gp], w8 = w >> 8;
-                float c0 = Q.init[g][0], c1 = c0, c2 = 0.0f, c3 = 0.0f;
-                if constexpr (MODE != kOnePiece8) {
-                    c2 = c3 = Q.init[g][1];
-                    mma_f16(c0, c1, c2, c3, a[0][0], a[0][1], a[0][2], a[0][3], w & 0x000F000Fu, w8 & 0x000F000Fu);
-                    mma_f16(c0, c1, c2, c3, a[1][0], a[1][1], a[1][2], a[1][3], w & 0x00F000F0u, w8 & 0x00F000F0u);
-                } else {
-                    mma_f16(c0, c1, c2, c3, a[0][0], 0u, a[0][1], 0u, w & 0x000F000Fu, w8 & 0x000F000Fu);
-                    mma_f16(c0, c1, c2, c3, a[1][0], 0u, a[1][1], 0u, w & 0x00F000F0u, w8 & 0x00F000F0u);
-                }
+                float c0 = Q.init[g][0], c1 = c0, c2 = MODE == kOnePiece8 ? 0.0f : Q.init[g][1], c3 = c2;
+                mma_f16(c0, c1, c2, c3, a[0][0], a[0][1], a[0][2], a[0][3], w & 0x000F000Fu, w8 & 0x000F000Fu);
+                mma_f16(c0, c1, c2, c3, a[1][0], a[1][1], a[1][2], a[1][3], w & 0x00F000F0u, w8 & 0x00F000F0u);
                 const float d0 = half_at(ks, (2 * h) * G + g), d1 = half_at(ks, (2 * h + 1) * G + g);
                 if constexpr (MODE == kTwoPiece) c0 += c2, c1 += c3;
                 s[0][h][0] = fmaf(d0, c0, s[0][h][0]);
@@ -330,12 +325,7 @@ __device__ __forceinline__ void block16(State<G, MODE> &S, const Query<G, MODE> 
             for (int j = 0; j < 4; ++j) {
                 const uint32_t b0 = j & 1 ? signed_nibbles<1>(j & 2 ? v0 : u0) : signed_nibbles<0>(j & 2 ? v0 : u0);
                 const uint32_t b1 = j & 1 ? signed_nibbles<1>(j & 2 ? v1 : u1) : signed_nibbles<0>(j & 2 ? v1 : u1);
-                if constexpr (State<G, MODE>::kHalfTile) {
-                    float z2 = 0.0f, z3 = 0.0f;
-                    mma_f16(S.o[g][j][0], S.o[g][j][1], z2, z3, a0, 0u, a2, 0u, b0, b1);
-                } else {
-                    mma_f16(S.o[g][j][0], S.o[g][j][1], S.o[g][j][2], S.o[g][j][3], a0, a1, a2, a3, b0, b1);
-                }
+                mma_f16(S.o[g][j][0], S.o[g][j][1], S.o[g][j][2], S.o[g][j][3], a0, a1, a2, a3, b0, b1);
             }
         }
     }
@@ -347,16 +337,18 @@ struct Shape {
     static constexpr int D = 32 * G, RT = MODE == kOnePiece16 ? 16 : 8;
     static constexpr int block_bytes = 18 * D;
     static constexpr int NST = G <= 2 ? 6 : 4;
-    static constexpr int frag_bytes = G * 2 * 32 * (MODE == kOnePiece8 ? 8 : 16);
+    static constexpr int frag_bytes = G * 2 * 32 * 16;
     static constexpr int part_bytes = RT * (D + 4) * 4 + RT * 8;      // rows padded by 4 floats; (M, l) of each row
     static constexpr int ring_bytes = NST * block_bytes;
     static constexpr int warp_bytes = ((ring_bytes > part_bytes ? ring_bytes : part_bytes) + 127) / 128 * 128;
-    static constexpr int smem = frag_bytes + kWarps * warp_bytes + kWarps * NST * 8 + 64;
+    static constexpr int bars_at = frag_bytes + kWarps * warp_bytes;
+    static constexpr int init_at = bars_at + kWarps * NST * 8 + 16;   // after the barriers and the join's flag
+    static constexpr int smem = init_at + 16 * G * 4 + 16 * 4;
     static constexpr int part_floats = RT * D + 2 * RT;               // in the workspace
 };
 
 template <int G, int MODE>
-__global__ void __launch_bounds__(kWarps * 32, 1) attn_kernel(const AttnArgs a)
+__global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm<G>) attn_kernel(const AttnArgs a)
 {
     using Sh = Shape<G, MODE>;
     constexpr int D = Sh::D, RT = Sh::RT, NST = Sh::NST, NR = State<G, MODE>::NR;
@@ -364,8 +356,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attn_kernel(const AttnArgs a)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r8 = lane >> 2, c = lane & 3;
     uint8_t *ring = smem + Sh::frag_bytes + warp * Sh::warp_bytes;
-    const uint32_t bars = smem_u32(smem + Sh::frag_bytes + kWarps * Sh::warp_bytes) + warp * NST * 8;
-    int *shared_flag = reinterpret_cast<int *>(smem + Sh::frag_bytes + kWarps * Sh::warp_bytes + kWarps * NST * 8);
+    const uint32_t bars = smem_u32(smem + Sh::bars_at) + warp * NST * 8;
+    int *shared_flag = reinterpret_cast<int *>(smem + Sh::bars_at + kWarps * NST * 8);
     if (lane == 0) {
         for (int i = 0; i < NST; ++i) mbar_init(bars + 8 * i, 1);
         fence_barrier_init();
@@ -447,80 +439,61 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attn_kernel(const AttnArgs a)
     // query rows: scaled by a power of two to [2^10, 2^11), fp16 pieces in fragment order.  Two pieces are whole
     // numbers and multiples of 2^-12, so that every product and sum of a group is exact in the tensor cores (which
     // cut what they add at 2^-24 of the largest term: with floating pieces a score lost four bits to that, 1.2e-5
-    // of an output over 32768 keys instead of 1e-6)
-    Query<G, MODE> Q;
+    // of an output over 32768 keys instead of 1e-6).  One warp takes a row, a lane one channel of each group.
     const uint32_t qfrag = smem_u32(smem);
-    float piece_sum[G][2] = {};
-#pragma unroll
-    for (int half = 0; half < NR; ++half) {
-        const int row = r8 + 8 * half;
+    float *row_init = reinterpret_cast<float *>(smem + Sh::init_at);     // [group][16]
+    float *row_log2 = row_init + 16 * G;                                 // [row]
+    for (int row = warp; row < RT; row += kWarps) {
         const bool in = row < rows;
         const int i = in ? (first + row) / a.rep : 0;
-        const int64_t at = (r0 + i) * a.ldq + (static_cast<int64_t>(hk) * a.rep + (in ? (first + row) % a.rep : 0)) * D;
-        float big = 0.0f;
+        const int64_t at = (r0 + i) * a.ldq + (static_cast<int64_t>(hk) * a.rep + (first + row - i * a.rep)) * D;
+        float x[G], big = 0.0f;
 #pragma unroll
-        for (int g = 0; g < G; ++g)
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (in) big = fmaxf(big, fabsf(load_as_float(a.q, at + 32 * g + 8 * c + j, a.q_type)));
-        big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, 1));
-        big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, 2));
+        for (int g = 0; g < G; ++g) {
+            x[g] = in ? load_as_float(a.q, at + 32 * g + lane, a.q_type) : 0.0f;
+            big = fmaxf(big, fabsf(x[g]));
+        }
+        big = __uint_as_float(redux_max_u32(0xFFFFFFFFu, __float_as_uint(big)));
         int e = 127;
         if (big > 0.0f && big < INFINITY) e = 127 + 10 - (static_cast<int>(__float_as_uint(big) >> 23) - 127);
         e = min(e, 250);
         // the scale's sign goes to the query, so that -inf masks a score whatever the scale
         const float up = copysignf(__uint_as_float(static_cast<uint32_t>(e) << 23), a.scale_log2);
         // exponent of 2 per unit of (q' n 2^-24), never 0: scale * log2(e) * 2^24 / up
-        Q.to_log2[half] = fmaxf(a.scale_log2 * kTwo24 / up, 1.2e-38f);
-        const int64_t pos = L - (r1 - r0) + i;
-        const int64_t base = (blk_lo + b0) * kBlockTokens;
-        int64_t lo = a.window > 0 ? pos - a.window + 1 - base : -1, hi = pos + 1 - base;
-        if (!in) hi = -1;
-        Q.lo[half] = static_cast<int>(lo < -1 ? -1 : (lo > INT32_MAX ? INT32_MAX : lo));
-        Q.hi[half] = static_cast<int>(hi < -1 ? -1 : (hi > INT32_MAX ? INT32_MAX : hi));
+        if (lane == 0) row_log2[row] = fmaxf(a.scale_log2 * kTwo24 / up, 1.2e-38f);
+        const int j = lane & 7, st = j & 1;
+        // the pair's register of the fragment (x[st], x[st + 4]) or (x[st + 2], x[st + 6]), and the half in it
+        const int flane = (row & 7) * 4 + (lane >> 3), second = (j >> 1) & 1, upper = j >> 2;
+        const float sixteenth = st ? 0.0625f : 1.0f;     // odd channels' nibbles come 16 times as large
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-            float x[8], y[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                x[j] = in ? load_as_float(a.q, at + 32 * g + 8 * c + j, a.q_type) * up : 0.0f;
-                float lead = __half2float(__float2half_rn(x[j]));
-                if (MODE == kTwoPiece) {
-                    lead = rintf(x[j]);
-                    y[j] = rintf((x[j] - lead) * 4096.0f) * (1.0f / 4096.0f);
-                    x[j] = lead;
-                    piece_sum[g][1] += y[j];
-                }
-                piece_sum[g][half] += lead;
-                if (j & 1) x[j] *= 0.0625f, y[j] *= 0.0625f;   // those keys' nibbles come 16 times as large
+            float v = x[g] * up, rest = 0.0f;
+            if (MODE == kTwoPiece) {
+                const float lead = rintf(v);
+                rest = rintf((v - lead) * 4096.0f) * (1.0f / 4096.0f);
+                v = lead;
+            } else {
+                v = __half2float(__float2half_rn(v));
             }
-            if (g % kWarps == warp % (G < kWarps ? G : kWarps) && warp < G) {
+            uint8_t *to = smem + ((g * 2 + st) * 32 + flane) * 16 + 8 * second + 2 * upper;
+            const __half lead = __float2half_rn(v * sixteenth);
+            if constexpr (MODE == kOnePiece16) {
+                *reinterpret_cast<__half *>(to + 4 * (row >> 3)) = lead;
+            } else {
+                *reinterpret_cast<__half *>(to) = lead;
+                *reinterpret_cast<__half *>(to + 4) = __float2half_rn(rest * sixteenth);   // 0 with one piece
+            }
 #pragma unroll
-                for (int st = 0; st < 2; ++st) {
-                    const uint32_t lead0 = pack_half(x[st], x[st + 4]), lead1 = pack_half(x[st + 2], x[st + 6]);
-                    const uint32_t rest0 = pack_half(y[st], y[st + 4]), rest1 = pack_half(y[st + 2], y[st + 6]);
-                    uint8_t *to = smem + ((g * 2 + st) * 32 + lane) * (MODE == kOnePiece8 ? 8 : 16);
-                    if constexpr (MODE == kTwoPiece) {
-                        *reinterpret_cast<uint4 *>(to) = make_uint4(lead0, rest0, lead1, rest1);
-                    } else if constexpr (MODE == kOnePiece8) {
-                        *reinterpret_cast<uint2 *>(to) = make_uint2(lead0, lead1);
-                    } else {
-                        reinterpret_cast<uint32_t *>(to)[half] = lead0;
-                        reinterpret_cast<uint32_t *>(to)[2 + half] = lead1;
-                    }
-                }
+            for (int o = 16; o; o >>= 1) {
+                v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+                if (MODE == kTwoPiece) rest += __shfl_xor_sync(0xFFFFFFFFu, rest, o);
+            }
+            if (lane == 0) {
+                row_init[16 * g + row] = v * (-8.0f / kTwo24);
+                if (MODE != kOnePiece16) row_init[16 * g + 8 + row] = rest * (-8.0f / kTwo24);
             }
         }
     }
-#pragma unroll
-    for (int g = 0; g < G; ++g)
-#pragma unroll
-        for (int k = 0; k < Query<G, MODE>::NP; ++k) {
-            float x = piece_sum[g][k];
-            x += __shfl_xor_sync(0xFFFFFFFFu, x, 1);
-            x += __shfl_xor_sync(0xFFFFFFFFu, x, 2);
-            Q.init[g][k] = x * (-8.0f / kTwo24);
-        }
 
     State<G, MODE> S;
 #pragma unroll
@@ -528,7 +501,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attn_kernel(const AttnArgs a)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int k = 0; k < (State<G, MODE>::kHalfTile ? 2 : 4); ++k) S.o[g][j][k] = 0.0f;
+            for (int k = 0; k < 4; ++k) S.o[g][j][k] = 0.0f;
     }
 #pragma unroll
     for (int k = 0; k < NR; ++k) S.m[k] = kNoMax, S.l[k] = 0.0f;
@@ -536,8 +509,23 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attn_kernel(const AttnArgs a)
     S.scale_lim = 0;
     __syncthreads();
 
-    // keys every row sees, counted from the split's first block
     const int64_t base = (blk_lo + b0) * kBlockTokens;
+    Query<G, MODE> Q;
+#pragma unroll
+    for (int half = 0; half < NR; ++half) {
+        const int row = r8 + 8 * half;
+        Q.to_log2[half] = row_log2[row];
+        const int64_t pos = L - (r1 - r0) + (row < rows ? (first + row) / a.rep : 0);
+        const int64_t lo = a.window > 0 ? pos - a.window + 1 - base : -1, hi = row < rows ? pos + 1 - base : -1;
+        Q.lo[half] = static_cast<int>(lo < -1 ? -1 : (lo > INT32_MAX ? INT32_MAX : lo));
+        Q.hi[half] = static_cast<int>(hi < -1 ? -1 : (hi > INT32_MAX ? INT32_MAX : hi));
+    }
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) Q.init[g][k] = row_init[16 * g + r8 + 8 * k];
+
+    // keys every row sees, counted from the split's first block
     const int64_t last_lo = a.window > 0 ? pos1 - a.window + 1 - base : 0;
     const int64_t first_hi = pos0 + 1 - base;
     const int all_lo = static_cast<int>(key_lo - base < 0 ? 0 : key_lo - base);
@@ -664,9 +652,7 @@ struct Cut {
 };
 
 constexpr int64_t kCounters = 16384;         // at the start of every workspace, whatever the call
-constexpr int64_t kAim = 152 * 2 * 4;        // thread blocks a call is cut into, where its keys allow it
-
-Cut cut_for(int64_t B, int n_kv, int rep, int64_t max_q, int64_t max_len, bool fp32)
+Cut cut_for(int64_t B, int n_kv, int rep, int D, int64_t max_q, int64_t max_len, bool fp32)
 {
     Cut c{};
     const int64_t rows = max_q * rep;
@@ -675,15 +661,21 @@ Cut cut_for(int64_t B, int n_kv, int rep, int64_t max_q, int64_t max_len, bool f
     c.tiles = static_cast<int>((rows + c.row_tile - 1) / c.row_tile);
     c.groups = B * n_kv * c.tiles;
     const int64_t blocks = (max_len + kBlockTokens - 1) / kBlockTokens;
-    // a split of fewer than two blocks a warp spends its time on filling the ring
-    c.min_blocks = 2 * kWarps;
-    int64_t s = c.groups <= kCounters ? (kAim + c.groups - 1) / c.groups : 1;
-    const int64_t most = (blocks + c.min_blocks - 1) / c.min_blocks;
-    if (s > most) s = most;
-    if (s < 1) s = 1;
-    c.splits = static_cast<int>(s);
-    const int64_t per = (blocks + s - 1) / s;
-    if (per > c.min_blocks) c.min_blocks = per;
+    // The split with the least of (rounds of thread blocks) * (steps of a warp + a thread block's start and join,
+    // about 10 steps), of splits that leave every warp two blocks.
+    int sms = 152, smem = 0;
+    device_limits(&sms, &smem);
+    const int64_t slots = static_cast<int64_t>(sms) * (D > 128 ? 1 : 2);
+    int64_t best = 1, best_cost = INT64_MAX;
+    for (int64_t s = 1; s <= 512 && c.groups <= kCounters; ++s) {
+        const int64_t per = (blocks + s - 1) / s;
+        if (s > 1 && per < 2 * kWarps) break;
+        const int64_t cost = (c.groups * s + slots - 1) / slots * ((per + kWarps - 1) / kWarps + 10);
+        if (cost < best_cost) best = s, best_cost = cost;
+    }
+    c.splits = static_cast<int>(best);
+    c.min_blocks = (blocks + best - 1) / best;
+    if (c.min_blocks < 2 * kWarps) c.min_blocks = 2 * kWarps;
     return c;
 }
 
@@ -733,7 +725,7 @@ size_t qk_attn_q4_workspace_bytes(int64_t B, int n_q_heads, int n_kv_heads, int 
         return 0;
     size_t most = 0;
     for (const bool fp32 : {true, false}) {
-        const Cut c = cut_for(B, n_kv_heads, n_q_heads / n_kv_heads, max_q, max_len, fp32);
+        const Cut c = cut_for(B, n_kv_heads, n_q_heads / n_kv_heads, head_dim, max_q, max_len, fp32);
         const size_t n = c.splits > 1 ? 4 * kCounters + c.groups * c.splits * part_bytes_of(c, head_dim) : 0;
         if (n > most) most = n;
     }
@@ -770,7 +762,7 @@ int qk_attn_q4(const qk_kv_cache_q4 *cache, const void *q, int64_t ldq, int q_ty
         max_pages > INT32_MAX / cache->page_tokens)
         return QK_ERR_TOO_LARGE;
     const int64_t keys = max_pages * cache->page_tokens;
-    Cut cut = cut_for(B, n_kv, rep, max_q, max_len > 0 && max_len < keys ? max_len : keys, q_type == QK_F32);
+    Cut cut = cut_for(B, n_kv, rep, D, max_q, max_len > 0 && max_len < keys ? max_len : keys, q_type == QK_F32);
     // as many splits as the workspace holds
     const int64_t room = workspace ? static_cast<int64_t>(workspace_bytes) - 4 * kCounters : 0;
     const int64_t fit = room > 0 ? room / (cut.groups * part_bytes_of(cut, D)) : 0;
