@@ -26,6 +26,7 @@
 // Blocks of 16 tokens arrive by bulk copies in a ring of stages of each warp
 // (no barrier across warps in the loop); a sequence's blocks are split over
 // thread blocks, and the last to finish joins the parts in a fixed order.
+#include <atomic>
 #include <cmath>
 
 #include "qk_device.cuh"
@@ -667,9 +668,14 @@ Cut cut_for(int64_t B, int n_kv, int rep, int D, int64_t max_q, int64_t max_len,
     device_limits(&sms, &smem);
     const int64_t slots = static_cast<int64_t>(sms) * (D > 128 ? 1 : 2);
     int64_t best = 1, best_cost = INT64_MAX;
-    for (int64_t s = 1; s <= 512 && c.groups <= kCounters; ++s) {
+    for (int64_t rounds = 1, last = 0; rounds <= 12 && c.groups <= kCounters; ++rounds) {
+        // as many splits as `rounds` rounds hold, or one
+        int64_t s = slots * rounds / c.groups;
+        if (s * 2 * kWarps > blocks) s = blocks / (2 * kWarps);
+        if (s < 1) s = 1;
+        if (s == last) continue;
+        last = s;
         const int64_t per = (blocks + s - 1) / s;
-        if (s > 1 && per < 2 * kWarps) break;
         const int64_t cost = (c.groups * s + slots - 1) / slots * ((per + kWarps - 1) / kWarps + 10);
         if (cost < best_cost) best = s, best_cost = cost;
     }
@@ -687,8 +693,16 @@ cudaError_t launch(const AttnArgs &a, int64_t grid, cudaStream_t st)
     const auto kern = attn_kernel<G, MODE>;
     constexpr int smem = Shape<G, MODE>::smem;
     static_assert(smem <= 227 * 1024, "shared memory of a block");
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    // once a device; two threads that find it undone both do it
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    if (dev >= 64 || !(done.load(std::memory_order_acquire) >> dev & 1)) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) done.fetch_or(1ull << dev, std::memory_order_release);
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
     cfg.blockDim = dim3(kWarps * 32);

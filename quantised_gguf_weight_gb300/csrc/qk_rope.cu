@@ -258,6 +258,204 @@ __global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const RowsArgs a)
     }
 }
 
+// ---------------------------------------------------------------- heads of 64, 96, 128 or 256 channels
+
+// Eight channels a lane, two chunks of four.  Interleaved pairs (and values,
+// which do not rotate) take eight neighbours; the half layout takes
+// 4i..4i+3 and their partners half + 4i.., so a pair is always in one lane and
+// nothing is exchanged.  The lanes of a token's heads share its table row and
+// keep it in registers over HPT heads.
+struct Chunks {
+    int a, b;        // first channels of the lane's two chunks
+    bool turn;       // they rotate
+};
+__device__ __forceinline__ Chunks chunks_of(int i, int rot, bool interleaved)
+{
+    if (interleaved || 8 * i >= rot) return {8 * i, 8 * i + 4, 8 * i < rot};
+    return {4 * i, (rot >> 1) + 4 * i, true};
+}
+
+// Eight neighbouring channels of a head to the cache: the group's scale over
+// 4 lanes, one word of key nibbles or two halves of value words.
+template <int D>
+__device__ __forceinline__ void store_eight(uint8_t *block, int t, int ch, bool active, const float (&x)[8], bool is_key,
+                                            int lane)
+{
+    float hi = x[0], lo = x[0];
+    bool odd = false;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        hi = fmaxf(hi, x[e]), lo = fminf(lo, x[e]);
+        odd |= !(fabsf(x[e]) <= FLT_MAX);
+    }
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+        hi = fmaxf(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, o));
+        lo = fminf(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
+    }
+    const uint32_t odd_lanes = __ballot_sync(0xFFFFFFFFu, odd);
+    if (!active) return;
+    const bool group_odd = (odd_lanes >> (lane & 28)) & 15u;
+    const float m = hi >= -lo ? hi : lo;
+    const float want = fminf(fmaxf(m * -0.125f, -65504.0f), 65504.0f);
+    const __half dh = group_odd ? __ushort_as_half(0x7FFF) : __float2half_rn(want);
+    const float d = __half2float(dh);
+    uint32_t bits = 0x88888888u;
+    if (d != 0.0f && !group_odd) {
+        bits = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float n = fminf(fmaxf(floorf(__fadd_rn(__fdiv_rn(x[e], d), 8.5f)), 0.0f), 15.0f);
+            bits |= static_cast<uint32_t>(n) << (4 * e);
+        }
+    }
+    if (is_key) {
+        *reinterpret_cast<uint32_t *>(block + kv4_key_place(D, t, ch).byte) = bits;
+    } else {
+        const Kv4Place p = kv4_value_place(D, t, ch), q = kv4_value_place(D, t, ch + 4);
+        *reinterpret_cast<uint16_t *>(block + p.byte + (p.nibble >> 1)) = static_cast<uint16_t>(bits);
+        *reinterpret_cast<uint16_t *>(block + q.byte + (q.nibble >> 1)) = static_cast<uint16_t>(bits >> 16);
+    }
+    if ((lane & 3) == 0) {
+        const int s = is_key ? kv4_key_scale(D, t, ch >> 5) : kv4_value_scale(D, t, ch >> 5);
+        *reinterpret_cast<__half *>(block + s) = dh;
+    }
+}
+
+template <int D>
+constexpr int kRowsPerWarp = D == 96 ? 2 : 256 / D;
+
+template <int D, int TYPE, int HPT, bool APPEND>
+__global__ void __launch_bounds__(kRowWarps * 32) heads_kernel(const RowsArgs a)
+{
+    constexpr int LPR = D / 8, RPW = kRowsPerWarp<D>, NG = kRowWarps * RPW;
+    __shared__ __align__(16) float turn[APPEND ? kRowWarps * RPW : 1][APPEND ? D : 4];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int sub = lane / LPR, i = lane - sub * LPR;            // row of the warp, lane of the row
+    const bool on = sub < RPW;                                   // 96 channels leave 8 lanes idle
+    const int heads = a.n_q + a.n_k + a.n_v, parts = (heads + NG * HPT - 1) / (NG * HPT);
+    const int64_t t = blockIdx.x / parts;
+    const int h0 = static_cast<int>(blockIdx.x - t * parts) * NG * HPT + warp * RPW + sub;
+    const Chunks pair = chunks_of(i, a.rot, a.interleaved != 0), plain = {8 * i, 8 * i + 4, false};
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    bool bad = false;
+    int32_t pos = 0;
+    if (a.rot > 0) {
+        pos = a.positions[t];
+        bad = pos < 0 || pos >= a.n_pos;
+        if (bad) {
+            pos = 0;
+            if (threadIdx.x == 0) record_error(a.err, kErrBadIndex);
+        }
+    }
+    float x[HPT][8];
+#pragma unroll
+    for (int k = 0; k < HPT; ++k) {
+        const int h = h0 + k * NG;
+        const bool is_q = h < a.n_q, is_v = h >= a.n_q + a.n_k;
+        const Chunks ch = is_v ? plain : pair;
+        const void *src = is_q ? a.q : (is_v ? a.v : a.k);
+        const int64_t at = t * (is_q ? a.ldq : (is_v ? a.ldv : a.ldk)) +
+                           static_cast<int64_t>(is_q ? h : (is_v ? h - a.n_q - a.n_k : h - a.n_q)) * D;
+        float lo[4] = {}, hi[4] = {};
+        if (on && h < heads) load4(src, at + ch.a, TYPE, lo), load4(src, at + ch.b, TYPE, hi);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[k][e] = lo[e], x[k][4 + e] = hi[e];
+    }
+    float cs[8];          // (cos, sin) of the lane's four pairs
+#pragma unroll
+    for (int e = 0; e < 8; ++e) cs[e] = 0.0f;
+    if (on && pair.turn) {
+        const float4 *row = reinterpret_cast<const float4 *>(a.table + static_cast<int64_t>(pos) * (a.rot >> 1) + 4 * i);
+        const float4 u = row[0], v = row[1];
+        cs[0] = u.x, cs[1] = u.y, cs[2] = u.z, cs[3] = u.w, cs[4] = v.x, cs[5] = v.y, cs[6] = v.z, cs[7] = v.w;
+    }
+    int64_t slot = -1;
+    if (APPEND) slot = a.slots[t];
+#pragma unroll
+    for (int k = 0; k < HPT; ++k) {
+        const int h = h0 + k * NG;
+        const bool is_q = h < a.n_q, is_v = h >= a.n_q + a.n_k;
+        const float *weight = is_q ? a.q_weight : (is_v ? nullptr : a.k_weight);
+        if (a.q_weight || a.k_weight) {
+            float s = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s = fmaf(x[k][e], x[k][e], s);
+            if constexpr (D == 96) {      // 12 lanes a row: 8 + 4 by halving, the odd third added last
+                s += __shfl_xor_sync(0xFFFFFFFFu, s, 1);     // rows begin at lanes 0 and 12: pairs stay inside
+                s += __shfl_xor_sync(0xFFFFFFFFu, s, 2);     // and groups of four too
+                const int first = sub * LPR;
+                s = __shfl_sync(0xFFFFFFFFu, s, first) + __shfl_sync(0xFFFFFFFFu, s, first + 4) +
+                    __shfl_sync(0xFFFFFFFFu, s, (first + 8) & 31);
+            } else {
+#pragma unroll
+                for (int o = LPR / 2; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+            }
+            if (weight && on) {
+                const float r = __frsqrt_rn(__fadd_rn(__fdiv_rn(s, static_cast<float>(D)), a.eps));
+                const float4 u = *reinterpret_cast<const float4 *>(weight + pair.a);
+                const float4 v = *reinterpret_cast<const float4 *>(weight + pair.b);
+                const float w[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[k][e] = __fmul_rn(__fmul_rn(x[k][e], r), w[e]);
+            }
+        }
+        if (pair.turn && !is_v) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                // pair e: neighbours 2e, 2e + 1 of the eight, or e of both chunks
+                float &p = a.interleaved ? x[k][2 * e] : x[k][e], &q = a.interleaved ? x[k][2 * e + 1] : x[k][4 + e];
+                const float c = cs[2 * e], s = cs[2 * e + 1], u = p, v = q;
+                p = __fsub_rn(__fmul_rn(u, c), __fmul_rn(v, s));
+                q = __fadd_rn(__fmul_rn(u, s), __fmul_rn(v, c));
+            }
+        }
+        if (bad && !is_v)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[k][e] = __int_as_float(0x7FC00000);
+        if (!APPEND || is_q) {
+            void *dst = is_q ? a.q_out : a.k_out;
+            const int64_t to = t * (is_q ? a.ldqo : a.ldko) + static_cast<int64_t>(is_q ? h : h - a.n_q) * D;
+            if (on && h < heads) {
+                const float lo[4] = {x[k][0], x[k][1], x[k][2], x[k][3]}, hi[4] = {x[k][4], x[k][5], x[k][6], x[k][7]};
+                store4(dst, to + pair.a, a.out_type, lo);
+                store4(dst, to + pair.b, a.out_type, hi);
+            }
+        }
+        if constexpr (APPEND) {
+            // a warp with a key or value row among its rows stores them (queries of the same warp only take part)
+            const bool store = !is_q && h < heads && on && slot >= 0 && slot < a.n_slots;
+            if (__any_sync(0xFFFFFFFFu, !is_q && h < heads)) {
+                if (!is_q && h < heads && on && slot >= a.n_slots && i == 0) record_error(a.err, kErrBadIndex);
+                if (!a.interleaved) {      // eight neighbours a lane, as the cache wants them
+                    float *row = turn[warp * RPW + (on ? sub : 0)];
+                    const Chunks ch = is_v ? plain : pair;
+                    if (on) {
+                        *reinterpret_cast<float4 *>(row + ch.a) = make_float4(x[k][0], x[k][1], x[k][2], x[k][3]);
+                        *reinterpret_cast<float4 *>(row + ch.b) = make_float4(x[k][4], x[k][5], x[k][6], x[k][7]);
+                    }
+                    __syncwarp();
+                    if (on) {
+                        const float4 u = *reinterpret_cast<const float4 *>(row + 8 * i);
+                        const float4 v = *reinterpret_cast<const float4 *>(row + 8 * i + 4);
+                        x[k][0] = u.x, x[k][1] = u.y, x[k][2] = u.z, x[k][3] = u.w;
+                        x[k][4] = v.x, x[k][5] = v.y, x[k][6] = v.z, x[k][7] = v.w;
+                    }
+                    __syncwarp();
+                }
+                const int64_t page = store ? slot / a.page_tokens : 0;
+                const int off = store ? static_cast<int>(slot - page * a.page_tokens) : 0;
+                const int hk = is_v ? h - a.n_q - a.n_k : h - a.n_q;
+                uint8_t *block = a.pages + ((page * a.n_k + hk) * (a.page_tokens / kBlockTokens) + off / kBlockTokens) *
+                                               static_cast<int64_t>(18 * D);
+                store_eight<D>(block, off % kBlockTokens, 8 * i, store, x[k], !is_v, lane);
+            }
+        }
+    }
+}
+
 struct ReadArgs {
     const uint8_t *pages;
     int64_t n_slots;
@@ -271,46 +469,56 @@ struct ReadArgs {
     int *err;
 };
 
-// One warp reads one head of one slot, keys or values.
+// A lane reads eight channels of a slot's key or value head: one word, or two halves of words.
 __global__ void __launch_bounds__(kRowWarps * 32) read_kernel(const ReadArgs a)
 {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int lane = threadIdx.x & 31;
-    const int heads = a.n_kv * ((a.k ? 1 : 0) + (a.v ? 1 : 0));
-    const int64_t item = static_cast<int64_t>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
+    const int lpr = a.D / 8, heads = a.n_kv * ((a.k ? 1 : 0) + (a.v ? 1 : 0));
+    const int64_t item = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+    const int64_t row = item / lpr, t = row / heads;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (item >= a.T * heads) return;
-    const int64_t t = item / heads;
-    int h = static_cast<int>(item - t * heads);
+    if (t >= a.T) return;
+    const int ch = static_cast<int>(item - row * lpr) * 8;
+    int h = static_cast<int>(row - t * heads);
     const bool is_key = a.k && h < a.n_kv;
     if (a.k && !is_key) h -= a.n_kv;
     void *dst = is_key ? a.k : a.v;
-    const int64_t to = t * (is_key ? a.ldk : a.ldv) + static_cast<int64_t>(h) * a.D;
+    const int64_t to = t * (is_key ? a.ldk : a.ldv) + static_cast<int64_t>(h) * a.D + ch;
     const int64_t slot = a.slots[t];
-    const bool inside = slot >= 0 && slot < a.n_slots;
-    if (slot >= a.n_slots && lane == 0) record_error(a.err, kErrBadIndex);
-    const int64_t page = inside ? slot / a.page_tokens : 0;
-    const int off = inside ? static_cast<int>(slot - page * a.page_tokens) : 0;
-    const uint8_t *block = a.pages + ((page * a.n_kv + h) * (a.page_tokens / kBlockTokens) + off / kBlockTokens) *
-                                         static_cast<int64_t>(18 * a.D);
-    for (int ch = lane * 4; ch < a.D; ch += 128) {
-        float x[4];
-        if (inside) {
-            const int tk = off % kBlockTokens;
-            const Kv4Place p = is_key ? kv4_key_place(a.D, tk, ch) : kv4_value_place(a.D, tk, ch);
-            const uint32_t n = *reinterpret_cast<const uint16_t *>(block + p.byte + (p.nibble >> 1));
-            const int s = is_key ? kv4_key_scale(a.D, tk, ch >> 5) : kv4_value_scale(a.D, tk, ch >> 5);
-            const float d = __half2float(*reinterpret_cast<const __half *>(block + s));
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = d * (static_cast<float>((n >> (4 * e)) & 15u) - 8.0f);
+    float lo[4], hi[4];
+    if (slot >= 0 && slot < a.n_slots) {
+        const int64_t page = slot / a.page_tokens;
+        const int off = static_cast<int>(slot - page * a.page_tokens), tk = off % kBlockTokens;
+        const uint8_t *block = a.pages + ((page * a.n_kv + h) * (a.page_tokens / kBlockTokens) + off / kBlockTokens) *
+                                             static_cast<int64_t>(18 * a.D);
+        uint32_t n;
+        if (is_key) {
+            n = *reinterpret_cast<const uint32_t *>(block + kv4_key_place(a.D, tk, ch).byte);
         } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = slot < 0 ? 0.0f : __int_as_float(0x7FC00000);
+            const Kv4Place p = kv4_value_place(a.D, tk, ch), q = kv4_value_place(a.D, tk, ch + 4);
+            n = *reinterpret_cast<const uint16_t *>(block + p.byte + (p.nibble >> 1)) |
+                static_cast<uint32_t>(*reinterpret_cast<const uint16_t *>(block + q.byte + (q.nibble >> 1))) << 16;
         }
-        if (a.vec) store4(dst, to + ch, a.type, x);
-        else
+        const int s = is_key ? kv4_key_scale(a.D, tk, ch >> 5) : kv4_value_scale(a.D, tk, ch >> 5);
+        const float d = __half2float(*reinterpret_cast<const __half *>(block + s));
 #pragma unroll
-            for (int e = 0; e < 4; ++e) store_float_as(dst, to + ch + e, a.type, x[e]);
+        for (int e = 0; e < 4; ++e) {
+            lo[e] = d * (static_cast<float>((n >> (4 * e)) & 15u) - 8.0f);
+            hi[e] = d * (static_cast<float>((n >> (4 * e + 16)) & 15u) - 8.0f);
+        }
+    } else {
+        if (slot >= 0) record_error(a.err, kErrBadIndex);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) lo[e] = hi[e] = slot < 0 ? 0.0f : __int_as_float(0x7FC00000);
+    }
+    if (a.vec) {
+        store4(dst, to, a.type, lo);
+        store4(dst, to + 4, a.type, hi);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) store_float_as(dst, to + e, a.type, lo[e]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) store_float_as(dst, to + 4 + e, a.type, hi[e]);
     }
 }
 
@@ -381,9 +589,38 @@ cudaError_t launch(void (*kern)(const Args), int64_t grid, int threads, size_t s
     return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
+template <int D, int TYPE, bool APPEND>
+cudaError_t launch_heads(const RowsArgs &a, cudaStream_t st)
+{
+    constexpr int NG = kRowWarps * kRowsPerWarp<D>;
+    const int heads = a.n_q + a.n_k + a.n_v;
+    // four heads a lane share a table row and keep four loads going; few tokens spread over more blocks instead
+    const int64_t parts = (heads + 4 * NG - 1) / (4 * NG);
+    if (a.T * parts >= 304) return launch(heads_kernel<D, TYPE, 4, APPEND>, a.T * parts, kRowWarps * 32, 0, st, a);
+    return launch(heads_kernel<D, TYPE, 1, APPEND>, a.T * ((heads + NG - 1) / NG), kRowWarps * 32, 0, st, a);
+}
+
+template <int D, bool APPEND>
+cudaError_t launch_heads_type(const RowsArgs &a, cudaStream_t st)
+{
+    if (a.in_type == QK_F32) return launch_heads<D, QK_F32, APPEND>(a, st);
+    if (a.in_type == QK_F16) return launch_heads<D, QK_F16, APPEND>(a, st);
+    return launch_heads<D, QK_BF16, APPEND>(a, st);
+}
+
 template <bool APPEND>
 cudaError_t launch_rows(const RowsArgs &a, cudaStream_t st)
 {
+    const bool wide = a.vec_in && (a.vec_out || (APPEND && !a.n_q)) && a.rot % 8 == 0 && multiple(a.table, 16) &&
+                      multiple(a.q_weight, 16) && multiple(a.k_weight, 16);
+    if (wide) {
+        switch (a.D) {
+        case 64: return launch_heads_type<64, APPEND>(a, st);
+        case 96: return launch_heads_type<96, APPEND>(a, st);
+        case 128: return launch_heads_type<128, APPEND>(a, st);
+        case 256: return launch_heads_type<256, APPEND>(a, st);
+        }
+    }
     const int64_t grid = blocks_for(a.T * (a.n_q + a.n_k + a.n_v));
     if (a.D <= 128) return launch(rows_kernel<1, APPEND>, grid, kRowWarps * 32, 0, st, a);
     if (a.D <= 256) return launch(rows_kernel<2, APPEND>, grid, kRowWarps * 32, 0, st, a);
@@ -476,7 +713,7 @@ int qk_norm_rope(const void *x, int64_t ldx, int x_type, int n_q_heads, int n_k_
     if (!multiple(x, size_of(x_type)) || !multiple(y, size_of(y_type)) || !multiple(q_weight, 4) ||
         !multiple(k_weight, 4))
         return QK_ERR_ALIGN;
-    if (T > (static_cast<int64_t>(INT32_MAX) * kRowWarps) / heads) return QK_ERR_TOO_LARGE;
+    if (T > INT32_MAX / blocks_for(heads)) return QK_ERR_TOO_LARGE;
     RowsArgs a{};
     a.q = x, a.q_out = y;
     a.k = static_cast<const char *>(x) + static_cast<int64_t>(n_q_heads) * head_dim * size_of(x_type);
@@ -520,7 +757,7 @@ int qk_kv_append_q4(const qk_kv_cache_q4 *cache, const void *q, int64_t ldq, int
         !multiple(k_weight, 4) || (q && (!multiple(q, size_of(type)) || !multiple(q_out, size_of(q_out_type)))))
         return QK_ERR_ALIGN;
     const int64_t heads = static_cast<int64_t>(n_q_heads) + 2 * n_kv;
-    if (T > (static_cast<int64_t>(INT32_MAX) * kRowWarps) / heads) return QK_ERR_TOO_LARGE;
+    if (T > INT32_MAX / blocks_for(heads)) return QK_ERR_TOO_LARGE;
     RowsArgs a{};
     a.q = q, a.k = k, a.v = v, a.q_out = q_out;
     a.ldq = ldq, a.ldk = ldk, a.ldv = ldv, a.ldqo = ldqo;
@@ -552,7 +789,7 @@ int qk_kv_read_q4(const qk_kv_cache_q4 *cache, const int64_t *slots, int64_t T, 
     if (T == 0) return QK_OK;
     if (!slots || (!k && !v)) return QK_ERR_NULL;
     if (!multiple(slots, 8) || !multiple(k, size_of(type)) || !multiple(v, size_of(type))) return QK_ERR_ALIGN;
-    if (T > (static_cast<int64_t>(INT32_MAX) * kRowWarps) / (2 * cache->n_kv_heads)) return QK_ERR_TOO_LARGE;
+    if (T > INT32_MAX / blocks_for(2 * cache->n_kv_heads)) return QK_ERR_TOO_LARGE;
     ReadArgs a{};
     a.pages = static_cast<const uint8_t *>(cache->pages);
     a.n_slots = cache->n_pages * cache->page_tokens;
@@ -561,8 +798,8 @@ int qk_kv_read_q4(const qk_kv_cache_q4 *cache, const int64_t *slots, int64_t T, 
     a.vec = (!k || vec_ok(k, ldk, a.D, type)) && (!v || vec_ok(v, ldv, a.D, type));
     a.err = library_error_word();
     if (!a.err) return QK_ERR_CUDA;
-    const int64_t items = T * a.n_kv * ((k ? 1 : 0) + (v ? 1 : 0));
-    return launch(read_kernel, blocks_for(items), kRowWarps * 32, 0, reinterpret_cast<cudaStream_t>(stream), a) ==
+    const int64_t items = T * a.n_kv * ((k ? 1 : 0) + (v ? 1 : 0)) * (a.D / 8);
+    return launch(read_kernel, (items + kRowWarps * 32 - 1) / (kRowWarps * 32), kRowWarps * 32, 0, reinterpret_cast<cudaStream_t>(stream), a) ==
                    cudaSuccess
                ? QK_OK
                : QK_ERR_CUDA;

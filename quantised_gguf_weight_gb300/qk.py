@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 import torch
@@ -55,6 +56,8 @@ def library_path() -> str:
 def load(path: str | None = None):
     """Load the in-tree libqk.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -100,7 +103,7 @@ def load(path: str | None = None):
         lib.qk_set_strict_blocks.argtypes = [I]
         lib.qk_set_strict_blocks.restype = I
         F, D = ctypes.c_float, ctypes.c_double
-        C = ctypes.POINTER(_KVCacheQ4)
+        C = P      # a qk_kv_cache_q4, as its bytes
         lib.qk_rope_table.argtypes = [P, I64, I, D, D, P, I64, D, D, D, P]
         lib.qk_norm_rope.argtypes = [P, I64, I, I, I, I, P, P, F, P, I64, I, I, P, I64, P, I64, I, P]
         lib.qk_kv_append_q4.argtypes = [C, P, I64, I, P, I64, P, I64, I, P, P, F, P, I64, I, I, P, P, I64, P, I64,
@@ -126,8 +129,14 @@ def load(path: str | None = None):
         return lib
 
 
+# the current stream's handle without the Stream object around it (0.1 us against 2.9 us a call on the Grace host)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -367,52 +376,67 @@ def qgemm_swiglu_q4_k(w, gate_offset, up_offset, F, K, x, h=None, ldh=0, workspa
 
 # ---------------------------------------------------------------- attention operators
 
-def _rows(t, width: int, name: str, dtype=None) -> None:
-    """Rows of `width` elements of an element type the attention operators take, unit stride inside a row."""
-    _on_device(t, name, dtype)
-    if t.dtype not in DTYPES:
+# A call of a small shape costs what its host side costs, so the checks below ask each tensor once and cheaply.
+_CACHE_BYTES = struct.Struct("@Pqiii4x").pack        # qk_kv_cache_q4
+
+
+def _rows(t, width: int, name: str, dev: int, dtype=None) -> tuple[int, int, int]:
+    """(rows, row stride, element type) of rows of `width` elements with unit stride inside a row."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or (dtype is not None and t.dtype is not dtype):
+        _on_device(t, name, dtype)
+    code = DTYPES.get(t.dtype)
+    if code is None:
         raise ValueError(f"{name} must be float32, float16 or bfloat16, not {t.dtype}")
-    if t.dim() != 2 or t.shape[1] != width or (width > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name} must be rows of {width} elements with unit stride, got shape {tuple(t.shape)} "
-                         f"stride {t.stride()}")
-    if t.shape[0] > 1 and t.stride(0) < width:
-        raise ValueError(f"{name} rows are {t.stride(0)} elements apart, less than their {width}")
+    shape = t.shape
+    if len(shape) != 2 or shape[1] != width:
+        raise ValueError(f"{name} must be rows of {width} elements, got shape {tuple(shape)}")
+    n = shape[0]
+    ld, unit = t.stride()
+    if unit != 1 and width > 1:
+        raise ValueError(f"{name} must have unit stride inside a row, got {unit}")
+    if n <= 1:
+        ld = width         # a single row has no stride of its own
+    elif ld < width:
+        raise ValueError(f"{name} rows are {ld} elements apart, less than their {width}")
+    return n, ld, code
 
 
-def _ld(t, width: int) -> int:
-    """Row stride of a checked tensor (a single row has none)."""
-    return t.stride(0) if t.shape[0] > 1 else width
-
-
-def _vector(t, n: int, dtype, name: str):
+def _vector(t, n: int, dtype, name: str, dev: int):
     """Pointer of a contiguous vector of at least n elements (None: null)."""
     if t is None:
         return None
-    _on_device(t, name, dtype)
-    if not t.is_contiguous() or t.numel() < n:
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype is not dtype:
+        _on_device(t, name, dtype)
+    if t.numel() < n or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous with at least {n} elements")
     return t.data_ptr()
 
 
-def _table(table, positions, T: int, D: int):
+def _table(table, positions, T: int, D: int, dev: int):
     """(table pointer, positions in it, rotating channels, positions pointer)."""
     if table is None:
         return None, 0, 0, None
-    _on_device(table, "table", torch.float32)
-    if table.dim() != 3 or table.shape[2] != 2 or not table.is_contiguous() or 2 * table.shape[1] > D:
-        raise ValueError(f"table must be contiguous [n_pos][rot/2][2] with rot <= {D}, got {tuple(table.shape)}")
+    if not isinstance(table, torch.Tensor) or table.get_device() != dev or table.dtype is not torch.float32:
+        _on_device(table, "table", torch.float32)
+    shape = table.shape
+    if len(shape) != 3 or shape[2] != 2 or 2 * shape[1] > D or not table.is_contiguous():
+        raise ValueError(f"table must be contiguous [n_pos][rot/2][2] with rot <= {D}, got {tuple(shape)}")
     if positions is None:
         raise ValueError("positions are needed with a table")
-    return table.data_ptr(), table.shape[0], 2 * table.shape[1], _vector(positions, T, torch.int32, "positions")
+    return table.data_ptr(), shape[0], 2 * shape[1], _vector(positions, T, torch.int32, "positions", dev)
 
 
-def _cache(cache) -> _KVCacheQ4:
-    _on_device(cache, "cache", torch.uint8)
-    if cache.dim() != 4 or not cache.is_contiguous() or cache.shape[3] % 18:
+def _cache(cache, dev: int) -> tuple[bytes, int, int]:
+    """(qk_kv_cache_q4 as bytes, kv heads, head size) of a cache tensor."""
+    if not isinstance(cache, torch.Tensor) or cache.get_device() != dev or cache.dtype is not torch.uint8:
+        _on_device(cache, "cache", torch.uint8)
+    shape = cache.shape
+    if len(shape) != 4 or shape[3] % 18 or not cache.is_contiguous():
         raise ValueError("cache must be a contiguous uint8 tensor [pages][kv heads][page_tokens/16][18*head_dim] "
-                         f"(kv_cache_q4), got shape {tuple(cache.shape)}")
-    n, h, b, s = cache.shape
-    return _KVCacheQ4(cache.data_ptr(), n, h, s // 18, 16 * b)
+                         f"(kv_cache_q4), got shape {tuple(shape)}")
+    n, h, b, size = shape
+    D = size // 18
+    return _CACHE_BYTES(cache.data_ptr(), n, h, D, 16 * b), h, D
 
 
 def rope_table(n_pos: int, rot: int, base: float = 10000.0, freq_scale: float = 1.0,
@@ -421,12 +445,12 @@ def rope_table(n_pos: int, rot: int, base: float = 10000.0, freq_scale: float = 
                stream=None) -> torch.Tensor:
     """[n_pos][rot/2][2] fp32 (cos, sin) of the position angles; freq_scale interpolates positions, freq_factors
     divides each frequency, orig_ctx > 0 ramps between kept and interpolated frequencies (see include/qk.h)."""
+    dev = torch.cuda.current_device()
     if table is None:
         table = torch.empty((max(n_pos, 0), max(rot, 0) // 2, 2), dtype=torch.float32, device="cuda")
-    _vector(table, n_pos * (rot // 2) * 2, torch.float32, "table")
-    st = load().qk_rope_table(table.data_ptr(), n_pos, rot, base, freq_scale,
-                              _vector(freq_factors, rot // 2, torch.float32, "freq_factors"), orig_ctx, beta_fast,
-                              beta_slow, amplitude, _stream(stream))
+    st = load().qk_rope_table(_vector(table, n_pos * (rot // 2) * 2, torch.float32, "table", dev), n_pos, rot, base,
+                              freq_scale, _vector(freq_factors, rot // 2, torch.float32, "freq_factors", dev),
+                              orig_ctx, beta_fast, beta_slow, amplitude, _stream(stream))
     _check(st, "qk_rope_table")
     return table
 
@@ -437,21 +461,20 @@ def norm_rope(x: torch.Tensor, n_q_heads: int, n_k_heads: int, head_dim: int, po
               y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """RMS norm of every head (a weight of None: no norm) and rotation of its first channels by the table's row of
     the token's position, over rows of n_q_heads + n_k_heads heads.  y may be x."""
+    dev = torch.cuda.current_device()
     width = (n_q_heads + n_k_heads) * head_dim
-    _rows(x, width, "x")
-    T = x.shape[0]
+    T, ldx, xt = _rows(x, width, "x", dev)
     if y is None:
-        y = torch.empty((T, width), dtype=x.dtype, device=x.device)
+        y, ldy, yt = torch.empty((T, width), dtype=x.dtype, device=x.device), width, xt
     else:
-        _rows(y, width, "y")
-        if y.shape[0] < T:
-            raise ValueError(f"y has {y.shape[0]} rows, x {T}")
-    tp, n_pos, rot, pp = _table(table, positions, T, head_dim)
-    st = load().qk_norm_rope(x.data_ptr(), _ld(x, width), DTYPES[x.dtype], n_q_heads, n_k_heads, head_dim,
-                             _vector(q_weight, head_dim, torch.float32, "q_weight"),
-                             _vector(k_weight, head_dim, torch.float32, "k_weight"), eps, tp, n_pos, rot,
-                             1 if interleaved else 0, pp, T, y.data_ptr(), _ld(y, width), DTYPES[y.dtype],
-                             _stream(stream))
+        n, ldy, yt = _rows(y, width, "y", dev)
+        if n < T:
+            raise ValueError(f"y has {n} rows, x {T}")
+    tp, n_pos, rot, pp = _table(table, positions, T, head_dim, dev)
+    st = load().qk_norm_rope(x.data_ptr(), ldx, xt, n_q_heads, n_k_heads, head_dim,
+                             _vector(q_weight, head_dim, torch.float32, "q_weight", dev),
+                             _vector(k_weight, head_dim, torch.float32, "k_weight", dev), eps, tp, n_pos, rot,
+                             1 if interleaved else 0, pp, T, y.data_ptr(), ldy, yt, _stream(stream))
     _check(st, "qk_norm_rope")
     return y
 
@@ -470,33 +493,36 @@ def kv_append_q4(cache: torch.Tensor, q: torch.Tensor | None, k: torch.Tensor, v
                  interleaved: bool = False, q_out: torch.Tensor | None = None, stream=None) -> torch.Tensor | None:
     """Norm and rotation of T tokens' queries and keys, with keys and values stored into `cache` at `slots` (int64;
     negative: not stored).  Returns the queries (rows of q's heads; q_out may be q), None without q."""
-    c = _cache(cache)
-    D, width = c.head_dim, c.n_kv_heads * c.head_dim
-    _rows(k, width, "k")
-    _rows(v, width, "v", k.dtype)
-    T = k.shape[0]
-    if v.shape[0] != T:
-        raise ValueError(f"k has {T} rows, v {v.shape[0]}")
-    sp = _vector(slots, T, torch.int64, "slots")
-    tp, n_pos, rot, pp = _table(table, positions, T, D)
-    wq = heads = 0
+    dev = torch.cuda.current_device()
+    c, n_kv, D = _cache(cache, dev)
+    width = n_kv * D
+    T, ldk, kt = _rows(k, width, "k", dev)
+    n, ldv, _ = _rows(v, width, "v", dev, k.dtype)
+    if n != T:
+        raise ValueError(f"k has {T} rows, v {n}")
+    sp = _vector(slots, T, torch.int64, "slots", dev)
+    tp, n_pos, rot, pp = _table(table, positions, T, D, dev)
+    qp = qop = None
+    heads = ldq = ldo = ot = 0
     if q is not None:
         wq = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 2 else 0
         if wq == 0 or wq % D:
             raise ValueError(f"q must be rows of heads of {D} channels")
-        _rows(q, wq, "q", k.dtype)
+        n, ldq, _ = _rows(q, wq, "q", dev, k.dtype)
+        if n != T:
+            raise ValueError(f"q has {n} rows, k {T}")
         heads = wq // D
         if q_out is None:
-            q_out = torch.empty((T, wq), dtype=q.dtype, device=q.device)
-        _rows(q_out, wq, "q_out")
-        if q.shape[0] != T or q_out.shape[0] < T:
-            raise ValueError(f"q has {q.shape[0]} and q_out {q_out.shape[0]} rows, k {T}")
-    st = load().qk_kv_append_q4(
-        ctypes.byref(c), q.data_ptr() if heads else None, _ld(q, wq) if heads else 0, heads, k.data_ptr(),
-        _ld(k, width), v.data_ptr(), _ld(v, width), DTYPES[k.dtype],
-        _vector(q_weight, D, torch.float32, "q_weight"), _vector(k_weight, D, torch.float32, "k_weight"), eps, tp,
-        n_pos, rot, 1 if interleaved else 0, pp, sp, T, q_out.data_ptr() if heads else None,
-        _ld(q_out, wq) if heads else 0, DTYPES[q_out.dtype] if heads else 0, _stream(stream))
+            q_out, ldo, ot = torch.empty((T, wq), dtype=q.dtype, device=q.device), wq, kt
+        else:
+            n, ldo, ot = _rows(q_out, wq, "q_out", dev)
+            if n < T:
+                raise ValueError(f"q_out has {n} rows, q {T}")
+        qp, qop = q.data_ptr(), q_out.data_ptr()
+    st = load().qk_kv_append_q4(c, qp, ldq, heads, k.data_ptr(), ldk, v.data_ptr(), ldv, kt,
+                                _vector(q_weight, D, torch.float32, "q_weight", dev),
+                                _vector(k_weight, D, torch.float32, "k_weight", dev), eps, tp, n_pos, rot,
+                                1 if interleaved else 0, pp, sp, T, qop, ldo, ot, _stream(stream))
     _check(st, "qk_kv_append_q4")
     return q_out if heads else None
 
@@ -504,16 +530,18 @@ def kv_append_q4(cache: torch.Tensor, q: torch.Tensor | None, k: torch.Tensor, v
 def kv_read_q4(cache: torch.Tensor, slots: torch.Tensor, dtype: torch.dtype = torch.float16,
                stream=None) -> tuple[torch.Tensor, torch.Tensor]:
     """The keys and values that the cache holds at `slots`: two [T][kv heads * head_dim] tensors of `dtype`."""
-    c = _cache(cache)
-    if dtype not in DTYPES:
+    dev = torch.cuda.current_device()
+    c, n_kv, D = _cache(cache, dev)
+    code = DTYPES.get(dtype)
+    if code is None:
         raise ValueError(f"dtype must be float32, float16 or bfloat16, not {dtype}")
     T = slots.numel()
-    sp = _vector(slots, T, torch.int64, "slots")
-    kv = torch.empty((2, T, c.n_kv_heads * c.head_dim), dtype=dtype, device=cache.device)
-    st = load().qk_kv_read_q4(ctypes.byref(c), sp, T, kv[0].data_ptr(), 0, kv[1].data_ptr(), 0, DTYPES[dtype],
-                              _stream(stream))
+    sp = _vector(slots, T, torch.int64, "slots", dev)
+    k = torch.empty((T, n_kv * D), dtype=dtype, device=cache.device)
+    v = torch.empty((T, n_kv * D), dtype=dtype, device=cache.device)
+    st = load().qk_kv_read_q4(c, sp, T, k.data_ptr(), 0, v.data_ptr(), 0, code, _stream(stream))
     _check(st, "qk_kv_read_q4")
-    return kv[0], kv[1]
+    return k, v
 
 
 def attn_q4_workspace(B: int, n_q_heads: int, n_kv_heads: int, head_dim: int, max_q: int = 1, max_len: int = 0,
@@ -531,38 +559,41 @@ def attn_q4(cache: torch.Tensor, q: torch.Tensor, page_table: torch.Tensor, lens
     pages page_table[b], and the rows q_start[b]..q_start[b+1] (None: max_q each) as its last positions.  scale
     defaults to head_dim^-0.5; window > 0 lets a row see that many keys up to its own.  `workspace` (zeroed once,
     attn_q4_workspace) lets long sequences spread over the GPU; without it they are not split."""
-    c = _cache(cache)
-    D = c.head_dim
+    dev = torch.cuda.current_device()
+    c, n_kv, D = _cache(cache, dev)
     width = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 2 else 0
-    if width == 0 or width % (D * c.n_kv_heads):
-        raise ValueError(f"q must be rows of a multiple of {c.n_kv_heads} heads of {D} channels")
-    _rows(q, width, "q")
-    T, B = q.shape[0], lens.numel()
-    lp = _vector(lens, B, torch.int32, "lens")
-    _on_device(page_table, "page_table", torch.int32)
-    if page_table.dim() != 2 or page_table.shape[0] < B or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
-        raise ValueError(f"page_table must be [{B}][pages] with unit stride, got {tuple(page_table.shape)}")
-    pages = page_table.shape[1]
-    ld = page_table.stride(0) if page_table.shape[0] > 1 else pages
-    if ld < pages:
-        raise ValueError(f"page_table rows are {ld} entries apart, less than their {pages}")
-    qs = _vector(q_start, B + 1, torch.int32, "q_start")
+    if width == 0 or width % (D * n_kv):
+        raise ValueError(f"q must be rows of a multiple of {n_kv} heads of {D} channels")
+    T, ldq, qt = _rows(q, width, "q", dev)
+    B = lens.numel()
+    lp = _vector(lens, B, torch.int32, "lens", dev)
+    if page_table.get_device() != dev or page_table.dtype is not torch.int32:
+        _on_device(page_table, "page_table", torch.int32)
+    if page_table.dim() != 2 or page_table.shape[0] < B:
+        raise ValueError(f"page_table must be [{B}][pages], got {tuple(page_table.shape)}")
+    rows, pages = page_table.shape
+    ld, unit = page_table.stride()
+    if rows <= 1:
+        ld = pages
+    if (unit != 1 and pages > 1) or ld < pages:
+        raise ValueError(f"page_table must have unit stride and rows at least {pages} apart, got {(ld, unit)}")
     if out is None:
-        out = torch.empty((T, width), dtype=q.dtype, device=q.device)
+        out, ldo, ot = torch.empty((T, width), dtype=q.dtype, device=q.device), width, qt
     else:
-        _rows(out, width, "out")
-        if out.shape[0] < T:
-            raise ValueError(f"out has {out.shape[0]} rows, q {T}")
+        n, ldo, ot = _rows(out, width, "out", dev)
+        if n < T:
+            raise ValueError(f"out has {n} rows, q {T}")
     wp, wb = None, 0
     if workspace is not None:
-        _on_device(workspace, "workspace")
+        if workspace.get_device() != dev:
+            _on_device(workspace, "workspace")
         if not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
-        wp, wb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    st = load().qk_attn_q4(ctypes.byref(c), q.data_ptr(), _ld(q, width), DTYPES[q.dtype], width // D,
-                           page_table.data_ptr(), ld, pages, lp, qs, B, T, max_q, max_len,
-                           D ** -0.5 if scale is None else scale, window, out.data_ptr(), _ld(out, width),
-                           DTYPES[out.dtype], wp, wb, _stream(stream))
+        wp, wb = workspace.data_ptr(), workspace.nbytes
+    st = load().qk_attn_q4(c, q.data_ptr(), ldq, qt, width // D, page_table.data_ptr(), ld, pages, lp,
+                           _vector(q_start, B + 1, torch.int32, "q_start", dev), B, T, max_q, max_len,
+                           D ** -0.5 if scale is None else scale, window, out.data_ptr(), ldo, ot, wp, wb,
+                           _stream(stream))
     _check(st, "qk_attn_q4")
     return out
 
