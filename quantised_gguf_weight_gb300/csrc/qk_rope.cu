@@ -9,6 +9,7 @@
 // scale is three shuffles.  All of it is bound by the bytes of the rows.
 #include <cfloat>
 #include <cmath>
+#include <type_traits>
 
 #include "qk_device.cuh"
 #include "qk_internal.h"
@@ -264,15 +265,34 @@ __global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const RowsArgs a)
 // which do not rotate) take eight neighbours; the half layout takes
 // 4i..4i+3 and their partners half + 4i.., so a pair is always in one lane and
 // nothing is exchanged.  The lanes of a token's heads share its table row and
-// keep it in registers over HPT heads.
-struct Chunks {
-    int a, b;        // first channels of the lane's two chunks
-    bool turn;       // they rotate
-};
-__device__ __forceinline__ Chunks chunks_of(int i, int rot, bool interleaved)
+// keep it in registers over up to kHeadsPerLane heads.
+constexpr int kHeadsPerLane = 4;
+
+template <int D>
+constexpr int kRowsPerWarp = D == 96 ? 2 : 256 / D;
+
+// Nibbles floor(x / d + 8.5) of eight values, d != 0.  The product with 1/d
+// is within 2^-17 of the quotient; lowered by twice that it gives the floor or
+// one less, and the comparison of x with the next edge, (n - 7.5) * d, which
+// fp32 holds exactly, tells which.  (Quotients on an edge are common: x and d
+// have few bits when the values come in 16.)
+__device__ __forceinline__ uint32_t nibbles_of(const float (&x)[8], float d)
 {
-    if (interleaved || 8 * i >= rot) return {8 * i, 8 * i + 4, 8 * i < rot};
-    return {4 * i, (rot >> 1) + 4 * i, true};
+    // 1/d of a subnormal fp16 is at most 2^24; the quotient is within +-16
+    const float step = fabsf(d), inv = __fdividef(1.0f, step);
+    const uint32_t sign = __float_as_uint(d) & 0x80000000u;
+    float w[2];
+#pragma unroll
+    for (int half = 0; half < 2; ++half)
+#pragma unroll
+        for (int e = 3; e >= 0; --e) {
+            const float v = __uint_as_float(__float_as_uint(x[4 * half + e]) ^ sign);
+            float n = __fadd_rd(fmaf(v, inv, 8.5f - 1.6e-5f), kTwo23) - kTwo23;
+            if (fmaf(7.5f - n, step, v) >= 0.0f) n += 1.0f;
+            n = fminf(fmaxf(n, 0.0f), 15.0f);
+            w[half] = e == 3 ? n : fmaf(w[half], 16.0f, n);     // four nibbles are exact in fp32
+        }
+    return static_cast<uint32_t>(w[0]) | static_cast<uint32_t>(w[1]) << 16;
 }
 
 // Eight neighbouring channels of a head to the cache: the group's scale over
@@ -282,12 +302,13 @@ __device__ __forceinline__ void store_eight(uint8_t *block, int t, int ch, bool 
                                             int lane)
 {
     float hi = x[0], lo = x[0];
-    bool odd = false;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        hi = fmaxf(hi, x[e]), lo = fminf(lo, x[e]);
-        odd |= !(fabsf(x[e]) <= FLT_MAX);
-    }
+    for (int e = 1; e < 8; ++e) hi = fmaxf(hi, x[e]), lo = fminf(lo, x[e]);
+    // a NaN or an infinity: 0 * x is NaN for these alone
+    float zero = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) zero = fmaf(x[e], 0.0f, zero);
+    const bool odd = !(zero == 0.0f);
 #pragma unroll
     for (int o = 1; o < 4; o <<= 1) {
         hi = fmaxf(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, o));
@@ -300,21 +321,14 @@ __device__ __forceinline__ void store_eight(uint8_t *block, int t, int ch, bool 
     const float want = fminf(fmaxf(m * -0.125f, -65504.0f), 65504.0f);
     const __half dh = group_odd ? __ushort_as_half(0x7FFF) : __float2half_rn(want);
     const float d = __half2float(dh);
-    uint32_t bits = 0x88888888u;
-    if (d != 0.0f && !group_odd) {
-        bits = 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float n = fminf(fmaxf(floorf(__fadd_rn(__fdiv_rn(x[e], d), 8.5f)), 0.0f), 15.0f);
-            bits |= static_cast<uint32_t>(n) << (4 * e);
-        }
-    }
+    const uint32_t bits = d != 0.0f && !group_odd ? nibbles_of(x, d) : 0x88888888u;
     if (is_key) {
         *reinterpret_cast<uint32_t *>(block + kv4_key_place(D, t, ch).byte) = bits;
     } else {
-        const Kv4Place p = kv4_value_place(D, t, ch), q = kv4_value_place(D, t, ch + 4);
-        *reinterpret_cast<uint16_t *>(block + p.byte + (p.nibble >> 1)) = static_cast<uint16_t>(bits);
-        *reinterpret_cast<uint16_t *>(block + q.byte + (q.nibble >> 1)) = static_cast<uint16_t>(bits >> 16);
+        // the next four channels are one r further
+        uint8_t *to = block + kv4_value_place(D, t, ch).byte + 2 * (t & 1);
+        *reinterpret_cast<uint16_t *>(to) = static_cast<uint16_t>(bits);
+        *reinterpret_cast<uint16_t *>(to + 16 * kv4_gp(D / 32)) = static_cast<uint16_t>(bits >> 16);
     }
     if ((lane & 3) == 0) {
         const int s = is_key ? kv4_key_scale(D, t, ch >> 5) : kv4_value_scale(D, t, ch >> 5);
@@ -322,136 +336,212 @@ __device__ __forceinline__ void store_eight(uint8_t *block, int t, int ch, bool 
     }
 }
 
-template <int D>
-constexpr int kRowsPerWarp = D == 96 ? 2 : 256 / D;
-
-template <int D, int TYPE, int HPT, bool APPEND>
-__global__ void __launch_bounds__(kRowWarps * 32) heads_kernel(const RowsArgs a)
+// 1 / sqrt(m): the approximation and one Newton step, within 1 ulp.  Where m
+// is 0, an infinity, a NaN or a subnormal (which the approximation takes as 0)
+// the step is left out.
+__device__ __forceinline__ float rsqrt_newton(float m)
 {
-    constexpr int LPR = D / 8, RPW = kRowsPerWarp<D>, NG = kRowWarps * RPW;
-    __shared__ __align__(16) float turn[APPEND ? kRowWarps * RPW : 1][APPEND ? D : 4];
+    float r;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(m));
+    const float e = fmaf(-m * r, r, 1.0f);
+    return fabsf(e) <= 1.0f ? fmaf(0.5f * r, e, r) : r;
+}
+
+// Norm and rotation of a lane's eight channels.  Pair e is neighbours 2e,
+// 2e + 1 of the eight, or element e of both chunks.
+template <int D, bool INTER>
+__device__ __forceinline__ void turn_eight(float (&x)[8], bool norm, bool weigh, const float (&w)[8], float eps,
+                                           bool turn, const float (&c)[4], const float (&s)[4], int sub)
+{
+    constexpr int LPR = D / 8;
+    if (norm) {       // warp-uniform: some row of the call has a weight
+        float q = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) q = fmaf(x[e], x[e], q);
+        if constexpr (D == 96) {      // 12 lanes a row: groups of four stay inside it
+            q += __shfl_xor_sync(0xFFFFFFFFu, q, 1);
+            q += __shfl_xor_sync(0xFFFFFFFFu, q, 2);
+            const int first = sub * LPR;
+            q = __shfl_sync(0xFFFFFFFFu, q, first) + __shfl_sync(0xFFFFFFFFu, q, first + 4) +
+                __shfl_sync(0xFFFFFFFFu, q, (first + 8) & 31);
+        } else {
+#pragma unroll
+            for (int o = LPR / 2; o; o >>= 1) q += __shfl_xor_sync(0xFFFFFFFFu, q, o);
+        }
+        const float r = weigh ? rsqrt_newton(__fadd_rn(q * (1.0f / D), eps)) : 1.0f;   // without: the weights are 1
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = __fmul_rn(__fmul_rn(x[e], r), w[e]);
+    }
+    // each product and sum is rounded by itself, so the stored nibbles do not depend on how a compiler fuses them
+    if (turn)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            constexpr int step = INTER ? 2 : 1, other = INTER ? 1 : 4;
+            const float u = x[step * e], v = x[step * e + other];
+            x[step * e] = __fsub_rn(__fmul_rn(u, c[e]), __fmul_rn(v, s[e]));
+            x[step * e + other] = __fadd_rn(__fmul_rn(u, s[e]), __fmul_rn(v, c[e]));
+        }
+}
+
+__device__ __forceinline__ void load_weights(float (&w)[8], const float *weight, int ca, int cb)
+{
+    float4 u = make_float4(1.0f, 1.0f, 1.0f, 1.0f), v = u;
+    if (weight) u = *reinterpret_cast<const float4 *>(weight + ca), v = *reinterpret_cast<const float4 *>(weight + cb);
+    w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w, w[4] = v.x, w[5] = v.y, w[6] = v.z, w[7] = v.w;
+}
+
+// Four elements as they lie in memory, and as floats.
+template <int TYPE>
+struct Raw {
+    using Word = typename std::conditional<TYPE == QK_F32, uint4, uint2>::type;
+    static constexpr int size = TYPE == QK_F32 ? 4 : 2;
+    Word w;
+    __device__ __forceinline__ void load(const uint8_t *p) { w = *reinterpret_cast<const Word *>(p); }
+    __device__ __forceinline__ void poison()      // a NaN in every type
+    {
+        if constexpr (TYPE == QK_F32) w = make_uint4(0x7FFFFFFFu, 0x7FFFFFFFu, 0x7FFFFFFFu, 0x7FFFFFFFu);
+        else w = make_uint2(0x7FFF7FFFu, 0x7FFF7FFFu);
+    }
+    __device__ __forceinline__ void to(float *x) const
+    {
+        if constexpr (TYPE == QK_F32) {
+            x[0] = __uint_as_float(w.x), x[1] = __uint_as_float(w.y);
+            x[2] = __uint_as_float(w.z), x[3] = __uint_as_float(w.w);
+        } else if constexpr (TYPE == QK_F16) {
+            const float2 u = __half22float2(*reinterpret_cast<const __half2 *>(&w.x));
+            const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&w.y));
+            x[0] = u.x, x[1] = u.y, x[2] = v.x, x[3] = v.y;
+        } else {
+            x[0] = __uint_as_float(w.x << 16), x[1] = __uint_as_float(w.x & 0xFFFF0000u);
+            x[2] = __uint_as_float(w.y << 16), x[3] = __uint_as_float(w.y & 0xFFFF0000u);
+        }
+    }
+};
+
+template <int D, int TYPE, bool INTER, bool APPEND>
+__global__ void __launch_bounds__(kRowWarps * 32) heads_kernel(const RowsArgs a, int hpl_front, int hpl_back, int q_parts,
+                                                                int parts)
+{
+    constexpr int LPR = D / 8, RPW = kRowsPerWarp<D>, NG = kRowWarps * RPW, size = Raw<TYPE>::size;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int sub = lane / LPR, i = lane - sub * LPR;            // row of the warp, lane of the row
     const bool on = sub < RPW;                                   // 96 channels leave 8 lanes idle
-    const int heads = a.n_q + a.n_k + a.n_v, parts = (heads + NG * HPT - 1) / (NG * HPT);
-    const int64_t t = blockIdx.x / parts;
-    const int h0 = static_cast<int>(blockIdx.x - t * parts) * NG * HPT + warp * RPW + sub;
-    const Chunks pair = chunks_of(i, a.rot, a.interleaved != 0), plain = {8 * i, 8 * i + 4, false};
+    const int t = static_cast<int>(blockIdx.x) / parts, part = static_cast<int>(blockIdx.x) - t * parts;
+    const bool front = !APPEND || part < q_parts;                // rows that go out; else rows that are stored
+    const int hpl = front ? hpl_front : hpl_back;                // heads a lane
+    const int h0 = (front ? part : part - q_parts) * NG * hpl + warp * RPW + sub;
+    const int heads = !APPEND ? a.n_q + a.n_k : (front ? a.n_q : 2 * a.n_k);
+    const int mine = on && h0 < heads ? min(hpl, (heads - h0 + NG - 1) / NG) : 0;       // heads of this lane
+    const int first_mine = front ? a.n_q : a.n_k;                                       // those before it are q, or keys
+    const bool turn = on && 8 * i < a.rot;
+    const int ca = INTER || !turn ? 8 * i : 4 * i, cb = INTER || !turn ? 8 * i + 4 : (a.rot >> 1) + 4 * i;
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
-    bool bad = false;
-    int32_t pos = 0;
-    if (a.rot > 0) {
-        pos = a.positions[t];
-        bad = pos < 0 || pos >= a.n_pos;
-        if (bad) {
-            pos = 0;
-            if (threadIdx.x == 0) record_error(a.err, kErrBadIndex);
-        }
-    }
-    float x[HPT][8];
+    // rows and position first, together: nothing waits before all of it is on its way
+    int32_t pos = a.rot > 0 ? a.positions[t] : 0;
+    Raw<TYPE> xa[kHeadsPerLane], xb[kHeadsPerLane];
+    {
+        const uint8_t *pa = static_cast<const uint8_t *>(front ? a.q : a.k) +
+                            (static_cast<int64_t>(t) * (front ? a.ldq : a.ldk) + h0 * D) * size;
+        const uint8_t *pv = APPEND && !front ? static_cast<const uint8_t *>(a.v) +
+                                                   (static_cast<int64_t>(t) * a.ldv + (h0 - a.n_k) * D + 8 * i) * size
+                                             : nullptr;
 #pragma unroll
-    for (int k = 0; k < HPT; ++k) {
-        const int h = h0 + k * NG;
-        const bool is_q = h < a.n_q, is_v = h >= a.n_q + a.n_k;
-        const Chunks ch = is_v ? plain : pair;
-        const void *src = is_q ? a.q : (is_v ? a.v : a.k);
-        const int64_t at = t * (is_q ? a.ldq : (is_v ? a.ldv : a.ldk)) +
-                           static_cast<int64_t>(is_q ? h : (is_v ? h - a.n_q - a.n_k : h - a.n_q)) * D;
-        float lo[4] = {}, hi[4] = {};
-        if (on && h < heads) load4(src, at + ch.a, TYPE, lo), load4(src, at + ch.b, TYPE, hi);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[k][e] = lo[e], x[k][4 + e] = hi[e];
-    }
-    float cs[8];          // (cos, sin) of the lane's four pairs
-#pragma unroll
-    for (int e = 0; e < 8; ++e) cs[e] = 0.0f;
-    if (on && pair.turn) {
-        const float4 *row = reinterpret_cast<const float4 *>(a.table + static_cast<int64_t>(pos) * (a.rot >> 1) + 4 * i);
-        const float4 u = row[0], v = row[1];
-        cs[0] = u.x, cs[1] = u.y, cs[2] = u.z, cs[3] = u.w, cs[4] = v.x, cs[5] = v.y, cs[6] = v.z, cs[7] = v.w;
-    }
-    int64_t slot = -1;
-    if (APPEND) slot = a.slots[t];
-#pragma unroll
-    for (int k = 0; k < HPT; ++k) {
-        const int h = h0 + k * NG;
-        const bool is_q = h < a.n_q, is_v = h >= a.n_q + a.n_k;
-        const float *weight = is_q ? a.q_weight : (is_v ? nullptr : a.k_weight);
-        if (a.q_weight || a.k_weight) {
-            float s = 0.0f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) s = fmaf(x[k][e], x[k][e], s);
-            if constexpr (D == 96) {      // 12 lanes a row: 8 + 4 by halving, the odd third added last
-                s += __shfl_xor_sync(0xFFFFFFFFu, s, 1);     // rows begin at lanes 0 and 12: pairs stay inside
-                s += __shfl_xor_sync(0xFFFFFFFFu, s, 2);     // and groups of four too
-                const int first = sub * LPR;
-                s = __shfl_sync(0xFFFFFFFFu, s, first) + __shfl_sync(0xFFFFFFFFu, s, first + 4) +
-                    __shfl_sync(0xFFFFFFFFu, s, (first + 8) & 31);
-            } else {
-#pragma unroll
-                for (int o = LPR / 2; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-            }
-            if (weight && on) {
-                const float r = __frsqrt_rn(__fadd_rn(__fdiv_rn(s, static_cast<float>(D)), a.eps));
-                const float4 u = *reinterpret_cast<const float4 *>(weight + pair.a);
-                const float4 v = *reinterpret_cast<const float4 *>(weight + pair.b);
-                const float w[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[k][e] = __fmul_rn(__fmul_rn(x[k][e], r), w[e]);
-            }
-        }
-        if (pair.turn && !is_v) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                // pair e: neighbours 2e, 2e + 1 of the eight, or e of both chunks
-                float &p = a.interleaved ? x[k][2 * e] : x[k][e], &q = a.interleaved ? x[k][2 * e + 1] : x[k][4 + e];
-                const float c = cs[2 * e], s = cs[2 * e + 1], u = p, v = q;
-                p = __fsub_rn(__fmul_rn(u, c), __fmul_rn(v, s));
-                q = __fadd_rn(__fmul_rn(u, s), __fmul_rn(v, c));
-            }
-        }
-        if (bad && !is_v)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[k][e] = __int_as_float(0x7FC00000);
-        if (!APPEND || is_q) {
-            void *dst = is_q ? a.q_out : a.k_out;
-            const int64_t to = t * (is_q ? a.ldqo : a.ldko) + static_cast<int64_t>(is_q ? h : h - a.n_q) * D;
-            if (on && h < heads) {
-                const float lo[4] = {x[k][0], x[k][1], x[k][2], x[k][3]}, hi[4] = {x[k][4], x[k][5], x[k][6], x[k][7]};
-                store4(dst, to + pair.a, a.out_type, lo);
-                store4(dst, to + pair.b, a.out_type, hi);
-            }
-        }
-        if constexpr (APPEND) {
-            // a warp with a key or value row among its rows stores them (queries of the same warp only take part)
-            const bool store = !is_q && h < heads && on && slot >= 0 && slot < a.n_slots;
-            if (__any_sync(0xFFFFFFFFu, !is_q && h < heads)) {
-                if (!is_q && h < heads && on && slot >= a.n_slots && i == 0) record_error(a.err, kErrBadIndex);
-                if (!a.interleaved) {      // eight neighbours a lane, as the cache wants them
-                    float *row = turn[warp * RPW + (on ? sub : 0)];
-                    const Chunks ch = is_v ? plain : pair;
-                    if (on) {
-                        *reinterpret_cast<float4 *>(row + ch.a) = make_float4(x[k][0], x[k][1], x[k][2], x[k][3]);
-                        *reinterpret_cast<float4 *>(row + ch.b) = make_float4(x[k][4], x[k][5], x[k][6], x[k][7]);
-                    }
-                    __syncwarp();
-                    if (on) {
-                        const float4 u = *reinterpret_cast<const float4 *>(row + 8 * i);
-                        const float4 v = *reinterpret_cast<const float4 *>(row + 8 * i + 4);
-                        x[k][0] = u.x, x[k][1] = u.y, x[k][2] = u.z, x[k][3] = u.w;
-                        x[k][4] = v.x, x[k][5] = v.y, x[k][6] = v.z, x[k][7] = v.w;
-                    }
-                    __syncwarp();
+        for (int k = 0; k < kHeadsPerLane; ++k) {
+            xa[k].w = {}, xb[k].w = {};
+            if (k < mine) {
+                if (!APPEND || front || h0 + k * NG < a.n_k) {
+                    xa[k].load(pa + ca * size + k * (NG * D * size));
+                    xb[k].load(pa + cb * size + k * (NG * D * size));
+                } else {
+                    xa[k].load(pv + k * (NG * D * size));
+                    xb[k].load(pv + 4 * size + k * (NG * D * size));
                 }
-                const int64_t page = store ? slot / a.page_tokens : 0;
-                const int off = store ? static_cast<int>(slot - page * a.page_tokens) : 0;
-                const int hk = is_v ? h - a.n_q - a.n_k : h - a.n_q;
-                uint8_t *block = a.pages + ((page * a.n_k + hk) * (a.page_tokens / kBlockTokens) + off / kBlockTokens) *
-                                               static_cast<int64_t>(18 * D);
-                store_eight<D>(block, off % kBlockTokens, 8 * i, store, x[k], !is_v, lane);
             }
+        }
+    }
+    const bool bad = a.rot > 0 && (pos < 0 || pos >= a.n_pos);
+    float c[4] = {}, s[4] = {};
+    if (turn) {
+        const float4 *row = reinterpret_cast<const float4 *>(a.table + static_cast<int64_t>(bad ? 0 : pos) * (a.rot >> 1) +
+                                                             4 * i);
+        const float4 u = row[0], v = row[1];
+        c[0] = u.x, s[0] = u.y, c[1] = u.z, s[1] = u.w, c[2] = v.x, s[2] = v.y, c[3] = v.z, s[3] = v.w;
+    }
+    float w[8];
+    const float *weight = h0 < first_mine ? (front ? a.q_weight : a.k_weight) : (front ? a.k_weight : nullptr);
+    load_weights(w, mine ? weight : nullptr, ca, cb);
+    if (bad) {
+        if (threadIdx.x == 0) record_error(a.err, kErrBadIndex);
+#pragma unroll
+        for (int k = 0; k < kHeadsPerLane; ++k)
+            if (front || h0 + k * NG < a.n_k) xa[k].poison(), xb[k].poison();
+    }
+    const bool norm = a.q_weight || a.k_weight;
+    if (front) {
+        uint8_t *to = static_cast<uint8_t *>(a.q_out) +
+                      (static_cast<int64_t>(t) * a.ldqo + h0 * D) * (a.out_type == QK_F32 ? 4 : 2);
+#pragma unroll
+        for (int k = 0; k < kHeadsPerLane; ++k) {
+            if (k >= hpl) break;
+            float x[8];
+            xa[k].to(x), xb[k].to(x + 4);
+            if (!APPEND && k > 0 && h0 + k * NG >= first_mine && h0 + (k - 1) * NG < first_mine) {
+                weight = a.k_weight;      // from here the lane's heads are keys
+                load_weights(w, k < mine ? weight : nullptr, ca, cb);
+            }
+            turn_eight<D, INTER>(x, norm, weight && k < mine, w, a.eps, turn, c, s, sub);
+            if (k < mine) {
+                const float lo[4] = {x[0], x[1], x[2], x[3]}, hi[4] = {x[4], x[5], x[6], x[7]};
+                if (a.out_type == TYPE) {
+                    store4(to + (ca + k * (NG * D)) * size, 0, TYPE, lo);
+                    store4(to + (cb + k * (NG * D)) * size, 0, TYPE, hi);
+                } else {
+                    store4(to, ca + k * (NG * D), a.out_type, lo);
+                    store4(to, cb + k * (NG * D), a.out_type, hi);
+                }
+            }
+        }
+        return;
+    }
+    if constexpr (APPEND) {
+        __shared__ __align__(16) float exchange[INTER ? 1 : kRowWarps * RPW][INTER ? 4 : D];
+        const int64_t slot = a.slots[t];
+        if (slot < 0) return;
+        if (slot >= a.n_slots) {
+            if (threadIdx.x == 0) record_error(a.err, kErrBadIndex);
+            return;
+        }
+        const int64_t page = slot / a.page_tokens;
+        const int off = static_cast<int>(slot - page * a.page_tokens), tk = off % kBlockTokens;
+        const int head_bytes = a.page_tokens / kBlockTokens * (18 * D);
+        uint8_t *first = a.pages + page * a.n_k * static_cast<int64_t>(head_bytes) + off / kBlockTokens * (18 * D);
+#pragma unroll
+        for (int k = 0; k < kHeadsPerLane; ++k) {
+            if (k >= hpl) break;
+            const int h = h0 + k * NG;
+            const bool is_key = h < a.n_k;
+            float x[8];
+            xa[k].to(x), xb[k].to(x + 4);
+            if (!is_key) load_weights(w, nullptr, ca, cb);
+            turn_eight<D, INTER>(x, norm, weight && k < mine && is_key, w, a.eps, turn && is_key, c, s, sub);
+            if constexpr (!INTER) {      // eight neighbours a lane, as the cache wants them
+                float *row = exchange[warp * RPW + (on ? sub : 0)];
+                if (on && is_key) {
+                    *reinterpret_cast<float4 *>(row + ca) = make_float4(x[0], x[1], x[2], x[3]);
+                    *reinterpret_cast<float4 *>(row + cb) = make_float4(x[4], x[5], x[6], x[7]);
+                }
+                __syncwarp();
+                if (on && is_key) {
+                    const float4 u = *reinterpret_cast<const float4 *>(row + 8 * i);
+                    const float4 v = *reinterpret_cast<const float4 *>(row + 8 * i + 4);
+                    x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w, x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
+                }
+                __syncwarp();
+            }
+            store_eight<D>(first + static_cast<int64_t>(is_key ? h : h - a.n_k) * head_bytes, tk, 8 * i, k < mine, x,
+                           is_key, lane);
         }
     }
 }
@@ -589,23 +679,44 @@ cudaError_t launch(void (*kern)(const Args), int64_t grid, int threads, size_t s
     return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
-template <int D, int TYPE, bool APPEND>
+template <int D, int TYPE, bool INTER, bool APPEND>
 cudaError_t launch_heads(const RowsArgs &a, cudaStream_t st)
 {
     constexpr int NG = kRowWarps * kRowsPerWarp<D>;
-    const int heads = a.n_q + a.n_k + a.n_v;
-    // four heads a lane share a table row and keep four loads going; few tokens spread over more blocks instead
-    const int64_t parts = (heads + 4 * NG - 1) / (4 * NG);
-    if (a.T * parts >= 304) return launch(heads_kernel<D, TYPE, 4, APPEND>, a.T * parts, kRowWarps * 32, 0, st, a);
-    return launch(heads_kernel<D, TYPE, 1, APPEND>, a.T * ((heads + NG - 1) / NG), kRowWarps * 32, 0, st, a);
+    const int front = APPEND ? a.n_q : a.n_q + a.n_k, back = APPEND ? 2 * a.n_k : 0;
+    // several heads a lane share a table row and keep as many loads going; few tokens spread over more blocks
+    // instead (one token of 40 heads of 128: 1.5 us with one head a lane)
+    const auto cut = [](int heads, int most, int *per) {
+        const int parts = (heads + NG * most - 1) / (NG * most);
+        *per = parts ? (heads + NG * parts - 1) / (NG * parts) : 1;
+        return parts;
+    };
+    int hf = 1, hb = 1, fp = cut(front, kHeadsPerLane, &hf), parts = fp + cut(back, kHeadsPerLane, &hb);
+    if (a.T * parts < 304) fp = cut(front, 1, &hf), parts = fp + cut(back, 1, &hb);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(a.T * parts));
+    cfg.blockDim = dim3(kRowWarps * 32);
+    cfg.stream = st;
+    cudaLaunchAttribute at = {};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = library_programmatic() ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, heads_kernel<D, TYPE, INTER, APPEND>, a, hf, hb, fp, parts);
+}
+
+template <int D, int TYPE, bool APPEND>
+cudaError_t launch_heads_layout(const RowsArgs &a, cudaStream_t st)
+{
+    return a.interleaved ? launch_heads<D, TYPE, true, APPEND>(a, st) : launch_heads<D, TYPE, false, APPEND>(a, st);
 }
 
 template <int D, bool APPEND>
 cudaError_t launch_heads_type(const RowsArgs &a, cudaStream_t st)
 {
-    if (a.in_type == QK_F32) return launch_heads<D, QK_F32, APPEND>(a, st);
-    if (a.in_type == QK_F16) return launch_heads<D, QK_F16, APPEND>(a, st);
-    return launch_heads<D, QK_BF16, APPEND>(a, st);
+    if (a.in_type == QK_F32) return launch_heads_layout<D, QK_F32, APPEND>(a, st);
+    if (a.in_type == QK_F16) return launch_heads_layout<D, QK_F16, APPEND>(a, st);
+    return launch_heads_layout<D, QK_BF16, APPEND>(a, st);
 }
 
 template <bool APPEND>
