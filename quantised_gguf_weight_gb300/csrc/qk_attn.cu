@@ -31,13 +31,13 @@
 
 #include "qk_device.cuh"
 #include "qk_internal.h"
-#include "qk_kv4.cuh"
+#include "qk_attn.cuh"
 
 namespace qk {
+using namespace attn;
 namespace {
 
 constexpr int kWarps = 8;
-constexpr float kNoMax = -3.0e38f;
 constexpr float kTwo24 = 16777216.0f;
 
 // Thread blocks an SM holds: two (128 registers a thread), one where a head of 256 channels needs more.
@@ -49,29 +49,6 @@ constexpr int kTwoPiece = 0;    // 8 rows, fp32 queries
 constexpr int kOnePiece8 = 1;   // 8 rows, 16-bit queries
 constexpr int kOnePiece16 = 2;  // 16 rows, 16-bit queries
 
-struct AttnArgs {
-    const uint8_t *pages;
-    int64_t n_pages;
-    int n_kv, page_blocks, rep;      // page_blocks: 16-token blocks a page
-    const void *q;
-    int64_t ldq;
-    int q_type;
-    const int32_t *page_table;
-    int64_t ld_pages, max_pages;
-    const int32_t *lens, *q_start;
-    int64_t T, max_q, window;
-    float scale_log2;                // scale * log2(e)
-    void *out;
-    int64_t ldo;
-    int out_type;
-    int tiles, splits;               // row tiles a sequence and head, splits of its blocks
-    int64_t min_blocks;              // blocks a split takes at least
-    int *counters;
-    float *parts;
-    int *err;
-    uint64_t wait_ns;
-};
-
 __device__ __forceinline__ void mma_f16(float &c0, float &c1, float &c2, float &c3, uint32_t a0, uint32_t a1,
                                         uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
 {
@@ -79,13 +56,6 @@ __device__ __forceinline__ void mma_f16(float &c0, float &c1, float &c2, float &
         "{%0, %1, %2, %3};"
         : "+f"(c0), "+f"(c1), "+f"(c2), "+f"(c3)
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ float ex2(float x)
-{
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
 }
 
 // N 32-bit words from shared memory at a multiple of the widest load that N allows.
@@ -114,24 +84,6 @@ __device__ __forceinline__ float half_at(const uint32_t (&w)[N], int i)
 {
     const __half2 h = *reinterpret_cast<const __half2 *>(&w[i >> 1]);
     return i & 1 ? __high2float(h) : __low2float(h);
-}
-
-__device__ __forceinline__ uint32_t pack_half(float lo, float hi)
-{
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-
-// n - 8 as an fp16 pair, of nibble AT (0 or 1) of both halves of a word: the nibble in the mantissa of 1024 (where
-// the lowest bit counts 1) or of 64 (where bit 4 does), less the constant.
-template <int AT>
-__device__ __forceinline__ uint32_t signed_nibbles(uint32_t w)
-{
-    uint32_t r;
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "n"(AT ? 0x00F000F0 : 0x000F000F), "n"(AT ? 0x54005400 : 0x64006400));
-    const uint32_t bias = AT ? 0x54805480u : 0x64086408u;   // 72, 1032
-    const __half2 d = __hsub2(*reinterpret_cast<const __half2 *>(&r), *reinterpret_cast<const __half2 *>(&bias));
-    return *reinterpret_cast<const uint32_t *>(&d);
 }
 
 // One warp's running state.
@@ -375,34 +327,20 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm<G>) attn_kernel(cons
     const int64_t b = u / a.n_kv;
 
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    int64_t r0 = b * a.max_q, r1 = r0 + a.max_q;
-    if (a.q_start) r0 = a.q_start[b], r1 = a.q_start[b + 1];
-    const int64_t L = a.lens[b];
-    const bool bad_rows = r0 < 0 || r1 > a.T || r1 < r0 || r1 - r0 > a.max_q;
-    if (bad_rows || L < 0 || L > a.max_pages * a.page_blocks * kBlockTokens) {
-        // every row that q_start names becomes NaN, shared out over the row tiles
-        if (split != 0) return;
-        if (threadIdx.x == 0 && tile == 0) record_error(a.err, kErrBadIndex);
-        for (int64_t row = (r0 < 0 ? 0 : r0) + tile; row < (r1 > a.T ? a.T : r1); row += a.tiles)
-            for (int i = threadIdx.x; i < a.rep * D; i += kWarps * 32)
-                store_float_as(a.out, row * a.ldo + static_cast<int64_t>(hk) * a.rep * D + i, a.out_type,
-                               __int_as_float(0x7FC00000));
+    const Sequence seq = sequence_of(a, b);
+    if (seq.bad) {
+        if (split == 0) poison_rows(a, seq, hk, tile, a.rep * D);
         return;
     }
+    const int64_t r0 = seq.r0, r1 = seq.r1, L = seq.len;
     const int n = static_cast<int>(r1 - r0) * a.rep;      // rows of this sequence and head
     const int first = tile * RT;
     if (first >= n) return;
     const int rows = min(RT, n - first);
-    // keys that some row of the tile sees: positions of its first and last row
-    const int64_t pos0 = L - (r1 - r0) + first / a.rep, pos1 = L - (r1 - r0) + (first + rows - 1) / a.rep;
-    const int64_t key_lo = a.window > 0 && pos0 - a.window + 1 > 0 ? pos0 - a.window + 1 : 0;
-    const int64_t key_hi = pos1 + 1 > 0 ? pos1 + 1 : 0;
-    const int64_t blk_lo = key_lo / kBlockTokens;
-    const int64_t nblk = key_hi > key_lo ? (key_hi + kBlockTokens - 1) / kBlockTokens - blk_lo : 0;
-    int64_t per = (nblk + a.splits - 1) / a.splits;
-    if (per < a.min_blocks) per = a.min_blocks;
-    const int active = nblk > per ? static_cast<int>((nblk + per - 1) / per) : 1;
+    const Span span = span_of(a, seq, first, rows);
+    const int active = span.active;
     if (split >= active) return;
+    const int64_t blk_lo = span.blk_lo, nblk = span.blocks, per = span.per, pos0 = span.pos0, pos1 = span.pos1;
     const int64_t b0 = split * per, b1 = nblk < b0 + per ? nblk : b0 + per;    // blocks from blk_lo
     const int nk = b1 - b0 > warp ? static_cast<int>((b1 - b0 - warp + kWarps - 1) / kWarps) : 0;
 
@@ -427,7 +365,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm<G>) attn_kernel(cons
     };
     auto issue = [&](int k) {
         const uint64_t from = __shfl_sync(0xFFFFFFFFu, reinterpret_cast<uint64_t>(addr), k & 31);
-        if (lane == 0) {
+        if (lane == 0 && !(k == a.skip_block && blockIdx.x == 0 && warp == 0)) {
             const uint32_t bar = bars + 8 * (k % NST);
             mbar_arrive_expect_tx(bar, Sh::block_bytes);
             bulk_g2s(smem_u32(ring) + (k % NST) * Sh::block_bytes, reinterpret_cast<const void *>(from),
@@ -517,9 +455,8 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm<G>) attn_kernel(cons
         const int row = r8 + 8 * half;
         Q.to_log2[half] = row_log2[row];
         const int64_t pos = L - (r1 - r0) + (row < rows ? (first + row) / a.rep : 0);
-        const int64_t lo = a.window > 0 ? pos - a.window + 1 - base : -1, hi = row < rows ? pos + 1 - base : -1;
-        Q.lo[half] = static_cast<int>(lo < -1 ? -1 : (lo > INT32_MAX ? INT32_MAX : lo));
-        Q.hi[half] = static_cast<int>(hi < -1 ? -1 : (hi > INT32_MAX ? INT32_MAX : hi));
+        Q.lo[half] = clamp_key(a.window > 0 ? pos - a.window + 1 - base : -1);
+        Q.hi[half] = row < rows ? clamp_key(pos + 1 - base) : -1;
     }
 #pragma unroll
     for (int g = 0; g < G; ++g)
@@ -529,12 +466,11 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm<G>) attn_kernel(cons
     // keys every row sees, counted from the split's first block
     const int64_t last_lo = a.window > 0 ? pos1 - a.window + 1 - base : 0;
     const int64_t first_hi = pos0 + 1 - base;
-    const int all_lo = static_cast<int>(key_lo - base < 0 ? 0 : key_lo - base);
-    const int64_t span = key_hi - base;
-    const int all_hi = static_cast<int>(span > INT32_MAX ? INT32_MAX : span);
+    const int all_lo = clamp_key(span.key_lo - base), all_hi = clamp_key(span.key_hi - base);
     bool dead = false;
     for (int k = 0; k < nk; ++k) {
-        if (!mbar_wait(bars + 8 * (k % NST), (k / NST) & 1, a.wait_ns)) {
+        // the warp shares the outcome: a limit may run out for one lane and not another
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(bars + 8 * (k % NST), (k / NST) & 1, a.wait_ns))) {
             // give up: the copies still in flight are waited for before their memory is used for anything else
             dead = true;
             for (int i = k; i < nk && i < k + NST; ++i) mbar_wait(bars + 8 * (i % NST), (i / NST) & 1, a.wait_ns);
@@ -652,13 +588,18 @@ struct Cut {
     int64_t min_blocks, groups;      // groups: sequences * heads * tiles
 };
 
+std::atomic<int> g_skip_block{-1};
+
+constexpr int kChunk = 3;                    // Cut::mode of the many-row form (qk_attn_chunk.cu)
+constexpr int64_t kChunkFrom = 64;           // rows a sequence and head from which it is taken
 constexpr int64_t kCounters = 16384;         // at the start of every workspace, whatever the call
 Cut cut_for(int64_t B, int n_kv, int rep, int D, int64_t max_q, int64_t max_len, bool fp32)
 {
     Cut c{};
     const int64_t rows = max_q * rep;
     c.mode = fp32 ? kTwoPiece : (rows <= 8 ? kOnePiece8 : kOnePiece16);
-    c.row_tile = c.mode == kOnePiece16 ? 16 : 8;
+    if (!fp32 && rows >= kChunkFrom && D <= 128) c.mode = kChunk;
+    c.row_tile = c.mode == kChunk ? kChunkRows : c.mode == kOnePiece16 ? 16 : 8;
     c.tiles = static_cast<int>((rows + c.row_tile - 1) / c.row_tile);
     c.groups = B * n_kv * c.tiles;
     const int64_t blocks = (max_len + kBlockTokens - 1) / kBlockTokens;
@@ -666,6 +607,26 @@ Cut cut_for(int64_t B, int n_kv, int rep, int D, int64_t max_q, int64_t max_len,
     // about 10 steps), of splits that leave every warp two blocks.
     int sms = 152, smem = 0;
     device_limits(&sms, &smem);
+    if (c.mode == kChunk) {
+        // rounds of one thread block an SM, of key tiles of 8 blocks (about 1.2 us each) and 3 tiles' worth of start
+        // and end; parts of several splits are written and read again (5 TB/s) by a second kernel (2 us)
+        const int64_t tiles = (blocks + 7) / 8;
+        double best = 1e30;
+        c.splits = 1;
+        for (int64_t rounds = 1, last = 0; rounds <= 8; ++rounds) {
+            int64_t s = sms * rounds / c.groups;
+            if (s * 2 > tiles) s = tiles / 2;
+            if (s < 1) s = 1;
+            if (s == last) continue;
+            last = s;
+            const double us = 1.2 * static_cast<double>((c.groups * s + sms - 1) / sms * ((tiles + s - 1) / s + 3)) +
+                              (s > 1 ? 2.0 + 2e-7 * static_cast<double>(2 * s * c.groups * chunk_part_bytes(D)) : 0.0);
+            if (us < best) best = us, c.splits = static_cast<int>(s);
+        }
+        c.min_blocks = (tiles + c.splits - 1) / c.splits * 8;
+        if (c.min_blocks < 16) c.min_blocks = 16;
+        return c;
+    }
     const int64_t slots = static_cast<int64_t>(sms) * (D > 128 ? 1 : 2);
     int64_t best = 1, best_cost = INT64_MAX;
     for (int64_t rounds = 1, last = 0; rounds <= 12 && c.groups <= kCounters; ++rounds) {
@@ -685,7 +646,11 @@ Cut cut_for(int64_t B, int n_kv, int rep, int D, int64_t max_q, int64_t max_len,
     return c;
 }
 
-int64_t part_bytes_of(const Cut &c, int D) { return (static_cast<int64_t>(c.row_tile) * D + 2 * c.row_tile) * 4; }
+int64_t part_bytes_of(const Cut &c, int D)
+{
+    if (c.mode == kChunk) return chunk_part_bytes(D);
+    return (static_cast<int64_t>(c.row_tile) * D + 2 * c.row_tile) * 4;
+}
 
 template <int G, int MODE>
 cudaError_t launch(const AttnArgs &a, int64_t grid, cudaStream_t st)
@@ -730,6 +695,12 @@ cudaError_t launch_mode(const AttnArgs &a, int mode, int64_t grid, cudaStream_t 
 using namespace qk;
 
 extern "C" {
+
+// Test hook, not part of the public header: thread block 0 of every later
+// attention launch never copies its 16-token block number `block` (the
+// few-row form: of its first warp; -1 restores normal operation), so that a
+// bounded wait runs out and the launch records QK_ERR_TIMEOUT.
+int qk_debug_attn_skip_block(int block) { return g_skip_block.exchange(block); }
 
 size_t qk_attn_q4_workspace_bytes(int64_t B, int n_q_heads, int n_kv_heads, int head_dim, int64_t max_q,
                                   int64_t max_len)
@@ -799,6 +770,8 @@ int qk_attn_q4(const qk_kv_cache_q4 *cache, const void *q, int64_t ldq, int q_ty
     if (!a.err) return QK_ERR_CUDA;
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = cudaErrorInvalidValue;
+    a.skip_block = g_skip_block.load();
+    if (cut.mode == kChunk) return chunk_launch(a, D, cut.groups, s) == cudaSuccess ? QK_OK : QK_ERR_CUDA;
     switch (D) {
     case 64: e = launch_mode<2>(a, cut.mode, grid, s); break;
     case 96: e = launch_mode<3>(a, cut.mode, grid, s); break;

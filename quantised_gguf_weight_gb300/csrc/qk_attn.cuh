@@ -1,0 +1,122 @@
+// qk_attn.cuh -- what the two forms of attention over the 4-bit cache share.
+#pragma once
+
+#include "qk_device.cuh"
+#include "qk_kv4.cuh"
+
+namespace qk {
+namespace attn {
+
+constexpr float kNoMax = -3.0e38f;      // a row's reference before it has seen a key
+
+struct AttnArgs {
+    const uint8_t *pages;
+    int64_t n_pages;
+    int n_kv, page_blocks, rep;      // page_blocks: 16-token blocks a page
+    const void *q;
+    int64_t ldq;
+    int q_type;
+    const int32_t *page_table;
+    int64_t ld_pages, max_pages;
+    const int32_t *lens, *q_start;
+    int64_t T, max_q, window;
+    float scale_log2;                // scale * log2(e)
+    void *out;
+    int64_t ldo;
+    int out_type;
+    int tiles, splits;               // row tiles a sequence and head, splits of its blocks
+    int64_t min_blocks;              // blocks a split takes at least
+    int *counters;
+    float *parts;
+    int *err;
+    uint64_t wait_ns;
+    int skip_block;                  // test hook: this block of thread block 0 (its first warp's) is never copied
+};
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi)
+{
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// n - 8 as an fp16 pair, of nibble AT (0 or 1) of both halves of a word: the nibble in the mantissa of 1024 (where
+// the lowest bit counts 1) or of 64 (where bit 4 does), less the constant.
+template <int AT>
+__device__ __forceinline__ uint32_t signed_nibbles(uint32_t w)
+{
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "n"(AT ? 0x00F000F0 : 0x000F000F), "n"(AT ? 0x54005400 : 0x64006400));
+    const uint32_t bias = AT ? 0x54805480u : 0x64086408u;   // 72, 1032
+    const __half2 d = __hsub2(*reinterpret_cast<const __half2 *>(&r), *reinterpret_cast<const __half2 *>(&bias));
+    return *reinterpret_cast<const uint32_t *>(&d);
+}
+
+// A call's rows and keys as a thread block sees them.
+struct Sequence {
+    int64_t r0, r1;       // its query rows
+    int64_t len;
+    bool bad;             // an index out of range
+};
+__device__ __forceinline__ Sequence sequence_of(const AttnArgs &a, int64_t b)
+{
+    Sequence s;
+    s.r0 = b * a.max_q, s.r1 = s.r0 + a.max_q;
+    if (a.q_start) s.r0 = a.q_start[b], s.r1 = a.q_start[b + 1];
+    s.len = a.lens[b];
+    s.bad = s.r0 < 0 || s.r1 > a.T || s.r1 < s.r0 || s.r1 - s.r0 > a.max_q || s.len < 0 ||
+            s.len > a.max_pages * a.page_blocks * kBlockTokens;
+    return s;
+}
+
+// Every row that q_start names becomes NaN, shared out over the row tiles.
+__device__ __forceinline__ void poison_rows(const AttnArgs &a, const Sequence &s, int hk, int tile, int width)
+{
+    if (threadIdx.x == 0 && tile == 0) record_error(a.err, kErrBadIndex);
+    for (int64_t row = (s.r0 < 0 ? 0 : s.r0) + tile; row < (s.r1 > a.T ? a.T : s.r1); row += a.tiles)
+        for (int i = threadIdx.x; i < width; i += blockDim.x)
+            store_float_as(a.out, row * a.ldo + static_cast<int64_t>(hk) * width + i, a.out_type,
+                           __int_as_float(0x7FC00000));
+}
+
+// The 16-token blocks that the rows [first, first + rows) of a sequence see,
+// and how many splits take them.
+struct Span {
+    int64_t pos0, pos1;          // positions of the first and the last row
+    int64_t key_lo, key_hi;      // keys that some row sees
+    int64_t blk_lo, blocks;
+    int64_t per;                 // blocks a split
+    int active;                  // splits with blocks (at least one)
+};
+__device__ __forceinline__ Span span_of(const AttnArgs &a, const Sequence &s, int first, int rows)
+{
+    Span p;
+    p.pos0 = s.len - (s.r1 - s.r0) + first / a.rep, p.pos1 = s.len - (s.r1 - s.r0) + (first + rows - 1) / a.rep;
+    p.key_lo = a.window > 0 && p.pos0 - a.window + 1 > 0 ? p.pos0 - a.window + 1 : 0;
+    p.key_hi = p.pos1 + 1 > 0 ? p.pos1 + 1 : 0;
+    p.blk_lo = p.key_lo / kBlockTokens;
+    p.blocks = p.key_hi > p.key_lo ? (p.key_hi + kBlockTokens - 1) / kBlockTokens - p.blk_lo : 0;
+    p.per = (p.blocks + a.splits - 1) / a.splits;
+    if (p.per < a.min_blocks) p.per = a.min_blocks;
+    p.active = p.blocks > p.per ? static_cast<int>((p.blocks + p.per - 1) / p.per) : 1;
+    return p;
+}
+
+__device__ __forceinline__ int clamp_key(int64_t k) { return static_cast<int>(k < -1 ? -1 : (k > INT32_MAX ? INT32_MAX : k)); }
+
+// The many-row form (qk_attn_chunk.cu): tiles of kChunkRows rows on the 5th-generation tensor cores.
+constexpr int kChunkRows = 256;
+cudaError_t chunk_launch(const AttnArgs &a, int D, int64_t groups, cudaStream_t st);
+__host__ __device__ inline int64_t chunk_part_bytes(int D)
+{
+    return (static_cast<int64_t>(kChunkRows) * D + 2 * kChunkRows) * 4;
+}
+
+}  // namespace attn
+}  // namespace qk

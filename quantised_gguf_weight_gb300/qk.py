@@ -115,6 +115,8 @@ def load(path: str | None = None):
             getattr(lib, name).restype = I
         lib.qk_attn_q4_workspace_bytes.argtypes = [I64, I, I, I, I64, I64]
         lib.qk_attn_q4_workspace_bytes.restype = ctypes.c_size_t
+        lib.qk_debug_attn_skip_block.argtypes = [I]
+        lib.qk_debug_attn_skip_block.restype = I
         lib.qk_debug_skip_item.argtypes = [I64]
         lib.qk_debug_skip_item.restype = I64
         lib.qk_debug_gemv_plan.argtypes = [I, I64, I64, I, ctypes.POINTER(ctypes.c_int64), I]
@@ -606,6 +608,11 @@ def debug_gemm_skip_chunk(chunk: int) -> int:
 def device_error(stream=None) -> int:
     """Synchronise the stream, then read and clear the device error word."""
     return int(load().qk_device_error(_stream(stream)))
+
+
+def debug_attn_skip_block(block: int) -> int:
+    """Test hook: thread block 0 of later attention launches never copies its 16-token block `block` (-1: off)."""
+    return int(load().qk_debug_attn_skip_block(int(block)))
 
 
 def set_wait_limit_ns(ns: int) -> int:

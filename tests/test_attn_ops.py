@@ -547,6 +547,26 @@ def test_programmatic_launch_and_graph(qk):
     assert torch.equal(out, want)
 
 
+@pytest.mark.parametrize("dtype,n", [("f32", 1), ("bf16", 1), ("bf16", 80)])
+def test_attn_timeout_is_reported(qk, dtype, n):
+    """A block that is never copied: the bounded waits run out, the call ends, the error word says so, the thread
+    block's rows are NaN, and the next call is right."""
+    cache, tab, _, _ = make_cache(1, [300, 200], 2, 64, 16)
+    lens = torch.tensor([300, 200], dtype=torch.int32).cuda()
+    q = rand(3, 2 * n, 4 * 64, dtype=dtype)
+    want = qk.attn_q4(cache, q, tab, lens, max_q=n)
+    limit = qk.set_wait_limit_ns(20_000_000)
+    qk.debug_attn_skip_block(1)
+    try:
+        got = qk.attn_q4(cache, q, tab, lens, max_q=n)
+        assert qk.device_error() == 6
+    finally:
+        qk.debug_attn_skip_block(-1)
+        qk.set_wait_limit_ns(limit)
+    assert torch.isnan(got[0, :2 * 64]).all() and torch.equal(got[n:], want[n:])
+    assert torch.equal(qk.attn_q4(cache, q, tab, lens, max_q=n), want) and qk.device_error() == 0
+
+
 # ---------------------------------------------------------------- refusals of the binding
 
 def test_binding_refuses(qk):
