@@ -110,6 +110,12 @@ __device__ __forceinline__ Span span_of(const AttnArgs &a, const Sequence &s, in
 
 __device__ __forceinline__ int clamp_key(int64_t k) { return static_cast<int>(k < -1 ? -1 : (k > INT32_MAX ? INT32_MAX : k)); }
 
+// The few-row form (qk_attn_rows.cuh), by head size: rows of `pieces` fp16 pieces in `sets` sets of 8 columns.
+cudaError_t rows_launch_64(const AttnArgs &a, int pieces, int sets, int64_t grid, cudaStream_t st);
+cudaError_t rows_launch_96(const AttnArgs &a, int pieces, int sets, int64_t grid, cudaStream_t st);
+cudaError_t rows_launch_128(const AttnArgs &a, int pieces, int sets, int64_t grid, cudaStream_t st);
+cudaError_t rows_launch_256(const AttnArgs &a, int pieces, int sets, int64_t grid, cudaStream_t st);
+
 // The many-row form (qk_attn_chunk.cu): tiles of kChunkRows rows on the 5th-generation tensor cores.
 constexpr int kChunkRows = 256;
 cudaError_t chunk_launch(const AttnArgs &a, int D, int64_t groups, cudaStream_t st);

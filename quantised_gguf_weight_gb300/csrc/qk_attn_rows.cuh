@@ -1,0 +1,651 @@
+// qk_attn_rows.cuh -- attention over the 4-bit paged cache for few query rows a
+// key/value head (single tokens, short chunks, fp32 queries).
+//
+// Mathematics.  With K_j = d_jg (n_jc - 8) in each 32-channel group g,
+//   s_j = scale * sum_g d_jg (sum_c q_c n_jc - 8 sum_c q_c)
+//   o_c = sum_j (p_j e_jg) (n_jc - 8)     (e: the values' scales)
+// so both products run on the tensor cores (m16n8k16, fp16 in, fp32 out) with
+// the nibbles themselves as the 16-row operand: S^T = K Q^T takes 16 keys by 8
+// query columns, O^T = V^T P^T 16 channels by 8 columns.  Grouped heads are
+// few, and as columns they fill the products' narrow side; the other way round
+// (queries as the 16 rows) four heads left 12 rows of every product empty, and
+// a block took 32 products and 432 instructions instead of 16 and about 300.
+// The scores' accumulator, rounded to fp16 and transposed by movmatrix, is the
+// second product's operand as it stands: the cache's token order is made for
+// it.
+//
+// For the scores a nibble under a mask is the fp16 subnormal n * 2^-24 (or
+// 16 n * 2^-24), so a word of 8 nibbles becomes four fp16 pairs in four masks
+// and a shift.  For the values n - 8 is formed in normal fp16 (one more
+// subtraction a pair): sums over keys are not exact, and the tensor cores cut
+// them relative to the operands' exponents, which a subnormal hides (2e-6 of
+// the sum instead of 1e-7).  Scales stay in fp32, on the scores and on the
+// probabilities.
+//
+// fp32 queries keep fp32 accuracy: a row's query (and probability) is two
+// fp16 pieces of 22 bits together, in neighbouring columns.
+//
+// The softmax is one pass: P_j = 2^(z_j - M) against a reference M that moves
+// only when a P could leave fp16's range next to its value scale, so most
+// blocks need no shuffle and no rescaling.
+//
+// Blocks of 16 tokens arrive by bulk copies in a ring of stages of each warp
+// (no barrier across warps in the loop); a sequence's blocks are split over
+// thread blocks, and the last to finish joins the parts in a fixed order.
+#pragma once
+
+#include <atomic>
+
+#include "qk_attn.cuh"
+#include "qk_internal.h"
+
+namespace qk {
+namespace attn {
+
+constexpr int kWarps = 8;
+constexpr float kTwo24 = 16777216.0f;
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// 8 x 8 fp16 matrix of a warp, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x)
+{
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+
+// N 32-bit words from shared memory at a multiple of the widest load that N allows.
+template <int N>
+__device__ __forceinline__ void lds(uint32_t (&w)[N], uint32_t addr)
+{
+    if constexpr (N % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < N; i += 4)
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
+                         : "r"(addr + 4 * i));
+    } else if constexpr (N % 2 == 0) {
+#pragma unroll
+        for (int i = 0; i < N; i += 2)
+            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[i]), "=r"(w[i + 1]) : "r"(addr + 4 * i));
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[i]) : "r"(addr + 4 * i));
+    }
+}
+
+// G fp16 scales of one token as floats.
+template <int G>
+__device__ __forceinline__ void load_scales(float (&d)[G], uint32_t addr)
+{
+    if constexpr (G % 2 == 0) {
+        uint32_t w[G / 2];
+        lds(w, addr);
+#pragma unroll
+        for (int g = 0; g < G; g += 2) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[g / 2]));
+            d[g] = f.x, d[g + 1] = f.y;
+        }
+    } else {
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            uint16_t h;
+            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(addr + 2 * g));
+            d[g] = __half2float(__ushort_as_half(h));
+        }
+    }
+}
+
+// A warp's tile: NT sets of 8 columns; PIECES 1: a column is a row, 2: a row
+// has its two pieces in columns 2k, 2k + 1.
+template <int G, int PIECES, int NT>
+struct Shape {
+    static constexpr int D = 32 * G, RT = NT * 8 / PIECES;
+    static constexpr int NR = 2 / PIECES;                             // rows of a lane in each column set
+    static constexpr int block_bytes = 18 * D;
+    static constexpr int blocks_per_sm = (G <= 4 && NT <= 2) || NT == 1 ? 2 : 1;
+    static constexpr int NST = G <= 2 ? 6 : 4;
+    static constexpr bool q_in_regs = G * NT <= 4;
+    static constexpr int frag_bytes = NT * G * 2 * 32 * 8;
+    static constexpr int part_stride = D + 4;                         // floats a row, padded
+    static constexpr int part_bytes = RT * part_stride * 4 + RT * 8;  // and (M, l) of each row
+    static constexpr int ring_bytes = NST * block_bytes;
+    static constexpr int warp_bytes = ((ring_bytes > part_bytes ? ring_bytes : part_bytes) + 127) / 128 * 128;
+    static constexpr int bars_at = frag_bytes + kWarps * warp_bytes;
+    static constexpr int init_at = bars_at + kWarps * NST * 8 + 16;   // after the barriers and the join's flag
+    static constexpr int smem = init_at + NT * 8 * G * 4 + RT * 4;
+    static constexpr int part_floats = RT * D + 2 * RT;               // in the workspace
+};
+
+// One warp's running state.  A lane (r = lane/4, c = lane%4) has, in each column set, rows 2c, 2c + 1 (or c).
+template <int G, int PIECES, int NT>
+struct State {
+    static constexpr int NR = Shape<G, PIECES, NT>::NR;
+    float o[NT][G][2][4];        // [..][m][x]: channel 32g + 4r + m (+ 2 for x >= 2), column 2c + x%2
+    float m[NT][NR], l[NT][NR];
+    float limit;                 // exponents above it leave fp16's range
+    uint32_t scale_lim;          // largest value scale seen (fp16 bits, twice)
+};
+
+// What a lane needs of its query rows.
+template <int G, int PIECES, int NT>
+struct Query {
+    static constexpr int NR = Shape<G, PIECES, NT>::NR;
+    uint32_t b[Shape<G, PIECES, NT>::q_in_regs ? NT * G * 4 : 1];    // operand fragments [set][group][step][2]
+    float init[NT][G][2];        // -8 * 2^-24 * (the group's sum of q') of columns 2c, 2c + 1
+    float to_log2[NT][NR];       // score -> exponent
+    int lo[NT][NR], hi[NT][NR];  // keys [lo, hi) of each row, from the split's first block
+};
+
+template <int G, int PIECES, int NT, bool MASK>
+__device__ __forceinline__ void block16(State<G, PIECES, NT> &S, const Query<G, PIECES, NT> &Q, uint32_t blk,
+                                        uint32_t qfrag, int key0, int all_lo, int all_hi, int lane)
+{
+    using Sh = Shape<G, PIECES, NT>;
+    constexpr int Gp = kv4_gp(G), NR = Sh::NR, D = Sh::D;
+    const int tok = 4 * (lane >> 3) + ((lane >> 2) & 1);      // the lane's tokens: tok and tok + 2
+
+    // scores: s[set][token h][row]
+    float s[NT][2][NR];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int r = 0; r < NR; ++r) s[n][0][r] = s[n][1][r] = 0.0f;
+    {
+        float dk[2][G];
+        load_scales<G>(dk[0], blk + 16 * D + tok * 2 * G);
+        load_scales<G>(dk[1], blk + 16 * D + (tok + 2) * 2 * G);
+#pragma unroll
+        for (int pl = 0; pl < G / Gp; ++pl) {
+            uint32_t kw[2][Gp];
+            lds(kw[0], blk + pl * 256 * Gp + lane * 4 * Gp);
+            lds(kw[1], blk + pl * 256 * Gp + 128 * Gp + lane * 4 * Gp);
+#pragma unroll
+            for (int gp = 0; gp < Gp; ++gp) {
+                const int g = pl * Gp + gp;
+                const uint32_t w0 = kw[0][gp], w1 = kw[1][gp], x0 = w0 >> 8, x1 = w1 >> 8;
+                const uint32_t a0[4] = {w0 & 0x000F000Fu, w1 & 0x000F000Fu, x0 & 0x000F000Fu, x1 & 0x000F000Fu};
+                const uint32_t a1[4] = {w0 & 0x00F000F0u, w1 & 0x00F000F0u, x0 & 0x00F000F0u, x1 & 0x00F000F0u};
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    uint32_t q[4];
+                    if constexpr (Sh::q_in_regs) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) q[k] = Q.b[(n * G + g) * 4 + k];
+                    } else {
+                        lds(q, qfrag + ((n * G + g) * 32 + lane) * 16);
+                    }
+                    float c[4] = {Q.init[n][g][0], Q.init[n][g][1], Q.init[n][g][0], Q.init[n][g][1]};
+                    mma_f16(c, a0, q[0], q[1]);
+                    mma_f16(c, a1, q[2], q[3]);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if constexpr (PIECES == 2) {
+                            s[n][h][0] = fmaf(dk[h][g], c[2 * h] + c[2 * h + 1], s[n][h][0]);
+                        } else {
+                            s[n][h][0] = fmaf(dk[h][g], c[2 * h], s[n][h][0]);
+                            s[n][h][NR - 1] = fmaf(dk[h][g], c[2 * h + 1], s[n][h][NR - 1]);
+                        }
+                    }
+                }
+            }
+        }
+    }
+
+    // the value scales' largest magnitude: each lane looks at G/4 of the block's 8G words
+    {
+        bool grown = false;
+        uint32_t w[(8 * G + 31) / 32];
+#pragma unroll
+        for (int i = 0; i < (8 * G + 31) / 32; ++i) {
+            const int at = i * 32 + lane;
+            w[i] = 0;
+            if (8 * G % 32 == 0 || at < 8 * G) {
+                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[i]) : "r"(blk + 17 * D + 4 * at));
+                w[i] &= 0x7FFF7FFFu;
+                if (MASK) {   // slots without a token may hold anything
+                    const int t0 = key0 + 2 * at / G, t1 = key0 + (2 * at + 1) / G;
+                    if (t0 < all_lo || t0 >= all_hi) w[i] &= 0xFFFF0000u;
+                    if (t1 < all_lo || t1 >= all_hi) w[i] &= 0x0000FFFFu;
+                }
+            }
+            grown |= __vmaxu2(w[i], S.scale_lim) != S.scale_lim;
+        }
+        if (__any_sync(0xFFFFFFFFu, grown)) {
+            uint32_t m = S.scale_lim & 0xFFFFu;
+#pragma unroll
+            for (int i = 0; i < (8 * G + 31) / 32; ++i) m = max(m, max(w[i] & 0xFFFFu, w[i] >> 16));
+            m = min(redux_max_u32(0xFFFFFFFFu, m), 0x7BFFu);
+            S.scale_lim = m | m << 16;
+            // |scale| < 2^(e + 1): probabilities up to 2^limit keep P * scale below 2^14
+            const int e = m >= 0x0400u ? static_cast<int>(m >> 10) - 15 : -15;
+            S.limit = static_cast<float>(13 - e);
+        }
+    }
+
+    // exponents against the reference
+    float p[NT][2][NR];
+    bool over = false;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+                if (MASK) {
+                    const int t = key0 + tok + 2 * h;
+                    if (t < Q.lo[n][r] || t >= Q.hi[n][r]) s[n][h][r] = -INFINITY;
+                }
+                p[n][h][r] = fmaf(s[n][h][r], Q.to_log2[n][r], -S.m[n][r]);
+                over |= p[n][h][r] > S.limit;
+            }
+    if (__any_sync(0xFFFFFFFFu, over)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+                float z = fmaxf(s[n][0][r], s[n][1][r]) * Q.to_log2[n][r];
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) z = fmaxf(z, __shfl_xor_sync(0xFFFFFFFFu, z, x));
+                if (z - S.m[n][r] > S.limit) {      // the row's new largest sits 2^6 below the limit
+                    const float m = z - (S.limit - 6.0f), f = ex2(S.m[n][r] - m);
+                    S.m[n][r] = m;
+                    S.l[n][r] *= f;
+#pragma unroll
+                    for (int g = 0; g < G; ++g)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                if (PIECES == 2 || (x & 1) == r) S.o[n][g][k][x] *= f;
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) p[n][h][r] = fmaf(s[n][h][r], Q.to_log2[n][r], -S.m[n][r]);
+            }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            p[n][0][r] = ex2(p[n][0][r]), p[n][1][r] = ex2(p[n][1][r]);
+            S.l[n][r] += p[n][0][r] + p[n][1][r];
+        }
+
+    // values
+    float dv[2][G];
+    load_scales<G>(dv[0], blk + 17 * D + tok * 2 * G);
+    load_scales<G>(dv[1], blk + 17 * D + (tok + 2) * 2 * G);
+#pragma unroll
+    for (int pl = 0; pl < G / Gp; ++pl) {
+        uint32_t vw[2][Gp];
+        lds(vw[0], blk + 8 * D + pl * 256 * Gp + lane * 4 * Gp);
+        lds(vw[1], blk + 8 * D + pl * 256 * Gp + 128 * Gp + lane * 4 * Gp);
+#pragma unroll
+        for (int gp = 0; gp < Gp; ++gp) {
+            const int g = pl * Gp + gp;
+            const uint32_t w0 = vw[0][gp], w1 = vw[1][gp], x0 = w0 >> 8, x1 = w1 >> 8;
+            const uint32_t a0[4] = {signed_nibbles<0>(w0), signed_nibbles<0>(x0), signed_nibbles<0>(w1), signed_nibbles<0>(x1)};
+            const uint32_t a1[4] = {signed_nibbles<1>(w0), signed_nibbles<1>(x0), signed_nibbles<1>(w1), signed_nibbles<1>(x1)};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                uint32_t b[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float x[NR];
+#pragma unroll
+                    for (int r = 0; r < NR; ++r) {
+                        x[r] = p[n][h][r] * dv[h][g];
+                        if (MASK) {   // 0 * (a scale that is not of a key the row sees) may be NaN
+                            const int t = key0 + tok + 2 * h;
+                            if (t < Q.lo[n][r] || t >= Q.hi[n][r]) x[r] = 0.0f;
+                        }
+                    }
+                    if constexpr (PIECES == 2) {     // the leading 11 bits, and the rest
+                        const float lead = __uint_as_float(__float_as_uint(x[0]) & 0xFFFFE000u);
+                        b[h] = transpose8(pack_half(lead, x[0] - lead));
+                    } else {
+                        b[h] = transpose8(pack_half(x[0], x[NR - 1]));
+                    }
+                }
+                mma_f16(S.o[n][g][0], a0, b[0], b[1]);
+                mma_f16(S.o[n][g][1], a1, b[0], b[1]);
+            }
+        }
+    }
+}
+
+template <int G, int PIECES, int NT>
+__global__ void __launch_bounds__(kWarps * 32, Shape<G, PIECES, NT>::blocks_per_sm) rows_kernel(const AttnArgs a)
+{
+    using Sh = Shape<G, PIECES, NT>;
+    constexpr int D = Sh::D, RT = Sh::RT, NST = Sh::NST, NR = Sh::NR;
+    extern __shared__ __align__(128) uint8_t smem[];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r8 = lane >> 2, c = lane & 3;
+    uint8_t *ring = smem + Sh::frag_bytes + warp * Sh::warp_bytes;
+    const uint32_t bars = smem_u32(smem + Sh::bars_at) + warp * NST * 8;
+    int *shared_flag = reinterpret_cast<int *>(smem + Sh::bars_at + kWarps * NST * 8);
+    if (lane == 0) {
+        for (int i = 0; i < NST; ++i) mbar_init(bars + 8 * i, 1);
+        fence_barrier_init();
+    }
+    __syncwarp();
+
+    // unit: row tile, split, head, sequence
+    int64_t u = blockIdx.x;
+    const int tile = static_cast<int>(u % a.tiles);
+    u /= a.tiles;
+    const int split = static_cast<int>(u % a.splits);
+    u /= a.splits;
+    const int hk = static_cast<int>(u % a.n_kv);
+    const int64_t b = u / a.n_kv;
+
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const Sequence seq = sequence_of(a, b);
+    if (seq.bad) {
+        if (split == 0) poison_rows(a, seq, hk, tile, a.rep * D);
+        return;
+    }
+    const int64_t r0 = seq.r0;
+    const int n_rows = static_cast<int>(seq.r1 - r0) * a.rep;      // rows of this sequence and head
+    const int first = tile * RT;
+    if (first >= n_rows) return;
+    const int rows = min(RT, n_rows - first);
+    const Span span = span_of(a, seq, first, rows);
+    const int active = span.active;
+    if (split >= active) return;
+    const int64_t b0 = split * span.per, b1 = span.blocks < b0 + span.per ? span.blocks : b0 + span.per;
+    const int nk = b1 - b0 > warp ? static_cast<int>((b1 - b0 - warp + kWarps - 1) / kWarps) : 0;
+
+    // addresses of this warp's next 32 blocks, one a lane
+    const uint64_t policy = l2_evict_first_policy();
+    bool poison = false;
+    const uint8_t *addr = nullptr;
+    auto look_up = [&](int k) {
+        addr = a.pages;
+        if (k + lane < nk) {
+            const int64_t blk = span.blk_lo + b0 + warp + static_cast<int64_t>(kWarps) * (k + lane);
+            const int64_t pg = blk / a.page_blocks;
+            const int32_t page = a.page_table[b * a.ld_pages + pg];
+            if (page < 0 || page >= a.n_pages) {
+                poison = true;
+                record_error(a.err, kErrBadIndex);
+            } else {
+                addr += ((static_cast<int64_t>(page) * a.n_kv + hk) * a.page_blocks + (blk - pg * a.page_blocks)) *
+                        static_cast<int64_t>(Sh::block_bytes);
+            }
+        }
+    };
+    auto issue = [&](int k) {
+        const uint64_t from = __shfl_sync(0xFFFFFFFFu, reinterpret_cast<uint64_t>(addr), k & 31);
+        if (lane == 0 && !(k == a.skip_block && blockIdx.x == 0 && warp == 0)) {
+            const uint32_t bar = bars + 8 * (k % NST);
+            mbar_arrive_expect_tx(bar, Sh::block_bytes);
+            bulk_g2s(smem_u32(ring) + (k % NST) * Sh::block_bytes, reinterpret_cast<const void *>(from),
+                     Sh::block_bytes, bar, policy);
+        }
+    };
+    if (nk > 0) look_up(0);
+    for (int k = 0; k < NST && k < nk; ++k) issue(k);
+
+    // query rows: scaled by a power of two to [2^10, 2^11), fp16 pieces in fragment order.  Two pieces are whole
+    // numbers and multiples of 2^-12, so that every product and sum of a group is exact in the tensor cores (which
+    // cut what they add at 2^-24 of the largest term: with floating pieces a score lost four bits to that, 1.2e-5
+    // of an output over 32768 keys instead of 1e-6).  One warp takes a row, a lane one channel of each group.
+    const uint32_t qfrag = smem_u32(smem);
+    float *col_init = reinterpret_cast<float *>(smem + Sh::init_at);     // [group][column]
+    float *row_log2 = col_init + NT * 8 * G;                             // [row]
+    for (int row = warp; row < RT; row += kWarps) {
+        const bool in = row < rows;
+        const int i = in ? (first + row) / a.rep : 0;
+        const int64_t at = (r0 + i) * a.ldq + (static_cast<int64_t>(hk) * a.rep + (first + row - i * a.rep)) * D;
+        float x[G], big = 0.0f;
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            x[g] = in ? load_as_float(a.q, at + 32 * g + lane, a.q_type) : 0.0f;
+            big = fmaxf(big, fabsf(x[g]));
+        }
+        big = __uint_as_float(redux_max_u32(0xFFFFFFFFu, __float_as_uint(big)));
+        int e = 127;
+        if (big > 0.0f && big < INFINITY) e = 127 + 10 - (static_cast<int>(__float_as_uint(big) >> 23) - 127);
+        e = min(e, 250);
+        // the scale's sign goes to the query, so that -inf masks a score whatever the scale
+        const float up = copysignf(__uint_as_float(static_cast<uint32_t>(e) << 23), a.scale_log2);
+        // exponent of 2 per unit of (q' n 2^-24), never 0: scale * log2(e) * 2^24 / up
+        if (lane == 0) row_log2[row] = fmaxf(a.scale_log2 * kTwo24 / up, 1.2e-38f);
+        const int col = row * PIECES, j = lane & 7, st = j & 1;
+        // the pair's register of the fragment (x[st], x[st + 4]) or (x[st + 2], x[st + 6]), and the half in it
+        const int at_half = st * 8 + ((j >> 1) & 1) * 4 + (j >> 2) * 2;
+        uint8_t *to = smem + ((col >> 3) * G * 32 + (col & 7) * 4 + (lane >> 3)) * 16 + at_half;
+        const float sixteenth = st ? 0.0625f : 1.0f;     // odd channels' nibbles come 16 times as large
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            float v = x[g] * up, rest = 0.0f;
+            if (PIECES == 2) {
+                const float lead = rintf(v);
+                rest = rintf((v - lead) * 4096.0f) * (1.0f / 4096.0f);
+                v = lead;
+                *reinterpret_cast<__half *>(to + g * 512 + 64) = __float2half_rn(rest * sixteenth);   // the next column
+            } else {
+                v = __half2float(__float2half_rn(v));
+            }
+            *reinterpret_cast<__half *>(to + g * 512) = __float2half_rn(v * sixteenth);
+#pragma unroll
+            for (int o = 16; o; o >>= 1) {
+                v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+                if (PIECES == 2) rest += __shfl_xor_sync(0xFFFFFFFFu, rest, o);
+            }
+            if (lane == 0) {
+                col_init[NT * 8 * g + col] = v * (-8.0f / kTwo24);
+                if (PIECES == 2) col_init[NT * 8 * g + col + 1] = rest * (-8.0f / kTwo24);
+            }
+        }
+    }
+
+    State<G, PIECES, NT> S;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) S.o[n][g][k >> 2][k & 3] = 0.0f;
+#pragma unroll
+        for (int r = 0; r < NR; ++r) S.m[n][r] = kNoMax, S.l[n][r] = 0.0f;
+    }
+    S.limit = 28.0f;
+    S.scale_lim = 0;
+    __syncthreads();
+
+    const int64_t base = (span.blk_lo + b0) * kBlockTokens;
+    Query<G, PIECES, NT> Q;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            const int row = n * (8 / PIECES) + c * NR + r;
+            Q.to_log2[n][r] = row_log2[row];
+            const int64_t pos = seq.len - (seq.r1 - r0) + (row < rows ? (first + row) / a.rep : 0);
+            Q.lo[n][r] = clamp_key(a.window > 0 ? pos - a.window + 1 - base : -1);
+            Q.hi[n][r] = row < rows ? clamp_key(pos + 1 - base) : -1;
+        }
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) Q.init[n][g][x] = col_init[NT * 8 * g + n * 8 + 2 * c + x];
+            if constexpr (Sh::q_in_regs) {
+                uint32_t q[4];
+                lds(q, qfrag + ((n * G + g) * 32 + lane) * 16);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) Q.b[(n * G + g) * 4 + k] = q[k];
+            }
+        }
+    }
+
+    // keys every row sees, counted from the split's first block
+    const int64_t last_lo = a.window > 0 ? span.pos1 - a.window + 1 - base : 0;
+    const int64_t first_hi = span.pos0 + 1 - base;
+    const int all_lo = clamp_key(span.key_lo - base), all_hi = clamp_key(span.key_hi - base);
+    bool dead = false;
+    for (int k = 0; k < nk; ++k) {
+        // the warp shares the outcome: a limit may run out for one lane and not another
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(bars + 8 * (k % NST), (k / NST) & 1, a.wait_ns))) {
+            // give up: the copies still in flight are waited for before their memory is used for anything else
+            dead = true;
+            for (int i = k; i < nk && i < k + NST; ++i) mbar_wait(bars + 8 * (i % NST), (i / NST) & 1, a.wait_ns);
+            break;
+        }
+        const uint32_t blk = smem_u32(ring) + (k % NST) * Sh::block_bytes;
+        const int key0 = (warp + kWarps * k) * kBlockTokens;
+        if (key0 >= last_lo && key0 + kBlockTokens <= first_hi)
+            block16<G, PIECES, NT, false>(S, Q, blk, qfrag, key0, all_lo, all_hi, lane);
+        else
+            block16<G, PIECES, NT, true>(S, Q, blk, qfrag, key0, all_lo, all_hi, lane);
+        __syncwarp();
+        const int next = k + NST;
+        if (next < nk) {
+            if ((next & 31) == 0) look_up(next);
+            issue(next);
+        }
+    }
+    if (__any_sync(0xFFFFFFFFu, dead) && lane == 0) record_error(a.err, kErrTimeout);
+    poison = __any_sync(0xFFFFFFFFu, poison || dead);
+
+    // the warp's part: rows of D values and (M, l), in its own ring
+    float *part = reinterpret_cast<float *>(ring);
+    float *ml = part + RT * Sh::part_stride;
+    __syncwarp();
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            float l = S.l[n][r];
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, x);
+            if (poison) l = __int_as_float(0x7FC00000);
+            const int row = n * (8 / PIECES) + c * NR + r;
+            if (r8 == 0) ml[2 * row] = S.m[n][r], ml[2 * row + 1] = l;
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                float v[4];      // channels 32g + 4 r8 + 0..3
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+                        v[m + 2 * x] = PIECES == 2 ? S.o[n][g][m][2 * x] + S.o[n][g][m][2 * x + 1] : S.o[n][g][m][2 * x + r];
+                *reinterpret_cast<float4 *>(part + row * Sh::part_stride + 32 * g + 4 * r8) =
+                    make_float4(v[0], v[1], v[2], v[3]);
+            }
+        }
+    __syncthreads();
+
+    // join the warps' parts; a thread takes whole columns of rows
+    const uint8_t *rings = smem + Sh::frag_bytes;
+    auto warp_part = [&](int w) { return reinterpret_cast<const float *>(rings + w * Sh::warp_bytes); };
+    float *mine = nullptr;
+    int *counter = nullptr;
+    if (active > 1) {
+        const int64_t group = (b * a.n_kv + hk) * a.tiles + tile;
+        counter = a.counters + group;
+        mine = a.parts + (group * a.splits) * Sh::part_floats;
+    }
+    for (int i = threadIdx.x; i < rows * D; i += kWarps * 32) {
+        const int row = i / D, ch = i % D;
+        float m = kNoMax;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) m = fmaxf(m, warp_part(w)[RT * Sh::part_stride + 2 * row]);
+        float v = 0.0f, l = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float f = ex2(warp_part(w)[RT * Sh::part_stride + 2 * row] - m);
+            v = fmaf(f, warp_part(w)[row * Sh::part_stride + ch], v);
+            l = fmaf(f, warp_part(w)[RT * Sh::part_stride + 2 * row + 1], l);
+        }
+        if (active == 1) {
+            const int64_t to = (r0 + (first + row) / a.rep) * a.ldo +
+                               (static_cast<int64_t>(hk) * a.rep + (first + row) % a.rep) * D + ch;
+            store_float_as(a.out, to, a.out_type, l == 0.0f ? 0.0f : v / l);
+        } else {
+            float *to = mine + static_cast<int64_t>(split) * Sh::part_floats;
+            to[i] = v;
+            if (ch == 0) to[RT * D + 2 * row] = m, to[RT * D + 2 * row + 1] = l;
+        }
+    }
+    if (active == 1) return;
+
+    // the last split to get here joins all parts, in their order
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        const int seen = atomicAdd(counter, 1);
+        if (seen == active - 1) *counter = 0;
+        *shared_flag = seen == active - 1;
+    }
+    __syncthreads();
+    if (!*shared_flag) return;
+    __threadfence();
+    for (int i = threadIdx.x; i < rows * D; i += kWarps * 32) {
+        const int row = i / D, ch = i % D;
+        float m = kNoMax;
+        for (int w = 0; w < active; ++w) m = fmaxf(m, __ldcg(mine + static_cast<int64_t>(w) * Sh::part_floats + RT * D + 2 * row));
+        float v = 0.0f, l = 0.0f;
+#pragma unroll 4
+        for (int w = 0; w < active; ++w) {
+            const float *from = mine + static_cast<int64_t>(w) * Sh::part_floats;
+            const float f = ex2(__ldcg(from + RT * D + 2 * row) - m);
+            v = fmaf(f, __ldcg(from + i), v);
+            l = fmaf(f, __ldcg(from + RT * D + 2 * row + 1), l);
+        }
+        const int64_t to = (r0 + (first + row) / a.rep) * a.ldo +
+                           (static_cast<int64_t>(hk) * a.rep + (first + row) % a.rep) * D + ch;
+        store_float_as(a.out, to, a.out_type, l == 0.0f ? 0.0f : v / l);
+    }
+}
+
+template <int G, int PIECES, int NT>
+cudaError_t launch_rows(const AttnArgs &a, int64_t grid, cudaStream_t st)
+{
+    const auto kern = rows_kernel<G, PIECES, NT>;
+    constexpr int smem = Shape<G, PIECES, NT>::smem;
+    static_assert(smem <= 227 * 1024, "shared memory of a block");
+    // once a device; two threads that find it undone both do it
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 64 || !(done.load(std::memory_order_acquire) >> dev & 1)) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) done.fetch_or(1ull << dev, std::memory_order_release);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(kWarps * 32);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at = {};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = library_programmatic() ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kern, a);
+}
+
+// Column sets: 1, 2, or as many as the accumulators leave room for.
+template <int G>
+cudaError_t launch_rows_of(const AttnArgs &a, int pieces, int sets, int64_t grid, cudaStream_t st)
+{
+    if (sets == 1) return pieces == 2 ? launch_rows<G, 2, 1>(a, grid, st) : launch_rows<G, 1, 1>(a, grid, st);
+    if (sets == 2) return pieces == 2 ? launch_rows<G, 2, 2>(a, grid, st) : launch_rows<G, 1, 2>(a, grid, st);
+    if constexpr (G <= 4) return pieces == 2 ? launch_rows<G, 2, 4>(a, grid, st) : launch_rows<G, 1, 4>(a, grid, st);
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace attn
+}  // namespace qk
