@@ -11,8 +11,6 @@ namespace qk {
 using namespace attn;
 namespace {
 
-constexpr int kWarps = 8;      // of a thread block of the few-row form
-
 bool multiple(const void *p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 bool type_ok(int t) { return t == QK_F32 || t == QK_F16 || t == QK_BF16; }
 
@@ -20,14 +18,16 @@ bool type_ok(int t) { return t == QK_F32 || t == QK_F16 || t == QK_BF16; }
 struct Cut {
     int pieces, sets, row_tile, tiles, splits;
     bool chunk;                      // the many-row form (qk_attn_chunk.cu)
+    int64_t cut;                     // few rows: thread blocks that share all blocks (0: one a head)
     int64_t min_blocks, groups;      // groups: sequences * heads * tiles
 };
 
 std::atomic<int> g_skip_block{-1};
 
 constexpr int64_t kChunkFrom = 64;           // rows a sequence and head from which it is taken
-constexpr int64_t kCounters = 16384;         // at the start of every workspace, whatever the call
-Cut cut_for(int64_t B, int n_kv, int rep, int D, int64_t max_q, int64_t max_len, bool fp32)
+constexpr int64_t kCounters = 16384;         // ints at the start of every workspace, whatever the call
+// max_len sizes the cut; no sequence is longer than `longest`.
+Cut cut_for(int64_t B, int n_kv, int rep, int D, int64_t max_q, int64_t max_len, int64_t longest, bool fp32)
 {
     Cut c{};
     const int64_t rows = max_q * rep;
@@ -41,16 +41,14 @@ Cut cut_for(int64_t B, int n_kv, int rep, int D, int64_t max_q, int64_t max_len,
     c.tiles = static_cast<int>((rows + c.row_tile - 1) / c.row_tile);
     c.groups = B * n_kv * c.tiles;
     const int64_t blocks = (max_len + kBlockTokens - 1) / kBlockTokens;
-    // The split with the least of (rounds of thread blocks) * (steps of a warp + a thread block's start and join,
-    // about 10 steps), of splits that leave every warp two blocks.
     int sms = 152, smem = 0;
     device_limits(&sms, &smem);
+    c.splits = 1;
     if (c.chunk) {
         // rounds of one thread block an SM, of key tiles of 8 blocks (about 1.2 us each) and 3 tiles' worth of start
         // and end; parts of several splits are written and read again (5 TB/s) by a second kernel (2 us)
         const int64_t tiles = (blocks + 7) / 8;
         double best = 1e30;
-        c.splits = 1;
         for (int64_t rounds = 1, last = 0; rounds <= 8; ++rounds) {
             int64_t s = sms * rounds / c.groups;
             if (s * 2 > tiles) s = tiles / 2;
@@ -65,22 +63,13 @@ Cut cut_for(int64_t B, int n_kv, int rep, int D, int64_t max_q, int64_t max_len,
         if (c.min_blocks < 16) c.min_blocks = 16;
         return c;
     }
-    const int64_t slots = static_cast<int64_t>(sms) * (c.sets > 2 || (D > 128 && c.sets > 1) ? 1 : 2);
-    int64_t best = 1, best_cost = INT64_MAX;
-    for (int64_t rounds = 1, last = 0; rounds <= 12 && c.groups <= kCounters; ++rounds) {
-        // as many splits as `rounds` rounds hold, or one
-        int64_t s = slots * rounds / c.groups;
-        if (s * 2 * kWarps > blocks) s = blocks / (2 * kWarps);
-        if (s < 1) s = 1;
-        if (s == last) continue;
-        last = s;
-        const int64_t per = (blocks + s - 1) / s;
-        const int64_t cost = (c.groups * s + slots - 1) / slots * ((per + kWarps - 1) / kWarps + 10);
-        if (cost < best_cost) best = s, best_cost = cost;
-    }
-    c.splits = static_cast<int>(best);
-    c.min_blocks = (blocks + best - 1) / best;
-    if (c.min_blocks < 2 * kWarps) c.min_blocks = 2 * kWarps;
+    // few rows: split where heads are at most half of the thread blocks that the GPU holds and have blocks to split,
+    // over as many thread blocks as that.  (With more heads than that, one thread block a head: 512 heads of 8192
+    // tokens take 146 us whole and 148, 160, 162 us in 2, 3, 4 parts.)
+    const int64_t hold = static_cast<int64_t>(sms) * rows_blocks_per_sm(D / 32, c.sets);
+    if (blocks > 2 * kWarps && c.groups * 2 <= hold && B * c.tiles <= kRowItems &&
+        c.groups * ((longest + kBlockTokens - 1) / kBlockTokens) < (1 << 30))
+        c.cut = hold;
     return c;
 }
 
@@ -111,8 +100,9 @@ size_t qk_attn_q4_workspace_bytes(int64_t B, int n_q_heads, int n_kv_heads, int 
         return 0;
     size_t most = 0;
     for (const bool fp32 : {true, false}) {
-        const Cut c = cut_for(B, n_kv_heads, n_q_heads / n_kv_heads, head_dim, max_q, max_len, fp32);
-        const size_t n = c.splits > 1 ? 4 * kCounters + c.groups * c.splits * part_bytes_of(c, head_dim) : 0;
+        const Cut c = cut_for(B, n_kv_heads, n_q_heads / n_kv_heads, head_dim, max_q, max_len, max_len, fp32);
+        const size_t n = c.cut ? 4 * kCounters + c.cut * part_bytes_of(c, head_dim)
+                               : c.splits > 1 ? 4 * kCounters + c.groups * c.splits * part_bytes_of(c, head_dim) : 0;
         if (n > most) most = n;
     }
     return most;
@@ -148,12 +138,13 @@ int qk_attn_q4(const qk_kv_cache_q4 *cache, const void *q, int64_t ldq, int q_ty
         max_pages > INT32_MAX / cache->page_tokens)
         return QK_ERR_TOO_LARGE;
     const int64_t keys = max_pages * cache->page_tokens;
-    Cut cut = cut_for(B, n_kv, rep, D, max_q, max_len > 0 && max_len < keys ? max_len : keys, q_type == QK_F32);
-    // as many splits as the workspace holds
+    Cut cut = cut_for(B, n_kv, rep, D, max_q, max_len > 0 && max_len < keys ? max_len : keys, keys, q_type == QK_F32);
+    // as many splits, or parts of thread blocks, as the workspace holds
     const int64_t room = workspace ? static_cast<int64_t>(workspace_bytes) - 4 * kCounters : 0;
-    const int64_t fit = room > 0 ? room / (cut.groups * part_bytes_of(cut, D)) : 0;
-    if (cut.splits > fit) cut.splits = fit > 1 ? static_cast<int>(fit) : 1;
-    const int64_t grid = cut.groups * cut.splits;
+    const int64_t fit = room > 0 ? room / part_bytes_of(cut, D) : 0;
+    if (cut.splits > 1 && cut.splits > fit / cut.groups) cut.splits = fit / cut.groups > 1 ? static_cast<int>(fit / cut.groups) : 1;
+    if (cut.cut > fit) cut.cut = fit > cut.groups ? fit : 0;
+    const int64_t grid = cut.cut ? cut.cut : cut.groups * cut.splits;
     if (grid > INT32_MAX) return QK_ERR_TOO_LARGE;
     AttnArgs a{};
     a.pages = static_cast<const uint8_t *>(cache->pages), a.n_pages = cache->n_pages;
@@ -163,7 +154,8 @@ int qk_attn_q4(const qk_kv_cache_q4 *cache, const void *q, int64_t ldq, int q_ty
     a.lens = lens, a.q_start = q_start, a.T = T, a.max_q = max_q, a.window = window;
     a.scale_log2 = static_cast<float>(scale * 1.4426950408889634074);
     a.out = out, a.ldo = ldo, a.out_type = out_type;
-    a.tiles = cut.tiles, a.splits = cut.splits, a.min_blocks = cut.min_blocks;
+    a.tiles = cut.tiles, a.items = static_cast<int>(B * cut.tiles), a.cut = static_cast<int>(cut.cut);
+    a.splits = cut.splits, a.min_blocks = static_cast<int>(cut.min_blocks < INT32_MAX ? cut.min_blocks : INT32_MAX);
     a.counters = static_cast<int *>(workspace);
     a.parts = reinterpret_cast<float *>(static_cast<char *>(workspace) + 4 * kCounters);
     a.err = library_error_word();

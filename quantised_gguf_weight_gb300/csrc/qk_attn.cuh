@@ -24,8 +24,10 @@ struct AttnArgs {
     void *out;
     int64_t ldo;
     int out_type;
-    int tiles, splits;               // row tiles a sequence and head, splits of its blocks
-    int64_t min_blocks;              // blocks a split takes at least
+    int tiles, items;                // row tiles a sequence, and of all sequences
+    int cut;                         // few rows: thread blocks that split heads share (0: one a head and item)
+    int splits;                      // many rows: splits of a head's blocks
+    int min_blocks;                  // blocks a split takes at least
     int *counters;
     float *parts;
     int *err;
@@ -85,14 +87,12 @@ __device__ __forceinline__ void poison_rows(const AttnArgs &a, const Sequence &s
                            __int_as_float(0x7FC00000));
 }
 
-// The 16-token blocks that the rows [first, first + rows) of a sequence see,
-// and how many splits take them.
+// The 16-token blocks that the rows [first, first + rows) of a sequence see.
 struct Span {
     int64_t pos0, pos1;          // positions of the first and the last row
     int64_t key_lo, key_hi;      // keys that some row sees
-    int64_t blk_lo, blocks;
-    int64_t per;                 // blocks a split
-    int active;                  // splits with blocks (at least one)
+    int64_t blk_lo;
+    int blocks;                  // at most 2^27: lengths are below 2^31
 };
 __device__ __forceinline__ Span span_of(const AttnArgs &a, const Sequence &s, int first, int rows)
 {
@@ -101,14 +101,17 @@ __device__ __forceinline__ Span span_of(const AttnArgs &a, const Sequence &s, in
     p.key_lo = a.window > 0 && p.pos0 - a.window + 1 > 0 ? p.pos0 - a.window + 1 : 0;
     p.key_hi = p.pos1 + 1 > 0 ? p.pos1 + 1 : 0;
     p.blk_lo = p.key_lo / kBlockTokens;
-    p.blocks = p.key_hi > p.key_lo ? (p.key_hi + kBlockTokens - 1) / kBlockTokens - p.blk_lo : 0;
-    p.per = (p.blocks + a.splits - 1) / a.splits;
-    if (p.per < a.min_blocks) p.per = a.min_blocks;
-    p.active = p.blocks > p.per ? static_cast<int>((p.blocks + p.per - 1) / p.per) : 1;
+    p.blocks = p.key_hi > p.key_lo ? static_cast<int>((p.key_hi + kBlockTokens - 1) / kBlockTokens - p.blk_lo) : 0;
     return p;
 }
 
 __device__ __forceinline__ int clamp_key(int64_t k) { return static_cast<int>(k < -1 ? -1 : (k > INT32_MAX ? INT32_MAX : k)); }
+
+// Thread blocks an SM holds of the few-row form: two (128 registers a thread), one where accumulators and queries
+// need more.
+constexpr int kWarps = 8;
+__host__ __device__ constexpr int rows_blocks_per_sm(int G, int NT) { return G <= 4 && NT <= 2 ? 2 : 1; }
+constexpr int kRowItems = 512;           // row tiles of all sequences whose heads may be split
 
 // The few-row form (qk_attn_rows.cuh), by head size: rows of `pieces` fp16 pieces in `sets` sets of 8 columns.
 cudaError_t rows_launch_64(const AttnArgs &a, int pieces, int sets, int64_t grid, cudaStream_t st);

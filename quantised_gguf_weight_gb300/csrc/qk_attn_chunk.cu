@@ -123,6 +123,13 @@ struct Bars {
     __device__ __forceinline__ uint32_t odone(int i) const { return at + 8 * (2 * kSlots + 12 + i); }
 };
 
+// Splits of a head that have blocks, at least one: each takes the same number.
+__device__ __forceinline__ int active_splits(const AttnArgs &a, int blocks)
+{
+    const int per = max((blocks + a.splits - 1) / a.splits, a.min_blocks);
+    return blocks > per ? (blocks + per - 1) / per : 1;
+}
+
 // What a thread block works on.
 struct Work {
     int64_t b;
@@ -130,6 +137,7 @@ struct Work {
     Sequence seq;
     Span span;
     int n, first, rows;          // rows of the sequence and head; this block's
+    int active;                  // splits with blocks (at least one)
     int nblk, ntiles;            // 16-token blocks and key tiles of this split
     int64_t blk0;                // its first block in the sequence
     int two;                     // both row tiles hold rows
@@ -254,10 +262,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttnArgs a)
     w.rows = min(kChunkRows, w.n - w.first);
     w.two = w.rows > 128;
     w.span = span_of(a, w.seq, w.first, w.rows);
-    if (w.split >= w.span.active) return;
-    const int64_t b0 = w.split * w.span.per;
-    w.nblk = static_cast<int>(w.span.blocks < b0 + w.span.per ? w.span.blocks - b0 : w.span.per);
-    if (w.nblk < 0) w.nblk = 0;
+    const int per = max((w.span.blocks + a.splits - 1) / a.splits, a.min_blocks);
+    w.active = active_splits(a, w.span.blocks);
+    if (w.split >= w.active) return;
+    const int b0 = w.split * per;
+    w.nblk = min(w.span.blocks - b0, per);
     w.ntiles = (w.nblk + kTileBlocks - 1) / kTileBlocks;
     w.blk0 = w.span.blk_lo + b0;
     const int64_t base = w.blk0 * kBlockTokens;
@@ -558,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttnArgs a)
         if (poison) R.l = __int_as_float(0x7FC00000);
         const float inv = R.l == 0.0f ? 0.0f : 1.0f / R.l;
         float *part = nullptr;
-        if (w.span.active > 1) {
+        if (w.active > 1) {
             const int64_t group = (w.b * a.tiles + w.tile) * a.n_kv + w.hk;
             part = a.parts + (group * a.splits + w.split) * (chunk_part_bytes(D) / 4);
             if (row_in) {
@@ -612,7 +621,7 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnArgs a, int D, int6
     if (seq.bad) return;
     const int n = static_cast<int>(seq.r1 - seq.r0) * a.rep, first = tile * kChunkRows;
     if (first + row >= n) return;
-    const int active = span_of(a, seq, first, min(kChunkRows, n - first)).active;
+    const int active = active_splits(a, span_of(a, seq, first, min(kChunkRows, n - first)).blocks);
     if (active <= 1) return;
     const int64_t stride = chunk_part_bytes(D) / 4;
     const float *part = a.parts + group * a.splits * stride;

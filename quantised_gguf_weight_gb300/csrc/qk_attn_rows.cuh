@@ -30,8 +30,14 @@
 // blocks need no shuffle and no rescaling.
 //
 // Blocks of 16 tokens arrive by bulk copies in a ring of stages of each warp
-// (no barrier across warps in the loop); a sequence's blocks are split over
-// thread blocks, and the last to finish joins the parts in a fixed order.
+// (no barrier across warps in the loop).  Where heads are fewer than the
+// thread blocks that the GPU holds, each head's blocks are split evenly over
+// several thread blocks, by the lengths found on the device, and the last of
+// them to finish joins their parts in their order; else a thread block has a
+// head to itself.  (One line of all heads' blocks cut into equal pieces that
+// cross heads, a thread block going through several heads, balanced better
+// but cost 12% more instructions a block: 64 x 8192 tokens 149 us against
+// 146.)
 #pragma once
 
 #include <atomic>
@@ -42,7 +48,6 @@
 namespace qk {
 namespace attn {
 
-constexpr int kWarps = 8;
 constexpr float kTwo24 = 16777216.0f;
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
@@ -105,12 +110,14 @@ __device__ __forceinline__ void load_scales(float (&d)[G], uint32_t addr)
 
 // A warp's tile: NT sets of 8 columns; PIECES 1: a column is a row, 2: a row
 // has its two pieces in columns 2k, 2k + 1.
+constexpr int kMaxItems = kRowItems;
+
 template <int G, int PIECES, int NT>
 struct Shape {
     static constexpr int D = 32 * G, RT = NT * 8 / PIECES;
     static constexpr int NR = 2 / PIECES;                             // rows of a lane in each column set
     static constexpr int block_bytes = 18 * D;
-    static constexpr int blocks_per_sm = (G <= 4 && NT <= 2) || NT == 1 ? 2 : 1;
+    static constexpr int blocks_per_sm = rows_blocks_per_sm(G, NT);
     static constexpr int NST = G <= 2 ? 6 : 4;
     static constexpr bool q_in_regs = G * NT <= 4;
     static constexpr int frag_bytes = NT * G * 2 * 32 * 8;
@@ -119,9 +126,11 @@ struct Shape {
     static constexpr int ring_bytes = NST * block_bytes;
     static constexpr int warp_bytes = ((ring_bytes > part_bytes ? ring_bytes : part_bytes) + 127) / 128 * 128;
     static constexpr int bars_at = frag_bytes + kWarps * warp_bytes;
-    static constexpr int init_at = bars_at + kWarps * NST * 8 + 16;   // after the barriers and the join's flag
+    static constexpr int misc_at = bars_at + kWarps * NST * 8;        // the scan's sums, where this thread block stands
+    static constexpr int init_at = misc_at + kWarps * 4 + 32;         // [group][column], then [row]
     static constexpr int smem = init_at + NT * 8 * G * 4 + RT * 4;
     static constexpr int part_floats = RT * D + 2 * RT;               // in the workspace
+    static_assert(smem <= 227 * 1024, "shared memory of a block");
 };
 
 // One warp's running state.  A lane (r = lane/4, c = lane%4) has, in each column set, rows 2c, 2c + 1 (or c).
@@ -321,48 +330,180 @@ __device__ __forceinline__ void block16(State<G, PIECES, NT> &S, const Query<G, 
     }
 }
 
+// Rows without a key are 0.
+__device__ __forceinline__ void zero_rows(const AttnArgs &a, const Sequence &s, int hk, int first, int row_tile, int D)
+{
+    const int n = static_cast<int>(s.r1 - s.r0) * a.rep;
+    for (int row = first; row < n && row < first + row_tile; ++row) {
+        const int64_t at = (s.r0 + row / a.rep) * a.ldo + (static_cast<int64_t>(hk) * a.rep + row % a.rep) * D;
+        for (int i = threadIdx.x; i < D; i += blockDim.x) store_float_as(a.out, at + i, a.out_type, 0.0f);
+    }
+}
+
+// Four channels of a row out, divided by the row's sum.
+__device__ __forceinline__ void store_row4(const AttnArgs &a, int64_t at, const float4 &v, float l)
+{
+    const float x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) store_float_as(a.out, at + e, a.out_type, l == 0.0f ? 0.0f : x[e] / l);
+}
+
+// The parts of the thread blocks that share a head: `count` from c_first on.  Rows' references and sums come first, into shared memory, a batch of parts at a time; then a thread
+// takes four channels of every `ways`-th part, and the ways are added in order.
+template <int RT, int D, class OutAt>
+__device__ __forceinline__ void join_parts(const AttnArgs &a, int c_first, int count, int rows, float *buf, int buf_floats,
+                                           OutAt out_at)
+{
+    constexpr int part_floats = RT * D + 2 * RT, kThreads = kWarps * 32;
+    auto part = [&](int p) { return a.parts + static_cast<int64_t>(c_first + p) * part_floats; };
+    const int cols = rows * (D / 4);
+    const int ways = cols >= kThreads ? 1 : kThreads / cols;
+    float *sum = buf, *ml = buf + (ways > 1 ? ways * cols * 4 : 0);
+    const int batch = (buf_floats - static_cast<int>(ml - buf)) / (2 * rows);      // parts whose (M, l) fit beside the sums
+    for (int i0 = 0; i0 < cols; i0 += kThreads) {        // more than one round only where ways is 1
+        const int i = i0 + static_cast<int>(threadIdx.x), way = i / cols;
+        const int col = ways > 1 ? i % cols : i, row = col / (D / 4), ch = col % (D / 4) * 4;
+        const bool on = ways > 1 ? way < ways : i < cols;
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        float m = kNoMax, l = 0.0f;
+        for (int p0 = 0; p0 < count; p0 += batch) {
+            const int n = min(batch, count - p0);
+            __syncthreads();
+            for (int j = threadIdx.x; j < 2 * rows * n; j += kThreads)
+                ml[j] = __ldcg(part(p0 + j / (2 * rows)) + RT * D + j % (2 * rows));
+            __syncthreads();
+            if (on) {
+                float m2 = m;
+                for (int p = 0; p < n; ++p) m2 = fmaxf(m2, ml[2 * rows * p + 2 * row]);
+                const float f0 = ex2(m - m2);
+                m = m2, l *= f0, v.x *= f0, v.y *= f0, v.z *= f0, v.w *= f0;
+                for (int p = 0; p < n; ++p) l = fmaf(ex2(ml[2 * rows * p + 2 * row] - m), ml[2 * rows * p + 2 * row + 1], l);
+                const int start = ways > 1 ? way : 0;
+#pragma unroll 8
+                for (int p = start; p < n; p += ways) {
+                    const float f = ex2(ml[2 * rows * p + 2 * row] - m);
+                    const float4 x = __ldcg(reinterpret_cast<const float4 *>(part(p0 + p) + row * D + ch));
+                    v.x = fmaf(f, x.x, v.x), v.y = fmaf(f, x.y, v.y), v.z = fmaf(f, x.z, v.z), v.w = fmaf(f, x.w, v.w);
+                }
+            }
+        }
+        if (ways == 1) {
+            if (on) store_row4(a, out_at(row) + ch, v, l);
+        } else {
+            __syncthreads();
+            if (on) *reinterpret_cast<float4 *>(sum + (way * cols + col) * 4) = v;
+            __syncthreads();
+            if (on && way == 0) {
+                for (int y = 1; y < ways; ++y) {
+                    const float4 x = *reinterpret_cast<const float4 *>(sum + (y * cols + col) * 4);
+                    v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+                }
+                store_row4(a, out_at(row) + ch, v, l);
+            }
+        }
+    }
+}
+
 template <int G, int PIECES, int NT>
 __global__ void __launch_bounds__(kWarps * 32, Shape<G, PIECES, NT>::blocks_per_sm) rows_kernel(const AttnArgs a)
 {
     using Sh = Shape<G, PIECES, NT>;
-    constexpr int D = Sh::D, RT = Sh::RT, NST = Sh::NST, NR = Sh::NR;
+    constexpr int D = Sh::D, RT = Sh::RT, NST = Sh::NST, NR = Sh::NR, kThreads = kWarps * 32;
     extern __shared__ __align__(128) uint8_t smem[];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r8 = lane >> 2, c = lane & 3;
     uint8_t *ring = smem + Sh::frag_bytes + warp * Sh::warp_bytes;
     const uint32_t bars = smem_u32(smem + Sh::bars_at) + warp * NST * 8;
-    int *shared_flag = reinterpret_cast<int *>(smem + Sh::bars_at + kWarps * NST * 8);
+    int *sums = reinterpret_cast<int *>(smem + Sh::misc_at), *stand = sums + kWarps;
     if (lane == 0) {
         for (int i = 0; i < NST; ++i) mbar_init(bars + 8 * i, 1);
         fence_barrier_init();
     }
     __syncwarp();
-
-    // unit: row tile, split, head, sequence
-    int64_t u = blockIdx.x;
-    const int tile = static_cast<int>(u % a.tiles);
-    u /= a.tiles;
-    const int split = static_cast<int>(u % a.splits);
-    u /= a.splits;
-    const int hk = static_cast<int>(u % a.n_kv);
-    const int64_t b = u / a.n_kv;
-
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const Sequence seq = sequence_of(a, b);
-    if (seq.bad) {
-        if (split == 0) poison_rows(a, seq, hk, tile, a.rep * D);
-        return;
+
+    // This thread block's item (row tile of a sequence), head and split.
+    auto blocks_of = [&](int item, int *why) -> int {
+        const Sequence s = sequence_of(a, item / a.tiles);
+        const int at = item % a.tiles * RT, n = s.bad ? 0 : static_cast<int>(s.r1 - s.r0) * a.rep;
+        const int blocks = at < n ? span_of(a, s, at, min(RT, n - at)).blocks : 0;
+        *why = s.bad ? 1 : (at < n && blocks == 0 ? 2 : 0);
+        return blocks;
+    };
+    auto rows_without_blocks = [&](int item, int hk, int why) {
+        const Sequence s = sequence_of(a, item / a.tiles);
+        if (why == 1) poison_rows(a, s, hk, item % a.tiles, a.rep * D);
+        else zero_rows(a, s, hk, item % a.tiles * RT, RT, D);
+    };
+    int item = static_cast<int>(blockIdx.x / a.n_kv), hk = static_cast<int>(blockIdx.x) - item * a.n_kv;
+    int b0 = 0, c_first = 0, active = 1, per = INT32_MAX;
+    if (a.cut) {
+        // Every item's blocks (below 2^31 in all: the host sees to it), two items a thread; from their sum the blocks
+        // a split takes, so that all splits fit the thread blocks; then which split this one is.
+        static_assert(kMaxItems <= 2 * kThreads, "two items a thread");
+        int n[2] = {0, 0}, why[2] = {0, 0};
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            if (2 * static_cast<int>(threadIdx.x) + k < a.items) n[k] = blocks_of(2 * threadIdx.x + k, &why[k]);
+        int total = n[0] + n[1];
+        if (a.items > 1) {
+            total = __reduce_add_sync(0xFFFFFFFFu, total);
+            if (lane == 0) sums[warp] = total;
+            __syncthreads();
+            total = 0;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) total += sums[w];
+        } else {
+            total = __shfl_sync(0xFFFFFFFFu, blocks_of(0, &why[1]), 0), why[1] = 0;
+        }
+        total *= a.n_kv;
+        const int room = a.cut - a.items * a.n_kv;       // above 0: the host splits where heads are few
+        per = max((total + room - 1) / room, 2 * kWarps);
+        const int u[2] = {(n[0] + per - 1) / per * a.n_kv, (n[1] + per - 1) / per * a.n_kv};
+        int run = u[0] + u[1];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int below = __shfl_up_sync(0xFFFFFFFFu, run, o);
+            if (lane >= o) run += below;
+        }
+        if (a.items > 1) __syncthreads();
+        if (threadIdx.x == 0) stand[0] = -1;
+        if (lane == 31) sums[warp] = run;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) run += sums[w];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int end = k ? run : run - u[1], begin = end - u[k];
+            if (static_cast<int>(blockIdx.x) >= begin && static_cast<int>(blockIdx.x) < end) {
+                const int at = static_cast<int>(blockIdx.x) - begin, each = u[k] / a.n_kv;
+                stand[0] = 2 * threadIdx.x + k, stand[1] = at / each, stand[2] = at % each, stand[3] = each;
+            }
+        }
+        // rows without blocks: the thread block of the item's number, and so on round
+        if (__syncthreads_or(why[0] | why[1]))
+            for (int it = blockIdx.x; it < a.items; it += gridDim.x) {
+                int w;
+                blocks_of(it, &w);
+                if (w)
+                    for (int h = 0; h < a.n_kv; ++h) rows_without_blocks(it, h, w);
+            }
+        item = stand[0], hk = stand[1], active = stand[3];
+        if (item < 0) return;
+        b0 = stand[2] * per, c_first = static_cast<int>(blockIdx.x) - stand[2];
+    } else {
+        int why;
+        if (blocks_of(item, &why) == 0) {
+            if (why) rows_without_blocks(item, hk, why);
+            return;
+        }
     }
+    const int64_t b = item / a.tiles;
+    const Sequence seq = sequence_of(a, b);
     const int64_t r0 = seq.r0;
-    const int n_rows = static_cast<int>(seq.r1 - r0) * a.rep;      // rows of this sequence and head
-    const int first = tile * RT;
-    if (first >= n_rows) return;
-    const int rows = min(RT, n_rows - first);
+    const int first = item % a.tiles * RT, rows = min(RT, static_cast<int>(seq.r1 - r0) * a.rep - first);
     const Span span = span_of(a, seq, first, rows);
-    const int active = span.active;
-    if (split >= active) return;
-    const int64_t b0 = split * span.per, b1 = span.blocks < b0 + span.per ? span.blocks : b0 + span.per;
-    const int nk = b1 - b0 > warp ? static_cast<int>((b1 - b0 - warp + kWarps - 1) / kWarps) : 0;
+    const int b1 = span.blocks - b0 < per ? span.blocks : b0 + per;
+    const int nk = b1 - b0 > warp ? (b1 - b0 - warp + kWarps - 1) / kWarps : 0;
 
     // addresses of this warp's next 32 blocks, one a lane
     const uint64_t policy = l2_evict_first_policy();
@@ -383,13 +524,11 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<G, PIECES, NT>::blocks_per_
             }
         }
     };
-    auto issue = [&](int k) {
-        const uint64_t from = __shfl_sync(0xFFFFFFFFu, reinterpret_cast<uint64_t>(addr), k & 31);
-        if (lane == 0 && !(k == a.skip_block && blockIdx.x == 0 && warp == 0)) {
+    auto issue = [&](int k) {        // by the lane that holds the address
+        if (lane == (k & 31) && !(k == a.skip_block && blockIdx.x == 0 && warp == 0)) {
             const uint32_t bar = bars + 8 * (k % NST);
             mbar_arrive_expect_tx(bar, Sh::block_bytes);
-            bulk_g2s(smem_u32(ring) + (k % NST) * Sh::block_bytes, reinterpret_cast<const void *>(from),
-                     Sh::block_bytes, bar, policy);
+            bulk_g2s(smem_u32(ring) + (k % NST) * Sh::block_bytes, addr, Sh::block_bytes, bar, policy);
         }
     };
     if (nk > 0) look_up(0);
@@ -463,7 +602,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<G, PIECES, NT>::blocks_per_
     S.scale_lim = 0;
     __syncthreads();
 
-    const int64_t base = (span.blk_lo + b0) * kBlockTokens;
+    const int64_t base = (span.blk_lo + b0) * kBlockTokens;      // the first key of this split
     Query<G, PIECES, NT> Q;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -545,67 +684,51 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<G, PIECES, NT>::blocks_per_
         }
     __syncthreads();
 
-    // join the warps' parts; a thread takes whole columns of rows
+    // join the warps' parts; a thread takes four channels of a row
     const uint8_t *rings = smem + Sh::frag_bytes;
     auto warp_part = [&](int w) { return reinterpret_cast<const float *>(rings + w * Sh::warp_bytes); };
-    float *mine = nullptr;
-    int *counter = nullptr;
-    if (active > 1) {
-        const int64_t group = (b * a.n_kv + hk) * a.tiles + tile;
-        counter = a.counters + group;
-        mine = a.parts + (group * a.splits) * Sh::part_floats;
-    }
-    for (int i = threadIdx.x; i < rows * D; i += kWarps * 32) {
-        const int row = i / D, ch = i % D;
+    auto out_at = [&](int row) {
+        const int i = (first + row) / a.rep;
+        return (r0 + i) * a.ldo + (static_cast<int64_t>(hk) * a.rep + first + row - i * a.rep) * D;
+    };
+    float *mine = active > 1 ? a.parts + static_cast<int64_t>(blockIdx.x) * Sh::part_floats : nullptr;
+    for (int i = threadIdx.x; i < rows * (D / 4); i += kThreads) {
+        const int row = i / (D / 4), ch = i % (D / 4) * 4;
         float m = kNoMax;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) m = fmaxf(m, warp_part(w)[RT * Sh::part_stride + 2 * row]);
-        float v = 0.0f, l = 0.0f;
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        float l = 0.0f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
             const float f = ex2(warp_part(w)[RT * Sh::part_stride + 2 * row] - m);
-            v = fmaf(f, warp_part(w)[row * Sh::part_stride + ch], v);
+            const float4 x = *reinterpret_cast<const float4 *>(warp_part(w) + row * Sh::part_stride + ch);
+            v.x = fmaf(f, x.x, v.x), v.y = fmaf(f, x.y, v.y), v.z = fmaf(f, x.z, v.z), v.w = fmaf(f, x.w, v.w);
             l = fmaf(f, warp_part(w)[RT * Sh::part_stride + 2 * row + 1], l);
         }
-        if (active == 1) {
-            const int64_t to = (r0 + (first + row) / a.rep) * a.ldo +
-                               (static_cast<int64_t>(hk) * a.rep + (first + row) % a.rep) * D + ch;
-            store_float_as(a.out, to, a.out_type, l == 0.0f ? 0.0f : v / l);
+        if (mine) {
+            *reinterpret_cast<float4 *>(mine + row * D + ch) = v;
+            if (ch == 0) mine[RT * D + 2 * row] = m, mine[RT * D + 2 * row + 1] = l;
         } else {
-            float *to = mine + static_cast<int64_t>(split) * Sh::part_floats;
-            to[i] = v;
-            if (ch == 0) to[RT * D + 2 * row] = m, to[RT * D + 2 * row + 1] = l;
+            store_row4(a, out_at(row) + ch, v, l);
         }
     }
-    if (active == 1) return;
+    if (!mine) return;
 
-    // the last split to get here joins all parts, in their order
+    // the last of the head's thread blocks to get here joins their parts, in their order
     __threadfence();
     __syncthreads();
     if (threadIdx.x == 0) {
+        int *counter = a.counters + static_cast<int64_t>(item) * a.n_kv + hk;
         const int seen = atomicAdd(counter, 1);
         if (seen == active - 1) *counter = 0;
-        *shared_flag = seen == active - 1;
+        stand[0] = seen == active - 1;
     }
     __syncthreads();
-    if (!*shared_flag) return;
+    if (!stand[0]) return;
     __threadfence();
-    for (int i = threadIdx.x; i < rows * D; i += kWarps * 32) {
-        const int row = i / D, ch = i % D;
-        float m = kNoMax;
-        for (int w = 0; w < active; ++w) m = fmaxf(m, __ldcg(mine + static_cast<int64_t>(w) * Sh::part_floats + RT * D + 2 * row));
-        float v = 0.0f, l = 0.0f;
-#pragma unroll 4
-        for (int w = 0; w < active; ++w) {
-            const float *from = mine + static_cast<int64_t>(w) * Sh::part_floats;
-            const float f = ex2(__ldcg(from + RT * D + 2 * row) - m);
-            v = fmaf(f, __ldcg(from + i), v);
-            l = fmaf(f, __ldcg(from + RT * D + 2 * row + 1), l);
-        }
-        const int64_t to = (r0 + (first + row) / a.rep) * a.ldo +
-                           (static_cast<int64_t>(hk) * a.rep + (first + row) % a.rep) * D + ch;
-        store_float_as(a.out, to, a.out_type, l == 0.0f ? 0.0f : v / l);
-    }
+    join_parts<RT, D>(a, c_first, active, rows, reinterpret_cast<float *>(smem + Sh::frag_bytes),
+                      kWarps * Sh::warp_bytes / 4, out_at);
 }
 
 template <int G, int PIECES, int NT>
@@ -613,7 +736,6 @@ cudaError_t launch_rows(const AttnArgs &a, int64_t grid, cudaStream_t st)
 {
     const auto kern = rows_kernel<G, PIECES, NT>;
     constexpr int smem = Shape<G, PIECES, NT>::smem;
-    static_assert(smem <= 227 * 1024, "shared memory of a block");
     // once a device; two threads that find it undone both do it
     static std::atomic<uint64_t> done{0};
     int dev = 0;
