@@ -3,10 +3,14 @@
 // tensor cores.
 //
 // A thread block takes 256 rows (queries x grouped heads) of one key/value
-// head as two tiles of 128 and walks the keys in tiles of 128:
-//   S = Q K'^T        M 128, N 128, K = D     (Q, K' in shared memory)
-//   O += P V'         M 128, N = D, K = 128   (P in tensor memory, V' in shared memory)
-// with S, P and O in tensor memory (P takes the place of the S it came from).
+// head as two tiles of 128 and walks the keys in tiles of 64:
+//   S = Q K'^T        M 128, N 64, K = D
+//   O += P V'         M 128, N = D, K = 64
+// with K' and V' in shared memory and S, P and O in tensor memory, and Q too
+// but for the second tile's at 128 channels, where tensor memory is full.
+// (With Q in shared memory and 128 keys a tile the products' operands alone
+// filled the shared memory's 128 bytes a clock.)  P has columns of its own, so
+// the next scores are formed while these are turned into P.
 // K' and V' are the cache's values in fp16, formed once for both row tiles
 // straight in the operands' 128-byte-swizzled layouts.
 //
@@ -18,9 +22,9 @@
 // be passed, so most tiles need neither a row maximum nor a rescaling of O.
 //
 // Warps: 0-3 and 4-7 softmax of the two row tiles (a thread is a row), 8-13
-// the dequantisation (each takes every sixth 16-token block), 14 issues the
-// MMAs, 15 copies raw blocks into a ring.  While one row tile's softmax runs,
-// the other's products do.
+// the dequantisation (each takes every sixth 16-token block and copies its own
+// raw blocks, two ahead), 14 and 15 issue the MMAs, one for each row tile, so
+// that the waits of one are covered by the products of the other.
 #include <atomic>
 
 #include "qk_attn.cuh"
@@ -32,14 +36,15 @@ using namespace attn;
 namespace {
 
 // Sixteen warps, so that a thread may have 128 registers.
-constexpr int kSoftmaxWarps = 8, kDequantWarps = 6, kMmaWarp = 14, kLoadWarp = 15;
+constexpr int kSoftmaxWarps = 8, kDequantWarps = 6, kMmaWarp = 14;
 constexpr int kThreads = 16 * 32;
-constexpr int kTile = 128;                 // keys a tile
+constexpr int kTile = 64;                  // keys a tile
+constexpr int kStages = 4;                 // tiles of K' and of V'
+constexpr int kMetas = 8;                  // tiles whose exponents are kept: more than stages and tiles at work
 constexpr int kTileBlocks = kTile / kBlockTokens;
-// Raw blocks in flight: a multiple of the dequantising warps, so that a slot is always the same warp's and its phases
-// are waited for one by one (a warp that met a slot only every second time could take an old phase for its own).
-constexpr int kSlots = 2 * kDequantWarps;
-constexpr float kLimit = 14.0f;            // log2 of the largest P
+constexpr int kSlots = 2 * kDequantWarps;  // raw blocks in flight: two a dequantising warp, its own
+constexpr float kMost = 16384.0f;          // the largest P, and sum of 16
+constexpr float kTwo24 = 16777216.0f;
 constexpr float kFresh = 4.0f;             // and of a row's largest when its reference moves
 
 template <int G>
@@ -47,21 +52,25 @@ struct ChunkShape {
     static constexpr int D = 32 * G;
     static constexpr int kblocks = (D + 63) / 64;                    // 64-column blocks of a K-major operand row
     static constexpr int block_bytes = 18 * D;
-    static constexpr int q_bytes = kblocks * 128 * 128;              // one row tile of Q, one tile of K'
-    static constexpr int v_bytes = 2 * D * 128;                      // V' transposed: D rows of 128 keys
-    static constexpr int q_at = 0;
-    static constexpr int k_at = q_at + 2 * q_bytes;
-    static constexpr int v_at = k_at + 2 * q_bytes;
-    static constexpr int raw_at = v_at + 2 * v_bytes;
+    static constexpr int k_bytes = kblocks * kTile * 128;            // one tile of K'
+    static constexpr int v_bytes = D * 128;                          // and of V' transposed: D rows of 64 keys
+    static constexpr int k_at = 0;
+    static constexpr int v_at = k_at + kStages * k_bytes;
+    static constexpr bool q2_in_smem = D > 96;                       // Q of the second row tile
+    static constexpr int q2_at = v_at + kStages * v_bytes;
+    static constexpr int raw_at = q2_at + (q2_in_smem ? kblocks * 128 * 128 : 0);
     static constexpr int scale_at = raw_at + kSlots * block_bytes;   // the dequantising warps' scaled scales
-    static constexpr int scale_bytes = 2 * 16 * G * 2;
+    static constexpr int scale_bytes = (8 + 6) * 16 * G;             // keys 3 of 4 fp16 a scale, values 3 rows
     static constexpr int meta_at = scale_at + kDequantWarps * scale_bytes;       // [tile % 4][block] (2^kk, kt, 2^-kt, 0)
-    static constexpr int bars_at = meta_at + 4 * kTileBlocks * 16;
-    static constexpr int flags_at = bars_at + (2 * kSlots + 14) * 8;
+    static constexpr int bars_at = meta_at + kMetas * kTileBlocks * 16;
+    static constexpr int flags_at = bars_at + (kSlots + 4 * kStages + 8) * 8;
     static constexpr int bytes = flags_at + 16;
-    static_assert(kSlots % kDequantWarps == 0 && kDequantWarps <= kTileBlocks, "every warp meets every phase");
+    // a warp meets every second tile or more often: no phase of a barrier that it waits for can be taken for an older
+    static_assert(kDequantWarps <= 2 * kTileBlocks && kStages >= 2, "phases");
     static constexpr int smem = bytes + 1008;                        // the base is brought to 1024 bytes
-    static constexpr int o_col = 256;                                // tensor memory: S 0..255, O after
+    // tensor memory: S 0..127, P 128..191, Q of the first tile 192..255, O after, Q of the second from 448
+    static constexpr int p_col = 128, q_col = 192, o_col = 256, q2_col = 448;
+    static_assert(q2_in_smem || (o_col + 2 * D <= q2_col && q2_col + D / 2 <= 512), "tensor memory");
 };
 
 // One operand row's 16-byte chunk (8 elements from element 8 * c) in 128-byte swizzle.
@@ -96,11 +105,39 @@ __device__ __forceinline__ void lds128(uint32_t (&w)[4], uint32_t addr)
                  : "r"(addr));
 }
 
-__device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b)
+// a * b + c on fp16 pairs, rounded once, subnormals kept.
+__device__ __forceinline__ uint32_t fma_half2(uint32_t a, uint32_t b, uint32_t c)
 {
     uint32_t r;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
     return r;
+}
+
+__device__ __forceinline__ void lds64(uint32_t &a, uint32_t &b, uint32_t addr)
+{
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(a), "=r"(b) : "r"(addr));
+}
+
+// N neighbouring words by the widest load that N allows.
+template <int N>
+__device__ __forceinline__ void lds_words(uint32_t (&w)[N], uint32_t addr)
+{
+    if constexpr (N == 4) {
+        lds128(w, addr);
+    } else if constexpr (N == 2) {
+        lds64(w[0], w[1], addr);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) w[i] = lds32(addr + 4 * i);
+    }
+}
+
+// One thread of the warp, the same each time.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
 // A wait whose outcome the whole warp shares (a limit may run out for one lane and not another).
@@ -113,14 +150,14 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_
 struct Bars {
     uint32_t at;
     __device__ __forceinline__ uint32_t rfull(int i) const { return at + 8 * i; }
-    __device__ __forceinline__ uint32_t rempty(int i) const { return at + 8 * (kSlots + i); }
-    __device__ __forceinline__ uint32_t kfull(int i) const { return at + 8 * (2 * kSlots + i); }
-    __device__ __forceinline__ uint32_t kempty(int i) const { return at + 8 * (2 * kSlots + 2 + i); }
-    __device__ __forceinline__ uint32_t vfull(int i) const { return at + 8 * (2 * kSlots + 4 + i); }
-    __device__ __forceinline__ uint32_t vempty(int i) const { return at + 8 * (2 * kSlots + 6 + i); }
-    __device__ __forceinline__ uint32_t sfull(int i) const { return at + 8 * (2 * kSlots + 8 + i); }
-    __device__ __forceinline__ uint32_t pfull(int i) const { return at + 8 * (2 * kSlots + 10 + i); }
-    __device__ __forceinline__ uint32_t odone(int i) const { return at + 8 * (2 * kSlots + 12 + i); }
+    __device__ __forceinline__ uint32_t kfull(int i) const { return at + 8 * (kSlots + i); }
+    __device__ __forceinline__ uint32_t kempty(int i) const { return at + 8 * (kSlots + kStages + i); }
+    __device__ __forceinline__ uint32_t vfull(int i) const { return at + 8 * (kSlots + 2 * kStages + i); }
+    __device__ __forceinline__ uint32_t vempty(int i) const { return at + 8 * (kSlots + 3 * kStages + i); }
+    __device__ __forceinline__ uint32_t sfull(int x) const { return at + 8 * (kSlots + 4 * kStages + x); }
+    __device__ __forceinline__ uint32_t sread(int x) const { return at + 8 * (kSlots + 4 * kStages + 2 + x); }
+    __device__ __forceinline__ uint32_t pfull(int x) const { return at + 8 * (kSlots + 4 * kStages + 4 + x); }
+    __device__ __forceinline__ uint32_t odone(int x) const { return at + 8 * (kSlots + 4 * kStages + 6 + x); }
 };
 
 // Splits of a head that have blocks, at least one: each takes the same number.
@@ -143,68 +180,85 @@ struct Work {
     int two;                     // both row tiles hold rows
 };
 
-// One row's state and its softmax over 32 columns of a score tile.
+// One row's state.
 struct Row {
     float m, l, to_log2;
     int lo, hi;
 };
 
+// P of a row's 64 scores v, as fp16 pairs, and the sums of each block's 16.
+template <bool MASK>
+__device__ __forceinline__ void exponents64(const Row &R, const uint32_t (&v)[2][32], const float (&f)[4], const float (&kt)[4],
+                                            int key0, uint32_t (&p)[32], float (&sum)[4])
+{
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+        const float at = kt[b] - R.m;
+        const uint64_t f2 = pack2f(f[b], f[b]), at2 = pack2f(at, at);
+        uint64_t total = 0;      // two zeros
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int c = 16 * b + 2 * i;
+            float2 z = unpack2f(fma_f32x2(pack2(v[c >> 5][c & 31], v[c >> 5][(c & 31) + 1]), f2, at2));
+            if (MASK) {
+                if (key0 + c < R.lo || key0 + c >= R.hi) z.x = -INFINITY;
+                if (key0 + c + 1 < R.lo || key0 + c + 1 >= R.hi) z.y = -INFINITY;
+            }
+            z.x = ex2(z.x), z.y = ex2(z.y);
+            total = add_f32x2(total, pack2f(z.x, z.y));
+            p[8 * b + i] = pack_half(z.x, z.y);
+        }
+        const float2 t = unpack2f(total);
+        sum[b] = t.x + t.y;
+    }
+}
+
+// A row's 64 scores of one key tile to probabilities.  Returns false if the
+// wait for the last tile's products (which read P and form O) ran out.
 template <int G, bool MASK>
-__device__ __forceinline__ void softmax32(Row &R, uint32_t s_addr, uint32_t o_addr, uint32_t meta, int chunk, int key0,
-                                          bool has_o)
+__device__ __forceinline__ bool softmax_tile(Row &R, uint32_t s_addr, uint32_t p_addr, uint32_t o_addr, uint32_t meta,
+                                             int key0, uint32_t sread, uint32_t odone, int tile, uint64_t wait_ns, int lane)
 {
     constexpr int D = 32 * G;
-    uint32_t v[32];
-    tmem_ld_32x32b_x32(s_addr + 32 * chunk, v);
-    float f[2], kt[2], inv[2];
+    uint32_t v[2][32];
+    tmem_ld_32x32b_x32(s_addr, v[0]);
+    tmem_ld_32x32b_x32(s_addr + 32, v[1]);
+    float f[4], kt[4], inv[4];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int b = 0; b < 4; ++b) {
         uint32_t w[4];
-        lds128(w, meta + 16 * (2 * chunk + h));
-        f[h] = R.to_log2 * __uint_as_float(w[0]);
-        kt[h] = __uint_as_float(w[1]);
-        inv[h] = __uint_as_float(w[2]);
+        lds128(w, meta + 16 * b);
+        f[b] = R.to_log2 * __uint_as_float(w[0]);
+        kt[b] = __uint_as_float(w[1]);
+        inv[b] = __uint_as_float(w[2]);
     }
     tmem_ld_wait();
-    float big = kNoMax;
-    const float base0 = kt[0] - R.m, base1 = kt[1] - R.m;
-    float z[32];
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        z[i] = fmaf(__uint_as_float(v[i]), f[i >> 4], i < 16 ? base0 : base1);
-        if (MASK && (key0 + i < R.lo || key0 + i >= R.hi)) z[i] = -INFINITY;
-        big = fmaxf(big, z[i]);
-    }
-    if (__any_sync(0xFFFFFFFFu, big > kLimit)) {
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(sread);          // the next scores may come
+    uint32_t p[32];
+    float sum[4];
+    exponents64<MASK>(R, v, f, kt, key0, p, sum);
+    if (tile > 0 && !warp_wait(odone, (tile - 1) & 1, wait_ns)) return false;
+    tc_fence_after();
+    float most = fmaxf(fmaxf(sum[0], sum[1]), fmaxf(sum[2], sum[3]));
+    if (__any_sync(0xFFFFFFFFu, most > kMost)) {
         // rows past the limit take a new reference; what they have so far is scaled to it
         float factor = 1.0f;
-        if (big > kLimit) {
+        if (most > kMost) {
             float top = kNoMax;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const float y = fmaf(__uint_as_float(v[i]), f[i >> 4], kt[i >> 4]);
+            for (int i = 0; i < 64; ++i) {
+                const float y = fmaf(__uint_as_float(v[i >> 5][i & 31]), f[i >> 4], kt[i >> 4]);
                 if (!MASK || (key0 + i >= R.lo && key0 + i < R.hi)) top = fmaxf(top, y);
             }
             const float m = ceilf(top) - kFresh;
             factor = ex2(R.m - m);
             R.m = m;
             R.l *= factor;
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                z[i] = fmaf(__uint_as_float(v[i]), f[i >> 4], kt[i >> 4] - m);
-                if (MASK && (key0 + i < R.lo || key0 + i >= R.hi)) z[i] = -INFINITY;
-            }
         }
-        const uint32_t f2 = pack_half(factor, factor);
-        for (int c = 0; c < chunk; ++c) {
-            uint32_t w[16];
-            tmem_ld_32x32b_x16(s_addr + 16 * c, w);
-            tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 16; ++i) w[i] = mul_half2(w[i], f2);
-            tmem_st_32x32b_x16(s_addr + 16 * c, w);
-        }
-        if (has_o) {
+        exponents64<MASK>(R, v, f, kt, key0, p, sum);
+        if (tile > 0) {
             for (int c = 0; c < D / 16; ++c) {
                 uint32_t w[16];
                 tmem_ld_32x32b_x16(o_addr + 16 * c, w);
@@ -214,18 +268,13 @@ __device__ __forceinline__ void softmax32(Row &R, uint32_t s_addr, uint32_t o_ad
                 tmem_st_32x32b_x16(o_addr + 16 * c, w);
             }
         }
-        tmem_st_wait();
     }
-    uint32_t p[16];
-    float sum[2] = {0.0f, 0.0f};
 #pragma unroll
-    for (int i = 0; i < 32; i += 2) {
-        const float x = ex2(z[i]), y = ex2(z[i + 1]);
-        sum[i >> 4] += x + y;
-        p[i >> 1] = pack_half(x, y);
-    }
-    R.l = fmaf(sum[0], inv[0], fmaf(sum[1], inv[1], R.l));
-    tmem_st_32x32b_x16(s_addr + 16 * chunk, p);
+    for (int b = 0; b < 4; ++b) R.l = fmaf(sum[b], inv[b], R.l);
+    tmem_st_32x32b_x32(p_addr, p);
+    tmem_st_wait();
+    tc_fence_before();
+    return true;
 }
 
 template <int G>
@@ -272,11 +321,14 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttnArgs a)
     const int64_t base = w.blk0 * kBlockTokens;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kSlots; ++i) mbar_init(bars.rfull(i), 1), mbar_init(bars.rempty(i), 1);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(bars.kfull(i), 8), mbar_init(bars.kempty(i), 1);
-            mbar_init(bars.vfull(i), 8), mbar_init(bars.vempty(i), 1);
-            mbar_init(bars.sfull(i), 1), mbar_init(bars.pfull(i), 4), mbar_init(bars.odone(i), 1);
+        for (int i = 0; i < kSlots; ++i) mbar_init(bars.rfull(i), 1);
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(bars.kfull(i), kTileBlocks), mbar_init(bars.kempty(i), 1 + w.two);
+            mbar_init(bars.vfull(i), kTileBlocks), mbar_init(bars.vempty(i), 1 + w.two);
+        }
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(bars.sfull(x), 1), mbar_init(bars.sread(x), 4);
+            mbar_init(bars.pfull(x), 4), mbar_init(bars.odone(x), 1);
         }
         flags[1] = flags[2] = 0;
         fence_barrier_init();
@@ -286,11 +338,17 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttnArgs a)
         tmem_relinquish_1();
     }
 
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = __reduce_or_sync(0xFFFFFFFFu, flags[0]);      // in a uniform register
+
     // softmax threads: their row of Q, scaled by a power of two to [2^10, 2^11), channels 0 4 1 5 2 6 3 7 of each
-    // eight (the order in which masks take a word's nibbles apart)
+    // eight (the order in which masks take a word's nibbles apart), to tensor memory
     Row R{kNoMax, 0.0f, 1.2e-38f, 0, INT32_MAX};
     const int half = warp >> 2, my_row = threadIdx.x & 127;
-    const bool softmax_warp = warp < 8;
+    const bool softmax_warp = warp < kSoftmaxWarps;
+    const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;       // 32 lanes a warp, lane in bits 16..
     int64_t row_token = 0, row_head = 0;
     const bool row_in = softmax_warp && half * 128 + my_row < w.rows;
     if (softmax_warp && (half == 0 || w.two)) {
@@ -312,113 +370,129 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttnArgs a)
             R.lo = clamp_key(a.window > 0 ? pos - a.window + 1 - base : -1);
             R.hi = clamp_key(pos + 1 - base);
         }
-        for (int c = 0; c < D / 8; ++c) {
-            float x[8];
+        for (int c = 0; c < D / 32; ++c) {
+            uint32_t q[16];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = row_in ? load_as_float(a.q, at + 8 * c + j, a.q_type) * up : 0.0f;
-            sts128(sb + Sh::q_at + half * Sh::q_bytes + operand_chunk(my_row, c, 128), pack_half(x[0], x[4]),
-                   pack_half(x[1], x[5]), pack_half(x[2], x[6]), pack_half(x[3], x[7]));
+            for (int k = 0; k < 4; ++k) {
+                float x[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] = row_in ? load_as_float(a.q, at + 32 * c + 8 * k + j, a.q_type) * up : 0.0f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) q[4 * k + j] = pack_half(x[j], x[j + 4]);
+            }
+            if (half == 0) {
+                tmem_st_32x32b_x16(tmem + lanes + Sh::q_col + 16 * c, q);
+            } else if constexpr (!Sh::q2_in_smem) {
+                tmem_st_32x32b_x16(tmem + lanes + Sh::q2_col + 16 * c, q);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    sts128(sb + Sh::q2_at + operand_chunk(my_row, 4 * c + k, 128), q[4 * k], q[4 * k + 1], q[4 * k + 2], q[4 * k + 3]);
+            }
         }
+        tmem_st_wait();
         fence_proxy_async_smem();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = flags[0];
     bool dead = false, poison = false;
 
-    if (warp == kLoadWarp) {
-        // ------------------------------------------------ raw blocks into the ring
-        const uint64_t policy = l2_evict_first_policy();
-        const uint8_t *addr = nullptr;
-        for (int j = 0; j < w.nblk && !dead; ++j) {
-            if ((j & 31) == 0) {           // addresses of the next 32 blocks, one a lane
-                addr = a.pages;
-                if (j + lane < w.nblk) {
-                    const int64_t blk = w.blk0 + j + lane, pg = blk / a.page_blocks;
-                    const int32_t page = a.page_table[w.b * a.ld_pages + pg];
-                    if (page < 0 || page >= a.n_pages) {
-                        poison = true;
-                        record_error(a.err, kErrBadIndex);
-                    } else {
-                        addr += ((static_cast<int64_t>(page) * a.n_kv + w.hk) * a.page_blocks +
-                                 (blk - pg * a.page_blocks)) * static_cast<int64_t>(Sh::block_bytes);
-                    }
-                }
-            }
-            const uint64_t from = __shfl_sync(0xFFFFFFFFu, reinterpret_cast<uint64_t>(addr), j & 31);
-            const int slot = j % kSlots;
-            if (j >= kSlots && !warp_wait(bars.rempty(slot), ((j / kSlots) - 1) & 1, a.wait_ns)) dead = true;
-            if (dead || (j == a.skip_block && blockIdx.x == 0)) continue;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(bars.rfull(slot), Sh::block_bytes);
-                bulk_g2s(sb + Sh::raw_at + slot * Sh::block_bytes, reinterpret_cast<const void *>(from), Sh::block_bytes,
-                         bars.rfull(slot), policy);
-            }
-            __syncwarp();
-        }
-        // a copy in flight when a wait ran out is waited for before the block ends
-        if (dead)
-            for (int i = 0; i < kSlots; ++i) {
-                mbar_wait(bars.rfull(i), 0, a.wait_ns / 16 + 1);
-                mbar_wait(bars.rfull(i), 1, a.wait_ns / 16 + 1);
-            }
-        poison = __any_sync(0xFFFFFFFFu, poison);
-        if (poison && lane == 0) flags[1] = 1;
-    } else if (warp == kMmaWarp) {
-        // ------------------------------------------------ the MMAs, one thread
-        if (lane == 0 && w.ntiles > 0) {
+    if (warp >= kMmaWarp) {
+        // ------------------------------------------------ the MMAs of row tile x, by one elected thread; the warp waits
+        // together and what the instructions take is the warp's, so that it stays in uniform registers
+        const int x = warp - kMmaWarp;
+        if (w.ntiles > 0 && x <= w.two) {
             constexpr uint32_t idesc_s = idesc_f16_f32(128, kTile), idesc_o = idesc_f16_f32(128, D);
-            const int qts = w.two ? 2 : 1;
-            auto scores = [&](int x, int i) {
-                const uint64_t q0 = smem_desc_sw128_kmajor(sb + Sh::q_at + x * Sh::q_bytes);
-                const uint64_t k0 = smem_desc_sw128_kmajor(sb + Sh::k_at + (i & 1) * Sh::q_bytes);
+            const uint32_t s_col = tmem + 64 * x, p_col = tmem + Sh::p_col + 32 * x, o_col = tmem + Sh::o_col + D * x;
+            auto scores = [&](int stage) {
+                const uint64_t k0 = smem_desc_sw128_kmajor(sb + Sh::k_at + stage * Sh::k_bytes);
+                if (elect_one()) {
+                    if (Sh::q2_in_smem && x == 1) {
+                        const uint64_t q0 = smem_desc_sw128_kmajor(sb + Sh::q2_at);
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint64_t off = (k >> 2) * (128 * 128 / 16) + (k & 3) * 2;
-                    tc_mma_f16(tmem + 128 * x, q0 + off, k0 + off, idesc_s, k > 0);
+                        for (int k = 0; k < D / 16; ++k)
+                            tc_mma_f16(s_col, q0 + (k >> 2) * (128 * 128 / 16) + (k & 3) * 2,
+                                       k0 + (k >> 2) * (kTile * 128 / 16) + (k & 3) * 2, idesc_s, k > 0);
+                    } else {
+                        const uint32_t q = tmem + (x ? Sh::q2_col : Sh::q_col);
+#pragma unroll
+                        for (int k = 0; k < D / 16; ++k)
+                            tc_mma_f16_tmem_a(s_col, q + 8 * k, k0 + (k >> 2) * (kTile * 128 / 16) + (k & 3) * 2, idesc_s, k > 0);
+                    }
+                    tc_commit_1(bars.sfull(x));
+                    tc_commit_1(bars.kempty(stage));
                 }
-                tc_commit_1(bars.sfull(x));
-                if (x == qts - 1) tc_commit_1(bars.kempty(i & 1));
+                __syncwarp();
             };
-            dead = !mbar_wait(bars.kfull(0), 0, a.wait_ns);
+            dead = !warp_wait(bars.kfull(0), 0, a.wait_ns);
             tc_fence_after();
-            for (int x = 0; x < qts && !dead; ++x) scores(x, 0);
+            if (!dead) scores(0);
             for (int i = 0; i < w.ntiles && !dead; ++i) {
-                const bool more = i + 1 < w.ntiles;
-                for (int x = 0; x < qts && !dead; ++x) {
-                    if (x == 0 && !mbar_wait(bars.vfull(i & 1), (i >> 1) & 1, a.wait_ns)) { dead = true; break; }
-                    if (!mbar_wait(bars.pfull(x), i & 1, a.wait_ns)) { dead = true; break; }
+                const int stage = i % kStages, next = (i + 1) % kStages;
+                if (i + 1 < w.ntiles) {         // the next scores, once these have been read
+                    if (!warp_wait(bars.kfull(next), ((i + 1) / kStages) & 1, a.wait_ns) ||
+                        !warp_wait(bars.sread(x), i & 1, a.wait_ns)) { dead = true; break; }
                     tc_fence_after();
-                    const uint64_t v0 = smem_desc_sw128_kmajor(sb + Sh::v_at + (i & 1) * Sh::v_bytes);
+                    scores(next);
+                }
+                if (!warp_wait(bars.vfull(stage), (i / kStages) & 1, a.wait_ns) || !warp_wait(bars.pfull(x), i & 1, a.wait_ns)) {
+                    dead = true;
+                    break;
+                }
+                tc_fence_after();
+                const uint64_t v0 = smem_desc_sw128_kmajor(sb + Sh::v_at + stage * Sh::v_bytes);
+                if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < kTile / 16; ++k)
-                        tc_mma_f16_tmem_a(tmem + Sh::o_col + D * x, tmem + 128 * x + 8 * k,
-                                          v0 + (k >> 2) * (D * 128 / 16) + (k & 3) * 2, idesc_o, i > 0 || k > 0);
+                        tc_mma_f16_tmem_a(o_col, p_col + 8 * k, v0 + 2 * k, idesc_o, i > 0 || k > 0);
                     tc_commit_1(bars.odone(x));
-                    if (x == qts - 1) tc_commit_1(bars.vempty(i & 1));
-                    if (more) {
-                        if (x == 0 && !mbar_wait(bars.kfull((i + 1) & 1), ((i + 1) >> 1) & 1, a.wait_ns)) { dead = true; break; }
-                        // the next scores take the place of these probabilities
-                        if (!mbar_wait(bars.odone(x), i & 1, a.wait_ns)) { dead = true; break; }
-                        tc_fence_after();
-                        scores(x, i + 1);
-                    }
+                    tc_commit_1(bars.vempty(stage));
                 }
+                __syncwarp();
             }
         }
-        __syncwarp();
     } else if (warp >= kSoftmaxWarps) {
         // ------------------------------------------------ dequantisation: block j of the split, 16 tokens
         const int r8 = lane >> 2, c = lane & 3;
         const uint32_t scales = sb + Sh::scale_at + (warp - kSoftmaxWarps) * Sh::scale_bytes;      // keys [token][G], values [G][token]
         const int all_lo = clamp_key(w.span.key_lo - base), all_hi = clamp_key(w.span.key_hi - base);
-        for (int j = warp - kSoftmaxWarps; j < w.ntiles * kTileBlocks; j += kDequantWarps) {
+        // this warp's blocks are number me, me + 6, ..; its n-th goes to slot me + 6 (n % 2).  A lane holds the address
+        // of one of the next 32
+        const int me = warp - kSoftmaxWarps, mine = w.nblk > me ? (w.nblk - me + kDequantWarps - 1) / kDequantWarps : 0;
+        const uint64_t policy = l2_evict_first_policy();
+        const uint8_t *addr = a.pages;
+        auto copy = [&](int n) {
+            if (n >= mine) return;
+            if ((n & 31) == 0) {
+                addr = a.pages;
+                if (n + lane < mine) {
+                    const int64_t blk = w.blk0 + me + kDequantWarps * (n + lane), pg = blk / a.page_blocks;
+                    const int32_t page = a.page_table[w.b * a.ld_pages + pg];
+                    if (page < 0 || page >= a.n_pages) {
+                        poison = true;
+                        record_error(a.err, kErrBadIndex);
+                    } else {
+                        addr += ((static_cast<int64_t>(page) * a.n_kv + w.hk) * a.page_blocks + (blk - pg * a.page_blocks)) *
+                                static_cast<int64_t>(Sh::block_bytes);
+                    }
+                }
+            }
+            if (lane == (n & 31) && !(me + kDequantWarps * n == a.skip_block && blockIdx.x == 0)) {
+                const int slot = me + kDequantWarps * (n & 1);
+                mbar_arrive_expect_tx(bars.rfull(slot), Sh::block_bytes);
+                bulk_g2s(sb + Sh::raw_at + slot * Sh::block_bytes, addr, Sh::block_bytes, bars.rfull(slot), policy);
+            }
+        };
+        copy(0);
+        copy(1);
+        int n = 0;
+        for (int j = me; j < w.ntiles * kTileBlocks; j += kDequantWarps, ++n) {
             const int i = j / kTileBlocks, bi = j % kTileBlocks;      // key tile, block of it
             const bool have = j < w.nblk;
-            const int slot = j % kSlots;
+            const int slot = me + kDequantWarps * (n & 1);
             const uint32_t raw = sb + Sh::raw_at + slot * Sh::block_bytes;
-            if (have && !warp_wait(bars.rfull(slot), (j / kSlots) & 1, a.wait_ns)) { dead = true; break; }
+            if (have && !warp_wait(bars.rfull(slot), (n >> 1) & 1, a.wait_ns)) { dead = true; break; }
             // scales: the block's exponents, and the scales less them as fp16
             uint32_t dk[(16 * G + 31) / 32], dv[(16 * G + 31) / 32], top_k = 0, top_v = 0, odd = 0;
 #pragma unroll
@@ -440,27 +514,35 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttnArgs a)
             // largest scale in [2^e, 2^(e+1)); a subnormal or 0 counts as 2^-15
             const int ek = top_k >= 0x0400u ? static_cast<int>(top_k >> 10) - 15 : -15;
             const int ev = top_v >= 0x0400u ? static_cast<int>(top_v >> 10) - 15 : -15;
-            const float down_k = __uint_as_float(static_cast<uint32_t>(127 - ek) << 23);
-            const float down_v = __uint_as_float(static_cast<uint32_t>(127 - ev) << 23);
+            const float down_k = __uint_as_float(static_cast<uint32_t>(127 - ek - 9) << 23);
+            const float down_v = __uint_as_float(static_cast<uint32_t>(127 - ev - 9) << 23);
+            // A nibble under a mask is the fp16 subnormal n 2^-24 (or 16 n 2^-24), so (n - 8) s is one multiply-add,
+            // rounded once: n 2^-24 * (s 2^24) - 8 s.  For s 2^24 to be an fp16, s is the scale over 2^(e + 9): below
+            // 2^-8, its products of at least 2^-14 normal for scales down to 1/64 of the block's largest.
 #pragma unroll
             for (int k = 0; k < (16 * G + 31) / 32; ++k) {
                 const int at = 32 * k + lane, t = at / G, g = at - t * G;
                 if (at < 16 * G) {
-                    const __half hk = __float2half_rn(half_bits_to_float(dk[k]) * down_k);
+                    const float sk = half_bits_to_float(dk[k]) * down_k;
                     // a value scale that is not finite: the key's scores become NaN instead (below), and with them
                     // the rows that see it
                     const bool fine = (dv[k] & 0x7C00u) != 0x7C00u;
-                    const __half hv = __float2half_rn(fine ? half_bits_to_float(dv[k]) * down_v : 0.0f);
-                    *reinterpret_cast<__half *>(sm + (scales - sb) + 2 * at) = hk;
-                    *reinterpret_cast<__half *>(sm + (scales - sb) + 32 * G + 2 * (16 * g + t)) = hv;
+                    const float sv = fine ? half_bits_to_float(dv[k]) * down_v : 0.0f;
+                    uint8_t *keys = sm + (scales - sb) + 8 * at;
+                    *reinterpret_cast<uint2 *>(keys) =
+                        make_uint2(pack_half(sk * kTwo24, sk * (kTwo24 / 16.0f)), pack_half(sk * -8.0f, 0.0f));
+                    __half *vals = reinterpret_cast<__half *>(sm + (scales - sb) + 128 * G) + 16 * g + t;
+                    vals[0] = __float2half_rn(sv * kTwo24);
+                    vals[16 * G] = __float2half_rn(sv * (kTwo24 / 16.0f));
+                    vals[32 * G] = __float2half_rn(sv * -8.0f);
                 }
             }
             if (lane == 0) {
                 float4 m;
-                m.x = __uint_as_float(static_cast<uint32_t>(127 + ek) << 23);
-                m.y = static_cast<float>(ev);
+                m.x = __uint_as_float(static_cast<uint32_t>(127 + ek + 9) << 23);
+                m.y = static_cast<float>(ev + 9);
                 m.z = down_v, m.w = 0.0f;
-                *reinterpret_cast<float4 *>(sm + Sh::meta_at + ((i & 3) * kTileBlocks + bi) * 16) = m;
+                *reinterpret_cast<float4 *>(sm + Sh::meta_at + (i % kMetas * kTileBlocks + bi) * 16) = m;
             }
             __syncwarp();
             if (odd) {
@@ -468,67 +550,106 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttnArgs a)
                 for (int k = 0; k < (16 * G + 31) / 32; ++k) {
                     const int at = 32 * k + lane, t = at / G;
                     if (at < 16 * G && (dv[k] & 0x7C00u) == 0x7C00u)
-                        *reinterpret_cast<uint16_t *>(sm + (scales - sb) + 2 * (t * G)) = 0x7FFFu;
+                        *reinterpret_cast<uint32_t *>(sm + (scales - sb) + 8 * (t * G)) = 0x7FFF7FFFu;
                 }
                 __syncwarp();
             }
             // keys: lane (r, c) has token 4(r/2) + 2h + r%2, channels 32g + 8c..8c+7 a word
-            if (i >= 2 && !warp_wait(bars.kempty(i & 1), ((i >> 1) - 1) & 1, a.wait_ns)) { dead = true; break; }
-            const uint32_t kb = sb + Sh::k_at + (i & 1) * Sh::q_bytes;
+            if (i >= kStages && !warp_wait(bars.kempty(i % kStages), (i / kStages - 1) & 1, a.wait_ns)) { dead = true; break; }
+            // (odd r take the groups in another order: a quarter of the warp then writes all eight 16-byte columns)
+            const uint32_t kb = sb + Sh::k_at + i % kStages * Sh::k_bytes;
+            const int swap = G % 2 == 0 ? r8 & 1 : 0;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int t = 4 * (r8 >> 1) + 2 * h + (r8 & 1);
+                uint32_t words[G];
+                if (have) {
+                    lds_words<G>(words, raw + h * 128 * G + lane * 4 * G);
+                } else {
+#pragma unroll
+                    for (int g = 0; g < G; ++g) words[g] = 0x88888888u;
+                }
 #pragma unroll
                 for (int g = 0; g < G; ++g) {
-                    const uint32_t word = have ? lds32(raw + h * 128 * G + (lane * G + g) * 4) : 0x88888888u;
-                    const uint32_t s1 = lds16(scales + 2 * (t * G + g)), s2 = s1 | s1 << 16;
-                    sts128(kb + operand_chunk(bi * kBlockTokens + t, 4 * g + c, 128),
-                           mul_half2(signed_nibbles<0>(word), s2), mul_half2(signed_nibbles<1>(word), s2),
-                           mul_half2(signed_nibbles<0>(word >> 8), s2), mul_half2(signed_nibbles<1>(word >> 8), s2));
+                    const int mine = g ^ swap;
+                    const uint32_t word = G % 2 == 0 && swap ? words[g ^ (G % 2 == 0)] : words[g], high = word >> 8;
+                    uint32_t x, y;       // (s 2^24, s 2^20) and (-8 s, 0)
+                    lds64(x, y, scales + 8 * (t * G + mine));
+                    const uint32_t s0 = __byte_perm(x, x, 0x1010), s1 = __byte_perm(x, x, 0x3232), s8 = __byte_perm(y, y, 0x1010);
+                    sts128(kb + operand_chunk(bi * kBlockTokens + t, 4 * mine + c, kTile), fma_half2(word & 0x000F000Fu, s0, s8),
+                           fma_half2(word & 0x00F000F0u, s1, s8), fma_half2(high & 0x000F000Fu, s0, s8),
+                           fma_half2(high & 0x00F000F0u, s1, s8));
                 }
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bars.kfull(i & 1));
-            // values: an item is (g, r, half of the block's tokens): 4 words, channels 32g + 4r + j, 8 tokens a chunk
-            if (i >= 2 && !warp_wait(bars.vempty(i & 1), ((i >> 1) - 1) & 1, a.wait_ns)) { dead = true; break; }
-            const uint32_t vb = sb + Sh::v_at + (i & 1) * Sh::v_bytes;
+            if (lane == 0) mbar_arrive(bars.kfull(i % kStages));
+            // values: an item is (g, r, half of the block's tokens): 4 words, channels 32g + 4r + j, 8 tokens a chunk; the
+            // items of a quarter of the warp start at other j, so that they too write all eight columns
+            if (i >= kStages && !warp_wait(bars.vempty(i % kStages), (i / kStages - 1) & 1, a.wait_ns)) { dead = true; break; }
+            const uint32_t vb = sb + Sh::v_at + i % kStages * Sh::v_bytes;
+            constexpr int kItems = (16 * G + 31) / 32;
+            uint32_t words[kItems][4];      // tokens 8kp + 0,1 | 2,3 | 4,5 | 6,7
+            const int r = G == 3 ? (lane >> 1) & 7 : lane >> 2, kp = G == 3 ? lane & 1 : (lane >> 1) & 1;
+            const int turn = G == 3 ? (r >> 1) & 1 : lane & 1;
+            auto group_of = [&](int k) { return G == 3 ? 2 * k + (lane >> 4) : kItems * (lane & 1) + k; };
 #pragma unroll
-            for (int k = 0; k < (16 * G + 31) / 32; ++k) {
-                const int item = 32 * k + lane;
-                if (item < 16 * G) {
-                    const int g = item >> 4, r = (item >> 1) & 7, kp = item & 1;
-                    const uint32_t from = raw + 8 * D + ((r * 4 + 2 * kp) * G + g) * 4;
-                    uint32_t word[4];      // tokens 8kp + 0,1 | 2,3 | 4,5 | 6,7
-                    word[0] = have ? lds32(from) : 0x88888888u;
-                    word[1] = have ? lds32(from + 128 * G) : 0x88888888u;
-                    word[2] = have ? lds32(from + 4 * G) : 0x88888888u;
-                    word[3] = have ? lds32(from + 4 * G + 128 * G) : 0x88888888u;
-                    uint32_t s[4];
-                    lds128(s, scales + 32 * G + 2 * (16 * g + 8 * kp));
+            for (int k = 0; k < kItems; ++k)
 #pragma unroll
-                    for (int jj = 0; jj < 4; ++jj) {
-                        uint32_t x[4];
+                for (int e = 0; e < 4; ++e) words[k][e] = 0x88888888u;
+            if (have) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const uint32_t src = jj & 2 ? word[e] >> 8 : word[e];
-                            x[e] = mul_half2(jj & 1 ? signed_nibbles<1>(src) : signed_nibbles<0>(src), s[e]);
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t from = raw + 8 * D + (e & 1) * 128 * G + (r * 4 + 2 * kp + (e >> 1)) * 4 * G;
+                    if constexpr (G == 4) {
+                        lds64(words[0][e], words[kItems - 1][e], from + 4 * group_of(0));
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < kItems; ++k)
+                            if (group_of(k) < G) words[k][e] = lds32(from + 4 * group_of(k));
+                    }
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kItems; ++k) {
+                const int g = group_of(k);
+                if (G != 3 || g < G) {
+                    uint32_t s0[4], s1[4], s8[4];
+                    lds128(s0, scales + 128 * G + 2 * (16 * g + 8 * kp));
+                    lds128(s1, scales + 160 * G + 2 * (16 * g + 8 * kp));
+                    lds128(s8, scales + 192 * G + 2 * (16 * g + 8 * kp));
+#pragma unroll
+                    for (int half_j = 0; half_j < 2; ++half_j) {
+                        const int shift = 8 * (half_j ^ turn);
+                        uint32_t src[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) src[e] = words[k][e] >> shift;
+#pragma unroll
+                        for (int jj = 0; jj < 2; ++jj) {
+                            uint32_t x[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                x[e] = jj ? fma_half2(src[e] & 0x00F000F0u, s1[e], s8[e]) : fma_half2(src[e] & 0x000F000Fu, s0[e], s8[e]);
+                            sts128(vb + operand_chunk(32 * g + 4 * r + 2 * (half_j ^ turn) + jj, 2 * bi + kp, D), x[0], x[1], x[2],
+                                   x[3]);
                         }
-                        sts128(vb + operand_chunk(32 * g + 4 * r + jj, 2 * bi + kp, D), x[0], x[1], x[2], x[3]);
                     }
                 }
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(bars.vfull(i & 1));
-                if (have) mbar_arrive(bars.rempty(slot));
-            }
+            if (lane == 0) mbar_arrive(bars.vfull(i % kStages));
+            copy(n + 2);       // into the slot just read
         }
+        // copies still in flight when a wait ran out are waited for before the block ends
+        if (dead)
+            for (int k = n; k < n + 2 && k < mine; ++k)
+                mbar_wait(bars.rfull(me + kDequantWarps * (k & 1)), (k >> 1) & 1, a.wait_ns);
+        if (__any_sync(0xFFFFFFFFu, poison) && lane == 0) flags[1] = 1;
     } else if (half == 0 || w.two) {
         // ------------------------------------------------ softmax: a thread is a row
-        const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;          // 32 lanes a warp, lane in bits 16..
-        const uint32_t s_addr = tmem + lanes + 128 * half, o_addr = tmem + lanes + Sh::o_col + D * half;
+        const uint32_t s_addr = tmem + lanes + 64 * half, p_addr = tmem + lanes + Sh::p_col + 32 * half,
+                       o_addr = tmem + lanes + Sh::o_col + D * half;
         // keys that every row of this tile sees
         const int last = min(w.rows, half * 128 + 128) - 1;
         const int64_t p0 = w.seq.len - (w.seq.r1 - w.seq.r0) + (w.first + half * 128) / a.rep;
@@ -538,16 +659,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttnArgs a)
             if (!warp_wait(bars.sfull(half), i & 1, a.wait_ns)) { dead = true; break; }
             tc_fence_after();
             const int key0 = i * kTile;
-            const uint32_t meta = sb + Sh::meta_at + (i & 3) * kTileBlocks * 16;
-            if (key0 >= see_lo && key0 + kTile <= see_hi) {
-#pragma unroll 1
-                for (int c = 0; c < 4; ++c) softmax32<G, false>(R, s_addr, o_addr, meta, c, key0 + 32 * c, i > 0);
-            } else {
-#pragma unroll 1
-                for (int c = 0; c < 4; ++c) softmax32<G, true>(R, s_addr, o_addr, meta, c, key0 + 32 * c, i > 0);
+            const uint32_t meta = sb + Sh::meta_at + i % kMetas * kTileBlocks * 16;
+            const bool whole = key0 >= see_lo && key0 + kTile <= see_hi;
+            if (whole ? !softmax_tile<G, false>(R, s_addr, p_addr, o_addr, meta, key0, bars.sread(half), bars.odone(half), i, a.wait_ns, lane)
+                      : !softmax_tile<G, true>(R, s_addr, p_addr, o_addr, meta, key0, bars.sread(half), bars.odone(half), i, a.wait_ns, lane)) {
+                dead = true;
+                break;
             }
-            tmem_st_wait();
-            tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bars.pfull(half));
         }
@@ -563,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttnArgs a)
 
     // rows out, or to the workspace
     if (softmax_warp && (half == 0 || w.two)) {
-        const uint32_t o_addr = tmem + (static_cast<uint32_t>(warp & 3) << 21) + Sh::o_col + D * half;
+        const uint32_t o_addr = tmem + lanes + Sh::o_col + D * half;
         if (poison) R.l = __int_as_float(0x7FC00000);
         const float inv = R.l == 0.0f ? 0.0f : 1.0f / R.l;
         float *part = nullptr;
