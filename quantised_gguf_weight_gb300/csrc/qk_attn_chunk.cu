@@ -39,7 +39,7 @@ namespace {
 constexpr int kSoftmaxWarps = 8, kDequantWarps = 6, kMmaWarp = 14;
 constexpr int kThreads = 16 * 32;
 constexpr int kTile = 64;                  // keys a tile
-constexpr int kStages = 4;                 // tiles of K' and of V'
+constexpr int kStages = 3;                 // tiles of K' and of V'
 constexpr int kMetas = 8;                  // tiles whose exponents are kept: more than stages and tiles at work
 constexpr int kTileBlocks = kTile / kBlockTokens;
 constexpr int kSlots = 2 * kDequantWarps;  // raw blocks in flight: two a dequantising warp, its own
@@ -60,7 +60,7 @@ struct ChunkShape {
     static constexpr int q2_at = v_at + kStages * v_bytes;
     static constexpr int raw_at = q2_at + (q2_in_smem ? kblocks * 128 * 128 : 0);
     static constexpr int scale_at = raw_at + kSlots * block_bytes;   // the dequantising warps' scaled scales
-    static constexpr int scale_bytes = (8 + 6) * 16 * G;             // keys 3 of 4 fp16 a scale, values 3 rows
+    static constexpr int scale_bytes = (16 + 6) * 16 * G;            // 3 fp16 pairs of 4 a key scale, 3 rows of values'
     static constexpr int meta_at = scale_at + kDequantWarps * scale_bytes;       // [tile % 4][block] (2^kk, kt, 2^-kt, 0)
     static constexpr int bars_at = meta_at + kMetas * kTileBlocks * 16;
     static constexpr int flags_at = bars_at + (kSlots + 4 * kStages + 8) * 8;
@@ -82,6 +82,11 @@ __device__ __forceinline__ uint32_t operand_chunk(int row, int c, int rows)
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
 {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+__device__ __forceinline__ void sts32(uint32_t addr, uint32_t a)
+{
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(a) : "memory");
 }
 
 __device__ __forceinline__ uint32_t lds32(uint32_t addr)
@@ -454,7 +459,23 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttnArgs a)
         }
     } else if (warp >= kSoftmaxWarps) {
         // ------------------------------------------------ dequantisation: block j of the split, 16 tokens
-        const int r8 = lane >> 2, c = lane & 3;
+        const int r8 = lane >> 2, c = lane & 3, swap = G % 2 == 0 ? r8 & 1 : 0;
+        // scales: group sg of tokens st, st + 1
+        const int sg = lane % G, st = 2 * (lane / G);
+        const bool scale_lane = lane < 8 * G;
+        // keys: tokens key_token + 2h; where their 16-byte chunk of group 0 (1, with swap) lies among the block's rows
+        const int key_token = 4 * (r8 >> 1) + (r8 & 1);
+        uint32_t key_at[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            key_at[h] = key_token * 128 + (((4 * swap + c) ^ ((key_token + 2 * h) & 7)) << 4);
+        // values: an item is (g, r, half of the block's tokens): 4 words, channels 32g + 4r + j, 8 tokens a chunk; the items
+        // of a quarter of the warp start at other j, so that they too write all eight columns
+        constexpr int kItems = (16 * G + 31) / 32;
+        const int vr = G == 3 ? (lane >> 1) & 7 : lane >> 2, kp = G == 3 ? lane & 1 : (lane >> 1) & 1;
+        const int turn = G == 3 ? (vr >> 1) & 1 : lane & 1, shift = 8 * turn;
+        const uint32_t value_at = (4 * vr + 2 * turn) * 128 + (((4 * vr + 2 * turn) & 7) << 4);
+        auto group_of = [&](int k) { return G == 3 ? 2 * k + (lane >> 4) : kItems * (lane & 1) + k; };
         const uint32_t scales = sb + Sh::scale_at + (warp - kSoftmaxWarps) * Sh::scale_bytes;      // keys [token][G], values [G][token]
         const int all_lo = clamp_key(w.span.key_lo - base), all_hi = clamp_key(w.span.key_hi - base);
         // this warp's blocks are number me, me + 6, ..; its n-th goes to slot me + 6 (n % 2).  A lane holds the address
@@ -493,121 +514,91 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttnArgs a)
             const int slot = me + kDequantWarps * (n & 1);
             const uint32_t raw = sb + Sh::raw_at + slot * Sh::block_bytes;
             if (have && !warp_wait(bars.rfull(slot), (n >> 1) & 1, a.wait_ns)) { dead = true; break; }
-            // scales: the block's exponents, and the scales less them as fp16
-            uint32_t dk[(16 * G + 31) / 32], dv[(16 * G + 31) / 32], top_k = 0, top_v = 0, odd = 0;
+            // scales: a lane has those of one group g of two neighbouring tokens
+            uint32_t dk[2] = {0, 0}, dv[2] = {0, 0}, top_k = 0, top_v = 0, odd = 0;
+            const bool inner = have && j * kBlockTokens >= all_lo && (j + 1) * kBlockTokens <= all_hi;
+            if (scale_lane) {
 #pragma unroll
-            for (int k = 0; k < (16 * G + 31) / 32; ++k) {
-                const int at = 32 * k + lane, t = at / G;
-                dk[k] = dv[k] = 0;
-                const int key = j * kBlockTokens + t;
-                if (have && at < 16 * G && key >= all_lo && key < all_hi) {
-                    dk[k] = lds16(raw + 16 * D + 2 * at);
-                    dv[k] = lds16(raw + 17 * D + 2 * at);
-                    if ((dk[k] & 0x7C00u) != 0x7C00u) top_k = max(top_k, dk[k] & 0x7FFFu);
-                    if ((dv[k] & 0x7C00u) != 0x7C00u) top_v = max(top_v, dv[k] & 0x7FFFu);
-                    else odd = 1;
+                for (int e = 0; e < 2; ++e) {
+                    const int key = j * kBlockTokens + st + e;
+                    if (inner || (have && key >= all_lo && key < all_hi)) {
+                        dk[e] = lds16(raw + 16 * D + 2 * ((st + e) * G + sg));
+                        dv[e] = lds16(raw + 17 * D + 2 * ((st + e) * G + sg));
+                    }
+                    if ((dk[e] & 0x7C00u) != 0x7C00u) top_k = max(top_k, dk[e] & 0x7FFFu);
+                    if ((dv[e] & 0x7C00u) != 0x7C00u) top_v = max(top_v, dv[e] & 0x7FFFu);
+                    else odd |= 1 << e;
                 }
             }
             top_k = redux_max_u32(0xFFFFFFFFu, top_k);
             top_v = redux_max_u32(0xFFFFFFFFu, top_v);
-            odd = __any_sync(0xFFFFFFFFu, odd);
             // largest scale in [2^e, 2^(e+1)); a subnormal or 0 counts as 2^-15
-            const int ek = top_k >= 0x0400u ? static_cast<int>(top_k >> 10) - 15 : -15;
-            const int ev = top_v >= 0x0400u ? static_cast<int>(top_v >> 10) - 15 : -15;
+            const int ek = static_cast<int>(top_k >> 10) - 15;
+            const int ev = static_cast<int>(top_v >> 10) - 15;
             const float down_k = __uint_as_float(static_cast<uint32_t>(127 - ek - 9) << 23);
             const float down_v = __uint_as_float(static_cast<uint32_t>(127 - ev - 9) << 23);
             // A nibble under a mask is the fp16 subnormal n 2^-24 (or 16 n 2^-24), so (n - 8) s is one multiply-add,
             // rounded once: n 2^-24 * (s 2^24) - 8 s.  For s 2^24 to be an fp16, s is the scale over 2^(e + 9): below
-            // 2^-8, its products of at least 2^-14 normal for scales down to 1/64 of the block's largest.
+            // 2^-8, its products of at least 2^-14 normal for scales down to 1/32 of the block's largest.
+            if (scale_lane) {
+                float sv[2];
 #pragma unroll
-            for (int k = 0; k < (16 * G + 31) / 32; ++k) {
-                const int at = 32 * k + lane, t = at / G, g = at - t * G;
-                if (at < 16 * G) {
-                    const float sk = half_bits_to_float(dk[k]) * down_k;
-                    // a value scale that is not finite: the key's scores become NaN instead (below), and with them
-                    // the rows that see it
-                    const bool fine = (dv[k] & 0x7C00u) != 0x7C00u;
-                    const float sv = fine ? half_bits_to_float(dv[k]) * down_v : 0.0f;
-                    uint8_t *keys = sm + (scales - sb) + 8 * at;
-                    *reinterpret_cast<uint2 *>(keys) =
-                        make_uint2(pack_half(sk * kTwo24, sk * (kTwo24 / 16.0f)), pack_half(sk * -8.0f, 0.0f));
-                    __half *vals = reinterpret_cast<__half *>(sm + (scales - sb) + 128 * G) + 16 * g + t;
-                    vals[0] = __float2half_rn(sv * kTwo24);
-                    vals[16 * G] = __float2half_rn(sv * (kTwo24 / 16.0f));
-                    vals[32 * G] = __float2half_rn(sv * -8.0f);
+                for (int e = 0; e < 2; ++e) {
+                    const float sk = half_bits_to_float(dk[e]) * down_k;
+                    // a value scale that is not finite counts as 0, and makes the key's scores NaN (below), and with
+                    // them the rows that see it
+                    sv[e] = odd >> e & 1 ? 0.0f : half_bits_to_float(dv[e]) * down_v;
+                    const float s24 = sk * kTwo24, s20 = sk * (kTwo24 / 16.0f), s8 = sk * -8.0f;
+                    sts128(scales + 16 * ((st + e) * G + sg), pack_half(s24, s24), pack_half(s20, s20), pack_half(s8, s8), 0u);
                 }
+                const uint32_t to = scales + 256 * G + 2 * (16 * sg + st);
+                sts32(to, pack_half(sv[0] * kTwo24, sv[1] * kTwo24));
+                sts32(to + 32 * G, pack_half(sv[0] * (kTwo24 / 16.0f), sv[1] * (kTwo24 / 16.0f)));
+                sts32(to + 64 * G, pack_half(sv[0] * -8.0f, sv[1] * -8.0f));
             }
-            if (lane == 0) {
-                float4 m;
-                m.x = __uint_as_float(static_cast<uint32_t>(127 + ek + 9) << 23);
-                m.y = static_cast<float>(ev + 9);
-                m.z = down_v, m.w = 0.0f;
-                *reinterpret_cast<float4 *>(sm + Sh::meta_at + (i % kMetas * kTileBlocks + bi) * 16) = m;
-            }
+            if (lane == 0)
+                sts128(sb + Sh::meta_at + (i % kMetas * kTileBlocks + bi) * 16, static_cast<uint32_t>(127 + ek + 9) << 23,
+                       __float_as_uint(static_cast<float>(ev + 9)), __float_as_uint(down_v), 0u);
             __syncwarp();
-            if (odd) {
-#pragma unroll
-                for (int k = 0; k < (16 * G + 31) / 32; ++k) {
-                    const int at = 32 * k + lane, t = at / G;
-                    if (at < 16 * G && (dv[k] & 0x7C00u) == 0x7C00u)
-                        *reinterpret_cast<uint32_t *>(sm + (scales - sb) + 8 * (t * G)) = 0x7FFF7FFFu;
-                }
+            if (__any_sync(0xFFFFFFFFu, odd)) {
+                for (int e = 0; e < 2; ++e)
+                    if (odd >> e & 1) sts128(scales + 16 * ((st + e) * G), 0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu, 0u);
                 __syncwarp();
             }
             // keys: lane (r, c) has token 4(r/2) + 2h + r%2, channels 32g + 8c..8c+7 a word
             if (i >= kStages && !warp_wait(bars.kempty(i % kStages), (i / kStages - 1) & 1, a.wait_ns)) { dead = true; break; }
-            // (odd r take the groups in another order: a quarter of the warp then writes all eight 16-byte columns)
-            const uint32_t kb = sb + Sh::k_at + i % kStages * Sh::k_bytes;
-            const int swap = G % 2 == 0 ? r8 & 1 : 0;
+            const uint32_t kb = sb + Sh::k_at + i % kStages * Sh::k_bytes + bi * kBlockTokens * 128;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int t = 4 * (r8 >> 1) + 2 * h + (r8 & 1);
                 uint32_t words[G];
-                if (have) {
-                    lds_words<G>(words, raw + h * 128 * G + lane * 4 * G);
-                } else {
-#pragma unroll
-                    for (int g = 0; g < G; ++g) words[g] = 0x88888888u;
-                }
+                lds_words<G>(words, raw + h * 128 * G + lane * 4 * G);
 #pragma unroll
                 for (int g = 0; g < G; ++g) {
-                    const int mine = g ^ swap;
+                    // odd r take the groups in pairs the other way round: a quarter of the warp then writes all eight
+                    // 16-byte columns
                     const uint32_t word = G % 2 == 0 && swap ? words[g ^ (G % 2 == 0)] : words[g], high = word >> 8;
-                    uint32_t x, y;       // (s 2^24, s 2^20) and (-8 s, 0)
-                    lds64(x, y, scales + 8 * (t * G + mine));
-                    const uint32_t s0 = __byte_perm(x, x, 0x1010), s1 = __byte_perm(x, x, 0x3232), s8 = __byte_perm(y, y, 0x1010);
-                    sts128(kb + operand_chunk(bi * kBlockTokens + t, 4 * mine + c, kTile), fma_half2(word & 0x000F000Fu, s0, s8),
-                           fma_half2(word & 0x00F000F0u, s1, s8), fma_half2(high & 0x000F000Fu, s0, s8),
-                           fma_half2(high & 0x00F000F0u, s1, s8));
+                    uint32_t sc[4];      // s 2^24, s 2^20, -8 s
+                    lds128(sc, scales + 16 * ((key_token + 2 * h) * G + (g ^ swap)));
+                    // chunk 4 (g ^ swap) + c of row t, 16 bytes each: its column of 8 is xored with t % 8
+                    const uint32_t at = kb + (g >> 1) * (kTile * 128) + h * 256 + (key_at[h] ^ ((g & 1) << 6));
+                    sts128(at, fma_half2(word & 0x000F000Fu, sc[0], sc[2]), fma_half2(word & 0x00F000F0u, sc[1], sc[2]),
+                           fma_half2(high & 0x000F000Fu, sc[0], sc[2]), fma_half2(high & 0x00F000F0u, sc[1], sc[2]));
                 }
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(bars.kfull(i % kStages));
-            // values: an item is (g, r, half of the block's tokens): 4 words, channels 32g + 4r + j, 8 tokens a chunk; the
-            // items of a quarter of the warp start at other j, so that they too write all eight columns
             if (i >= kStages && !warp_wait(bars.vempty(i % kStages), (i / kStages - 1) & 1, a.wait_ns)) { dead = true; break; }
-            const uint32_t vb = sb + Sh::v_at + i % kStages * Sh::v_bytes;
-            constexpr int kItems = (16 * G + 31) / 32;
+            const uint32_t vb = sb + Sh::v_at + i % kStages * Sh::v_bytes, column = (2 * bi + kp) << 4;
             uint32_t words[kItems][4];      // tokens 8kp + 0,1 | 2,3 | 4,5 | 6,7
-            const int r = G == 3 ? (lane >> 1) & 7 : lane >> 2, kp = G == 3 ? lane & 1 : (lane >> 1) & 1;
-            const int turn = G == 3 ? (r >> 1) & 1 : lane & 1;
-            auto group_of = [&](int k) { return G == 3 ? 2 * k + (lane >> 4) : kItems * (lane & 1) + k; };
 #pragma unroll
-            for (int k = 0; k < kItems; ++k)
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t from = raw + 8 * D + (e & 1) * 128 * G + (vr * 4 + 2 * kp + (e >> 1)) * 4 * G;
+                if constexpr (G == 4) {
+                    lds64(words[0][e], words[kItems - 1][e], from + 4 * group_of(0));
+                } else {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) words[k][e] = 0x88888888u;
-            if (have) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint32_t from = raw + 8 * D + (e & 1) * 128 * G + (r * 4 + 2 * kp + (e >> 1)) * 4 * G;
-                    if constexpr (G == 4) {
-                        lds64(words[0][e], words[kItems - 1][e], from + 4 * group_of(0));
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < kItems; ++k)
-                            if (group_of(k) < G) words[k][e] = lds32(from + 4 * group_of(k));
-                    }
+                    for (int k = 0; k < kItems; ++k) words[k][e] = group_of(k) < G ? lds32(from + 4 * group_of(k)) : 0;
                 }
             }
 #pragma unroll
@@ -615,23 +606,23 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttnArgs a)
                 const int g = group_of(k);
                 if (G != 3 || g < G) {
                     uint32_t s0[4], s1[4], s8[4];
-                    lds128(s0, scales + 128 * G + 2 * (16 * g + 8 * kp));
-                    lds128(s1, scales + 160 * G + 2 * (16 * g + 8 * kp));
-                    lds128(s8, scales + 192 * G + 2 * (16 * g + 8 * kp));
+                    lds128(s0, scales + 256 * G + 2 * (16 * g + 8 * kp));
+                    lds128(s1, scales + 288 * G + 2 * (16 * g + 8 * kp));
+                    lds128(s8, scales + 320 * G + 2 * (16 * g + 8 * kp));
 #pragma unroll
                     for (int half_j = 0; half_j < 2; ++half_j) {
-                        const int shift = 8 * (half_j ^ turn);
                         uint32_t src[4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) src[e] = words[k][e] >> shift;
+                        for (int e = 0; e < 4; ++e) src[e] = words[k][e] >> (half_j ? 8 - shift : shift);
+                        // row 32g + 4r + j with j = 2 (half_j ^ turn) + jj, its columns xored with row % 8
+                        const uint32_t row = g * 4096 + (value_at ^ (half_j ? 256 + 32 : 0));
 #pragma unroll
                         for (int jj = 0; jj < 2; ++jj) {
                             uint32_t x[4];
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
                                 x[e] = jj ? fma_half2(src[e] & 0x00F000F0u, s1[e], s8[e]) : fma_half2(src[e] & 0x000F000Fu, s0[e], s8[e]);
-                            sts128(vb + operand_chunk(32 * g + 4 * r + 2 * (half_j ^ turn) + jj, 2 * bi + kp, D), x[0], x[1], x[2],
-                                   x[3]);
+                            sts128(vb + ((row ^ (jj ? 128 + 16 : 0)) ^ column), x[0], x[1], x[2], x[3]);
                         }
                     }
                 }
