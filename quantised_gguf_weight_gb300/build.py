@@ -3,6 +3,9 @@
 Each translation unit under csrc/ is compiled in parallel with
 `-gencode arch=compute_103a,code=sm_103a`, then linked into
 quantised_gguf_weight_gb300/_build/libqk.so against the CUDA runtime.
+The calls from PyTorch tensors (csrc/qk_torch.cpp) are a CPython extension,
+_build/qk_torch.so, compiled by g++ beside them against the headers of the
+installed torch and linked to libqk.so.
 Rebuilds only when a source or header is newer than the library.
 """
 from __future__ import annotations
@@ -18,6 +21,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD_DIR, "libqk.so")
+BINDING = os.path.join(BUILD_DIR, "qk_torch.so")
+BINDING_SOURCE = os.path.join(CSRC, "qk_torch.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -38,10 +43,35 @@ def _deps() -> list[str]:
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return False
     t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(d) <= t for d in _deps())
+    return all(os.path.getmtime(d) <= t for d in _deps()) and \
+        os.path.getmtime(BINDING_SOURCE) <= os.path.getmtime(BINDING)
+
+
+def _binding_command(out: str) -> list[str]:
+    """Compiles the extension to an object file: Python's and torch's own headers, nothing generated."""
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-c", BINDING_SOURCE, "-o", out,
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(root, "include"),
+            "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+            "-isystem", os.path.join(cuda, "include")]
+
+
+def _link_binding(obj: str) -> None:
+    import torch
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING + f".tmp{os.getpid()}"
+    subprocess.check_call(["g++", "-shared", "-o", tmp, obj, "-L", BUILD_DIR, "-l:libqk.so", "-Wl,-rpath,$ORIGIN",
+                           "-L", libs, f"-Wl,-rpath,{libs}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
+                           "-lc10_cuda"])
+    os.replace(tmp, BINDING)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -51,7 +81,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
     flags = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE,
                     "--expt-relaxed-constexpr"]
-    procs = []
+    binding_obj = os.path.join(BUILD_DIR, "qk_torch.cpp.o")
+    procs = [(BINDING_SOURCE, subprocess.Popen(_binding_command(binding_obj), stdout=subprocess.PIPE,
+                                               stderr=subprocess.STDOUT))]
     objs = []
     for src in sources():
         obj = os.path.join(BUILD_DIR, os.path.basename(src) + ".o")
@@ -68,10 +100,11 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if p.returncode != 0:
             failed.append(src)
     if failed:
-        raise RuntimeError(f"nvcc failed for {failed}")
+        raise RuntimeError(f"compilation failed for {failed}")
     tmp = LIB + f".tmp{os.getpid()}"
     subprocess.check_call([nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart"])
     os.replace(tmp, LIB)
+    _link_binding(binding_obj)
     return LIB
 
 

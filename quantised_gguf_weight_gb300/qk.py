@@ -1,15 +1,16 @@
 """Python binding of libqk (include/qk.h): argument marshalling only.
 
 Every call forwards device pointers, sizes and the current torch CUDA stream
-to the C ABI; all the work runs in the library's CUDA kernels.  There is no
+to the C ABI (by ctypes, the attention operators by the extension module
+qk_torch); all the work runs in the library's CUDA kernels.  There is no
 fallback: if the library is missing or fails to load, every call raises.
 PyTorch is used for device memory and streams only.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
-import struct
 import threading
 
 import torch
@@ -378,67 +379,41 @@ def qgemm_swiglu_q4_k(w, gate_offset, up_offset, F, K, x, h=None, ldh=0, workspa
 
 # ---------------------------------------------------------------- attention operators
 
-# A call of a small shape costs what its host side costs, so the checks below ask each tensor once and cheaply.
-_CACHE_BYTES = struct.Struct("@Pqiii4x").pack        # qk_kv_cache_q4
+# Their checks, outputs and calls into the library are in csrc/qk_torch.cpp: a call of a small shape costs what its host
+# side costs.
+
+_ext = None
 
 
-def _rows(t, width: int, name: str, dev: int, dtype=None) -> tuple[int, int, int]:
-    """(rows, row stride, element type) of rows of `width` elements with unit stride inside a row."""
-    if not isinstance(t, torch.Tensor) or t.get_device() != dev or (dtype is not None and t.dtype is not dtype):
-        _on_device(t, name, dtype)
-    code = DTYPES.get(t.dtype)
-    if code is None:
-        raise ValueError(f"{name} must be float32, float16 or bfloat16, not {t.dtype}")
-    shape = t.shape
-    if len(shape) != 2 or shape[1] != width:
-        raise ValueError(f"{name} must be rows of {width} elements, got shape {tuple(shape)}")
-    n = shape[0]
-    ld, unit = t.stride()
-    if unit != 1 and width > 1:
-        raise ValueError(f"{name} must have unit stride inside a row, got {unit}")
-    if n <= 1:
-        ld = width         # a single row has no stride of its own
-    elif ld < width:
-        raise ValueError(f"{name} rows are {ld} elements apart, less than their {width}")
-    return n, ld, code
+def _binding():
+    """The extension module qk_torch (built beside libqk.so)."""
+    global _ext
+    if _ext is None:
+        load()
+        if not os.path.exists(_build.BINDING):
+            raise RuntimeError(f"qk_torch.so not built ({_build.BINDING}); run __graft_entry__.build()")
+        spec = importlib.util.spec_from_file_location("qk_torch", _build.BINDING)
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+        _ext = mod
+    return _ext
 
 
-def _vector(t, n: int, dtype, name: str, dev: int):
+def _result(r, what: str):
+    """What a call of the extension gave, or its status as an error."""
+    if type(r) is int:
+        raise QKError(r, what)
+    return r
+
+
+def _vector(t, n: int, dtype, name: str):
     """Pointer of a contiguous vector of at least n elements (None: null)."""
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype is not dtype:
-        _on_device(t, name, dtype)
+    _on_device(t, name, dtype)
     if t.numel() < n or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous with at least {n} elements")
     return t.data_ptr()
-
-
-def _table(table, positions, T: int, D: int, dev: int):
-    """(table pointer, positions in it, rotating channels, positions pointer)."""
-    if table is None:
-        return None, 0, 0, None
-    if not isinstance(table, torch.Tensor) or table.get_device() != dev or table.dtype is not torch.float32:
-        _on_device(table, "table", torch.float32)
-    shape = table.shape
-    if len(shape) != 3 or shape[2] != 2 or 2 * shape[1] > D or not table.is_contiguous():
-        raise ValueError(f"table must be contiguous [n_pos][rot/2][2] with rot <= {D}, got {tuple(shape)}")
-    if positions is None:
-        raise ValueError("positions are needed with a table")
-    return table.data_ptr(), shape[0], 2 * shape[1], _vector(positions, T, torch.int32, "positions", dev)
-
-
-def _cache(cache, dev: int) -> tuple[bytes, int, int]:
-    """(qk_kv_cache_q4 as bytes, kv heads, head size) of a cache tensor."""
-    if not isinstance(cache, torch.Tensor) or cache.get_device() != dev or cache.dtype is not torch.uint8:
-        _on_device(cache, "cache", torch.uint8)
-    shape = cache.shape
-    if len(shape) != 4 or shape[3] % 18 or not cache.is_contiguous():
-        raise ValueError("cache must be a contiguous uint8 tensor [pages][kv heads][page_tokens/16][18*head_dim] "
-                         f"(kv_cache_q4), got shape {tuple(shape)}")
-    n, h, b, size = shape
-    D = size // 18
-    return _CACHE_BYTES(cache.data_ptr(), n, h, D, 16 * b), h, D
 
 
 def rope_table(n_pos: int, rot: int, base: float = 10000.0, freq_scale: float = 1.0,
@@ -447,11 +422,10 @@ def rope_table(n_pos: int, rot: int, base: float = 10000.0, freq_scale: float = 
                stream=None) -> torch.Tensor:
     """[n_pos][rot/2][2] fp32 (cos, sin) of the position angles; freq_scale interpolates positions, freq_factors
     divides each frequency, orig_ctx > 0 ramps between kept and interpolated frequencies (see include/qk.h)."""
-    dev = torch.cuda.current_device()
     if table is None:
         table = torch.empty((max(n_pos, 0), max(rot, 0) // 2, 2), dtype=torch.float32, device="cuda")
-    st = load().qk_rope_table(_vector(table, n_pos * (rot // 2) * 2, torch.float32, "table", dev), n_pos, rot, base,
-                              freq_scale, _vector(freq_factors, rot // 2, torch.float32, "freq_factors", dev),
+    st = load().qk_rope_table(_vector(table, n_pos * (rot // 2) * 2, torch.float32, "table"), n_pos, rot, base,
+                              freq_scale, _vector(freq_factors, rot // 2, torch.float32, "freq_factors"),
                               orig_ctx, beta_fast, beta_slow, amplitude, _stream(stream))
     _check(st, "qk_rope_table")
     return table
@@ -463,22 +437,9 @@ def norm_rope(x: torch.Tensor, n_q_heads: int, n_k_heads: int, head_dim: int, po
               y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """RMS norm of every head (a weight of None: no norm) and rotation of its first channels by the table's row of
     the token's position, over rows of n_q_heads + n_k_heads heads.  y may be x."""
-    dev = torch.cuda.current_device()
-    width = (n_q_heads + n_k_heads) * head_dim
-    T, ldx, xt = _rows(x, width, "x", dev)
-    if y is None:
-        y, ldy, yt = torch.empty((T, width), dtype=x.dtype, device=x.device), width, xt
-    else:
-        n, ldy, yt = _rows(y, width, "y", dev)
-        if n < T:
-            raise ValueError(f"y has {n} rows, x {T}")
-    tp, n_pos, rot, pp = _table(table, positions, T, head_dim, dev)
-    st = load().qk_norm_rope(x.data_ptr(), ldx, xt, n_q_heads, n_k_heads, head_dim,
-                             _vector(q_weight, head_dim, torch.float32, "q_weight", dev),
-                             _vector(k_weight, head_dim, torch.float32, "k_weight", dev), eps, tp, n_pos, rot,
-                             1 if interleaved else 0, pp, T, y.data_ptr(), ldy, yt, _stream(stream))
-    _check(st, "qk_norm_rope")
-    return y
+    return _result((_ext or _binding()).norm_rope(
+        x, n_q_heads, n_k_heads, head_dim, positions, table, q_weight, k_weight, eps, interleaved, y,
+        None if stream is None else _stream(stream)), "qk_norm_rope")
 
 
 def kv_cache_q4(n_pages: int, n_kv_heads: int, page_tokens: int, head_dim: int, device=None) -> torch.Tensor:
@@ -495,55 +456,19 @@ def kv_append_q4(cache: torch.Tensor, q: torch.Tensor | None, k: torch.Tensor, v
                  interleaved: bool = False, q_out: torch.Tensor | None = None, stream=None) -> torch.Tensor | None:
     """Norm and rotation of T tokens' queries and keys, with keys and values stored into `cache` at `slots` (int64;
     negative: not stored).  Returns the queries (rows of q's heads; q_out may be q), None without q."""
-    dev = torch.cuda.current_device()
-    c, n_kv, D = _cache(cache, dev)
-    width = n_kv * D
-    T, ldk, kt = _rows(k, width, "k", dev)
-    n, ldv, _ = _rows(v, width, "v", dev, k.dtype)
-    if n != T:
-        raise ValueError(f"k has {T} rows, v {n}")
-    sp = _vector(slots, T, torch.int64, "slots", dev)
-    tp, n_pos, rot, pp = _table(table, positions, T, D, dev)
-    qp = qop = None
-    heads = ldq = ldo = ot = 0
-    if q is not None:
-        wq = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 2 else 0
-        if wq == 0 or wq % D:
-            raise ValueError(f"q must be rows of heads of {D} channels")
-        n, ldq, _ = _rows(q, wq, "q", dev, k.dtype)
-        if n != T:
-            raise ValueError(f"q has {n} rows, k {T}")
-        heads = wq // D
-        if q_out is None:
-            q_out, ldo, ot = torch.empty((T, wq), dtype=q.dtype, device=q.device), wq, kt
-        else:
-            n, ldo, ot = _rows(q_out, wq, "q_out", dev)
-            if n < T:
-                raise ValueError(f"q_out has {n} rows, q {T}")
-        qp, qop = q.data_ptr(), q_out.data_ptr()
-    st = load().qk_kv_append_q4(c, qp, ldq, heads, k.data_ptr(), ldk, v.data_ptr(), ldv, kt,
-                                _vector(q_weight, D, torch.float32, "q_weight", dev),
-                                _vector(k_weight, D, torch.float32, "k_weight", dev), eps, tp, n_pos, rot,
-                                1 if interleaved else 0, pp, sp, T, qop, ldo, ot, _stream(stream))
-    _check(st, "qk_kv_append_q4")
-    return q_out if heads else None
+    return _result((_ext or _binding()).kv_append_q4(
+        cache, q, k, v, positions, slots, table, q_weight, k_weight, eps, interleaved, q_out,
+        None if stream is None else _stream(stream)), "qk_kv_append_q4")
 
 
 def kv_read_q4(cache: torch.Tensor, slots: torch.Tensor, dtype: torch.dtype = torch.float16,
                stream=None) -> tuple[torch.Tensor, torch.Tensor]:
     """The keys and values that the cache holds at `slots`: two [T][kv heads * head_dim] tensors of `dtype`."""
-    dev = torch.cuda.current_device()
-    c, n_kv, D = _cache(cache, dev)
     code = DTYPES.get(dtype)
     if code is None:
         raise ValueError(f"dtype must be float32, float16 or bfloat16, not {dtype}")
-    T = slots.numel()
-    sp = _vector(slots, T, torch.int64, "slots", dev)
-    k = torch.empty((T, n_kv * D), dtype=dtype, device=cache.device)
-    v = torch.empty((T, n_kv * D), dtype=dtype, device=cache.device)
-    st = load().qk_kv_read_q4(c, sp, T, k.data_ptr(), 0, v.data_ptr(), 0, code, _stream(stream))
-    _check(st, "qk_kv_read_q4")
-    return k, v
+    return _result((_ext or _binding()).kv_read_q4(cache, slots, code, None if stream is None else _stream(stream)),
+                   "qk_kv_read_q4")
 
 
 def attn_q4_workspace(B: int, n_q_heads: int, n_kv_heads: int, head_dim: int, max_q: int = 1, max_len: int = 0,
@@ -561,43 +486,9 @@ def attn_q4(cache: torch.Tensor, q: torch.Tensor, page_table: torch.Tensor, lens
     pages page_table[b], and the rows q_start[b]..q_start[b+1] (None: max_q each) as its last positions.  scale
     defaults to head_dim^-0.5; window > 0 lets a row see that many keys up to its own.  `workspace` (zeroed once,
     attn_q4_workspace) lets long sequences spread over the GPU; without it they are not split."""
-    dev = torch.cuda.current_device()
-    c, n_kv, D = _cache(cache, dev)
-    width = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 2 else 0
-    if width == 0 or width % (D * n_kv):
-        raise ValueError(f"q must be rows of a multiple of {n_kv} heads of {D} channels")
-    T, ldq, qt = _rows(q, width, "q", dev)
-    B = lens.numel()
-    lp = _vector(lens, B, torch.int32, "lens", dev)
-    if page_table.get_device() != dev or page_table.dtype is not torch.int32:
-        _on_device(page_table, "page_table", torch.int32)
-    if page_table.dim() != 2 or page_table.shape[0] < B:
-        raise ValueError(f"page_table must be [{B}][pages], got {tuple(page_table.shape)}")
-    rows, pages = page_table.shape
-    ld, unit = page_table.stride()
-    if rows <= 1:
-        ld = pages
-    if (unit != 1 and pages > 1) or ld < pages:
-        raise ValueError(f"page_table must have unit stride and rows at least {pages} apart, got {(ld, unit)}")
-    if out is None:
-        out, ldo, ot = torch.empty((T, width), dtype=q.dtype, device=q.device), width, qt
-    else:
-        n, ldo, ot = _rows(out, width, "out", dev)
-        if n < T:
-            raise ValueError(f"out has {n} rows, q {T}")
-    wp, wb = None, 0
-    if workspace is not None:
-        if workspace.get_device() != dev:
-            _on_device(workspace, "workspace")
-        if not workspace.is_contiguous():
-            raise ValueError("workspace must be contiguous")
-        wp, wb = workspace.data_ptr(), workspace.nbytes
-    st = load().qk_attn_q4(c, q.data_ptr(), ldq, qt, width // D, page_table.data_ptr(), ld, pages, lp,
-                           _vector(q_start, B + 1, torch.int32, "q_start", dev), B, T, max_q, max_len,
-                           D ** -0.5 if scale is None else scale, window, out.data_ptr(), ldo, ot, wp, wb,
-                           _stream(stream))
-    _check(st, "qk_attn_q4")
-    return out
+    return _result((_ext or _binding()).attn_q4(
+        cache, q, page_table, lens, q_start, max_q, max_len, scale, window, out, workspace,
+        None if stream is None else _stream(stream)), "qk_attn_q4")
 
 
 def debug_gemm_skip_chunk(chunk: int) -> int:
