@@ -24,29 +24,42 @@ struct Cut {
 
 std::atomic<int> g_skip_block{-1};
 
-constexpr int64_t kChunkFrom = 64;           // rows a sequence and head from which it is taken
+// Rows a sequence and head from which it is taken.  Times of the few-row form and of it, us, heads of 128 in 16 bits:
+//   8 sequences of 4096 tokens, 8 heads   16 rows 29 and 45, 32 41 and 45, 48 66 and 47, 256 248 and 65
+//   1 sequence of 16384, 8 heads          16 rows 21 and 27, 32 28 and 27, 48 38 and 28, 256 170 and 34
+//   8 of 4096, 32 heads of 96             16 rows 51 and 128, 32 96 and 128, 48 178 and 129
+constexpr int64_t kChunkFrom = 33;
 constexpr int64_t kCounters = 16384;         // ints at the start of every workspace, whatever the call
 // max_len sizes the cut; no sequence is longer than `longest`.
 Cut cut_for(int64_t B, int n_kv, int rep, int D, int64_t max_q, int64_t max_len, int64_t longest, bool fp32)
 {
     Cut c{};
     const int64_t rows = max_q * rep;
+    int sms = 152, smem = 0;
+    device_limits(&sms, &smem);
     c.pieces = fp32 ? 2 : 1;
     c.chunk = !fp32 && rows >= kChunkFrom && D <= 128;
-    // columns of a warp's tile: as few sets of 8 as hold the rows; with more sets a block of keys is taken apart once
-    // for more rows (four sets of fp32 rows against one, 64 rows over 5000 keys: see the rule's measurements below)
+    // Columns of a warp's tile, in sets of 8: a block of keys is taken apart once for all of them, but the more there
+    // are the fewer thread blocks there are to fill the GPU.  fp32 rows have two columns each and take two sets at
+    // once (16 columns, 16 short sequences: 15 us, one set 16), four where their heads and tiles still make three
+    // quarters of the thread blocks that the GPU holds (8 x 32 rows over 4096 keys 54 us, two sets 58; 8 x 64 rows
+    // over up to 5000 154 and 160).  16-bit rows take one, and two under the same condition: 64 x 16 rows over 4096
+    // keys 122 us, one set 137; 64 x 32 rows 213, one 263, four 249; but 8 x 16 rows 32 us, one 29.
     c.sets = 1;
-    while (c.sets * 8 < rows * c.pieces && c.sets < (D <= 128 ? 4 : 2)) c.sets *= 2;
+    for (int n = 2; n <= (fp32 && D <= 128 ? 4 : 2) && n * 4 < rows * c.pieces; n *= 2)
+        if ((fp32 && n == 2) ||
+            4 * B * n_kv * ((rows * c.pieces + n * 8 - 1) / (n * 8)) >= 3 * sms * rows_blocks_per_sm(D / 32, n))
+            c.sets = n;
     c.row_tile = c.chunk ? kChunkRows : c.sets * 8 / c.pieces;
     c.tiles = static_cast<int>((rows + c.row_tile - 1) / c.row_tile);
     c.groups = B * n_kv * c.tiles;
     const int64_t blocks = (max_len + kBlockTokens - 1) / kBlockTokens;
-    int sms = 152, smem = 0;
-    device_limits(&sms, &smem);
     c.splits = 1;
     if (c.chunk) {
-        // rounds of one thread block an SM, of key tiles of 8 blocks (about 1.2 us each) and 3 tiles' worth of start
-        // and end; parts of several splits are written and read again (5 TB/s) by a second kernel (2 us)
+        // rounds of one thread block an SM, of 8 blocks' keys in about 2 us and as much as 7 of them for start and end;
+        // parts of several splits are written and read again (3 TB/s) by a second kernel (5 us).  256 rows of 8 heads:
+        // 16384 keys whole 268 us, in 19 splits 34; 8 sequences of 4096 keys whole 78, in 2 splits 65, in 4 87; 1024
+        // rows, 16384 keys: in 4 splits 90, in 9 111
         const int64_t tiles = (blocks + 7) / 8;
         double best = 1e30;
         for (int64_t rounds = 1, last = 0; rounds <= 8; ++rounds) {
@@ -55,19 +68,19 @@ Cut cut_for(int64_t B, int n_kv, int rep, int D, int64_t max_q, int64_t max_len,
             if (s < 1) s = 1;
             if (s == last) continue;
             last = s;
-            const double us = 1.2 * static_cast<double>((c.groups * s + sms - 1) / sms * ((tiles + s - 1) / s + 3)) +
-                              (s > 1 ? 2.0 + 2e-7 * static_cast<double>(2 * s * c.groups * chunk_part_bytes(D)) : 0.0);
+            const double us = 2.0 * static_cast<double>((c.groups * s + sms - 1) / sms * ((tiles + s - 1) / s + 7)) +
+                              (s > 1 ? 5.0 + 3e-7 * static_cast<double>(2 * s * c.groups * chunk_part_bytes(D)) : 0.0);
             if (us < best) best = us, c.splits = static_cast<int>(s);
         }
         c.min_blocks = (tiles + c.splits - 1) / c.splits * 8;
         if (c.min_blocks < 16) c.min_blocks = 16;
         return c;
     }
-    // few rows: split where heads are at most half of the thread blocks that the GPU holds and have blocks to split,
-    // over as many thread blocks as that.  (With more heads than that, one thread block a head: 512 heads of 8192
-    // tokens take 146 us whole and 148, 160, 162 us in 2, 3, 4 parts.)
+    // few rows: split where heads are at most a third of the thread blocks that the GPU holds and have blocks to split,
+    // over as many thread blocks as that (304: 64 heads of 4096 tokens 27 us, whole 41; 128 heads 36 us, whole 29; 512
+    // heads of 8192 whole 146, in 2, 3, 4 parts 148, 160, 162).
     const int64_t hold = static_cast<int64_t>(sms) * rows_blocks_per_sm(D / 32, c.sets);
-    if (blocks > 2 * kWarps && c.groups * 2 <= hold && B * c.tiles <= kRowItems &&
+    if (blocks > 2 * kWarps && c.groups * 3 <= hold && B * c.tiles <= kRowItems &&
         c.groups * ((longest + kBlockTokens - 1) / kBlockTokens) < (1 << 30))
         c.cut = hold;
     return c;

@@ -151,6 +151,20 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_
     return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, limit_ns));
 }
 
+// A 16-bit element's value.
+__device__ __forceinline__ float float_of(uint32_t bits, bool bf16)
+{
+    return bf16 ? __uint_as_float(bits << 16) : half_bits_to_float(bits);
+}
+
+// Two values as a pair of 16-bit elements.
+__device__ __forceinline__ uint32_t pack_as(float lo, float hi, bool bf16)
+{
+    if (!bf16) return pack_half(lo, hi);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
 // Barrier addresses.
 struct Bars {
     uint32_t at;
@@ -362,9 +376,23 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttnArgs a)
         row_token = w.seq.r0 + i;
         row_head = static_cast<int64_t>(w.hk) * a.rep + (row_in ? row - i * a.rep : 0);
         const int64_t at = row_token * a.ldq + row_head * D;
-        float big = 0.0f;
-        if (row_in)
-            for (int c = 0; c < D; ++c) big = fmaxf(big, fabsf(load_as_float(a.q, at + c, a.q_type)));
+        // the row as it is, 16 bytes a load where base and stride allow it (one element a load: 45 us more a call)
+        const uint16_t *from = static_cast<const uint16_t *>(a.q) + at;
+        uint32_t raw[D / 2], top = 0;
+        if (((reinterpret_cast<uintptr_t>(a.q) | 2 * a.ldq) & 15) == 0) {
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) {
+                const uint4 x = row_in ? __ldg(reinterpret_cast<const uint4 *>(from) + c) : make_uint4(0, 0, 0, 0);
+                raw[4 * c] = x.x, raw[4 * c + 1] = x.y, raw[4 * c + 2] = x.z, raw[4 * c + 3] = x.w;
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < D / 2; ++c) raw[c] = row_in ? __ldg(from + 2 * c) | __ldg(from + 2 * c + 1) << 16 : 0;
+        }
+#pragma unroll
+        for (int c = 0; c < D / 2; ++c) top = __vmaxu2(top, raw[c] & 0x7FFF7FFFu);
+        const bool bf16 = a.q_type == QK_BF16;
+        const float big = float_of(max(top >> 16, top & 0xFFFFu), bf16);
         int e = 127;
         if (big > 0.0f && big < INFINITY) e = 127 + 10 - (static_cast<int>(__float_as_uint(big) >> 23) - 127);
         e = min(e, 250);
@@ -375,13 +403,17 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttnArgs a)
             R.lo = clamp_key(a.window > 0 ? pos - a.window + 1 - base : -1);
             R.hi = clamp_key(pos + 1 - base);
         }
+#pragma unroll
         for (int c = 0; c < D / 32; ++c) {
             uint32_t q[16];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 float x[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] = row_in ? load_as_float(a.q, at + 32 * c + 8 * k + j, a.q_type) * up : 0.0f;
+                for (int j = 0; j < 8; j += 2) {
+                    const uint32_t pair = raw[16 * c + 4 * k + j / 2];
+                    x[j] = float_of(pair & 0xFFFFu, bf16) * up, x[j + 1] = float_of(pair >> 16, bf16) * up;
+                }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) q[4 * k + j] = pack_half(x[j], x[j + 4]);
             }
@@ -683,8 +715,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttnArgs a)
                 part[kChunkRows * D + 2 * (half * 128 + my_row)] = R.m;
                 part[kChunkRows * D + 2 * (half * 128 + my_row) + 1] = R.l;
             }
-            part += (half * 128 + my_row) * D;
+            part += (half * 128 + my_row) * 4;       // a warp's 32 rows of four channels lie side by side
         }
+        const bool wide = ((reinterpret_cast<uintptr_t>(a.out) | a.ldo * (a.out_type == QK_F32 ? 4 : 2)) & 15) == 0;
         const int64_t to = row_token * a.ldo + row_head * D;
         for (int c = 0; c < D / 16; ++c) {
             uint32_t v[16];
@@ -699,12 +732,26 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttnArgs a)
             if (part) {
 #pragma unroll
                 for (int i = 0; i < 16; i += 4)
-                    *reinterpret_cast<uint4 *>(part + 16 * c + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-            } else {
+                    *reinterpret_cast<uint4 *>(part + (4 * c + i / 4) * (kChunkRows * 4)) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                continue;
+            }
+            float x[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    store_float_as(a.out, to + 16 * c + i, a.out_type,
-                                   R.l == 0.0f ? 0.0f : __uint_as_float(v[i]) * inv);
+            for (int i = 0; i < 16; ++i) x[i] = R.l == 0.0f ? 0.0f : __uint_as_float(v[i]) * inv;
+            if (!wide) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) store_float_as(a.out, to + 16 * c + i, a.out_type, x[i]);
+            } else if (a.out_type == QK_F32) {
+#pragma unroll
+                for (int i = 0; i < 16; i += 4)
+                    *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + to + 16 * c + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+            } else {
+                const bool bf16 = a.out_type == QK_BF16;
+#pragma unroll
+                for (int i = 0; i < 16; i += 8)
+                    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + to + 16 * c + i) =
+                        make_uint4(pack_as(x[i], x[i + 1], bf16), pack_as(x[i + 2], x[i + 3], bf16),
+                                   pack_as(x[i + 4], x[i + 5], bf16), pack_as(x[i + 6], x[i + 7], bf16));
             }
         }
         tc_fence_before();
@@ -716,15 +763,16 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttnArgs a)
     }
 }
 
-// Joins the splits' parts in their order: a warp a row and head.
+// Joins the splits' parts in their order: a warp 8 rows of 16 channels, a lane a row of 4; eight parts are on their way
+// at once.
 __global__ void __launch_bounds__(256) join_kernel(const AttnArgs a, int D, int64_t groups)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31;
-    const int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    const int64_t group = item / kChunkRows;
+    const int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5), group = item / (2 * D);
     if (group >= groups) return;
-    const int row = static_cast<int>(item - group * kChunkRows);
+    const int at = static_cast<int>(item - group * (2 * D));
+    const int row = at % 32 * 8 + (lane & 7), vec = at / 32 * 4 + (lane >> 3);
     const int hk = static_cast<int>(group % a.n_kv), tile = static_cast<int>(group / a.n_kv % a.tiles);
     const Sequence seq = sequence_of(a, group / a.n_kv / a.tiles);
     if (seq.bad) return;
@@ -734,33 +782,44 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnArgs a, int D, int6
     if (active <= 1) return;
     const int64_t stride = chunk_part_bytes(D) / 4;
     const float *part = a.parts + group * a.splits * stride;
-    float m = kNoMax;
-    for (int s = lane; s < active; s += 32) m = fmaxf(m, part[s * stride + kChunkRows * D + 2 * row]);
+    float m = kNoMax, l = 0.0f, v[4] = {};
+    for (int s0 = 0; s0 < active; s0 += 8) {
+        float2 ml[8];
+        float4 x[8];
 #pragma unroll
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-    float4 v[2] = {};
-    float l = 0.0f;
-    const int vecs = D / 4;
-#pragma unroll 4
-    for (int s = 0; s < active; ++s) {
-        const float *p = part + s * stride;
-        const float f = ex2(p[kChunkRows * D + 2 * row] - m);
-        l = fmaf(f, p[kChunkRows * D + 2 * row + 1], l);
-        for (int k = 0; k < 2; ++k)
-            if (lane + 32 * k < vecs) {
-                const float4 x = *reinterpret_cast<const float4 *>(p + row * D + 4 * (lane + 32 * k));
-                v[k].x = fmaf(f, x.x, v[k].x), v[k].y = fmaf(f, x.y, v[k].y);
-                v[k].z = fmaf(f, x.z, v[k].z), v[k].w = fmaf(f, x.w, v[k].w);
+        for (int k = 0; k < 8; ++k) {
+            ml[k] = make_float2(kNoMax, 0.0f), x[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (s0 + k < active) {
+                const float *p = part + (s0 + k) * stride;
+                ml[k] = *reinterpret_cast<const float2 *>(p + kChunkRows * D + 2 * row);
+                x[k] = *reinterpret_cast<const float4 *>(p + (vec * kChunkRows + row) * 4);
             }
+        }
+        float top = m;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) top = fmaxf(top, ml[k].x);
+        const float f0 = ex2(m - top);
+        m = top, l *= f0, v[0] *= f0, v[1] *= f0, v[2] *= f0, v[3] *= f0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float f = ex2(ml[k].x - m);
+            l = fmaf(f, ml[k].y, l);
+            v[0] = fmaf(f, x[k].x, v[0]), v[1] = fmaf(f, x[k].y, v[1]), v[2] = fmaf(f, x[k].z, v[2]), v[3] = fmaf(f, x[k].w, v[3]);
+        }
     }
     const int i = (first + row) / a.rep;
-    const int64_t to = (seq.r0 + i) * a.ldo + (static_cast<int64_t>(hk) * a.rep + first + row - i * a.rep) * D;
-    for (int k = 0; k < 2; ++k)
-        if (lane + 32 * k < vecs) {
-            const float x[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-            for (int e = 0; e < 4; ++e)
-                store_float_as(a.out, to + 4 * (lane + 32 * k) + e, a.out_type, l == 0.0f ? 0.0f : x[e] / l);
-        }
+    const int64_t to = (seq.r0 + i) * a.ldo + (static_cast<int64_t>(hk) * a.rep + first + row - i * a.rep) * D + 4 * vec;
+    const int size = a.out_type == QK_F32 ? 4 : 2;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = l == 0.0f ? 0.0f : v[e] / l;
+    if ((reinterpret_cast<uintptr_t>(a.out) | a.ldo * size) % (4 * size) != 0) {
+        for (int e = 0; e < 4; ++e) store_float_as(a.out, to + e, a.out_type, v[e]);
+    } else if (size == 4) {
+        *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + to) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+        const bool bf16 = a.out_type == QK_BF16;
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + to) = make_uint2(pack_as(v[0], v[1], bf16), pack_as(v[2], v[3], bf16));
+    }
 }
 
 template <int G>
@@ -791,7 +850,7 @@ cudaError_t launch(const AttnArgs &a, int64_t groups, cudaStream_t st)
     e = cudaLaunchKernelEx(&cfg, kern, a);
     if (e != cudaSuccess || a.splits == 1) return e;
     // the join may be scheduled while the tiles still run: it waits for all of them
-    cfg.gridDim = dim3(static_cast<unsigned>((groups * kChunkRows + 7) / 8));
+    cfg.gridDim = dim3(static_cast<unsigned>(groups * (8 * G)));
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
     cfg.numAttrs = 1;

@@ -759,13 +759,14 @@ cudaError_t launch_rows(const AttnArgs &a, int64_t grid, cudaStream_t st)
     return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
-// Column sets: 1, 2, or as many as the accumulators leave room for.
+// Column sets: 1 or 2, and 4 for fp32 rows where the accumulators leave room for them.
 template <int G>
 cudaError_t launch_rows_of(const AttnArgs &a, int pieces, int sets, int64_t grid, cudaStream_t st)
 {
     if (sets == 1) return pieces == 2 ? launch_rows<G, 2, 1>(a, grid, st) : launch_rows<G, 1, 1>(a, grid, st);
     if (sets == 2) return pieces == 2 ? launch_rows<G, 2, 2>(a, grid, st) : launch_rows<G, 1, 2>(a, grid, st);
-    if constexpr (G <= 4) return pieces == 2 ? launch_rows<G, 2, 4>(a, grid, st) : launch_rows<G, 1, 4>(a, grid, st);
+    if constexpr (G <= 4)
+        if (pieces == 2) return launch_rows<G, 2, 4>(a, grid, st);
     return cudaErrorInvalidValue;
 }
 
