@@ -38,7 +38,7 @@ Cut cut_for(int64_t B, int n_kv, int rep, int D, int64_t max_q, int64_t max_len,
     int sms = 152, smem = 0;
     device_limits(&sms, &smem);
     c.pieces = fp32 ? 2 : 1;
-    c.chunk = !fp32 && rows >= kChunkFrom && D <= 128;
+    c.chunk = rows >= kChunkFrom && D <= 128;
     // Columns of a warp's tile, in sets of 8: a block of keys is taken apart once for all of them, but the more there
     // are the fewer thread blocks there are to fill the GPU.  fp32 rows have two columns each and take two sets at
     // once (16 columns, 16 short sequences: 15 us, one set 16), four where their heads and tiles still make three
@@ -50,7 +50,7 @@ Cut cut_for(int64_t B, int n_kv, int rep, int D, int64_t max_q, int64_t max_len,
         if ((fp32 && n == 2) ||
             4 * B * n_kv * ((rows * c.pieces + n * 8 - 1) / (n * 8)) >= 3 * sms * rows_blocks_per_sm(D / 32, n))
             c.sets = n;
-    c.row_tile = c.chunk ? kChunkRows : c.sets * 8 / c.pieces;
+    c.row_tile = c.chunk ? (fp32 ? kChunkRows32 : kChunkRows) : c.sets * 8 / c.pieces;
     c.tiles = static_cast<int>((rows + c.row_tile - 1) / c.row_tile);
     c.groups = B * n_kv * c.tiles;
     const int64_t blocks = (max_len + kBlockTokens - 1) / kBlockTokens;
@@ -69,7 +69,7 @@ Cut cut_for(int64_t B, int n_kv, int rep, int D, int64_t max_q, int64_t max_len,
             if (s == last) continue;
             last = s;
             const double us = 2.0 * static_cast<double>((c.groups * s + sms - 1) / sms * ((tiles + s - 1) / s + 7)) +
-                              (s > 1 ? 5.0 + 3e-7 * static_cast<double>(2 * s * c.groups * chunk_part_bytes(D)) : 0.0);
+                              (s > 1 ? 5.0 + 3e-7 * static_cast<double>(2 * s * c.groups * chunk_part_bytes(D, c.row_tile)) : 0.0);
             if (us < best) best = us, c.splits = static_cast<int>(s);
         }
         c.min_blocks = (tiles + c.splits - 1) / c.splits * 8;
@@ -88,7 +88,7 @@ Cut cut_for(int64_t B, int n_kv, int rep, int D, int64_t max_q, int64_t max_len,
 
 int64_t part_bytes_of(const Cut &c, int D)
 {
-    if (c.chunk) return chunk_part_bytes(D);
+    if (c.chunk) return chunk_part_bytes(D, c.row_tile);
     return (static_cast<int64_t>(c.row_tile) * D + 2 * c.row_tile) * 4;
 }
 
@@ -177,7 +177,10 @@ int qk_attn_q4(const qk_kv_cache_q4 *cache, const void *q, int64_t ldq, int q_ty
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = cudaErrorInvalidValue;
     a.skip_block = g_skip_block.load();
-    if (cut.chunk) return chunk_launch(a, D, cut.groups, s) == cudaSuccess ? QK_OK : QK_ERR_CUDA;
+    if (cut.chunk) {
+        e = q_type == QK_F32 ? chunk32_launch(a, D, cut.groups, s) : chunk_launch(a, D, cut.groups, s);
+        return e == cudaSuccess ? QK_OK : QK_ERR_CUDA;
+    }
     switch (D) {
     case 64: e = rows_launch_64(a, cut.pieces, cut.sets, grid, s); break;
     case 96: e = rows_launch_96(a, cut.pieces, cut.sets, grid, s); break;

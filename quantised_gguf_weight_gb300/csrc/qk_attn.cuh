@@ -119,12 +119,14 @@ cudaError_t rows_launch_96(const AttnArgs &a, int pieces, int sets, int64_t grid
 cudaError_t rows_launch_128(const AttnArgs &a, int pieces, int sets, int64_t grid, cudaStream_t st);
 cudaError_t rows_launch_256(const AttnArgs &a, int pieces, int sets, int64_t grid, cudaStream_t st);
 
-// The many-row form (qk_attn_chunk.cu): tiles of kChunkRows rows on the 5th-generation tensor cores.
-constexpr int kChunkRows = 256;
+// The many-row forms, on the 5th-generation tensor cores: tiles of kChunkRows rows in 16 bits (qk_attn_chunk.cu), of
+// kChunkRows32 in fp32 (qk_attn_chunk32.cu).
+constexpr int kChunkRows = 256, kChunkRows32 = 128;
 cudaError_t chunk_launch(const AttnArgs &a, int D, int64_t groups, cudaStream_t st);
-__host__ __device__ inline int64_t chunk_part_bytes(int D)
+cudaError_t chunk32_launch(const AttnArgs &a, int D, int64_t groups, cudaStream_t st);
+__host__ __device__ inline int64_t chunk_part_bytes(int D, int rows)
 {
-    return (static_cast<int64_t>(kChunkRows) * D + 2 * kChunkRows) * 4;
+    return (static_cast<int64_t>(rows) * D + 2 * rows) * 4;
 }
 
 }  // namespace attn

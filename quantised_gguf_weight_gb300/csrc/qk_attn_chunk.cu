@@ -25,27 +25,21 @@
 // the dequantisation (each takes every sixth 16-token block and copies its own
 // raw blocks, two ahead), 14 and 15 issue the MMAs, one for each row tile, so
 // that the waits of one are covered by the products of the other.
-#include <atomic>
-
-#include "qk_attn.cuh"
+#include "qk_attn_chunk.cuh"
 #include "qk_internal.h"
-#include "qk_tc.cuh"
 
 namespace qk {
 using namespace attn;
+using namespace chunk;
 namespace {
 
 // Sixteen warps, so that a thread may have 128 registers.
 constexpr int kSoftmaxWarps = 8, kDequantWarps = 6, kMmaWarp = 14;
 constexpr int kThreads = 16 * 32;
-constexpr int kTile = 64;                  // keys a tile
 constexpr int kStages = 3;                 // tiles of K' and of V'
 constexpr int kMetas = 8;                  // tiles whose exponents are kept: more than stages and tiles at work
-constexpr int kTileBlocks = kTile / kBlockTokens;
 constexpr int kSlots = 2 * kDequantWarps;  // raw blocks in flight: two a dequantising warp, its own
-constexpr float kMost = 16384.0f;          // the largest P, and sum of 16
 constexpr float kTwo24 = 16777216.0f;
-constexpr float kFresh = 4.0f;             // and of a row's largest when its reference moves
 
 template <int G>
 struct ChunkShape {
@@ -61,7 +55,7 @@ struct ChunkShape {
     static constexpr int raw_at = q2_at + (q2_in_smem ? kblocks * 128 * 128 : 0);
     static constexpr int scale_at = raw_at + kSlots * block_bytes;   // the dequantising warps' scaled scales
     static constexpr int scale_bytes = (16 + 6) * 16 * G;            // 3 fp16 pairs of 4 a key scale, 3 rows of values'
-    static constexpr int meta_at = scale_at + kDequantWarps * scale_bytes;       // [tile % 4][block] (2^kk, kt, 2^-kt, 0)
+    static constexpr int meta_at = scale_at + kDequantWarps * scale_bytes;       // [tile % kMetas][block] (2^kk, kt, 2^-kt, 0)
     static constexpr int bars_at = meta_at + kMetas * kTileBlocks * 16;
     static constexpr int flags_at = bars_at + (kSlots + 4 * kStages + 8) * 8;
     static constexpr int bytes = flags_at + 16;
@@ -72,98 +66,6 @@ struct ChunkShape {
     static constexpr int p_col = 128, q_col = 192, o_col = 256, q2_col = 448;
     static_assert(q2_in_smem || (o_col + 2 * D <= q2_col && q2_col + D / 2 <= 512), "tensor memory");
 };
-
-// One operand row's 16-byte chunk (8 elements from element 8 * c) in 128-byte swizzle.
-__device__ __forceinline__ uint32_t operand_chunk(int row, int c, int rows)
-{
-    return static_cast<uint32_t>((c >> 3) * rows * 128 + row * 128 + (((c & 7) ^ (row & 7)) << 4));
-}
-
-__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
-{
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
-}
-
-__device__ __forceinline__ void sts32(uint32_t addr, uint32_t a)
-{
-    asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(a) : "memory");
-}
-
-__device__ __forceinline__ uint32_t lds32(uint32_t addr)
-{
-    uint32_t r;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r) : "r"(addr));
-    return r;
-}
-
-__device__ __forceinline__ uint32_t lds16(uint32_t addr)
-{
-    uint16_t r;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(r) : "r"(addr));
-    return r;
-}
-
-__device__ __forceinline__ void lds128(uint32_t (&w)[4], uint32_t addr)
-{
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                 : "r"(addr));
-}
-
-// a * b + c on fp16 pairs, rounded once, subnormals kept.
-__device__ __forceinline__ uint32_t fma_half2(uint32_t a, uint32_t b, uint32_t c)
-{
-    uint32_t r;
-    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
-    return r;
-}
-
-__device__ __forceinline__ void lds64(uint32_t &a, uint32_t &b, uint32_t addr)
-{
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(a), "=r"(b) : "r"(addr));
-}
-
-// N neighbouring words by the widest load that N allows.
-template <int N>
-__device__ __forceinline__ void lds_words(uint32_t (&w)[N], uint32_t addr)
-{
-    if constexpr (N == 4) {
-        lds128(w, addr);
-    } else if constexpr (N == 2) {
-        lds64(w[0], w[1], addr);
-    } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i) w[i] = lds32(addr + 4 * i);
-    }
-}
-
-// One thread of the warp, the same each time.
-__device__ __forceinline__ bool elect_one()
-{
-    uint32_t p;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-    return p != 0;
-}
-
-// A wait whose outcome the whole warp shares (a limit may run out for one lane and not another).
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns)
-{
-    return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, limit_ns));
-}
-
-// A 16-bit element's value.
-__device__ __forceinline__ float float_of(uint32_t bits, bool bf16)
-{
-    return bf16 ? __uint_as_float(bits << 16) : half_bits_to_float(bits);
-}
-
-// Two values as a pair of 16-bit elements.
-__device__ __forceinline__ uint32_t pack_as(float lo, float hi, bool bf16)
-{
-    if (!bf16) return pack_half(lo, hi);
-    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
 
 // Barrier addresses.
 struct Bars {
@@ -177,32 +79,6 @@ struct Bars {
     __device__ __forceinline__ uint32_t sread(int x) const { return at + 8 * (kSlots + 4 * kStages + 2 + x); }
     __device__ __forceinline__ uint32_t pfull(int x) const { return at + 8 * (kSlots + 4 * kStages + 4 + x); }
     __device__ __forceinline__ uint32_t odone(int x) const { return at + 8 * (kSlots + 4 * kStages + 6 + x); }
-};
-
-// Splits of a head that have blocks, at least one: each takes the same number.
-__device__ __forceinline__ int active_splits(const AttnArgs &a, int blocks)
-{
-    const int per = max((blocks + a.splits - 1) / a.splits, a.min_blocks);
-    return blocks > per ? (blocks + per - 1) / per : 1;
-}
-
-// What a thread block works on.
-struct Work {
-    int64_t b;
-    int hk, tile, split;
-    Sequence seq;
-    Span span;
-    int n, first, rows;          // rows of the sequence and head; this block's
-    int active;                  // splits with blocks (at least one)
-    int nblk, ntiles;            // 16-token blocks and key tiles of this split
-    int64_t blk0;                // its first block in the sequence
-    int two;                     // both row tiles hold rows
-};
-
-// One row's state.
-struct Row {
-    float m, l, to_log2;
-    int lo, hi;
 };
 
 // P of a row's 64 scores v, as fp16 pairs, and the sums of each block's 16.
@@ -309,34 +185,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttnArgs a)
     const Bars bars{sb + Sh::bars_at};
     uint32_t *flags = reinterpret_cast<uint32_t *>(sm + Sh::flags_at);     // tensor memory address, poison, dead
 
-    // unit: split, row tile, head, sequence
     asm volatile("griddepcontrol.wait;" ::: "memory");
     Work w;
-    int64_t u = blockIdx.x;
-    w.split = static_cast<int>(u % a.splits);
-    u /= a.splits;
-    w.hk = static_cast<int>(u % a.n_kv);
-    u /= a.n_kv;
-    w.tile = static_cast<int>(u % a.tiles);
-    w.b = u / a.tiles;
-    w.seq = sequence_of(a, w.b);
-    if (w.seq.bad) {
-        if (w.split == 0) poison_rows(a, w.seq, w.hk, w.tile, a.rep * D);
-        return;
-    }
-    w.n = static_cast<int>(w.seq.r1 - w.seq.r0) * a.rep;
-    w.first = w.tile * kChunkRows;
-    if (w.first >= w.n) return;
-    w.rows = min(kChunkRows, w.n - w.first);
-    w.two = w.rows > 128;
-    w.span = span_of(a, w.seq, w.first, w.rows);
-    const int per = max((w.span.blocks + a.splits - 1) / a.splits, a.min_blocks);
-    w.active = active_splits(a, w.span.blocks);
-    if (w.split >= w.active) return;
-    const int b0 = w.split * per;
-    w.nblk = min(w.span.blocks - b0, per);
-    w.ntiles = (w.nblk + kTileBlocks - 1) / kTileBlocks;
-    w.blk0 = w.span.blk_lo + b0;
+    if (!find_work(a, kChunkRows, D, w)) return;
     const int64_t base = w.blk0 * kBlockTokens;
 
     if (threadIdx.x == 0) {
@@ -710,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttnArgs a)
         float *part = nullptr;
         if (w.active > 1) {
             const int64_t group = (w.b * a.tiles + w.tile) * a.n_kv + w.hk;
-            part = a.parts + (group * a.splits + w.split) * (chunk_part_bytes(D) / 4);
+            part = a.parts + (group * a.splits + w.split) * (chunk_part_bytes(D, kChunkRows) / 4);
             if (row_in) {
                 part[kChunkRows * D + 2 * (half * 128 + my_row)] = R.m;
                 part[kChunkRows * D + 2 * (half * 128 + my_row) + 1] = R.l;
@@ -738,21 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttnArgs a)
             float x[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) x[i] = R.l == 0.0f ? 0.0f : __uint_as_float(v[i]) * inv;
-            if (!wide) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) store_float_as(a.out, to + 16 * c + i, a.out_type, x[i]);
-            } else if (a.out_type == QK_F32) {
-#pragma unroll
-                for (int i = 0; i < 16; i += 4)
-                    *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + to + 16 * c + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
-            } else {
-                const bool bf16 = a.out_type == QK_BF16;
-#pragma unroll
-                for (int i = 0; i < 16; i += 8)
-                    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + to + 16 * c + i) =
-                        make_uint4(pack_as(x[i], x[i + 1], bf16), pack_as(x[i + 2], x[i + 3], bf16),
-                                   pack_as(x[i + 4], x[i + 5], bf16), pack_as(x[i + 6], x[i + 7], bf16));
-            }
+            store16(a, to + 16 * c, x, wide);
         }
         tc_fence_before();
     }
@@ -765,22 +602,22 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttnArgs a)
 
 // Joins the splits' parts in their order: a warp 8 rows of 16 channels, a lane a row of 4; eight parts are on their way
 // at once.
-__global__ void __launch_bounds__(256) join_kernel(const AttnArgs a, int D, int64_t groups)
+__global__ void __launch_bounds__(256) join_kernel(const AttnArgs a, int D, int rows, int64_t groups)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31;
-    const int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5), group = item / (2 * D);
+    const int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5), per_group = rows / 8 * (D / 16), group = item / per_group;
     if (group >= groups) return;
-    const int at = static_cast<int>(item - group * (2 * D));
-    const int row = at % 32 * 8 + (lane & 7), vec = at / 32 * 4 + (lane >> 3);
+    const int at = static_cast<int>(item - group * per_group);
+    const int row = at % (rows / 8) * 8 + (lane & 7), vec = at / (rows / 8) * 4 + (lane >> 3);
     const int hk = static_cast<int>(group % a.n_kv), tile = static_cast<int>(group / a.n_kv % a.tiles);
     const Sequence seq = sequence_of(a, group / a.n_kv / a.tiles);
     if (seq.bad) return;
-    const int n = static_cast<int>(seq.r1 - seq.r0) * a.rep, first = tile * kChunkRows;
+    const int n = static_cast<int>(seq.r1 - seq.r0) * a.rep, first = tile * rows;
     if (first + row >= n) return;
-    const int active = active_splits(a, span_of(a, seq, first, min(kChunkRows, n - first)).blocks);
+    const int active = active_splits(a, span_of(a, seq, first, min(rows, n - first)).blocks);
     if (active <= 1) return;
-    const int64_t stride = chunk_part_bytes(D) / 4;
+    const int64_t stride = chunk_part_bytes(D, rows) / 4;
     const float *part = a.parts + group * a.splits * stride;
     float m = kNoMax, l = 0.0f, v[4] = {};
     for (int s0 = 0; s0 < active; s0 += 8) {
@@ -791,8 +628,8 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnArgs a, int D, int6
             ml[k] = make_float2(kNoMax, 0.0f), x[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             if (s0 + k < active) {
                 const float *p = part + (s0 + k) * stride;
-                ml[k] = *reinterpret_cast<const float2 *>(p + kChunkRows * D + 2 * row);
-                x[k] = *reinterpret_cast<const float4 *>(p + (vec * kChunkRows + row) * 4);
+                ml[k] = *reinterpret_cast<const float2 *>(p + rows * D + 2 * row);
+                x[k] = *reinterpret_cast<const float4 *>(p + (vec * rows + row) * 4);
             }
         }
         float top = m;
@@ -822,24 +659,24 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnArgs a, int D, int6
     }
 }
 
-template <int G>
-cudaError_t launch(const AttnArgs &a, int64_t groups, cudaStream_t st)
+}  // namespace
+
+namespace chunk {
+
+cudaError_t launch_tiles(void (*kern)(const AttnArgs), std::atomic<uint64_t> &done, int smem, int threads, const AttnArgs &a, int D,
+                         int rows, int64_t groups, cudaStream_t st)
 {
-    const auto kern = chunk_kernel<G>;
-    constexpr int smem = ChunkShape<G>::smem;
-    static_assert(smem <= 227 * 1024, "shared memory of a block");
-    static std::atomic<uint64_t> done{0};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    if (dev >= 64 || !(done.load(std::memory_order_acquire) >> dev & 1)) {
+    if (dev >= 64 || !(done.load(std::memory_order_acquire) >> dev & 1)) {      // two threads that find it undone both do it
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
         if (dev < 64) done.fetch_or(1ull << dev, std::memory_order_release);
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(groups * a.splits));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute at = {};
@@ -850,11 +687,23 @@ cudaError_t launch(const AttnArgs &a, int64_t groups, cudaStream_t st)
     e = cudaLaunchKernelEx(&cfg, kern, a);
     if (e != cudaSuccess || a.splits == 1) return e;
     // the join may be scheduled while the tiles still run: it waits for all of them
-    cfg.gridDim = dim3(static_cast<unsigned>(groups * (8 * G)));
+    cfg.gridDim = dim3(static_cast<unsigned>((groups * (rows / 8) * (D / 16) + 7) / 8));
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, join_kernel, a, 32 * G, groups);
+    return cudaLaunchKernelEx(&cfg, join_kernel, a, D, rows, groups);
+}
+
+}  // namespace chunk
+
+namespace {
+
+template <int G>
+cudaError_t launch(const AttnArgs &a, int64_t groups, cudaStream_t st)
+{
+    static std::atomic<uint64_t> done{0};
+    static_assert(ChunkShape<G>::smem <= 227 * 1024, "shared memory of a block");
+    return launch_tiles(chunk_kernel<G>, done, ChunkShape<G>::smem, kThreads, a, 32 * G, kChunkRows, groups, st);
 }
 
 }  // namespace

@@ -1,0 +1,647 @@
+// qk_attn_chunk32.cu -- attention over the 4-bit cache for many query rows a
+// key/value head with fp32 queries, on the 5th-generation tensor cores.
+//
+// A thread block takes 128 rows (queries x grouped heads) of one key/value
+// head and walks the keys in tiles of 64.  fp32 accuracy comes from operands
+// of two fp16 pieces and three of their four products:
+//   S = Q1 K1^T + Q2 K1^T + Q1 K2^T      O += P1 V1 + P2 V1 + P1 V2
+// Queries, a power of two away from themselves, are whole numbers below 2^11
+// and multiples of 2^-12; K = (n - 8) d has 15 bits, K1 its leading 11 and K2
+// exactly the rest; P1 and P2 are a probability's first and next 11 bits.  The
+// product left out is below 2^-22 of the sum's terms.
+//
+// The tensor cores cut what they add at about 2^-24 of the largest term, the
+// accumulator too, always the same way; over thousands of keys that would be
+// 2^-24 a product.  So O takes the products of kFlush tiles and is then added
+// to a second accumulator in fp32, which rounds.
+//
+// Everything but the shared-memory operands K1, K2, V1, V2 (64 KB a tile at
+// 128 channels) is in tensor memory: S 64 columns, P1, P2 32 each, Q1, Q2 and
+// both accumulators D/2 and D each, 512 at 128 channels.
+//
+// Scales, references and masks are as in the 16-bit form: K' = K 2^-kk with kk
+// from a 16-token block's largest scale, here brought to [2^10, 2^11), so that
+// scales down to 2^-24 of it keep all their bits.
+//
+// Warps: 0-3 softmax (a thread is a row), 4-10 dequantisation (each takes every
+// seventh 16-token block and copies its own raw blocks, two ahead), 11 issues
+// the MMAs.
+#include "qk_attn_chunk.cuh"
+#include "qk_internal.h"
+
+namespace qk {
+using namespace attn;
+using namespace chunk;
+namespace {
+
+constexpr int kSoftmaxWarps = 4, kDequantWarps = 7, kMmaWarp = 11;
+constexpr int kThreads = 12 * 32;       // so that a thread may have 168 registers
+constexpr int kStages = 2;                 // tiles of K' and of V'
+constexpr int kMetas = 8;                  // tiles whose exponents are kept: more than stages and tiles at work
+constexpr int kSlots = 2 * kDequantWarps;  // raw blocks in flight: two a dequantising warp, its own
+constexpr int kFlush = 4;                  // tiles whose products one accumulator takes
+
+template <int G>
+struct Shape {
+    static constexpr int D = 32 * G;
+    static constexpr int kblocks = (D + 63) / 64;                    // 64-column blocks of a K-major operand row
+    static constexpr int block_bytes = 18 * D;
+    static constexpr int k_piece = kblocks * kTile * 128;            // one piece of a tile of K'
+    static constexpr int v_piece = D * 128;                          // and of V' transposed: D rows of 64 keys
+    static constexpr int k_at = 0;
+    static constexpr int v_at = k_at + kStages * 2 * k_piece;
+    static constexpr int raw_at = v_at + kStages * 2 * v_piece;
+    static constexpr int scale_at = raw_at + kSlots * block_bytes;   // the dequantising warps' scaled scales
+    static constexpr int scale_bytes = (4 + 2) * 16 * G;             // a fp16 pair a key scale, a row of values' a group
+    static constexpr int meta_at = scale_at + kDequantWarps * scale_bytes;       // [tile % kMetas][block] (2^kk, kt, 2^-kt, 0)
+    static constexpr int bars_at = meta_at + kMetas * kTileBlocks * 16;
+    static constexpr int flags_at = bars_at + (kSlots + 4 * kStages + 4) * 8;
+    static constexpr int bytes = flags_at + 16;
+    // a warp meets every second tile or more often: no phase of a barrier that it waits for can be taken for an older
+    static_assert(kDequantWarps <= kStages * kTileBlocks && kStages >= 2, "phases");
+    static constexpr int smem = bytes + 1008;                        // the base is brought to 1024 bytes
+    static_assert(smem <= 227 * 1024, "shared memory of a block");
+    // tensor memory
+    static constexpr int p_col = 64, q_col = 128, o_col = 256, sum_col = 384;      // P: two pieces of 32; Q: two of D/2
+    static_assert(D <= 128, "tensor memory");
+};
+
+// Barrier addresses.
+struct Bars {
+    uint32_t at;
+    __device__ __forceinline__ uint32_t rfull(int i) const { return at + 8 * i; }
+    __device__ __forceinline__ uint32_t kfull(int i) const { return at + 8 * (kSlots + i); }
+    __device__ __forceinline__ uint32_t kempty(int i) const { return at + 8 * (kSlots + kStages + i); }
+    __device__ __forceinline__ uint32_t vfull(int i) const { return at + 8 * (kSlots + 2 * kStages + i); }
+    __device__ __forceinline__ uint32_t vempty(int i) const { return at + 8 * (kSlots + 3 * kStages + i); }
+    __device__ __forceinline__ uint32_t sfull() const { return at + 8 * (kSlots + 4 * kStages); }
+    __device__ __forceinline__ uint32_t sread() const { return at + 8 * (kSlots + 4 * kStages + 1); }
+    __device__ __forceinline__ uint32_t pfull() const { return at + 8 * (kSlots + 4 * kStages + 2); }
+    __device__ __forceinline__ uint32_t odone() const { return at + 8 * (kSlots + 4 * kStages + 3); }
+};
+
+__device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// m s of fp16 pairs in two pieces: the rounded product, and what it left (exact).
+__device__ __forceinline__ void two_pieces(uint32_t m, uint32_t s, uint32_t &lead, uint32_t &rest)
+{
+    lead = mul_half2(m, s);
+    rest = fma_half2(m, s, lead ^ 0x80008000u);
+}
+
+// P of a row's 64 scores v in two fp16 pieces, and the sums of each block's 16.
+template <bool MASK>
+__device__ __forceinline__ void exponents64(const Row &R, const uint32_t (&v)[2][32], const float (&f)[4], const float (&kt)[4],
+                                            int key0, uint32_t (&p1)[32], uint32_t (&p2)[32], float (&sum)[4])
+{
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+        const float at = kt[b] - R.m;
+        const uint64_t f2 = pack2f(f[b], f[b]), at2 = pack2f(at, at);
+        uint64_t total = 0;      // two zeros
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int c = 16 * b + 2 * i;
+            float2 z = unpack2f(fma_f32x2(pack2(v[c >> 5][c & 31], v[c >> 5][(c & 31) + 1]), f2, at2));
+            if (MASK) {
+                if (key0 + c < R.lo || key0 + c >= R.hi) z.x = -INFINITY;
+                if (key0 + c + 1 < R.lo || key0 + c + 1 >= R.hi) z.y = -INFINITY;
+            }
+            z.x = ex2(z.x), z.y = ex2(z.y);
+            total = add_f32x2(total, pack2f(z.x, z.y));
+            // the leading 11 bits, and what rounding to them left, itself to 11 (nothing below 2^-25 counts)
+            const uint32_t lead = pack_half(z.x, z.y);
+            const float2 l = __half22float2(*reinterpret_cast<const __half2 *>(&lead));
+            p1[8 * b + i] = lead;
+            p2[8 * b + i] = pack_half(z.x - l.x, z.y - l.y);
+        }
+        const float2 t = unpack2f(total);
+        sum[b] = t.x + t.y;
+    }
+}
+
+// The accumulators of 16 channels scaled by a factor.
+__device__ __forceinline__ void scale16(uint32_t addr, float factor)
+{
+    uint32_t w[16];
+    tmem_ld_32x32b_x16(addr, w);
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * factor);
+    tmem_st_32x32b_x16(addr, w);
+}
+
+// A row's 64 scores of one key tile to probabilities.  Returns false if the
+// wait for the last tile's products (which read P and form O) ran out.
+template <int G, bool MASK>
+__device__ __forceinline__ bool softmax_tile(Row &R, uint32_t tmem, uint32_t meta, int key0, const Bars &bars, int tile,
+                                             uint64_t wait_ns, int lane)
+{
+    using Sh = Shape<G>;
+    constexpr int D = Sh::D;
+    uint32_t v[2][32];
+    tmem_ld_32x32b_x32(tmem, v[0]);
+    tmem_ld_32x32b_x32(tmem + 32, v[1]);
+    float f[4], kt[4], inv[4];
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+        uint32_t w[4];
+        lds128(w, meta + 16 * b);
+        f[b] = R.to_log2 * __uint_as_float(w[0]);
+        kt[b] = __uint_as_float(w[1]);
+        inv[b] = __uint_as_float(w[2]);
+    }
+    tmem_ld_wait();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bars.sread());          // the next scores may come
+    uint32_t p1[32], p2[32];
+    float sum[4];
+    exponents64<MASK>(R, v, f, kt, key0, p1, p2, sum);
+    if (tile > 0 && !warp_wait(bars.odone(), (tile - 1) & 1, wait_ns)) return false;
+    tc_fence_after();
+    if (tile > 0 && tile % kFlush == 0) {
+#pragma unroll 2
+        for (int c = 0; c < D / 16; ++c) {
+            uint32_t w[16], s[16];
+            tmem_ld_32x32b_x16(tmem + Sh::o_col + 16 * c, w);
+            if (tile > kFlush) tmem_ld_32x32b_x16(tmem + Sh::sum_col + 16 * c, s);
+            tmem_ld_wait();
+            if (tile > kFlush) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) + __uint_as_float(s[i]));
+            }
+            tmem_st_32x32b_x16(tmem + Sh::sum_col + 16 * c, w);
+        }
+        tmem_st_wait();
+    }
+    const float most = fmaxf(fmaxf(sum[0], sum[1]), fmaxf(sum[2], sum[3]));
+    if (__any_sync(0xFFFFFFFFu, most > kMost)) {
+        // rows past the limit take a new reference; what they have so far is scaled to it
+        float factor = 1.0f;
+        if (most > kMost) {
+            float top = kNoMax;
+#pragma unroll
+            for (int i = 0; i < 64; ++i) {
+                const float y = fmaf(__uint_as_float(v[i >> 5][i & 31]), f[i >> 4], kt[i >> 4]);
+                if (!MASK || (key0 + i >= R.lo && key0 + i < R.hi)) top = fmaxf(top, y);
+            }
+            const float m = ceilf(top) - kFresh;
+            factor = ex2(R.m - m);
+            R.m = m;
+            R.l *= factor;
+        }
+        exponents64<MASK>(R, v, f, kt, key0, p1, p2, sum);
+        for (int c = 0; c < D / 16; ++c) {
+            if (tile % kFlush != 0) scale16(tmem + Sh::o_col + 16 * c, factor);
+            if (tile >= kFlush) scale16(tmem + Sh::sum_col + 16 * c, factor);
+        }
+    }
+#pragma unroll
+    for (int b = 0; b < 4; ++b) R.l = fmaf(sum[b], inv[b], R.l);
+    tmem_st_32x32b_x32(tmem + Sh::p_col, p1);
+    tmem_st_32x32b_x32(tmem + Sh::p_col + 32, p2);
+    tmem_st_wait();
+    tc_fence_before();
+    return true;
+}
+
+// 32 channels of a row; wide: 16 bytes a load.
+__device__ __forceinline__ void load32(float (&x)[32], const float *from, bool in, bool wide)
+{
+    if (wide) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float4 v = in ? __ldg(reinterpret_cast<const float4 *>(from) + i) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x[i] = in ? __ldg(from + i) : 0.0f;
+    }
+}
+
+template <int G>
+__global__ void __launch_bounds__(kThreads, 1) chunk32_kernel(const AttnArgs a)
+{
+    using Sh = Shape<G>;
+    constexpr int D = Sh::D;
+    extern __shared__ uint8_t smem_raw[];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    uint8_t *sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    const uint32_t sb = smem_u32(sm);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const Bars bars{sb + Sh::bars_at};
+    uint32_t *flags = reinterpret_cast<uint32_t *>(sm + Sh::flags_at);     // tensor memory address, poison, dead
+
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    Work w;
+    if (!find_work(a, kChunkRows32, D, w)) return;
+    const int64_t base = w.blk0 * kBlockTokens;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kSlots; ++i) mbar_init(bars.rfull(i), 1);
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(bars.kfull(i), kTileBlocks), mbar_init(bars.kempty(i), 1);
+            mbar_init(bars.vfull(i), kTileBlocks), mbar_init(bars.vempty(i), 1);
+        }
+        mbar_init(bars.sfull(), 1), mbar_init(bars.sread(), kSoftmaxWarps);
+        mbar_init(bars.pfull(), kSoftmaxWarps), mbar_init(bars.odone(), 1);
+        flags[1] = flags[2] = 0;
+        fence_barrier_init();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc_1(sb + Sh::flags_at, 512);
+        tmem_relinquish_1();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = __reduce_or_sync(0xFFFFFFFFu, flags[0]);      // in a uniform register
+
+    // softmax threads: their row of Q, scaled by a power of two to [2^10, 2^11), in two pieces, channels 0 4 1 5 2 6 3 7
+    // of each eight (the order in which masks take a word's nibbles apart), to tensor memory
+    Row R{kNoMax, 0.0f, 1.2e-38f, 0, INT32_MAX};
+    const bool softmax_warp = warp < kSoftmaxWarps;
+    const uint32_t mine_tmem = tmem + (static_cast<uint32_t>(warp & 3) << 21);       // 32 lanes a warp, lane in bits 16..
+    const int my_row = threadIdx.x;
+    const bool row_in = softmax_warp && my_row < w.rows;
+    int64_t row_token = 0, row_head = 0;
+    if (softmax_warp) {
+        const int row = w.first + my_row, i = row_in ? row / a.rep : 0;
+        row_token = w.seq.r0 + i;
+        row_head = static_cast<int64_t>(w.hk) * a.rep + (row_in ? row - i * a.rep : 0);
+        const float *from = static_cast<const float *>(a.q) + row_token * a.ldq + row_head * D;
+        const bool wide = ((reinterpret_cast<uintptr_t>(a.q) | 4 * a.ldq) & 15) == 0;
+        float big = 0.0f;
+#pragma unroll
+        for (int c = 0; c < G; ++c) {
+            float x[32];
+            load32(x, from + 32 * c, row_in, wide);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) big = fmaxf(big, fabsf(x[k]));
+        }
+        int e = 127;
+        if (big > 0.0f && big < INFINITY) e = 127 + 10 - (static_cast<int>(__float_as_uint(big) >> 23) - 127);
+        e = min(e, 250);
+        const float up = copysignf(__uint_as_float(static_cast<uint32_t>(e) << 23), a.scale_log2);
+        R.to_log2 = fmaxf(a.scale_log2 / up, 1.2e-38f);
+        if (row_in) {
+            const int64_t pos = w.seq.len - (w.seq.r1 - w.seq.r0) + i;
+            R.lo = clamp_key(a.window > 0 ? pos - a.window + 1 - base : -1);
+            R.hi = clamp_key(pos + 1 - base);
+        }
+        for (int c = 0; c < G; ++c) {
+            float x[32];
+            load32(x, from + 32 * c, row_in, wide);
+            uint32_t q1[16], q2[16];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float lead[2], rest[2];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float v = x[8 * k + j + 4 * h] * up;
+                        lead[h] = rintf(v);
+                        rest[h] = rintf((v - lead[h]) * 4096.0f) * (1.0f / 4096.0f);
+                    }
+                    q1[4 * k + j] = pack_half(lead[0], lead[1]);
+                    q2[4 * k + j] = pack_half(rest[0], rest[1]);
+                }
+            tmem_st_32x32b_x16(mine_tmem + Sh::q_col + 16 * c, q1);
+            tmem_st_32x32b_x16(mine_tmem + Sh::q_col + D / 2 + 16 * c, q2);
+        }
+        tmem_st_wait();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    bool dead = false, poison = false;
+
+    if (warp == kMmaWarp) {
+        // ------------------------------------------------ the MMAs, by one elected thread; the warp waits together
+        if (w.ntiles > 0) {
+            constexpr uint32_t idesc_s = idesc_f16_f32(128, kTile), idesc_o = idesc_f16_f32(128, D);
+            const uint32_t p_col = tmem + Sh::p_col, q_col = tmem + Sh::q_col, o_col = tmem + Sh::o_col;
+            // the small products first
+            auto scores = [&](int stage) {
+                const uint64_t k0 = smem_desc_sw128_kmajor(sb + Sh::k_at + stage * 2 * Sh::k_piece);
+                if (elect_one()) {
+#pragma unroll
+                    for (int x = 0; x < 3; ++x) {
+                        const uint32_t q = q_col + (x == 1 ? D / 2 : 0);
+                        const uint64_t kx = k0 + (x == 0 ? Sh::k_piece / 16 : 0);
+#pragma unroll
+                        for (int k = 0; k < D / 16; ++k)
+                            tc_mma_f16_tmem_a(tmem, q + 8 * k, kx + (k >> 2) * (kTile * 128 / 16) + (k & 3) * 2, idesc_s, x > 0 || k > 0);
+                    }
+                    tc_commit_1(bars.sfull());
+                    tc_commit_1(bars.kempty(stage));
+                }
+                __syncwarp();
+            };
+            dead = !warp_wait(bars.kfull(0), 0, a.wait_ns);
+            tc_fence_after();
+            if (!dead) scores(0);
+            for (int i = 0; i < w.ntiles && !dead; ++i) {
+                const int stage = i % kStages, next = (i + 1) % kStages;
+                if (i + 1 < w.ntiles) {         // the next scores, once these have been read
+                    if (!warp_wait(bars.kfull(next), ((i + 1) / kStages) & 1, a.wait_ns) ||
+                        !warp_wait(bars.sread(), i & 1, a.wait_ns)) { dead = true; break; }
+                    tc_fence_after();
+                    scores(next);
+                }
+                if (!warp_wait(bars.vfull(stage), (i / kStages) & 1, a.wait_ns) || !warp_wait(bars.pfull(), i & 1, a.wait_ns)) {
+                    dead = true;
+                    break;
+                }
+                tc_fence_after();
+                const uint64_t v0 = smem_desc_sw128_kmajor(sb + Sh::v_at + stage * 2 * Sh::v_piece);
+                if (elect_one()) {
+#pragma unroll
+                    for (int x = 0; x < 3; ++x) {
+                        const uint32_t p = p_col + (x == 1 ? 32 : 0);
+                        const uint64_t vx = v0 + (x == 0 ? Sh::v_piece / 16 : 0);
+#pragma unroll
+                        for (int k = 0; k < kTile / 16; ++k)
+                            tc_mma_f16_tmem_a(o_col, p + 8 * k, vx + 2 * k, idesc_o, i % kFlush != 0 || x > 0 || k > 0);
+                    }
+                    tc_commit_1(bars.odone());
+                    tc_commit_1(bars.vempty(stage));
+                }
+                __syncwarp();
+            }
+        }
+    } else if (!softmax_warp) {
+        // ------------------------------------------------ dequantisation: block j of the split, 16 tokens
+        const int r8 = lane >> 2, c = lane & 3, swap = G % 2 == 0 ? r8 & 1 : 0;
+        // scales: group sg of tokens st, st + 1
+        const int sg = lane % G, st = 2 * (lane / G);
+        const bool scale_lane = lane < 8 * G;
+        // keys: tokens key_token + 2h; where their 16-byte chunk of group 0 (1, with swap) lies among the block's rows
+        const int key_token = 4 * (r8 >> 1) + (r8 & 1);
+        uint32_t key_at[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            key_at[h] = key_token * 128 + (((4 * swap + c) ^ ((key_token + 2 * h) & 7)) << 4);
+        // values: an item is (g, r, half of the block's tokens): 4 words, channels 32g + 4r + j, 8 tokens a chunk; the items
+        // of a quarter of the warp start at other j, so that they too write all eight columns
+        constexpr int kItems = (16 * G + 31) / 32;
+        const int vr = G == 3 ? (lane >> 1) & 7 : lane >> 2, kp = G == 3 ? lane & 1 : (lane >> 1) & 1;
+        const int turn = G == 3 ? (vr >> 1) & 1 : lane & 1, shift = 8 * turn;
+        const uint32_t value_at = (4 * vr + 2 * turn) * 128 + (((4 * vr + 2 * turn) & 7) << 4);
+        auto group_of = [&](int k) { return G == 3 ? 2 * k + (lane >> 4) : kItems * (lane & 1) + k; };
+        const int me = warp - kSoftmaxWarps;
+        const uint32_t scales = sb + Sh::scale_at + me * Sh::scale_bytes;      // keys [token][G], values [G][token]
+        const int all_lo = clamp_key(w.span.key_lo - base), all_hi = clamp_key(w.span.key_hi - base);
+        // this warp's blocks are number me, me + 7, ..; its n-th goes to slot me + 7 (n % 2).  A lane holds the address
+        // of one of the next 32
+        const int mine = w.nblk > me ? (w.nblk - me + kDequantWarps - 1) / kDequantWarps : 0;
+        const uint64_t policy = l2_evict_first_policy();
+        const uint8_t *addr = a.pages;
+        auto copy = [&](int n) {
+            if (n >= mine) return;
+            if ((n & 31) == 0) {
+                addr = a.pages;
+                if (n + lane < mine) {
+                    const int64_t blk = w.blk0 + me + kDequantWarps * (n + lane), pg = blk / a.page_blocks;
+                    const int32_t page = a.page_table[w.b * a.ld_pages + pg];
+                    if (page < 0 || page >= a.n_pages) {
+                        poison = true;
+                        record_error(a.err, kErrBadIndex);
+                    } else {
+                        addr += ((static_cast<int64_t>(page) * a.n_kv + w.hk) * a.page_blocks + (blk - pg * a.page_blocks)) *
+                                static_cast<int64_t>(Sh::block_bytes);
+                    }
+                }
+            }
+            if (lane == (n & 31) && !(me + kDequantWarps * n == a.skip_block && blockIdx.x == 0)) {
+                const int slot = me + kDequantWarps * (n & 1);
+                mbar_arrive_expect_tx(bars.rfull(slot), Sh::block_bytes);
+                bulk_g2s(sb + Sh::raw_at + slot * Sh::block_bytes, addr, Sh::block_bytes, bars.rfull(slot), policy);
+            }
+        };
+        copy(0);
+        copy(1);
+        int n = 0;
+        for (int j = me; j < w.ntiles * kTileBlocks; j += kDequantWarps, ++n) {
+            const int i = j / kTileBlocks, bi = j % kTileBlocks;      // key tile, block of it
+            const bool have = j < w.nblk;
+            const int slot = me + kDequantWarps * (n & 1);
+            const uint32_t raw = sb + Sh::raw_at + slot * Sh::block_bytes;
+            if (have && !warp_wait(bars.rfull(slot), (n >> 1) & 1, a.wait_ns)) { dead = true; break; }
+            // scales: a lane has those of one group g of two neighbouring tokens
+            uint32_t dk[2] = {0, 0}, dv[2] = {0, 0}, top_k = 0, top_v = 0, odd = 0;
+            const bool inner = have && j * kBlockTokens >= all_lo && (j + 1) * kBlockTokens <= all_hi;
+            if (scale_lane) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int key = j * kBlockTokens + st + e;
+                    if (inner || (have && key >= all_lo && key < all_hi)) {
+                        dk[e] = lds16(raw + 16 * D + 2 * ((st + e) * G + sg));
+                        dv[e] = lds16(raw + 17 * D + 2 * ((st + e) * G + sg));
+                    }
+                    if ((dk[e] & 0x7C00u) != 0x7C00u) top_k = max(top_k, dk[e] & 0x7FFFu);
+                    if ((dv[e] & 0x7C00u) != 0x7C00u) top_v = max(top_v, dv[e] & 0x7FFFu);
+                    else odd |= 1 << e;
+                }
+            }
+            top_k = redux_max_u32(0xFFFFFFFFu, top_k);
+            top_v = redux_max_u32(0xFFFFFFFFu, top_v);
+            // largest scale in [2^e, 2^(e+1)), a subnormal or 0 counts as 2^-15; brought to [2^10, 2^11)
+            const int ek = static_cast<int>(top_k >> 10) - 15;
+            const int ev = static_cast<int>(top_v >> 10) - 15;
+            const float down_k = __uint_as_float(static_cast<uint32_t>(127 - ek + 10) << 23);
+            const float down_v = __uint_as_float(static_cast<uint32_t>(127 - ev + 10) << 23);
+            if (scale_lane) {
+                float sv[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float sk = half_bits_to_float(dk[e]) * down_k;
+                    // a value scale that is not finite counts as 0, and makes the key's scores NaN (below), and with
+                    // them the rows that see it
+                    sv[e] = odd >> e & 1 ? 0.0f : half_bits_to_float(dv[e]) * down_v;
+                    sts32(scales + 4 * ((st + e) * G + sg), pack_half(sk, sk));
+                }
+                sts32(scales + 64 * G + 2 * (16 * sg + st), pack_half(sv[0], sv[1]));
+            }
+            if (lane == 0)
+                sts128(sb + Sh::meta_at + (i % kMetas * kTileBlocks + bi) * 16, static_cast<uint32_t>(127 + ek - 10) << 23,
+                       __float_as_uint(static_cast<float>(ev - 10)), __float_as_uint(down_v), 0u);
+            __syncwarp();
+            if (__any_sync(0xFFFFFFFFu, odd)) {
+                for (int e = 0; e < 2; ++e)
+                    if (odd >> e & 1) sts32(scales + 4 * ((st + e) * G), 0x7FFF7FFFu);
+                __syncwarp();
+            }
+            // keys: lane (r, c) has token 4(r/2) + 2h + r%2, channels 32g + 8c..8c+7 a word
+            if (i >= kStages && !warp_wait(bars.kempty(i % kStages), (i / kStages - 1) & 1, a.wait_ns)) { dead = true; break; }
+            const uint32_t kb = sb + Sh::k_at + i % kStages * 2 * Sh::k_piece + bi * kBlockTokens * 128;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t words[G];
+                lds_words<G>(words, raw + h * 128 * G + lane * 4 * G);
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+                    // odd r take the groups in pairs the other way round: a quarter of the warp then writes all eight
+                    // 16-byte columns
+                    const uint32_t word = G % 2 == 0 && swap ? words[g ^ (G % 2 == 0)] : words[g], high = word >> 8;
+                    const uint32_t s = lds32(scales + 4 * ((key_token + 2 * h) * G + (g ^ swap)));
+                    const uint32_t m[4] = {signed_nibbles<0>(word), signed_nibbles<1>(word), signed_nibbles<0>(high), signed_nibbles<1>(high)};
+                    uint32_t lead[4], rest[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) two_pieces(m[k], s, lead[k], rest[k]);
+                    // chunk 4 (g ^ swap) + c of row t, 16 bytes each: its column of 8 is xored with t % 8
+                    const uint32_t at = kb + (g >> 1) * (kTile * 128) + h * 256 + (key_at[h] ^ ((g & 1) << 6));
+                    sts128(at, lead[0], lead[1], lead[2], lead[3]);
+                    sts128(at + Sh::k_piece, rest[0], rest[1], rest[2], rest[3]);
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bars.kfull(i % kStages));
+            if (i >= kStages && !warp_wait(bars.vempty(i % kStages), (i / kStages - 1) & 1, a.wait_ns)) { dead = true; break; }
+            const uint32_t vb = sb + Sh::v_at + i % kStages * 2 * Sh::v_piece, column = (2 * bi + kp) << 4;
+#pragma unroll
+            for (int k = 0; k < kItems; ++k) {
+                const int g = group_of(k);
+                if (G != 3 || g < G) {
+                    uint32_t words[4], s[4];      // tokens 8kp + 0,1 | 2,3 | 4,5 | 6,7
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        words[e] = lds32(raw + 8 * D + (e & 1) * 128 * G + (vr * 4 + 2 * kp + (e >> 1)) * 4 * G + 4 * g);
+                    lds128(s, scales + 64 * G + 2 * (16 * g + 8 * kp));
+#pragma unroll
+                    for (int half_j = 0; half_j < 2; ++half_j) {
+                        uint32_t src[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) src[e] = words[e] >> (half_j ? 8 - shift : shift);
+                        // row 32g + 4r + j with j = 2 (half_j ^ turn) + jj, its columns xored with row % 8
+                        const uint32_t row = g * 4096 + (value_at ^ (half_j ? 256 + 32 : 0));
+#pragma unroll
+                        for (int jj = 0; jj < 2; ++jj) {
+                            uint32_t lead[4], rest[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                two_pieces(jj ? signed_nibbles<1>(src[e]) : signed_nibbles<0>(src[e]), s[e], lead[e], rest[e]);
+                            const uint32_t at = vb + ((row ^ (jj ? 128 + 16 : 0)) ^ column);
+                            sts128(at, lead[0], lead[1], lead[2], lead[3]);
+                            sts128(at + Sh::v_piece, rest[0], rest[1], rest[2], rest[3]);
+                        }
+                    }
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bars.vfull(i % kStages));
+            copy(n + 2);       // into the slot just read
+        }
+        // copies still in flight when a wait ran out are waited for before the block ends
+        if (dead)
+            for (int k = n; k < n + 2 && k < mine; ++k)
+                mbar_wait(bars.rfull(me + kDequantWarps * (k & 1)), (k >> 1) & 1, a.wait_ns);
+        if (__any_sync(0xFFFFFFFFu, poison) && lane == 0) flags[1] = 1;
+    } else {
+        // ------------------------------------------------ softmax: a thread is a row
+        // keys that every row sees
+        const int64_t p0 = w.seq.len - (w.seq.r1 - w.seq.r0) + w.first / a.rep;
+        const int64_t p1 = w.seq.len - (w.seq.r1 - w.seq.r0) + (w.first + w.rows - 1) / a.rep;
+        const int see_lo = clamp_key(a.window > 0 ? p1 - a.window + 1 - base : 0), see_hi = clamp_key(p0 + 1 - base);
+        for (int i = 0; i < w.ntiles; ++i) {
+            if (!warp_wait(bars.sfull(), i & 1, a.wait_ns)) { dead = true; break; }
+            tc_fence_after();
+            const int key0 = i * kTile;
+            const uint32_t meta = sb + Sh::meta_at + i % kMetas * kTileBlocks * 16;
+            const bool whole = key0 >= see_lo && key0 + kTile <= see_hi;
+            if (whole ? !softmax_tile<G, false>(R, mine_tmem, meta, key0, bars, i, a.wait_ns, lane)
+                      : !softmax_tile<G, true>(R, mine_tmem, meta, key0, bars, i, a.wait_ns, lane)) {
+                dead = true;
+                break;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bars.pfull());
+        }
+        if (w.ntiles > 0 && !dead && !warp_wait(bars.odone(), (w.ntiles - 1) & 1, a.wait_ns)) dead = true;
+        tc_fence_after();
+    }
+    if (__any_sync(0xFFFFFFFFu, dead) && lane == 0) {
+        record_error(a.err, kErrTimeout);
+        flags[2] = 1;
+    }
+    __syncthreads();
+    poison = flags[1] || flags[2];
+
+    // rows out, or to the workspace
+    if (softmax_warp) {
+        if (poison) R.l = __int_as_float(0x7FC00000);
+        float *part = nullptr;
+        if (w.active > 1) {
+            const int64_t group = (w.b * a.tiles + w.tile) * a.n_kv + w.hk;
+            part = a.parts + (group * a.splits + w.split) * (chunk_part_bytes(D, kChunkRows32) / 4);
+            if (row_in) {
+                part[kChunkRows32 * D + 2 * my_row] = R.m;
+                part[kChunkRows32 * D + 2 * my_row + 1] = R.l;
+            }
+            part += my_row * 4;       // a warp's 32 rows of four channels lie side by side
+        }
+        const bool wide = ((reinterpret_cast<uintptr_t>(a.out) | a.ldo * (a.out_type == QK_F32 ? 4 : 2)) & 15) == 0;
+        const int64_t to = row_token * a.ldo + row_head * D;
+        for (int c = 0; c < D / 16; ++c) {
+            uint32_t v[16], s[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = s[i] = 0;
+            if (w.ntiles > 0 && !flags[2]) {
+                tmem_ld_32x32b_x16(mine_tmem + Sh::o_col + 16 * c, v);
+                if (w.ntiles > kFlush) tmem_ld_32x32b_x16(mine_tmem + Sh::sum_col + 16 * c, s);
+                tmem_ld_wait();
+            }
+            if (!row_in) continue;
+            float x[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(v[i]) + __uint_as_float(s[i]);
+            if (part) {
+#pragma unroll
+                for (int i = 0; i < 16; i += 4)
+                    *reinterpret_cast<float4 *>(part + (4 * c + i / 4) * (kChunkRows32 * 4)) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+                continue;
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] = R.l == 0.0f ? 0.0f : x[i] / R.l;
+            store16(a, to + 16 * c, x, wide);
+        }
+        tc_fence_before();
+    }
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc_1(tmem, 512);
+    }
+}
+
+template <int G>
+cudaError_t launch(const AttnArgs &a, int64_t groups, cudaStream_t st)
+{
+    static std::atomic<uint64_t> done{0};
+    return launch_tiles(chunk32_kernel<G>, done, Shape<G>::smem, kThreads, a, 32 * G, kChunkRows32, groups, st);
+}
+
+}  // namespace
+
+namespace attn {
+
+cudaError_t chunk32_launch(const AttnArgs &a, int D, int64_t groups, cudaStream_t st)
+{
+    if (D == 64) return launch<2>(a, groups, st);
+    if (D == 96) return launch<3>(a, groups, st);
+    if (D == 128) return launch<4>(a, groups, st);
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace attn
+}  // namespace qk
