@@ -23,9 +23,11 @@
 // from a 16-token block's largest scale, here brought to [2^10, 2^11), so that
 // scales down to 2^-24 of it keep all their bits.
 //
-// Warps: 0-3 softmax (a thread is a row), 4-10 dequantisation (each takes every
-// seventh 16-token block and copies its own raw blocks, two ahead), 11 issues
-// the MMAs.
+// Warps: 0-7 softmax (a thread is a row and half of a tile's keys, and for the
+// accumulators half of the channels), 8-14 dequantisation (each takes every
+// seventh 16-token block and copies its own raw blocks, two ahead), 15 issues
+// the MMAs.  (With four softmax warps, a thread a whole row, the softmax took
+// 3700 cycles a tile, and the tensor cores less than half of that.)
 #include "qk_attn_chunk.cuh"
 #include "qk_internal.h"
 
@@ -34,8 +36,8 @@ using namespace attn;
 using namespace chunk;
 namespace {
 
-constexpr int kSoftmaxWarps = 4, kDequantWarps = 7, kMmaWarp = 11;
-constexpr int kThreads = 12 * 32;       // so that a thread may have 168 registers
+constexpr int kSoftmaxWarps = 8, kDequantWarps = 7, kMmaWarp = 15;
+constexpr int kThreads = 16 * 32;
 constexpr int kStages = 2;                 // tiles of K' and of V'
 constexpr int kMetas = 8;                  // tiles whose exponents are kept: more than stages and tiles at work
 constexpr int kSlots = 2 * kDequantWarps;  // raw blocks in flight: two a dequantising warp, its own
@@ -56,7 +58,8 @@ struct Shape {
     static constexpr int meta_at = scale_at + kDequantWarps * scale_bytes;       // [tile % kMetas][block] (2^kk, kt, 2^-kt, 0)
     static constexpr int bars_at = meta_at + kMetas * kTileBlocks * 16;
     static constexpr int flags_at = bars_at + (kSlots + 4 * kStages + 4) * 8;
-    static constexpr int bytes = flags_at + 16;
+    static constexpr int rows_at = flags_at + 16;                    // a float of each row's two threads
+    static constexpr int bytes = rows_at + 2 * kChunkRows32 * 4;
     // a warp meets every second tile or more often: no phase of a barrier that it waits for can be taken for an older
     static_assert(kDequantWarps <= kStages * kTileBlocks && kStages >= 2, "phases");
     static constexpr int smem = bytes + 1008;                        // the base is brought to 1024 bytes
@@ -94,20 +97,31 @@ __device__ __forceinline__ void two_pieces(uint32_t m, uint32_t s, uint32_t &lea
     rest = fma_half2(m, s, lead ^ 0x80008000u);
 }
 
-// P of a row's 64 scores v in two fp16 pieces, and the sums of each block's 16.
+// Whether `over` is true in any softmax thread; all of them call it.
+__device__ __forceinline__ bool any_softmax(bool over)
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\tbarrier.cta.red.or.pred p, 1, %2, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(r)
+                 : "r"(static_cast<uint32_t>(over)), "n"(kSoftmaxWarps * 32)
+                 : "memory");
+    return r != 0;
+}
+
+// P of 32 scores v of a row in two fp16 pieces, and the sums of each block's 16.
 template <bool MASK>
-__device__ __forceinline__ void exponents64(const Row &R, const uint32_t (&v)[2][32], const float (&f)[4], const float (&kt)[4],
-                                            int key0, uint32_t (&p1)[32], uint32_t (&p2)[32], float (&sum)[4])
+__device__ __forceinline__ void exponents32(const Row &R, const uint32_t (&v)[32], const float (&f)[2], const float (&kt)[2],
+                                            int key0, uint32_t (&p1)[16], uint32_t (&p2)[16], float (&sum)[2])
 {
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
+    for (int b = 0; b < 2; ++b) {
         const float at = kt[b] - R.m;
         const uint64_t f2 = pack2f(f[b], f[b]), at2 = pack2f(at, at);
         uint64_t total = 0;      // two zeros
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int c = 16 * b + 2 * i;
-            float2 z = unpack2f(fma_f32x2(pack2(v[c >> 5][c & 31], v[c >> 5][(c & 31) + 1]), f2, at2));
+            float2 z = unpack2f(fma_f32x2(pack2(v[c], v[c + 1]), f2, at2));
             if (MASK) {
                 if (key0 + c < R.lo || key0 + c >= R.hi) z.x = -INFINITY;
                 if (key0 + c + 1 < R.lo || key0 + c + 1 >= R.hi) z.y = -INFINITY;
@@ -136,22 +150,20 @@ __device__ __forceinline__ void scale16(uint32_t addr, float factor)
     tmem_st_32x32b_x16(addr, w);
 }
 
-// A row's 64 scores of one key tile to probabilities.  Returns false if the
-// wait for the last tile's products (which read P and form O) ran out.
+// 32 of a row's 64 scores of one key tile to probabilities.  All softmax threads call it together; ok: this warp's
+// waits so far have not run out.  Returns false if any thread's have.
 template <int G, bool MASK>
-__device__ __forceinline__ bool softmax_tile(Row &R, uint32_t tmem, uint32_t meta, int key0, const Bars &bars, int tile,
-                                             uint64_t wait_ns, int lane)
+__device__ __forceinline__ bool softmax_tile(Row &R, uint32_t tmem, int half, uint32_t meta, float *rows, int key0,
+                                             const Bars &bars, int tile, uint64_t wait_ns, int lane, bool ok)
 {
     using Sh = Shape<G>;
-    constexpr int D = Sh::D;
-    uint32_t v[2][32];
-    tmem_ld_32x32b_x32(tmem, v[0]);
-    tmem_ld_32x32b_x32(tmem + 32, v[1]);
-    float f[4], kt[4], inv[4];
+    uint32_t v[32];
+    tmem_ld_32x32b_x32(tmem + 32 * half, v);
+    float f[2], kt[2], inv[2];
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
+    for (int b = 0; b < 2; ++b) {
         uint32_t w[4];
-        lds128(w, meta + 16 * b);
+        lds128(w, meta + 16 * (2 * half + b));
         f[b] = R.to_log2 * __uint_as_float(w[0]);
         kt[b] = __uint_as_float(w[1]);
         inv[b] = __uint_as_float(w[2]);
@@ -160,52 +172,64 @@ __device__ __forceinline__ bool softmax_tile(Row &R, uint32_t tmem, uint32_t met
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(bars.sread());          // the next scores may come
-    uint32_t p1[32], p2[32];
-    float sum[4];
-    exponents64<MASK>(R, v, f, kt, key0, p1, p2, sum);
-    if (tile > 0 && !warp_wait(bars.odone(), (tile - 1) & 1, wait_ns)) return false;
+    uint32_t p1[16], p2[16];
+    float sum[2];
+    key0 += 32 * half;
+    exponents32<MASK>(R, v, f, kt, key0, p1, p2, sum);
+    // the last tile's products, which read P and form O
+    if (tile > 0) ok = warp_wait(bars.odone(), (tile - 1) & 1, wait_ns) && ok;
     tc_fence_after();
+    const float most = fmaxf(sum[0], sum[1]);
+    const bool over = any_softmax(most > kMost || !ok);
+    if (over && any_softmax(!ok)) return false;
+    const uint32_t o_addr = tmem + Sh::o_col + 16 * G * half, sum_addr = tmem + Sh::sum_col + 16 * G * half;
     if (tile > 0 && tile % kFlush == 0) {
 #pragma unroll 2
-        for (int c = 0; c < D / 16; ++c) {
+        for (int c = 0; c < G; ++c) {
             uint32_t w[16], s[16];
-            tmem_ld_32x32b_x16(tmem + Sh::o_col + 16 * c, w);
-            if (tile > kFlush) tmem_ld_32x32b_x16(tmem + Sh::sum_col + 16 * c, s);
+            tmem_ld_32x32b_x16(o_addr + 16 * c, w);
+            if (tile > kFlush) tmem_ld_32x32b_x16(sum_addr + 16 * c, s);
             tmem_ld_wait();
             if (tile > kFlush) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) + __uint_as_float(s[i]));
             }
-            tmem_st_32x32b_x16(tmem + Sh::sum_col + 16 * c, w);
+            tmem_st_32x32b_x16(sum_addr + 16 * c, w);
         }
         tmem_st_wait();
     }
-    const float most = fmaxf(fmaxf(sum[0], sum[1]), fmaxf(sum[2], sum[3]));
-    if (__any_sync(0xFFFFFFFFu, most > kMost)) {
+    if (over) {
         // rows past the limit take a new reference; what they have so far is scaled to it
-        float factor = 1.0f;
+        float top = kNoMax;
         if (most > kMost) {
-            float top = kNoMax;
 #pragma unroll
-            for (int i = 0; i < 64; ++i) {
-                const float y = fmaf(__uint_as_float(v[i >> 5][i & 31]), f[i >> 4], kt[i >> 4]);
+            for (int i = 0; i < 32; ++i) {
+                const float y = fmaf(__uint_as_float(v[i]), f[i >> 4], kt[i >> 4]);
                 if (!MASK || (key0 + i >= R.lo && key0 + i < R.hi)) top = fmaxf(top, y);
             }
+        }
+        const int row = threadIdx.x & 127;
+        rows[kChunkRows32 * half + row] = top;
+        any_softmax(false);
+        top = fmaxf(top, rows[kChunkRows32 * (1 - half) + row]);
+        any_softmax(false);          // both have read it
+        float factor = 1.0f;
+        if (top > kNoMax) {
             const float m = ceilf(top) - kFresh;
             factor = ex2(R.m - m);
             R.m = m;
             R.l *= factor;
         }
-        exponents64<MASK>(R, v, f, kt, key0, p1, p2, sum);
-        for (int c = 0; c < D / 16; ++c) {
-            if (tile % kFlush != 0) scale16(tmem + Sh::o_col + 16 * c, factor);
-            if (tile >= kFlush) scale16(tmem + Sh::sum_col + 16 * c, factor);
+        exponents32<MASK>(R, v, f, kt, key0, p1, p2, sum);
+        for (int c = 0; c < G; ++c) {
+            if (tile % kFlush != 0) scale16(o_addr + 16 * c, factor);
+            if (tile >= kFlush) scale16(sum_addr + 16 * c, factor);
         }
     }
 #pragma unroll
-    for (int b = 0; b < 4; ++b) R.l = fmaf(sum[b], inv[b], R.l);
-    tmem_st_32x32b_x32(tmem + Sh::p_col, p1);
-    tmem_st_32x32b_x32(tmem + Sh::p_col + 32, p2);
+    for (int b = 0; b < 2; ++b) R.l = fmaf(sum[b], inv[b], R.l);
+    tmem_st_32x32b_x16(tmem + Sh::p_col + 16 * half, p1);
+    tmem_st_32x32b_x16(tmem + Sh::p_col + 32 + 16 * half, p2);
     tmem_st_wait();
     tc_fence_before();
     return true;
@@ -269,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk32_kernel(const AttnArgs a)
     Row R{kNoMax, 0.0f, 1.2e-38f, 0, INT32_MAX};
     const bool softmax_warp = warp < kSoftmaxWarps;
     const uint32_t mine_tmem = tmem + (static_cast<uint32_t>(warp & 3) << 21);       // 32 lanes a warp, lane in bits 16..
-    const int my_row = threadIdx.x;
+    const int my_row = threadIdx.x & 127, half = warp >> 2;       // half: of a tile's keys, and of the channels
     const bool row_in = softmax_warp && my_row < w.rows;
     int64_t row_token = 0, row_head = 0;
     if (softmax_warp) {
@@ -296,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk32_kernel(const AttnArgs a)
             R.lo = clamp_key(a.window > 0 ? pos - a.window + 1 - base : -1);
             R.hi = clamp_key(pos + 1 - base);
         }
-        for (int c = 0; c < G; ++c) {
+        for (int c = half; c < G; c += 2) {
             float x[32];
             load32(x, from + 32 * c, row_in, wide);
             uint32_t q1[16], q2[16];
@@ -553,14 +577,15 @@ __global__ void __launch_bounds__(kThreads, 1) chunk32_kernel(const AttnArgs a)
         const int64_t p0 = w.seq.len - (w.seq.r1 - w.seq.r0) + w.first / a.rep;
         const int64_t p1 = w.seq.len - (w.seq.r1 - w.seq.r0) + (w.first + w.rows - 1) / a.rep;
         const int see_lo = clamp_key(a.window > 0 ? p1 - a.window + 1 - base : 0), see_hi = clamp_key(p0 + 1 - base);
+        float *rows = reinterpret_cast<float *>(sm + Sh::rows_at);
         for (int i = 0; i < w.ntiles; ++i) {
-            if (!warp_wait(bars.sfull(), i & 1, a.wait_ns)) { dead = true; break; }
+            const bool ok = warp_wait(bars.sfull(), i & 1, a.wait_ns);
             tc_fence_after();
             const int key0 = i * kTile;
             const uint32_t meta = sb + Sh::meta_at + i % kMetas * kTileBlocks * 16;
             const bool whole = key0 >= see_lo && key0 + kTile <= see_hi;
-            if (whole ? !softmax_tile<G, false>(R, mine_tmem, meta, key0, bars, i, a.wait_ns, lane)
-                      : !softmax_tile<G, true>(R, mine_tmem, meta, key0, bars, i, a.wait_ns, lane)) {
+            if (whole ? !softmax_tile<G, false>(R, mine_tmem, half, meta, rows, key0, bars, i, a.wait_ns, lane, ok)
+                      : !softmax_tile<G, true>(R, mine_tmem, half, meta, rows, key0, bars, i, a.wait_ns, lane, ok)) {
                 dead = true;
                 break;
             }
@@ -569,6 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk32_kernel(const AttnArgs a)
         }
         if (w.ntiles > 0 && !dead && !warp_wait(bars.odone(), (w.ntiles - 1) & 1, a.wait_ns)) dead = true;
         tc_fence_after();
+        rows[kChunkRows32 * half + my_row] = R.l;
     }
     if (__any_sync(0xFFFFFFFFu, dead) && lane == 0) {
         record_error(a.err, kErrTimeout);
@@ -579,12 +605,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk32_kernel(const AttnArgs a)
 
     // rows out, or to the workspace
     if (softmax_warp) {
-        if (poison) R.l = __int_as_float(0x7FC00000);
+        const float *rows = reinterpret_cast<const float *>(sm + Sh::rows_at);
+        R.l = poison ? __int_as_float(0x7FC00000) : rows[my_row] + rows[kChunkRows32 + my_row];
         float *part = nullptr;
         if (w.active > 1) {
             const int64_t group = (w.b * a.tiles + w.tile) * a.n_kv + w.hk;
             part = a.parts + (group * a.splits + w.split) * (chunk_part_bytes(D, kChunkRows32) / 4);
-            if (row_in) {
+            if (row_in && half == 0) {
                 part[kChunkRows32 * D + 2 * my_row] = R.m;
                 part[kChunkRows32 * D + 2 * my_row + 1] = R.l;
             }
@@ -592,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk32_kernel(const AttnArgs a)
         }
         const bool wide = ((reinterpret_cast<uintptr_t>(a.out) | a.ldo * (a.out_type == QK_F32 ? 4 : 2)) & 15) == 0;
         const int64_t to = row_token * a.ldo + row_head * D;
-        for (int c = 0; c < D / 16; ++c) {
+        for (int c = G * half; c < G * half + G; ++c) {
             uint32_t v[16], s[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) v[i] = s[i] = 0;
