@@ -4,7 +4,7 @@
 #include <atomic>
 #include <cmath>
 
-#include "qk_attn.cuh"
+#include "qk_attn_chunk.cuh"
 #include "qk_internal.h"
 
 namespace qk {
@@ -16,27 +16,31 @@ bool type_ok(int t) { return t == QK_F32 || t == QK_F16 || t == QK_BF16; }
 
 // How a call's rows and keys are cut.
 struct Cut {
-    int pieces, sets, row_tile, tiles, splits;
-    bool chunk;                      // the many-row form (qk_attn_chunk.cu)
-    int64_t cut;                     // few rows: thread blocks that share all blocks (0: one a head)
-    int64_t min_blocks, groups;      // groups: sequences * heads * tiles
+    int pieces, sets, row_tile, tiles, sms;
+    bool chunk;                      // the many-row forms (qk_attn_chunk.cuh)
+    int64_t cut;                     // thread blocks that share all blocks (0: one a head and row tile)
+    int64_t groups;                  // sequences * heads * tiles
 };
 
 std::atomic<int> g_skip_block{-1};
 
-// Rows a sequence and head from which it is taken.  Times of the few-row form and of it, us, heads of 128 in 16 bits:
-//   8 sequences of 4096 tokens, 8 heads   16 rows 29 and 45, 32 41 and 45, 48 66 and 47, 256 248 and 65
-//   1 sequence of 16384, 8 heads          16 rows 21 and 27, 32 28 and 27, 48 38 and 28, 256 170 and 34
-//   8 of 4096, 32 heads of 96             16 rows 51 and 128, 32 96 and 128, 48 178 and 129
+// Rows a sequence and head from which it is taken.  Times of the few-row form and of it, us, heads of 128:
+//   bf16, 8 sequences of 4096 tokens, 8 heads  16 rows 29 and 45, 32 41 and 45, 48 66 and 47, 256 248 and 68
+//   bf16, 1 sequence of 16384, 8 heads         16 rows 21 and 27, 32 28 and 27, 48 38 and 28, 256 170 and 42
+//   bf16, 8 of 4096, 32 heads of 96            16 rows 51 and 128, 32 96 and 128, 48 178 and 129
+//   fp32, 8 of 4096, 8 heads                   16 rows 41 and 60, 32 54 and 61, 64 106 and 64, 128 209 and 69
 constexpr int64_t kChunkFrom = 33;
 constexpr int64_t kCounters = 16384;         // ints at the start of every workspace, whatever the call
+constexpr int64_t kHead = 4 * kCounters + chunk::kPlanBytes;      // bytes before the parts
 // max_len sizes the cut; no sequence is longer than `longest`.
-Cut cut_for(int64_t B, int n_kv, int rep, int D, int64_t max_q, int64_t max_len, int64_t longest, bool fp32)
+Cut cut_for(int64_t B, int n_kv, int rep, int D, int64_t max_q, int64_t max_len, int64_t longest, int type)
 {
     Cut c{};
+    const bool fp32 = type == QK_F32;
     const int64_t rows = max_q * rep;
     int sms = 152, smem = 0;
     device_limits(&sms, &smem);
+    c.sms = sms;
     c.pieces = fp32 ? 2 : 1;
     c.chunk = rows >= kChunkFrom && D <= 128;
     // Columns of a warp's tile, in sets of 8: a block of keys is taken apart once for all of them, but the more there
@@ -50,30 +54,30 @@ Cut cut_for(int64_t B, int n_kv, int rep, int D, int64_t max_q, int64_t max_len,
         if ((fp32 && n == 2) ||
             4 * B * n_kv * ((rows * c.pieces + n * 8 - 1) / (n * 8)) >= 3 * sms * rows_blocks_per_sm(D / 32, n))
             c.sets = n;
-    c.row_tile = c.chunk ? (fp32 ? kChunkRows32 : kChunkRows) : c.sets * 8 / c.pieces;
+    c.row_tile = c.chunk ? (type == QK_BF16 ? kChunkRows : kChunkRows32) : c.sets * 8 / c.pieces;
     c.tiles = static_cast<int>((rows + c.row_tile - 1) / c.row_tile);
     c.groups = B * n_kv * c.tiles;
     const int64_t blocks = (max_len + kBlockTokens - 1) / kBlockTokens;
-    c.splits = 1;
     if (c.chunk) {
-        // rounds of one thread block an SM, of 8 blocks' keys in about 2 us and as much as 7 of them for start and end;
-        // parts of several splits are written and read again (3 TB/s) by a second kernel (5 us).  256 rows of 8 heads:
-        // 16384 keys whole 268 us, in 19 splits 34; 8 sequences of 4096 keys whole 78, in 2 splits 65, in 4 87; 1024
-        // rows, 16384 keys: in 4 splits 90, in 9 111
-        const int64_t tiles = (blocks + 7) / 8;
-        double best = 1e30;
-        for (int64_t rounds = 1, last = 0; rounds <= 8; ++rounds) {
-            int64_t s = sms * rounds / c.groups;
-            if (s * 2 > tiles) s = tiles / 2;
-            if (s < 1) s = 1;
-            if (s == last) continue;
-            last = s;
-            const double us = 2.0 * static_cast<double>((c.groups * s + sms - 1) / sms * ((tiles + s - 1) / s + 7)) +
-                              (s > 1 ? 5.0 + 3e-7 * static_cast<double>(2 * s * c.groups * chunk_part_bytes(D, c.row_tile)) : 0.0);
-            if (us < best) best = us, c.splits = static_cast<int>(s);
+        // one thread block an SM: heads are cut where they are few (and their items fit the cutting's tables), over at
+        // most two for each.  Of one sequence the lengths are known here, and whether cutting it pays
+        // (8 heads in 16 bits: 512 queries over 2048 keys whole 45 us, in two 51; 64 over 16384 whole 266 us, cut 42).
+        const int64_t items = B * c.tiles;
+        bool pays = items <= chunk::kItems && 2 * c.groups <= 3 * sms && 2 * sms <= chunk::kPlanBlocks &&
+                    c.groups * ((longest + kBlockTokens - 1) / kBlockTokens) < (1 << 30);
+        if (pays && B == 1) {
+            const int most = static_cast<int>(blocks);
+            const auto cost = [&](int k) {
+                const int per = chunk::part_of(most, k);
+                const int64_t parts = c.groups * ((most + per - 1) / per);
+                return chunk::part_cost(static_cast<float>(c.groups * blocks), static_cast<int>(parts), per, sms,
+                                        chunk_part_bytes(D, c.row_tile), k > 0);
+            };
+            bool better = false;
+            for (int k = 1; k < chunk::kCutChoices; ++k) better |= cost(k) < cost(0);
+            pays = better;
         }
-        c.min_blocks = (tiles + c.splits - 1) / c.splits * 8;
-        if (c.min_blocks < 16) c.min_blocks = 16;
+        if (pays) c.cut = 2 * sms;
         return c;
     }
     // few rows: split where heads are at most a third of the thread blocks that the GPU holds and have blocks to split,
@@ -112,10 +116,9 @@ size_t qk_attn_q4_workspace_bytes(int64_t B, int n_q_heads, int n_kv_heads, int 
         max_len <= 0 || B > INT32_MAX / max_q)
         return 0;
     size_t most = 0;
-    for (const bool fp32 : {true, false}) {
-        const Cut c = cut_for(B, n_kv_heads, n_q_heads / n_kv_heads, head_dim, max_q, max_len, max_len, fp32);
-        const size_t n = c.cut ? 4 * kCounters + c.cut * part_bytes_of(c, head_dim)
-                               : c.splits > 1 ? 4 * kCounters + c.groups * c.splits * part_bytes_of(c, head_dim) : 0;
+    for (const int type : {QK_F32, QK_F16, QK_BF16}) {
+        const Cut c = cut_for(B, n_kv_heads, n_q_heads / n_kv_heads, head_dim, max_q, max_len, max_len, type);
+        const size_t n = c.cut ? kHead + c.cut * part_bytes_of(c, head_dim) : 0;
         if (n > most) most = n;
     }
     return most;
@@ -151,13 +154,12 @@ int qk_attn_q4(const qk_kv_cache_q4 *cache, const void *q, int64_t ldq, int q_ty
         max_pages > INT32_MAX / cache->page_tokens)
         return QK_ERR_TOO_LARGE;
     const int64_t keys = max_pages * cache->page_tokens;
-    Cut cut = cut_for(B, n_kv, rep, D, max_q, max_len > 0 && max_len < keys ? max_len : keys, keys, q_type == QK_F32);
-    // as many splits, or parts of thread blocks, as the workspace holds
-    const int64_t room = workspace ? static_cast<int64_t>(workspace_bytes) - 4 * kCounters : 0;
+    Cut cut = cut_for(B, n_kv, rep, D, max_q, max_len > 0 && max_len < keys ? max_len : keys, keys, q_type);
+    // as many parts as the workspace holds
+    const int64_t room = workspace ? static_cast<int64_t>(workspace_bytes) - kHead : 0;
     const int64_t fit = room > 0 ? room / part_bytes_of(cut, D) : 0;
-    if (cut.splits > 1 && cut.splits > fit / cut.groups) cut.splits = fit / cut.groups > 1 ? static_cast<int>(fit / cut.groups) : 1;
     if (cut.cut > fit) cut.cut = fit > cut.groups ? fit : 0;
-    const int64_t grid = cut.cut ? cut.cut : cut.groups * cut.splits;
+    const int64_t grid = cut.cut ? cut.cut : cut.groups;
     if (grid > INT32_MAX) return QK_ERR_TOO_LARGE;
     AttnArgs a{};
     a.pages = static_cast<const uint8_t *>(cache->pages), a.n_pages = cache->n_pages;
@@ -168,9 +170,10 @@ int qk_attn_q4(const qk_kv_cache_q4 *cache, const void *q, int64_t ldq, int q_ty
     a.scale_log2 = static_cast<float>(scale * 1.4426950408889634074);
     a.out = out, a.ldo = ldo, a.out_type = out_type;
     a.tiles = cut.tiles, a.items = static_cast<int>(B * cut.tiles), a.cut = static_cast<int>(cut.cut);
-    a.splits = cut.splits, a.min_blocks = static_cast<int>(cut.min_blocks < INT32_MAX ? cut.min_blocks : INT32_MAX);
+    a.sms = cut.sms;
     a.counters = static_cast<int *>(workspace);
-    a.parts = reinterpret_cast<float *>(static_cast<char *>(workspace) + 4 * kCounters);
+    a.parts = reinterpret_cast<float *>(static_cast<char *>(workspace) + kHead);
+    a.plan = static_cast<char *>(workspace) + 4 * kCounters;
     a.err = library_error_word();
     a.wait_ns = library_wait_limit_ns();
     if (!a.err) return QK_ERR_CUDA;
@@ -178,7 +181,7 @@ int qk_attn_q4(const qk_kv_cache_q4 *cache, const void *q, int64_t ldq, int q_ty
     cudaError_t e = cudaErrorInvalidValue;
     a.skip_block = g_skip_block.load();
     if (cut.chunk) {
-        e = q_type == QK_F32 ? chunk32_launch(a, D, cut.groups, s) : chunk_launch(a, D, cut.groups, s);
+        e = q_type == QK_BF16 ? chunk_launch(a, D, cut.groups, s) : chunk32_launch(a, D, cut.groups, s);
         return e == cudaSuccess ? QK_OK : QK_ERR_CUDA;
     }
     switch (D) {

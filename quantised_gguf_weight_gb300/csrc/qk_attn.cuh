@@ -25,11 +25,11 @@ struct AttnArgs {
     int64_t ldo;
     int out_type;
     int tiles, items;                // row tiles a sequence, and of all sequences
-    int cut;                         // few rows: thread blocks that split heads share (0: one a head and item)
-    int splits;                      // many rows: splits of a head's blocks
-    int min_blocks;                  // blocks a split takes at least
+    int cut;                         // thread blocks that cut heads share (0: one a head and item)
+    int sms;
     int *counters;
     float *parts;
+    void *plan;                      // many rows: how the blocks are shared out
     int *err;
     uint64_t wait_ns;
     int skip_block;                  // test hook: this block of thread block 0 (its first warp's) is never copied
@@ -119,8 +119,8 @@ cudaError_t rows_launch_96(const AttnArgs &a, int pieces, int sets, int64_t grid
 cudaError_t rows_launch_128(const AttnArgs &a, int pieces, int sets, int64_t grid, cudaStream_t st);
 cudaError_t rows_launch_256(const AttnArgs &a, int pieces, int sets, int64_t grid, cudaStream_t st);
 
-// The many-row forms, on the 5th-generation tensor cores: tiles of kChunkRows rows in 16 bits (qk_attn_chunk.cu), of
-// kChunkRows32 in fp32 (qk_attn_chunk32.cu).
+// The many-row forms, on the 5th-generation tensor cores: tiles of kChunkRows rows in bf16 (qk_attn_chunk.cu), of
+// kChunkRows32 in fp32 and fp16 (qk_attn_chunk32.cu).
 constexpr int kChunkRows = 256, kChunkRows32 = 128;
 cudaError_t chunk_launch(const AttnArgs &a, int D, int64_t groups, cudaStream_t st);
 cudaError_t chunk32_launch(const AttnArgs &a, int D, int64_t groups, cudaStream_t st);

@@ -1,5 +1,5 @@
 // qk_attn_chunk.cu -- attention over the 4-bit cache for many query rows a
-// key/value head (prompt chunks) with 16-bit queries, on the 5th-generation
+// key/value head (prompt chunks) with bf16 queries, on the 5th-generation
 // tensor cores.
 //
 // A thread block takes 256 rows (queries x grouped heads) of one key/value
@@ -188,13 +188,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttnArgs a)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     Work w;
     if (!find_work(a, kChunkRows, D, w)) return;
-    const int64_t base = w.blk0 * kBlockTokens;
+    const int two = w.rows > 128;                // both row tiles hold rows
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kSlots; ++i) mbar_init(bars.rfull(i), 1);
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(bars.kfull(i), kTileBlocks), mbar_init(bars.kempty(i), 1 + w.two);
-            mbar_init(bars.vfull(i), kTileBlocks), mbar_init(bars.vempty(i), 1 + w.two);
+            mbar_init(bars.kfull(i), kTileBlocks), mbar_init(bars.kempty(i), 1 + two);
+            mbar_init(bars.vfull(i), kTileBlocks), mbar_init(bars.vempty(i), 1 + two);
         }
         for (int x = 0; x < 2; ++x) {
             mbar_init(bars.sfull(x), 1), mbar_init(bars.sread(x), 4);
@@ -219,14 +219,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttnArgs a)
     const int half = warp >> 2, my_row = threadIdx.x & 127;
     const bool softmax_warp = warp < kSoftmaxWarps;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;       // 32 lanes a warp, lane in bits 16..
-    int64_t row_token = 0, row_head = 0;
     const bool row_in = softmax_warp && half * 128 + my_row < w.rows;
-    if (softmax_warp && (half == 0 || w.two)) {
-        const int row = w.first + half * 128 + my_row;
-        const int i = row_in ? row / a.rep : 0;
-        row_token = w.seq.r0 + i;
-        row_head = static_cast<int64_t>(w.hk) * a.rep + (row_in ? row - i * a.rep : 0);
-        const int64_t at = row_token * a.ldq + row_head * D;
+    if (softmax_warp && (half == 0 || two)) {
+        const int64_t at = row_at(a, w, half * 128 + my_row, row_in, a.ldq, D);
         // the row as it is, 16 bytes a load where base and stride allow it (one element a load: 45 us more a call)
         const uint16_t *from = static_cast<const uint16_t *>(a.q) + at;
         uint32_t raw[D / 2], top = 0;
@@ -242,18 +237,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttnArgs a)
         }
 #pragma unroll
         for (int c = 0; c < D / 2; ++c) top = __vmaxu2(top, raw[c] & 0x7FFF7FFFu);
-        const bool bf16 = a.q_type == QK_BF16;
-        const float big = float_of(max(top >> 16, top & 0xFFFFu), bf16);
+        const float big = __uint_as_float(max(top >> 16, top & 0xFFFFu) << 16);
         int e = 127;
         if (big > 0.0f && big < INFINITY) e = 127 + 10 - (static_cast<int>(__float_as_uint(big) >> 23) - 127);
         e = min(e, 250);
         const float up = copysignf(__uint_as_float(static_cast<uint32_t>(e) << 23), a.scale_log2);
         R.to_log2 = fmaxf(a.scale_log2 / up, 1.2e-38f);
-        if (row_in) {
-            const int64_t pos = w.seq.len - (w.seq.r1 - w.seq.r0) + i;
-            R.lo = clamp_key(a.window > 0 ? pos - a.window + 1 - base : -1);
-            R.hi = clamp_key(pos + 1 - base);
-        }
+        if (row_in) row_keys(a, w, half * 128 + my_row, R.lo, R.hi);
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
             uint32_t q[16];
@@ -263,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttnArgs a)
 #pragma unroll
                 for (int j = 0; j < 8; j += 2) {
                     const uint32_t pair = raw[16 * c + 4 * k + j / 2];
-                    x[j] = float_of(pair & 0xFFFFu, bf16) * up, x[j + 1] = float_of(pair >> 16, bf16) * up;
+                    x[j] = __uint_as_float(pair << 16) * up, x[j + 1] = __uint_as_float(pair & 0xFFFF0000u) * up;
                 }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) q[4 * k + j] = pack_half(x[j], x[j + 4]);
@@ -290,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttnArgs a)
         // ------------------------------------------------ the MMAs of row tile x, by one elected thread; the warp waits
         // together and what the instructions take is the warp's, so that it stays in uniform registers
         const int x = warp - kMmaWarp;
-        if (w.ntiles > 0 && x <= w.two) {
+        if (w.ntiles > 0 && x <= two) {
             constexpr uint32_t idesc_s = idesc_f16_f32(128, kTile), idesc_o = idesc_f16_f32(128, D);
             const uint32_t s_col = tmem + 64 * x, p_col = tmem + Sh::p_col + 32 * x, o_col = tmem + Sh::o_col + D * x;
             auto scores = [&](int stage) {
@@ -360,7 +350,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttnArgs a)
         const uint32_t value_at = (4 * vr + 2 * turn) * 128 + (((4 * vr + 2 * turn) & 7) << 4);
         auto group_of = [&](int k) { return G == 3 ? 2 * k + (lane >> 4) : kItems * (lane & 1) + k; };
         const uint32_t scales = sb + Sh::scale_at + (warp - kSoftmaxWarps) * Sh::scale_bytes;      // keys [token][G], values [G][token]
-        const int all_lo = clamp_key(w.span.key_lo - base), all_hi = clamp_key(w.span.key_hi - base);
         // this warp's blocks are number me, me + 6, ..; its n-th goes to slot me + 6 (n % 2).  A lane holds the address
         // of one of the next 32
         const int me = warp - kSoftmaxWarps, mine = w.nblk > me ? (w.nblk - me + kDequantWarps - 1) / kDequantWarps : 0;
@@ -371,8 +360,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttnArgs a)
             if ((n & 31) == 0) {
                 addr = a.pages;
                 if (n + lane < mine) {
-                    const int64_t blk = w.blk0 + me + kDequantWarps * (n + lane), pg = blk / a.page_blocks;
-                    const int32_t page = a.page_table[w.b * a.ld_pages + pg];
+                    const int64_t blk = static_cast<int64_t>(w.blk0) + me + kDequantWarps * (n + lane), pg = blk / a.page_blocks;
+                    const int32_t page = a.page_table[static_cast<int64_t>(w.b) * a.ld_pages + pg];
                     if (page < 0 || page >= a.n_pages) {
                         poison = true;
                         record_error(a.err, kErrBadIndex);
@@ -399,12 +388,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttnArgs a)
             if (have && !warp_wait(bars.rfull(slot), (n >> 1) & 1, a.wait_ns)) { dead = true; break; }
             // scales: a lane has those of one group g of two neighbouring tokens
             uint32_t dk[2] = {0, 0}, dv[2] = {0, 0}, top_k = 0, top_v = 0, odd = 0;
-            const bool inner = have && j * kBlockTokens >= all_lo && (j + 1) * kBlockTokens <= all_hi;
+            const bool inner = have && j * kBlockTokens >= w.lo && (j + 1) * kBlockTokens <= w.hi;
             if (scale_lane) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int key = j * kBlockTokens + st + e;
-                    if (inner || (have && key >= all_lo && key < all_hi)) {
+                    if (inner || (have && key >= w.lo && key < w.hi)) {
                         dk[e] = lds16(raw + 16 * D + 2 * ((st + e) * G + sg));
                         dv[e] = lds16(raw + 17 * D + 2 * ((st + e) * G + sg));
                     }
@@ -520,15 +509,15 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttnArgs a)
             for (int k = n; k < n + 2 && k < mine; ++k)
                 mbar_wait(bars.rfull(me + kDequantWarps * (k & 1)), (k >> 1) & 1, a.wait_ns);
         if (__any_sync(0xFFFFFFFFu, poison) && lane == 0) flags[1] = 1;
-    } else if (half == 0 || w.two) {
+    } else if (half == 0 || two) {
         // ------------------------------------------------ softmax: a thread is a row
         const uint32_t s_addr = tmem + lanes + 64 * half, p_addr = tmem + lanes + Sh::p_col + 32 * half,
                        o_addr = tmem + lanes + Sh::o_col + D * half;
         // keys that every row of this tile sees
         const int last = min(w.rows, half * 128 + 128) - 1;
-        const int64_t p0 = w.seq.len - (w.seq.r1 - w.seq.r0) + (w.first + half * 128) / a.rep;
-        const int64_t p1 = w.seq.len - (w.seq.r1 - w.seq.r0) + (w.first + last) / a.rep;
-        const int see_lo = clamp_key(a.window > 0 ? p1 - a.window + 1 - base : 0), see_hi = clamp_key(p0 + 1 - base);
+        int see_lo, see_hi, none;
+        row_keys(a, w, last, see_lo, none);
+        row_keys(a, w, half * 128, none, see_hi);
         for (int i = 0; i < w.ntiles; ++i) {
             if (!warp_wait(bars.sfull(half), i & 1, a.wait_ns)) { dead = true; break; }
             tc_fence_after();
@@ -554,14 +543,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttnArgs a)
     poison = flags[1] || flags[2];
 
     // rows out, or to the workspace
-    if (softmax_warp && (half == 0 || w.two)) {
+    if (softmax_warp && (half == 0 || two)) {
         const uint32_t o_addr = tmem + lanes + Sh::o_col + D * half;
         if (poison) R.l = __int_as_float(0x7FC00000);
         const float inv = R.l == 0.0f ? 0.0f : 1.0f / R.l;
         float *part = nullptr;
         if (w.active > 1) {
-            const int64_t group = (w.b * a.tiles + w.tile) * a.n_kv + w.hk;
-            part = a.parts + (group * a.splits + w.split) * (chunk_part_bytes(D, kChunkRows) / 4);
+            part = a.parts + static_cast<int64_t>(blockIdx.x) * (chunk_part_bytes(D, kChunkRows) / 4);
             if (row_in) {
                 part[kChunkRows * D + 2 * (half * 128 + my_row)] = R.m;
                 part[kChunkRows * D + 2 * (half * 128 + my_row) + 1] = R.l;
@@ -569,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttnArgs a)
             part += (half * 128 + my_row) * 4;       // a warp's 32 rows of four channels lie side by side
         }
         const bool wide = ((reinterpret_cast<uintptr_t>(a.out) | a.ldo * (a.out_type == QK_F32 ? 4 : 2)) & 15) == 0;
-        const int64_t to = row_token * a.ldo + row_head * D;
+        const int64_t to = row_at(a, w, half * 128 + my_row, row_in, a.ldo, D);
         for (int c = 0; c < D / 16; ++c) {
             uint32_t v[16];
             if (w.ntiles > 0 && !flags[2]) {
@@ -600,25 +588,91 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttnArgs a)
     }
 }
 
-// Joins the splits' parts in their order: a warp 8 rows of 16 channels, a lane a row of 4; eight parts are on their way
-// at once.
+// The plan: a thread an item.
+__global__ void __launch_bounds__(kItems) plan_kernel(const AttnArgs a, int D, int tile_rows)
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    constexpr int kW = kItems / 32;
+    __shared__ int tops[kW], sums[kCutChoices + 1][kW], ends[kW];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int item = static_cast<int>(threadIdx.x);
+    int n = 0;
+    bool has = false;
+    if (item < a.items) {
+        const Sequence s = sequence_of(a, item / a.tiles);
+        const int at = item % a.tiles * tile_rows, rows = s.bad ? 0 : static_cast<int>(s.r1 - s.r0) * a.rep;
+        has = s.bad || at < rows;
+        if (at < rows) n = span_of(a, s, at, min(tile_rows, rows - at)).blocks;
+    }
+    int top = n, all = n;
+    top = __reduce_max_sync(0xFFFFFFFFu, top);
+    all = __reduce_add_sync(0xFFFFFFFFu, all);
+    if (lane == 0) tops[warp] = top, sums[kCutChoices][warp] = all;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kW; ++w) top = max(top, tops[w]);
+    for (int c = 0; c < kCutChoices; ++c) {
+        const int per = part_of(top, c);
+        const int parts = __reduce_add_sync(0xFFFFFFFFu, has ? max(1, (n + per - 1) / per) : 0);
+        if (lane == 0) sums[c][warp] = parts;
+    }
+    __syncthreads();
+    uint32_t key = 0xFFFFFFFFu;
+    if (lane < kCutChoices) {
+        int parts = 0;
+        float blocks = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kW; ++w) parts += sums[lane][w], blocks += static_cast<float>(sums[kCutChoices][w]);
+        parts *= a.n_kv;
+        const float cost = part_cost(blocks * a.n_kv, parts, part_of(top, lane), a.sms, chunk_part_bytes(D, tile_rows), lane > 0);
+        if (parts <= a.cut) key = (__float_as_uint(cost) & ~15u) | lane;
+    }
+    key = __reduce_min_sync(0xFFFFFFFFu, key);
+    const int per = part_of(top, static_cast<int>(key & 15u));
+    const int count = has ? max(1, (n + per - 1) / per) : 0;
+    int run = count * a.n_kv;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int below = __shfl_up_sync(0xFFFFFFFFu, run, o);
+        if (lane >= o) run += below;
+    }
+    if (lane == 31) ends[warp] = run;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) run += ends[w];
+    if (item < a.items) plan_of_items(a)[item] = make_int2(run - count * a.n_kv, count);
+    if (threadIdx.x == 0) *plan_any(a) = top > per;
+    // thread blocks: of this warp's items one after another, a lane a thread block
+    for (int from = 0; from < 32; ++from) {
+        const int parts = __shfl_sync(0xFFFFFFFFu, count, from), end = __shfl_sync(0xFFFFFFFFu, run, from);
+        for (int u = lane; u < parts * a.n_kv; u += 32)
+            plan_of_blocks(a)[end - parts * a.n_kv + u] = make_int4(32 * warp + from, u / parts, u % parts, per);
+    }
+    for (int w = warp; w < kW; ++w) run += w > warp ? ends[w] : 0;
+    const int used = __shfl_sync(0xFFFFFFFFu, run, 31);
+    for (int u = used + static_cast<int>(threadIdx.x); u < a.cut; u += kItems) plan_of_blocks(a)[u] = make_int4(-1, 0, 0, 0);
+}
+
+// Joins the parts of cut heads in their order: a warp 8 rows of 16 channels, a lane a row of 4; eight parts are on
+// their way at once.
 __global__ void __launch_bounds__(256) join_kernel(const AttnArgs a, int D, int rows, int64_t groups)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int lane = threadIdx.x & 31;
-    const int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5), per_group = rows / 8 * (D / 16), group = item / per_group;
+    if (!*plan_any(a)) return;
+    const int lane = threadIdx.x & 31, per_group = rows / 8 * (D / 16);
+    const int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5), group = item / per_group;
     if (group >= groups) return;
     const int at = static_cast<int>(item - group * per_group);
     const int row = at % (rows / 8) * 8 + (lane & 7), vec = at / (rows / 8) * 4 + (lane >> 3);
-    const int hk = static_cast<int>(group % a.n_kv), tile = static_cast<int>(group / a.n_kv % a.tiles);
-    const Sequence seq = sequence_of(a, group / a.n_kv / a.tiles);
-    if (seq.bad) return;
+    const int of = static_cast<int>(group / a.n_kv), hk = static_cast<int>(group) - of * a.n_kv, tile = of % a.tiles;
+    const int2 plan = plan_of_items(a)[of];
+    const int active = plan.y;
+    if (active <= 1) return;       // not cut, without rows, or with an index out of range
+    const Sequence seq = sequence_of(a, of / a.tiles);
     const int n = static_cast<int>(seq.r1 - seq.r0) * a.rep, first = tile * rows;
     if (first + row >= n) return;
-    const int active = active_splits(a, span_of(a, seq, first, min(rows, n - first)).blocks);
-    if (active <= 1) return;
     const int64_t stride = chunk_part_bytes(D, rows) / 4;
-    const float *part = a.parts + group * a.splits * stride;
+    const float *part = a.parts + (plan.x + hk * active) * stride;
     float m = kNoMax, l = 0.0f, v[4] = {};
     for (int s0 = 0; s0 < active; s0 += 8) {
         float2 ml[8];
@@ -675,22 +729,27 @@ cudaError_t launch_tiles(void (*kern)(const AttnArgs), std::atomic<uint64_t> &do
         if (dev < 64) done.fetch_or(1ull << dev, std::memory_order_release);
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(groups * a.splits));
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute at = {};
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &at;
     cfg.numAttrs = library_programmatic() ? 1 : 0;
+    if (a.cut) {
+        cfg.gridDim = dim3(1);
+        cfg.blockDim = dim3(kItems);
+        e = cudaLaunchKernelEx(&cfg, plan_kernel, a, D, rows);
+        if (e != cudaSuccess) return e;
+        cfg.numAttrs = 1;      // what follows may be scheduled while the last kernel still runs: it waits for all of it
+    }
+    cfg.gridDim = dim3(static_cast<unsigned>(a.cut ? a.cut : groups));
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
     e = cudaLaunchKernelEx(&cfg, kern, a);
-    if (e != cudaSuccess || a.splits == 1) return e;
-    // the join may be scheduled while the tiles still run: it waits for all of them
+    if (e != cudaSuccess || !a.cut) return e;
     cfg.gridDim = dim3(static_cast<unsigned>((groups * (rows / 8) * (D / 16) + 7) / 8));
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
-    cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, join_kernel, a, D, rows, groups);
 }
 

@@ -96,12 +96,6 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_
     return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, limit_ns));
 }
 
-// A 16-bit element's value.
-__device__ __forceinline__ float float_of(uint32_t bits, bool bf16)
-{
-    return bf16 ? __uint_as_float(bits << 16) : half_bits_to_float(bits);
-}
-
 // Two values as a pair of 16-bit elements.
 __device__ __forceinline__ uint32_t pack_as(float lo, float hi, bool bf16)
 {
@@ -110,24 +104,49 @@ __device__ __forceinline__ uint32_t pack_as(float lo, float hi, bool bf16)
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// Splits of a head that have blocks, at least one: each takes the same number.
-__device__ __forceinline__ int active_splits(const AttnArgs &a, int blocks)
+// How a call's blocks are shared out where heads are few: found on the device from the lengths by a kernel of one
+// thread block (every thread block finding it for itself cost as much, and registers).  A head of an item (a row tile of a sequence) is cut into parts of `per` 16-token blocks, each a thread
+// block's; `per` is the longest item's blocks over one of kCuts, the one whose estimated time is least: of the
+// longest part, or of all parts over the GPU, with kPartFixed blocks' time for a part's start and end (about 15 us,
+// a block 0.26 us in 16 bits, 0.35 in fp32), and for cut heads the join of the parts.
+// 8 x 64 fp32 queries over up to 5000 keys, uneven: 108 us in whole heads, 78 us so; 1 x 64 over 16384 361 and 68, in 16 bits 266
+// and 42; 8 x 64 over 4096 each in 16 bits 78 and 68, but in fp32, where nothing can be cut, 105 and 115.
+constexpr int kItems = 512;              // items of a call whose heads may be cut
+constexpr int kCutChoices = 16;
+constexpr float kPartFixed = 50.0f, kJoinFixed = 25.0f, kJoinBytes = 400.0e3f;      // in blocks; bytes a block's time
+__host__ __device__ constexpr int cut_of(int c)
 {
-    const int per = max((blocks + a.splits - 1) / a.splits, a.min_blocks);
-    return blocks > per ? (blocks + per - 1) / per : 1;
+    return c < 10 ? c + 1 : c == 10 ? 12 : c == 11 ? 14 : c == 12 ? 16 : c == 13 ? 19 : c == 14 ? 25 : 38;
+}
+__host__ __device__ inline int part_of(int longest, int c)
+{
+    const int per = ((longest + cut_of(c) - 1) / cut_of(c) + kTileBlocks - 1) / kTileBlocks * kTileBlocks;      // whole tiles
+    return per > 16 ? per : 16;
+}
+__host__ __device__ inline float part_cost(float all_blocks, int parts, int per, int sms, int64_t part_bytes, bool cut)
+{
+    const float spread = (all_blocks + kPartFixed * parts) / sms + 0.5f * per;           // uneven parts, packed
+    const float rounds = (parts + sms - 1) / sms * (all_blocks / parts + kPartFixed);      // even ones
+    const float run = parts <= sms ? per + kPartFixed : spread > rounds ? spread : rounds;
+    return run + (cut ? kJoinFixed + parts * static_cast<float>(part_bytes) / kJoinBytes : 0.0f);
 }
 
-// What a thread block works on.
+// The sharing out lies in the workspace's plan: for each thread block item, head, part and blocks a part (item -1:
+// none), for each item its first thread block and parts a head, and at the end whether any head is cut.
+constexpr int kPlanBytes = 16384, kPlanBlocks = (kPlanBytes - kItems * 8) / 16 - 1;
+__device__ __forceinline__ int4 *plan_of_blocks(const AttnArgs &a) { return static_cast<int4 *>(a.plan); }
+__device__ __forceinline__ int2 *plan_of_items(const AttnArgs &a) { return reinterpret_cast<int2 *>(plan_of_blocks(a) + kPlanBlocks); }
+__device__ __forceinline__ int *plan_any(const AttnArgs &a) { return reinterpret_cast<int *>(plan_of_items(a) + kItems); }
+
+// What a thread block works on, in few registers.  Keys and positions count from the part's first key.
 struct Work {
-    int64_t b;
-    int hk, tile, split;
-    Sequence seq;
-    Span span;
-    int n, first, rows;          // rows of the sequence and head; this block's
-    int active;                  // splits with blocks (at least one)
-    int nblk, ntiles;            // 16-token blocks and key tiles of this split
-    int64_t blk0;                // its first block in the sequence
-    int two;                     // both row tiles hold rows
+    int b, hk, first, rows;      // sequence, head; this block's rows of them
+    int active;                  // parts of the head (at least one)
+    int nblk, ntiles;            // 16-token blocks and key tiles of this part
+    int blk0;                    // its first block in the sequence
+    int r0;                      // the sequence's first row among the queries
+    int pos;                     // and its position
+    int lo, hi;                  // keys that some row sees
 };
 
 // One row's state.
@@ -136,35 +155,56 @@ struct Row {
     int lo, hi;
 };
 
-// This thread block's work: split, head, row tile, sequence.  False where it has none.
+// This thread block's work; false where it has none.
 __device__ __forceinline__ bool find_work(const AttnArgs &a, int tile_rows, int D, Work &w)
 {
-    int64_t u = blockIdx.x;
-    w.split = static_cast<int>(u % a.splits);
-    u /= a.splits;
-    w.hk = static_cast<int>(u % a.n_kv);
-    u /= a.n_kv;
-    w.tile = static_cast<int>(u % a.tiles);
-    w.b = u / a.tiles;
-    w.seq = sequence_of(a, w.b);
-    if (w.seq.bad) {
-        if (w.split == 0) poison_rows(a, w.seq, w.hk, w.tile, a.rep * D);
+    int item = static_cast<int>(blockIdx.x / a.n_kv), per = INT32_MAX;
+    w.hk = static_cast<int>(blockIdx.x) - item * a.n_kv;
+    int split = 0;
+    w.active = 1;
+    if (a.cut) {
+        const int4 mine = plan_of_blocks(a)[blockIdx.x];
+        item = mine.x;
+        if (item < 0) return false;
+        w.hk = mine.y, split = mine.z, per = mine.w;
+        w.active = plan_of_items(a)[item].y;
+    }
+    w.b = item / a.tiles;
+    const int tile = item - w.b * a.tiles;
+    const Sequence seq = sequence_of(a, w.b);
+    if (seq.bad) {
+        if (split == 0) poison_rows(a, seq, w.hk, tile, a.rep * D);
         return false;
     }
-    w.n = static_cast<int>(w.seq.r1 - w.seq.r0) * a.rep;
-    w.first = w.tile * tile_rows;
-    if (w.first >= w.n) return false;
-    w.rows = min(tile_rows, w.n - w.first);
-    w.two = w.rows > 128;
-    w.span = span_of(a, w.seq, w.first, w.rows);
-    const int per = max((w.span.blocks + a.splits - 1) / a.splits, a.min_blocks);
-    w.active = active_splits(a, w.span.blocks);
-    if (w.split >= w.active) return false;
-    const int b0 = w.split * per;
-    w.nblk = min(w.span.blocks - b0, per);
+    const int n = static_cast<int>(seq.r1 - seq.r0) * a.rep;
+    w.first = tile * tile_rows;
+    if (w.first >= n) return false;
+    w.rows = min(tile_rows, n - w.first);
+    const Span span = span_of(a, seq, w.first, w.rows);
+    const int b0 = split ? split * per : 0;
+    w.nblk = min(span.blocks - b0, per);
     w.ntiles = (w.nblk + kTileBlocks - 1) / kTileBlocks;
-    w.blk0 = w.span.blk_lo + b0;
+    w.blk0 = static_cast<int>(span.blk_lo) + b0;
+    const int64_t base = static_cast<int64_t>(w.blk0) * kBlockTokens;
+    w.r0 = static_cast<int>(seq.r0);
+    w.pos = static_cast<int>(seq.len - (seq.r1 - seq.r0) - base);
+    w.lo = clamp_key(span.key_lo - base), w.hi = clamp_key(span.key_hi - base);
     return true;
+}
+
+// Where a row of this block begins among rows of stride ld (rows beyond them: where the first does).
+__device__ __forceinline__ int64_t row_at(const AttnArgs &a, const Work &w, int row, bool in, int64_t ld, int D)
+{
+    const int r = w.first + (in ? row : 0), i = r / a.rep;
+    return (static_cast<int64_t>(w.r0) + i) * ld + (static_cast<int64_t>(w.hk) * a.rep + (r - i * a.rep)) * D;
+}
+
+// The keys that a row sees.
+__device__ __forceinline__ void row_keys(const AttnArgs &a, const Work &w, int row, int &lo, int &hi)
+{
+    const int64_t pos = static_cast<int64_t>(w.pos) + (w.first + row) / a.rep;
+    lo = clamp_key(a.window > 0 ? pos - a.window + 1 : -1);
+    hi = clamp_key(pos + 1);
 }
 
 // 16 channels of a row out; wide: 16 bytes an access.
@@ -187,7 +227,7 @@ __device__ __forceinline__ void store16(const AttnArgs &a, int64_t to, const flo
     }
 }
 
-// Launches the tiles' kernel and, where heads are split, the join of their parts.
+// Launches the tiles' kernel and, where heads may be cut, the plan before and the join of the parts after.
 cudaError_t launch_tiles(void (*kern)(const AttnArgs), std::atomic<uint64_t> &done, int smem, int threads, const AttnArgs &a, int D,
                          int rows, int64_t groups, cudaStream_t st);
 

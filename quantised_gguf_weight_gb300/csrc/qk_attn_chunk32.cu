@@ -1,5 +1,6 @@
 // qk_attn_chunk32.cu -- attention over the 4-bit cache for many query rows a
-// key/value head with fp32 queries, on the 5th-generation tensor cores.
+// key/value head with fp32 or fp16 queries, on the 5th-generation tensor
+// cores.
 //
 // A thread block takes 128 rows (queries x grouped heads) of one key/value
 // head and walks the keys in tiles of 64.  fp32 accuracy comes from operands
@@ -8,7 +9,10 @@
 // Queries, a power of two away from themselves, are whole numbers below 2^11
 // and multiples of 2^-12; K = (n - 8) d has 15 bits, K1 its leading 11 and K2
 // exactly the rest; P1 and P2 are a probability's first and next 11 bits.  The
-// product left out is below 2^-22 of the sum's terms.
+// product left out is below 2^-22 of the sum's terms.  fp16 queries are one
+// piece, and S two products.  (In the bf16 form, whose K, P and V are rounded to
+// 11 bits, fp16 outputs were 4e-4 off, twice their own rounding; bf16's own is
+// 1.7e-3.)
 //
 // The tensor cores cut what they add at about 2^-24 of the largest term, the
 // accumulator too, always the same way; over thousands of keys that would be
@@ -183,21 +187,6 @@ __device__ __forceinline__ bool softmax_tile(Row &R, uint32_t tmem, int half, ui
     const bool over = any_softmax(most > kMost || !ok);
     if (over && any_softmax(!ok)) return false;
     const uint32_t o_addr = tmem + Sh::o_col + 16 * G * half, sum_addr = tmem + Sh::sum_col + 16 * G * half;
-    if (tile > 0 && tile % kFlush == 0) {
-#pragma unroll 2
-        for (int c = 0; c < G; ++c) {
-            uint32_t w[16], s[16];
-            tmem_ld_32x32b_x16(o_addr + 16 * c, w);
-            if (tile > kFlush) tmem_ld_32x32b_x16(sum_addr + 16 * c, s);
-            tmem_ld_wait();
-            if (tile > kFlush) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) + __uint_as_float(s[i]));
-            }
-            tmem_st_32x32b_x16(sum_addr + 16 * c, w);
-        }
-        tmem_st_wait();
-    }
     if (over) {
         // rows past the limit take a new reference; what they have so far is scaled to it
         float top = kNoMax;
@@ -222,20 +211,51 @@ __device__ __forceinline__ bool softmax_tile(Row &R, uint32_t tmem, int half, ui
         }
         exponents32<MASK>(R, v, f, kt, key0, p1, p2, sum);
         for (int c = 0; c < G; ++c) {
-            if (tile % kFlush != 0) scale16(o_addr + 16 * c, factor);
-            if (tile >= kFlush) scale16(sum_addr + 16 * c, factor);
+            if (tile > 0) scale16(o_addr + 16 * c, factor);
+            if (tile > kFlush) scale16(sum_addr + 16 * c, factor);
         }
     }
 #pragma unroll
     for (int b = 0; b < 2; ++b) R.l = fmaf(sum[b], inv[b], R.l);
     tmem_st_32x32b_x16(tmem + Sh::p_col + 16 * half, p1);
     tmem_st_32x32b_x16(tmem + Sh::p_col + 32 + 16 * half, p2);
+    // the accumulator to the sum, before these products begin it anew
+    if (tile > 0 && tile % kFlush == 0) {
+#pragma unroll 2
+        for (int c = 0; c < G; ++c) {
+            uint32_t w[16], s[16];
+            tmem_ld_32x32b_x16(o_addr + 16 * c, w);
+            if (tile > kFlush) tmem_ld_32x32b_x16(sum_addr + 16 * c, s);
+            tmem_ld_wait();
+            if (tile > kFlush) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) + __uint_as_float(s[i]));
+            }
+            tmem_st_32x32b_x16(sum_addr + 16 * c, w);
+        }
+    }
     tmem_st_wait();
     tc_fence_before();
     return true;
 }
 
 // 32 channels of a row; wide: 16 bytes a load.
+__device__ __forceinline__ void load32(float (&x)[32], const __half *from, bool in, bool wide)
+{
+    if (wide) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint4 v = in ? __ldg(reinterpret_cast<const uint4 *>(from) + i) : make_uint4(0, 0, 0, 0);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                x[8 * i + 2 * k] = half_bits_to_float(w[k]), x[8 * i + 2 * k + 1] = half_bits_to_float(w[k] >> 16);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x[i] = in ? __half2float(from[i]) : 0.0f;
+    }
+}
 __device__ __forceinline__ void load32(float (&x)[32], const float *from, bool in, bool wide)
 {
     if (wide) {
@@ -250,11 +270,12 @@ __device__ __forceinline__ void load32(float (&x)[32], const float *from, bool i
     }
 }
 
-template <int G>
+template <int G, class Q>
 __global__ void __launch_bounds__(kThreads, 1) chunk32_kernel(const AttnArgs a)
 {
     using Sh = Shape<G>;
     constexpr int D = Sh::D;
+    constexpr bool two_q = sizeof(Q) == 4;       // fp32 queries are two pieces
     extern __shared__ uint8_t smem_raw[];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     uint8_t *sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -266,7 +287,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk32_kernel(const AttnArgs a)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     Work w;
     if (!find_work(a, kChunkRows32, D, w)) return;
-    const int64_t base = w.blk0 * kBlockTokens;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kSlots; ++i) mbar_init(bars.rfull(i), 1);
@@ -295,13 +315,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk32_kernel(const AttnArgs a)
     const uint32_t mine_tmem = tmem + (static_cast<uint32_t>(warp & 3) << 21);       // 32 lanes a warp, lane in bits 16..
     const int my_row = threadIdx.x & 127, half = warp >> 2;       // half: of a tile's keys, and of the channels
     const bool row_in = softmax_warp && my_row < w.rows;
-    int64_t row_token = 0, row_head = 0;
     if (softmax_warp) {
-        const int row = w.first + my_row, i = row_in ? row / a.rep : 0;
-        row_token = w.seq.r0 + i;
-        row_head = static_cast<int64_t>(w.hk) * a.rep + (row_in ? row - i * a.rep : 0);
-        const float *from = static_cast<const float *>(a.q) + row_token * a.ldq + row_head * D;
-        const bool wide = ((reinterpret_cast<uintptr_t>(a.q) | 4 * a.ldq) & 15) == 0;
+        const Q *from = static_cast<const Q *>(a.q) + row_at(a, w, my_row, row_in, a.ldq, D);
+        const bool wide = ((reinterpret_cast<uintptr_t>(a.q) | sizeof(Q) * a.ldq) & 15) == 0;
         float big = 0.0f;
 #pragma unroll
         for (int c = 0; c < G; ++c) {
@@ -315,11 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk32_kernel(const AttnArgs a)
         e = min(e, 250);
         const float up = copysignf(__uint_as_float(static_cast<uint32_t>(e) << 23), a.scale_log2);
         R.to_log2 = fmaxf(a.scale_log2 / up, 1.2e-38f);
-        if (row_in) {
-            const int64_t pos = w.seq.len - (w.seq.r1 - w.seq.r0) + i;
-            R.lo = clamp_key(a.window > 0 ? pos - a.window + 1 - base : -1);
-            R.hi = clamp_key(pos + 1 - base);
-        }
+        if (row_in) row_keys(a, w, my_row, R.lo, R.hi);
         for (int c = half; c < G; c += 2) {
             float x[32];
             load32(x, from + 32 * c, row_in, wide);
@@ -332,14 +344,14 @@ __global__ void __launch_bounds__(kThreads, 1) chunk32_kernel(const AttnArgs a)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const float v = x[8 * k + j + 4 * h] * up;
-                        lead[h] = rintf(v);
-                        rest[h] = rintf((v - lead[h]) * 4096.0f) * (1.0f / 4096.0f);
+                        lead[h] = two_q ? rintf(v) : v;
+                        rest[h] = two_q ? rintf((v - lead[h]) * 4096.0f) * (1.0f / 4096.0f) : 0.0f;
                     }
                     q1[4 * k + j] = pack_half(lead[0], lead[1]);
                     q2[4 * k + j] = pack_half(rest[0], rest[1]);
                 }
             tmem_st_32x32b_x16(mine_tmem + Sh::q_col + 16 * c, q1);
-            tmem_st_32x32b_x16(mine_tmem + Sh::q_col + D / 2 + 16 * c, q2);
+            if (two_q) tmem_st_32x32b_x16(mine_tmem + Sh::q_col + D / 2 + 16 * c, q2);
         }
         tmem_st_wait();
     }
@@ -359,6 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk32_kernel(const AttnArgs a)
                 if (elect_one()) {
 #pragma unroll
                     for (int x = 0; x < 3; ++x) {
+                        if (x == 1 && !two_q) continue;
                         const uint32_t q = q_col + (x == 1 ? D / 2 : 0);
                         const uint64_t kx = k0 + (x == 0 ? Sh::k_piece / 16 : 0);
 #pragma unroll
@@ -423,7 +436,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk32_kernel(const AttnArgs a)
         auto group_of = [&](int k) { return G == 3 ? 2 * k + (lane >> 4) : kItems * (lane & 1) + k; };
         const int me = warp - kSoftmaxWarps;
         const uint32_t scales = sb + Sh::scale_at + me * Sh::scale_bytes;      // keys [token][G], values [G][token]
-        const int all_lo = clamp_key(w.span.key_lo - base), all_hi = clamp_key(w.span.key_hi - base);
         // this warp's blocks are number me, me + 7, ..; its n-th goes to slot me + 7 (n % 2).  A lane holds the address
         // of one of the next 32
         const int mine = w.nblk > me ? (w.nblk - me + kDequantWarps - 1) / kDequantWarps : 0;
@@ -434,8 +446,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk32_kernel(const AttnArgs a)
             if ((n & 31) == 0) {
                 addr = a.pages;
                 if (n + lane < mine) {
-                    const int64_t blk = w.blk0 + me + kDequantWarps * (n + lane), pg = blk / a.page_blocks;
-                    const int32_t page = a.page_table[w.b * a.ld_pages + pg];
+                    const int64_t blk = static_cast<int64_t>(w.blk0) + me + kDequantWarps * (n + lane), pg = blk / a.page_blocks;
+                    const int32_t page = a.page_table[static_cast<int64_t>(w.b) * a.ld_pages + pg];
                     if (page < 0 || page >= a.n_pages) {
                         poison = true;
                         record_error(a.err, kErrBadIndex);
@@ -462,12 +474,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk32_kernel(const AttnArgs a)
             if (have && !warp_wait(bars.rfull(slot), (n >> 1) & 1, a.wait_ns)) { dead = true; break; }
             // scales: a lane has those of one group g of two neighbouring tokens
             uint32_t dk[2] = {0, 0}, dv[2] = {0, 0}, top_k = 0, top_v = 0, odd = 0;
-            const bool inner = have && j * kBlockTokens >= all_lo && (j + 1) * kBlockTokens <= all_hi;
+            const bool inner = have && j * kBlockTokens >= w.lo && (j + 1) * kBlockTokens <= w.hi;
             if (scale_lane) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int key = j * kBlockTokens + st + e;
-                    if (inner || (have && key >= all_lo && key < all_hi)) {
+                    if (inner || (have && key >= w.lo && key < w.hi)) {
                         dk[e] = lds16(raw + 16 * D + 2 * ((st + e) * G + sg));
                         dv[e] = lds16(raw + 17 * D + 2 * ((st + e) * G + sg));
                     }
@@ -574,9 +586,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk32_kernel(const AttnArgs a)
     } else {
         // ------------------------------------------------ softmax: a thread is a row
         // keys that every row sees
-        const int64_t p0 = w.seq.len - (w.seq.r1 - w.seq.r0) + w.first / a.rep;
-        const int64_t p1 = w.seq.len - (w.seq.r1 - w.seq.r0) + (w.first + w.rows - 1) / a.rep;
-        const int see_lo = clamp_key(a.window > 0 ? p1 - a.window + 1 - base : 0), see_hi = clamp_key(p0 + 1 - base);
+        int see_lo, see_hi, none;
+        row_keys(a, w, w.rows - 1, see_lo, none);
+        row_keys(a, w, 0, none, see_hi);
         float *rows = reinterpret_cast<float *>(sm + Sh::rows_at);
         for (int i = 0; i < w.ntiles; ++i) {
             const bool ok = warp_wait(bars.sfull(), i & 1, a.wait_ns);
@@ -609,8 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk32_kernel(const AttnArgs a)
         R.l = poison ? __int_as_float(0x7FC00000) : rows[my_row] + rows[kChunkRows32 + my_row];
         float *part = nullptr;
         if (w.active > 1) {
-            const int64_t group = (w.b * a.tiles + w.tile) * a.n_kv + w.hk;
-            part = a.parts + (group * a.splits + w.split) * (chunk_part_bytes(D, kChunkRows32) / 4);
+            part = a.parts + static_cast<int64_t>(blockIdx.x) * (chunk_part_bytes(D, kChunkRows32) / 4);
             if (row_in && half == 0) {
                 part[kChunkRows32 * D + 2 * my_row] = R.m;
                 part[kChunkRows32 * D + 2 * my_row + 1] = R.l;
@@ -618,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk32_kernel(const AttnArgs a)
             part += my_row * 4;       // a warp's 32 rows of four channels lie side by side
         }
         const bool wide = ((reinterpret_cast<uintptr_t>(a.out) | a.ldo * (a.out_type == QK_F32 ? 4 : 2)) & 15) == 0;
-        const int64_t to = row_token * a.ldo + row_head * D;
+        const int64_t to = row_at(a, w, my_row, row_in, a.ldo, D);
         for (int c = G * half; c < G * half + G; ++c) {
             uint32_t v[16], s[16];
 #pragma unroll
@@ -651,11 +662,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk32_kernel(const AttnArgs a)
     }
 }
 
-template <int G>
+template <int G, class Q>
 cudaError_t launch(const AttnArgs &a, int64_t groups, cudaStream_t st)
 {
     static std::atomic<uint64_t> done{0};
-    return launch_tiles(chunk32_kernel<G>, done, Shape<G>::smem, kThreads, a, 32 * G, kChunkRows32, groups, st);
+    return launch_tiles(chunk32_kernel<G, Q>, done, Shape<G>::smem, kThreads, a, 32 * G, kChunkRows32, groups, st);
 }
 
 }  // namespace
@@ -664,9 +675,10 @@ namespace attn {
 
 cudaError_t chunk32_launch(const AttnArgs &a, int D, int64_t groups, cudaStream_t st)
 {
-    if (D == 64) return launch<2>(a, groups, st);
-    if (D == 96) return launch<3>(a, groups, st);
-    if (D == 128) return launch<4>(a, groups, st);
+    const bool half = a.q_type == QK_F16;
+    if (D == 64) return half ? launch<2, __half>(a, groups, st) : launch<2, float>(a, groups, st);
+    if (D == 96) return half ? launch<3, __half>(a, groups, st) : launch<3, float>(a, groups, st);
+    if (D == 128) return half ? launch<4, __half>(a, groups, st) : launch<4, float>(a, groups, st);
     return cudaErrorInvalidValue;
 }
 

@@ -297,8 +297,8 @@ def check_attn(qk, lens, new, nq, nkv, D, page, window=0, dtype="f32", out=None,
         at += n
         ref, A, S = ko.attention(x, keys[b], vals[b], L - n + np.arange(n), scale, window)
         e = (2.0 ** -17 * A + 2.0 ** -16 if dtype == "f32" else 2.0 ** -10 * A + 2.0 ** -9)[..., None] * S
-        refs.append(ref.reshape(n, -1))
-        bounds.append((e + u * np.abs(ref)).reshape(n, -1) + 2.0 ** -24)
+        refs.append(ref.reshape(n, nq * D))
+        bounds.append((e + u * np.abs(ref)).reshape(n, nq * D) + 2.0 ** -24)
     ref = np.concatenate(refs)
     close(o, ref, np.concatenate(bounds), "attention")
     norm = np.linalg.norm(ref)
@@ -337,6 +337,68 @@ def test_attn_one_sequence_lengths(qk, L, dtype):
 ])
 def test_attn_chunks(qk, lens, new, nq, nkv, D, page, window, dtype):
     check_attn(qk, lens, new, nq, nkv, D, page, window=window, dtype=dtype, seed=sum(lens))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("lens,new,nq,nkv,D,page,window", [
+    ([2000], [64], 4, 2, 128, 16, 0),              # parts that are no whole number of key tiles of the whole
+    ([1999], [47], 4, 1, 96, 48, 0),
+    ([3000, 0, 700, 50], [64, 0, 64, 1], 4, 2, 64, 32, 0),
+    ([2500, 2400], [200, 3], 4, 2, 128, 64, 700),
+    ([1030], [1030], 2, 1, 64, 16, 0),
+    ([16000], [40], 2, 1, 128, 64, 0),
+    ([777] * 40, [33] * 40, 2, 2, 64, 16, 0),      # more heads than may be cut
+])
+def test_attn_cut_chunks(qk, lens, new, nq, nkv, D, page, window, dtype):
+    check_attn(qk, lens, new, nq, nkv, D, page, window=window, dtype=dtype, seed=sum(new))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+@pytest.mark.parametrize("qscale,scale", [(1e-3, None), (60.0, None), (1.5, -0.1), (1e20, 1e-21)])
+def test_attn_chunks_flat_and_peaked(qk, dtype, qscale, scale):
+    check_attn(qk, [500], [50], 4, 2, 128, 32, dtype=dtype, qscale=qscale if dtype == "f32" else min(qscale, 60.0),
+               scale=scale if dtype == "f32" or scale != 1e-21 else None)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_attn_cut_faults(qk, dtype):
+    """A page out of range, or a block that never comes, in one part of a cut head: the rows that see it are NaN, the
+    other sequence is as it was, and the workspace stays usable."""
+    D, page, n = 128, 16, 80
+    cache, tab, _, _ = make_cache(4, [2100, 90], 2, D, page)
+    lens = torch.tensor([2100, 90], dtype=torch.int32).cuda()
+    q = rand(3, 2 * n, 4 * D, dtype=dtype)
+    ws = qk.attn_q4_workspace(2, 4, 2, D, n, 2100)
+    ref = qk.attn_q4(cache, q, tab, lens, max_q=n, workspace=ws).reshape(2, n, 4, D)
+    assert not torch.isnan(ref).any() and qk.device_error() == 0
+    t = tab.clone()
+    t[0, 70] = cache.shape[0]
+    o = qk.attn_q4(cache, q, t, lens, max_q=n, workspace=ws).reshape(2, n, 4, D)
+    assert qk.device_error() == 9 and torch.isnan(o[0]).all() and torch.equal(o[1], ref[1])
+    limit = qk.set_wait_limit_ns(20_000_000)
+    qk.debug_attn_skip_block(1)
+    try:
+        o = qk.attn_q4(cache, q, tab, lens, max_q=n, workspace=ws).reshape(2, n, 4, D)
+        assert qk.device_error() == 6
+    finally:
+        qk.debug_attn_skip_block(-1)
+        qk.set_wait_limit_ns(limit)
+    assert torch.isnan(o[0, 0, 0]).all() and torch.equal(o[1], ref[1])
+    o = qk.attn_q4(cache, q, tab, lens, max_q=n, workspace=ws).reshape(2, n, 4, D)
+    assert torch.equal(o, ref) and qk.device_error() == 0
+
+
+def test_attn_fp32_chunk_strides(qk):
+    """fp32 rows and outputs off 16-byte boundaries."""
+    D, nq, n = 64, 6, 40
+    cache, tab, _, _ = make_cache(5, [90, 200], 2, D, 32)
+    lens = torch.tensor([90, 200], dtype=torch.int32).cuda()
+    q = rand(1, 2 * n, nq * D + 9)[:, 3:3 + nq * D]
+    ref = qk.attn_q4(cache, q.contiguous(), tab, lens, max_q=n)
+    out = torch.full((2 * n, nq * D + 3), 5.0, device="cuda")
+    qk.attn_q4(cache, q, tab, lens, max_q=n, out=out[:, 1:1 + nq * D])
+    assert torch.equal(out[:, 1:1 + nq * D], ref)
+    assert (out[:, 0] == 5).all() and (out[:, 1 + nq * D:] == 5).all()
 
 
 @pytest.mark.parametrize("dtype", ["f32", "f16"])
