@@ -29,8 +29,10 @@
 //
 // Warps: 0-7 softmax (a thread is a row and half of a tile's keys, and for the
 // accumulators half of the channels), 8-14 dequantisation (each takes every
-// seventh 16-token block and copies its own raw blocks, two ahead), 15 issues
-// the MMAs.  (With four softmax warps, a thread a whole row, the softmax took
+// seventh 16-token block and copies its own raw blocks, two ahead; a block's
+// values come after the next block's keys, as the scores need those first: 512
+// queries of 32 heads over 16384 keys 324 us, both at once 361), 15 issues the
+// MMAs.  (With four softmax warps, a thread a whole row, the softmax took
 // 3700 cycles a tile, and the tensor cores less than half of that.)
 #include "qk_attn_chunk.cuh"
 #include "qk_internal.h"
@@ -44,7 +46,7 @@ constexpr int kSoftmaxWarps = 8, kDequantWarps = 7, kMmaWarp = 15;
 constexpr int kThreads = 16 * 32;
 constexpr int kStages = 2;                 // tiles of K' and of V'
 constexpr int kMetas = 8;                  // tiles whose exponents are kept: more than stages and tiles at work
-constexpr int kSlots = 2 * kDequantWarps;  // raw blocks in flight: two a dequantising warp, its own
+constexpr int kSlots = 3 * kDequantWarps;  // raw blocks in flight and at work: three a dequantising warp, its own
 constexpr int kFlush = 4;                  // tiles whose products one accumulator takes
 
 template <int G>
@@ -58,7 +60,7 @@ struct Shape {
     static constexpr int v_at = k_at + kStages * 2 * k_piece;
     static constexpr int raw_at = v_at + kStages * 2 * v_piece;
     static constexpr int scale_at = raw_at + kSlots * block_bytes;   // the dequantising warps' scaled scales
-    static constexpr int scale_bytes = (4 + 2) * 16 * G;             // a fp16 pair a key scale, a row of values' a group
+    static constexpr int scale_bytes = (4 + 2 * 2) * 16 * G;         // a fp16 pair a key scale, a row of values' a group, twice
     static constexpr int meta_at = scale_at + kDequantWarps * scale_bytes;       // [tile % kMetas][block] (2^kk, kt, 2^-kt, 0)
     static constexpr int bars_at = meta_at + kMetas * kTileBlocks * 16;
     static constexpr int flags_at = bars_at + (kSlots + 4 * kStages + 4) * 8;
@@ -436,13 +438,15 @@ __global__ void __launch_bounds__(kThreads, 1) chunk32_kernel(const AttnArgs a)
         auto group_of = [&](int k) { return G == 3 ? 2 * k + (lane >> 4) : kItems * (lane & 1) + k; };
         const int me = warp - kSoftmaxWarps;
         const uint32_t scales = sb + Sh::scale_at + me * Sh::scale_bytes;      // keys [token][G], values [G][token]
-        // this warp's blocks are number me, me + 7, ..; its n-th goes to slot me + 7 (n % 2).  A lane holds the address
+        // this warp's blocks are number me, me + 7, ..; its n-th goes to slot me + 7 (n % 3).  A lane holds the address
         // of one of the next 32
         const int mine = w.nblk > me ? (w.nblk - me + kDequantWarps - 1) / kDequantWarps : 0;
         const uint64_t policy = l2_evict_first_policy();
         const uint8_t *addr = a.pages;
+        int issued = 0, arrived = 0;
         auto copy = [&](int n) {
             if (n >= mine) return;
+            issued = n + 1;
             if ((n & 31) == 0) {
                 addr = a.pages;
                 if (n + lane < mine) {
@@ -458,20 +462,21 @@ __global__ void __launch_bounds__(kThreads, 1) chunk32_kernel(const AttnArgs a)
                 }
             }
             if (lane == (n & 31) && !(me + kDequantWarps * n == a.skip_block && blockIdx.x == 0)) {
-                const int slot = me + kDequantWarps * (n & 1);
+                const int slot = me + kDequantWarps * (n % 3);
                 mbar_arrive_expect_tx(bars.rfull(slot), Sh::block_bytes);
                 bulk_g2s(sb + Sh::raw_at + slot * Sh::block_bytes, addr, Sh::block_bytes, bars.rfull(slot), policy);
             }
         };
-        copy(0);
-        copy(1);
-        int n = 0;
-        for (int j = me; j < w.ntiles * kTileBlocks; j += kDequantWarps, ++n) {
+        // Keys of block j, its n-th of this warp.  False if a wait ran out.
+        auto keys = [&](int j, int n) {
             const int i = j / kTileBlocks, bi = j % kTileBlocks;      // key tile, block of it
             const bool have = j < w.nblk;
-            const int slot = me + kDequantWarps * (n & 1);
+            const int slot = me + kDequantWarps * (n % 3);
             const uint32_t raw = sb + Sh::raw_at + slot * Sh::block_bytes;
-            if (have && !warp_wait(bars.rfull(slot), (n >> 1) & 1, a.wait_ns)) { dead = true; break; }
+            if (have) {
+                if (!warp_wait(bars.rfull(slot), (n / 3) & 1, a.wait_ns)) return false;
+                arrived = n + 1;
+            }
             // scales: a lane has those of one group g of two neighbouring tokens
             uint32_t dk[2] = {0, 0}, dv[2] = {0, 0}, top_k = 0, top_v = 0, odd = 0;
             const bool inner = have && j * kBlockTokens >= w.lo && (j + 1) * kBlockTokens <= w.hi;
@@ -505,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk32_kernel(const AttnArgs a)
                     sv[e] = odd >> e & 1 ? 0.0f : half_bits_to_float(dv[e]) * down_v;
                     sts32(scales + 4 * ((st + e) * G + sg), pack_half(sk, sk));
                 }
-                sts32(scales + 64 * G + 2 * (16 * sg + st), pack_half(sv[0], sv[1]));
+                sts32(scales + 64 * G + 32 * G * (n & 1) + 2 * (16 * sg + st), pack_half(sv[0], sv[1]));
             }
             if (lane == 0)
                 sts128(sb + Sh::meta_at + (i % kMetas * kTileBlocks + bi) * 16, static_cast<uint32_t>(127 + ek - 10) << 23,
@@ -517,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk32_kernel(const AttnArgs a)
                 __syncwarp();
             }
             // keys: lane (r, c) has token 4(r/2) + 2h + r%2, channels 32g + 8c..8c+7 a word
-            if (i >= kStages && !warp_wait(bars.kempty(i % kStages), (i / kStages - 1) & 1, a.wait_ns)) { dead = true; break; }
+            if (i >= kStages && !warp_wait(bars.kempty(i % kStages), (i / kStages - 1) & 1, a.wait_ns)) return false;
             const uint32_t kb = sb + Sh::k_at + i % kStages * 2 * Sh::k_piece + bi * kBlockTokens * 128;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -542,7 +547,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk32_kernel(const AttnArgs a)
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(bars.kfull(i % kStages));
-            if (i >= kStages && !warp_wait(bars.vempty(i % kStages), (i / kStages - 1) & 1, a.wait_ns)) { dead = true; break; }
+            return true;
+        };
+        // And its values.
+        auto values = [&](int j, int n) {
+            const int i = j / kTileBlocks, bi = j % kTileBlocks;
+            const uint32_t raw = sb + Sh::raw_at + (me + kDequantWarps * (n % 3)) * Sh::block_bytes;
+            if (i >= kStages && !warp_wait(bars.vempty(i % kStages), (i / kStages - 1) & 1, a.wait_ns)) return false;
             const uint32_t vb = sb + Sh::v_at + i % kStages * 2 * Sh::v_piece, column = (2 * bi + kp) << 4;
 #pragma unroll
             for (int k = 0; k < kItems; ++k) {
@@ -552,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk32_kernel(const AttnArgs a)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         words[e] = lds32(raw + 8 * D + (e & 1) * 128 * G + (vr * 4 + 2 * kp + (e >> 1)) * 4 * G + 4 * g);
-                    lds128(s, scales + 64 * G + 2 * (16 * g + 8 * kp));
+                    lds128(s, scales + 64 * G + 32 * G * (n & 1) + 2 * (16 * g + 8 * kp));
 #pragma unroll
                     for (int half_j = 0; half_j < 2; ++half_j) {
                         uint32_t src[4];
@@ -576,12 +587,22 @@ __global__ void __launch_bounds__(kThreads, 1) chunk32_kernel(const AttnArgs a)
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(bars.vfull(i % kStages));
-            copy(n + 2);       // into the slot just read
+            return true;
+        };
+        copy(0);
+        copy(1);
+        copy(2);
+        const int blocks = w.ntiles * kTileBlocks;
+        for (int j = me, n = 0; j < blocks + kDequantWarps && !dead; j += kDequantWarps, ++n) {
+            if (j < blocks && !keys(j, n)) dead = true;
+            if (n > 0 && !dead) {
+                if (!values(j - kDequantWarps, n - 1)) dead = true;
+                else copy(n + 2);       // into the slot just read
+            }
         }
         // copies still in flight when a wait ran out are waited for before the block ends
         if (dead)
-            for (int k = n; k < n + 2 && k < mine; ++k)
-                mbar_wait(bars.rfull(me + kDequantWarps * (k & 1)), (k >> 1) & 1, a.wait_ns);
+            for (int k = arrived; k < issued; ++k) mbar_wait(bars.rfull(me + kDequantWarps * (k % 3)), (k / 3) & 1, a.wait_ns);
         if (__any_sync(0xFFFFFFFFu, poison) && lane == 0) flags[1] = 1;
     } else {
         // ------------------------------------------------ softmax: a thread is a row
