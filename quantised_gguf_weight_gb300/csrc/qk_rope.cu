@@ -2,11 +2,24 @@
 // and values to the 4-bit cache with both on the way, the cache's read-back,
 // and the rotation tables.
 //
-// One warp takes one head of one token: lane l holds channels 4l..4l+3 (and
-// the same 128 further on, for larger heads).  The norm is a warp sum, the
-// partner of a half-layout pair is read back from the warp's row in shared
-// memory, and a 4-bit group of 32 channels is 8 neighbouring lanes, so its
-// scale is three shuffles.  All of it is bound by the bytes of the rows.
+// Mathematics.  A head x of D channels becomes y_j = x_j w_j / sqrt(mean(x^2) +
+// eps), then each pair (a, b) of its first rot channels (a c - b s, b c + a s)
+// with its position's (c, s).  A stored group of 32 channels is a scale d =
+// fp16(m / -8), m the value of largest magnitude, and nibbles
+// clamp(floor(x / d + 8.5), 0, 15).
+//
+// Heads of 64, 96, 128 and 256 channels whose rows allow 8-byte accesses take
+// heads_kernel: a lane has 8 channels of a head, both members of each pair
+// among them, so only the norm's sum and a group's extremes cross lanes.  All
+// else takes rows_kernel, a warp a head, which is right for every size,
+// stride and alignment.
+//
+// What bounds them: instructions, not the rows' bytes.  8191 tokens of 64 heads
+// of 96 in bf16 are 201 MB, 30 us at the memory's rate; the kernel takes 48
+// (4.2 TB/s) with the issue slots three quarters busy at 44 million warp
+// instructions, conversions, products and sums being about half of them.  The
+// append of 8192 tokens of 48 heads of 128 takes 52 us (100 MB of rows in,
+// 67 out and 9 of cache: 26 at the memory's rate), its read-back 22 (6).
 #include <cfloat>
 #include <cmath>
 #include <type_traits>
@@ -128,8 +141,8 @@ __device__ __forceinline__ void norm_rotate(float (&x)[NV][4], const RowsArgs &a
                     if (ch < a.rot) {
                         const float2 t = cs[ch >> 1];
                         const float u = x[i][e], w = x[i][e + 1];
-                        x[i][e] = __fsub_rn(__fmul_rn(u, t.x), __fmul_rn(w, t.y));
-                        x[i][e + 1] = __fadd_rn(__fmul_rn(u, t.y), __fmul_rn(w, t.x));
+                        x[i][e] = fmaf(u, t.x, -__fmul_rn(w, t.y));
+                        x[i][e + 1] = fmaf(w, t.x, __fmul_rn(u, t.y));
                     }
                 }
         } else {
@@ -147,10 +160,10 @@ __device__ __forceinline__ void norm_rotate(float (&x)[NV][4], const RowsArgs &a
                     const int ch = (i * 32 + lane) * 4 + e;
                     if (ch < half) {
                         const float2 t = cs[ch];
-                        x[i][e] = __fsub_rn(__fmul_rn(x[i][e], t.x), __fmul_rn(row[ch + half], t.y));
+                        x[i][e] = fmaf(x[i][e], t.x, -__fmul_rn(row[ch + half], t.y));
                     } else if (ch < a.rot) {
                         const float2 t = cs[ch - half];
-                        x[i][e] = __fadd_rn(__fmul_rn(row[ch - half], t.y), __fmul_rn(x[i][e], t.x));
+                        x[i][e] = fmaf(x[i][e], t.x, __fmul_rn(row[ch - half], t.y));
                     }
                 }
             __syncwarp();
@@ -280,8 +293,13 @@ __global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const RowsArgs a)
 // which do not rotate) take eight neighbours; the half layout takes
 // 4i..4i+3 and their partners half + 4i.., so a pair is always in one lane and
 // nothing is exchanged.  The lanes of a token's heads share its table row and
-// keep it in registers over up to kHeadsPerLane heads.
-constexpr int kHeadsPerLane = 4;
+// keep it in registers over up to heads_per_lane heads; more would share
+// more but need registers of the blocks that hide the loads: 8191 tokens of 64
+// heads of 96 in 48 us with 4 heads and 4 blocks an SM, 65 with 3 (two blocks
+// a token), 52 with 6; the append of 4 x 2048 tokens, 48 heads of 128, read
+// back, 75 us with 2 heads and 5 blocks, 79 with 4 and 4, 78 with 3 and 4.
+__host__ __device__ constexpr int heads_per_lane(bool append) { return append ? 2 : 4; }
+__host__ __device__ constexpr int heads_blocks(bool append) { return append ? 5 : 4; }
 
 template <int D>
 constexpr int kRowsPerWarp = D == 96 ? 2 : 256 / D;
@@ -296,18 +314,21 @@ __device__ __forceinline__ uint32_t nibbles_of(const float (&x)[8], float d)
     // 1/d of a subnormal fp16 is at most 2^24; the quotient is within +-16
     const float step = fabsf(d), inv = __fdividef(1.0f, step);
     const uint32_t sign = __float_as_uint(d) & 0x80000000u;
-    float w[2];
+    const uint64_t inv2 = pack2f(inv, inv), step2 = pack2f(step, step);
+    float2 w;      // four nibbles each, exact in fp32
 #pragma unroll
-    for (int half = 0; half < 2; ++half)
-#pragma unroll
-        for (int e = 3; e >= 0; --e) {
-            const float v = __uint_as_float(__float_as_uint(x[4 * half + e]) ^ sign);
-            float n = __fadd_rd(fmaf(v, inv, 8.5f - 1.6e-5f), kTwo23) - kTwo23;
-            if (fmaf(7.5f - n, step, v) >= 0.0f) n += 1.0f;
-            n = fminf(fmaxf(n, 0.0f), 15.0f);
-            w[half] = e == 3 ? n : fmaf(w[half], 16.0f, n);     // four nibbles are exact in fp32
-        }
-    return static_cast<uint32_t>(w[0]) | static_cast<uint32_t>(w[1]) << 16;
+    for (int e = 3; e >= 0; --e) {
+        const uint64_t v = pack2(__float_as_uint(x[e]) ^ sign, __float_as_uint(x[e + 4]) ^ sign);
+        const uint64_t low = fma_f32x2(v, inv2, pack2f(8.5f - 1.6e-5f, 8.5f - 1.6e-5f));
+        const uint64_t n2 = add_f32x2(add_down_f32x2(low, pack2f(kTwo23, kTwo23)), pack2f(-kTwo23, -kTwo23));
+        const float2 past = unpack2f(fma_f32x2(fma_f32x2(n2, pack2f(-1.0f, -1.0f), pack2f(7.5f, 7.5f)), step2, v));
+        float2 n = unpack2f(n2);
+        if (past.x >= 0.0f) n.x += 1.0f;
+        if (past.y >= 0.0f) n.y += 1.0f;
+        n.x = fminf(fmaxf(n.x, 0.0f), 15.0f), n.y = fminf(fmaxf(n.y, 0.0f), 15.0f);
+        w = e == 3 ? n : unpack2f(fma_f32x2(pack2f(w.x, w.y), pack2f(16.0f, 16.0f), pack2f(n.x, n.y)));
+    }
+    return static_cast<uint32_t>(w.x) | static_cast<uint32_t>(w.y) << 16;
 }
 
 // Eight neighbouring channels of a head to the cache: the group's scale over
@@ -320,10 +341,11 @@ __device__ __forceinline__ void store_eight(uint8_t *block, int t, int ch, bool 
 #pragma unroll
     for (int e = 1; e < 8; ++e) hi = fmaxf(hi, x[e]), lo = fminf(lo, x[e]);
     // a NaN or an infinity: 0 * x is NaN for these alone
-    float zero = 0.0f;
+    uint64_t zero = 0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) zero = fmaf(x[e], 0.0f, zero);
-    const bool odd = !(zero == 0.0f);
+    for (int e = 0; e < 8; e += 2) zero = fma_f32x2(pack2f(x[e], x[e + 1]), 0, zero);
+    const float2 z = unpack2f(zero);
+    const bool odd = !(z.x + z.y == 0.0f);
 #pragma unroll
     for (int o = 1; o < 4; o <<= 1) {
         hi = fmaxf(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, o));
@@ -370,9 +392,11 @@ __device__ __forceinline__ void turn_eight(float (&x)[8], bool norm, bool weigh,
 {
     constexpr int LPR = D / 8;
     if (norm) {       // warp-uniform: some row of the call has a weight
-        float q = 0.0f;
+        uint64_t squares = 0;      // two zeros
 #pragma unroll
-        for (int e = 0; e < 8; ++e) q = fmaf(x[e], x[e], q);
+        for (int e = 0; e < 8; e += 2) squares = fma_f32x2(pack2f(x[e], x[e + 1]), pack2f(x[e], x[e + 1]), squares);
+        const float2 two = unpack2f(squares);
+        float q = two.x + two.y;
         if constexpr (D == 96) {      // 12 lanes a row: groups of four stay inside it
             q += __shfl_xor_sync(0xFFFFFFFFu, q, 1);
             q += __shfl_xor_sync(0xFFFFFFFFu, q, 2);
@@ -384,17 +408,31 @@ __device__ __forceinline__ void turn_eight(float (&x)[8], bool norm, bool weigh,
             for (int o = LPR / 2; o; o >>= 1) q += __shfl_xor_sync(0xFFFFFFFFu, q, o);
         }
         const float r = weigh ? rsqrt_newton(__fadd_rn(q * (1.0f / D), eps)) : 1.0f;   // without: the weights are 1
+        const uint64_t r2 = pack2f(r, r);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = __fmul_rn(__fmul_rn(x[e], r), w[e]);
+        for (int e = 0; e < 8; e += 2) {
+            const float2 y = unpack2f(mul_f32x2(mul_f32x2(pack2f(x[e], x[e + 1]), r2), pack2f(w[e], w[e + 1])));
+            x[e] = y.x, x[e + 1] = y.y;
+        }
     }
-    // each product and sum is rounded by itself, so the stored nibbles do not depend on how a compiler fuses them
+    // (u c - v s, v c + u s), the product with s rounded, the other fused, so that the stored nibbles do not depend on
+    // what a compiler would fuse
     if (turn)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            constexpr int step = INTER ? 2 : 1, other = INTER ? 1 : 4;
-            const float u = x[step * e], v = x[step * e + other];
-            x[step * e] = __fsub_rn(__fmul_rn(u, c[e]), __fmul_rn(v, s[e]));
-            x[step * e + other] = __fadd_rn(__fmul_rn(u, s[e]), __fmul_rn(v, c[e]));
+        for (int e = 0; e < 4; e += 2) {
+            if constexpr (INTER) {
+#pragma unroll
+                for (int k = e; k < e + 2; ++k) {
+                    const float u = x[2 * k], v = x[2 * k + 1];
+                    x[2 * k] = fmaf(u, c[k], -__fmul_rn(v, s[k]));
+                    x[2 * k + 1] = fmaf(v, c[k], __fmul_rn(u, s[k]));
+                }
+            } else {
+                const uint64_t u = pack2f(x[e], x[e + 1]), v = pack2f(x[e + 4], x[e + 5]);
+                const uint64_t c2 = pack2f(c[e], c[e + 1]), s2 = pack2f(s[e], s[e + 1]), minus = pack2f(-s[e], -s[e + 1]);
+                const float2 y = unpack2f(fma_f32x2(u, c2, mul_f32x2(v, minus))), z = unpack2f(fma_f32x2(v, c2, mul_f32x2(u, s2)));
+                x[e] = y.x, x[e + 1] = y.y, x[e + 4] = z.x, x[e + 5] = z.y;
+            }
         }
 }
 
@@ -434,9 +472,10 @@ struct Raw {
 };
 
 template <int D, int TYPE, bool INTER, bool APPEND>
-__global__ void __launch_bounds__(kRowWarps * 32) heads_kernel(const RowsArgs a, int hpl_front, int hpl_back, int q_parts,
+__global__ void __launch_bounds__(kRowWarps * 32, heads_blocks(APPEND)) heads_kernel(const RowsArgs a, int hpl_front, int hpl_back, int q_parts,
                                                                 int parts)
 {
+    constexpr int kHeadsPerLane = heads_per_lane(APPEND);
     constexpr int LPR = D / 8, RPW = kRowsPerWarp<D>, NG = kRowWarps * RPW, size = Raw<TYPE>::size;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -711,10 +750,12 @@ cudaError_t launch(void (*kern)(const Args), int64_t grid, int threads, size_t s
 template <int D, int TYPE, bool INTER, bool APPEND>
 cudaError_t launch_heads(const RowsArgs &a, cudaStream_t st)
 {
+    constexpr int kHeadsPerLane = heads_per_lane(APPEND);
     constexpr int NG = kRowWarps * kRowsPerWarp<D>;
     const int front = APPEND ? a.n_q : a.n_q + a.n_k, back = APPEND ? 2 * a.n_k : 0;
     // several heads a lane share a table row and keep as many loads going; few tokens spread over more blocks
-    // instead (one token of 40 heads of 128: 1.5 us with one head a lane)
+    // instead (40 heads of 128: one token 2.7 us with four heads a lane, 2.1 with one, 64 tokens 2.5 and 2.4, 256
+    // tokens 3.1 and 3.7)
     const auto cut = [](int heads, int most, int *per) {
         const int parts = (heads + NG * most - 1) / (NG * most);
         *per = parts ? (heads + NG * parts - 1) / (NG * parts) : 1;
@@ -723,9 +764,10 @@ cudaError_t launch_heads(const RowsArgs &a, cudaStream_t st)
     int hf = 1, hb = 1, fp = cut(front, kHeadsPerLane, &hf), parts = fp + cut(back, kHeadsPerLane, &hb);
     if (a.T * parts < 304) fp = cut(front, 1, &hf), parts = fp + cut(back, 1, &hb);
     // appending many tokens, thread blocks go from token to token and work out only once what does not change (8192
-    // tokens of 32 + 2 x 8 heads of 128: 85 us in four rounds of the blocks that the GPU holds, 91 with a block a
-    // token; without the nibbles there is less to save than the waits cost, 57 us against 50 for 8191 x 64 of 96)
-    const int64_t most = APPEND ? (4 * 4 * 152 + parts - 1) / parts : a.T, tokens = a.T < most ? a.T : most;
+    // tokens of 32 + 2 x 8 heads of 128, read back: 74 us in six rounds of the blocks that the GPU holds, 75 in four,
+    // 84 with a block a token; without the nibbles there is less to save than the waits cost, 57 us against 50 for
+    // 8191 x 64 of 96)
+    const int64_t most = APPEND ? (6 * heads_blocks(true) * 152 + parts - 1) / parts : a.T, tokens = a.T < most ? a.T : most;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(tokens * parts));
     cfg.blockDim = dim3(kRowWarps * 32);
