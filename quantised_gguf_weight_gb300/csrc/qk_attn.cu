@@ -1,6 +1,7 @@
 // qk_attn.cu -- attention over the 4-bit paged cache: the entry point, its
 // argument checks, and how a call's rows and keys are cut over thread blocks.
-// The kernels are in qk_attn_rows.cuh (few rows) and qk_attn_chunk.cu (many).
+// The kernels are in qk_attn_rows.cuh (few rows), qk_attn_chunk.cu and
+// qk_attn_chunk32.cu (many).
 #include <atomic>
 #include <cmath>
 

@@ -1,6 +1,6 @@
 // qk_attn_chunk.cuh -- what the two many-row forms of attention over the 4-bit
 // cache share: accesses to shared memory, the work of a thread block, a row's
-// state, outputs, and the join of the parts of a head's splits.
+// state, outputs, and the join of a cut head's parts.
 #pragma once
 
 #include <atomic>

@@ -6,6 +6,7 @@
 // head and walks the keys in tiles of 64.  fp32 accuracy comes from operands
 // of two fp16 pieces and three of their four products:
 //   S = Q1 K1^T + Q2 K1^T + Q1 K2^T      O += P1 V1 + P2 V1 + P1 V2
+// (1e-6 off over 16384 keys; the few-row form 2e-6)
 // Queries, a power of two away from themselves, are whole numbers below 2^11
 // and multiples of 2^-12; K = (n - 8) d has 15 bits, K1 its leading 11 and K2
 // exactly the rest; P1 and P2 are a probability's first and next 11 bits.  The
@@ -32,7 +33,12 @@
 // seventh 16-token block and copies its own raw blocks, two ahead; a block's
 // values come after the next block's keys, as the scores need those first: 512
 // queries of 32 heads over 16384 keys 324 us, both at once 361), 15 issues the
-// MMAs.  (With four softmax warps, a thread a whole row, the softmax took
+// MMAs.
+//
+// What bounds it: the softmax warps, 2000 of a tile's 2400 cycles (read S, two
+// exponentials' pieces, write P), the tensor cores being busy for 1540.  512
+// queries of 32 heads of 128 over 16384 keys take 324 us in fp32 (133 GFLOP, 0.41
+// PFLOP/s counted once, 1.2 of products; the few-row form 1287), 312 in fp16 (743).  (With four softmax warps, a thread a whole row, the softmax took
 // 3700 cycles a tile, and the tensor cores less than half of that.)
 #include "qk_attn_chunk.cuh"
 #include "qk_internal.h"
@@ -418,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk32_kernel(const AttnArgs a)
             }
         }
     } else if (!softmax_warp) {
-        // ------------------------------------------------ dequantisation: block j of the split, 16 tokens
+        // ------------------------------------------------ dequantisation: block j of the part, 16 tokens
         const int r8 = lane >> 2, c = lane & 3, swap = G % 2 == 0 ? r8 & 1 : 0;
         // scales: group sg of tokens st, st + 1
         const int sg = lane % G, st = 2 * (lane / G);

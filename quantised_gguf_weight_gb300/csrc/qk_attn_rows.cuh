@@ -1,5 +1,5 @@
 // qk_attn_rows.cuh -- attention over the 4-bit paged cache for few query rows a
-// key/value head (single tokens, short chunks, fp32 queries).
+// key/value head (single tokens, short chunks), and heads of 256 channels.
 //
 // Mathematics.  With K_j = d_jg (n_jc - 8) in each 32-channel group g,
 //   s_j = scale * sum_g d_jg (sum_c q_c n_jc - 8 sum_c q_c)
@@ -38,6 +38,14 @@
 // cross heads, a thread block going through several heads, balanced better
 // but cost 12% more instructions a block: 64 x 8192 tokens 149 us against
 // 146.)
+//
+// What bounds it: instructions.  64 sequences of 8192 tokens, 8 heads of 128
+// with 4 queries each in bf16, are 604 MB in 146 us (4.1 TB/s, 61% of the copy
+// rate): 354 warp instructions a block of 16 tokens, the integer pipe half and
+// the issue slots 61% busy with 16 warps an SM, a third of them taking nibbles
+// apart.  Short calls are their fixed part, 4 to 5 us of dependent reads
+// (lengths, page table, first blocks) and the join: 1 x 32768 20 us, 4 of them
+// before the first block.
 #pragma once
 
 #include <atomic>
@@ -348,8 +356,9 @@ __device__ __forceinline__ void store_row4(const AttnArgs &a, int64_t at, const 
     for (int e = 0; e < 4; ++e) store_float_as(a.out, at + e, a.out_type, l == 0.0f ? 0.0f : x[e] / l);
 }
 
-// The parts of the thread blocks that share a head: `count` from c_first on.  Rows' references and sums come first, into shared memory, a batch of parts at a time; then a thread
-// takes four channels of every `ways`-th part, and the ways are added in order.
+// The parts of the thread blocks that share a head: `count` from c_first on.  Rows' references and sums come first,
+// into shared memory, a batch of parts at a time; then a thread takes four channels of every `ways`-th part, and the
+// ways are added in order.
 template <int RT, int D, class OutAt>
 __device__ __forceinline__ void join_parts(const AttnArgs &a, int c_first, int count, int rows, float *buf, int buf_floats,
                                            OutAt out_at)
