@@ -15,10 +15,10 @@
 // stride and alignment.
 //
 // What bounds them: instructions, not the rows' bytes.  8191 tokens of 64 heads
-// of 96 in bf16 are 201 MB, 30 us at the memory's rate; the kernel takes 48
-// (4.2 TB/s) with the issue slots three quarters busy at 44 million warp
+// of 96 in bf16 are 201 MB, 30 us at the memory's rate; the kernel takes 50
+// (4.0 TB/s) with the issue slots three quarters busy at 44 million warp
 // instructions, conversions, products and sums being about half of them.  The
-// append of 8192 tokens of 48 heads of 128 takes 52 us (100 MB of rows in,
+// append of 8192 tokens of 48 heads of 128 takes 53 us (100 MB of rows in,
 // 67 out and 9 of cache: 26 at the memory's rate), its read-back 22 (6).
 #include <cfloat>
 #include <cmath>
@@ -141,8 +141,8 @@ __device__ __forceinline__ void norm_rotate(float (&x)[NV][4], const RowsArgs &a
                     if (ch < a.rot) {
                         const float2 t = cs[ch >> 1];
                         const float u = x[i][e], w = x[i][e + 1];
-                        x[i][e] = fmaf(u, t.x, -__fmul_rn(w, t.y));
-                        x[i][e + 1] = fmaf(w, t.x, __fmul_rn(u, t.y));
+                        x[i][e] = __fsub_rn(__fmul_rn(u, t.x), __fmul_rn(w, t.y));
+                        x[i][e + 1] = __fadd_rn(__fmul_rn(u, t.y), __fmul_rn(w, t.x));
                     }
                 }
         } else {
@@ -160,10 +160,10 @@ __device__ __forceinline__ void norm_rotate(float (&x)[NV][4], const RowsArgs &a
                     const int ch = (i * 32 + lane) * 4 + e;
                     if (ch < half) {
                         const float2 t = cs[ch];
-                        x[i][e] = fmaf(x[i][e], t.x, -__fmul_rn(row[ch + half], t.y));
+                        x[i][e] = __fsub_rn(__fmul_rn(x[i][e], t.x), __fmul_rn(row[ch + half], t.y));
                     } else if (ch < a.rot) {
                         const float2 t = cs[ch - half];
-                        x[i][e] = fmaf(x[i][e], t.x, __fmul_rn(row[ch - half], t.y));
+                        x[i][e] = __fadd_rn(__fmul_rn(row[ch - half], t.y), __fmul_rn(x[i][e], t.x));
                     }
                 }
             __syncwarp();
@@ -415,24 +415,26 @@ __device__ __forceinline__ void turn_eight(float (&x)[8], bool norm, bool weigh,
             x[e] = y.x, x[e + 1] = y.y;
         }
     }
-    // (u c - v s, v c + u s), the product with s rounded, the other fused, so that the stored nibbles do not depend on
-    // what a compiler would fuse
+    // each product and sum is rounded by itself, so the stored nibbles do not depend on how a compiler fuses them (which
+    // it does where the sums too are in pairs)
     if (turn)
 #pragma unroll
         for (int e = 0; e < 4; e += 2) {
+            constexpr int step = INTER ? 2 : 1, other = INTER ? 1 : 4;
+            float2 uc, vs, us, vc;
             if constexpr (INTER) {
-#pragma unroll
-                for (int k = e; k < e + 2; ++k) {
-                    const float u = x[2 * k], v = x[2 * k + 1];
-                    x[2 * k] = fmaf(u, c[k], -__fmul_rn(v, s[k]));
-                    x[2 * k + 1] = fmaf(v, c[k], __fmul_rn(u, s[k]));
-                }
+                uc = make_float2(__fmul_rn(x[2 * e], c[e]), __fmul_rn(x[2 * e + 2], c[e + 1]));
+                vs = make_float2(__fmul_rn(x[2 * e + 1], s[e]), __fmul_rn(x[2 * e + 3], s[e + 1]));
+                us = make_float2(__fmul_rn(x[2 * e], s[e]), __fmul_rn(x[2 * e + 2], s[e + 1]));
+                vc = make_float2(__fmul_rn(x[2 * e + 1], c[e]), __fmul_rn(x[2 * e + 3], c[e + 1]));
             } else {
                 const uint64_t u = pack2f(x[e], x[e + 1]), v = pack2f(x[e + 4], x[e + 5]);
-                const uint64_t c2 = pack2f(c[e], c[e + 1]), s2 = pack2f(s[e], s[e + 1]), minus = pack2f(-s[e], -s[e + 1]);
-                const float2 y = unpack2f(fma_f32x2(u, c2, mul_f32x2(v, minus))), z = unpack2f(fma_f32x2(v, c2, mul_f32x2(u, s2)));
-                x[e] = y.x, x[e + 1] = y.y, x[e + 4] = z.x, x[e + 5] = z.y;
+                const uint64_t c2 = pack2f(c[e], c[e + 1]), s2 = pack2f(s[e], s[e + 1]);
+                uc = unpack2f(mul_f32x2(u, c2)), vs = unpack2f(mul_f32x2(v, s2));
+                us = unpack2f(mul_f32x2(u, s2)), vc = unpack2f(mul_f32x2(v, c2));
             }
+            x[step * e] = __fsub_rn(uc.x, vs.x), x[step * (e + 1)] = __fsub_rn(uc.y, vs.y);
+            x[step * e + other] = __fadd_rn(us.x, vc.x), x[step * (e + 1) + other] = __fadd_rn(us.y, vc.y);
         }
 }
 
