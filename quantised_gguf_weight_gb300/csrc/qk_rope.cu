@@ -15,11 +15,11 @@
 // stride and alignment.
 //
 // What bounds them: instructions, not the rows' bytes.  8191 tokens of 64 heads
-// of 96 in bf16 are 201 MB, 30 us at the memory's rate; the kernel takes 50
-// (4.0 TB/s) with the issue slots three quarters busy at 44 million warp
+// of 96 in bf16 are 201 MB, 30 us at the memory's rate; the kernel takes 49
+// (4.1 TB/s) with the issue slots three quarters busy at 42 million warp
 // instructions, conversions, products and sums being about half of them.  The
 // append of 8192 tokens of 48 heads of 128 takes 53 us (100 MB of rows in,
-// 67 out and 9 of cache: 26 at the memory's rate), its read-back 22 (6).
+// 67 out and 9 of cache: 26 at the memory's rate), its read-back 13 (6).
 #include <cfloat>
 #include <cmath>
 #include <type_traits>
@@ -296,8 +296,8 @@ __global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const RowsArgs a)
 // keep it in registers over up to heads_per_lane heads; more would share
 // more but need registers of the blocks that hide the loads: 8191 tokens of 64
 // heads of 96 in 48 us with 4 heads and 4 blocks an SM, 65 with 3 (two blocks
-// a token), 52 with 6; the append of 4 x 2048 tokens, 48 heads of 128, read
-// back, 75 us with 2 heads and 5 blocks, 79 with 4 and 4, 78 with 3 and 4.
+// a token), 52 with 6; the append of 4 x 2048 tokens, 48 heads of 128, 53 us
+// with 2 heads and 5 blocks, 57 with 4 and 4, 56 with 3 and 4.
 __host__ __device__ constexpr int heads_per_lane(bool append) { return append ? 2 : 4; }
 __host__ __device__ constexpr int heads_blocks(bool append) { return append ? 5 : 4; }
 
@@ -474,8 +474,7 @@ struct Raw {
 };
 
 template <int D, int TYPE, bool INTER, bool APPEND>
-__global__ void __launch_bounds__(kRowWarps * 32, heads_blocks(APPEND)) heads_kernel(const RowsArgs a, int hpl_front, int hpl_back, int q_parts,
-                                                                int parts)
+__global__ void __launch_bounds__(kRowWarps * 32, heads_blocks(APPEND)) heads_kernel(const RowsArgs a, int hpl_front, int hpl_back, int q_parts)
 {
     constexpr int kHeadsPerLane = heads_per_lane(APPEND);
     constexpr int LPR = D / 8, RPW = kRowsPerWarp<D>, NG = kRowWarps * RPW, size = Raw<TYPE>::size;
@@ -483,8 +482,8 @@ __global__ void __launch_bounds__(kRowWarps * 32, heads_blocks(APPEND)) heads_ke
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int sub = lane / LPR, i = lane - sub * LPR;            // row of the warp, lane of the row
     const bool on = sub < RPW;                                   // 96 channels leave 8 lanes idle
-    const int part = static_cast<int>(blockIdx.x) % parts;
-    const int t_first = static_cast<int>(blockIdx.x) / parts, t_step = static_cast<int>(gridDim.x) / parts;
+    const int part = static_cast<int>(blockIdx.y);
+    const uint32_t t_first = blockIdx.x, t_step = gridDim.x;      // T is below 2^31: their sum stays in 32 bits
     const bool front = !APPEND || part < q_parts;                // rows that go out; else rows that are stored
     const int hpl = front ? hpl_front : hpl_back;                // heads a lane
     const int h0 = (front ? part : part - q_parts) * NG * hpl + warp * RPW + sub;
@@ -501,7 +500,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, heads_blocks(APPEND)) heads_ke
     const bool changes = mine > 0 && h0 < first_mine && h0 + (mine - 1) * NG >= first_mine;
     float w[8];
     load_weights(w, mine ? first_weight : nullptr, ca, cb);
-    for (int t = t_first; t < a.T; t += t_step) {
+    for (uint32_t t = t_first; t < a.T; t += t_step) {
         // rows and position first, together: nothing waits before all of it is on its way
         int32_t pos = a.rot > 0 ? a.positions[t] : 0;
         Raw<TYPE> xa[kHeadsPerLane], xb[kHeadsPerLane];
@@ -621,64 +620,77 @@ struct ReadArgs {
     int64_t ldk, ldv;
     int type;
     bool vec;
-    int parts, tokens;       // thread blocks a token, or tokens a thread block
+    int tokens;              // of a thread block
     int *err;
 };
 
-// A lane reads eight channels of a slot's key or value head: one word, or two halves of words.  A thread block takes
-// whole tokens, or a part of one.
+// Eight stored values from their nibbles (in order from the low end) and scale.  A nibble under the bits of 2^23 is
+// 2^23 + n 16^e, and one multiply-add gives n - 8 of it exactly.
+__device__ __forceinline__ void values_of(uint32_t n, float d, float (&lo)[4], float (&hi)[4])
+{
+    const uint32_t m = n >> 16;
+    lo[0] = __uint_as_float(magic_field<0x000Fu>(n)), hi[0] = __uint_as_float(magic_field<0x000Fu>(m));
+    lo[1] = __uint_as_float(magic_field<0x00F0u>(n)), hi[1] = __uint_as_float(magic_field<0x00F0u>(m));
+    lo[2] = __uint_as_float(magic_field<0x0F00u>(n)), hi[2] = __uint_as_float(magic_field<0x0F00u>(m));
+    lo[3] = __uint_as_float(magic_field<0xF000u>(n)), hi[3] = __uint_as_float(magic_field<0xF000u>(m));
+    float down = 1.0f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e, down *= 0.0625f) {
+        const float less = -(kTwo23 * down + 8.0f);
+        lo[e] = d * fmaf(lo[e], down, less), hi[e] = d * fmaf(hi[e], down, less);
+    }
+}
+
+// A lane reads eight channels of a slot's key head and value head.  A thread block takes whole tokens, or (blockIdx.y)
+// a part of one.
 template <int D>
 __global__ void __launch_bounds__(kRowWarps * 32) read_kernel(const ReadArgs a)
 {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     constexpr int lpr = D / 8;
-    const int items = a.n_kv * ((a.k ? 1 : 0) + (a.v ? 1 : 0)) * lpr;      // of a token
-    const int part = static_cast<int>(blockIdx.x) % a.parts, own = static_cast<int>(threadIdx.x) / items;
-    const int64_t t = static_cast<int64_t>(blockIdx.x / a.parts) * a.tokens + own;
-    const int item = a.tokens > 1 ? static_cast<int>(threadIdx.x) - own * items : part * kRowWarps * 32 + static_cast<int>(threadIdx.x);
+    const int items = a.n_kv * lpr;      // of a token
+    int own = 0, item = static_cast<int>(blockIdx.y * (kRowWarps * 32) + threadIdx.x);
+    if (a.tokens > 1) own = item / items, item -= own * items;
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * a.tokens + own;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (t >= a.T || item >= items || own >= a.tokens) return;
-    int h = item / lpr;
-    const int ch = (item - h * lpr) * 8;
-    const bool is_key = a.k && h < a.n_kv;
-    if (a.k && !is_key) h -= a.n_kv;
-    void *dst = is_key ? a.k : a.v;
-    const int64_t to = t * (is_key ? a.ldk : a.ldv) + static_cast<int64_t>(h) * D + ch;
+    const int h = item / lpr, ch = (item - h * lpr) * 8;
     const int64_t slot = a.slots[t];
-    float lo[4], hi[4];
+    uint32_t nibbles[2] = {0x88888888u, 0x88888888u};
+    float scale[2];
     if (slot >= 0 && slot < a.n_slots) {
         const Slot at = slot_of(slot, a.page_tokens, a.n_slots);
-        const int off = at.token, tk = off % kBlockTokens;
-        const uint8_t *block = a.pages + ((at.page * a.n_kv + h) * (a.page_tokens / kBlockTokens) + off / kBlockTokens) *
+        const int tk = at.token % kBlockTokens;
+        const uint8_t *block = a.pages + ((at.page * a.n_kv + h) * (a.page_tokens / kBlockTokens) + at.token / kBlockTokens) *
                                              static_cast<int64_t>(18 * D);
-        uint32_t n;
-        if (is_key) {
-            n = *reinterpret_cast<const uint32_t *>(block + kv4_key_place(D, tk, ch).byte);
-        } else {
+        if (a.k) nibbles[0] = *reinterpret_cast<const uint32_t *>(block + kv4_key_place(D, tk, ch).byte);
+        if (a.v) {
             const uint8_t *from = block + kv4_value_place(D, tk, ch).byte + 2 * (tk & 1);      // the next four channels are one r further
-            n = *reinterpret_cast<const uint16_t *>(from) |
-                static_cast<uint32_t>(*reinterpret_cast<const uint16_t *>(from + 16 * kv4_gp(D / 32))) << 16;
+            nibbles[1] = *reinterpret_cast<const uint16_t *>(from) |
+                         static_cast<uint32_t>(*reinterpret_cast<const uint16_t *>(from + 16 * kv4_gp(D / 32))) << 16;
         }
-        const int s = is_key ? kv4_key_scale(D, tk, ch >> 5) : kv4_value_scale(D, tk, ch >> 5);
-        const float d = __half2float(*reinterpret_cast<const __half *>(block + s));
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            lo[e] = d * (static_cast<float>((n >> (4 * e)) & 15u) - 8.0f);
-            hi[e] = d * (static_cast<float>((n >> (4 * e + 16)) & 15u) - 8.0f);
-        }
+        scale[0] = __half2float(*reinterpret_cast<const __half *>(block + kv4_key_scale(D, tk, ch >> 5)));
+        scale[1] = __half2float(*reinterpret_cast<const __half *>(block + kv4_value_scale(D, tk, ch >> 5)));
     } else {
         if (slot >= 0) record_error(a.err, kErrBadIndex);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) lo[e] = hi[e] = slot < 0 ? 0.0f : __int_as_float(0x7FC00000);
+        scale[0] = scale[1] = slot < 0 ? 0.0f : __int_as_float(0x7FC00000);
     }
-    if (a.vec) {
-        store4(dst, to, a.type, lo);
-        store4(dst, to + 4, a.type, hi);
-    } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) store_float_as(dst, to + e, a.type, lo[e]);
+    for (int kind = 0; kind < 2; ++kind) {
+        void *dst = kind ? a.v : a.k;
+        if (!dst) continue;
+        const int64_t to = t * (kind ? a.ldv : a.ldk) + static_cast<int64_t>(h) * D + ch;
+        float lo[4], hi[4];
+        values_of(nibbles[kind], scale[kind], lo, hi);
+        if (a.vec) {
+            store4(dst, to, a.type, lo);
+            store4(dst, to + 4, a.type, hi);
+        } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) store_float_as(dst, to + 4 + e, a.type, hi[e]);
+            for (int e = 0; e < 4; ++e) store_float_as(dst, to + e, a.type, lo[e]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) store_float_as(dst, to + 4 + e, a.type, hi[e]);
+        }
     }
 }
 
@@ -734,10 +746,10 @@ bool vec_ok(const void *p, int64_t ld, int D, int type)
 int64_t blocks_for(int64_t items) { return (items + kRowWarps - 1) / kRowWarps; }
 
 template <class Args>
-cudaError_t launch(void (*kern)(const Args), int64_t grid, int threads, size_t smem, cudaStream_t st, const Args &a)
+cudaError_t launch(void (*kern)(const Args), dim3 grid, int threads, size_t smem, cudaStream_t st, const Args &a)
 {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
@@ -766,12 +778,12 @@ cudaError_t launch_heads(const RowsArgs &a, cudaStream_t st)
     int hf = 1, hb = 1, fp = cut(front, kHeadsPerLane, &hf), parts = fp + cut(back, kHeadsPerLane, &hb);
     if (a.T * parts < 304) fp = cut(front, 1, &hf), parts = fp + cut(back, 1, &hb);
     // appending many tokens, thread blocks go from token to token and work out only once what does not change (8192
-    // tokens of 32 + 2 x 8 heads of 128, read back: 74 us in six rounds of the blocks that the GPU holds, 75 in four,
-    // 84 with a block a token; without the nibbles there is less to save than the waits cost, 57 us against 50 for
+    // tokens of 32 + 2 x 8 heads of 128: 52 us in six rounds of the blocks that the GPU holds, 53 in four, 62 with a
+    // block a token; without the nibbles there is less to save than the waits cost, 57 us against 50 for
     // 8191 x 64 of 96)
     const int64_t most = APPEND ? (6 * heads_blocks(true) * 152 + parts - 1) / parts : a.T, tokens = a.T < most ? a.T : most;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(tokens * parts));
+    cfg.gridDim = dim3(static_cast<unsigned>(tokens), static_cast<unsigned>(parts));
     cfg.blockDim = dim3(kRowWarps * 32);
     cfg.stream = st;
     cudaLaunchAttribute at = {};
@@ -779,7 +791,7 @@ cudaError_t launch_heads(const RowsArgs &a, cudaStream_t st)
     at.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &at;
     cfg.numAttrs = library_programmatic() ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, heads_kernel<D, TYPE, INTER, APPEND>, a, hf, hb, fp, parts);
+    return cudaLaunchKernelEx(&cfg, heads_kernel<D, TYPE, INTER, APPEND>, a, hf, hb, fp);
 }
 
 template <int D, int TYPE, bool APPEND>
@@ -809,7 +821,7 @@ cudaError_t launch_rows(const RowsArgs &a, cudaStream_t st)
         case 256: return launch_heads_type<256, APPEND>(a, st);
         }
     }
-    const int64_t grid = blocks_for(a.T * (a.n_q + a.n_k + a.n_v));
+    const dim3 grid(static_cast<unsigned>(blocks_for(a.T * (a.n_q + a.n_k + a.n_v))));
     if (a.D <= 128) return launch(rows_kernel<1, APPEND>, grid, kRowWarps * 32, 0, st, a);
     if (a.D <= 256) return launch(rows_kernel<2, APPEND>, grid, kRowWarps * 32, 0, st, a);
     if constexpr (!APPEND) return launch(rows_kernel<4, APPEND>, grid, kRowWarps * 32, 0, st, a);
@@ -875,7 +887,7 @@ int qk_rope_table(float *table, int64_t n_pos, int rot, double base, double freq
         a.hi = std::fmin(rot - 1.0, std::ceil(dim(beta_slow)));
     }
     const int64_t want = (n_pos * a.half + 1023) / 1024;
-    return launch(table_kernel, want < 1216 ? want : 1216, 256, sizeof(double) * a.half,
+    return launch(table_kernel, dim3(static_cast<unsigned>(want < 1216 ? want : 1216)), 256, sizeof(double) * a.half,
                   reinterpret_cast<cudaStream_t>(stream), a) == cudaSuccess ? QK_OK : QK_ERR_CUDA;
 }
 
@@ -987,10 +999,9 @@ int qk_kv_read_q4(const qk_kv_cache_q4 *cache, const int64_t *slots, int64_t T, 
     a.err = library_error_word();
     if (!a.err) return QK_ERR_CUDA;
     constexpr int kThreads = kRowWarps * 32;
-    const int items = a.n_kv * ((k ? 1 : 0) + (v ? 1 : 0)) * (a.D / 8);
+    const int items = a.n_kv * (a.D / 8), parts = (items + kThreads - 1) / kThreads;
     a.tokens = items < kThreads ? kThreads / items : 1;
-    a.parts = (items + kThreads - 1) / kThreads;
-    const int64_t grid = (T + a.tokens - 1) / a.tokens * a.parts;
+    const dim3 grid(static_cast<unsigned>((T + a.tokens - 1) / a.tokens), static_cast<unsigned>(parts));
     const auto kern = a.D == 64 ? read_kernel<64> : a.D == 96 ? read_kernel<96> : a.D == 128 ? read_kernel<128> : read_kernel<256>;
     return launch(kern, grid, kThreads, 0, reinterpret_cast<cudaStream_t>(stream), a) == cudaSuccess ? QK_OK : QK_ERR_CUDA;
 }
