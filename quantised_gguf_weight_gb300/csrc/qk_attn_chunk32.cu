@@ -363,9 +363,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk32_kernel(const AttnArgs a)
         }
         tmem_st_wait();
     }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
+    if (softmax_warp || warp == kMmaWarp) {       // the dequantising warps need no query
+        tc_fence_before();
+        named_bar_sync(2, (kSoftmaxWarps + 1) * 32);
+        tc_fence_after();
+    }
     bool dead = false, poison = false;
 
     if (warp == kMmaWarp) {
