@@ -363,7 +363,7 @@ template <int RT, int D, class OutAt>
 __device__ __forceinline__ void join_parts(const AttnArgs &a, int c_first, int count, int rows, float *buf, int buf_floats,
                                            OutAt out_at)
 {
-    constexpr int part_floats = RT * D + 2 * RT, kThreads = kWarps * 32;
+    constexpr int part_floats = RT * D + 2 * RT, kThreads = kWarps * 32, kAhead = 20;
     auto part = [&](int p) { return a.parts + static_cast<int64_t>(c_first + p) * part_floats; };
     const int cols = rows * (D / 4);
     const int ways = cols >= kThreads ? 1 : kThreads / cols;
@@ -388,11 +388,18 @@ __device__ __forceinline__ void join_parts(const AttnArgs &a, int c_first, int c
                 m = m2, l *= f0, v.x *= f0, v.y *= f0, v.z *= f0, v.w *= f0;
                 for (int p = 0; p < n; ++p) l = fmaf(ex2(ml[2 * rows * p + 2 * row] - m), ml[2 * rows * p + 2 * row + 1], l);
                 const int start = ways > 1 ? way : 0;
-#pragma unroll 8
-                for (int p = start; p < n; p += ways) {
-                    const float f = ex2(ml[2 * rows * p + 2 * row] - m);
-                    const float4 x = __ldcg(reinterpret_cast<const float4 *>(part(p0 + p) + row * D + ch));
-                    v.x = fmaf(f, x.x, v.x), v.y = fmaf(f, x.y, v.y), v.z = fmaf(f, x.z, v.z), v.w = fmaf(f, x.w, v.w);
+                for (int p = start; p < n; p += kAhead * ways) {      // that many parts on their way at once
+                    float4 x[kAhead];
+#pragma unroll
+                    for (int k = 0; k < kAhead; ++k)
+                        x[k] = p + k * ways < n ? __ldcg(reinterpret_cast<const float4 *>(part(p0 + p + k * ways) + row * D + ch))
+                                                : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                    for (int k = 0; k < kAhead; ++k) {
+                        const float f = p + k * ways < n ? ex2(ml[2 * rows * (p + k * ways) + 2 * row] - m) : 0.0f;
+                        v.x = fmaf(f, x[k].x, v.x), v.y = fmaf(f, x[k].y, v.y);
+                        v.z = fmaf(f, x[k].z, v.z), v.w = fmaf(f, x[k].w, v.w);
+                    }
                 }
             }
         }
@@ -446,7 +453,23 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<G, PIECES, NT>::blocks_per_
     };
     int item = static_cast<int>(blockIdx.x / a.n_kv), hk = static_cast<int>(blockIdx.x) - item * a.n_kv;
     int b0 = 0, c_first = 0, active = 1, per = INT32_MAX;
-    if (a.cut) {
+    if (a.cut && a.items == 1) {
+        // one item: as below, without a scan
+        int why;
+        const int n = blocks_of(0, &why);
+        if (n == 0) {
+            if (why && blockIdx.x == 0)
+                for (int h = 0; h < a.n_kv; ++h) rows_without_blocks(0, h, why);
+            return;
+        }
+        const int room = a.cut - a.n_kv;
+        per = max((n * a.n_kv + room - 1) / room, 2 * kWarps);
+        active = (n + per - 1) / per;
+        if (static_cast<int>(blockIdx.x) >= active * a.n_kv) return;
+        item = 0, hk = static_cast<int>(blockIdx.x) / active;
+        const int split = static_cast<int>(blockIdx.x) - hk * active;
+        b0 = split * per, c_first = static_cast<int>(blockIdx.x) - split;
+    } else if (a.cut) {
         // Every item's blocks (below 2^31 in all: the host sees to it), two items a thread; from their sum the blocks
         // a split takes, so that all splits fit the thread blocks; then which split this one is.
         static_assert(kMaxItems <= 2 * kThreads, "two items a thread");
@@ -455,16 +478,12 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<G, PIECES, NT>::blocks_per_
         for (int k = 0; k < 2; ++k)
             if (2 * static_cast<int>(threadIdx.x) + k < a.items) n[k] = blocks_of(2 * threadIdx.x + k, &why[k]);
         int total = n[0] + n[1];
-        if (a.items > 1) {
-            total = __reduce_add_sync(0xFFFFFFFFu, total);
-            if (lane == 0) sums[warp] = total;
-            __syncthreads();
-            total = 0;
+        total = __reduce_add_sync(0xFFFFFFFFu, total);
+        if (lane == 0) sums[warp] = total;
+        __syncthreads();
+        total = 0;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) total += sums[w];
-        } else {
-            total = __shfl_sync(0xFFFFFFFFu, blocks_of(0, &why[1]), 0), why[1] = 0;
-        }
+        for (int w = 0; w < kWarps; ++w) total += sums[w];
         total *= a.n_kv;
         const int room = a.cut - a.items * a.n_kv;       // above 0: the host splits where heads are few
         per = max((total + room - 1) / room, 2 * kWarps);
@@ -475,7 +494,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<G, PIECES, NT>::blocks_per_
             const int below = __shfl_up_sync(0xFFFFFFFFu, run, o);
             if (lane >= o) run += below;
         }
-        if (a.items > 1) __syncthreads();
+        __syncthreads();
         if (threadIdx.x == 0) stand[0] = -1;
         if (lane == 31) sums[warp] = run;
         __syncthreads();
@@ -521,8 +540,8 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<G, PIECES, NT>::blocks_per_
     auto look_up = [&](int k) {
         addr = a.pages;
         if (k + lane < nk) {
-            const int64_t blk = span.blk_lo + b0 + warp + static_cast<int64_t>(kWarps) * (k + lane);
-            const int64_t pg = blk / a.page_blocks;
+            const uint32_t blk = static_cast<uint32_t>(span.blk_lo) + b0 + warp + kWarps * (k + lane);      // below 2^27
+            const uint32_t pg = blk / static_cast<uint32_t>(a.page_blocks);
             const int32_t page = a.page_table[b * a.ld_pages + pg];
             if (page < 0 || page >= a.n_pages) {
                 poison = true;
@@ -540,6 +559,16 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<G, PIECES, NT>::blocks_per_
             bulk_g2s(smem_u32(ring) + (k % NST) * Sh::block_bytes, addr, Sh::block_bytes, bar, policy);
         }
     };
+    // this warp's first query row is on its way meanwhile
+    auto load_row = [&](int row, float (&x)[G]) {
+        const bool in = row < rows;
+        const int i = in ? (first + row) / a.rep : 0;
+        const int64_t at = (r0 + i) * a.ldq + (static_cast<int64_t>(hk) * a.rep + (first + row - i * a.rep)) * D;
+#pragma unroll
+        for (int g = 0; g < G; ++g) x[g] = in ? load_as_float(a.q, at + 32 * g + lane, a.q_type) : 0.0f;
+    };
+    float x[G];
+    load_row(warp, x);
     if (nk > 0) look_up(0);
     for (int k = 0; k < NST && k < nk; ++k) issue(k);
 
@@ -551,15 +580,10 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<G, PIECES, NT>::blocks_per_
     float *col_init = reinterpret_cast<float *>(smem + Sh::init_at);     // [group][column]
     float *row_log2 = col_init + NT * 8 * G;                             // [row]
     for (int row = warp; row < RT; row += kWarps) {
-        const bool in = row < rows;
-        const int i = in ? (first + row) / a.rep : 0;
-        const int64_t at = (r0 + i) * a.ldq + (static_cast<int64_t>(hk) * a.rep + (first + row - i * a.rep)) * D;
-        float x[G], big = 0.0f;
+        if (row != warp) load_row(row, x);
+        float big = 0.0f;
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-            x[g] = in ? load_as_float(a.q, at + 32 * g + lane, a.q_type) : 0.0f;
-            big = fmaxf(big, fabsf(x[g]));
-        }
+        for (int g = 0; g < G; ++g) big = fmaxf(big, fabsf(x[g]));
         big = __uint_as_float(redux_max_u32(0xFFFFFFFFu, __float_as_uint(big)));
         int e = 127;
         if (big > 0.0f && big < INFINITY) e = 127 + 10 - (static_cast<int>(__float_as_uint(big) >> 23) - 127);
