@@ -40,12 +40,12 @@
 // 146.)
 //
 // What bounds it: instructions.  64 sequences of 8192 tokens, 8 heads of 128
-// with 4 queries each in bf16, are 604 MB in 146 us (4.1 TB/s, 61% of the copy
+// with 4 queries each in bf16, are 604 MB in 147 us (4.1 TB/s, 61% of the copy
 // rate): 354 warp instructions a block of 16 tokens, the integer pipe half and
 // the issue slots 61% busy with 16 warps an SM, a third of them taking nibbles
-// apart.  Short calls are their fixed part, 4 to 5 us of dependent reads
-// (lengths, page table, first blocks) and the join: 1 x 32768 20 us, 4 of them
-// before the first block.
+// apart.  Short calls are their fixed part, dependent reads (lengths, page
+// table, first blocks) and the join: 1 x 32768 18 us, 4 of them before the
+// first block, 6.5 over the keys, 5 for parts and join.
 #pragma once
 
 #include <atomic>
