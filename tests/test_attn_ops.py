@@ -388,6 +388,60 @@ def test_attn_cut_faults(qk, dtype):
     assert torch.equal(o, ref) and qk.device_error() == 0
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_cut_chunks_programmatic_and_graph(qk, dtype):
+    """Append and cut attention calls one after another, of other lengths on one workspace, under programmatic launch
+    and from a captured graph: the plain calls' bits."""
+    D, nkv, nq, page, n = 128, 2, 4, 16, 70
+    cache, tab, _, _ = make_cache(6, [1800, 900], nkv, D, page)
+    rot = table(2048, D)
+    qkv = rand(1, 2 * n, (nq + 2 * nkv) * D, dtype=dtype)
+    q, k, v = qkv.split([nq * D, nkv * D, nkv * D], 1)
+    ws = qk.attn_q4_workspace(2, nq, nkv, D, n, 1800)
+    lens = [torch.tensor(x, dtype=torch.int32).cuda() for x in ([1800, 900], [600, 880], [90, 71])]
+    steps = []
+    for l in lens:
+        at = (l[:, None] - n + torch.arange(n, dtype=torch.int32).cuda()).long()
+        slots = tab.long().gather(1, at // page) * page + at % page
+        steps.append((l, at.int().reshape(-1), slots.reshape(-1)))
+    base = cache.clone()
+    outs = [torch.empty(2 * n, nq * D, dtype=DT[dtype], device="cuda") for _ in lens]
+    qo = torch.empty(2 * n, nq * D, dtype=DT[dtype], device="cuda")
+
+    def run():
+        for (l, pos, slots), o in zip(steps, outs):
+            qk.kv_append_q4(cache, q, k, v, pos, slots, rot, q_out=qo)
+            qk.attn_q4(cache, qo, tab, l, max_q=n, max_len=1800, out=o, workspace=ws)
+
+    run()
+    want = [o.clone() for o in outs]
+    qk.set_programmatic_launch(True)
+    try:
+        for _ in range(10):
+            cache.copy_(base)
+            for o in outs:
+                o.zero_()
+            run()
+            assert all(torch.equal(o, w) for o, w in zip(outs, want))
+    finally:
+        qk.set_programmatic_launch(False)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            run()
+    for _ in range(3):
+        cache.copy_(base)
+        for o in outs:
+            o.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, w) for o, w in zip(outs, want))
+    assert qk.device_error() == 0
+
+
 def test_attn_fp32_chunk_strides(qk):
     """fp32 rows and outputs off 16-byte boundaries."""
     D, nq, n = 64, 6, 40
