@@ -109,8 +109,9 @@ __device__ __forceinline__ uint32_t pack_as(float lo, float hi, bool bf16)
 // block's; `per` is the longest item's blocks over one of kCuts, the one whose estimated time is least: of the
 // longest part, or of all parts over the GPU, with kPartFixed blocks' time for a part's start and end (about 15 us,
 // a block 0.26 us in 16 bits, 0.35 in fp32), and for cut heads the join of the parts.
-// 8 x 64 fp32 queries over up to 5000 keys, uneven: 108 us in whole heads, 78 us so; 1 x 64 over 16384 361 and 68, in 16 bits 266
-// and 42; 8 x 64 over 4096 each in 16 bits 78 and 68, but in fp32, where nothing can be cut, 105 and 115.
+// Whole and cut so: 8 x 64 fp32 queries over up to 5000 keys, uneven, 108 us and 78; 64 fp32 queries over 16384 keys
+// 361 and 62, bf16 266 and 40; 8 x 64 over 4096 keys each, bf16 78 and 66, but fp32, where nothing can be cut, 105
+// and 115.
 constexpr int kItems = 512;              // items of a call whose heads may be cut
 constexpr int kCutChoices = 16;
 constexpr float kPartFixed = 50.0f, kJoinFixed = 25.0f, kJoinBytes = 400.0e3f;      // in blocks; bytes a block's time
