@@ -222,6 +222,7 @@ __device__ __forceinline__ bool softmax_tile(Row &R, uint32_t tmem, int half, ui
             if (tile > 0) scale16(o_addr + 16 * c, factor);
             if (tile > kFlush) scale16(sum_addr + 16 * c, factor);
         }
+        tmem_st_wait();          // the flush below loads what these stores wrote, and nothing else orders the two
     }
 #pragma unroll
     for (int b = 0; b < 2; ++b) R.l = fmaf(sum[b], inv[b], R.l);
