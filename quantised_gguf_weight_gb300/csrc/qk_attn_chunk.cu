@@ -14,9 +14,13 @@
 // K' and V' are the cache's values in fp16, formed once for both row tiles
 // straight in the operands' 128-byte-swizzled layouts.
 //
-// Scales: K' = K 2^-kk and V' = V 2^-kt, kk and kt the exponents of a
-// 16-token block's largest scales, so fp16 holds both whatever their
-// magnitude; 2^kk goes to the scores and 2^kt to the exponents of P.  Each row
+// Scales: K' = K 2^-kk and V' = V 2^-kt, products (n - 8) (d 2^-kk) rounded
+// once to fp16, which holds them with all its 11 bits from 2^-20 up; kk and kt
+// are -6 but for 16-token blocks with scales of 2^6 and more (power_of).  (With
+// kk and kt from every block's largest scale, and n - 8 and its product in one
+// multiply-add below fp16's normal range, a group or token of scales 2^-12 of
+// the block's largest was 0.7% off, one of 2^-18 half.)  2^kk goes to the scores
+// and 2^kt to the exponents of P.  Each row
 // keeps a reference M (a whole number, so moving it scales by a power of
 // two): P = 2^(z + kt - M) stays below 2^14, and M moves only when that would
 // be passed, so most tiles need neither a row maximum nor a rescaling of O.
@@ -27,7 +31,7 @@
 // that the waits of one are covered by the products of the other.
 //
 // What bounds it: three things at once.  1024 queries of 32 heads of 128 over
-// 16384 keys, 8 key/value heads, 266 GFLOP, take 264 us (1.0 PFLOP/s, 53% of
+// 16384 keys, 8 key/value heads, 266 GFLOP, take 268 us (1.0 PFLOP/s, 52% of
 // the cuBLAS rate); a tile of 64 keys for 256 rows is 2000 cycles, of which the
 // softmax warps work 1790, the dequantising ones 1650 and the tensor cores
 // 1250 (busy 62% of the time where a thread block is: 128 of 152 SMs).
@@ -45,7 +49,12 @@ constexpr int kThreads = 16 * 32;
 constexpr int kStages = 3;                 // tiles of K' and of V'
 constexpr int kMetas = 8;                  // tiles whose exponents are kept: more than stages and tiles at work
 constexpr int kSlots = 2 * kDequantWarps;  // raw blocks in flight: two a dequantising warp, its own
-constexpr float kTwo24 = 16777216.0f;
+
+// The power of two taken off the scales of a 16-token block whose largest has the fp16 bits `top`.  Times 2^6 an fp16
+// scale is below 2^12, and its products with n - 8 in fp16's range, up to 2^6; above it more is taken off.  It is the
+// same for nearly every block: a row's probabilities carry the values' power, and where one block took off much more
+// than the others, theirs would sink below fp16's range.
+__device__ __forceinline__ int power_of(uint32_t top) { return max(static_cast<int>(top >> 10) - 26, -6); }
 
 template <int G>
 struct ChunkShape {
@@ -60,7 +69,7 @@ struct ChunkShape {
     static constexpr int q2_at = v_at + kStages * v_bytes;
     static constexpr int raw_at = q2_at + (q2_in_smem ? kblocks * 128 * 128 : 0);
     static constexpr int scale_at = raw_at + kSlots * block_bytes;   // the dequantising warps' scaled scales
-    static constexpr int scale_bytes = (16 + 6) * 16 * G;            // 3 fp16 pairs of 4 a key scale, 3 rows of values'
+    static constexpr int scale_bytes = (4 + 2) * 16 * G;             // a fp16 pair a key scale, a row of values' a group
     static constexpr int meta_at = scale_at + kDequantWarps * scale_bytes;       // [tile % kMetas][block] (2^kk, kt, 2^-kt, 0)
     static constexpr int bars_at = meta_at + kMetas * kTileBlocks * 16;
     static constexpr int flags_at = bars_at + (kSlots + 4 * kStages + 8) * 8;
@@ -412,14 +421,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttnArgs a)
             }
             top_k = redux_max_u32(0xFFFFFFFFu, top_k);
             top_v = redux_max_u32(0xFFFFFFFFu, top_v);
-            // largest scale in [2^e, 2^(e+1)); a subnormal or 0 counts as 2^-15
-            const int ek = static_cast<int>(top_k >> 10) - 15;
-            const int ev = static_cast<int>(top_v >> 10) - 15;
-            const float down_k = __uint_as_float(static_cast<uint32_t>(127 - ek - 9) << 23);
-            const float down_v = __uint_as_float(static_cast<uint32_t>(127 - ev - 9) << 23);
-            // A nibble under a mask is the fp16 subnormal n 2^-24 (or 16 n 2^-24), so (n - 8) s is one multiply-add,
-            // rounded once: n 2^-24 * (s 2^24) - 8 s.  For s 2^24 to be an fp16, s is the scale over 2^(e + 9): below
-            // 2^-8, its products of at least 2^-14 normal for scales down to 1/32 of the block's largest.
+            const int kk = power_of(top_k), kt = power_of(top_v);
+            const float down_k = __uint_as_float(static_cast<uint32_t>(127 - kk) << 23);
+            const float down_v = __uint_as_float(static_cast<uint32_t>(127 - kt) << 23);
             if (scale_lane) {
                 float sv[2];
 #pragma unroll
@@ -428,21 +432,17 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttnArgs a)
                     // a value scale that is not finite counts as 0, and makes the key's scores NaN (below), and with
                     // them the rows that see it
                     sv[e] = odd >> e & 1 ? 0.0f : half_bits_to_float(dv[e]) * down_v;
-                    const float s24 = sk * kTwo24, s20 = sk * (kTwo24 / 16.0f), s8 = sk * -8.0f;
-                    sts128(scales + 16 * ((st + e) * G + sg), pack_half(s24, s24), pack_half(s20, s20), pack_half(s8, s8), 0u);
+                    sts32(scales + 4 * ((st + e) * G + sg), pack_half(sk, sk));
                 }
-                const uint32_t to = scales + 256 * G + 2 * (16 * sg + st);
-                sts32(to, pack_half(sv[0] * kTwo24, sv[1] * kTwo24));
-                sts32(to + 32 * G, pack_half(sv[0] * (kTwo24 / 16.0f), sv[1] * (kTwo24 / 16.0f)));
-                sts32(to + 64 * G, pack_half(sv[0] * -8.0f, sv[1] * -8.0f));
+                sts32(scales + 64 * G + 2 * (16 * sg + st), pack_half(sv[0], sv[1]));
             }
             if (lane == 0)
-                sts128(sb + Sh::meta_at + (i % kMetas * kTileBlocks + bi) * 16, static_cast<uint32_t>(127 + ek + 9) << 23,
-                       __float_as_uint(static_cast<float>(ev + 9)), __float_as_uint(down_v), 0u);
+                sts128(sb + Sh::meta_at + (i % kMetas * kTileBlocks + bi) * 16, static_cast<uint32_t>(127 + kk) << 23,
+                       __float_as_uint(static_cast<float>(kt)), __float_as_uint(down_v), 0u);
             __syncwarp();
             if (__any_sync(0xFFFFFFFFu, odd)) {
                 for (int e = 0; e < 2; ++e)
-                    if (odd >> e & 1) sts128(scales + 16 * ((st + e) * G), 0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu, 0u);
+                    if (odd >> e & 1) sts32(scales + 4 * ((st + e) * G), 0x7FFF7FFFu);
                 __syncwarp();
             }
             // keys: lane (r, c) has token 4(r/2) + 2h + r%2, channels 32g + 8c..8c+7 a word
@@ -457,12 +457,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttnArgs a)
                     // odd r take the groups in pairs the other way round: a quarter of the warp then writes all eight
                     // 16-byte columns
                     const uint32_t word = G % 2 == 0 && swap ? words[g ^ (G % 2 == 0)] : words[g], high = word >> 8;
-                    uint32_t sc[4];      // s 2^24, s 2^20, -8 s
-                    lds128(sc, scales + 16 * ((key_token + 2 * h) * G + (g ^ swap)));
+                    const uint32_t s = lds32(scales + 4 * ((key_token + 2 * h) * G + (g ^ swap)));
                     // chunk 4 (g ^ swap) + c of row t, 16 bytes each: its column of 8 is xored with t % 8
                     const uint32_t at = kb + (g >> 1) * (kTile * 128) + h * 256 + (key_at[h] ^ ((g & 1) << 6));
-                    sts128(at, fma_half2(word & 0x000F000Fu, sc[0], sc[2]), fma_half2(word & 0x00F000F0u, sc[1], sc[2]),
-                           fma_half2(high & 0x000F000Fu, sc[0], sc[2]), fma_half2(high & 0x00F000F0u, sc[1], sc[2]));
+                    sts128(at, mul_half2(signed_nibbles<0>(word), s), mul_half2(signed_nibbles<1>(word), s),
+                           mul_half2(signed_nibbles<0>(high), s), mul_half2(signed_nibbles<1>(high), s));
                 }
             }
             fence_proxy_async_smem();
@@ -485,10 +484,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttnArgs a)
             for (int k = 0; k < kItems; ++k) {
                 const int g = group_of(k);
                 if (G != 3 || g < G) {
-                    uint32_t s0[4], s1[4], s8[4];
-                    lds128(s0, scales + 256 * G + 2 * (16 * g + 8 * kp));
-                    lds128(s1, scales + 288 * G + 2 * (16 * g + 8 * kp));
-                    lds128(s8, scales + 320 * G + 2 * (16 * g + 8 * kp));
+                    uint32_t s[4];
+                    lds128(s, scales + 64 * G + 2 * (16 * g + 8 * kp));
 #pragma unroll
                     for (int half_j = 0; half_j < 2; ++half_j) {
                         uint32_t src[4];
@@ -501,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttnArgs a)
                             uint32_t x[4];
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
-                                x[e] = jj ? fma_half2(src[e] & 0x00F000F0u, s1[e], s8[e]) : fma_half2(src[e] & 0x000F000Fu, s0[e], s8[e]);
+                                x[e] = mul_half2(jj ? signed_nibbles<1>(src[e]) : signed_nibbles<0>(src[e]), s[e]);
                             sts128(vb + ((row ^ (jj ? 128 + 16 : 0)) ^ column), x[0], x[1], x[2], x[3]);
                         }
                     }

@@ -55,6 +55,14 @@ __device__ __forceinline__ void lds128(uint32_t (&w)[4], uint32_t addr)
                  : "r"(addr));
 }
 
+// Products of fp16 pairs, rounded once, subnormals kept.
+__device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
 // a * b + c on fp16 pairs, rounded once, subnormals kept.
 __device__ __forceinline__ uint32_t fma_half2(uint32_t a, uint32_t b, uint32_t c)
 {

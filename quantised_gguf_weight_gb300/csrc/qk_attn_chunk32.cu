@@ -95,13 +95,6 @@ struct Bars {
     __device__ __forceinline__ uint32_t odone() const { return at + 8 * (kSlots + 4 * kStages + 3); }
 };
 
-__device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b)
-{
-    uint32_t r;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-
 // m s of fp16 pairs in two pieces: the rounded product, and what it left (exact).
 __device__ __forceinline__ void two_pieces(uint32_t m, uint32_t s, uint32_t &lead, uint32_t &rest)
 {
