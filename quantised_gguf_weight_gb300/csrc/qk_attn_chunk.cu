@@ -50,12 +50,6 @@ constexpr int kStages = 3;                 // tiles of K' and of V'
 constexpr int kMetas = 8;                  // tiles whose exponents are kept: more than stages and tiles at work
 constexpr int kSlots = 2 * kDequantWarps;  // raw blocks in flight: two a dequantising warp, its own
 
-// The power of two taken off the scales of a 16-token block whose largest has the fp16 bits `top`.  Times 2^6 an fp16
-// scale is below 2^12, and its products with n - 8 in fp16's range, up to 2^6; above it more is taken off.  It is the
-// same for nearly every block: a row's probabilities carry the values' power, and where one block took off much more
-// than the others, theirs would sink below fp16's range.
-__device__ __forceinline__ int power_of(uint32_t top) { return max(static_cast<int>(top >> 10) - 26, -6); }
-
 template <int G>
 struct ChunkShape {
     static constexpr int D = 32 * G;

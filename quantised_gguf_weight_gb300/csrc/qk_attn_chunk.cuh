@@ -71,6 +71,12 @@ __device__ __forceinline__ uint32_t fma_half2(uint32_t a, uint32_t b, uint32_t c
     return r;
 }
 
+// The power of two taken off the scales of a 16-token block whose largest has the fp16 bits `top`.  Times 2^6 an fp16
+// scale is below 2^12, and its products with n - 8 in fp16's range, up to 2^6; above it more is taken off.  It is the
+// same for nearly every block: a row's probabilities carry the values' power, and where one block took off much more
+// than the others, theirs would sink below fp16's range.
+__device__ __forceinline__ int power_of(uint32_t top) { return max(static_cast<int>(top >> 10) - 26, -6); }
+
 __device__ __forceinline__ void lds64(uint32_t &a, uint32_t &b, uint32_t addr)
 {
     asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(a), "=r"(b) : "r"(addr));

@@ -24,9 +24,11 @@
 // 128 channels) is in tensor memory: S 64 columns, P1, P2 32 each, Q1, Q2 and
 // both accumulators D/2 and D each, 512 at 128 channels.
 //
-// Scales, references and masks are as in the 16-bit form: K' = K 2^-kk with kk
-// from a 16-token block's largest scale, here brought to [2^10, 2^11), so that
-// scales down to 2^-24 of it keep all their bits.
+// Scales, references and masks are as in the 16-bit form: K' = K 2^-kk and V'
+// = V 2^-kt, whose two pieces hold all their bits.  kk and kt are the same for
+// nearly all 16-token blocks.  (With those of each block's largest scale, a
+// block with one value 2^16 above the others, of no weight itself, left the other
+// blocks' probabilities 2^-16 smaller, and fp32 outputs 1e-4 off.)
 //
 // Warps: 0-7 softmax (a thread is a row and half of a tile's keys, and for the
 // accumulators half of the channels), 8-14 dequantisation (each takes every
@@ -497,11 +499,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk32_kernel(const AttnArgs a)
             }
             top_k = redux_max_u32(0xFFFFFFFFu, top_k);
             top_v = redux_max_u32(0xFFFFFFFFu, top_v);
-            // largest scale in [2^e, 2^(e+1)), a subnormal or 0 counts as 2^-15; brought to [2^10, 2^11)
-            const int ek = static_cast<int>(top_k >> 10) - 15;
-            const int ev = static_cast<int>(top_v >> 10) - 15;
-            const float down_k = __uint_as_float(static_cast<uint32_t>(127 - ek + 10) << 23);
-            const float down_v = __uint_as_float(static_cast<uint32_t>(127 - ev + 10) << 23);
+            const int kk = power_of(top_k), kt = power_of(top_v);
+            const float down_k = __uint_as_float(static_cast<uint32_t>(127 - kk) << 23);
+            const float down_v = __uint_as_float(static_cast<uint32_t>(127 - kt) << 23);
             if (scale_lane) {
                 float sv[2];
 #pragma unroll
@@ -515,8 +515,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk32_kernel(const AttnArgs a)
                 sts32(scales + 64 * G + 32 * G * (n & 1) + 2 * (16 * sg + st), pack_half(sv[0], sv[1]));
             }
             if (lane == 0)
-                sts128(sb + Sh::meta_at + (i % kMetas * kTileBlocks + bi) * 16, static_cast<uint32_t>(127 + ek - 10) << 23,
-                       __float_as_uint(static_cast<float>(ev - 10)), __float_as_uint(down_v), 0u);
+                sts128(sb + Sh::meta_at + (i % kMetas * kTileBlocks + bi) * 16, static_cast<uint32_t>(127 + kk) << 23,
+                       __float_as_uint(static_cast<float>(kt)), __float_as_uint(down_v), 0u);
             __syncwarp();
             if (__any_sync(0xFFFFFFFFu, odd)) {
                 for (int e = 0; e < 2; ++e)
