@@ -23,7 +23,10 @@
 // probabilities.
 //
 // fp32 queries keep fp32 accuracy: a row's query (and probability) is two
-// fp16 pieces of 22 bits together, in neighbouring columns.
+// fp16 pieces of 22 bits together, in neighbouring columns.  A probability's
+// second piece is held 2^11 times as large: what fp16's least value cuts off is
+// below 2^-36, next to leading terms of 2^7 and more.  (At 2^-25, a group of
+// values 2^-16 of the largest was 5e-5 off.)
 //
 // The softmax is one pass: P_j = 2^(z_j - M) against a reference M that moves
 // only when a P could leave fp16's range next to its value scale, so most
@@ -57,6 +60,7 @@ namespace qk {
 namespace attn {
 
 constexpr float kTwo24 = 16777216.0f;
+constexpr float kRest = 2048.0f;      // what a probability's second piece is multiplied by
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
@@ -313,23 +317,24 @@ __device__ __forceinline__ void block16(State<G, PIECES, NT> &S, const Query<G, 
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 uint32_t b[2];
+                float x[2][NR];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float x[NR];
+                for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int r = 0; r < NR; ++r) {
-                        x[r] = p[n][h][r] * dv[h][g];
+                        x[h][r] = p[n][h][r] * dv[h][g];
                         if (MASK) {   // 0 * (a scale that is not of a key the row sees) may be NaN
                             const int t = key0 + tok + 2 * h;
-                            if (t < Q.lo[n][r] || t >= Q.hi[n][r]) x[r] = 0.0f;
+                            if (t < Q.lo[n][r] || t >= Q.hi[n][r]) x[h][r] = 0.0f;
                         }
                     }
-                    if constexpr (PIECES == 2) {     // the leading 11 bits, and the rest
-                        const float lead = __uint_as_float(__float_as_uint(x[0]) & 0xFFFFE000u);
-                        b[h] = transpose8(pack_half(lead, x[0] - lead));
-                    } else {
-                        b[h] = transpose8(pack_half(x[0], x[NR - 1]));
-                    }
+                if constexpr (PIECES == 2) {     // rounded to 11 bits, and what that left, times kRest
+                    const uint32_t lead = pack_half(x[0][0], x[1][0]);
+                    const float2 l = __half22float2(*reinterpret_cast<const __half2 *>(&lead));
+                    const uint32_t rest = pack_half((x[0][0] - l.x) * kRest, (x[1][0] - l.y) * kRest);
+                    b[0] = transpose8(__byte_perm(lead, rest, 0x5410)), b[1] = transpose8(__byte_perm(lead, rest, 0x7632));
+                } else {
+                    b[0] = transpose8(pack_half(x[0][0], x[0][NR - 1])), b[1] = transpose8(pack_half(x[1][0], x[1][NR - 1]));
                 }
                 mma_f16(S.o[n][g][0], a0, b[0], b[1]);
                 mma_f16(S.o[n][g][1], a1, b[0], b[1]);
@@ -710,7 +715,8 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<G, PIECES, NT>::blocks_per_
                 for (int m = 0; m < 2; ++m)
 #pragma unroll
                     for (int x = 0; x < 2; ++x)
-                        v[m + 2 * x] = PIECES == 2 ? S.o[n][g][m][2 * x] + S.o[n][g][m][2 * x + 1] : S.o[n][g][m][2 * x + r];
+                        v[m + 2 * x] = PIECES == 2 ? fmaf(S.o[n][g][m][2 * x + 1], 1.0f / kRest, S.o[n][g][m][2 * x])
+                                                   : S.o[n][g][m][2 * x + r];
                 *reinterpret_cast<float4 *>(part + row * Sh::part_stride + 32 * g + 4 * r8) =
                     make_float4(v[0], v[1], v[2], v[3]);
             }

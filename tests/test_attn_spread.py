@@ -54,7 +54,7 @@ KINDS = ["key groups", "value groups", "late key", "late value", "ignored value"
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("dtype,D,n", [("bf16", 64, 80), ("bf16", 96, 80), ("bf16", 128, 300), ("f16", 128, 80),
                                        ("f32", 64, 80), ("f32", 96, 80), ("f32", 128, 300), ("bf16", 128, 70),
-                                       ("f16", 64, 9), ("bf16", 256, 70)])
+                                       ("f32", 128, 9), ("f16", 64, 9), ("bf16", 256, 70)])
 def test_scales_apart(qk, dtype, D, n, kind, r):
     nkv, rep = 1, 2
     g = np.random.default_rng(r + D + n)
