@@ -464,7 +464,7 @@ int qk_attn_q4(const qk_kv_cache_q4 *cache, const void *q, int64_t ldq, int q_ty
                int64_t window, void *out, int64_t ldo, int out_type, void *workspace, size_t workspace_bytes,
                qk_stream_t stream);
 
-/* Workspace bytes that a qk_attn_q4 call of these sizes can make use of. */
+/* Workspace bytes that a qk_attn_q4 call of these sizes can make use of; max_len 0: of any length. */
 size_t qk_attn_q4_workspace_bytes(int64_t B, int n_q_heads, int n_kv_heads, int head_dim, int64_t max_q,
                                   int64_t max_len);
 

@@ -114,14 +114,20 @@ size_t qk_attn_q4_workspace_bytes(int64_t B, int n_q_heads, int n_kv_heads, int 
                                   int64_t max_len)
 {
     if (B <= 0 || n_kv_heads <= 0 || n_q_heads <= 0 || n_q_heads % n_kv_heads || head_dim <= 0 || max_q <= 0 ||
-        max_len <= 0 || B > INT32_MAX / max_q)
+        max_len < 0 || B > INT32_MAX / max_q)
         return 0;
     size_t most = 0;
-    for (const int type : {QK_F32, QK_F16, QK_BF16}) {
-        const Cut c = cut_for(B, n_kv_heads, n_q_heads / n_kv_heads, head_dim, max_q, max_len, max_len, type);
-        const size_t n = c.cut ? kHead + c.cut * part_bytes_of(c, head_dim) : 0;
-        if (n > most) most = n;
-    }
+    const auto of_length = [&](int64_t len) {
+        for (const int type : {QK_F32, QK_F16, QK_BF16}) {
+            const Cut c = cut_for(B, n_kv_heads, n_q_heads / n_kv_heads, head_dim, max_q, len, len, type);
+            const size_t n = c.cut ? kHead + c.cut * part_bytes_of(c, head_dim) : 0;
+            if (n > most) most = n;
+        }
+    };
+    // a cut's bytes do not depend on the length, only whether there is one
+    if (max_len > 0) of_length(max_len);
+    else
+        for (int64_t len = 256; len < INT32_MAX; len *= 2) of_length(len);
     return most;
 }
 

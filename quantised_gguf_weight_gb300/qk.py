@@ -473,7 +473,7 @@ def kv_read_q4(cache: torch.Tensor, slots: torch.Tensor, dtype: torch.dtype = to
 
 def attn_q4_workspace(B: int, n_q_heads: int, n_kv_heads: int, head_dim: int, max_q: int = 1, max_len: int = 0,
                       device=None) -> torch.Tensor:
-    """Zeroed scratch for attn_q4 calls of these sizes (one for each stream that calls)."""
+    """Zeroed scratch for attn_q4 calls of these sizes (one for each stream that calls); max_len 0: of any length."""
     n = load().qk_attn_q4_workspace_bytes(B, n_q_heads, n_kv_heads, head_dim, max_q, max_len)
     return torch.zeros(max(256, n), dtype=torch.uint8, device=device or "cuda")
 
