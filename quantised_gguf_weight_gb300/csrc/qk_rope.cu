@@ -177,7 +177,8 @@ __device__ __forceinline__ void norm_rotate(float (&x)[NV][4], const RowsArgs &a
 }
 
 // Four channels of a head to the cache: the group's scale over its 8 lanes,
-// then the lane's four nibbles as two bytes.
+// then the lane's four nibbles (of the exact quotients, as nibbles_of has them)
+// as two bytes.
 __device__ __forceinline__ void store_nibbles(uint8_t *block, int D, int t, int ch, bool active, const float (&x)[4],
                                               bool is_key, int lane)
 {
@@ -202,8 +203,12 @@ __device__ __forceinline__ void store_nibbles(uint8_t *block, int D, int t, int 
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         float n = 8.0f;
-        if (d != 0.0f && !group_odd)
-            n = fminf(fmaxf(floorf(__fadd_rn(__fdiv_rn(x[e], d), 8.5f)), 0.0f), 15.0f);
+        if (d != 0.0f && !group_odd) {
+            // the rounded quotient and sum may have reached the next edge, (n - 8.5) d: then x lies below it
+            n = floorf(__fadd_rn(__fdiv_rn(x[e], d), 8.5f));
+            if (fmaf(8.5f - n, fabsf(d), copysignf(1.0f, d) * x[e]) < 0.0f) n -= 1.0f;
+            n = fminf(fmaxf(n, 0.0f), 15.0f);
+        }
         bits |= static_cast<uint32_t>(n) << (4 * e);
     }
     const Kv4Place p = is_key ? kv4_key_place(D, t, ch) : kv4_value_place(D, t, ch);

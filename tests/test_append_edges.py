@@ -1,0 +1,61 @@
+"""What the append stores for values next to a nibble's edge, wherever the rows lie: floor(x / d + 8.5) of the exact
+quotient, byte for byte the 64-bit oracle's."""
+import numpy as np
+import pytest
+import torch
+
+from tests import kv4_oracle as ko
+from tests.test_attn_ops import table
+
+pytestmark = pytest.mark.gpu
+
+
+def edge_rows(seed, T, heads, D):
+    """fp32 rows whose groups hold a value that sets the scale and others on an edge, one step below it and one above."""
+    g = np.random.default_rng(seed)
+    d = (g.uniform(0.5, 1, (T, heads, D // 32, 1)) * 2.0 ** g.integers(-13, 9, (T, heads, D // 32, 1))).astype(np.float16)
+    d = d.astype(np.float32) * np.where(g.random(d.shape) < 0.5, 1, -1).astype(np.float32)
+    x = ((g.integers(1, 16, (T, heads, D // 32, 32)) - np.float32(8.5)) * d).astype(np.float32)      # exact
+    side = g.integers(-1, 2, x.shape)
+    x = np.where(side < 0, np.nextafter(x, np.float32(-np.inf)), np.where(side > 0, np.nextafter(x, np.float32(np.inf)), x))
+    x[..., 5:6] = -8 * d
+    return x.reshape(T, heads * D).astype(np.float32)
+
+
+def place(x, off, pad):
+    """The rows inside a wider buffer, `off` elements from its start."""
+    buf = torch.zeros(x.shape[0], x.shape[1] + pad, device="cuda")
+    buf[:, off:off + x.shape[1]] = torch.from_numpy(x).cuda()
+    return buf[:, off:off + x.shape[1]]
+
+
+@pytest.mark.parametrize("nkv,D", [(8, 128), (3, 64), (2, 96), (1, 256)])
+def test_edges(qk, nkv, D):
+    T, page = 300, 32
+    k, v = edge_rows(D, T, nkv, D), edge_rows(D + 1, T, nkv, D)
+    pages = -(-T // page)
+    as_pages = [np.concatenate([t.reshape(T, nkv, D), np.zeros((pages * page - T, nkv, D))]).reshape(pages, page, nkv, D)
+                .transpose(0, 2, 1, 3) for t in (k, v)]
+    want = ko.pack(*ko.quantise(as_pages[0]), *ko.quantise(as_pages[1]))
+    empty = ko.pack(*ko.quantise(as_pages[0] * 0), *ko.quantise(as_pages[1] * 0))
+    for off, pad in ((0, 0), (4, 4), (1, 1), (2, 7)):      # the last two rule out wide loads
+        cache = torch.from_numpy(empty).cuda()
+        qk.kv_append_q4(cache, None, place(k, off, pad), place(v, off, pad), None, torch.arange(T).cuda(), None)
+        got = cache.cpu().numpy()
+        assert (got != want).sum() == 0, f"offset {off}"
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rotated_keys_are_the_same_bytes_anywhere(qk, interleaved):
+    """Without a norm every product and sum is rounded by itself: rows off a boundary are stored as aligned ones."""
+    T, nkv, D, page = 200, 4, 128, 64
+    g = torch.Generator().manual_seed(4)
+    k = torch.randn(T, nkv * D, generator=g).numpy()
+    pos = torch.randint(0, 500, (T,), generator=g).int().cuda()
+    got = []
+    for off, pad in ((0, 0), (3, 5)):
+        cache = qk.kv_cache_q4(-(-T // page), nkv, page, D)
+        kv = place(k, off, pad)
+        qk.kv_append_q4(cache, None, kv, kv, pos, torch.arange(T).cuda(), table(500, D), interleaved=interleaved)
+        got.append(cache)
+    assert torch.equal(*got) and qk.device_error() == 0
