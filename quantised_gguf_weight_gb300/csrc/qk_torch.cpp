@@ -9,6 +9,7 @@
 
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -128,9 +129,17 @@ qk_stream_t stream_of(PyObject *o)
     return reinterpret_cast<qk_stream_t>(int_of(o));
 }
 
-at::Tensor new_rows(int64_t n, int64_t width, const at::Tensor &like, at::ScalarType type)
+// New memory that a call on `stream` writes.  It is that stream's, so that nothing queued on another still uses it, and
+// is not given out again before what the current stream has queued by the time it is freed is done.
+at::Tensor new_rows(int64_t n, int64_t width, const at::Tensor &like, at::ScalarType type, PyObject *stream)
 {
-    return at::empty({n, width}, like.options().dtype(type));
+    if (stream == Py_None) return at::empty({n, width}, like.options().dtype(type));
+    const auto current = c10::cuda::getCurrentCUDAStream();
+    const auto own = c10::cuda::getStreamFromExternal(reinterpret_cast<cudaStream_t>(stream_of(stream)), like.get_device());
+    const c10::cuda::CUDAStreamGuard guard(own);
+    const at::Tensor t = at::empty({n, width}, like.options().dtype(type));
+    t.record_stream(current);
+    return t;
 }
 
 // A status other than QK_OK, as an int; else the result.
@@ -155,7 +164,7 @@ PyObject *norm_rope(PyObject *, PyObject *const *a, Py_ssize_t n)
     const Rows x = rows_of(xt, width, "x");
     at::Tensor made;
     const bool given = a[10] != Py_None;
-    if (!given) made = new_rows(x.n, width, xt, xt.scalar_type());
+    if (!given) made = new_rows(x.n, width, xt, xt.scalar_type(), a[11]);
     const Rows y = rows_of(given ? tensor_of(a[10], "y", dev) : made, width, "y");
     TORCH_CHECK_VALUE(y.n >= x.n, "y has ", y.n, " rows, x ", x.n);
     const Table t = table_of(a[5], a[4], x.n, D, dev);
@@ -192,7 +201,7 @@ PyObject *kv_append_q4(PyObject *, PyObject *const *a, Py_ssize_t n)
         q = rows_of(qt, wq, "q");
         TORCH_CHECK_VALUE(q.type == k.type, "q and k must have one element type");
         TORCH_CHECK_VALUE(q.n == k.n, "q has ", q.n, " rows, k ", k.n);
-        if (!given) made = new_rows(q.n, wq, qt, qt.scalar_type());
+        if (!given) made = new_rows(q.n, wq, qt, qt.scalar_type(), a[12]);
         qo = rows_of(given ? tensor_of(a[11], "q_out", dev) : made, wq, "q_out");
         TORCH_CHECK_VALUE(qo.n >= q.n, "q_out has ", qo.n, " rows, q ", q.n);
         heads = static_cast<int>(wq / D);
@@ -218,7 +227,7 @@ PyObject *kv_read_q4(PyObject *, PyObject *const *a, Py_ssize_t n)
     const int type = int32_of(a[2], "type");
     const at::ScalarType st = type == QK_F32 ? at::kFloat : (type == QK_F16 ? at::kHalf : at::kBFloat16);
     const at::Tensor &like = THPVariable_Unpack(a[0]);
-    const at::Tensor k = new_rows(T, width, like, st), v = new_rows(T, width, like, st);
+    const at::Tensor k = new_rows(T, width, like, st, a[3]), v = new_rows(T, width, like, st, a[3]);
     const int status = qk_kv_read_q4(&c, slots, T, k.data_ptr(), 0, v.data_ptr(), 0, type, stream_of(a[3]));
     if (status != QK_OK) return PyLong_FromLong(status);
     PyObject *pair = PyTuple_New(2);
@@ -252,7 +261,7 @@ PyObject *attn_q4(PyObject *, PyObject *const *a, Py_ssize_t n)
                       pages, " apart, got ", pt.strides());
     at::Tensor made;
     const bool given = a[9] != Py_None;
-    if (!given) made = new_rows(q.n, width, qt, qt.scalar_type());
+    if (!given) made = new_rows(q.n, width, qt, qt.scalar_type(), a[11]);
     const Rows o = rows_of(given ? tensor_of(a[9], "out", dev) : made, width, "out");
     TORCH_CHECK_VALUE(o.n >= q.n, "out has ", o.n, " rows, q ", q.n);
     void *workspace = nullptr;

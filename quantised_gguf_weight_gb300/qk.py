@@ -146,6 +146,18 @@ def _stream(stream) -> int:
     return int(stream)
 
 
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """New memory that a call on `stream` writes.  It is that stream's, so that nothing queued on another still uses it,
+    and is not given out again before what the current stream has queued by the time it is freed is done."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+    with torch.cuda.stream(s):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream())
+    return t
+
+
 def row_bytes(fmt: str, K: int) -> int:
     lib = load()
     return int({"q8_0": lib.qk_row_bytes_q8_0, "q4_k": lib.qk_row_bytes_q4_k, "q6_k": lib.qk_row_bytes_q6_k}[fmt](K))
@@ -222,7 +234,7 @@ def _qmatvec(name: str, w: torch.Tensor, row_offset: int, rows: int, K: int, x: 
     if rows > 0 and row_offset >= 0:
         _check_w(w, row_offset + rows, _fmt_row_bytes(name[-4:], K))
     if y is None:
-        y = torch.empty((batch, rows), dtype=torch.float32, device=x.device)
+        y = _empty((batch, rows), torch.float32, x.device, stream)
         ldy = rows
     if rows > 0:
         _check_out(y, batch, rows, ldy)
@@ -254,7 +266,7 @@ def qmatvec_swiglu(fmt: str, w: torch.Tensor, gate_offset: int, up_offset: int, 
     if F > 0 and gate_offset >= 0 and up_offset >= 0:
         _check_w(w, max(gate_offset, up_offset) + F, _fmt_row_bytes(fmt, K))
     if h is None:
-        h = torch.empty((batch, F), dtype=torch.float32, device=x.device)
+        h = _empty((batch, F), torch.float32, x.device, stream)
         ldh = F
     if F > 0:
         _check_out(h, batch, F, ldh, "h")
@@ -281,7 +293,7 @@ def qmatvec_experts(fmt: str, w: torch.Tensor, n_experts: int, rows: int, K: int
     if n_experts > 0 and rows > 0:
         _check_w(w, n_experts * rows, _fmt_row_bytes(fmt, K))
     if y is None:
-        y = torch.empty((n_assign, rows), dtype=torch.float32, device=x.device)
+        y = _empty((n_assign, rows), torch.float32, x.device, stream)
         ldy = rows
     if n_assign > 0 and rows > 0:
         _check_out(y, n_assign, rows, ldy)
@@ -309,12 +321,12 @@ def _gemm(name: str, w: torch.Tensor, row_offset: int, N: int, K: int, x: torch.
     if N > 0 and row_offset >= 0:
         _check_w(w, row_offset + N, _fmt_row_bytes("q8_0" if "q8_0" in name else "q4_k", K))
     if y is None:
-        y = torch.empty((M, N), dtype=torch.float32, device=x.device)
+        y = _empty((M, N), torch.float32, x.device, stream)
         ldy = N
     if N > 0 and M > 0:
         _check_out(y, M, N, ldy)
     if workspace is None:
-        workspace = torch.empty(gemm_workspace_bytes(M, N, K), dtype=torch.uint8, device=x.device)
+        workspace = _empty(gemm_workspace_bytes(M, N, K), torch.uint8, x.device, stream)
     _on_device(workspace, "workspace")
     st = getattr(load(), name)(w.data_ptr(), row_offset, N, K, x.data_ptr(), M, y.data_ptr(), ldy,
                                workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream))
@@ -359,12 +371,12 @@ def qgemm_swiglu(fmt: str, w: torch.Tensor, gate_offset: int, up_offset: int, F:
     if F > 0 and gate_offset >= 0 and up_offset >= 0:
         _check_w(w, max(gate_offset, up_offset) + F, _fmt_row_bytes(fmt, K))
     if h is None:
-        h = torch.empty((M, F), dtype=torch.float32, device=x.device)
+        h = _empty((M, F), torch.float32, x.device, stream)
         ldh = F
     if F > 0 and M > 0:
         _check_out(h, M, F, ldh, "h")
     if workspace is None:
-        workspace = torch.empty(gemm_workspace_bytes(M, F, K), dtype=torch.uint8, device=x.device)
+        workspace = _empty(gemm_workspace_bytes(M, F, K), torch.uint8, x.device, stream)
     _on_device(workspace, "workspace")
     name = {"q4_k": "qgemm_swiglu_q4_k", "q8_0": "qgemm_swiglu_q8_0"}[fmt]
     st = getattr(load(), name)(w.data_ptr(), gate_offset, up_offset, F, K, x.data_ptr(), M, h.data_ptr(), ldh,
@@ -423,7 +435,7 @@ def rope_table(n_pos: int, rot: int, base: float = 10000.0, freq_scale: float = 
     """[n_pos][rot/2][2] fp32 (cos, sin) of the position angles; freq_scale interpolates positions, freq_factors
     divides each frequency, orig_ctx > 0 ramps between kept and interpolated frequencies (see include/qk.h)."""
     if table is None:
-        table = torch.empty((max(n_pos, 0), max(rot, 0) // 2, 2), dtype=torch.float32, device="cuda")
+        table = _empty((max(n_pos, 0), max(rot, 0) // 2, 2), torch.float32, "cuda", stream)
     st = load().qk_rope_table(_vector(table, n_pos * (rot // 2) * 2, torch.float32, "table"), n_pos, rot, base,
                               freq_scale, _vector(freq_factors, rot // 2, torch.float32, "freq_factors"),
                               orig_ctx, beta_fast, beta_slow, amplitude, _stream(stream))
