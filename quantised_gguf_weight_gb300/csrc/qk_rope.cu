@@ -379,12 +379,12 @@ __device__ __forceinline__ void store_eight(uint8_t *block, int t, int ch, bool 
 }
 
 // 1 / sqrt(m): the approximation and one Newton step, within 1 ulp.  Where m
-// is 0, an infinity, a NaN or a subnormal (which the approximation takes as 0)
-// the step is left out.
+// is 0, an infinity or a NaN the step is left out.  A subnormal m (rows below
+// 2^-63 and no eps) counts as any other.
 __device__ __forceinline__ float rsqrt_newton(float m)
 {
     float r;
-    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(m));
+    asm("rsqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(m));
     const float e = fmaf(-m * r, r, 1.0f);
     return fabsf(e) <= 1.0f ? fmaf(0.5f * r, e, r) : r;
 }
