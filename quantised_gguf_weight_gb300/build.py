@@ -5,8 +5,8 @@ Each translation unit under csrc/ is compiled in parallel with
 quantised_gguf_weight_gb300/_build/libqk.so against the CUDA runtime.
 The calls from PyTorch tensors (csrc/qk_torch.cpp) are a CPython extension,
 _build/qk_torch.so, compiled by g++ beside them against the headers of the
-installed torch and linked to libqk.so.
-Rebuilds only when a source or header is newer than the library.
+installed torch and linked to libqk.so; without torch there is only libqk.so.
+Rebuilds only what a source or header is newer than.
 """
 from __future__ import annotations
 
@@ -42,12 +42,28 @@ def _deps() -> list[str]:
         glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
+def _have_torch() -> bool:
+    try:
+        import torch  # noqa: F401
+    except ImportError:
         return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(d) <= t for d in _deps()) and \
-        os.path.getmtime(BINDING_SOURCE) <= os.path.getmtime(BINDING)
+    return True
+
+
+def _newer_than(made: str, deps: list[str]) -> bool:
+    return os.path.exists(made) and all(os.path.getmtime(d) <= os.path.getmtime(made) for d in deps)
+
+
+def _library_up_to_date() -> bool:
+    return _newer_than(LIB, _deps())
+
+
+def _binding_up_to_date() -> bool:
+    return _newer_than(BINDING, [BINDING_SOURCE, *glob.glob(os.path.join(INCLUDE, "*.h")), os.path.abspath(__file__)])
+
+
+def up_to_date() -> bool:
+    return _library_up_to_date() and (not _have_torch() or _binding_up_to_date())
 
 
 def _binding_command(out: str) -> list[str]:
@@ -74,24 +90,7 @@ def _link_binding(obj: str) -> None:
     os.replace(tmp, BINDING)
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and up_to_date():
-        return LIB
-    nvcc = _nvcc()
-    os.makedirs(BUILD_DIR, exist_ok=True)
-    flags = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE,
-                    "--expt-relaxed-constexpr"]
-    binding_obj = os.path.join(BUILD_DIR, "qk_torch.cpp.o")
-    procs = [(BINDING_SOURCE, subprocess.Popen(_binding_command(binding_obj), stdout=subprocess.PIPE,
-                                               stderr=subprocess.STDOUT))]
-    objs = []
-    for src in sources():
-        obj = os.path.join(BUILD_DIR, os.path.basename(src) + ".o")
-        objs.append(obj)
-        cmd = [nvcc, *flags, "-c", src, "-o", obj]
-        if verbose:
-            cmd.insert(1, "-Xptxas=-v")
-        procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
+def _run(procs, verbose: bool) -> None:
     failed = []
     for src, p in procs:
         out, _ = p.communicate()
@@ -101,10 +100,37 @@ def build(force: bool = False, verbose: bool = False) -> str:
             failed.append(src)
     if failed:
         raise RuntimeError(f"compilation failed for {failed}")
-    tmp = LIB + f".tmp{os.getpid()}"
-    subprocess.check_call([nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart"])
-    os.replace(tmp, LIB)
-    _link_binding(binding_obj)
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    library = force or not _library_up_to_date()
+    binding = _have_torch() and (force or not _binding_up_to_date())
+    if not library and not binding:
+        return LIB
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    procs, objs = [], []
+    binding_obj = os.path.join(BUILD_DIR, "qk_torch.cpp.o")
+    if binding:
+        procs.append((BINDING_SOURCE, subprocess.Popen(_binding_command(binding_obj), stdout=subprocess.PIPE,
+                                                       stderr=subprocess.STDOUT)))
+    if library:
+        nvcc = _nvcc()
+        flags = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE,
+                        "--expt-relaxed-constexpr"]
+        for src in sources():
+            obj = os.path.join(BUILD_DIR, os.path.basename(src) + ".o")
+            objs.append(obj)
+            cmd = [nvcc, *flags, "-c", src, "-o", obj]
+            if verbose:
+                cmd.insert(1, "-Xptxas=-v")
+            procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
+    _run(procs, verbose)
+    if library:
+        tmp = LIB + f".tmp{os.getpid()}"
+        subprocess.check_call([nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart"])
+        os.replace(tmp, LIB)
+    if binding:
+        _link_binding(binding_obj)
     return LIB
 
 
