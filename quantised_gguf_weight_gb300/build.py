@@ -6,7 +6,8 @@ quantised_gguf_weight_gb300/_build/libqk.so against the CUDA runtime.
 The calls from PyTorch tensors (csrc/qk_torch.cpp) are a CPython extension,
 _build/qk_torch.so, compiled by g++ beside them against the headers of the
 installed torch and linked to libqk.so; without torch there is only libqk.so.
-Rebuilds only what a source or header is newer than.
+Rebuilds only what a source or header is newer than, and the extension where it
+was made for another torch or Python.
 """
 from __future__ import annotations
 
@@ -22,6 +23,7 @@ INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD_DIR, "libqk.so")
 BINDING = os.path.join(BUILD_DIR, "qk_torch.so")
+BINDING_FOR = os.path.join(BUILD_DIR, "qk_torch.for")      # the torch and Python that BINDING was made for
 BINDING_SOURCE = os.path.join(CSRC, "qk_torch.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -58,8 +60,19 @@ def _library_up_to_date() -> bool:
     return _newer_than(LIB, _deps())
 
 
+def _torch_and_python() -> str:
+    import torch
+    return f"{torch.__version__} {os.path.dirname(torch.__file__)} {sys.implementation.cache_tag}"
+
+
 def _binding_up_to_date() -> bool:
-    return _newer_than(BINDING, [BINDING_SOURCE, *glob.glob(os.path.join(INCLUDE, "*.h")), os.path.abspath(__file__)])
+    try:
+        with open(BINDING_FOR) as f:
+            made_for = f.read()
+    except OSError:
+        return False
+    return made_for == _torch_and_python() and \
+        _newer_than(BINDING, [BINDING_SOURCE, *glob.glob(os.path.join(INCLUDE, "*.h")), os.path.abspath(__file__)])
 
 
 def up_to_date() -> bool:
@@ -88,6 +101,8 @@ def _link_binding(obj: str) -> None:
                            "-L", libs, f"-Wl,-rpath,{libs}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
                            "-lc10_cuda"])
     os.replace(tmp, BINDING)
+    with open(BINDING_FOR, "w") as f:
+        f.write(_torch_and_python())
 
 
 def _run(procs, verbose: bool) -> None:

@@ -15,6 +15,7 @@ def commands(tmp_path, monkeypatch):
     monkeypatch.setattr(qbuild, "BUILD_DIR", str(tmp_path))
     monkeypatch.setattr(qbuild, "LIB", str(tmp_path / "libqk.so"))
     monkeypatch.setattr(qbuild, "BINDING", str(tmp_path / "qk_torch.so"))
+    monkeypatch.setattr(qbuild, "BINDING_FOR", str(tmp_path / "qk_torch.for"), raising=False)
 
     def run(cmd):
         ran.append(cmd)
@@ -62,6 +63,17 @@ def test_binding_alone_where_the_library_is_there(commands, monkeypatch):
         m.setitem(sys.modules, "torch", None)
         qbuild.build()
     commands.clear()
+    assert not qbuild.up_to_date()
+    qbuild.build()
+    assert made(commands) == {"qk_torch.cpp.o", "qk_torch.so"} and qbuild.up_to_date()
+
+
+def test_binding_for_another_torch(commands, monkeypatch):
+    """A torch of another version has another binary interface: the binding is made again, the library is not."""
+    import torch
+    qbuild.build()
+    commands.clear()
+    monkeypatch.setattr(torch, "__version__", "9.9.9+other")
     assert not qbuild.up_to_date()
     qbuild.build()
     assert made(commands) == {"qk_torch.cpp.o", "qk_torch.so"} and qbuild.up_to_date()
