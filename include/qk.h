@@ -450,12 +450,18 @@ int qk_kv_read_q4(const qk_kv_cache_q4 *cache, const int64_t *slots, int64_t T, 
  * range.  A bad page makes the sequence's rows that see its keys NaN (and
  * may make its other rows NaN); a bad length or q_start makes every row of
  * the sequence NaN, as far as q_start names rows inside [0, T).
+ * A group of 32 values whose scale is not finite makes its channels NaN in
+ * the rows that see the key, and in chunks (below) those rows whole.
+ * Rows of out that no sequence has (before q_start[0], from q_start[B] on)
+ * are not written.
  * Accuracy: sums and the softmax are fp32 whatever the types.  With fp32
- * queries every product is formed from the exact 4-bit values and 22-bit
- * query and probability pieces; so it is with fp16 queries in chunks (more
- * than 32 rows a sequence and key/value head, head_dim <= 128).  Else with
- * 16-bit queries the probabilities are rounded to fp16 (2^-11), and in bf16
- * chunks the cache's values too.
+ * queries every product is formed from the exact 4-bit values, 22-bit
+ * probabilities, and queries of 22 bits below the row's largest channel; with
+ * fp16 queries in chunks (more than 32 rows a sequence and key/value head,
+ * head_dim <= 128) likewise, the queries exact.  Else with 16-bit queries the
+ * probabilities are rounded to fp16 (2^-11), and in bf16 chunks the cache's
+ * values too.  The scales of a head's groups and tokens may differ by 2^20
+ * without loss.
  * T == 0 or B == 0 is a call that does nothing.
  */
 int qk_attn_q4(const qk_kv_cache_q4 *cache, const void *q, int64_t ldq, int q_type, int n_q_heads,

@@ -240,10 +240,14 @@ __device__ __forceinline__ void block16(State<G, PIECES, NT> &S, const Query<G, 
             grown |= __vmaxu2(w[i], S.scale_lim) != S.scale_lim;
         }
         if (__any_sync(0xFFFFFFFFu, grown)) {
+            // one that is not finite makes its channels NaN as it is, and shall not move rows that do not see it
             uint32_t m = S.scale_lim & 0xFFFFu;
 #pragma unroll
-            for (int i = 0; i < (8 * G + 31) / 32; ++i) m = max(m, max(w[i] & 0xFFFFu, w[i] >> 16));
-            m = min(redux_max_u32(0xFFFFFFFFu, m), 0x7BFFu);
+            for (int i = 0; i < (8 * G + 31) / 32; ++i) {
+                const uint32_t lo = w[i] & 0xFFFFu, hi = w[i] >> 16;
+                m = max(m, max(lo < 0x7C00u ? lo : 0u, hi < 0x7C00u ? hi : 0u));
+            }
+            m = redux_max_u32(0xFFFFFFFFu, m);
             S.scale_lim = m | m << 16;
             // |scale| < 2^(e + 1): probabilities up to 2^limit keep P * scale below 2^14
             const int e = m >= 0x0400u ? static_cast<int>(m >> 10) - 15 : -15;

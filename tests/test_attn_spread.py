@@ -87,3 +87,33 @@ def test_scales_apart(qk, dtype, D, n, kind, r):
         x, y = got[..., at:at + 32], ref[..., at:at + 32]
         rel = np.linalg.norm(x - y) / np.linalg.norm(y)
         assert rel <= limit, f"{kind}, channels {at}..: 2-norm {rel:.2e}"
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("n", [8, 70])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_value_scale_not_finite(qk, n, dtype, bad):
+    """A value group without a finite scale: its 32 channels are NaN in the rows that see the key (in chunks the whole
+    rows), all else is as without it."""
+    D, nq, late = 128, 4, L - 3
+    pages = -(-L // PAGE)
+    cache = qk.kv_cache_q4(pages, 1, PAGE, D)
+    k, v, q = rand(1, L, D), rand(2, L, D), rand(3, n, nq * D, dtype=dtype)
+    tab = torch.arange(pages, dtype=torch.int32).reshape(1, -1).cuda()
+    lens = torch.tensor([L], dtype=torch.int32).cuda()
+
+    def attention():
+        qk.kv_append_q4(cache, None, k, v, None, torch.arange(L).cuda(), None)
+        return qk.attn_q4(cache, q, tab, lens, max_q=n).reshape(n, nq, D)
+
+    want = attention()
+    v[late, 40] = bad
+    got = attention()
+    sees = n - (L - late)
+    assert torch.equal(got[:sees], want[:sees]) and torch.isnan(got[sees:, :, 32:64]).all()
+    others = torch.cat([got[sees:, :, :32], got[sees:, :, 64:]], -1)
+    if n * nq > 32:
+        assert torch.isnan(others).all()
+    else:
+        assert torch.equal(others, torch.cat([want[sees:, :, :32], want[sees:, :, 64:]], -1))
+    assert qk.device_error() == 0
