@@ -771,9 +771,11 @@ cudaError_t launch_heads(const RowsArgs &a, cudaStream_t st)
 {
     constexpr int kHeadsPerLane = heads_per_lane(APPEND);
     constexpr int NG = kRowWarps * kRowsPerWarp<D>;
+    int sms = 152, smem = 0;
+    device_limits(&sms, &smem);
     const int front = APPEND ? a.n_q : a.n_q + a.n_k, back = APPEND ? 2 * a.n_k : 0;
-    // several heads a lane share a table row and keep as many loads going; few tokens spread over more blocks
-    // instead (40 heads of 128: one token 2.7 us with four heads a lane, 2.1 with one, 64 tokens 2.5 and 2.4, 256
+    // several heads a lane share a table row and keep as many loads going; below two blocks an SM tokens spread over
+    // more blocks instead (40 heads of 128: one token 2.7 us with four heads a lane, 2.1 with one, 64 tokens 2.5 and 2.4, 256
     // tokens 3.1 and 3.7)
     const auto cut = [](int heads, int most, int *per) {
         const int parts = (heads + NG * most - 1) / (NG * most);
@@ -781,12 +783,12 @@ cudaError_t launch_heads(const RowsArgs &a, cudaStream_t st)
         return parts;
     };
     int hf = 1, hb = 1, fp = cut(front, kHeadsPerLane, &hf), parts = fp + cut(back, kHeadsPerLane, &hb);
-    if (a.T * parts < 304) fp = cut(front, 1, &hf), parts = fp + cut(back, 1, &hb);
+    if (a.T * parts < 2 * sms) fp = cut(front, 1, &hf), parts = fp + cut(back, 1, &hb);
     // appending many tokens, thread blocks go from token to token and work out only once what does not change (8192
     // tokens of 32 + 2 x 8 heads of 128: 52 us in six rounds of the blocks that the GPU holds, 53 in four, 62 with a
     // block a token; without the nibbles there is less to save than the waits cost, 57 us against 50 for
     // 8191 x 64 of 96)
-    const int64_t most = APPEND ? (6 * heads_blocks(true) * 152 + parts - 1) / parts : a.T, tokens = a.T < most ? a.T : most;
+    const int64_t most = APPEND ? (6 * heads_blocks(true) * sms + parts - 1) / parts : a.T, tokens = a.T < most ? a.T : most;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(tokens), static_cast<unsigned>(parts));
     cfg.blockDim = dim3(kRowWarps * 32);
