@@ -32,9 +32,10 @@
 //
 // What bounds it: three things at once.  1024 queries of 32 heads of 128 over
 // 16384 keys, 8 key/value heads, 266 GFLOP, take 268 us (1.0 PFLOP/s, 52% of
-// the cuBLAS rate); a tile of 64 keys for 256 rows is 2000 cycles, of which the
-// softmax warps work 1790, the dequantising ones 1650 and the tensor cores
-// 1250 (busy 62% of the time where a thread block is: 128 of 152 SMs).
+// the cuBLAS rate); a tile of 64 keys for 256 rows is 2015 cycles, of which the
+// softmax warps work 1700 to 1830, the dequantising ones 1450 to 1570 and the
+// tensor cores 1210 (busy 60% of the time where a thread block is: 128 of 152
+// SMs).
 #include "qk_attn_chunk.cuh"
 #include "qk_internal.h"
 

@@ -9,7 +9,7 @@
 // query columns, O^T = V^T P^T 16 channels by 8 columns.  Grouped heads are
 // few, and as columns they fill the products' narrow side; the other way round
 // (queries as the 16 rows) four heads left 12 rows of every product empty, and
-// a block took 32 products and 432 instructions instead of 16 and about 300.
+// a block took 32 products and 432 instructions instead of 16 and 352.
 // The scores' accumulator, rounded to fp16 and transposed by movmatrix, is the
 // second product's operand as it stands: the cache's token order is made for
 // it.
@@ -42,11 +42,14 @@
 // but cost 12% more instructions a block: 64 x 8192 tokens 149 us against
 // 146.)
 //
-// What bounds it: instructions.  64 sequences of 8192 tokens, 8 heads of 128
-// with 4 queries each in bf16, are 604 MB in 147 us (4.1 TB/s, 61% of the copy
-// rate): 354 warp instructions a block of 16 tokens, the integer pipe half and
-// the issue slots 61% busy with 16 warps an SM, a third of them taking nibbles
-// apart.  Short calls are their fixed part, dependent reads (lengths, page
+// What bounds it: latency, at 16 warps an SM.  64 sequences of 8192 tokens, 8
+// heads of 128 with 4 queries each in bf16, are 604 MB in 147 us (4.1 TB/s, 61%
+// of the copy rate): 352 warp instructions a block of 16 tokens, a third of them
+// taking nibbles apart, with the issue slots 60% and the integer pipe 52% busy
+// and no pipe full; 128 registers a thread leave no room for more warps.  Two
+// column sets of 16-bit rows spill at that (442 bytes of stores, 480 of loads at
+// 128 channels, 202 and 160 at 96), and are taken where they measured faster all
+// the same.  Short calls are their fixed part, dependent reads (lengths, page
 // table, first blocks) and the join: 1 x 32768 18 us, 4 of them before the
 // first block, 6.5 over the keys, 5 for parts and join.
 #pragma once

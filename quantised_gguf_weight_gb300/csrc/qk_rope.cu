@@ -774,9 +774,9 @@ cudaError_t launch_heads(const RowsArgs &a, cudaStream_t st)
     int sms = 152, smem = 0;
     device_limits(&sms, &smem);
     const int front = APPEND ? a.n_q : a.n_q + a.n_k, back = APPEND ? 2 * a.n_k : 0;
-    // several heads a lane share a table row and keep as many loads going; below two blocks an SM tokens spread over
-    // more blocks instead (40 heads of 128: one token 2.7 us with four heads a lane, 2.1 with one, 64 tokens 2.5 and 2.4, 256
-    // tokens 3.1 and 3.7)
+    // several heads a lane share a table row and keep as many loads going; below two blocks an SM the heads spread over
+    // more blocks instead (40 heads of 128: one token 2.7 us with four heads a lane, 2.1 with one, 64 tokens 2.5 and
+    // 2.4, 256 tokens 3.1 and 3.7)
     const auto cut = [](int heads, int most, int *per) {
         const int parts = (heads + NG * most - 1) / (NG * most);
         *per = parts ? (heads + NG * parts - 1) / (NG * parts) : 1;
