@@ -115,14 +115,23 @@ __device__ __forceinline__ void norm_rotate(float (&x)[NV][4], const RowsArgs &a
 {
     const int D = a.D;
     if (weight) {
-        float s = 0.0f;
+        // the squares in the order of sum_in_order
 #pragma unroll
         for (int i = 0; i < NV; ++i)
+            *reinterpret_cast<float4 *>(row + (i * 32 + lane) * 4) =
+                make_float4(__fmul_rn(x[i][0], x[i][0]), __fmul_rn(x[i][1], x[i][1]), __fmul_rn(x[i][2], x[i][2]),
+                            __fmul_rn(x[i][3], x[i][3]));
+        __syncwarp();
+        float s = 0.0f;
+        if (D == 256) {
+            for (int e = 0; e < 4; ++e) s = __fadd_rn(s, __fadd_rn(row[4 * lane + e], row[128 + 4 * lane + e]));
+        } else {
+            for (int ch = lane; ch < D; ch += 32) s = __fadd_rn(s, row[ch]);
+        }
+        __syncwarp();
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s = fmaf(x[i][e], x[i][e], s);
-#pragma unroll
-        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-        const float r = __frsqrt_rn(__fadd_rn(__fdiv_rn(s, static_cast<float>(D)), a.eps));
+        for (int o = 1; o < 32; o <<= 1) s = __fadd_rn(s, __shfl_xor_sync(0xFFFFFFFFu, s, o));
+        const float r = rsqrtf(__fadd_rn(__fmul_rn(s, 1.0f / D), a.eps));
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
@@ -378,41 +387,83 @@ __device__ __forceinline__ void store_eight(uint8_t *block, int t, int ch, bool 
     }
 }
 
-// 1 / sqrt(m): the approximation and one Newton step, within 1 ulp.  Where m
-// is 0, an infinity or a NaN the step is left out.  A subnormal m (rows below
-// 2^-63 and no eps) counts as any other.
-__device__ __forceinline__ float rsqrt_newton(float m)
+// The sum of a head's squares in the order that a stored key's norm has wherever its row lies: channels 32 apart one
+// after another, then neighbouring sums in pairs; of 256 channels, those 128 apart, then four neighbours one after
+// another, then in pairs.  (PyTorch's mean of a row was found to add in this order, so keys are stored as a plain run
+// of the formula there stores them.  In another order a norm's last bit moved 7 of 8 million nibbles by a step.)
+// row: D floats of shared memory of this head; a lane's channels are ca..ca+3 and cb..cb+3.
+template <int D>
+__device__ __forceinline__ float sum_in_order(const float (&x)[8], float *row, int ca, int cb, int i, int sub, bool on)
 {
-    float r;
-    asm("rsqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(m));
-    const float e = fmaf(-m * r, r, 1.0f);
-    return fabsf(e) <= 1.0f ? fmaf(0.5f * r, e, r) : r;
+    if (on) {
+        *reinterpret_cast<float4 *>(row + ca) =
+            make_float4(__fmul_rn(x[0], x[0]), __fmul_rn(x[1], x[1]), __fmul_rn(x[2], x[2]), __fmul_rn(x[3], x[3]));
+        *reinterpret_cast<float4 *>(row + cb) =
+            make_float4(__fmul_rn(x[4], x[4]), __fmul_rn(x[5], x[5]), __fmul_rn(x[6], x[6]), __fmul_rn(x[7], x[7]));
+    }
+    __syncwarp();
+    float s = 0.0f;
+    if constexpr (D == 128) {
+        float2 t = *reinterpret_cast<const float2 *>(row + 2 * i);
+#pragma unroll
+        for (int c = 1; c < 4; ++c) {
+            const float2 u = *reinterpret_cast<const float2 *>(row + 32 * c + 2 * i);
+            t.x = __fadd_rn(t.x, u.x), t.y = __fadd_rn(t.y, u.y);
+        }
+        s = __fadd_rn(t.x, t.y);
+    } else if (D != 96 || (on && i < 8)) {
+        constexpr int step = D == 256 ? 128 : 32;
+        float4 t = *reinterpret_cast<const float4 *>(row + 4 * i);
+#pragma unroll
+        for (int c = step; c < D; c += step) {
+            const float4 u = *reinterpret_cast<const float4 *>(row + c + 4 * i);
+            t.x = __fadd_rn(t.x, u.x), t.y = __fadd_rn(t.y, u.y), t.z = __fadd_rn(t.z, u.z), t.w = __fadd_rn(t.w, u.w);
+        }
+        s = D == 256 ? __fadd_rn(__fadd_rn(__fadd_rn(t.x, t.y), t.z), t.w) : __fadd_rn(__fadd_rn(t.x, t.y), __fadd_rn(t.z, t.w));
+    }
+    __syncwarp();
+    if constexpr (D == 96) {      // 12 lanes a row, the sums in the first eight
+        const int first = sub * 12;
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) s = __fadd_rn(s, __shfl_sync(0xFFFFFFFFu, s, (first + (i ^ o)) & 31));
+        return __shfl_sync(0xFFFFFFFFu, s, first);
+    }
+#pragma unroll
+    for (int o = 1; o < D / 8; o <<= 1) s = __fadd_rn(s, __shfl_xor_sync(0xFFFFFFFFu, s, o));
+    return s;
 }
 
 // Norm and rotation of a lane's eight channels.  Pair e is neighbours 2e,
-// 2e + 1 of the eight, or element e of both chunks.
+// 2e + 1 of the eight, or element e of both chunks.  With `sum` the head's
+// sum of squares is there already.
 template <int D, bool INTER>
 __device__ __forceinline__ void turn_eight(float (&x)[8], bool norm, bool weigh, const float (&w)[8], float eps,
-                                           bool turn, const float (&c)[4], const float (&s)[4], int sub)
+                                           bool turn, const float (&c)[4], const float (&s)[4], int sub,
+                                           const float *sum = nullptr)
 {
     constexpr int LPR = D / 8;
     if (norm) {       // warp-uniform: some row of the call has a weight
-        uint64_t squares = 0;      // two zeros
-#pragma unroll
-        for (int e = 0; e < 8; e += 2) squares = fma_f32x2(pack2f(x[e], x[e + 1]), pack2f(x[e], x[e + 1]), squares);
-        const float2 two = unpack2f(squares);
-        float q = two.x + two.y;
-        if constexpr (D == 96) {      // 12 lanes a row: groups of four stay inside it
-            q += __shfl_xor_sync(0xFFFFFFFFu, q, 1);
-            q += __shfl_xor_sync(0xFFFFFFFFu, q, 2);
-            const int first = sub * LPR;
-            q = __shfl_sync(0xFFFFFFFFu, q, first) + __shfl_sync(0xFFFFFFFFu, q, first + 4) +
-                __shfl_sync(0xFFFFFFFFu, q, (first + 8) & 31);
+        float q;
+        if (sum) {
+            q = *sum;
         } else {
+            uint64_t squares = 0;      // two zeros
 #pragma unroll
-            for (int o = LPR / 2; o; o >>= 1) q += __shfl_xor_sync(0xFFFFFFFFu, q, o);
+            for (int e = 0; e < 8; e += 2) squares = fma_f32x2(pack2f(x[e], x[e + 1]), pack2f(x[e], x[e + 1]), squares);
+            const float2 two = unpack2f(squares);
+            q = two.x + two.y;
+            if constexpr (D == 96) {      // 12 lanes a row: groups of four stay inside it
+                q += __shfl_xor_sync(0xFFFFFFFFu, q, 1);
+                q += __shfl_xor_sync(0xFFFFFFFFu, q, 2);
+                const int first = sub * LPR;
+                q = __shfl_sync(0xFFFFFFFFu, q, first) + __shfl_sync(0xFFFFFFFFu, q, first + 4) +
+                    __shfl_sync(0xFFFFFFFFu, q, (first + 8) & 31);
+            } else {
+#pragma unroll
+                for (int o = LPR / 2; o; o >>= 1) q += __shfl_xor_sync(0xFFFFFFFFu, q, o);
+            }
         }
-        const float r = weigh ? rsqrt_newton(__fadd_rn(q * (1.0f / D), eps)) : 1.0f;   // without: the weights are 1
+        const float r = weigh ? rsqrtf(__fadd_rn(__fmul_rn(q, 1.0f / D), eps)) : 1.0f;   // without: the weights are 1
         const uint64_t r2 = pack2f(r, r);
 #pragma unroll
         for (int e = 0; e < 8; e += 2) {
@@ -573,7 +624,8 @@ __global__ void __launch_bounds__(kRowWarps * 32, heads_blocks(APPEND)) heads_ke
             else return;
         }
         if constexpr (APPEND) {
-            __shared__ __align__(16) float exchange[INTER ? 1 : kRowWarps * RPW][INTER ? 4 : D];
+            __shared__ __align__(16) float exchange[kRowWarps * RPW][D];
+            float *row = exchange[warp * RPW + (on ? sub : 0)];
             const int64_t slot = a.slots[t];
             if (slot < 0) continue;
             if (slot >= a.n_slots) {
@@ -593,9 +645,11 @@ __global__ void __launch_bounds__(kRowWarps * 32, heads_blocks(APPEND)) heads_ke
                 float x[8];
                 xa[k].to(x), xb[k].to(x + 4);
                 if (changes && !is_key) load_weights(w, nullptr, ca, cb);
-                turn_eight<D, INTER>(x, norm, weight && k < mine && is_key, w, a.eps, turn && is_key, c, s, sub);
+                const bool normed = a.k_weight && __any_sync(0xFFFFFFFFu, is_key);      // some row of the warp's
+                float sum = 0.0f;
+                if (normed) sum = sum_in_order<D>(x, row, ca, cb, i, sub, on);
+                turn_eight<D, INTER>(x, normed, weight && k < mine && is_key, w, a.eps, turn && is_key, c, s, sub, &sum);
                 if constexpr (!INTER) {      // eight neighbours a lane, as the cache wants them
-                    float *row = exchange[warp * RPW + (on ? sub : 0)];
                     if (on && is_key) {
                         *reinterpret_cast<float4 *>(row + ca) = make_float4(x[0], x[1], x[2], x[3]);
                         *reinterpret_cast<float4 *>(row + cb) = make_float4(x[4], x[5], x[6], x[7]);

@@ -59,3 +59,26 @@ def test_rotated_keys_are_the_same_bytes_anywhere(qk, interleaved):
         qk.kv_append_q4(cache, None, kv, kv, pos, torch.arange(T).cuda(), table(500, D), interleaved=interleaved)
         got.append(cache)
     assert torch.equal(*got) and qk.device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("nkv,D,rot", [(4, 128, 128), (8, 64, 32), (3, 96, 72), (2, 256, 256), (2, 256, 64), (5, 128, 0)])
+def test_normed_keys_are_the_same_bytes_anywhere(qk, nkv, D, rot, interleaved, dtype):
+    """A key's squares are added in one order whichever form takes its row, so its norm has the same bits."""
+    T, page = 3000, 64
+    g = torch.Generator().manual_seed(4)
+    k = torch.randn(T, nkv * D, generator=g)
+    if dtype == "bf16":
+        k = k.bfloat16()
+    pos, w = torch.randint(0, 500, (T,), generator=g).int().cuda(), (1 + 0.2 * torch.randn(D, generator=g)).cuda()
+    got = []
+    for off, pad in ((0, 0), (3, 5)):
+        cache = qk.kv_cache_q4(-(-T // page), nkv, page, D)
+        buf = torch.zeros(T, nkv * D + pad, dtype=k.dtype, device="cuda")
+        kv = buf[:, off:off + nkv * D]
+        kv.copy_(k)
+        qk.kv_append_q4(cache, None, kv, kv, pos, torch.arange(T).cuda(), table(500, rot) if rot else None, k_weight=w,
+                        interleaved=interleaved)
+        got.append(cache)
+    assert (got[0] != got[1]).sum() == 0 and qk.device_error() == 0
