@@ -367,7 +367,8 @@ int qk_norm_rope(const void *x, int64_t ldx, int x_type, int n_q_heads, int n_k_
  * A value is d * (n - 8): the scale d is fp16(m / -8), m the value of largest
  * magnitude of 32 neighbouring channels (the positive one of a tie; |d| is
  * held to 65504), and the nibble n = clamp(floor(x / d + 8.5), 0, 15), 8
- * where d is 0.  A group that holds a NaN or an infinity gets a NaN scale.
+ * where d is 0: in fp32, the quotient and the sum each rounded, wherever the
+ * rows lie.  A group that holds a NaN or an infinity gets a NaN scale.
  *
  * Block (16 tokens of one head; G = head_dim/32 scale groups, Gp = 4 where G
  * is a multiple of 4 and else G):

@@ -186,8 +186,7 @@ __device__ __forceinline__ void norm_rotate(float (&x)[NV][4], const RowsArgs &a
 }
 
 // Four channels of a head to the cache: the group's scale over its 8 lanes,
-// then the lane's four nibbles (of the exact quotients, as nibbles_of has them)
-// as two bytes.
+// then the lane's four nibbles (the same as nibbles_of's) as two bytes.
 __device__ __forceinline__ void store_nibbles(uint8_t *block, int D, int t, int ch, bool active, const float (&x)[4],
                                               bool is_key, int lane)
 {
@@ -212,12 +211,8 @@ __device__ __forceinline__ void store_nibbles(uint8_t *block, int D, int t, int 
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         float n = 8.0f;
-        if (d != 0.0f && !group_odd) {
-            // the rounded quotient and sum may have reached the next edge, (n - 8.5) d: then x lies below it
-            n = floorf(__fadd_rn(__fdiv_rn(x[e], d), 8.5f));
-            if (fmaf(8.5f - n, fabsf(d), copysignf(1.0f, d) * x[e]) < 0.0f) n -= 1.0f;
-            n = fminf(fmaxf(n, 0.0f), 15.0f);
-        }
+        if (d != 0.0f && !group_odd)
+            n = fminf(fmaxf(floorf(__fadd_rn(__fdiv_rn(x[e], d), 8.5f)), 0.0f), 15.0f);
         bits |= static_cast<uint32_t>(n) << (4 * e);
     }
     const Kv4Place p = is_key ? kv4_key_place(D, t, ch) : kv4_value_place(D, t, ch);
@@ -318,27 +313,25 @@ __host__ __device__ constexpr int heads_blocks(bool append) { return append ? 5 
 template <int D>
 constexpr int kRowsPerWarp = D == 96 ? 2 : 256 / D;
 
-// Nibbles floor(x / d + 8.5) of eight values, d != 0.  The product with 1/d
-// is within 2^-17 of the quotient; lowered by twice that it gives the floor or
-// one less, and the comparison of x with the next edge, (n - 7.5) * d, which
-// fp32 holds exactly, tells which.  (Quotients on an edge are common: x and d
-// have few bits when the values come in 16.)
+// Nibbles floor(x / d + 8.5) of eight values, d != 0, in fp32: the quotient rounded, then the sum, as a plain run of
+// the formula has them.  The product with 1/d is within 2^-17 of the quotient; lowered by twice that it gives the floor
+// or one less, n, and x - (n - 7.5) d, which fp32 holds to its last bit, how far x lies from the next edge.  That over
+// d, added to n - 7.5, is the quotient: correctly rounded near the edge, where it decides, and near enough elsewhere.
 __device__ __forceinline__ uint32_t nibbles_of(const float (&x)[8], float d)
 {
     // 1/d of a subnormal fp16 is at most 2^24; the quotient is within +-16
     const float step = fabsf(d), inv = __fdividef(1.0f, step);
     const uint32_t sign = __float_as_uint(d) & 0x80000000u;
-    const uint64_t inv2 = pack2f(inv, inv), step2 = pack2f(step, step);
+    const uint64_t inv2 = pack2f(inv, inv), down2 = pack2f(-step, -step);
     float2 w;      // four nibbles each, exact in fp32
 #pragma unroll
     for (int e = 3; e >= 0; --e) {
         const uint64_t v = pack2(__float_as_uint(x[e]) ^ sign, __float_as_uint(x[e + 4]) ^ sign);
         const uint64_t low = fma_f32x2(v, inv2, pack2f(8.5f - 1.6e-5f, 8.5f - 1.6e-5f));
         const uint64_t n2 = add_f32x2(add_down_f32x2(low, pack2f(kTwo23, kTwo23)), pack2f(-kTwo23, -kTwo23));
-        const float2 past = unpack2f(fma_f32x2(fma_f32x2(n2, pack2f(-1.0f, -1.0f), pack2f(7.5f, 7.5f)), step2, v));
-        float2 n = unpack2f(n2);
-        if (past.x >= 0.0f) n.x += 1.0f;
-        if (past.y >= 0.0f) n.y += 1.0f;
+        const uint64_t edge = add_f32x2(n2, pack2f(-7.5f, -7.5f));
+        const uint64_t sum = add_f32x2(fma_f32x2(fma_f32x2(edge, down2, v), inv2, edge), pack2f(8.5f, 8.5f));
+        float2 n = unpack2f(add_f32x2(add_down_f32x2(sum, pack2f(kTwo23, kTwo23)), pack2f(-kTwo23, -kTwo23)));
         n.x = fminf(fmaxf(n.x, 0.0f), 15.0f), n.y = fminf(fmaxf(n.y, 0.0f), 15.0f);
         w = e == 3 ? n : unpack2f(fma_f32x2(pack2f(w.x, w.y), pack2f(16.0f, 16.0f), pack2f(n.x, n.y)));
     }

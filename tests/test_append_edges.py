@@ -1,5 +1,5 @@
-"""What the append stores for values next to a nibble's edge, wherever the rows lie: floor(x / d + 8.5) of the exact
-quotient, byte for byte the 64-bit oracle's."""
+"""What the append stores for values next to a nibble's edge, wherever the rows lie: floor(x / d + 8.5) in fp32, the
+quotient and the sum each rounded, byte for byte."""
 import numpy as np
 import pytest
 import torch
@@ -22,6 +22,15 @@ def edge_rows(seed, T, heads, D):
     return x.reshape(T, heads * D).astype(np.float32)
 
 
+def quantise32(x):
+    """Nibbles and scales as kv4_oracle.quantise, in fp32."""
+    _, d = ko.quantise(x)
+    g, e = np.asarray(x, np.float32).reshape(*d.shape, 32), d.astype(np.float32)[..., None]
+    with np.errstate(divide="ignore", invalid="ignore"):
+        n = np.clip(np.floor((g / e).astype(np.float32) + np.float32(8.5)), 0, 15)
+    return np.where(e == 0, 8, n).reshape(x.shape).astype(np.uint8), d
+
+
 def place(x, off, pad):
     """The rows inside a wider buffer, `off` elements from its start."""
     buf = torch.zeros(x.shape[0], x.shape[1] + pad, device="cuda")
@@ -36,7 +45,9 @@ def test_edges(qk, nkv, D):
     pages = -(-T // page)
     as_pages = [np.concatenate([t.reshape(T, nkv, D), np.zeros((pages * page - T, nkv, D))]).reshape(pages, page, nkv, D)
                 .transpose(0, 2, 1, 3) for t in (k, v)]
-    want = ko.pack(*ko.quantise(as_pages[0]), *ko.quantise(as_pages[1]))
+    want = ko.pack(*quantise32(as_pages[0]), *quantise32(as_pages[1]))
+    exact = ko.pack(*ko.quantise(as_pages[0]), *ko.quantise(as_pages[1]))
+    assert (want != exact).any()        # the rows hold values that the roundings carry over an edge
     empty = ko.pack(*ko.quantise(as_pages[0] * 0), *ko.quantise(as_pages[1] * 0))
     for off, pad in ((0, 0), (4, 4), (1, 1), (2, 7)):      # the last two rule out wide loads
         cache = torch.from_numpy(empty).cuda()
