@@ -15,11 +15,12 @@
 // stride and alignment.
 //
 // What bounds them: instructions, not the rows' bytes.  8191 tokens of 64 heads
-// of 96 in bf16 are 201 MB, 30 us at the memory's rate; the kernel takes 49
-// (4.1 TB/s) with the issue slots three quarters busy at 42 million warp
-// instructions, conversions, products and sums being about half of them.  The
-// append of 8192 tokens of 48 heads of 128 takes 53 us (100 MB of rows in,
-// 67 out and 9 of cache: 26 at the memory's rate), its read-back 13 (6).
+// of 96 in bf16 are 201 MB, 30 us at the memory's rate; the kernel takes 47
+// (4.3 TB/s) with the issue slots 70% busy at 38 million warp instructions,
+// conversions, products and sums being about half of them.  The append of 8192
+// tokens of 48 heads of 128 takes 55 us (100 MB of rows in, 67 out and 9 of
+// cache: 26 at the memory's rate; issue slots 78% busy), its read-back 13 (6;
+// 78%).
 #include <cfloat>
 #include <cmath>
 #include <type_traits>
