@@ -475,6 +475,110 @@ int qk_attn_q4(const qk_kv_cache_q4 *cache, const void *q, int64_t ldq, int q_ty
 size_t qk_attn_q4_workspace_bytes(int64_t B, int n_q_heads, int n_kv_heads, int head_dim, int64_t max_q,
                                   int64_t max_len);
 
+/* ------------------------------------------------------------------------
+ * Beside the products: routing to experts and the experts' feed-forward
+ * products (nurllama 0.18.1 API reference, kernels.nu `moe_route`,
+ * `moe_scatter`; loom-port-llm SKILL.md, gen_moe.py), and low-rank adapters
+ * (its LoRA fine-tunes).  Sums are fp32 whatever the element types, with one
+ * rounding to the output's type.
+ */
+
+/* Expert scores of a token's logits z: softmax(z) over all experts, or 1 / (1 + e^-z) of each. */
+typedef enum { QK_SOFTMAX = 0, QK_SIGMOID = 1 } qk_score;
+
+/*
+ * Routing of T tokens: ids[t][j], weights[t][j] for j < top_k.
+ *   p = the scores;  c = p + bias (bias device fp32 [n_experts], or NULL: p).
+ *   Groups: the experts are n_groups runs of n_experts / n_groups; a group
+ *   counts as the sum of its group_top (1 or 2) largest c, and the top_groups
+ *   best groups stay (top_groups == n_groups: all).
+ *   ids: the top_k experts of largest c in them, largest first.  The lower
+ *   index wins a tie, of groups too.
+ *   weights: p[ids], over their sum with renorm != 0, times scale.
+ * The choice is that of the exact formulas: neighbours that 32-bit scores
+ * leave undecided are compared in 64 bits; without a bias (and with
+ * group_top 1, where groups count) the logits are compared.  Weights are
+ * within 1e-6 of themselves.
+ * A logit of -infinity has score 0.  A token none of whose chosen experts has
+ * a score gets weights of 0.  A token with a NaN among its logits or the
+ * biases, or (softmax) a logit of +infinity, gets ids 0..top_k-1 and NaN
+ * weights.
+ *   logits      device rows of n_experts elements of `type`, ld apart (0: packed).
+ *   ids, weights  device int32 and fp32 [T][top_k].
+ * n_experts <= 1024, top_k <= 32, n_groups <= 32 (else QK_ERR_TOO_LARGE);
+ * top_k <= top_groups * n_experts / n_groups.  T == 0 does nothing.
+ */
+int qk_moe_route(const void *logits, int64_t ld, int type, int64_t T, int n_experts, int top_k, int score,
+                 const float *bias, int n_groups, int top_groups, int group_top, int renorm, float scale, int32_t *ids,
+                 float *weights, qk_stream_t stream);
+
+/* Block formats of expert tensors. */
+typedef enum { QK_Q8_0 = 0, QK_Q4_K = 1, QK_Q6_K = 2 } qk_format;
+
+/*
+ * The experts' rows of one projection: expert e's row r is row
+ * row_offset + e * expert_rows + r of w (expert_rows 0: the call's row
+ * count).  A 3-D expert tensor has row_offset 0 and expert_rows 0; the halves
+ * of a fused gate-and-up tensor [E][2F][K] have row_offset 0 and F, and
+ * expert_rows 2F.  w's alignment as the format's GEMV.
+ */
+typedef struct {
+    const void *w;
+    int format;
+    int64_t row_offset, expert_rows;
+} qk_expert_weights;
+
+/*
+ * The experts' feed-forward products of T tokens:
+ *   y[t] = sum_{j < top_k} weights[t][j] * down_e h,
+ *   h = silu(gate_e x[t]) * (up_e x[t]),   e = ids[t][j],
+ * gate and up [F][K] (one format), down [N][F], each expert's weights read
+ * once for up to 32 of its tokens.  ids may be in any order and repeat; a
+ * negative id adds nothing (a token with none left gets 0).  An id past the
+ * last makes the token's row NaN and qk_device_error() reports
+ * QK_ERR_BAD_INDEX.
+ *   x, y        device rows of K and N elements of x_type / y_type, ldx / ldy
+ *               apart (0: packed), aligned to their element.
+ *   ids, weights  device int32 and fp32 [T][top_k].
+ *   workspace   device scratch, 256-byte aligned, of at least
+ *               qk_moe_ffn_workspace_bytes() bytes; its contents need not be
+ *               kept or set.  Calls that may overlap need one each.
+ * Accuracy: the weights' quants and scales are exact.  With fp32 x or y every
+ * activation (x, and h) is held to 2^-22 of itself or 2^-39 of its row's
+ * largest; else to 2^-11 or 2^-28 (fp16's, so bf16 values are exact above
+ * that).  Sums are fp32.
+ * A NaN or an infinity in a row of x makes that token's y not finite, and no other's.
+ * n_experts <= 1024; K, F, N <= 2^24; T * top_k <= 2^28.  T == 0 does nothing.
+ */
+int qk_moe_ffn(const qk_expert_weights *gate, const qk_expert_weights *up, const qk_expert_weights *down,
+               int64_t n_experts, int64_t K, int64_t F, int64_t N, const void *x, int64_t ldx, int x_type, int64_t T,
+               const int32_t *ids, const float *weights, int top_k, void *y, int64_t ldy, int y_type, void *workspace,
+               size_t workspace_bytes, qk_stream_t stream);
+
+/* Workspace bytes of a qk_moe_ffn call of these sizes, whatever the formats and types. */
+size_t qk_moe_ffn_workspace_bytes(int64_t T, int top_k, int64_t n_experts, int64_t K, int64_t F, int64_t N);
+
+/*
+ * Low-rank adapters beside a projection's output y:
+ *   out[t] = y[t] + scales[a] * B[a] (A[a] x[t]),   a = ids[t].
+ *   x           device rows of K elements of x_type, ldx apart (0: packed).
+ *   A, B        device [n_adapters][rank][K] and [n_adapters][N][rank] of
+ *               w_type; a smaller adapter is padded with zero ranks.
+ *   ids         device int32 [T]; a negative id: out[t] = y[t].  One past the
+ *               last makes the row NaN (QK_ERR_BAD_INDEX from qk_device_error()).
+ *   scales      device fp32 [n_adapters], or NULL: 1.
+ *   y, out      device rows of N elements of y_type, ldy / ldo apart (0:
+ *               packed); out may be y (with the same stride) and must not
+ *               overlap x.
+ * Tokens of one adapter may lie anywhere; neighbouring ones share its reads.
+ * Both products are fp32 sums of operands that are exact in 16 bits and held
+ * to 22 bits in fp32 (and A x, in between).
+ * rank <= 256; K, N <= 2^24; T <= 2^26.  T == 0 does nothing.
+ */
+int qk_lora(const void *x, int64_t ldx, int x_type, int64_t T, int64_t K, const void *A, const void *B, int w_type,
+            int64_t n_adapters, int rank, int64_t N, const int32_t *ids, const float *scales, const void *y,
+            int64_t ldy, void *out, int64_t ldo, int y_type, qk_stream_t stream);
+
 /*
  * Bytes of one row of a tensor with K columns: ceil(K/32)*34 (Q8_0),
  * ceil(K/256)*144 (Q4_K) or ceil(K/256)*210 (Q6_K).

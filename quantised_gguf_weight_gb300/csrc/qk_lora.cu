@@ -1,0 +1,409 @@
+// qk_lora.cu -- low-rank adapters of many requests beside a shared projection:
+//   out[t] = y[t] + scale[a] * B[a] (A[a] x[t]),  a = ids[t].
+//
+// A cluster of thread blocks takes a tile of neighbouring tokens and one adapter
+// after another of those that the tile has: each block forms its columns' part
+// of V = A x (rank values a token), the blocks add the parts through distributed
+// shared memory, always in their order, and each adds its columns of B V to y.
+// So x, y and out pass once, and one launch does both products.
+//
+// The products are m16n8k8 in tf32, which holds 16-bit adapters and activations
+// exactly; fp32 operands, and V, are two tf32 pieces (22 bits).  A lane's values
+// of an operand are neighbours in memory: which columns a product's slots stand
+// for is free as long as both operands agree.
+#include <algorithm>
+#include <cmath>
+
+#include "qk_kv4.cuh"
+#include "qk_moe.cuh"
+#include "qk_tc.cuh"
+
+namespace qk {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kCluster = 8;
+constexpr int kBlockRank = 64;                 // ranks of a pass of the first product
+constexpr int kMaxRank = 256;
+
+struct LoraArgs {
+    const void *x, *y, *A, *B;
+    void *out;
+    int64_t ldx, ldy, ldo, T, n_adapters;
+    int x_type, y_type, w_type, K, N, rank;
+    const int32_t *ids;
+    const float *scales;
+    int steps;                                 // clusters that share a tile's adapters
+    bool vec_x, vec_y, vec_a, vec_b;
+    int *err;
+};
+
+__device__ __forceinline__ uint32_t tf32_of(float v)
+{
+    uint32_t r;
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ void mma8(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Q neighbouring values of a row from element i on, 0 from element `n` (of the row) on.  WIDE: fp32.
+template <int Q, bool WIDE>
+__device__ __forceinline__ void load_values(float (&v)[Q], const void *base, int64_t row, int i, int n, bool vec, bool half)
+{
+    if (vec && i + Q <= n) {
+        if constexpr (WIDE) {
+            const float *p = static_cast<const float *>(base) + row + i;
+#pragma unroll
+            for (int k = 0; k < Q; k += 4)
+                if constexpr (Q >= 4) {
+                    const float4 f = __ldg(reinterpret_cast<const float4 *>(p + k));
+                    v[k] = f.x, v[k + 1] = f.y, v[k + 2] = f.z, v[k + 3] = f.w;
+                } else {
+                    const float2 f = __ldg(reinterpret_cast<const float2 *>(p + k));
+                    v[k] = f.x, v[k + 1] = f.y;
+                }
+        } else {
+            const uint16_t *p = static_cast<const uint16_t *>(base) + row + i;
+            uint32_t w[Q / 2];
+            if constexpr (Q >= 8) {
+#pragma unroll
+                for (int k = 0; k < Q / 8; ++k) {
+                    const uint4 f = __ldg(reinterpret_cast<const uint4 *>(p) + k);
+                    w[4 * k] = f.x, w[4 * k + 1] = f.y, w[4 * k + 2] = f.z, w[4 * k + 3] = f.w;
+                }
+            } else if constexpr (Q == 4) {
+                const uint2 f = __ldg(reinterpret_cast<const uint2 *>(p));
+                w[0] = f.x, w[1] = f.y;
+            } else {
+                w[0] = __ldg(reinterpret_cast<const uint32_t *>(p));
+            }
+#pragma unroll
+            for (int k = 0; k < Q / 2; ++k) {
+                const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&w[k]));
+                v[2 * k] = half ? h.x : __uint_as_float(w[k] << 16);
+                v[2 * k + 1] = half ? h.y : __uint_as_float(w[k] & 0xffff0000u);
+            }
+        }
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < Q; ++k)
+        v[k] = i + k < n ? load_as_float(base, row + i + k, WIDE ? QK_F32 : half ? QK_F16 : QK_BF16) : 0.0f;
+}
+
+// d += a b, of fp32 values in one or two tf32 pieces (PA, PB of them count).
+template <int PA, int PB>
+__device__ __forceinline__ void mma_pieces(float (&d)[4], const float (&a)[4], float b0, float b1)
+{
+    uint32_t ah[4], al[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        ah[i] = PA == 2 ? tf32_of(a[i]) : __float_as_uint(a[i]);
+        if constexpr (PA == 2) al[i] = tf32_of(a[i] - __uint_as_float(ah[i]));
+    }
+    const uint32_t h0 = PB == 2 ? tf32_of(b0) : __float_as_uint(b0), h1 = PB == 2 ? tf32_of(b1) : __float_as_uint(b1);
+    mma8(d, ah, h0, h1);
+    if constexpr (PA == 2) mma8(d, al, h0, h1);
+    if constexpr (PB == 2) mma8(d, ah, tf32_of(b0 - __uint_as_float(h0)), tf32_of(b1 - __uint_as_float(h1)));
+}
+
+__device__ __forceinline__ float4 read_remote(uint32_t addr)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+    return v;
+}
+
+// MT: 16-row tiles of tokens; NR: 8-rank tiles of a pass; XW, WW: activations and adapters in fp32.
+template <int MT, int NR, bool XW, bool WW>
+__global__ void __launch_bounds__(kThreads) lora_kernel(const LoraArgs a)
+{
+    constexpr int ROWS = 16 * MT, R8 = 8 * NR;
+    extern __shared__ __align__(16) float smem[];
+    __shared__ int ids[ROWS], list[ROWS], n_list;
+    const int blocks = (a.rank + R8 - 1) / R8, width = blocks * R8, pitch = width + 4;
+    float *parts = smem;                                     // [warp][ROWS][R8]
+    float *mine = parts + kWarps * ROWS * R8;                // [ROWS][width]: this block's part of V
+    float *V = mine + ROWS * width;                          // [ROWS][pitch]
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+    const int rank = static_cast<int>(cluster_ctarank());
+    const int64_t cluster = blockIdx.x / kCluster;
+    const int64_t t0 = cluster / a.steps * ROWS;
+    const int step = static_cast<int>(cluster % a.steps);
+    moe::let_next_start();
+    moe::wait_for_previous();
+    if (tid == 0) n_list = 0;
+    if (tid < ROWS) ids[tid] = t0 + tid < a.T ? a.ids[t0 + tid] : -1;
+    __syncthreads();
+    if (tid < 32)
+        for (int base = 0; base < ROWS; base += 32) {        // the tile's adapters, in the order of their first tokens
+            const int i = base + lane;
+            const int id = i < ROWS ? ids[i] : -1;
+            bool first = id >= 0 && id < a.n_adapters;
+            for (int k = 0; k < i && first; ++k) first = ids[k] != id;
+            const unsigned who = __ballot_sync(~0u, first);
+            if (first) list[n_list + __popc(who & ((1u << lane) - 1))] = id;
+            __syncwarp();
+            if (lane == 0) n_list += __popc(who);
+            __syncwarp();
+        }
+    __syncthreads();
+    const int n_adapters = n_list;
+    // columns of this block: of x, and of y
+    const int k_per = ((a.K + kCluster - 1) / kCluster + 31) / 32 * 32, k0 = min(a.K, rank * k_per), k1 = min(a.K, k0 + k_per);
+    const int n_per = ((a.N + kCluster - 1) / kCluster + 15) / 16 * 16, n0 = min(a.N, rank * n_per), n1 = min(a.N, n0 + n_per);
+    const bool x_half = a.x_type == QK_F16, w_half = a.w_type == QK_F16;
+
+    if (step == 0) {                                         // rows without an adapter
+        const bool moves = a.out != a.y;
+        for (int i = 0; i < ROWS; ++i) {
+            const int64_t t = t0 + i;
+            if (t >= a.T) break;
+            const bool bad = ids[i] >= a.n_adapters;
+            if (ids[i] >= 0 && !bad) continue;
+            if (bad && tid == 0 && rank == 0) record_error(a.err, kErrBadIndex);
+            if (bad || moves)
+                for (int n = n0 + tid; n < n1; n += kThreads)
+                    store_float_as(a.out, t * a.ldo + n, a.y_type,
+                                   bad ? __int_as_float(0x7fc00000) : load_as_float(a.y, t * a.ldy + n, a.y_type));
+        }
+    }
+
+    for (int j = step; j < n_adapters; j += a.steps) {
+        const int id = list[j];
+        const int64_t a_row = static_cast<int64_t>(id) * a.rank, b_row = static_cast<int64_t>(id) * a.N;
+        for (int rb = 0; rb < blocks; ++rb) {
+            float acc[MT][NR][4];
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int n = 0; n < NR; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.0f;
+            for (int k = k0 + warp * 32; k < k1; k += kWarps * 32) {
+                float xv[MT][2][8];
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int row = m * 16 + h * 8 + g;
+                        const bool in = ids[row] == id;
+                        if (in) load_values<8, XW>(xv[m][h], a.x, (t0 + row) * a.ldx, k + 8 * c, a.K, a.vec_x, x_half);
+                        else {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) xv[m][h][i] = 0.0f;
+                        }
+                    }
+#pragma unroll
+                for (int n = 0; n < NR; ++n) {
+                    const int r = rb * R8 + n * 8 + g;
+                    float av[8];
+                    if (r < a.rank) load_values<8, WW>(av, a.A, (a_row + r) * a.K, k + 8 * c, a.K, a.vec_a, w_half);
+                    else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) av[i] = 0.0f;
+                    }
+#pragma unroll
+                    for (int s = 0; s < 4; ++s)
+#pragma unroll
+                        for (int m = 0; m < MT; ++m) {
+                            const float xa[4] = {xv[m][0][2 * s], xv[m][1][2 * s], xv[m][0][2 * s + 1], xv[m][1][2 * s + 1]};
+                            mma_pieces<XW ? 2 : 1, WW ? 2 : 1>(acc[m][n], xa, av[2 * s], av[2 * s + 1]);
+                        }
+                }
+            }
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int n = 0; n < NR; ++n)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        *reinterpret_cast<float2 *>(parts + (warp * ROWS + m * 16 + h * 8 + g) * R8 + n * 8 + 2 * c) =
+                            make_float2(acc[m][n][2 * h], acc[m][n][2 * h + 1]);
+            __syncthreads();
+            for (int i = tid; i < ROWS * R8; i += kThreads) {
+                float s = parts[i];
+#pragma unroll
+                for (int w = 1; w < kWarps; ++w) s += parts[w * ROWS * R8 + i];
+                mine[i / R8 * width + rb * R8 + i % R8] = s;
+            }
+            __syncthreads();
+        }
+        cluster_sync();
+        const float scale = a.scales ? a.scales[id] : 1.0f;
+        const uint32_t at = smem_u32(mine);
+        for (int i = tid * 4; i < ROWS * width; i += kThreads * 4) {
+            float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            float4 p[kCluster];
+#pragma unroll
+            for (int q = 0; q < kCluster; ++q) p[q] = read_remote(mapa_shared(at + 4 * i, q));
+#pragma unroll
+            for (int q = 0; q < kCluster; ++q) s.x += p[q].x, s.y += p[q].y, s.z += p[q].z, s.w += p[q].w;
+            *reinterpret_cast<float4 *>(V + i / width * pitch + i % width) =
+                make_float4(s.x * scale, s.y * scale, s.z * scale, s.w * scale);
+        }
+        cluster_sync();                                      // everyone has read: the parts may be written again
+        // 16 columns a turn: lane c of a row gets four neighbours
+        for (int n = n0 + warp * 16; n < n1; n += kWarps * 16) {
+            float acc[MT][2][4];
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[m][q][i] = 0.0f;
+            for (int rb = 0; rb < blocks; ++rb) {
+                float bv[2][2 * NR];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const int col = n + 4 * (g >> 1) + 2 * q + (g & 1);
+                    if (col < a.N)
+                        load_values<2 * NR, WW>(bv[q], a.B, (b_row + col) * a.rank, rb * R8 + 2 * NR * c, a.rank, a.vec_b, w_half);
+                    else {
+#pragma unroll
+                        for (int i = 0; i < 2 * NR; ++i) bv[q][i] = 0.0f;
+                    }
+                }
+#pragma unroll
+                for (int s = 0; s < NR; ++s)
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) {
+                        const float2 u = *reinterpret_cast<const float2 *>(V + (m * 16 + g) * pitch + rb * R8 + 2 * NR * c + 2 * s);
+                        const float2 w = *reinterpret_cast<const float2 *>(V + (m * 16 + 8 + g) * pitch + rb * R8 + 2 * NR * c + 2 * s);
+                        const float va[4] = {u.x, w.x, u.y, w.y};
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) mma_pieces<2, WW ? 2 : 1>(acc[m][q], va, bv[q][2 * s], bv[q][2 * s + 1]);
+                    }
+            }
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int row = m * 16 + h * 8 + g;
+                    if (ids[row] != id) continue;
+                    const int64_t from = (t0 + row) * a.ldy, to = (t0 + row) * a.ldo;
+                    const int col = n + 4 * c;
+                    const float d[4] = {acc[m][0][2 * h], acc[m][0][2 * h + 1], acc[m][1][2 * h], acc[m][1][2 * h + 1]};
+                    if (a.vec_y && col + 4 <= a.N) {
+                        if (a.y_type == QK_F32) {
+                            float4 f = *reinterpret_cast<const float4 *>(static_cast<const float *>(a.y) + from + col);
+                            f.x += d[0], f.y += d[1], f.z += d[2], f.w += d[3];
+                            *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + to + col) = f;
+                        } else {
+                            const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(a.y) + from + col);
+                            uint2 o;
+                            if (a.y_type == QK_F16) {
+                                const float2 f0 = __half22float2(*reinterpret_cast<const __half2 *>(&w.x));
+                                const float2 f1 = __half22float2(*reinterpret_cast<const __half2 *>(&w.y));
+                                const __half2 r0 = __floats2half2_rn(f0.x + d[0], f0.y + d[1]), r1 = __floats2half2_rn(f1.x + d[2], f1.y + d[3]);
+                                o = make_uint2(*reinterpret_cast<const uint32_t *>(&r0), *reinterpret_cast<const uint32_t *>(&r1));
+                            } else {
+                                const __nv_bfloat162 r0 = __floats2bfloat162_rn(__uint_as_float(w.x << 16) + d[0], __uint_as_float(w.x & 0xffff0000u) + d[1]);
+                                const __nv_bfloat162 r1 = __floats2bfloat162_rn(__uint_as_float(w.y << 16) + d[2], __uint_as_float(w.y & 0xffff0000u) + d[3]);
+                                o = make_uint2(*reinterpret_cast<const uint32_t *>(&r0), *reinterpret_cast<const uint32_t *>(&r1));
+                            }
+                            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + to + col) = o;
+                        }
+                    } else {
+                        for (int i = 0; i < 4 && col + i < a.N; ++i)
+                            store_float_as(a.out, to + col + i, a.y_type, load_as_float(a.y, from + col + i, a.y_type) + d[i]);
+                    }
+                }
+        }
+        __syncthreads();                                     // V is read to the end
+    }
+}
+
+template <int MT, int NR, bool XW, bool WW>
+cudaError_t launch_as(const LoraArgs &a, cudaStream_t st)
+{
+    constexpr int ROWS = 16 * MT, R8 = 8 * NR;
+    const int width = (a.rank + R8 - 1) / R8 * R8;
+    const size_t smem = sizeof(float) * (kWarps * ROWS * R8 + ROWS * width + ROWS * (width + 4));
+    const auto kern = lora_kernel<MT, NR, XW, WW>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    const int64_t tiles = (a.T + ROWS - 1) / ROWS;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles * a.steps * kCluster)), cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem, cfg.stream = st;
+    cudaLaunchAttribute at[2]{};
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = kCluster, at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at, cfg.numAttrs = library_programmatic() ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, a);
+}
+
+template <int MT, int NR>
+cudaError_t launch_types(const LoraArgs &a, cudaStream_t st)
+{
+    if (a.x_type == QK_F32)
+        return a.w_type == QK_F32 ? launch_as<MT, NR, true, true>(a, st) : launch_as<MT, NR, true, false>(a, st);
+    return a.w_type == QK_F32 ? launch_as<MT, NR, false, true>(a, st) : launch_as<MT, NR, false, false>(a, st);
+}
+
+template <int MT>
+cudaError_t launch_rank(const LoraArgs &a, cudaStream_t st)
+{
+    if (a.rank <= 8) return launch_types<MT, 1>(a, st);
+    if (a.rank <= 16) return launch_types<MT, 2>(a, st);
+    if (a.rank <= 32) return launch_types<MT, 4>(a, st);
+    return launch_types<MT, 8>(a, st);
+}
+
+bool multiple(const void *p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+bool type_ok(int t) { return t == QK_F32 || t == QK_F16 || t == QK_BF16; }
+int size_of(int t) { return t == QK_F32 ? 4 : 2; }
+
+}  // namespace
+}  // namespace qk
+
+using namespace qk;
+
+extern "C" int qk_lora(const void *x, int64_t ldx, int x_type, int64_t T, int64_t K, const void *A, const void *B, int w_type,
+                       int64_t n_adapters, int rank, int64_t N, const int32_t *ids, const float *scales, const void *y,
+                       int64_t ldy, void *out, int64_t ldo, int y_type, qk_stream_t stream)
+{
+    if (!type_ok(x_type) || !type_ok(w_type) || !type_ok(y_type)) return QK_ERR_TYPE;
+    if (T < 0 || K <= 0 || N <= 0 || n_adapters <= 0 || rank <= 0) return QK_ERR_BAD_DIM;
+    if (ldx == 0) ldx = K;
+    if (ldy == 0) ldy = N;
+    if (ldo == 0) ldo = N;
+    if (ldx < K || ldy < N || ldo < N || (out && out == y && ldo != ldy)) return QK_ERR_BAD_DIM;
+    if (rank > kMaxRank || K > (1 << 24) || N > (1 << 24) || T > (1 << 26) || n_adapters > INT32_MAX) return QK_ERR_TOO_LARGE;
+    if (T == 0) return QK_OK;
+    if (!x || !A || !B || !ids || !y || !out) return QK_ERR_NULL;
+    if (!multiple(x, size_of(x_type)) || !multiple(A, size_of(w_type)) || !multiple(B, size_of(w_type)) ||
+        !multiple(y, size_of(y_type)) || !multiple(out, size_of(y_type)) || !multiple(ids, 4) || !multiple(scales, 4))
+        return QK_ERR_ALIGN;
+    LoraArgs a{};
+    a.x = x, a.y = y, a.A = A, a.B = B, a.out = out, a.ldx = ldx, a.ldy = ldy, a.ldo = ldo, a.T = T;
+    a.n_adapters = n_adapters, a.x_type = x_type, a.y_type = y_type, a.w_type = w_type;
+    a.K = static_cast<int>(K), a.N = static_cast<int>(N), a.rank = rank, a.ids = ids, a.scales = scales;
+    // rows that start on 16 bytes (y: four values)
+    const auto rows_ok = [](const void *p, int64_t ld, int size, int n) { return multiple(p, n * size) && ld % n == 0; };
+    a.vec_x = rows_ok(x, ldx, size_of(x_type), 16 / size_of(x_type));
+    a.vec_a = rows_ok(A, K, size_of(w_type), 16 / size_of(w_type));
+    a.vec_b = rows_ok(B, rank, size_of(w_type), 16 / size_of(w_type));
+    a.vec_y = rows_ok(y, ldy, size_of(y_type), 4) && rows_ok(out, ldo, size_of(y_type), 4);
+    a.err = library_error_word();
+    int sms = 0, smem = 0;
+    if (!a.err || !device_limits(&sms, &smem)) return QK_ERR_CUDA;
+    // few tokens may each have an adapter of their own: as many clusters a tile as the GPU holds, up to its tokens
+    const bool tall = T > 16LL * sms / kCluster;
+    const int rows = tall ? 32 : 16;
+    const int64_t tiles = (T + rows - 1) / rows;
+    a.steps = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({rows, n_adapters, T, 4LL * sms / (kCluster * tiles)})));
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const cudaError_t e = tall ? launch_rank<2>(a, st) : launch_rank<1>(a, st);
+    return e == cudaSuccess ? QK_OK : QK_ERR_CUDA;
+}

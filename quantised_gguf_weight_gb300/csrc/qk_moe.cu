@@ -1,0 +1,426 @@
+// qk_moe.cu -- the experts' feed-forward products: the entry point, its
+// argument checks, and the kernels around the products (the plan that groups
+// assignments by expert, the operands' layout, the weighted sum).
+#include <algorithm>
+
+#include "qk_kv4.cuh"
+#include "qk_moe.cuh"
+
+namespace qk {
+using namespace moe;
+namespace {
+
+constexpr int kPlanThreads = 1024;
+
+struct PlanArgs {
+    const int32_t *ids;
+    int n, experts, per_warp;      // per_warp: ids of a warp, a multiple of 32
+    Plan plan;
+    int *err;
+};
+
+// Sum over the thread block before this thread, and all of it.
+__device__ __forceinline__ int scan_before(int v, int *warp_sums, int &all)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int in = v;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        const int o = __shfl_up_sync(~0u, in, d);
+        if (lane >= d) in += o;
+    }
+    __syncthreads();
+    if (lane == 31) warp_sums[warp] = in;
+    __syncthreads();
+    int before = 0;
+    all = 0;
+    for (int w = 0; w < kPlanThreads / 32; ++w) {
+        if (w < warp) before += warp_sums[w];
+        all += warp_sums[w];
+    }
+    return before + in - v;
+}
+
+// Groups the assignments by expert: a counting sort by one thread block.  Each warp counts its own run of ids, a
+// thread an expert turns the counts into first places, and each warp places its run again in order, so that places
+// rise with the assignments.
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a)
+{
+    extern __shared__ int counts[];             // [warp][expert]
+    __shared__ int warp_sums[kPlanThreads / 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int first = warp * a.per_warp, last = min(a.n, first + a.per_warp);
+    let_next_start();
+    for (int i = threadIdx.x; i < kPlanThreads / 32 * a.experts; i += kPlanThreads) counts[i] = 0;
+    __syncthreads();
+    wait_for_previous();
+    int *mine = counts + warp * a.experts;
+    for (int base = first; base < last; base += 32) {
+        const int i = base + lane;
+        const int id = i < last ? a.ids[i] : -1;
+        const bool live = id >= 0 && id < a.experts;
+        if (i < last && id >= a.experts) record_error(a.err, kErrBadIndex);
+        const unsigned same = __match_any_sync(~0u, live ? id : -1);
+        if (live && lane == __ffs(same) - 1) mine[id] += __popc(same);
+        __syncwarp();
+    }
+    __syncthreads();
+    const int e = threadIdx.x;
+    int n = 0;
+    if (e < a.experts)
+        for (int w = 0; w < kPlanThreads / 32; ++w) {
+            const int k = counts[w * a.experts + e];
+            counts[w * a.experts + e] = n;
+            n += k;
+        }
+    int places, octets, sets;
+    const int first_place = scan_before(n, warp_sums, places);
+    const int octet0 = scan_before((n + 7) / 8, warp_sums, octets);
+    const int set0 = scan_before((n + 8 * kSetOctets - 1) / (8 * kSetOctets), warp_sums, sets);
+    __shared__ int place_of[kMaxExperts], octet_of[kMaxExperts];
+    if (e < a.experts) {
+        place_of[e] = first_place, octet_of[e] = octet0;
+        for (int i = 0, s = set0; i < n; i += 8 * kSetOctets, ++s)
+            a.plan.sets[s] = {e, first_place + i, min(8 * kSetOctets, n - i), octet0 + i / 8};
+    }
+    if (e == 0) a.plan.head[0] = sets, a.plan.head[1] = octets, a.plan.head[2] = places;
+    __syncthreads();
+    for (int base = first; base < last; base += 32) {
+        const int i = base + lane;
+        const int id = i < last ? a.ids[i] : -1;
+        const bool live = id >= 0 && id < a.experts;
+        const unsigned same = __match_any_sync(~0u, live ? id : -1);
+        const int before = live ? mine[id] : 0;
+        __syncwarp();
+        if (live) {
+            const int k = before + __popc(same & ((1u << lane) - 1));       // its number among the expert's
+            if (lane == __ffs(same) - 1) mine[id] = before + __popc(same);
+            const int p = place_of[id] + k;
+            a.plan.assignment[p] = i, a.plan.place[i] = p;
+            a.plan.column[p] = octet_of[id] * 8 + k;
+        } else if (i < last) {
+            a.plan.place[i] = id < 0 ? -1 : -2;
+        }
+        __syncwarp();
+    }
+}
+
+// Four neighbouring values of a row, 0 past its end.
+__device__ __forceinline__ float4 four(const void *x, int64_t row, int k, int cols, int type, bool vec)
+{
+    if (vec && k + 4 <= cols) {
+        if (type == QK_F32) return *reinterpret_cast<const float4 *>(static_cast<const float *>(x) + row + k);
+        const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(x) + row + k);
+        if (type == QK_F16) {
+            const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&w.x));
+            const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&w.y));
+            return make_float4(a.x, a.y, b.x, b.y);
+        }
+        return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
+                           __uint_as_float(w.y & 0xffff0000u));
+    }
+    float v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = k + i < cols ? load_as_float(x, row + k + i, type) : 0.0f;
+    return make_float4(v[0], v[1], v[2], v[3]);
+}
+
+__device__ __forceinline__ uint32_t pack2h(float a, float b)
+{
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// Four scaled values as hi (and lo) pieces, in the order (0, 2, 1, 3) that taking nibbles and bytes apart by masks gives.
+__device__ __forceinline__ void pieces_of(const float4 v, uint2 &hi, uint2 &lo)
+{
+    hi = make_uint2(pack2h(v.x, v.z), pack2h(v.y, v.w));
+    const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&hi.x));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&hi.y));
+    lo = make_uint2(pack2h(v.x - a.x, v.z - a.y), pack2h(v.y - b.x, v.w - b.y));
+}
+
+constexpr int kPackThreads = 256;
+
+// A thread block lays out one place's row.  Thread (unit, c, i) makes the 16 bytes that lane (column, c) of step i reads.
+__global__ void __launch_bounds__(kPackThreads) pack_kernel(const PackArgs a, bool vec)
+{
+    __shared__ uint32_t warp_max[kPackThreads / 32];
+    let_next_start();
+    wait_for_previous();
+    const int p = blockIdx.x;
+    if (p >= a.plan.head[2]) return;
+    const int64_t row = static_cast<int64_t>(a.top_k ? a.plan.assignment[p] / a.top_k : p) * a.ld;
+    uint32_t most = 0;          // magnitudes order as their bits do
+    for (int k = threadIdx.x * 4; k < a.cols; k += kPackThreads * 4) {
+        const float4 v = four(a.x, row, k, a.cols, a.type, vec);
+        most = max(max(most, max(__float_as_uint(v.x) & 0x7fffffffu, __float_as_uint(v.y) & 0x7fffffffu)),
+                   max(__float_as_uint(v.z) & 0x7fffffffu, __float_as_uint(v.w) & 0x7fffffffu));
+    }
+    most = __reduce_max_sync(~0u, most);
+    if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = most;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kPackThreads / 32; ++w) most = max(most, warp_max[w]);
+    // 2^e puts it into [2^14, 2^15); rows of zeros, infinities and NaN stay as they are, and e stops where 2^-e is
+    // no normal number any more
+    const int ex = most >= 0x7f800000u || most == 0 ? 141 : max(static_cast<int>(most >> 23), 15);
+    const float up = __uint_as_float(static_cast<uint32_t>(127 + 141 - ex) << 23);
+    if (threadIdx.x == 0) a.scale[p] = __uint_as_float(static_cast<uint32_t>(127 - 141 + ex) << 23);
+    const int64_t unit = octet_unit_bytes(a.fmt, a.pieces);
+    const int column = a.plan.column[p];
+    uint8_t *out = a.out + (column >> 3) * unit * a.units;
+    const int col = column & 7;
+    for (int j = threadIdx.x; j < a.units * 32; j += kPackThreads) {
+        const int u = j >> 5, c = (j >> 3) & 3, i = j & 7;
+        const int k = u * kUnit;
+        int k0, k1;
+        if (a.fmt == kFmtQ4K) k0 = k + 64 * c + 4 * i, k1 = k0 + 32;                     // sub-blocks 2c and 2c + 1
+        else if (a.fmt == kFmtQ80) k0 = k + 32 * i + 8 * c, k1 = k0 + 4;                 // block i
+        else k0 = k + 128 * (i >> 2) + 64 * (i & 1) + 16 * ((i >> 1) & 1) + 4 * c, k1 = k0 + 32;    // sub-blocks t, t + 1
+        float4 v0 = four(a.x, row, k0, a.cols, a.type, vec), v1 = four(a.x, row, k1, a.cols, a.type, vec);
+        v0.x *= up, v0.y *= up, v0.z *= up, v0.w *= up;
+        v1.x *= up, v1.y *= up, v1.z *= up, v1.w *= up;
+        uint2 h0, l0, h1, l1;
+        pieces_of(v0, h0, l0), pieces_of(v1, h1, l1);
+        uint8_t *at = out + u * unit;
+        const int lane = col * 4 + c;
+        *reinterpret_cast<uint4 *>(at + i * 512 + lane * 16) = make_uint4(h0.x, h0.y, h1.x, h1.y);
+        if (a.pieces == 2)
+            *reinterpret_cast<uint4 *>(at + kPieceBytes + i * 512 + lane * 16) = make_uint4(l0.x, l0.y, l1.x, l1.y);
+        if (a.fmt == kFmtQ4K) {
+            // sums of the values as the pieces hold them, over the 8 threads of a sub-block; 2^-5 of them in two pieces
+            const auto held = [&](uint2 h, uint2 l) {
+                const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&h.x));
+                const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&h.y));
+                float s = (x.x + x.y) + (y.x + y.y);
+                if (a.pieces == 2) {
+                    const float2 z = __half22float2(*reinterpret_cast<const __half2 *>(&l.x));
+                    const float2 w = __half22float2(*reinterpret_cast<const __half2 *>(&l.y));
+                    s += (z.x + z.y) + (w.x + w.y);
+                }
+                return s;
+            };
+            float s0 = held(h0, l0), s1 = held(h1, l1);
+#pragma unroll
+            for (int d = 1; d < 8; d *= 2) s0 += __shfl_xor_sync(~0u, s0, d), s1 += __shfl_xor_sync(~0u, s1, d);
+            s0 *= 0.03125f, s1 *= 0.03125f;
+            if (i == 0) {
+                const uint32_t hi = pack2h(s0, s1);
+                const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+                *reinterpret_cast<uint2 *>(at + a.pieces * kPieceBytes + lane * 8) =
+                    make_uint2(hi, pack2h(s0 - h.x, s1 - h.y));
+            }
+        }
+    }
+}
+
+struct SumArgs {
+    Plan plan;
+    const float *parts;       // [place][N]
+    const float *weights;
+    int top_k, N, type;
+    void *y;
+    int64_t ldy;
+};
+
+constexpr int kSumThreads = 256;
+
+// y[t] = sum over j, in order, of weights[t][j] * the part of assignment (t, j).
+__global__ void __launch_bounds__(kSumThreads) sum_kernel(const SumArgs a)
+{
+    let_next_start();
+    wait_for_previous();
+    const int64_t t = blockIdx.x;
+    const int n = (blockIdx.y * kSumThreads + threadIdx.x) * 4;
+    if (n >= a.N) return;
+    const bool vec = a.N % 4 == 0;
+    float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int j = 0; j < a.top_k; ++j) {
+        const int p = a.plan.place[t * a.top_k + j];
+        if (p == -1) continue;
+        const float w = p < 0 ? __int_as_float(0x7fc00000) : a.weights[t * a.top_k + j];
+        const float *part = a.parts + static_cast<int64_t>(p < 0 ? 0 : p) * a.N + n;
+        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (p >= 0 && vec) {
+            const float4 f = *reinterpret_cast<const float4 *>(part);
+            v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+        } else if (p >= 0) {
+            for (int i = 0; i < 4; ++i) v[i] = n + i < a.N ? part[i] : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] += w * v[i];
+    }
+    for (int i = 0; i < 4 && n + i < a.N; ++i) store_float_as(a.y, t * a.ldy + n + i, a.type, y[i]);
+}
+
+// ---------------------------------------------------------------- the call
+
+struct Layout {
+    int64_t A, octets, sets;
+    int pieces;
+    int64_t head, assignment, place, column, set, x_scale, h_scale, x, h, h_ops, parts, bytes;
+};
+
+int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
+
+// Where a call's scratch lies.  The types decide how many pieces an operand has.
+Layout layout_of(int64_t T, int top_k, int64_t E, int64_t K, int64_t F, int64_t N, int gate_fmt, int down_fmt, int x_type,
+                 int y_type)
+{
+    Layout l{};
+    l.A = T * top_k;
+    l.pieces = x_type == QK_F32 || y_type == QK_F32 ? 2 : 1;
+    const int64_t used = std::min(l.A, E);
+    l.octets = used + l.A / 8;
+    l.sets = used + l.A / (8 * kSetOctets);
+    int64_t at = 0;
+    const auto take = [&](int64_t n) {
+        const int64_t was = at;
+        at += up256(n);
+        return was;
+    };
+    const auto operands = [&](int fmt, int64_t cols) {
+        // a set's missing octets are read, too
+        return (l.octets + kSetOctets - 1) * ((cols + kUnit - 1) / kUnit) * octet_unit_bytes(fmt, l.pieces);
+    };
+    l.head = take(64), l.assignment = take(4 * l.A), l.place = take(4 * l.A), l.column = take(4 * l.A);
+    l.set = take(l.sets * sizeof(ExpertSet));
+    l.x_scale = take(4 * l.A), l.h_scale = take(4 * l.A);
+    l.x = take(operands(gate_fmt, K)), l.h = take(4 * l.A * F), l.h_ops = take(operands(down_fmt, F));
+    l.parts = take(4 * l.A * N);
+    l.bytes = at;
+    return l;
+}
+
+bool multiple(const void *p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+bool type_ok(int t) { return t == QK_F32 || t == QK_F16 || t == QK_BF16; }
+bool format_ok(int f) { return f == kFmtQ80 || f == kFmtQ4K || f == kFmtQ6K; }
+int size_of(int t) { return t == QK_F32 ? 4 : 2; }
+
+// An expert tensor's rows of `cols` columns, `rows` of each expert (a qk_status).
+int check_weights(const qk_expert_weights *w, int64_t E, int64_t rows, int64_t cols, Weights *out)
+{
+    if (!w || !w->w) return QK_ERR_NULL;
+    if (!format_ok(w->format)) return QK_ERR_TYPE;
+    const int64_t per = w->expert_rows == 0 ? rows : w->expert_rows;
+    if (w->row_offset < 0 || per < rows) return QK_ERR_BAD_DIM;
+    if (strict_blocks_reject(w->format, cols)) return QK_ERR_BAD_DIM;
+    const int64_t rb = row_bytes_of(w->format, cols);
+    if (per > INT32_MAX || w->row_offset > INT64_MAX / rb - E * per) return QK_ERR_TOO_LARGE;
+    if (!multiple(w->w, w->format == kFmtQ4K ? 16 : 2)) return QK_ERR_ALIGN;
+    *out = {static_cast<const uint8_t *>(w->w) + w->row_offset * rb, per, rb};
+    return QK_OK;
+}
+
+// Warps that share a tile's columns: enough for every SM's 16 warps to have work where tiles are few.
+int share(int64_t tiles, int units, int sms)
+{
+    int kw = 1;
+    while (kw < kRowWarps && 2 * kw <= units && tiles * kw < 16LL * sms) kw *= 2;
+    return kw;
+}
+
+cudaError_t rows_launch(const RowsArgs &a, bool paired, int sms, cudaStream_t st)
+{
+    return a.fmt == kFmtQ4K ? rows_launch_q4k(a, paired, sms, st)
+                            : a.fmt == kFmtQ80 ? rows_launch_q80(a, paired, sms, st) : rows_launch_q6k(a, paired, sms, st);
+}
+
+}  // namespace
+}  // namespace qk
+
+using namespace qk;
+
+extern "C" {
+
+size_t qk_moe_ffn_workspace_bytes(int64_t T, int top_k, int64_t n_experts, int64_t K, int64_t F, int64_t N)
+{
+    if (T <= 0 || top_k <= 0 || n_experts <= 0 || K <= 0 || F <= 0 || N <= 0) return 0;
+    if (T > INT32_MAX / top_k || K > INT32_MAX || F > INT32_MAX || N > INT32_MAX) return 0;
+    return static_cast<size_t>(layout_of(T, top_k, n_experts, K, F, N, kFmtQ4K, kFmtQ4K, QK_F32, QK_F32).bytes);
+}
+
+int qk_moe_ffn(const qk_expert_weights *gate, const qk_expert_weights *up, const qk_expert_weights *down, int64_t n_experts,
+               int64_t K, int64_t F, int64_t N, const void *x, int64_t ldx, int x_type, int64_t T, const int32_t *ids,
+               const float *weights, int top_k, void *y, int64_t ldy, int y_type, void *workspace, size_t workspace_bytes,
+               qk_stream_t stream)
+{
+    if (!gate || !up || !down) return QK_ERR_NULL;
+    if (!type_ok(x_type) || !type_ok(y_type) || gate->format != up->format) return QK_ERR_TYPE;
+    if (n_experts <= 0 || K <= 0 || F <= 0 || N <= 0 || T < 0 || top_k <= 0) return QK_ERR_BAD_DIM;
+    if (ldx == 0) ldx = K;
+    if (ldy == 0) ldy = N;
+    if (ldx < K || ldy < N) return QK_ERR_BAD_DIM;
+    if (n_experts > kMaxExperts || K > (1 << 24) || F > (1 << 24) || N > (1 << 24) || T > (1 << 28) / top_k)
+        return QK_ERR_TOO_LARGE;
+    Weights wg, wu, wd;
+    int st = check_weights(gate, n_experts, F, K, &wg);
+    if (st == QK_OK) st = check_weights(up, n_experts, F, K, &wu);
+    if (st == QK_OK) st = check_weights(down, n_experts, N, F, &wd);
+    if (st != QK_OK) return st;
+    if (T == 0) return QK_OK;
+    if (!x || !ids || !weights || !y) return QK_ERR_NULL;
+    if (!multiple(x, size_of(x_type)) || !multiple(y, size_of(y_type)) || !multiple(ids, 4) || !multiple(weights, 4))
+        return QK_ERR_ALIGN;
+    const Layout l = layout_of(T, top_k, n_experts, K, F, N, gate->format, down->format, x_type, y_type);
+    if (!workspace || !multiple(workspace, 256) || workspace_bytes < static_cast<size_t>(l.bytes)) return QK_ERR_WORKSPACE;
+    int sms = 0, smem = 0;
+    int *err = library_error_word();
+    if (!err || !device_limits(&sms, &smem)) return QK_ERR_CUDA;
+    char *ws = static_cast<char *>(workspace);
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+
+    PlanArgs pa{};
+    pa.ids = ids, pa.n = static_cast<int>(l.A), pa.experts = static_cast<int>(n_experts), pa.err = err;
+    constexpr int kWarps = kPlanThreads / 32;
+    pa.per_warp = static_cast<int>((l.A + 32 * kWarps - 1) / (32 * kWarps) * 32);
+    pa.plan = {reinterpret_cast<int *>(ws + l.head), reinterpret_cast<int *>(ws + l.assignment),
+               reinterpret_cast<int *>(ws + l.place), reinterpret_cast<int *>(ws + l.column),
+               reinterpret_cast<ExpertSet *>(ws + l.set)};
+    const size_t counts = sizeof(int) * kWarps * pa.experts;
+    cudaError_t e = cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(sizeof(int) * kWarps * kMaxExperts));
+    if (e == cudaSuccess) e = launch_chained(plan_kernel, dim3(1), kPlanThreads, counts, s, library_programmatic(), pa);
+    if (e != cudaSuccess) return QK_ERR_CUDA;
+
+    const auto pack = [&](const void *rows, int64_t ld, int type, int per_row, int64_t cols, int fmt, int64_t to, int64_t scale) {
+        PackArgs k{};
+        k.plan = pa.plan, k.x = rows, k.ld = ld, k.type = type, k.top_k = per_row;
+        k.cols = static_cast<int>(cols), k.units = static_cast<int>((cols + kUnit - 1) / kUnit);
+        k.pieces = l.pieces, k.fmt = fmt;
+        k.out = reinterpret_cast<uint8_t *>(ws + to), k.scale = reinterpret_cast<float *>(ws + scale);
+        const bool vec = multiple(rows, 4 * size_of(type)) && ld % 4 == 0;
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(static_cast<unsigned>(l.A)), cfg.blockDim = dim3(kPackThreads), cfg.stream = s;
+        cudaLaunchAttribute at{};
+        at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at.val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = &at, cfg.numAttrs = 1;
+        return cudaLaunchKernelEx(&cfg, pack_kernel, k, vec);
+    };
+    const auto products = [&](const Weights &a, const Weights &b, int fmt, int64_t cols, int64_t rows, bool paired,
+                              int64_t ops, int64_t scale, int64_t to) {
+        RowsArgs r{};
+        r.plan = pa.plan, r.a = a, r.b = b, r.fmt = fmt;
+        r.cols = static_cast<int>(cols), r.units = static_cast<int>((cols + kUnit - 1) / kUnit), r.pieces = l.pieces;
+        r.rows = static_cast<int>(rows), r.tiles = static_cast<int>(paired ? (rows + 7) / 8 : (rows + 15) / 16);
+        r.kw = share(std::min(l.A, n_experts) * r.tiles, r.units, sms);
+        r.x = reinterpret_cast<const uint8_t *>(ws + ops), r.scale = reinterpret_cast<const float *>(ws + scale);
+        r.out = reinterpret_cast<float *>(ws + to);
+        return rows_launch(r, paired, sms, s);
+    };
+    e = pack(x, ldx, x_type, top_k, K, gate->format, l.x, l.x_scale);
+    if (e == cudaSuccess) e = products(wg, wu, gate->format, K, F, true, l.x, l.x_scale, l.h);
+    if (e == cudaSuccess) e = pack(ws + l.h, F, QK_F32, 0, F, down->format, l.h_ops, l.h_scale);
+    if (e == cudaSuccess) e = products(wd, wd, down->format, F, N, false, l.h_ops, l.h_scale, l.parts);
+    if (e != cudaSuccess) return QK_ERR_CUDA;
+    SumArgs u{};
+    u.plan = pa.plan, u.parts = reinterpret_cast<const float *>(ws + l.parts), u.weights = weights;
+    u.top_k = top_k, u.N = static_cast<int>(N), u.type = y_type, u.y = y, u.ldy = ldy;
+    e = launch_chained(sum_kernel, dim3(static_cast<unsigned>(T), static_cast<unsigned>((N + 4 * kSumThreads - 1) / (4 * kSumThreads))),
+                       kSumThreads, 0, s, true, u);
+    return e == cudaSuccess ? QK_OK : QK_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -1,0 +1,106 @@
+// qk_moe.cuh -- what the kernels of the experts' feed-forward products share:
+// the call's sizes, the plan that groups the assignments by expert, and the
+// operands' layout.
+//
+// An assignment is a place (t, j) of ids [T][top_k].  The plan sorts the live
+// ones by expert (stable, so nothing depends on the order of atomics); `place`
+// is an assignment's place in that order.  Eight neighbouring places of one
+// expert are an octet, the 8 columns of an m16n8k16 product, and up to kSetOctets
+// octets a set, the columns that share one pass over the expert's weights.
+//
+// Operands: a row x is held as fp16 pieces hi + lo of x * 2^e, 2^e the power of
+// two that puts the row's largest magnitude into [2^14, 2^15): a value is then
+// exact to 2^-23 of itself, or to 2^-39 of the row's largest.
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "qk_device.cuh"
+#include "qk_internal.h"
+
+namespace qk {
+namespace moe {
+
+constexpr int kMaxExperts = 1024;
+constexpr int kSetOctets = 4;
+constexpr int kRowWarps = 8;                      // warps of a thread block of the few-token products
+constexpr int kUnit = 256;                        // columns of a unit of the products' loops
+constexpr int kPieceBytes = 8 * 32 * 16;          // an octet's unit, one piece: 8 steps of 16 bytes a lane
+constexpr int kSumBytes = 32 * 8;                 // the sums of its sub-blocks (Q4_K)
+
+struct ExpertSet {
+    int expert, first, count, octet;              // first place, places, first octet
+};
+
+struct Plan {
+    int *head;                // [0] sets, [1] octets, [2] live places
+    int *assignment;          // [A] assignment at a place
+    int *place;               // [A] place of an assignment; -1 none, -2 an id out of range
+    int *column;              // [A] octet * 8 + column of a place
+    ExpertSet *sets;
+};
+
+// Expert e's row r is row `first_row + e * expert_rows + r` of w.
+struct Weights {
+    const uint8_t *w;
+    int64_t expert_rows, row_bytes;
+};
+
+// Rows [A or T][ld] to operands.
+struct PackArgs {
+    Plan plan;
+    const void *x;
+    int64_t ld;
+    int type, top_k;          // row of a place: x[assignment / top_k], or x[place] where top_k == 0
+    int cols, units, pieces, fmt;
+    uint8_t *out;
+    float *scale;             // [place] 2^-e
+};
+
+struct RowsArgs {
+    Plan plan;
+    Weights a, b;             // gate and up; or down twice
+    int fmt, cols, units, pieces;
+    int rows, tiles;          // output columns and 16-row tiles (8 + 8 where gate and up are paired)
+    int kw;                   // warps that share a tile's units
+    const uint8_t *x;         // operands, octet after octet
+    const float *scale;
+    float *out;               // [place][rows]
+};
+
+__host__ __device__ constexpr int64_t octet_unit_bytes(int fmt, int pieces)
+{
+    return pieces * kPieceBytes + (fmt == kFmtQ4K ? kSumBytes : 0);
+}
+__host__ __device__ constexpr int unit_bytes(int fmt) { return fmt == kFmtQ4K ? 144 : fmt == kFmtQ80 ? 272 : 210; }
+__host__ __device__ inline int64_t row_bytes_of(int fmt, int64_t K)
+{
+    return fmt == kFmtQ80 ? (K + 31) / 32 * 34 : (K + 255) / 256 * unit_bytes(fmt);
+}
+
+cudaError_t rows_launch_q4k(const RowsArgs &a, bool paired, int sms, cudaStream_t st);
+cudaError_t rows_launch_q80(const RowsArgs &a, bool paired, int sms, cudaStream_t st);
+cudaError_t rows_launch_q6k(const RowsArgs &a, bool paired, int sms, cudaStream_t st);
+
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// A launch that may start while the kernel before it drains (its threads call wait_for_previous() before they read
+// what that one writes).
+template <class Kern, class Args>
+cudaError_t launch_chained(Kern kern, dim3 grid, int threads, size_t smem, cudaStream_t st, bool chained, const Args &a)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid, cfg.blockDim = dim3(threads), cfg.dynamicSmemBytes = smem, cfg.stream = st;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at, cfg.numAttrs = chained ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kern, a);
+}
+
+}  // namespace moe
+}  // namespace qk

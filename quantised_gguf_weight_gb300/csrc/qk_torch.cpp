@@ -280,6 +280,139 @@ PyObject *attn_q4(PyObject *, PyObject *const *a, Py_ssize_t n)
     END_HANDLE_TH_ERRORS
 }
 
+// [T][k] int32 and fp32, contiguous.
+template <class V>
+V *pairs_of(const at::Tensor &t, int64_t T, int64_t k, at::ScalarType type, const char *name)
+{
+    TORCH_CHECK_VALUE(t.scalar_type() == type, name, " must be ", type, ", not ", t.scalar_type());
+    TORCH_CHECK_VALUE(t.dim() == 2 && t.size(0) == T && t.size(1) == k && t.is_contiguous(), name, " must be contiguous [", T,
+                      "][", k, "], got ", t.sizes());
+    return static_cast<V *>(t.data_ptr());
+}
+
+// moe_route(logits, top_k, score, bias, n_groups, top_groups, group_top, renorm, scale, ids, weights, stream) -> (ids, weights)
+PyObject *moe_route(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    count_args(n, 12);
+    const int dev = c10::cuda::current_device();
+    const at::Tensor &lt = tensor_of(a[0], "logits", dev);
+    const int64_t E = lt.dim() == 2 ? lt.size(1) : 0;
+    TORCH_CHECK_VALUE(E > 0 && E <= INT32_MAX, "logits must be rows of the experts' logits, got shape ", lt.sizes());
+    const Rows l = rows_of(lt, E, "logits");
+    const int k = int32_of(a[1], "top_k");
+    TORCH_CHECK_VALUE(k > 0 && k <= E, "top_k must be in 1..", E, ", got ", k);
+    at::Tensor ids = a[9] == Py_None ? new_rows(l.n, k, lt, at::kInt, a[11]) : tensor_of(a[9], "ids", dev);
+    at::Tensor weights = a[10] == Py_None ? new_rows(l.n, k, lt, at::kFloat, a[11]) : tensor_of(a[10], "weights", dev);
+    int32_t *ip = pairs_of<int32_t>(ids, l.n, k, at::kInt, "ids");
+    float *wp = pairs_of<float>(weights, l.n, k, at::kFloat, "weights");
+    const int status = qk_moe_route(l.p, l.ld, l.type, l.n, static_cast<int>(E), k, int32_of(a[2], "score"),
+                                    vector_of<const float>(a[3], E, at::kFloat, "bias", dev), int32_of(a[4], "n_groups"),
+                                    int32_of(a[5], "top_groups"), int32_of(a[6], "group_top"), PyObject_IsTrue(a[7]),
+                                    float_of(a[8]), ip, wp, stream_of(a[11]));
+    if (status != QK_OK) return PyLong_FromLong(status);
+    PyObject *pair = PyTuple_New(2);
+    if (!pair) throw python_error();
+    PyTuple_SET_ITEM(pair, 0, THPVariable_Wrap(ids));
+    PyTuple_SET_ITEM(pair, 1, THPVariable_Wrap(weights));
+    return pair;
+    END_HANDLE_TH_ERRORS
+}
+
+int64_t row_bytes(int format, int64_t cols)
+{
+    return format == QK_Q8_0 ? qk_row_bytes_q8_0(cols) : format == QK_Q4_K ? qk_row_bytes_q4_k(cols) : qk_row_bytes_q6_k(cols);
+}
+
+// Four arguments from a[0]: format, bytes, row_offset, expert_rows; `rows` rows of `cols` columns of each of E experts.
+qk_expert_weights weights_of(PyObject *const *a, int64_t E, int64_t rows, int64_t cols, const char *name, int dev)
+{
+    qk_expert_weights w;
+    w.format = int32_of(a[0], "format");
+    const at::Tensor &t = tensor_of(a[1], name, dev);
+    TORCH_CHECK_VALUE(t.is_contiguous(), name, " must be contiguous");
+    w.w = t.data_ptr();
+    w.row_offset = int_of(a[2]), w.expert_rows = int_of(a[3]);
+    const int64_t per = w.expert_rows == 0 ? rows : w.expert_rows, rb = row_bytes(w.format, cols);
+    constexpr int64_t kMost = int64_t(1) << 40;          // no row number is beyond it: the products below cannot overflow
+    TORCH_CHECK_VALUE(w.row_offset >= 0 && per >= rows && w.row_offset <= kMost && per <= INT32_MAX && E <= (1 << 20), name,
+                      " has no such rows: offset ", w.row_offset, ", ", per, " an expert, of ", rows);
+    const int64_t need = w.row_offset + (E - 1) * per + rows;
+    TORCH_CHECK_VALUE(need <= static_cast<int64_t>(t.nbytes()) / rb, name, " holds ", t.nbytes(), " bytes, the call reads ", need,
+                      " rows of ", rb);
+    return w;
+}
+
+// moe_ffn(x, ids, weights, gate (4), up (4), down (4), n_experts, F, N, y, workspace, stream)
+PyObject *moe_ffn(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    count_args(n, 21);
+    const int dev = c10::cuda::current_device();
+    const at::Tensor &xt = tensor_of(a[0], "x", dev);
+    const int64_t K = xt.dim() == 2 ? xt.size(1) : 0;
+    TORCH_CHECK_VALUE(K > 0 && K <= INT32_MAX, "x must be rows, got shape ", xt.sizes());
+    const Rows x = rows_of(xt, K, "x");
+    const at::Tensor &it = tensor_of(a[1], "ids", dev), &wt = tensor_of(a[2], "weights", dev);
+    const int64_t k = it.dim() == 2 ? it.size(1) : 0;
+    TORCH_CHECK_VALUE(k > 0 && k <= INT32_MAX, "ids must be [tokens][top_k], got shape ", it.sizes());
+    const int32_t *ids = pairs_of<int32_t>(it, x.n, k, at::kInt, "ids");
+    const float *weights = pairs_of<float>(wt, x.n, k, at::kFloat, "weights");
+    const int64_t E = int_of(a[15]), F = int_of(a[16]), N = int_of(a[17]) == 0 ? K : int_of(a[17]);
+    TORCH_CHECK_VALUE(E > 0 && F > 0 && F <= INT32_MAX && N > 0 && N <= INT32_MAX, "n_experts, F and N must be positive, got ", E,
+                      ", ", F, ", ", N);
+    const qk_expert_weights gate = weights_of(a + 3, E, F, K, "gate", dev), up = weights_of(a + 7, E, F, K, "up", dev),
+                            down = weights_of(a + 11, E, N, F, "down", dev);
+    at::Tensor made;
+    const bool given = a[18] != Py_None;
+    if (!given) made = new_rows(x.n, N, xt, xt.scalar_type(), a[20]);
+    const Rows y = rows_of(given ? tensor_of(a[18], "y", dev) : made, N, "y");
+    TORCH_CHECK_VALUE(y.n >= x.n, "y has ", y.n, " rows, x ", x.n);
+    at::Tensor scratch;
+    if (a[19] == Py_None)
+        scratch = new_rows(1, static_cast<int64_t>(qk_moe_ffn_workspace_bytes(x.n, static_cast<int>(k), E, K, F, N)), xt, at::kByte,
+                           a[20]);
+    else
+        scratch = tensor_of(a[19], "workspace", dev);
+    TORCH_CHECK_VALUE(scratch.is_contiguous(), "workspace must be contiguous");
+    const int status = qk_moe_ffn(&gate, &up, &down, E, K, F, N, x.p, x.ld, x.type, x.n, ids, weights, static_cast<int>(k), y.p,
+                                  y.ld, y.type, scratch.data_ptr(), scratch.nbytes(), stream_of(a[20]));
+    return done(status, given ? a[18] : nullptr, made);
+    END_HANDLE_TH_ERRORS
+}
+
+// lora(x, y, A, B, ids, scales, out, stream)
+PyObject *lora(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    count_args(n, 8);
+    const int dev = c10::cuda::current_device();
+    const at::Tensor &xt = tensor_of(a[0], "x", dev), &yt = tensor_of(a[1], "y", dev);
+    const at::Tensor &At = tensor_of(a[2], "A", dev), &Bt = tensor_of(a[3], "B", dev);
+    TORCH_CHECK_VALUE(At.dim() == 3 && Bt.dim() == 3 && At.is_contiguous() && Bt.is_contiguous() && At.size(0) == Bt.size(0) &&
+                          At.size(1) == Bt.size(2) && At.size(0) > 0 && At.numel() > 0 && Bt.numel() > 0,
+                      "A and B must be contiguous [adapters][rank][K] and [adapters][N][rank], got ", At.sizes(), " and ", Bt.sizes());
+    const int w_type = code_of(At, "A");
+    TORCH_CHECK_VALUE(code_of(Bt, "B") == w_type, "A and B must have one element type");
+    TORCH_CHECK_VALUE(At.size(1) <= INT32_MAX, "rank is out of range: ", At.size(1));
+    const Rows x = rows_of(xt, At.size(2), "x"), y = rows_of(yt, Bt.size(1), "y");
+    TORCH_CHECK_VALUE(y.n == x.n, "x has ", x.n, " rows, y ", y.n);
+    at::Tensor made;
+    const bool given = a[6] != Py_None;
+    if (!given) made = new_rows(x.n, Bt.size(1), yt, yt.scalar_type(), a[7]);
+    const Rows o = rows_of(given ? tensor_of(a[6], "out", dev) : made, Bt.size(1), "out");
+    TORCH_CHECK_VALUE(o.type == y.type, "out and y must have one element type");
+    TORCH_CHECK_VALUE(o.n >= y.n, "out has ", o.n, " rows, y ", y.n);
+    const int32_t *ids = vector_of<const int32_t>(a[4], x.n, at::kInt, "ids", dev);
+    TORCH_CHECK_VALUE(ids || x.n == 0, "ids must be a CUDA tensor");
+    const int status = qk_lora(x.p, x.ld, x.type, x.n, At.size(2), At.data_ptr(), Bt.data_ptr(), w_type, At.size(0),
+                               static_cast<int>(At.size(1)), Bt.size(1), ids,
+                               vector_of<const float>(a[5], At.size(0), at::kFloat, "scales", dev), y.p, y.ld, o.p, o.ld, y.type,
+                               stream_of(a[7]));
+    return done(status, given ? a[6] : nullptr, made);
+    END_HANDLE_TH_ERRORS
+}
+
 template <class F>
 PyCFunction fast(F f)
 {
@@ -290,6 +423,9 @@ PyMethodDef methods[] = {{"norm_rope", fast(norm_rope), METH_FASTCALL, nullptr},
                          {"kv_append_q4", fast(kv_append_q4), METH_FASTCALL, nullptr},
                          {"kv_read_q4", fast(kv_read_q4), METH_FASTCALL, nullptr},
                          {"attn_q4", fast(attn_q4), METH_FASTCALL, nullptr},
+                         {"moe_route", fast(moe_route), METH_FASTCALL, nullptr},
+                         {"moe_ffn", fast(moe_ffn), METH_FASTCALL, nullptr},
+                         {"lora", fast(lora), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "qk_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

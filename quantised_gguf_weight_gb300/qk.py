@@ -12,6 +12,7 @@ import ctypes
 import importlib.util
 import os
 import threading
+from typing import NamedTuple
 
 import torch
 
@@ -26,6 +27,8 @@ STATUS = {0: "QK_OK", 1: "QK_ERR_NULL", 2: "QK_ERR_BAD_DIM", 3: "QK_ERR_ALIGN", 
           9: "QK_ERR_BAD_INDEX", 10: "QK_ERR_TYPE"}
 MAX_BATCH = 8
 DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}   # qk_dtype
+FORMATS = {"q8_0": 0, "q4_k": 1, "q6_k": 2}                         # qk_format
+SCORES = {"softmax": 0, "sigmoid": 1}                               # qk_score
 
 EXPORTS = ["qmatvec_q8_0", "qmatvec_q4_k", "qmatvec_q6_k", "qmatvec_swiglu_q8_0", "qmatvec_swiglu_q4_k",
            "qmatvec_swiglu_q6_k", "qmatvec_experts_q8_0", "qmatvec_experts_q4_k", "qmatvec_experts_q6_k",
@@ -34,13 +37,29 @@ EXPORTS = ["qmatvec_q8_0", "qmatvec_q4_k", "qmatvec_q6_k", "qmatvec_swiglu_q8_0"
            "qgemm_q4_k_noalloc", "qk_row_bytes_q8_0", "qk_row_bytes_q4_k",
            "qk_status_string", "qk_device_error", "qk_set_wait_limit_ns", "qk_set_programmatic_launch",
            "qk_set_strict_blocks", "qk_version", "qk_rope_table", "qk_norm_rope", "qk_kv_append_q4",
-           "qk_kv_read_q4", "qk_attn_q4", "qk_attn_q4_workspace_bytes"]
+           "qk_kv_read_q4", "qk_attn_q4", "qk_attn_q4_workspace_bytes", "qk_moe_route", "qk_moe_ffn",
+           "qk_moe_ffn_workspace_bytes", "qk_lora"]
 
 
 class _KVCacheQ4(ctypes.Structure):
     """qk_kv_cache_q4 of include/qk.h."""
     _fields_ = [("pages", ctypes.c_void_p), ("n_pages", ctypes.c_int64), ("n_kv_heads", ctypes.c_int),
                 ("head_dim", ctypes.c_int), ("page_tokens", ctypes.c_int)]
+
+
+class ExpertWeights(NamedTuple):
+    """The experts' rows of one projection: expert e's row r is row row_offset + e * expert_rows + r of the block bytes
+    `w` (uint8, device; expert_rows 0: the call's row count)."""
+    fmt: str
+    w: torch.Tensor
+    row_offset: int = 0
+    expert_rows: int = 0
+
+
+class _ExpertWeights(ctypes.Structure):
+    """qk_expert_weights of include/qk.h."""
+    _fields_ = [("w", ctypes.c_void_p), ("format", ctypes.c_int), ("row_offset", ctypes.c_int64),
+                ("expert_rows", ctypes.c_int64)]
 
 
 class QKError(RuntimeError):
@@ -112,7 +131,13 @@ def load(path: str | None = None):
         lib.qk_kv_read_q4.argtypes = [C, P, I64, P, I64, P, I64, I, P]
         lib.qk_attn_q4.argtypes = [C, P, I64, I, I, P, I64, I64, P, P, I64, I64, I64, I64, F, I64, P, I64, I, P,
                                    ctypes.c_size_t, P]
-        for name in ("qk_rope_table", "qk_norm_rope", "qk_kv_append_q4", "qk_kv_read_q4", "qk_attn_q4"):
+        lib.qk_moe_route.argtypes = [P, I64, I, I64, I, I, I, P, I, I, I, I, F, P, P, P]
+        lib.qk_moe_ffn.argtypes = [P, P, P, I64, I64, I64, I64, P, I64, I, I64, P, P, I, P, I64, I, P, ctypes.c_size_t, P]
+        lib.qk_moe_ffn_workspace_bytes.argtypes = [I64, I, I64, I64, I64, I64]
+        lib.qk_moe_ffn_workspace_bytes.restype = ctypes.c_size_t
+        lib.qk_lora.argtypes = [P, I64, I, I64, I64, P, P, I, I64, I, I64, P, P, P, I64, P, I64, I, P]
+        for name in ("qk_rope_table", "qk_norm_rope", "qk_kv_append_q4", "qk_kv_read_q4", "qk_attn_q4", "qk_moe_route",
+                     "qk_moe_ffn", "qk_lora"):
             getattr(lib, name).restype = I
         lib.qk_attn_q4_workspace_bytes.argtypes = [I64, I, I, I, I64, I64]
         lib.qk_attn_q4_workspace_bytes.restype = ctypes.c_size_t
@@ -501,6 +526,54 @@ def attn_q4(cache: torch.Tensor, q: torch.Tensor, page_table: torch.Tensor, lens
     return _result((_ext or _binding()).attn_q4(
         cache, q, page_table, lens, q_start, max_q, max_len, scale, window, out, workspace,
         None if stream is None else _stream(stream)), "qk_attn_q4")
+
+
+# ---------------------------------------------------------------- experts and adapters
+
+def moe_route(logits: torch.Tensor, top_k: int, score: str = "softmax", bias: torch.Tensor | None = None,
+              n_groups: int = 1, top_groups: int | None = None, group_top: int = 1, renorm: bool = True,
+              scale: float = 1.0, ids: torch.Tensor | None = None, weights: torch.Tensor | None = None,
+              stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """The top_k experts of each row of logits [T][experts] and their weights: ids int32 and weights fp32 [T][top_k].
+    Scores are the logits' softmax or sigmoid; the choice goes by score + bias inside the top_groups (None: all) best
+    of n_groups groups, and the weights are the scores, over their sum with renorm, times scale (see include/qk.h)."""
+    if score not in SCORES:
+        raise ValueError(f"score must be softmax or sigmoid, not {score}")
+    return _result((_ext or _binding()).moe_route(
+        logits, top_k, SCORES[score], bias, n_groups, n_groups if top_groups is None else top_groups, group_top, renorm,
+        scale, ids, weights, None if stream is None else _stream(stream)), "qk_moe_route")
+
+
+def moe_ffn_workspace(T: int, top_k: int, n_experts: int, K: int, F: int, N: int = 0, device=None) -> torch.Tensor:
+    """Scratch for moe_ffn calls of up to these sizes (one for each stream that calls); N 0: K."""
+    n = load().qk_moe_ffn_workspace_bytes(T, top_k, n_experts, K, F, N or K)
+    return torch.empty(max(256, n), dtype=torch.uint8, device=device or "cuda")
+
+
+def _format(w: ExpertWeights, name: str) -> int:
+    if w.fmt not in FORMATS:
+        raise ValueError(f"{name}'s format must be q8_0, q4_k or q6_k, not {w.fmt}")
+    return FORMATS[w.fmt]
+
+
+def moe_ffn(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, gate: ExpertWeights, up: ExpertWeights,
+            down: ExpertWeights, n_experts: int, F: int, N: int = 0, y: torch.Tensor | None = None,
+            workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """y[t] = sum_j weights[t][j] * down_e (silu(gate_e x[t]) * (up_e x[t])), e = ids[t][j] (int32; negative: nothing),
+    for rows x [T][K] and block bytes gate, up [experts][F][K] and down [experts][N][F] (N 0: K).  `workspace`
+    (moe_ffn_workspace) is allocated here through torch when not given."""
+    return _result((_ext or _binding()).moe_ffn(
+        x, ids, weights, _format(gate, "gate"), gate.w, gate.row_offset, gate.expert_rows, _format(up, "up"), up.w,
+        up.row_offset, up.expert_rows, _format(down, "down"), down.w, down.row_offset, down.expert_rows, n_experts, F, N,
+        y, workspace, None if stream is None else _stream(stream)), "qk_moe_ffn")
+
+
+def lora(x: torch.Tensor, y: torch.Tensor, A: torch.Tensor, B: torch.Tensor, ids: torch.Tensor,
+         scales: torch.Tensor | None = None, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """y[t] + scales[a] * B[a] (A[a] x[t]), a = ids[t] (int32; negative: y[t]), for rows x [T][K], y [T][N] and adapters
+    A [adapters][rank][K], B [adapters][N][rank] of one type.  out may be y."""
+    return _result((_ext or _binding()).lora(x, y, A, B, ids, scales, out, None if stream is None else _stream(stream)),
+                   "qk_lora")
 
 
 def debug_gemm_skip_chunk(chunk: int) -> int:
