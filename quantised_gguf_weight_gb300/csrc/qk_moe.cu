@@ -2,6 +2,7 @@
 // argument checks, and the kernels around the products (the plan that groups
 // assignments by expert, the operands' layout, the weighted sum).
 #include <algorithm>
+#include <atomic>
 
 #include "qk_kv4.cuh"
 #include "qk_moe.cuh"
@@ -11,10 +12,14 @@ using namespace moe;
 namespace {
 
 constexpr int kPlanThreads = 1024;
+// Tokens an expert from which the tile form takes them (qk_moe_tile.cuh).
+constexpr int kTileFrom = 48;
+std::atomic<int> g_skip_chunk{-1};
 
 struct PlanArgs {
     const int32_t *ids;
     int n, experts, per_warp;      // per_warp: ids of a warp, a multiple of 32
+    int tile_from, tile_tokens;    // tokens of an expert that goes by tile sets, and of a set at most
     Plan plan;
     int *err;
 };
@@ -75,15 +80,23 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a)
         }
     int places, octets, sets;
     const int first_place = scan_before(n, warp_sums, places);
-    const int octet0 = scan_before((n + 7) / 8, warp_sums, octets);
-    const int set0 = scan_before((n + 8 * kSetOctets - 1) / (8 * kSetOctets), warp_sums, sets);
+    const bool tiled = n >= a.tile_from;
+    // tile sets as even as 16 tokens allow, none of them empty
+    const int parts = (n + a.tile_tokens - 1) / a.tile_tokens;
+    const int per = tiled ? ((n + parts - 1) / parts + 15) / 16 * 16 : 1;
+    const int rows_n = tiled ? 0 : n, tile_n = tiled ? (n + per - 1) / per : 0;
+    const int octet0 = scan_before((rows_n + 7) / 8, warp_sums, octets);
+    const int set0 = scan_before((rows_n + 8 * kSetOctets - 1) / (8 * kSetOctets), warp_sums, sets);
+    int tile_sets;
+    const int tile0 = scan_before(tile_n, warp_sums, tile_sets);
     __shared__ int place_of[kMaxExperts], octet_of[kMaxExperts];
     if (e < a.experts) {
-        place_of[e] = first_place, octet_of[e] = octet0;
-        for (int i = 0, s = set0; i < n; i += 8 * kSetOctets, ++s)
+        place_of[e] = first_place, octet_of[e] = tiled ? -1 : octet0;
+        for (int i = 0, s = set0; i < rows_n; i += 8 * kSetOctets, ++s)
             a.plan.sets[s] = {e, first_place + i, min(8 * kSetOctets, n - i), octet0 + i / 8};
+        for (int i = 0; i < tile_n; ++i) a.plan.tile_sets[tile0 + i] = {e, first_place + i * per, min(per, n - i * per), 0};
     }
-    if (e == 0) a.plan.head[0] = sets, a.plan.head[1] = octets, a.plan.head[2] = places;
+    if (e == 0) a.plan.head[0] = sets, a.plan.head[1] = octets, a.plan.head[2] = places, a.plan.head[3] = tile_sets;
     __syncthreads();
     for (int base = first; base < last; base += 32) {
         const int i = base + lane;
@@ -97,7 +110,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a)
             if (lane == __ffs(same) - 1) mine[id] = before + __popc(same);
             const int p = place_of[id] + k;
             a.plan.assignment[p] = i, a.plan.place[i] = p;
-            a.plan.column[p] = octet_of[id] * 8 + k;
+            a.plan.column[p] = octet_of[id] < 0 ? -1 : octet_of[id] * 8 + k;
         } else if (i < last) {
             a.plan.place[i] = id < 0 ? -1 : -2;
         }
@@ -169,6 +182,19 @@ __global__ void __launch_bounds__(kPackThreads) pack_kernel(const PackArgs a, bo
     if (threadIdx.x == 0) a.scale[p] = __uint_as_float(static_cast<uint32_t>(127 - 141 + ex) << 23);
     const int64_t unit = octet_unit_bytes(a.fmt, a.pieces);
     const int column = a.plan.column[p];
+    if (column < 0) {
+        // a tile set's row, in the order in which its weights are taken apart: (0, 2, 1, 3) of every four
+        for (int k = threadIdx.x * 4; k < a.tile_cols; k += kPackThreads * 4) {
+            float4 v = four(a.x, row, k, a.cols, a.type, vec);
+            v.x *= up, v.y *= up, v.z *= up, v.w *= up;
+            uint2 h, l;
+            pieces_of(v, h, l);
+            __half *to = a.tile_out + static_cast<int64_t>(p) * a.tile_cols + k;
+            *reinterpret_cast<uint2 *>(to) = h;
+            if (a.pieces == 2) *reinterpret_cast<uint2 *>(to + a.tile_lo) = l;
+        }
+        return;
+    }
     uint8_t *out = a.out + (column >> 3) * unit * a.units;
     const int col = column & 7;
     for (int j = threadIdx.x; j < a.units * 32; j += kPackThreads) {
@@ -257,10 +283,12 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(const SumArgs a)
 // ---------------------------------------------------------------- the call
 
 struct Layout {
-    int64_t A, octets, sets;
-    int pieces;
-    int64_t head, assignment, place, column, set, x_scale, h_scale, x, h, h_ops, parts, bytes;
+    int64_t A, octets, sets, tile_sets;
+    int pieces, w_pieces, tile_tokens;
+    bool tiled;               // some expert may have enough tokens for the tile form
+    int64_t head, assignment, place, column, set, tile_set, x_scale, h_scale, x, x_tile, h, h_ops, h_tile, parts, bytes;
 };
+int64_t tile_cols(int64_t cols) { return (cols + 63) / 64 * 64; }
 
 int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
 
@@ -271,9 +299,14 @@ Layout layout_of(int64_t T, int top_k, int64_t E, int64_t K, int64_t F, int64_t 
     Layout l{};
     l.A = T * top_k;
     l.pieces = x_type == QK_F32 || y_type == QK_F32 ? 2 : 1;
+    l.w_pieces = x_type == QK_BF16 && y_type == QK_BF16 ? 1 : 2;
+    l.tile_tokens = l.w_pieces == 1 ? 192 : 128;
+    l.tiled = l.A >= kTileFrom;
     const int64_t used = std::min(l.A, E);
-    l.octets = used + l.A / 8;
+    // experts of fewer than kTileFrom tokens
+    l.octets = std::min(used + l.A / 8, E * ((kTileFrom + 6) / 8));
     l.sets = used + l.A / (8 * kSetOctets);
+    l.tile_sets = l.tiled ? l.A / 64 + std::min(E, l.A / kTileFrom) : 0;
     int64_t at = 0;
     const auto take = [&](int64_t n) {
         const int64_t was = at;
@@ -285,9 +318,11 @@ Layout layout_of(int64_t T, int top_k, int64_t E, int64_t K, int64_t F, int64_t 
         return (l.octets + kSetOctets - 1) * ((cols + kUnit - 1) / kUnit) * octet_unit_bytes(fmt, l.pieces);
     };
     l.head = take(64), l.assignment = take(4 * l.A), l.place = take(4 * l.A), l.column = take(4 * l.A);
-    l.set = take(l.sets * sizeof(ExpertSet));
+    l.set = take(l.sets * sizeof(ExpertSet)), l.tile_set = take(l.tile_sets * sizeof(ExpertSet));
+    const auto rows = [&](int64_t cols) { return l.tiled ? 2 * l.pieces * l.A * tile_cols(cols) : 0; };
     l.x_scale = take(4 * l.A), l.h_scale = take(4 * l.A);
-    l.x = take(operands(gate_fmt, K)), l.h = take(4 * l.A * F), l.h_ops = take(operands(down_fmt, F));
+    l.x = take(operands(gate_fmt, K)), l.x_tile = take(rows(K));
+    l.h = take(4 * l.A * F), l.h_ops = take(operands(down_fmt, F)), l.h_tile = take(rows(F));
     l.parts = take(4 * l.A * N);
     l.bytes = at;
     return l;
@@ -334,6 +369,11 @@ using namespace qk;
 
 extern "C" {
 
+// Test hook, not part of the public header: the first thread blocks of later
+// many-token launches never load chunk number `chunk` of the tokens (-1: off),
+// so that a bounded wait runs out and the launch records QK_ERR_TIMEOUT.
+int qk_debug_moe_skip_chunk(int chunk) { return g_skip_chunk.exchange(chunk); }
+
 size_t qk_moe_ffn_workspace_bytes(int64_t T, int top_k, int64_t n_experts, int64_t K, int64_t F, int64_t N)
 {
     if (T <= 0 || top_k <= 0 || n_experts <= 0 || K <= 0 || F <= 0 || N <= 0) return 0;
@@ -377,15 +417,17 @@ int qk_moe_ffn(const qk_expert_weights *gate, const qk_expert_weights *up, const
     pa.per_warp = static_cast<int>((l.A + 32 * kWarps - 1) / (32 * kWarps) * 32);
     pa.plan = {reinterpret_cast<int *>(ws + l.head), reinterpret_cast<int *>(ws + l.assignment),
                reinterpret_cast<int *>(ws + l.place), reinterpret_cast<int *>(ws + l.column),
-               reinterpret_cast<ExpertSet *>(ws + l.set)};
+               reinterpret_cast<ExpertSet *>(ws + l.set), reinterpret_cast<ExpertSet *>(ws + l.tile_set)};
+    pa.tile_from = kTileFrom, pa.tile_tokens = l.tile_tokens;
     const size_t counts = sizeof(int) * kWarps * pa.experts;
     cudaError_t e = cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(sizeof(int) * kWarps * kMaxExperts));
     if (e == cudaSuccess) e = launch_chained(plan_kernel, dim3(1), kPlanThreads, counts, s, library_programmatic(), pa);
     if (e != cudaSuccess) return QK_ERR_CUDA;
 
-    const auto pack = [&](const void *rows, int64_t ld, int type, int per_row, int64_t cols, int fmt, int64_t to, int64_t scale) {
+    const auto pack = [&](const void *rows, int64_t ld, int type, int per_row, int64_t cols, int fmt, int64_t to, int64_t tile_to, int64_t scale) {
         PackArgs k{};
+        k.tile_out = reinterpret_cast<__half *>(ws + tile_to), k.tile_cols = static_cast<int>(tile_cols(cols)), k.tile_lo = l.A * k.tile_cols;
         k.plan = pa.plan, k.x = rows, k.ld = ld, k.type = type, k.top_k = per_row;
         k.cols = static_cast<int>(cols), k.units = static_cast<int>((cols + kUnit - 1) / kUnit);
         k.pieces = l.pieces, k.fmt = fmt;
@@ -400,7 +442,33 @@ int qk_moe_ffn(const qk_expert_weights *gate, const qk_expert_weights *up, const
         return cudaLaunchKernelEx(&cfg, pack_kernel, k, vec);
     };
     const auto products = [&](const Weights &a, const Weights &b, int fmt, int64_t cols, int64_t rows, bool paired,
-                              int64_t ops, int64_t scale, int64_t to) {
+                              int64_t ops, int64_t tile_ops, int64_t scale, int64_t to) {
+        if (l.tiled) {
+            // rows [A][tile_cols] of fp16 as boxes of 64 columns and kBoxRows rows
+            CUtensorMap map[2];
+            const int64_t wide = tile_cols(cols);
+            for (int i = 0; i < l.pieces; ++i) {
+                const cuuint64_t dims[2] = {static_cast<cuuint64_t>(wide), static_cast<cuuint64_t>(l.A)};
+                const cuuint64_t strides[1] = {static_cast<cuuint64_t>(2 * wide)};
+                const cuuint32_t box[2] = {64, kTileBoxRows}, one[2] = {1, 1};
+                const gemm::EncodeTiledFn enc = gemm::encode_fn();
+                if (!enc || enc(&map[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, ws + tile_ops + i * 2 * l.A * wide, dims, strides, box, one,
+                                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+                    return cudaErrorInvalidValue;
+            }
+            if (l.pieces == 1) map[1] = map[0];
+            TileArgs t{};
+            t.plan = pa.plan, t.a = a, t.b = b, t.fmt = fmt, t.cols = static_cast<int>(cols), t.chunks = static_cast<int>(wide / 64);
+            t.pieces = l.pieces, t.w_pieces = l.w_pieces, t.rows = static_cast<int>(rows);
+            t.tiles = static_cast<int>(paired ? (rows + 63) / 64 : (rows + 127) / 128);
+            t.scale = reinterpret_cast<const float *>(ws + scale), t.out = reinterpret_cast<float *>(ws + to);
+            t.skip_chunk = g_skip_chunk.load(), t.wait_ns = library_wait_limit_ns(), t.err = err;
+            const cudaError_t e = fmt == kFmtQ4K ? tile_launch_q4k(map[0], map[1], t, paired, sms, s)
+                                : fmt == kFmtQ80 ? tile_launch_q80(map[0], map[1], t, paired, sms, s)
+                                                 : tile_launch_q6k(map[0], map[1], t, paired, sms, s);
+            if (e != cudaSuccess) return e;
+        }
         RowsArgs r{};
         r.plan = pa.plan, r.a = a, r.b = b, r.fmt = fmt;
         r.cols = static_cast<int>(cols), r.units = static_cast<int>((cols + kUnit - 1) / kUnit), r.pieces = l.pieces;
@@ -410,10 +478,10 @@ int qk_moe_ffn(const qk_expert_weights *gate, const qk_expert_weights *up, const
         r.out = reinterpret_cast<float *>(ws + to);
         return rows_launch(r, paired, sms, s);
     };
-    e = pack(x, ldx, x_type, top_k, K, gate->format, l.x, l.x_scale);
-    if (e == cudaSuccess) e = products(wg, wu, gate->format, K, F, true, l.x, l.x_scale, l.h);
-    if (e == cudaSuccess) e = pack(ws + l.h, F, QK_F32, 0, F, down->format, l.h_ops, l.h_scale);
-    if (e == cudaSuccess) e = products(wd, wd, down->format, F, N, false, l.h_ops, l.h_scale, l.parts);
+    e = pack(x, ldx, x_type, top_k, K, gate->format, l.x, l.x_tile, l.x_scale);
+    if (e == cudaSuccess) e = products(wg, wu, gate->format, K, F, true, l.x, l.x_tile, l.x_scale, l.h);
+    if (e == cudaSuccess) e = pack(ws + l.h, F, QK_F32, 0, F, down->format, l.h_ops, l.h_tile, l.h_scale);
+    if (e == cudaSuccess) e = products(wd, wd, down->format, F, N, false, l.h_ops, l.h_tile, l.h_scale, l.parts);
     if (e != cudaSuccess) return QK_ERR_CUDA;
     SumArgs u{};
     u.plan = pa.plan, u.parts = reinterpret_cast<const float *>(ws + l.parts), u.weights = weights;

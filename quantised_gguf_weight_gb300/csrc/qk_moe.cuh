@@ -26,6 +26,7 @@ namespace moe {
 
 constexpr int kMaxExperts = 1024;
 constexpr int kSetOctets = 4;
+constexpr int kTileBoxRows = 32;                  // rows of a TMA box of a tile set's operands
 constexpr int kRowWarps = 8;                      // warps of a thread block of the few-token products
 constexpr int kUnit = 256;                        // columns of a unit of the products' loops
 constexpr int kPieceBytes = 8 * 32 * 16;          // an octet's unit, one piece: 8 steps of 16 bytes a lane
@@ -36,11 +37,12 @@ struct ExpertSet {
 };
 
 struct Plan {
-    int *head;                // [0] sets, [1] octets, [2] live places
+    int *head;                // [0] sets, [1] octets, [2] live places, [3] tile sets
     int *assignment;          // [A] assignment at a place
     int *place;               // [A] place of an assignment; -1 none, -2 an id out of range
-    int *column;              // [A] octet * 8 + column of a place
+    int *column;              // [A] octet * 8 + column of a place; -1: of a tile set
     ExpertSet *sets;
+    ExpertSet *tile_sets;     // (octet is not used)
 };
 
 // Expert e's row r is row `first_row + e * expert_rows + r` of w.
@@ -57,6 +59,9 @@ struct PackArgs {
     int type, top_k;          // row of a place: x[assignment / top_k], or x[place] where top_k == 0
     int cols, units, pieces, fmt;
     uint8_t *out;
+    __half *tile_out;         // rows of the tile sets, hi pieces [place][tile_cols]; lo ones tile_lo further
+    int64_t tile_lo;
+    int tile_cols;
     float *scale;             // [place] 2^-e
 };
 
@@ -69,6 +74,18 @@ struct RowsArgs {
     const uint8_t *x;         // operands, octet after octet
     const float *scale;
     float *out;               // [place][rows]
+};
+
+struct TileArgs {
+    Plan plan;
+    Weights a, b;             // as above
+    int fmt, cols, chunks, pieces, w_pieces;
+    int rows, tiles;          // output columns and 128-row tiles (64 + 64 where paired)
+    const float *scale;
+    float *out;
+    int skip_chunk;           // test hook: the first cluster never loads this chunk of its (-1: none)
+    uint64_t wait_ns;
+    int *err;
 };
 
 __host__ __device__ constexpr int64_t octet_unit_bytes(int fmt, int pieces)
@@ -84,6 +101,9 @@ __host__ __device__ inline int64_t row_bytes_of(int fmt, int64_t K)
 cudaError_t rows_launch_q4k(const RowsArgs &a, bool paired, int sms, cudaStream_t st);
 cudaError_t rows_launch_q80(const RowsArgs &a, bool paired, int sms, cudaStream_t st);
 cudaError_t rows_launch_q6k(const RowsArgs &a, bool paired, int sms, cudaStream_t st);
+cudaError_t tile_launch_q4k(const CUtensorMap &hi, const CUtensorMap &lo, const TileArgs &a, bool paired, int sms, cudaStream_t st);
+cudaError_t tile_launch_q80(const CUtensorMap &hi, const CUtensorMap &lo, const TileArgs &a, bool paired, int sms, cudaStream_t st);
+cudaError_t tile_launch_q6k(const CUtensorMap &hi, const CUtensorMap &lo, const TileArgs &a, bool paired, int sms, cudaStream_t st);
 
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }

@@ -143,6 +143,8 @@ def load(path: str | None = None):
         lib.qk_attn_q4_workspace_bytes.restype = ctypes.c_size_t
         lib.qk_debug_attn_skip_block.argtypes = [I]
         lib.qk_debug_attn_skip_block.restype = I
+        lib.qk_debug_moe_skip_chunk.argtypes = [I]
+        lib.qk_debug_moe_skip_chunk.restype = I
         lib.qk_debug_skip_item.argtypes = [I64]
         lib.qk_debug_skip_item.restype = I64
         lib.qk_debug_gemv_plan.argtypes = [I, I64, I64, I, ctypes.POINTER(ctypes.c_int64), I]
@@ -589,6 +591,11 @@ def device_error(stream=None) -> int:
 def debug_attn_skip_block(block: int) -> int:
     """Test hook: thread block 0 of later attention launches never copies its 16-token block `block` (-1: off)."""
     return int(load().qk_debug_attn_skip_block(int(block)))
+
+
+def debug_moe_skip_chunk(chunk: int) -> int:
+    """Test hook: the first thread blocks of later many-token expert products never load their chunk `chunk` (-1: off)."""
+    return int(load().qk_debug_moe_skip_chunk(int(chunk)))
 
 
 def set_wait_limit_ns(ns: int) -> int:
