@@ -288,7 +288,7 @@ struct Layout {
     bool tiled;               // some expert may have enough tokens for the tile form
     int64_t head, assignment, place, column, set, tile_set, x_scale, h_scale, x, x_tile, h, h_ops, h_tile, parts, bytes;
 };
-int64_t tile_cols(int64_t cols) { return (cols + 63) / 64 * 64; }
+int64_t tile_cols(int64_t cols) { return (cols + 127) / 128 * 128; }
 
 int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
 
@@ -300,11 +300,12 @@ Layout layout_of(int64_t T, int top_k, int64_t E, int64_t K, int64_t F, int64_t 
     l.A = T * top_k;
     l.pieces = x_type == QK_F32 || y_type == QK_F32 ? 2 : 1;
     l.w_pieces = x_type == QK_BF16 && y_type == QK_BF16 ? 1 : 2;
-    l.tile_tokens = l.w_pieces == 1 ? 192 : 128;
-    l.tiled = l.A >= kTileFrom;
+    l.tile_tokens = 128;
+    // (an id may repeat within a token: such an expert goes by the few-token form, however many it has)
+    l.tiled = T >= kTileFrom;
     const int64_t used = std::min(l.A, E);
     // experts of fewer than kTileFrom tokens
-    l.octets = std::min(used + l.A / 8, E * ((kTileFrom + 6) / 8));
+    l.octets = l.tiled ? std::min(used + l.A / 8, E * ((kTileFrom + 6) / 8)) : used + l.A / 8;
     l.sets = used + l.A / (8 * kSetOctets);
     l.tile_sets = l.tiled ? l.A / 64 + std::min(E, l.A / kTileFrom) : 0;
     int64_t at = 0;
@@ -418,7 +419,7 @@ int qk_moe_ffn(const qk_expert_weights *gate, const qk_expert_weights *up, const
     pa.plan = {reinterpret_cast<int *>(ws + l.head), reinterpret_cast<int *>(ws + l.assignment),
                reinterpret_cast<int *>(ws + l.place), reinterpret_cast<int *>(ws + l.column),
                reinterpret_cast<ExpertSet *>(ws + l.set), reinterpret_cast<ExpertSet *>(ws + l.tile_set)};
-    pa.tile_from = kTileFrom, pa.tile_tokens = l.tile_tokens;
+    pa.tile_from = l.tiled ? kTileFrom : INT32_MAX, pa.tile_tokens = l.tile_tokens;
     const size_t counts = sizeof(int) * kWarps * pa.experts;
     cudaError_t e = cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(sizeof(int) * kWarps * kMaxExperts));
@@ -459,7 +460,7 @@ int qk_moe_ffn(const qk_expert_weights *gate, const qk_expert_weights *up, const
             }
             if (l.pieces == 1) map[1] = map[0];
             TileArgs t{};
-            t.plan = pa.plan, t.a = a, t.b = b, t.fmt = fmt, t.cols = static_cast<int>(cols), t.chunks = static_cast<int>(wide / 64);
+            t.plan = pa.plan, t.a = a, t.b = b, t.fmt = fmt, t.cols = static_cast<int>(cols), t.chunks = static_cast<int>(wide / (l.w_pieces == 1 ? 128 : 64));
             t.pieces = l.pieces, t.w_pieces = l.w_pieces, t.rows = static_cast<int>(rows);
             t.tiles = static_cast<int>(paired ? (rows + 63) / 64 : (rows + 127) / 128);
             t.scale = reinterpret_cast<const float *>(ws + scale), t.out = reinterpret_cast<float *>(ws + to);

@@ -1,6 +1,5 @@
 // qk_moe_tile.cuh -- the experts' products for many tokens an expert: tiles of
-// 128 weight rows x up to 192 (fp32 accuracy: 128) tokens on the tcgen05 tensor
-// cores.
+// 128 weight rows x up to 128 tokens on the tcgen05 tensor cores.
 //
 // A thread block keeps going over its items.  Its warps have roles: two groups
 // of four take the weights apart, a thread a row, and leave them as the A
@@ -16,9 +15,10 @@
 // such pieces, and fp32 activations too (qk_moe.cuh); the product of the two
 // low pieces is left out.
 //
-// Why A is in tensor memory: products of 128 x 192 x 16 take 96 cycles, in which
-// shared memory moves 12 KB; the tokens' operand alone is 6 KB written and 6 KB
-// read.  From shared memory (measured) the same product takes 145 cycles.
+// Why A is in tensor memory: a product of 128 x 128 x 16 takes 64 cycles, in which
+// shared memory moves 8 KB; the tokens' operand alone is 4 KB written and 4 KB
+// read.  From shared memory (measured) a product of 192 tokens takes 145 cycles
+// where one from tensor memory takes 100.
 #pragma once
 
 #include "qk_moe.cuh"
@@ -28,31 +28,49 @@ namespace qk {
 namespace moe {
 
 constexpr int kDeqWarp = 4, kDeqGroups = 2, kEpiWarp = 12;   // first warps of the roles
-constexpr int kFlush = 4;                                    // chunks whose products one accumulator takes, with fp32 accuracy
+constexpr int kFlush = 4;                                    // stages whose products one accumulator takes, with fp32 accuracy
 // Output warps: with fp32 accuracy two threads share a row, whose sums they keep.
 __host__ __device__ constexpr int tile_epi_warps(int PB) { return PB == 2 ? 8 : 4; }
 __host__ __device__ constexpr int tile_threads(int PB) { return 32 * (kEpiWarp + tile_epi_warps(PB)); }
-constexpr int kAStages = 4;
-constexpr int kChunk = 64;                                   // columns of a chunk
-
-__host__ __device__ constexpr int tile_b_bytes(int PA, int PB) { return (PA == 1 ? 192 : 128) * 128 * PB; }
-__host__ __device__ constexpr int tile_stages(int PA, int PB) { return PA == 1 ? 8 : PB == 1 ? 8 : 6; }
-__host__ __device__ constexpr int tile_smem(int PA, int PB) { return tile_stages(PA, PB) * tile_b_bytes(PA, PB) + 1024; }
+constexpr int kStages = 4;                                   // of both operands
+constexpr int kMaxN = 128;                                   // tokens of a set
+// Columns of a stage: eight products for each (a wait costs the issuing warp as much as three of them).
+__host__ __device__ constexpr int tile_cols_of_stage(int PA) { return PA == 1 ? 128 : 64; }
+__host__ __device__ constexpr int tile_b_bytes(int PA, int PB) { return kMaxN * 2 * tile_cols_of_stage(PA) * PB; }
+__host__ __device__ constexpr int tile_smem(int PA, int PB) { return kStages * tile_b_bytes(PA, PB) + 1024; }
 
 struct TileShared {
-    uint64_t full_b[8], empty_b[8], full_a[kAStages], empty_a[kAStages], acc_full[2], acc_empty[2], rs_full[2], rs_empty[2];
+    uint64_t full[kStages], empty_b[kStages], empty_a[kStages], acc_full[2], acc_empty[2], rs_full[2], rs_empty[2];
     float row_scale[2][128];                                 // 2^s of the rows
     uint32_t tmem;
     int abort;
 };
 
+// A bounded wait; one that runs out ends every other of the block.
 __device__ __forceinline__ bool tile_wait(uint32_t bar, uint32_t parity, const TileArgs &a, volatile int *abort)
 {
-    if (*abort) return false;
-    if (mbar_wait(bar, parity, a.wait_ns)) return true;
-    *abort = 1;
-    record_error(a.err, kErrTimeout);
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t deadline = globaltimer_ns() + a.wait_ns;
+    for (uint32_t i = 1; !*abort; ++i) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((i & 31u) == 0 && globaltimer_ns() > deadline) {
+            *abort = 1;
+            record_error(a.err, kErrTimeout);
+        }
+    }
     return false;
+}
+__device__ __forceinline__ bool tile_wait_warp(uint32_t bar, uint32_t parity, const TileArgs &a, volatile int *abort)
+{
+    return __all_sync(~0u, tile_wait(bar, parity, a, abort));
+}
+
+// One lane of the (converged) warp is elected.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
 }
 
 __device__ __forceinline__ void tma_load_2d_both(uint32_t dst, const CUtensorMap *m, int32_t x, int32_t y, uint32_t bar,
@@ -129,14 +147,14 @@ __device__ __forceinline__ float row_scale_of(const uint8_t *row, int cols)
     return __uint_as_float(static_cast<uint32_t>(127 + 141 - ex) << 23);
 }
 
-// A chunk's bytes of a row, in registers.
-template <int FMT>
+// A stage's bytes of a row, in registers.
+template <int FMT, int KC>
 struct Raw {
-    static constexpr int kWords = FMT == kFmtQ4K ? 12 : FMT == kFmtQ80 ? 18 : 27;
+    static constexpr int kWords = FMT == kFmtQ4K ? KC / 8 + 4 : FMT == kFmtQ80 ? KC / 64 * 17 + 1 : 27;
     uint32_t w[kWords];
 };
 
-// The 32-bit words that hold `words` words from a 2-byte aligned place on (one more where it is off).
+// The 32-bit words that hold N words from a 2-byte aligned place on (one more where it is off).
 template <int N>
 __device__ __forceinline__ void load_words2(uint32_t *w, const uint8_t *p)
 {
@@ -146,32 +164,34 @@ __device__ __forceinline__ void load_words2(uint32_t *w, const uint8_t *p)
     w[N] = reinterpret_cast<uintptr_t>(p) & 2 ? __ldg(q + N) : 0u;
 }
 
-template <int FMT>
-__device__ __forceinline__ void load_raw(Raw<FMT> &r, const uint8_t *row, int c, int cols)
+template <int FMT, int KC>
+__device__ __forceinline__ void load_raw(Raw<FMT, KC> &r, const uint8_t *row, int c, int cols)
 {
     if constexpr (FMT == kFmtQ4K) {
-        const uint8_t *blk = row + 144 * (c >> 2);
-        const uint4 h = __ldg(reinterpret_cast<const uint4 *>(blk));
-        const uint4 *q = reinterpret_cast<const uint4 *>(blk + 16 + 32 * (c & 3));
-        const uint4 a = __ldg(q), b = __ldg(q + 1);
-        r.w[0] = a.x, r.w[1] = a.y, r.w[2] = a.z, r.w[3] = a.w, r.w[4] = b.x, r.w[5] = b.y, r.w[6] = b.z, r.w[7] = b.w;
-        r.w[8] = h.x, r.w[9] = h.y, r.w[10] = h.z, r.w[11] = h.w;
-    } else if constexpr (FMT == kFmtQ80) {
-        // two blocks of 34 bytes; the second may be past the row's end
-        const uint8_t *p = row + 68 * c;
-        if (2 * c + 1 < (cols + 31) / 32) {
-            load_words2<17>(r.w, p);
-        } else {
-            const uint32_t *q = reinterpret_cast<const uint32_t *>(reinterpret_cast<uintptr_t>(p) & ~uintptr_t(3));
+        const int pair = c * (KC / 64);
+        const uint8_t *blk = row + 144 * (pair >> 2);
+        const uint4 *q = reinterpret_cast<const uint4 *>(blk + 16 + 32 * (pair & 3));
 #pragma unroll
-            for (int i = 0; i < 18; ++i) r.w[i] = i < 9 ? __ldg(q + i) : 0u;
+        for (int i = 0; i < KC / 32; ++i) {
+            const uint4 v = __ldg(q + i);
+            r.w[4 * i] = v.x, r.w[4 * i + 1] = v.y, r.w[4 * i + 2] = v.z, r.w[4 * i + 3] = v.w;
         }
+        const uint4 h = __ldg(reinterpret_cast<const uint4 *>(blk));
+        r.w[KC / 8] = h.x, r.w[KC / 8 + 1] = h.y, r.w[KC / 8 + 2] = h.z, r.w[KC / 8 + 3] = h.w;
+    } else if constexpr (FMT == kFmtQ80) {
+        // the words that the row's own blocks have bytes in
+        const int first = c * (KC / 32), blocks = min(KC / 32, (cols + 31) / 32 - first);
+        const uint8_t *p = row + 34 * static_cast<int64_t>(first);
+        const int off = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 2);
+        const uint32_t *q = reinterpret_cast<const uint32_t *>(p - off);
+#pragma unroll
+        for (int i = 0; i < Raw<FMT, KC>::kWords; ++i) r.w[i] = 4 * i < 34 * blocks + off ? __ldg(q + i) : 0u;
     } else {
-        const int hf = (c >> 1) & 1;
-        const uint8_t *blk = row + 210 * (c >> 2);
-        load_words2<8>(r.w, blk + 64 * hf);                          // low nibbles, 0..31
-        load_words2<8>(r.w + 9, blk + 64 * hf + 32);                 // 32..63
-        load_words2<8>(r.w + 18, blk + 128 + 32 * hf);               // high bits
+        const int half = c * KC / 128;
+        const uint8_t *blk = row + 210 * (half >> 1);
+        load_words2<8>(r.w, blk + 64 * (half & 1));                  // low nibbles, 0..31
+        load_words2<8>(r.w + 9, blk + 64 * (half & 1) + 32);         // 32..63
+        load_words2<8>(r.w + 18, blk + 128 + 32 * (half & 1));       // high bits
     }
 }
 
@@ -200,59 +220,59 @@ struct Pieces {
     }
 };
 
-// Half `k` of a chunk's 64 values, times 2^s, as fp16 pairs in the order (0, 2), (1, 3) of every four columns.
-template <int FMT, int PA>
-__device__ __forceinline__ void take_apart(Pieces<PA> &o, const Raw<FMT> &r, const uint8_t *row, int c, int cols, float up, int k)
+// Values 32 k .. 32 k + 31 of a stage, times 2^s, as fp16 pairs in the order (0, 2), (1, 3) of every four columns.
+template <int FMT, int PA, int KC>
+__device__ __forceinline__ void take_apart(Pieces<PA> &o, const Raw<FMT, KC> &r, const uint8_t *row, int c, int cols, float up, int k)
 {
     if constexpr (FMT == kFmtQ4K) {
-        // sub-block 2p + k
         const __half2 k1024 = __float2half2_rn(1024.0f);
-        const float2 d2 = __half22float2(tile_b2(r.w[8]));
-        const int p = c & 3, sh = (p & 1) * 16 + 8 * k;
-        const uint32_t A = r.w[9] >> sh, B = r.w[10] >> sh, C = r.w[11] >> sh;
-        const uint32_t sc = p < 2 ? A & 0x3fu : (C & 0x0fu) | ((A >> 2) & 0x30u);
-        const uint32_t mm = p < 2 ? B & 0x3fu : ((C >> 4) & 0x0fu) | ((B >> 2) & 0x30u);
+        const float2 d2 = __half22float2(tile_b2(r.w[KC / 8]));
+        const int pair = (c * (KC / 64) + (k >> 1)) & 3, high = k & 1, sh = (pair & 1) * 16 + 8 * high;     // sub-block 2 pair + high
+        const uint32_t A = r.w[KC / 8 + 1] >> sh, B = r.w[KC / 8 + 2] >> sh, C = r.w[KC / 8 + 3] >> sh;
+        const uint32_t sc = pair < 2 ? A & 0x3fu : (C & 0x0fu) | ((A >> 2) & 0x30u);
+        const uint32_t mm = pair < 2 ? B & 0x3fu : ((C >> 4) & 0x0fu) | ((B >> 2) & 0x30u);
         const __half2 s0 = __hsub2(tile_b2(0x64006400u | sc | sc << 16), k1024);
         const float d = d2.x * up, m = -d2.y * up * static_cast<float>(mm);
         const __half2 dh = __float2half2_rn(d), mh = __float2half2_rn(m);
-        const __half2 mul = k ? __hmul2(s0, __float2half2_rn(0.0625f)) : s0;
-        const __half2 add = __hmul2(s0, __float2half2_rn(k ? -64.0f : -1024.0f));
+        const __half2 mul = high ? __hmul2(s0, __float2half2_rn(0.0625f)) : s0;
+        const __half2 add = __hmul2(s0, __float2half2_rn(high ? -64.0f : -1024.0f));
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const uint32_t v = r.w[i];
+            const uint32_t v = r.w[8 * (k >> 1) + i];
             // scale times quant, exact
-            const __half2 a = __hfma2(k ? tile_field<0x00f000f0>(v) : tile_field<0x000f000f>(v), mul, add);
-            const __half2 b = __hfma2(k ? tile_field<0x00f000f0>(v >> 8) : tile_field<0x000f000f>(v >> 8), mul, add);
+            const __half2 a = __hfma2(high ? tile_field<0x00f000f0>(v) : tile_field<0x000f000f>(v), mul, add);
+            const __half2 b = __hfma2(high ? tile_field<0x00f000f0>(v >> 8) : tile_field<0x000f000f>(v >> 8), mul, add);
             o.set4(2 * i, a, b, d, m, dh, mh);
         }
     } else if constexpr (FMT == kFmtQ80) {
-        // block k of the two: d at byte 34 k, then the quants; none past the row's end
-        const uint32_t sh = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row + 68 * c) & 2) * 8;
+        // block k: d at byte 34 k, then the quants; none past the row's end
+        const int first = c * (KC / 32), base = 17 * (k >> 1);
+        const uint32_t sh = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row + 34 * static_cast<int64_t>(first)) & 2) * 8;
         const auto at = [&](int i) { return __funnelshift_r(r.w[i], r.w[i + 1], sh); };
         const __half2 bias = __float2half2_rn(1152.0f), zero = __float2half2_rn(0.0f);
-        const float d = 2 * c + k < (cols + 31) / 32 ? half_bits_to_float(k ? at(8) >> 16 : at(0)) * up : 0.0f;
+        const float d = first + k < (cols + 31) / 32 ? half_bits_to_float(k & 1 ? at(base + 8) >> 16 : at(base)) * up : 0.0f;
         const __half2 dh = __float2half2_rn(d);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const uint32_t q = (k ? at(9 + i) : __funnelshift_r(at(i), at(i + 1), 16)) ^ 0x80808080u;
+            const uint32_t q = (k & 1 ? at(base + 9 + i) : __funnelshift_r(at(base + i), at(base + i + 1), 16)) ^ 0x80808080u;
             o.set4(2 * i, __hsub2(tile_b2(__byte_perm(q, 0x64u, 0x4240)), bias), __hsub2(tile_b2(__byte_perm(q, 0x64u, 0x4341)), bias),
                    d, 0.0f, dh, zero);
         }
     } else {
-        // 32 columns t = 2 (c & 1) + k of the half
-        const int hf = (c >> 1) & 1, t0 = 2 * (c & 1);
-        const uint8_t *blk = row + 210 * (c >> 2);
+        // 32 columns t of the half
+        const int half = c * KC / 128, t = KC == 128 ? k : 2 * (c & 1) + k;
+        const uint8_t *blk = row + 210 * (half >> 1);
         const float d0 = half_at(blk + 208) * up;
         const uint32_t sh = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(blk) & 2) * 8;
         const __half2 bias = __float2half2_rn(1056.0f), zero = __float2half2_rn(0.0f);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            const float d = d0 * static_cast<float>(static_cast<int8_t>(__ldg(blk + 192 + 8 * hf + 2 * (t0 + k) + u)));
+            const float d = d0 * static_cast<float>(static_cast<int8_t>(__ldg(blk + 192 + 8 * (half & 1) + 2 * t + u)));
             const __half2 dh = __float2half2_rn(d);
 #pragma unroll
             for (int i = 4 * u; i < 4 * u + 4; ++i) {
-                const uint32_t low = __funnelshift_r(r.w[9 * k + i], r.w[9 * k + i + 1], sh) >> (2 * t0);
-                const uint32_t high = __funnelshift_r(r.w[18 + i], r.w[19 + i], sh) >> (2 * (t0 + k));
+                const uint32_t low = __funnelshift_r(r.w[9 * (k & 1) + i], r.w[9 * (k & 1) + i + 1], sh) >> (t & 2 ? 4 : 0);
+                const uint32_t high = __funnelshift_r(r.w[18 + i], r.w[19 + i], sh) >> (2 * t);
                 const uint32_t q = (low & 0x0f0f0f0fu) | ((high & 0x03030303u) << 4);
                 o.set4(2 * i, __hsub2(tile_b2(__byte_perm(q, 0x64u, 0x4240)), bias), __hsub2(tile_b2(__byte_perm(q, 0x64u, 0x4341)), bias),
                        d, 0.0f, dh, zero);
@@ -265,9 +285,9 @@ template <int FMT, int PA, int PB, bool PAIRED>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(tile_threads(PB), 1)
 tile_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ CUtensorMap map_lo, const TileArgs a)
 {
-    constexpr int kMaxN = PA == 1 ? 192 : 128, kStages = tile_stages(PA, PB), kStage = tile_b_bytes(PA, PB);
-    constexpr int kEpiWarps = tile_epi_warps(PB);
-    constexpr uint32_t kACols = 32 * PA, kA0 = 2 * kMaxN;         // tensor-memory columns of an A stage, and of the first
+    constexpr int KC = tile_cols_of_stage(PA), kStage = tile_b_bytes(PA, PB), kEpiWarps = tile_epi_warps(PB);
+    constexpr uint32_t kACols = KC / 2 * PA, kA0 = 2 * kMaxN;         // tensor-memory columns of a stage of A, and of the first
+    static_assert(kA0 + kStages * kACols == 512, "all of tensor memory");
     extern __shared__ uint8_t raw_smem[];
     __shared__ TileShared sh;
     const uint32_t b_base = (smem_u32(raw_smem) + 1023u) & ~1023u;
@@ -275,8 +295,10 @@ tile_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
     const int rank = static_cast<int>(cluster_ctarank());
     volatile int *abort = &sh.abort;
     if (tid == 0) {
-        for (int i = 0; i < kStages; ++i) mbar_init(smem_u32(&sh.full_b[i]), 1), mbar_init(smem_u32(&sh.empty_b[i]), 2);
-        for (int i = 0; i < kAStages; ++i) mbar_init(smem_u32(&sh.full_a[i]), 4), mbar_init(smem_u32(&sh.empty_a[i]), 1);
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(smem_u32(&sh.full[i]), 5);                     // a group's four warps, and the copies
+            mbar_init(smem_u32(&sh.empty_b[i]), 2), mbar_init(smem_u32(&sh.empty_a[i]), 1);
+        }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&sh.acc_full[i]), 1), mbar_init(smem_u32(&sh.acc_empty[i]), kEpiWarps);
             mbar_init(smem_u32(&sh.rs_full[i]), 2), mbar_init(smem_u32(&sh.rs_empty[i]), kEpiWarps);
@@ -300,7 +322,7 @@ tile_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
     const int pairs = (a.tiles + 1) / 2;
     const int64_t items = static_cast<int64_t>(a.plan.head[3]) * pairs, first = blockIdx.x >> 1, step = gridDim.x >> 1;
     const int nk = a.chunks;
-    const int per = PB == 2 ? kFlush : nk;                     // chunks an accumulator takes
+    const int per = PB == 2 ? kFlush : nk;                     // stages an accumulator takes
     const auto set_of = [&](int64_t item) { return a.plan.tile_sets[item / pairs]; };
     const auto tile_of = [&](int64_t item) { return static_cast<int>(item % pairs) * 2 + rank; };
 
@@ -318,57 +340,62 @@ tile_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
                         ok = false;
                         break;
                     }
-                    const uint32_t full = smem_u32(&sh.full_b[st]), to = b_base + st * kStage;
-                    mbar_arrive_expect_tx(full, boxes * kTileBoxRows * 128 * PB);
+                    const uint32_t full = smem_u32(&sh.full[st]), to = b_base + st * kStage;
+                    mbar_arrive_expect_tx(full, boxes * kTileBoxRows * 2 * KC * PB);
                     if (a.skip_chunk >= 0 && n == a.skip_chunk && blockIdx.x < 2) continue;     // test hook
-                    for (int b = rank; b < boxes; b += 2) {
-                        tma_load_2d_both(to + b * kTileBoxRows * 128, &map_hi, c * kChunk, s.first + b * kTileBoxRows, full, keep);
-                        if (PB == 2)
-                            tma_load_2d_both(to + kStage / 2 + b * kTileBoxRows * 128, &map_lo, c * kChunk, s.first + b * kTileBoxRows,
-                                             full, keep);
-                    }
+                    for (int b = rank; b < boxes; b += 2)
+#pragma unroll
+                        for (int k = 0; k < KC / 64; ++k) {
+                            const uint32_t at = to + k * (kMaxN * 128) + b * (kTileBoxRows * 128);
+                            tma_load_2d_both(at, &map_hi, c * KC + k * 64, s.first + b * kTileBoxRows, full, keep);
+                            if (PB == 2)
+                                tma_load_2d_both(at + kStage / 2, &map_lo, c * KC + k * 64, s.first + b * kTileBoxRows, full, keep);
+                        }
                 }
             }
             // every copy that this block has asked for lands before it leaves (the other's, too: the closing barrier)
-            for (int t = max(0, n - kStages); t < n; ++t) mbar_wait(smem_u32(&sh.full_b[t % kStages]), (t / kStages) & 1, a.wait_ns);
+            for (int t = max(0, n - kStages); t < n; ++t) mbar_wait(smem_u32(&sh.full[t % kStages]), (t / kStages) & 1, a.wait_ns);
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0) {
-            int n = 0, q = 0;                                  // chunks and accumulators so far
-            bool ok = true;
-            for (int64_t item = first; item < items && ok; item += step) {
-                const int count = set_of(item).count;
-                const uint32_t idesc = idesc_f16_f32(128, (count + 15) / 16 * 16);
-                for (int c = 0; c < nk; ++c, ++n) {
-                    const int sa = n % kAStages, sb = n % kStages, buf = q & 1;
-                    const bool fresh = c % per == 0;
-                    if ((fresh && q >= 2 && !tile_wait(smem_u32(&sh.acc_empty[buf]), (q / 2 - 1) & 1, a, abort)) ||
-                        !tile_wait(smem_u32(&sh.full_b[sb]), (n / kStages) & 1, a, abort) ||
-                        !tile_wait(smem_u32(&sh.full_a[sa]), (n / kAStages) & 1, a, abort)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t d = taddr + buf * kMaxN, at = taddr + kA0 + sa * kACols, b = b_base + sb * kStage;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const uint64_t bh = smem_desc_sw128_kmajor(b + 32 * k);
-                        tc_mma_f16_tmem_a(d, at + 8 * k, bh, idesc, !fresh || k > 0);
-                        if constexpr (PA == 2) tc_mma_f16_tmem_a(d, at + 32 + 8 * k, bh, idesc, 1);
-                        if constexpr (PB == 2)
-                            tc_mma_f16_tmem_a(d, at + 8 * k, smem_desc_sw128_kmajor(b + kStage / 2 + 32 * k), idesc, 1);
-                    }
-                    tc_commit_1(smem_u32(&sh.empty_a[sa]));
-                    tc_commit_both(smem_u32(&sh.empty_b[sb]));
-                    if (c + 1 == nk || (c + 1) % per == 0) tc_commit_1(smem_u32(&sh.acc_full[buf])), ++q;
+        // The warp stays together and elects a lane for each product: a thread of a branch of its own takes 118 cycles a
+        // product whatever its size (measured), an elected one N / 2.
+        int n = 0, q = 0;                                      // stages and accumulators so far
+        bool ok = true;
+        const uint64_t desc0 = smem_desc_sw128_kmajor(b_base);
+        for (int64_t item = first; item < items && ok; item += step) {
+            const int count = set_of(item).count;
+            const uint32_t idesc = idesc_f16_f32(128, (count + 15) / 16 * 16);
+            for (int c = 0; c < nk; ++c, ++n) {
+                const int st = n % kStages, buf = q & 1;
+                const bool fresh = c % per == 0, last = c + 1 == nk || (c + 1) % per == 0;
+                if ((fresh && q >= 2 && !tile_wait_warp(smem_u32(&sh.acc_empty[buf]), (q / 2 - 1) & 1, a, abort)) ||
+                    !tile_wait_warp(smem_u32(&sh.full[st]), (n / kStages) & 1, a, abort)) {
+                    ok = false;
+                    break;
                 }
+                tc_fence_after();
+                const uint32_t d = taddr + buf * kMaxN, at = taddr + kA0 + st * kACols;
+                const uint64_t b = desc0 + static_cast<uint64_t>(st * (kStage >> 4));
+                if (elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < KC / 16; ++k) {
+                        const uint64_t bk = b + (k >> 2) * (kMaxN * 128 >> 4) + 2 * (k & 3);
+                        tc_mma_f16_tmem_a(d, at + 8 * k, bk, idesc, !fresh || k > 0);
+                        if constexpr (PA == 2) tc_mma_f16_tmem_a(d, at + KC / 2 + 8 * k, bk, idesc, 1);
+                        if constexpr (PB == 2) tc_mma_f16_tmem_a(d, at + 8 * k, bk + (kStage >> 5), idesc, 1);
+                    }
+                    tc_commit_1(smem_u32(&sh.empty_a[st]));
+                    tc_commit_both(smem_u32(&sh.empty_b[st]));
+                    if (last) tc_commit_1(smem_u32(&sh.acc_full[buf]));
+                }
+                if (last) ++q;
             }
-            // products in flight end before tensor memory is freed
-            if (n > 0) mbar_wait(smem_u32(&sh.empty_a[(n - 1) % kAStages]), ((n - 1) / kAStages) & 1, a.wait_ns);
-            // and the other block's arrivals have come before this one leaves
-            for (int t = max(0, n - kStages); t < n; ++t) mbar_wait(smem_u32(&sh.empty_b[t % kStages]), (t / kStages) & 1, a.wait_ns);
         }
+        // products in flight end before tensor memory is freed
+        if (n > 0) mbar_wait(smem_u32(&sh.empty_a[(n - 1) % kStages]), ((n - 1) / kStages) & 1, a.wait_ns);
+        // and the other block's arrivals have come before this one leaves
+        for (int t = max(0, n - kStages); t < n; ++t) mbar_wait(smem_u32(&sh.empty_b[t % kStages]), (t / kStages) & 1, a.wait_ns);
         __syncwarp();
     } else if (warp < kDeqWarp) {
         // rows' scales, an item ahead
@@ -380,29 +407,29 @@ tile_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
 #pragma unroll
             for (int r = 0; r < 2; ++r)
                 v[r] = row_scale_of<FMT>(tile_row<PAIRED>(a, s.expert, tile_of(item), (warp - 2) * 64 + r * 32 + lane), a.cols);
-            if (it >= 2 && !__all_sync(~0u, tile_wait(smem_u32(&sh.rs_empty[buf]), (it / 2 - 1) & 1, a, abort))) break;
+            if (it >= 2 && !tile_wait_warp(smem_u32(&sh.rs_empty[buf]), (it / 2 - 1) & 1, a, abort)) break;
 #pragma unroll
             for (int r = 0; r < 2; ++r) sh.row_scale[buf][(warp - 2) * 64 + r * 32 + lane] = v[r];
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sh.rs_full[buf]));
         }
     } else if (warp < kEpiWarp) {
-        // takes chunks apart: group h has every other one of the block's
+        // takes stages' weights apart: group h has every other stage of the block's
         const int group = (warp - kDeqWarp) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
         int n = group, it = 0, c = group;
         int64_t item = first;
         while (c >= nk) c -= nk, ++it, item += step;
-        // the next chunk's bytes are on their way while one is taken apart
-        Raw<FMT> next;
+        // the next stage's bytes are on their way while one is taken apart
+        Raw<FMT, KC> next;
         const uint8_t *at = nullptr;
         if (item < items) {
             at = tile_row<PAIRED>(a, set_of(item).expert, tile_of(item), row);
-            load_raw<FMT>(next, at, c, a.cols);
+            load_raw<FMT, KC>(next, at, c, a.cols);
         }
         float up = 0.0f;
         int have = -1;
         while (item < items) {
-            const Raw<FMT> now = next;
+            const Raw<FMT, KC> now = next;
             const uint8_t *now_at = at;
             const int now_c = c, now_it = it;
             c += kDeqGroups;
@@ -410,28 +437,28 @@ tile_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
             while (c >= nk) c -= nk, ++it, item += step, moved = true;
             if (item < items) {
                 if (moved) at = tile_row<PAIRED>(a, set_of(item).expert, tile_of(item), row);
-                load_raw<FMT>(next, at, c, a.cols);
+                load_raw<FMT, KC>(next, at, c, a.cols);
             }
             if (have != now_it) {
-                if (!__all_sync(~0u, tile_wait(smem_u32(&sh.rs_full[now_it & 1]), (now_it / 2) & 1, a, abort))) break;
+                if (!tile_wait_warp(smem_u32(&sh.rs_full[now_it & 1]), (now_it / 2) & 1, a, abort)) break;
                 up = sh.row_scale[now_it & 1][row];
                 have = now_it;
             }
-            const int sa = n % kAStages;
-            if (n >= kAStages && !__all_sync(~0u, tile_wait(smem_u32(&sh.empty_a[sa]), (n / kAStages - 1) & 1, a, abort))) break;
+            const int st = n % kStages;
+            if (n >= kStages && !tile_wait_warp(smem_u32(&sh.empty_a[st]), (n / kStages - 1) & 1, a, abort)) break;
             tc_fence_after();
-            const uint32_t to = taddr + (static_cast<uint32_t>(quarter * 32) << 16) + kA0 + sa * kACols;
+            const uint32_t to = taddr + (static_cast<uint32_t>(quarter * 32) << 16) + kA0 + st * kACols;
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
+            for (int k = 0; k < KC / 32; ++k) {
                 Pieces<PA> o;
-                take_apart<FMT, PA>(o, now, now_at, now_c, a.cols, up, k);
+                take_apart<FMT, PA, KC>(o, now, now_at, now_c, a.cols, up, k);
                 tmem_st_32x32b_x16(to + 16 * k, o.hi);
-                if constexpr (PA == 2) tmem_st_32x32b_x16(to + 32 + 16 * k, o.lo);
+                if constexpr (PA == 2) tmem_st_32x32b_x16(to + KC / 2 + 16 * k, o.lo);
             }
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&sh.full_a[sa]));
+            if (lane == 0) mbar_arrive(smem_u32(&sh.full[st]));
             n += kDeqGroups;
         }
     } else {
@@ -470,7 +497,7 @@ tile_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
                 }
             };
             const auto ready = [&]() {
-                if (!__all_sync(~0u, tile_wait(smem_u32(&sh.acc_full[q & 1]), (q / 2) & 1, a, abort))) return ok = false;
+                if (!tile_wait_warp(smem_u32(&sh.acc_full[q & 1]), (q / 2) & 1, a, abort)) return ok = false;
                 tc_fence_after();
                 if (back == 0.0f) back = 1.0f / sh.row_scale[it & 1][row];      // a power of two
                 return true;
