@@ -6,6 +6,7 @@
 
 #include "qk_kv4.cuh"
 #include "qk_moe.cuh"
+#include "qk_tc.cuh"
 
 namespace qk {
 using namespace moe;
@@ -24,98 +25,128 @@ struct PlanArgs {
     int *err;
 };
 
-// Sum over the thread block before this thread, and all of it.
-__device__ __forceinline__ int scan_before(int v, int *warp_sums, int &all)
+__device__ __forceinline__ int4 plus(int4 a, int4 b) { return make_int4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w); }
+
+// Sums over the threads before this one, and over all of the thread block.
+__device__ __forceinline__ int4 scan_before(const int4 v, int4 *warp_sums, int4 &all)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int in = v;
+    const auto scan = [&](int4 in) {
 #pragma unroll
-    for (int d = 1; d < 32; d *= 2) {
-        const int o = __shfl_up_sync(~0u, in, d);
-        if (lane >= d) in += o;
-    }
-    __syncthreads();
+        for (int d = 1; d < 32; d *= 2) {
+            const int4 o = make_int4(__shfl_up_sync(~0u, in.x, d), __shfl_up_sync(~0u, in.y, d), __shfl_up_sync(~0u, in.z, d),
+                                     __shfl_up_sync(~0u, in.w, d));
+            if (lane >= d) in = plus(in, o);
+        }
+        return in;
+    };
+    const auto of_lane = [&](int4 in, int from) {
+        return make_int4(__shfl_sync(~0u, in.x, from), __shfl_sync(~0u, in.y, from), __shfl_sync(~0u, in.z, from),
+                         __shfl_sync(~0u, in.w, from));
+    };
+    const int4 in = scan(v);
     if (lane == 31) warp_sums[warp] = in;
     __syncthreads();
-    int before = 0;
-    all = 0;
-    for (int w = 0; w < kPlanThreads / 32; ++w) {
-        if (w < warp) before += warp_sums[w];
-        all += warp_sums[w];
-    }
-    return before + in - v;
+    const int4 sums = scan(warp_sums[lane]);                 // kPlanThreads / 32 warps: one a lane
+    all = of_lane(sums, 31);
+    const int4 before = of_lane(sums, warp > 0 ? warp - 1 : 0);
+    const int4 mine = make_int4(in.x - v.x, in.y - v.y, in.z - v.z, in.w - v.w);
+    return warp > 0 ? plus(before, mine) : mine;
 }
 
-// Groups the assignments by expert: a counting sort by one thread block.  Each warp counts its own run of ids, a
-// thread an expert turns the counts into first places, and each warp places its run again in order, so that places
-// rise with the assignments.
+// Groups the assignments by expert: a counting sort.  Each warp counts its own run of ids, a thread an expert turns the
+// counts into first places, and each warp places its run again in order, so that places rise with the assignments.
+// Many ids are shared out over the blocks of a cluster, which read each other's counts.
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a)
 {
     extern __shared__ int counts[];             // [warp][expert]
-    __shared__ int warp_sums[kPlanThreads / 32];
+    __shared__ int4 warp_sums[kPlanThreads / 32];
+    __shared__ int block_count[kMaxExperts], place_of[kMaxExperts], octet_of[kMaxExperts];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int first = warp * a.per_warp, last = min(a.n, first + a.per_warp);
+    const int blocks = static_cast<int>(gridDim.x), rank = static_cast<int>(blockIdx.x);
+    const int64_t first = (static_cast<int64_t>(rank) * (kPlanThreads / 32) + warp) * a.per_warp;
+    const int64_t last = min(static_cast<int64_t>(a.n), first + a.per_warp);
+    const int warps = min(kPlanThreads / 32, (a.n + a.per_warp - 1) / a.per_warp);      // that may have ids
     let_next_start();
-    for (int i = threadIdx.x; i < kPlanThreads / 32 * a.experts; i += kPlanThreads) counts[i] = 0;
+    for (int i = threadIdx.x; i < warps * a.experts; i += kPlanThreads) counts[i] = 0;
     __syncthreads();
     wait_for_previous();
     int *mine = counts + warp * a.experts;
-    for (int base = first; base < last; base += 32) {
-        const int i = base + lane;
-        const int id = i < last ? a.ids[i] : -1;
-        const bool live = id >= 0 && id < a.experts;
-        if (i < last && id >= a.experts) record_error(a.err, kErrBadIndex);
-        const unsigned same = __match_any_sync(~0u, live ? id : -1);
+    constexpr int kAhead = 4;                   // loads on their way at once
+    // f(assignment, id, the lanes with the same live id) over this warp's run, in order; -1: no live id
+    const auto over_run = [&](auto f) {
+        for (int64_t base = first; base < last; base += 32 * kAhead) {
+            int id[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) id[k] = base + 32 * k + lane < last ? a.ids[base + 32 * k + lane] : -1;
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                if (base + 32 * k >= last) break;
+                const bool live = id[k] >= 0 && id[k] < a.experts;
+                f(base + 32 * k + lane, id[k], live, __match_any_sync(~0u, live ? id[k] : -1));
+                __syncwarp();
+            }
+        }
+    };
+    over_run([&](int64_t, int id, bool live, unsigned same) {
+        if (id >= a.experts) record_error(a.err, kErrBadIndex);
         if (live && lane == __ffs(same) - 1) mine[id] += __popc(same);
-        __syncwarp();
-    }
+    });
     __syncthreads();
     const int e = threadIdx.x;
     int n = 0;
-    if (e < a.experts)
-        for (int w = 0; w < kPlanThreads / 32; ++w) {
+    if (e < a.experts) {
+        for (int w = 0; w < warps; ++w) {
             const int k = counts[w * a.experts + e];
             counts[w * a.experts + e] = n;
             n += k;
         }
-    int places, octets, sets;
-    const int first_place = scan_before(n, warp_sums, places);
+        block_count[e] = n;
+    }
+    int before = 0;                             // the expert's ids in the blocks before
+    if (blocks > 1) {
+        cluster_sync();
+        if (e < a.experts) {
+            n = 0;
+            for (int q = 0; q < blocks; ++q) {
+                int k;
+                asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(k) : "r"(mapa_shared(smem_u32(block_count + e), q)));
+                if (q < rank) before += k;
+                n += k;
+            }
+        }
+    }
     const bool tiled = n >= a.tile_from;
     // tile sets as even as 16 tokens allow, none of them empty
     const int parts = (n + a.tile_tokens - 1) / a.tile_tokens;
     const int per = tiled ? ((n + parts - 1) / parts + 15) / 16 * 16 : 1;
     const int rows_n = tiled ? 0 : n, tile_n = tiled ? (n + per - 1) / per : 0;
-    const int octet0 = scan_before((rows_n + 7) / 8, warp_sums, octets);
-    const int set0 = scan_before((rows_n + 8 * kSetOctets - 1) / (8 * kSetOctets), warp_sums, sets);
-    int tile_sets;
-    const int tile0 = scan_before(tile_n, warp_sums, tile_sets);
-    __shared__ int place_of[kMaxExperts], octet_of[kMaxExperts];
+    int4 all;
+    const int4 at = scan_before(make_int4(n, (rows_n + 7) / 8, (rows_n + 8 * kSetOctets - 1) / (8 * kSetOctets), tile_n), warp_sums, all);
     if (e < a.experts) {
-        place_of[e] = first_place, octet_of[e] = tiled ? -1 : octet0;
-        for (int i = 0, s = set0; i < rows_n; i += 8 * kSetOctets, ++s)
-            a.plan.sets[s] = {e, first_place + i, min(8 * kSetOctets, n - i), octet0 + i / 8};
-        for (int i = 0; i < tile_n; ++i) a.plan.tile_sets[tile0 + i] = {e, first_place + i * per, min(per, n - i * per), 0};
+        place_of[e] = at.x + before, octet_of[e] = tiled ? -1 : at.y * 8 + before;
+        if (rank == 0) {
+            for (int i = 0, s = at.z; i < rows_n; i += 8 * kSetOctets, ++s)
+                a.plan.sets[s] = {e, at.x + i, min(8 * kSetOctets, n - i), at.y + i / 8};
+            for (int i = 0; i < tile_n; ++i) a.plan.tile_sets[at.w + i] = {e, at.x + i * per, min(per, n - i * per), 0};
+        }
     }
-    if (e == 0) a.plan.head[0] = sets, a.plan.head[1] = octets, a.plan.head[2] = places, a.plan.head[3] = tile_sets;
+    if (e == 0 && rank == 0) a.plan.head[0] = all.z, a.plan.head[1] = all.y, a.plan.head[2] = all.x, a.plan.head[3] = all.w;
     __syncthreads();
-    for (int base = first; base < last; base += 32) {
-        const int i = base + lane;
-        const int id = i < last ? a.ids[i] : -1;
-        const bool live = id >= 0 && id < a.experts;
-        const unsigned same = __match_any_sync(~0u, live ? id : -1);
-        const int before = live ? mine[id] : 0;
+    over_run([&](int64_t i, int id, bool live, unsigned same) {
+        const int taken = live ? mine[id] : 0;
         __syncwarp();
         if (live) {
-            const int k = before + __popc(same & ((1u << lane) - 1));       // its number among the expert's
-            if (lane == __ffs(same) - 1) mine[id] = before + __popc(same);
+            const int k = taken + __popc(same & ((1u << lane) - 1));       // its number among this block's of the expert
+            if (lane == __ffs(same) - 1) mine[id] = taken + __popc(same);
             const int p = place_of[id] + k;
-            a.plan.assignment[p] = i, a.plan.place[i] = p;
-            a.plan.column[p] = octet_of[id] < 0 ? -1 : octet_of[id] * 8 + k;
+            a.plan.assignment[p] = static_cast<int>(i), a.plan.place[i] = p;
+            a.plan.column[p] = octet_of[id] < 0 ? -1 : octet_of[id] + k;
         } else if (i < last) {
             a.plan.place[i] = id < 0 ? -1 : -2;
         }
-        __syncwarp();
-    }
+    });
+    if (blocks > 1) cluster_sync();             // the counts are read to the end
 }
 
 // Four neighbouring values of a row, 0 past its end.
@@ -155,88 +186,108 @@ __device__ __forceinline__ void pieces_of(const float4 v, uint2 &hi, uint2 &lo)
 
 constexpr int kPackThreads = 256;
 
-// A thread block lays out one place's row.  Thread (unit, c, i) makes the 16 bytes that lane (column, c) of step i reads.
-__global__ void __launch_bounds__(kPackThreads) pack_kernel(const PackArgs a, bool vec)
+// Lays rows out as operands, WARPS warps a row: a token's row for each of its places (top_k > 0), or a place's own.
+template <int WARPS>
+__global__ void __launch_bounds__(kPackThreads) pack_kernel(const PackArgs a)
 {
+    constexpr int kThreads = 32 * WARPS;
     __shared__ uint32_t warp_max[kPackThreads / 32];
     let_next_start();
     wait_for_previous();
-    const int p = blockIdx.x;
-    if (p >= a.plan.head[2]) return;
-    const int64_t row = static_cast<int64_t>(a.top_k ? a.plan.assignment[p] / a.top_k : p) * a.ld;
+    const int tid = threadIdx.x % kThreads;
+    const int64_t r = static_cast<int64_t>(blockIdx.x) * (kPackThreads / kThreads) + threadIdx.x / kThreads;
+    if (r >= (a.top_k ? a.tokens : a.plan.head[2])) return;         // (whole rows: all of a block's threads, or of a warp)
+    const int64_t row = r * a.ld;
     uint32_t most = 0;          // magnitudes order as their bits do
-    for (int k = threadIdx.x * 4; k < a.cols; k += kPackThreads * 4) {
-        const float4 v = four(a.x, row, k, a.cols, a.type, vec);
+#pragma unroll 4
+    for (int k = tid * 4; k < a.cols; k += kThreads * 4) {
+        const float4 v = four(a.x, row, k, a.cols, a.type, a.vec);
         most = max(max(most, max(__float_as_uint(v.x) & 0x7fffffffu, __float_as_uint(v.y) & 0x7fffffffu)),
                    max(__float_as_uint(v.z) & 0x7fffffffu, __float_as_uint(v.w) & 0x7fffffffu));
     }
     most = __reduce_max_sync(~0u, most);
-    if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = most;
-    __syncthreads();
+    if constexpr (WARPS > 1) {
+        if ((tid & 31) == 0) warp_max[tid >> 5] = most;
+        __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kPackThreads / 32; ++w) most = max(most, warp_max[w]);
+        for (int w = 0; w < WARPS; ++w) most = max(most, warp_max[w]);
+    }
     // 2^e puts it into [2^14, 2^15); rows of zeros, infinities and NaN stay as they are, and e stops where 2^-e is
     // no normal number any more
     const int ex = most >= 0x7f800000u || most == 0 ? 141 : max(static_cast<int>(most >> 23), 15);
     const float up = __uint_as_float(static_cast<uint32_t>(127 + 141 - ex) << 23);
-    if (threadIdx.x == 0) a.scale[p] = __uint_as_float(static_cast<uint32_t>(127 - 141 + ex) << 23);
+    const float back = __uint_as_float(static_cast<uint32_t>(127 - 141 + ex) << 23);
     const int64_t unit = octet_unit_bytes(a.fmt, a.pieces);
-    const int column = a.plan.column[p];
-    if (column < 0) {
-        // a tile set's row, in the order in which its weights are taken apart: (0, 2, 1, 3) of every four
-        for (int k = threadIdx.x * 4; k < a.tile_cols; k += kPackThreads * 4) {
-            float4 v = four(a.x, row, k, a.cols, a.type, vec);
-            v.x *= up, v.y *= up, v.z *= up, v.w *= up;
-            uint2 h, l;
-            pieces_of(v, h, l);
+    const int places = a.top_k ? a.top_k : 1;
+    bool tiled = false;
+    for (int j = 0; j < places; ++j) {
+        const int p = a.top_k ? a.plan.place[r * a.top_k + j] : static_cast<int>(r);
+        if (p < 0) continue;
+        if (tid == 0) a.scale[p] = back;
+        const int column = a.plan.column[p];
+        if (column < 0) {
+            tiled = true;
+            continue;
+        }
+        // thread (unit, c, i) makes the 16 bytes that lane (column, c) of step i reads
+        uint8_t *out = a.out + (column >> 3) * unit * a.units;
+        const int col = column & 7;
+        for (int q = tid; q < a.units * 32; q += kThreads) {
+            const int u = q >> 5, c = (q >> 3) & 3, i = q & 7;
+            const int k = u * kUnit;
+            int k0, k1;
+            if (a.fmt == kFmtQ4K) k0 = k + 64 * c + 4 * i, k1 = k0 + 32;                     // sub-blocks 2c and 2c + 1
+            else if (a.fmt == kFmtQ80) k0 = k + 32 * i + 8 * c, k1 = k0 + 4;                 // block i
+            else k0 = k + 128 * (i >> 2) + 64 * (i & 1) + 16 * ((i >> 1) & 1) + 4 * c, k1 = k0 + 32;    // sub-blocks t, t + 1
+            float4 v0 = four(a.x, row, k0, a.cols, a.type, a.vec), v1 = four(a.x, row, k1, a.cols, a.type, a.vec);
+            v0.x *= up, v0.y *= up, v0.z *= up, v0.w *= up;
+            v1.x *= up, v1.y *= up, v1.z *= up, v1.w *= up;
+            uint2 h0, l0, h1, l1;
+            pieces_of(v0, h0, l0), pieces_of(v1, h1, l1);
+            uint8_t *at = out + u * unit;
+            const int lane = col * 4 + c;
+            *reinterpret_cast<uint4 *>(at + i * 512 + lane * 16) = make_uint4(h0.x, h0.y, h1.x, h1.y);
+            if (a.pieces == 2)
+                *reinterpret_cast<uint4 *>(at + kPieceBytes + i * 512 + lane * 16) = make_uint4(l0.x, l0.y, l1.x, l1.y);
+            if (a.fmt == kFmtQ4K) {
+                // sums of the values as the pieces hold them, over the 8 threads of a sub-block; 2^-5 of them in two pieces
+                const auto held = [&](uint2 h, uint2 l) {
+                    const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&h.x));
+                    const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&h.y));
+                    float s = (x.x + x.y) + (y.x + y.y);
+                    if (a.pieces == 2) {
+                        const float2 z = __half22float2(*reinterpret_cast<const __half2 *>(&l.x));
+                        const float2 w = __half22float2(*reinterpret_cast<const __half2 *>(&l.y));
+                        s += (z.x + z.y) + (w.x + w.y);
+                    }
+                    return s;
+                };
+                float s0 = held(h0, l0), s1 = held(h1, l1);
+#pragma unroll
+                for (int d = 1; d < 8; d *= 2) s0 += __shfl_xor_sync(~0u, s0, d), s1 += __shfl_xor_sync(~0u, s1, d);
+                s0 *= 0.03125f, s1 *= 0.03125f;
+                if (i == 0) {
+                    const uint32_t hi = pack2h(s0, s1);
+                    const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+                    *reinterpret_cast<uint2 *>(at + a.pieces * kPieceBytes + lane * 8) =
+                        make_uint2(hi, pack2h(s0 - h.x, s1 - h.y));
+                }
+            }
+        }
+    }
+    if (!tiled) return;
+    // rows of tile sets, in the order in which their weights are taken apart: (0, 2, 1, 3) of every four
+    for (int k = tid * 4; k < a.tile_cols; k += kThreads * 4) {
+        float4 v = four(a.x, row, k, a.cols, a.type, a.vec);
+        v.x *= up, v.y *= up, v.z *= up, v.w *= up;
+        uint2 h, l;
+        pieces_of(v, h, l);
+        for (int j = 0; j < places; ++j) {
+            const int p = a.top_k ? a.plan.place[r * a.top_k + j] : static_cast<int>(r);
+            if (p < 0 || a.plan.column[p] >= 0) continue;
             __half *to = a.tile_out + static_cast<int64_t>(p) * a.tile_cols + k;
             *reinterpret_cast<uint2 *>(to) = h;
             if (a.pieces == 2) *reinterpret_cast<uint2 *>(to + a.tile_lo) = l;
-        }
-        return;
-    }
-    uint8_t *out = a.out + (column >> 3) * unit * a.units;
-    const int col = column & 7;
-    for (int j = threadIdx.x; j < a.units * 32; j += kPackThreads) {
-        const int u = j >> 5, c = (j >> 3) & 3, i = j & 7;
-        const int k = u * kUnit;
-        int k0, k1;
-        if (a.fmt == kFmtQ4K) k0 = k + 64 * c + 4 * i, k1 = k0 + 32;                     // sub-blocks 2c and 2c + 1
-        else if (a.fmt == kFmtQ80) k0 = k + 32 * i + 8 * c, k1 = k0 + 4;                 // block i
-        else k0 = k + 128 * (i >> 2) + 64 * (i & 1) + 16 * ((i >> 1) & 1) + 4 * c, k1 = k0 + 32;    // sub-blocks t, t + 1
-        float4 v0 = four(a.x, row, k0, a.cols, a.type, vec), v1 = four(a.x, row, k1, a.cols, a.type, vec);
-        v0.x *= up, v0.y *= up, v0.z *= up, v0.w *= up;
-        v1.x *= up, v1.y *= up, v1.z *= up, v1.w *= up;
-        uint2 h0, l0, h1, l1;
-        pieces_of(v0, h0, l0), pieces_of(v1, h1, l1);
-        uint8_t *at = out + u * unit;
-        const int lane = col * 4 + c;
-        *reinterpret_cast<uint4 *>(at + i * 512 + lane * 16) = make_uint4(h0.x, h0.y, h1.x, h1.y);
-        if (a.pieces == 2)
-            *reinterpret_cast<uint4 *>(at + kPieceBytes + i * 512 + lane * 16) = make_uint4(l0.x, l0.y, l1.x, l1.y);
-        if (a.fmt == kFmtQ4K) {
-            // sums of the values as the pieces hold them, over the 8 threads of a sub-block; 2^-5 of them in two pieces
-            const auto held = [&](uint2 h, uint2 l) {
-                const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&h.x));
-                const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&h.y));
-                float s = (x.x + x.y) + (y.x + y.y);
-                if (a.pieces == 2) {
-                    const float2 z = __half22float2(*reinterpret_cast<const __half2 *>(&l.x));
-                    const float2 w = __half22float2(*reinterpret_cast<const __half2 *>(&l.y));
-                    s += (z.x + z.y) + (w.x + w.y);
-                }
-                return s;
-            };
-            float s0 = held(h0, l0), s1 = held(h1, l1);
-#pragma unroll
-            for (int d = 1; d < 8; d *= 2) s0 += __shfl_xor_sync(~0u, s0, d), s1 += __shfl_xor_sync(~0u, s1, d);
-            s0 *= 0.03125f, s1 *= 0.03125f;
-            if (i == 0) {
-                const uint32_t hi = pack2h(s0, s1);
-                const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
-                *reinterpret_cast<uint2 *>(at + a.pieces * kPieceBytes + lane * 8) =
-                    make_uint2(hi, pack2h(s0 - h.x, s1 - h.y));
-            }
         }
     }
 }
@@ -349,14 +400,6 @@ int check_weights(const qk_expert_weights *w, int64_t E, int64_t rows, int64_t c
     return QK_OK;
 }
 
-// Warps that share a tile's columns: enough for every SM's 16 warps to have work where tiles are few.
-int share(int64_t tiles, int units, int sms)
-{
-    int kw = 1;
-    while (kw < kRowWarps && 2 * kw <= units && tiles * kw < 16LL * sms) kw *= 2;
-    return kw;
-}
-
 cudaError_t rows_launch(const RowsArgs &a, bool paired, int sms, cudaStream_t st)
 {
     return a.fmt == kFmtQ4K ? rows_launch_q4k(a, paired, sms, st)
@@ -414,8 +457,10 @@ int qk_moe_ffn(const qk_expert_weights *gate, const qk_expert_weights *up, const
 
     PlanArgs pa{};
     pa.ids = ids, pa.n = static_cast<int>(l.A), pa.experts = static_cast<int>(n_experts), pa.err = err;
+    // 8 thread blocks where one would go over its ids more than four times (32768 ids: 82 us in one, see the kernel)
     constexpr int kWarps = kPlanThreads / 32;
-    pa.per_warp = static_cast<int>((l.A + 32 * kWarps - 1) / (32 * kWarps) * 32);
+    const int plan_blocks = l.A > 4 * 32 * kWarps ? 8 : 1;
+    pa.per_warp = static_cast<int>((l.A + 32LL * kWarps * plan_blocks - 1) / (32LL * kWarps * plan_blocks) * 32);
     pa.plan = {reinterpret_cast<int *>(ws + l.head), reinterpret_cast<int *>(ws + l.assignment),
                reinterpret_cast<int *>(ws + l.place), reinterpret_cast<int *>(ws + l.column),
                reinterpret_cast<ExpertSet *>(ws + l.set), reinterpret_cast<ExpertSet *>(ws + l.tile_set)};
@@ -423,7 +468,17 @@ int qk_moe_ffn(const qk_expert_weights *gate, const qk_expert_weights *up, const
     const size_t counts = sizeof(int) * kWarps * pa.experts;
     cudaError_t e = cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(sizeof(int) * kWarps * kMaxExperts));
-    if (e == cudaSuccess) e = launch_chained(plan_kernel, dim3(1), kPlanThreads, counts, s, library_programmatic(), pa);
+    if (e == cudaSuccess) {
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(plan_blocks), cfg.blockDim = dim3(kPlanThreads), cfg.dynamicSmemBytes = counts, cfg.stream = s;
+        cudaLaunchAttribute at[2]{};
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = plan_blocks, at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[1].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = at, cfg.numAttrs = library_programmatic() ? 2 : 1;
+        e = cudaLaunchKernelEx(&cfg, plan_kernel, pa);
+    }
     if (e != cudaSuccess) return QK_ERR_CUDA;
 
     const auto pack = [&](const void *rows, int64_t ld, int type, int per_row, int64_t cols, int fmt, int64_t to, int64_t tile_to, int64_t scale) {
@@ -433,14 +488,13 @@ int qk_moe_ffn(const qk_expert_weights *gate, const qk_expert_weights *up, const
         k.cols = static_cast<int>(cols), k.units = static_cast<int>((cols + kUnit - 1) / kUnit);
         k.pieces = l.pieces, k.fmt = fmt;
         k.out = reinterpret_cast<uint8_t *>(ws + to), k.scale = reinterpret_cast<float *>(ws + scale);
-        const bool vec = multiple(rows, 4 * size_of(type)) && ld % 4 == 0;
-        cudaLaunchConfig_t cfg{};
-        cfg.gridDim = dim3(static_cast<unsigned>(l.A)), cfg.blockDim = dim3(kPackThreads), cfg.stream = s;
-        cudaLaunchAttribute at{};
-        at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        at.val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = &at, cfg.numAttrs = 1;
-        return cudaLaunchKernelEx(&cfg, pack_kernel, k, vec);
+        k.vec = multiple(rows, 4 * size_of(type)) && ld % 4 == 0, k.tokens = T;
+        // a thread block a row where rows are few, else a warp
+        const int64_t n = per_row ? T : l.A;
+        const bool wide = n <= 4LL * sms;
+        return wide ? launch_chained(pack_kernel<kPackThreads / 32>, dim3(static_cast<unsigned>(n)), kPackThreads, 0, s, true, k)
+                    : launch_chained(pack_kernel<1>, dim3(static_cast<unsigned>((n + kPackThreads / 32 - 1) / (kPackThreads / 32))),
+                                     kPackThreads, 0, s, true, k);
     };
     const auto products = [&](const Weights &a, const Weights &b, int fmt, int64_t cols, int64_t rows, bool paired,
                               int64_t ops, int64_t tile_ops, int64_t scale, int64_t to) {
@@ -474,7 +528,7 @@ int qk_moe_ffn(const qk_expert_weights *gate, const qk_expert_weights *up, const
         r.plan = pa.plan, r.a = a, r.b = b, r.fmt = fmt;
         r.cols = static_cast<int>(cols), r.units = static_cast<int>((cols + kUnit - 1) / kUnit), r.pieces = l.pieces;
         r.rows = static_cast<int>(rows), r.tiles = static_cast<int>(paired ? (rows + 7) / 8 : (rows + 15) / 16);
-        r.kw = share(std::min(l.A, n_experts) * r.tiles, r.units, sms);
+        r.sms = sms;
         r.x = reinterpret_cast<const uint8_t *>(ws + ops), r.scale = reinterpret_cast<const float *>(ws + scale);
         r.out = reinterpret_cast<float *>(ws + to);
         return rows_launch(r, paired, sms, s);

@@ -57,6 +57,8 @@ struct PackArgs {
     const void *x;
     int64_t ld;
     int type, top_k;          // row of a place: x[assignment / top_k], or x[place] where top_k == 0
+    int64_t tokens;
+    bool vec;                 // rows start on four values
     int cols, units, pieces, fmt;
     uint8_t *out;
     __half *tile_out;         // rows of the tile sets, hi pieces [place][tile_cols]; lo ones tile_lo further
@@ -70,7 +72,7 @@ struct RowsArgs {
     Weights a, b;             // gate and up; or down twice
     int fmt, cols, units, pieces;
     int rows, tiles;          // output columns and 16-row tiles (8 + 8 where gate and up are paired)
-    int kw;                   // warps that share a tile's units
+    int sms;
     const uint8_t *x;         // operands, octet after octet
     const float *scale;
     float *out;               // [place][rows]

@@ -278,7 +278,7 @@ __device__ __forceinline__ void tile_products(float (&total)[NT][4], const RowsA
 }
 
 template <int FMT, int P, bool PAIRED, int NT>
-__device__ __forceinline__ void set_tile(const RowsArgs &a, const ExpertSet &s, int tile, int part, uint32_t ring,
+__device__ __forceinline__ void set_tile(const RowsArgs &a, const ExpertSet &s, int tile, int part, int kw, uint32_t ring,
                                          float *join, int lane, int warp)
 {
     const int g = lane >> 2, c = lane & 3, r = lane >> 1;
@@ -296,10 +296,10 @@ __device__ __forceinline__ void set_tile(const RowsArgs &a, const ExpertSet &s, 
         };
         const uint32_t al[2] = {static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row_of(g)) & 15),
                                 static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row_of(g + 8)) & 15)};
-        const int u0 = a.units * part / a.kw, u1 = a.units * (part + 1) / a.kw;
+        const int u0 = a.units * part / kw, u1 = a.units * (part + 1) / kw;
         tile_products<FMT, P, NT>(total, a, row_of(r), al, ring, u0, u1, s.octet, lane);
     }
-    if (a.kw > 1) {
+    if (kw > 1) {
         // parts of a tile, added in their order
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -307,7 +307,7 @@ __device__ __forceinline__ void set_tile(const RowsArgs &a, const ExpertSet &s, 
             for (int j = 0; j < 4; ++j) join[((warp * NT + n) * 4 + j) * 32 + lane] = total[n][j];
         __syncthreads();
         if (part == 0)
-            for (int k = 1; k < a.kw; ++k)
+            for (int k = 1; k < kw; ++k)
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -345,14 +345,18 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2) rows_kernel(const RowsArgs 
     const uint32_t ring = smem_u32(smem) + warp * ring_stages(FMT) * 16 * row_pitch(FMT);
     let_next_start();
     wait_for_previous();
-    const int per = kRowWarps / a.kw, blocks = (a.tiles + per - 1) / per;
-    const int64_t items = static_cast<int64_t>(a.plan.head[0]) * blocks;
+    // warps that share a tile's units: enough for every SM's 16 warps to have work where tiles are few
+    const int64_t sets = a.plan.head[0];
+    int kw = 1;
+    while (kw < kRowWarps && 2 * kw <= a.units && sets * a.tiles * kw < 16 * a.sms) kw *= 2;
+    const int per = kRowWarps / kw, blocks = (a.tiles + per - 1) / per;
+    const int64_t items = sets * blocks;
     for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
         const ExpertSet s = a.plan.sets[i / blocks];
-        const int tile = static_cast<int>(i % blocks) * per + warp / a.kw, part = warp % a.kw;
-        if (s.count <= 8) set_tile<FMT, P, PAIRED, 1>(a, s, tile, part, ring, join, lane, warp);
-        else if (s.count <= 16) set_tile<FMT, P, PAIRED, 2>(a, s, tile, part, ring, join, lane, warp);
-        else set_tile<FMT, P, PAIRED, 4>(a, s, tile, part, ring, join, lane, warp);
+        const int tile = static_cast<int>(i % blocks) * per + warp / kw, part = warp % kw;
+        if (s.count <= 8) set_tile<FMT, P, PAIRED, 1>(a, s, tile, part, kw, ring, join, lane, warp);
+        else if (s.count <= 16) set_tile<FMT, P, PAIRED, 2>(a, s, tile, part, kw, ring, join, lane, warp);
+        else set_tile<FMT, P, PAIRED, 4>(a, s, tile, part, kw, ring, join, lane, warp);
     }
 }
 
