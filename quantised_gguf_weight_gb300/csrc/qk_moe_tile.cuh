@@ -29,9 +29,8 @@ namespace moe {
 
 constexpr int kDeqWarp = 4, kDeqGroups = 2, kEpiWarp = 12;   // first warps of the roles
 constexpr int kFlush = 4;                                    // stages whose products one accumulator takes, with fp32 accuracy
-// Output warps: with fp32 accuracy two threads share a row, whose sums they keep.
-__host__ __device__ constexpr int tile_epi_warps(int PB) { return PB == 2 ? 8 : 4; }
-__host__ __device__ constexpr int tile_threads(int PB) { return 32 * (kEpiWarp + tile_epi_warps(PB)); }
+constexpr int kEpiWarps = 8;                                 // two threads share a row's tokens
+constexpr int kTileThreads = 32 * (kEpiWarp + kEpiWarps);
 constexpr int kStages = 4;                                   // of both operands
 constexpr int kMaxN = 128;                                   // tokens of a set
 // Columns of a stage: eight products for each (a wait costs the issuing warp as much as three of them).
@@ -42,6 +41,7 @@ __host__ __device__ constexpr int tile_smem(int PA, int PB) { return kStages * t
 struct TileShared {
     uint64_t full[kStages], empty_b[kStages], empty_a[kStages], acc_full[2], acc_empty[2], rs_full[2], rs_empty[2];
     float row_scale[2][128];                                 // 2^s of the rows
+    float token_scale[kEpiWarps][64];                        // 2^-e of a warp's tokens
     uint32_t tmem;
     int abort;
 };
@@ -282,10 +282,10 @@ __device__ __forceinline__ void take_apart(Pieces<PA> &o, const Raw<FMT, KC> &r,
 }
 
 template <int FMT, int PA, int PB, bool PAIRED>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(tile_threads(PB), 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
 tile_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ CUtensorMap map_lo, const TileArgs a)
 {
-    constexpr int KC = tile_cols_of_stage(PA), kStage = tile_b_bytes(PA, PB), kEpiWarps = tile_epi_warps(PB);
+    constexpr int KC = tile_cols_of_stage(PA), kStage = tile_b_bytes(PA, PB);
     constexpr uint32_t kACols = KC / 2 * PA, kA0 = 2 * kMaxN;         // tensor-memory columns of a stage of A, and of the first
     static_assert(kA0 + kStages * kACols == 512, "all of tensor memory");
     extern __shared__ uint8_t raw_smem[];
@@ -470,29 +470,39 @@ tile_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
             const ExpertSet s = set_of(item);
             const int tile = tile_of(item);
             float back = 0.0f;
-            // 32 tokens' sums of this thread's row, from token c0 on
+            // a warp's 64 tokens from c_first on
+            const int c_first = part * 64;
+            float *ts = sh.token_scale[warp - kEpiWarp];
+#pragma unroll
+            for (int j = lane; j < 64; j += 32) ts[j] = c_first + j < s.count ? a.scale[s.first + c_first + j] : 0.0f;
+            __syncwarp();
+            // 32 tokens' sums of this thread's row, from the warp's token c0 on
             const auto emit = [&](const uint32_t (&v)[32], int c0) {
-                const float ts = c0 + lane < s.count ? a.scale[s.first + c0 + lane] : 0.0f;
+                const int left = s.count - c_first - c0;
+                const float *t = ts + c0;
                 if constexpr (PAIRED) {
                     const int p = tile * 64 + quarter * 16 + (lane & 15);
                     const bool low = lane < 16;
+                    float *out = a.out + static_cast<int64_t>(s.first + c_first + c0 + !low) * a.rows + p;
+                    const int64_t next = 2 * static_cast<int64_t>(a.rows);
+                    const int mine = p < a.rows ? left - !low : 0;
 #pragma unroll
                     for (int j = 0; j < 32; j += 2) {
                         // this half of the warp keeps one token of two and gets its other row's sum
                         const float keep = __uint_as_float(low ? v[j] : v[j + 1]) * back, give = __uint_as_float(low ? v[j + 1] : v[j]) * back;
-                        const float got = __shfl_xor_sync(~0u, give, 16);
-                        const float t0 = __shfl_sync(~0u, ts, j), t1 = __shfl_sync(~0u, ts, j + 1), t = low ? t0 : t1;
-                        const int col = c0 + j + !low;
-                        if (col < s.count && p < a.rows)
-                            a.out[static_cast<int64_t>(s.first + col) * a.rows + p] = silu((low ? keep : got) * t) * ((low ? got : keep) * t);
+                        const float got = __shfl_xor_sync(~0u, give, 16), tj = t[j + !low];
+                        const float h = silu((low ? keep : got) * tj) * ((low ? got : keep) * tj);
+                        if (j < mine) *out = h;
+                        out += next;
                     }
                 } else {
                     const int p = tile * 128 + row;
+                    float *out = a.out + static_cast<int64_t>(s.first + c_first + c0) * a.rows + p;
+                    const int mine = p < a.rows ? left : 0;
 #pragma unroll
                     for (int j = 0; j < 32; ++j) {
-                        const float t = __shfl_sync(~0u, ts, j);
-                        if (c0 + j < s.count && p < a.rows)
-                            a.out[static_cast<int64_t>(s.first + c0 + j) * a.rows + p] = __uint_as_float(v[j]) * back * t;
+                        if (j < mine) *out = __uint_as_float(v[j]) * back * t[j];
+                        out += a.rows;
                     }
                 }
             };
@@ -518,9 +528,9 @@ tile_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
                     if (!ready()) break;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        if (part * 64 + h * 32 >= s.count) continue;
+                        if (c_first + h * 32 >= s.count) continue;
                         uint32_t v[32];
-                        tmem_ld_32x32b_x32(taddr + lanes + (q & 1) * kMaxN + part * 64 + h * 32, v);
+                        tmem_ld_32x32b_x32(taddr + lanes + (q & 1) * kMaxN + c_first + h * 32, v);
                         tmem_ld_wait();
 #pragma unroll
                         for (int j = 0; j < 32; ++j) sum[h][j] += __uint_as_float(v[j]);
@@ -530,17 +540,18 @@ tile_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
                 if (!ok) break;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    if (part * 64 + h * 32 >= s.count) continue;
+                    if (c_first + h * 32 >= s.count) continue;
                     uint32_t v[32];
 #pragma unroll
                     for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(sum[h][j]);
-                    emit(v, part * 64 + h * 32);
+                    emit(v, h * 32);
                 }
             } else {
                 if (!ready()) break;
-                for (int c0 = 0; c0 < s.count; c0 += 32) {
+#pragma unroll 1
+                for (int c0 = 0; c0 < 64 && c_first + c0 < s.count; c0 += 32) {
                     uint32_t v[32];
-                    tmem_ld_32x32b_x32(taddr + lanes + (q & 1) * kMaxN + c0, v);
+                    tmem_ld_32x32b_x32(taddr + lanes + (q & 1) * kMaxN + c_first + c0, v);
                     tmem_ld_wait();
                     emit(v, c0);
                 }
@@ -562,7 +573,7 @@ cudaError_t tile_launch_as(const CUtensorMap &hi, const CUtensorMap &lo, const T
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, tile_smem(PA, PB));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(sms / 2 * 2)), cfg.blockDim = dim3(tile_threads(PB));
+    cfg.gridDim = dim3(static_cast<unsigned>(sms / 2 * 2)), cfg.blockDim = dim3(kTileThreads);
     cfg.dynamicSmemBytes = tile_smem(PA, PB), cfg.stream = st;
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
