@@ -117,9 +117,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a)
         }
     }
     const bool tiled = n >= a.tile_from;
-    // tile sets as even as 16 tokens allow, none of them empty
+    // tile sets as even as 32 tokens allow, none of them empty
     const int parts = (n + a.tile_tokens - 1) / a.tile_tokens;
-    const int per = tiled ? ((n + parts - 1) / parts + 15) / 16 * 16 : 1;
+    const int per = tiled ? ((n + parts - 1) / parts + 31) / 32 * 32 : 1;
     const int rows_n = tiled ? 0 : n, tile_n = tiled ? (n + per - 1) / per : 0;
     int4 all;
     const int4 at = scan_before(make_int4(n, (rows_n + 7) / 8, (rows_n + 8 * kSetOctets - 1) / (8 * kSetOctets), tile_n), warp_sums, all);
@@ -394,7 +394,7 @@ int check_weights(const qk_expert_weights *w, int64_t E, int64_t rows, int64_t c
     if (w->row_offset < 0 || per < rows) return QK_ERR_BAD_DIM;
     if (strict_blocks_reject(w->format, cols)) return QK_ERR_BAD_DIM;
     const int64_t rb = row_bytes_of(w->format, cols);
-    if (per > INT32_MAX || w->row_offset > INT64_MAX / rb - E * per) return QK_ERR_TOO_LARGE;
+    if (per > INT32_MAX / E || w->row_offset > INT64_MAX / rb - E * per) return QK_ERR_TOO_LARGE;
     if (!multiple(w->w, w->format == kFmtQ4K ? 16 : 2)) return QK_ERR_ALIGN;
     *out = {static_cast<const uint8_t *>(w->w) + w->row_offset * rb, per, rb};
     return QK_OK;
@@ -499,29 +499,17 @@ int qk_moe_ffn(const qk_expert_weights *gate, const qk_expert_weights *up, const
     const auto products = [&](const Weights &a, const Weights &b, int fmt, int64_t cols, int64_t rows, bool paired,
                               int64_t ops, int64_t tile_ops, int64_t scale, int64_t to) {
         if (l.tiled) {
-            // rows [A][tile_cols] of fp16 as boxes of 64 columns and kBoxRows rows
-            CUtensorMap map[2];
             const int64_t wide = tile_cols(cols);
-            for (int i = 0; i < l.pieces; ++i) {
-                const cuuint64_t dims[2] = {static_cast<cuuint64_t>(wide), static_cast<cuuint64_t>(l.A)};
-                const cuuint64_t strides[1] = {static_cast<cuuint64_t>(2 * wide)};
-                const cuuint32_t box[2] = {64, kTileBoxRows}, one[2] = {1, 1};
-                const gemm::EncodeTiledFn enc = gemm::encode_fn();
-                if (!enc || enc(&map[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, ws + tile_ops + i * 2 * l.A * wide, dims, strides, box, one,
-                                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-                    return cudaErrorInvalidValue;
-            }
-            if (l.pieces == 1) map[1] = map[0];
+            const TileOperands o = {ws + tile_ops, ws + tile_ops + 2 * l.A * wide, l.A, wide};
             TileArgs t{};
-            t.plan = pa.plan, t.a = a, t.b = b, t.fmt = fmt, t.cols = static_cast<int>(cols), t.chunks = static_cast<int>(wide / (l.w_pieces == 1 ? 128 : 64));
+            t.plan = pa.plan, t.a = a, t.b = b, t.experts = n_experts, t.fmt = fmt, t.cols = static_cast<int>(cols), t.chunks = static_cast<int>(wide / (l.w_pieces == 1 ? 128 : 64));
             t.pieces = l.pieces, t.w_pieces = l.w_pieces, t.rows = static_cast<int>(rows);
             t.tiles = static_cast<int>(paired ? (rows + 63) / 64 : (rows + 127) / 128);
             t.scale = reinterpret_cast<const float *>(ws + scale), t.out = reinterpret_cast<float *>(ws + to);
             t.skip_chunk = g_skip_chunk.load(), t.wait_ns = library_wait_limit_ns(), t.err = err;
-            const cudaError_t e = fmt == kFmtQ4K ? tile_launch_q4k(map[0], map[1], t, paired, sms, s)
-                                : fmt == kFmtQ80 ? tile_launch_q80(map[0], map[1], t, paired, sms, s)
-                                                 : tile_launch_q6k(map[0], map[1], t, paired, sms, s);
+            const cudaError_t e = fmt == kFmtQ4K ? tile_launch_q4k(o, t, paired, sms, s)
+                                : fmt == kFmtQ80 ? tile_launch_q80(o, t, paired, sms, s)
+                                                 : tile_launch_q6k(o, t, paired, sms, s);
             if (e != cudaSuccess) return e;
         }
         RowsArgs r{};

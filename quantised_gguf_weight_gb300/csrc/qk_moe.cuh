@@ -81,13 +81,20 @@ struct RowsArgs {
 struct TileArgs {
     Plan plan;
     Weights a, b;             // as above
-    int fmt, cols, chunks, pieces, w_pieces;
+    int64_t experts;
+    int fmt, cols, chunks, pieces, w_pieces;      // chunks: stages of a row
     int rows, tiles;          // output columns and 128-row tiles (64 + 64 where paired)
     const float *scale;
     float *out;
     int skip_chunk;           // test hook: the first cluster never loads this chunk of its (-1: none)
     uint64_t wait_ns;
     int *err;
+};
+
+// The tokens' operands: rows [rows][cols] of fp16 pieces.
+struct TileOperands {
+    const void *hi, *lo;
+    int64_t rows, cols;
 };
 
 __host__ __device__ constexpr int64_t octet_unit_bytes(int fmt, int pieces)
@@ -103,9 +110,9 @@ __host__ __device__ inline int64_t row_bytes_of(int fmt, int64_t K)
 cudaError_t rows_launch_q4k(const RowsArgs &a, bool paired, int sms, cudaStream_t st);
 cudaError_t rows_launch_q80(const RowsArgs &a, bool paired, int sms, cudaStream_t st);
 cudaError_t rows_launch_q6k(const RowsArgs &a, bool paired, int sms, cudaStream_t st);
-cudaError_t tile_launch_q4k(const CUtensorMap &hi, const CUtensorMap &lo, const TileArgs &a, bool paired, int sms, cudaStream_t st);
-cudaError_t tile_launch_q80(const CUtensorMap &hi, const CUtensorMap &lo, const TileArgs &a, bool paired, int sms, cudaStream_t st);
-cudaError_t tile_launch_q6k(const CUtensorMap &hi, const CUtensorMap &lo, const TileArgs &a, bool paired, int sms, cudaStream_t st);
+cudaError_t tile_launch_q4k(const TileOperands &t, const TileArgs &a, bool paired, int sms, cudaStream_t st);
+cudaError_t tile_launch_q80(const TileOperands &t, const TileArgs &a, bool paired, int sms, cudaStream_t st);
+cudaError_t tile_launch_q6k(const TileOperands &t, const TileArgs &a, bool paired, int sms, cudaStream_t st);
 
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }

@@ -1,13 +1,14 @@
 // qk_moe_tile.cuh -- the experts' products for many tokens an expert: tiles of
 // 128 weight rows x up to 128 tokens on the tcgen05 tensor cores.
 //
-// A thread block keeps going over its items.  Its warps have roles: two groups
-// of four take the weights apart, a thread a row, and leave them as the A
-// operand in tensor memory; a thread issues the products; a thread fetches the
-// tokens' operands by TMA, half of them each of two neighbouring blocks for
-// both (they have the same tokens and neighbouring rows); four warps turn
-// finished accumulators into outputs while the next item's products run; two
-// look over the next item's rows for their largest scale.
+// Pairs of thread blocks keep going over their items; a product (cta_group::2)
+// is 256 rows, half of them each block's, x the set's tokens, half of which each
+// block holds.  A block's warps have roles: groups of four take the weights
+// apart, a thread a row, and leave them as the A operand in tensor memory; one
+// issues the pair's products (in the even block); one fetches the tokens'
+// operands, and Q4_K's bytes, by TMA; eight turn finished accumulators into
+// outputs while the next item's products run; two look over the next item's
+// rows for their largest scale.
 //
 // Weights are fp16 after a power of two a row that puts the largest value that
 // the row's scales allow into [2^14, 2^15): one rounding (Q4_K: the minimum's
@@ -15,10 +16,11 @@
 // such pieces, and fp32 activations too (qk_moe.cuh); the product of the two
 // low pieces is left out.
 //
-// Why A is in tensor memory: a product of 128 x 128 x 16 takes 64 cycles, in which
-// shared memory moves 8 KB; the tokens' operand alone is 4 KB written and 4 KB
-// read.  From shared memory (measured) a product of 192 tokens takes 145 cycles
-// where one from tensor memory takes 100.
+// Why A is in tensor memory and the tokens are shared: a product of 128 x 128 x
+// 16 takes 64 cycles, in which shared memory moves 8 KB.  One block's tokens
+// alone would be 4 KB written and 4 KB read, and A as much again (from shared
+// memory, measured, a product of 192 tokens takes 145 cycles where one from
+// tensor memory takes 100); half of the tokens leaves room.
 #pragma once
 
 #include "qk_moe.cuh"
@@ -27,32 +29,44 @@
 namespace qk {
 namespace moe {
 
-constexpr int kDeqWarp = 4, kDeqGroups = 2, kEpiWarp = 12;   // first warps of the roles
+constexpr int kDeqWarp = 4;                                  // first warp that takes weights apart
 constexpr int kFlush = 4;                                    // stages whose products one accumulator takes, with fp32 accuracy
 constexpr int kEpiWarps = 8;                                 // two threads share a row's tokens
-constexpr int kTileThreads = 32 * (kEpiWarp + kEpiWarps);
+// Groups of four warps that take weights apart.  More than two need the registers that fp32 sums, or bytes fetched a
+// stage ahead by the threads themselves (all formats but Q4_K), take.
+__host__ __device__ constexpr int tile_groups(int FMT, int PB) { return FMT == kFmtQ4K && PB == 1 ? 3 : 2; }
+__host__ __device__ constexpr int tile_epi_warp(int FMT, int PB) { return kDeqWarp + 4 * tile_groups(FMT, PB); }
+__host__ __device__ constexpr int tile_threads(int FMT, int PB) { return 32 * (tile_epi_warp(FMT, PB) + kEpiWarps); }
 constexpr int kStages = 4;                                   // of both operands
 constexpr int kMaxN = 128;                                   // tokens of a set
 // Columns of a stage: eight products for each (a wait costs the issuing warp as much as three of them).
 __host__ __device__ constexpr int tile_cols_of_stage(int PA) { return PA == 1 ? 128 : 64; }
-__host__ __device__ constexpr int tile_b_bytes(int PA, int PB) { return kMaxN * 2 * tile_cols_of_stage(PA) * PB; }
-__host__ __device__ constexpr int tile_smem(int PA, int PB) { return kStages * tile_b_bytes(PA, PB) + 1024; }
+__host__ __device__ constexpr int tile_b_bytes(int PA, int PB) { return kMaxN / 2 * 2 * tile_cols_of_stage(PA) * PB; }
+// Q4_K's bytes of a stage: [128 rows] of half its columns' number, and of 16 for the scales.
+__host__ __device__ constexpr int tile_raw_bytes(int FMT, int PA) { return FMT == kFmtQ4K ? 128 * (tile_cols_of_stage(PA) / 2 + 16) : 0; }
+__host__ __device__ constexpr int tile_smem(int FMT, int PA, int PB)
+{
+    return kStages * (tile_b_bytes(PA, PB) + tile_raw_bytes(FMT, PA)) + 1024;
+}
 
 struct TileShared {
-    uint64_t full[kStages], empty_b[kStages], empty_a[kStages], acc_full[2], acc_empty[2], rs_full[2], rs_empty[2];
+    uint64_t full[kStages], empty[kStages], raw_full[kStages], raw_empty[kStages], acc_full[2], acc_empty[2], rs_full[2], rs_empty[2];
     float row_scale[2][128];                                 // 2^s of the rows
     float token_scale[kEpiWarps][64];                        // 2^-e of a warp's tokens
     uint32_t tmem;
     int abort;
 };
 
-// A bounded wait; one that runs out ends every other of the block.
+// A bounded wait; one that runs out ends every other of the block.  POLL: without sleeping, and for arrivals from the
+// other block.
+template <bool POLL = false>
 __device__ __forceinline__ bool tile_wait(uint32_t bar, uint32_t parity, const TileArgs &a, volatile int *abort)
 {
-    if (mbar_try_wait(bar, parity)) return true;
+    const auto test = [&]() { return POLL ? mbar_test(bar, parity) : mbar_try_wait(bar, parity); };
+    if (test()) return true;
     const uint64_t deadline = globaltimer_ns() + a.wait_ns;
     for (uint32_t i = 1; !*abort; ++i) {
-        if (mbar_try_wait(bar, parity)) return true;
+        if (test()) return true;
         if ((i & 31u) == 0 && globaltimer_ns() > deadline) {
             *abort = 1;
             record_error(a.err, kErrTimeout);
@@ -60,9 +74,10 @@ __device__ __forceinline__ bool tile_wait(uint32_t bar, uint32_t parity, const T
     }
     return false;
 }
+template <bool POLL = false>
 __device__ __forceinline__ bool tile_wait_warp(uint32_t bar, uint32_t parity, const TileArgs &a, volatile int *abort)
 {
-    return __all_sync(~0u, tile_wait(bar, parity, a, abort));
+    return __all_sync(~0u, tile_wait<POLL>(bar, parity, a, abort));
 }
 
 // One lane of the (converged) warp is elected.
@@ -73,21 +88,14 @@ __device__ __forceinline__ bool elect_one()
     return r != 0;
 }
 
-__device__ __forceinline__ void tma_load_2d_both(uint32_t dst, const CUtensorMap *m, int32_t x, int32_t y, uint32_t bar,
-                                                 uint64_t policy)
+// D[tmem of both blocks] (+)= A[tmem of both] * B^T, M = 256.
+__device__ __forceinline__ void tc_mma_f16_tmem_a_pair(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate)
 {
     asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster.L2::cache_hint"
-        " [%0], [%1, {%2, %3}], [%4], %5, %6;" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(bar), "h"(static_cast<uint16_t>(3)), "l"(policy)
-        : "memory");
-}
-// Arrive once on the mbarrier at `bar` of both blocks when every product issued so far by this thread has completed.
-__device__ __forceinline__ void tc_commit_both(uint32_t bar)
-{
-    asm volatile(
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-        "h"(static_cast<uint16_t>(3))
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
 
@@ -281,36 +289,44 @@ __device__ __forceinline__ void take_apart(Pieces<PA> &o, const Raw<FMT, KC> &r,
     }
 }
 
+struct TileMaps {
+    CUtensorMap hi, lo;              // the tokens' operands
+    CUtensorMap wa, wb, ha, hb;      // Q4_K: nibbles and scales of a's and b's rows
+};
+
 template <int FMT, int PA, int PB, bool PAIRED>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
-tile_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ CUtensorMap map_lo, const TileArgs a)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(tile_threads(FMT, PB), 1)
+tile_kernel(const __grid_constant__ TileMaps maps, const TileArgs a)
 {
-    constexpr int KC = tile_cols_of_stage(PA), kStage = tile_b_bytes(PA, PB);
+    constexpr int KC = tile_cols_of_stage(PA), kStage = tile_b_bytes(PA, PB), kRaw = tile_raw_bytes(FMT, PA);
+    constexpr int kGroups = tile_groups(FMT, PB), kEpiWarp = tile_epi_warp(FMT, PB);
+    constexpr bool kCopied = FMT == kFmtQ4K;                 // the weights' bytes come by TMA
     constexpr uint32_t kACols = KC / 2 * PA, kA0 = 2 * kMaxN;         // tensor-memory columns of a stage of A, and of the first
     static_assert(kA0 + kStages * kACols == 512, "all of tensor memory");
     extern __shared__ uint8_t raw_smem[];
     __shared__ TileShared sh;
-    const uint32_t b_base = (smem_u32(raw_smem) + 1023u) & ~1023u;
+    const uint32_t b_base = (smem_u32(raw_smem) + 1023u) & ~1023u, raw_base = b_base + kStages * kStage;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = static_cast<int>(cluster_ctarank());
     volatile int *abort = &sh.abort;
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(smem_u32(&sh.full[i]), 5);                     // a group's four warps, and the copies
-            mbar_init(smem_u32(&sh.empty_b[i]), 2), mbar_init(smem_u32(&sh.empty_a[i]), 1);
+            mbar_init(smem_u32(&sh.full[i]), 9);             // (even block) a group's four warps of each block, and the copies
+            mbar_init(smem_u32(&sh.empty[i]), 1), mbar_init(smem_u32(&sh.raw_full[i]), 1), mbar_init(smem_u32(&sh.raw_empty[i]), 4);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&sh.acc_full[i]), 1), mbar_init(smem_u32(&sh.acc_empty[i]), kEpiWarps);
+            mbar_init(smem_u32(&sh.acc_full[i]), 1), mbar_init(smem_u32(&sh.acc_empty[i]), 2 * kEpiWarps);
             mbar_init(smem_u32(&sh.rs_full[i]), 2), mbar_init(smem_u32(&sh.rs_empty[i]), kEpiWarps);
         }
         sh.abort = 0;
         fence_barrier_init();
-        tma_prefetch_desc(&map_hi);
-        if (PB == 2) tma_prefetch_desc(&map_lo);
+        tma_prefetch_desc(&maps.hi);
+        if (PB == 2) tma_prefetch_desc(&maps.lo);
+        if (kCopied) tma_prefetch_desc(&maps.wa), tma_prefetch_desc(&maps.wb), tma_prefetch_desc(&maps.ha), tma_prefetch_desc(&maps.hb);
     }
     if (warp == 1) {
-        tmem_alloc_1(smem_u32(&sh.tmem), 512);
-        tmem_relinquish_1();
+        tmem_alloc_pair(smem_u32(&sh.tmem), 512);
+        tmem_relinquish_pair();
     }
     let_next_start();
     tc_fence_before();
@@ -325,52 +341,97 @@ tile_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
     const int per = PB == 2 ? kFlush : nk;                     // stages an accumulator takes
     const auto set_of = [&](int64_t item) { return a.plan.tile_sets[item / pairs]; };
     const auto tile_of = [&](int64_t item) { return static_cast<int>(item % pairs) * 2 + rank; };
+    const auto columns_of = [](int count) { return (count + 31) / 32 * 32; };       // of a product: a pair's are multiples of 32
+    // an arrival on a barrier of the even block
+    const auto arrive_even = [&](uint64_t *bar) {
+        if (rank == 0) mbar_arrive(smem_u32(bar));
+        else mbar_arrive_remote(mapa_shared(smem_u32(bar), 0));
+    };
 
     if (warp == 0) {
         if (lane == 0) {
-            const uint64_t keep = l2_evict_last_policy();
-            int n = 0;
+            const uint64_t keep = l2_evict_last_policy(), once = l2_evict_first_policy();
+            int n = 0, nr = 0;
             bool ok = true;
+            // the weights' bytes run ahead of the tokens by as much as their own barriers allow
+            int64_t raw_item = first;
+            int raw_c = 0;
+            const auto weights = [&]() {
+                if (!kCopied || raw_item >= items) return;
+                const int st = nr % kStages;
+                if (nr >= kStages && !mbar_test(smem_u32(&sh.raw_empty[st]), (nr / kStages - 1) & 1)) return;
+                const uint32_t bar = smem_u32(&sh.raw_full[st]), to = raw_base + st * kRaw;
+                mbar_arrive_expect_tx(bar, kRaw);
+                const int e = set_of(raw_item).expert, tile = tile_of(raw_item), pair = raw_c * (KC / 64);
+                const int r0 = static_cast<int>(e * a.a.expert_rows) + tile * (PAIRED ? 64 : 128);
+                const int r1 = PAIRED ? static_cast<int>(e * a.b.expert_rows) + tile * 64 : r0 + 64;
+                const int at = 144 * (pair >> 2);
+                tma_load_2d(to, &maps.wa, at + 16 + 32 * (pair & 3), r0, bar, once);
+                tma_load_2d(to + 64 * (KC / 2), &maps.wb, at + 16 + 32 * (pair & 3), r1, bar, once);
+                tma_load_2d(to + 128 * (KC / 2), &maps.ha, at, r0, bar, once);
+                tma_load_2d(to + 128 * (KC / 2) + 64 * 16, &maps.hb, at, r1, bar, once);
+                ++nr;
+                if (++raw_c == nk) raw_c = 0, raw_item += step;
+            };
             for (int64_t item = first; item < items && ok; item += step) {
                 const ExpertSet s = set_of(item);
-                const int boxes = (s.count + kTileBoxRows - 1) / kTileBoxRows;
+                const int cols = columns_of(s.count), boxes = (cols / 2 + kTileBoxRows - 1) / kTileBoxRows;
+                const int y = s.first + rank * (cols / 2);
                 for (int c = 0; c < nk; ++c, ++n) {
                     const int st = n % kStages;
-                    if (n >= kStages && !tile_wait(smem_u32(&sh.empty_b[st]), (n / kStages - 1) & 1, a, abort)) {
-                        ok = false;
-                        break;
+                    weights();
+                    if (n >= kStages) {
+                        // a bounded wait in which weights go on
+                        uint64_t since = 0;
+                        while (!mbar_test(smem_u32(&sh.empty[st]), (n / kStages - 1) & 1)) {
+                            weights();
+                            const uint64_t now = globaltimer_ns();
+                            if (since == 0) since = now;
+                            if (*abort || now - since > a.wait_ns) {
+                                if (!*abort) record_error(a.err, kErrTimeout);
+                                *abort = 1;
+                                ok = false;
+                                break;
+                            }
+                        }
+                        if (!ok) break;
                     }
                     const uint32_t full = smem_u32(&sh.full[st]), to = b_base + st * kStage;
-                    mbar_arrive_expect_tx(full, boxes * kTileBoxRows * 2 * KC * PB);
+                    if (rank == 0) mbar_arrive_expect_tx(full, 2 * boxes * kTileBoxRows * 2 * KC * PB);
                     if (a.skip_chunk >= 0 && n == a.skip_chunk && blockIdx.x < 2) continue;     // test hook
-                    for (int b = rank; b < boxes; b += 2)
+                    const uint32_t full0 = rank == 0 ? full : mapa_shared(full, 0);
+                    for (int b = 0; b < boxes; ++b)
 #pragma unroll
                         for (int k = 0; k < KC / 64; ++k) {
-                            const uint32_t at = to + k * (kMaxN * 128) + b * (kTileBoxRows * 128);
-                            tma_load_2d_both(at, &map_hi, c * KC + k * 64, s.first + b * kTileBoxRows, full, keep);
-                            if (PB == 2)
-                                tma_load_2d_both(at + kStage / 2, &map_lo, c * KC + k * 64, s.first + b * kTileBoxRows, full, keep);
+                            const uint32_t at = to + k * (kMaxN / 2 * 128) + b * (kTileBoxRows * 128);
+                            tma_load_2d_peer(at, &maps.hi, c * KC + k * 64, y + b * kTileBoxRows, full0, keep);
+                            if (PB == 2) tma_load_2d_peer(at + kStage / 2, &maps.lo, c * KC + k * 64, y + b * kTileBoxRows, full0, keep);
                         }
                 }
             }
-            // every copy that this block has asked for lands before it leaves (the other's, too: the closing barrier)
-            for (int t = max(0, n - kStages); t < n; ++t) mbar_wait(smem_u32(&sh.full[t % kStages]), (t / kStages) & 1, a.wait_ns);
+            for (const uint64_t since = globaltimer_ns(); ok && kCopied && nr < n && !*abort;) {
+                weights();
+                if (globaltimer_ns() - since > a.wait_ns) record_error(a.err, kErrTimeout), *abort = 1;
+            }
+            // every copy lands before the blocks leave: the tokens of both on the even block's barriers, and this one's weights
+            if (rank == 0)
+                for (int t = max(0, n - kStages); t < n; ++t) mbar_wait(smem_u32(&sh.full[t % kStages]), (t / kStages) & 1, a.wait_ns);
+            for (int t = max(0, nr - kStages); t < nr; ++t) mbar_wait(smem_u32(&sh.raw_full[t % kStages]), (t / kStages) & 1, a.wait_ns);
         }
         __syncwarp();
     } else if (warp == 1) {
         // The warp stays together and elects a lane for each product: a thread of a branch of its own takes 118 cycles a
         // product whatever its size (measured), an elected one N / 2.
         int n = 0, q = 0;                                      // stages and accumulators so far
-        bool ok = true;
+        bool ok = rank == 0;
         const uint64_t desc0 = smem_desc_sw128_kmajor(b_base);
         for (int64_t item = first; item < items && ok; item += step) {
-            const int count = set_of(item).count;
-            const uint32_t idesc = idesc_f16_f32(128, (count + 15) / 16 * 16);
+            const uint32_t idesc = idesc_f16_f32(256, columns_of(set_of(item).count));
             for (int c = 0; c < nk; ++c, ++n) {
                 const int st = n % kStages, buf = q & 1;
                 const bool fresh = c % per == 0, last = c + 1 == nk || (c + 1) % per == 0;
-                if ((fresh && q >= 2 && !tile_wait_warp(smem_u32(&sh.acc_empty[buf]), (q / 2 - 1) & 1, a, abort)) ||
-                    !tile_wait_warp(smem_u32(&sh.full[st]), (n / kStages) & 1, a, abort)) {
+                if ((fresh && q >= 2 && !tile_wait_warp<true>(smem_u32(&sh.acc_empty[buf]), (q / 2 - 1) & 1, a, abort)) ||
+                    !tile_wait_warp<true>(smem_u32(&sh.full[st]), (n / kStages) & 1, a, abort)) {
                     ok = false;
                     break;
                 }
@@ -380,22 +441,19 @@ tile_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
                 if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < KC / 16; ++k) {
-                        const uint64_t bk = b + (k >> 2) * (kMaxN * 128 >> 4) + 2 * (k & 3);
-                        tc_mma_f16_tmem_a(d, at + 8 * k, bk, idesc, !fresh || k > 0);
-                        if constexpr (PA == 2) tc_mma_f16_tmem_a(d, at + KC / 2 + 8 * k, bk, idesc, 1);
-                        if constexpr (PB == 2) tc_mma_f16_tmem_a(d, at + 8 * k, bk + (kStage >> 5), idesc, 1);
+                        const uint64_t bk = b + (k >> 2) * (kMaxN / 2 * 128 >> 4) + 2 * (k & 3);
+                        tc_mma_f16_tmem_a_pair(d, at + 8 * k, bk, idesc, !fresh || k > 0);
+                        if constexpr (PA == 2) tc_mma_f16_tmem_a_pair(d, at + KC / 2 + 8 * k, bk, idesc, 1);
+                        if constexpr (PB == 2) tc_mma_f16_tmem_a_pair(d, at + 8 * k, bk + (kStage >> 5), idesc, 1);
                     }
-                    tc_commit_1(smem_u32(&sh.empty_a[st]));
-                    tc_commit_both(smem_u32(&sh.empty_b[st]));
-                    if (last) tc_commit_1(smem_u32(&sh.acc_full[buf]));
+                    tc_commit_pair(smem_u32(&sh.empty[st]), 3);
+                    if (last) tc_commit_pair(smem_u32(&sh.acc_full[buf]), 3);
                 }
                 if (last) ++q;
             }
         }
-        // products in flight end before tensor memory is freed
-        if (n > 0) mbar_wait(smem_u32(&sh.empty_a[(n - 1) % kStages]), ((n - 1) / kStages) & 1, a.wait_ns);
-        // and the other block's arrivals have come before this one leaves
-        for (int t = max(0, n - kStages); t < n; ++t) mbar_wait(smem_u32(&sh.empty_b[t % kStages]), (t / kStages) & 1, a.wait_ns);
+        // products in flight end before tensor memory is freed; the other block sees their last arrivals as well
+        for (int t = max(0, n - kStages); t < n; ++t) mbar_wait(smem_u32(&sh.empty[t % kStages]), (t / kStages) & 1, a.wait_ns);
         __syncwarp();
     } else if (warp < kDeqWarp) {
         // rows' scales, an item ahead
@@ -414,28 +472,48 @@ tile_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
             if (lane == 0) mbar_arrive(smem_u32(&sh.rs_full[buf]));
         }
     } else if (warp < kEpiWarp) {
-        // takes stages' weights apart: group h has every other stage of the block's
+        // takes stages' weights apart: group h has every kGroups-th stage of the block's
         const int group = (warp - kDeqWarp) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
         int n = group, it = 0, c = group;
         int64_t item = first;
-        while (c >= nk) c -= nk, ++it, item += step;
-        // the next stage's bytes are on their way while one is taken apart
+        while (c >= nk && item < items) c -= nk, ++it, item += step;
         Raw<FMT, KC> next;
         const uint8_t *at = nullptr;
-        if (item < items) {
+        if (!kCopied && item < items) {
+            // the next stage's bytes are on their way while one is taken apart
             at = tile_row<PAIRED>(a, set_of(item).expert, tile_of(item), row);
             load_raw<FMT, KC>(next, at, c, a.cols);
         }
+        // this thread's row among the copied ones: gate's 64, then up's
+        const int raw_row = PAIRED ? (row >> 5) * 16 + (row & 15) + (row & 16 ? 64 : 0) : row;
         float up = 0.0f;
         int have = -1;
         while (item < items) {
-            const Raw<FMT, KC> now = next;
+            const int st = n % kStages;
+            Raw<FMT, KC> now;
             const uint8_t *now_at = at;
             const int now_c = c, now_it = it;
-            c += kDeqGroups;
+            if constexpr (kCopied) {
+                if (!tile_wait_warp(smem_u32(&sh.raw_full[st]), (n / kStages) & 1, a, abort)) break;
+                const uint32_t from = raw_base + st * kRaw;
+                // chunks of 16 bytes are swapped within 64 (32) bytes by the row, as the copy's swizzle does
+                const uint32_t x = KC == 128 ? (raw_row >> 1) & 3 : (raw_row >> 2) & 1;
+#pragma unroll
+                for (int i = 0; i < KC / 32; ++i) {
+                    const uint4 v = *reinterpret_cast<const uint4 *>(raw_smem + (from - smem_u32(raw_smem)) + raw_row * (KC / 2) + ((i ^ x) * 16));
+                    now.w[4 * i] = v.x, now.w[4 * i + 1] = v.y, now.w[4 * i + 2] = v.z, now.w[4 * i + 3] = v.w;
+                }
+                const uint4 h = *reinterpret_cast<const uint4 *>(raw_smem + (from - smem_u32(raw_smem)) + 128 * (KC / 2) + raw_row * 16);
+                now.w[KC / 8] = h.x, now.w[KC / 8 + 1] = h.y, now.w[KC / 8 + 2] = h.z, now.w[KC / 8 + 3] = h.w;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sh.raw_empty[st]));
+            } else {
+                now = next;
+            }
+            c += kGroups;
             bool moved = false;
-            while (c >= nk) c -= nk, ++it, item += step, moved = true;
-            if (item < items) {
+            while (c >= nk && item < items) c -= nk, ++it, item += step, moved = true;
+            if (!kCopied && item < items) {
                 if (moved) at = tile_row<PAIRED>(a, set_of(item).expert, tile_of(item), row);
                 load_raw<FMT, KC>(next, at, c, a.cols);
             }
@@ -444,8 +522,7 @@ tile_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
                 up = sh.row_scale[now_it & 1][row];
                 have = now_it;
             }
-            const int st = n % kStages;
-            if (n >= kStages && !tile_wait_warp(smem_u32(&sh.empty_a[st]), (n / kStages - 1) & 1, a, abort)) break;
+            if (n >= kStages && !tile_wait_warp(smem_u32(&sh.empty[st]), (n / kStages - 1) & 1, a, abort)) break;
             tc_fence_after();
             const uint32_t to = taddr + (static_cast<uint32_t>(quarter * 32) << 16) + kA0 + st * kACols;
 #pragma unroll
@@ -458,8 +535,8 @@ tile_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&sh.full[st]));
-            n += kDeqGroups;
+            if (lane == 0) arrive_even(&sh.full[st]);
+            n += kGroups;
         }
     } else {
         const int quarter = warp & 3, row = quarter * 32 + lane, part = (warp - kEpiWarp) >> 2;
@@ -515,7 +592,7 @@ tile_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
             const auto drained = [&]() {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&sh.acc_empty[q & 1]));
+                if (lane == 0) arrive_even(&sh.acc_empty[q & 1]);
                 ++q;
             };
             if constexpr (PB == 2) {
@@ -563,36 +640,63 @@ tile_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
     }
     tc_fence_before();
     cluster_sync();              // neither block leaves while the other may still write to it
-    if (warp == 1) tmem_dealloc_1(taddr, 512);
+    if (warp == 1) tmem_dealloc_pair(taddr, 512);
 }
 
 template <int FMT, int PA, int PB, bool PAIRED>
-cudaError_t tile_launch_as(const CUtensorMap &hi, const CUtensorMap &lo, const TileArgs &a, int sms, cudaStream_t st)
+cudaError_t tile_launch_as(const TileOperands &t, const TileArgs &a, int sms, cudaStream_t st)
 {
     const auto kern = tile_kernel<FMT, PA, PB, PAIRED>;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, tile_smem(PA, PB));
+    constexpr int smem = tile_smem(FMT, PA, PB), KC = tile_cols_of_stage(PA);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
+    TileMaps maps;
+    const gemm::EncodeTiledFn enc = gemm::encode_fn();
+    if (!enc) return cudaErrorNotSupported;
+    const auto encode = [&](CUtensorMap *m, bool bytes, const void *p, int64_t cols, int64_t rows, int box_cols, int box_rows,
+                            CUtensorMapSwizzle swizzle) {
+        const int64_t size = bytes ? 1 : 2;
+        const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+        const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols * size)};
+        const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows)}, one[2] = {1, 1};
+        return enc(m, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void *>(p), dims, strides,
+                   box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    bool ok = encode(&maps.hi, false, t.hi, t.cols, t.rows, 64, kTileBoxRows, CU_TENSOR_MAP_SWIZZLE_128B);
+    maps.lo = maps.hi;
+    if (PB == 2) ok = ok && encode(&maps.lo, false, t.lo, t.cols, t.rows, 64, kTileBoxRows, CU_TENSOR_MAP_SWIZZLE_128B);
+    maps.wa = maps.wb = maps.ha = maps.hb = maps.hi;
+    if (FMT == kFmtQ4K) {
+        const CUtensorMapSwizzle swizzle = KC == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B;
+        const auto rows = [&](const Weights &w) { return (a.experts - 1) * w.expert_rows + a.rows; };
+        ok = ok && encode(&maps.wa, true, a.a.w, a.a.row_bytes, rows(a.a), KC / 2, 64, swizzle) &&
+             encode(&maps.wb, true, a.b.w, a.b.row_bytes, rows(a.b), KC / 2, 64, swizzle) &&
+             encode(&maps.ha, true, a.a.w, a.a.row_bytes, rows(a.a), 16, 64, CU_TENSOR_MAP_SWIZZLE_NONE) &&
+             encode(&maps.hb, true, a.b.w, a.b.row_bytes, rows(a.b), 16, 64, CU_TENSOR_MAP_SWIZZLE_NONE);
+    }
+    if (!ok) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(sms / 2 * 2)), cfg.blockDim = dim3(kTileThreads);
-    cfg.dynamicSmemBytes = tile_smem(PA, PB), cfg.stream = st;
+    cfg.gridDim = dim3(static_cast<unsigned>(sms / 2 * 2)), cfg.blockDim = dim3(tile_threads(FMT, PB));
+    cfg.dynamicSmemBytes = smem, cfg.stream = st;
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &at, cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, hi, lo, a);
+    return cudaLaunchKernelEx(&cfg, kern, maps, a);
 }
 
 template <int FMT, bool PAIRED>
-cudaError_t tile_launch_pieces(const CUtensorMap &hi, const CUtensorMap &lo, const TileArgs &a, int sms, cudaStream_t st)
+cudaError_t tile_launch_pieces(const TileOperands &t, const TileArgs &a, int sms, cudaStream_t st)
 {
-    if (a.w_pieces == 1) return tile_launch_as<FMT, 1, 1, PAIRED>(hi, lo, a, sms, st);
-    return a.pieces == 1 ? tile_launch_as<FMT, 2, 1, PAIRED>(hi, lo, a, sms, st) : tile_launch_as<FMT, 2, 2, PAIRED>(hi, lo, a, sms, st);
+    if (a.w_pieces == 1) return tile_launch_as<FMT, 1, 1, PAIRED>(t, a, sms, st);
+    return a.pieces == 1 ? tile_launch_as<FMT, 2, 1, PAIRED>(t, a, sms, st) : tile_launch_as<FMT, 2, 2, PAIRED>(t, a, sms, st);
 }
 
 template <int FMT>
-cudaError_t tile_launch(const CUtensorMap &hi, const CUtensorMap &lo, const TileArgs &a, bool paired, int sms, cudaStream_t st)
+cudaError_t tile_launch(const TileOperands &t, const TileArgs &a, bool paired, int sms, cudaStream_t st)
 {
-    return paired ? tile_launch_pieces<FMT, true>(hi, lo, a, sms, st) : tile_launch_pieces<FMT, false>(hi, lo, a, sms, st);
+    return paired ? tile_launch_pieces<FMT, true>(t, a, sms, st) : tile_launch_pieces<FMT, false>(t, a, sms, st);
 }
 
 }  // namespace moe

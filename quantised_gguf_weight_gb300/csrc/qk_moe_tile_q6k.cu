@@ -3,9 +3,9 @@
 
 namespace qk {
 namespace moe {
-cudaError_t tile_launch_q6k(const CUtensorMap &hi, const CUtensorMap &lo, const TileArgs &a, bool paired, int sms, cudaStream_t st)
+cudaError_t tile_launch_q6k(const TileOperands &t, const TileArgs &a, bool paired, int sms, cudaStream_t st)
 {
-    return tile_launch<kFmtQ6K>(hi, lo, a, paired, sms, st);
+    return tile_launch<kFmtQ6K>(t, a, paired, sms, st);
 }
 }  // namespace moe
 }  // namespace qk

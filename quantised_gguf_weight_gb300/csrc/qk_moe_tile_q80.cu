@@ -3,9 +3,9 @@
 
 namespace qk {
 namespace moe {
-cudaError_t tile_launch_q80(const CUtensorMap &hi, const CUtensorMap &lo, const TileArgs &a, bool paired, int sms, cudaStream_t st)
+cudaError_t tile_launch_q80(const TileOperands &t, const TileArgs &a, bool paired, int sms, cudaStream_t st)
 {
-    return tile_launch<kFmtQ80>(hi, lo, a, paired, sms, st);
+    return tile_launch<kFmtQ80>(t, a, paired, sms, st);
 }
 }  // namespace moe
 }  // namespace qk
