@@ -502,7 +502,7 @@ int qk_moe_ffn(const qk_expert_weights *gate, const qk_expert_weights *up, const
             const int64_t wide = tile_cols(cols);
             const TileOperands o = {ws + tile_ops, ws + tile_ops + 2 * l.A * wide, l.A, wide};
             TileArgs t{};
-            t.plan = pa.plan, t.a = a, t.b = b, t.experts = n_experts, t.fmt = fmt, t.cols = static_cast<int>(cols), t.chunks = static_cast<int>(wide / (l.w_pieces == 1 ? 128 : 64));
+            t.plan = pa.plan, t.a = a, t.b = b, t.fmt = fmt, t.cols = static_cast<int>(cols), t.chunks = static_cast<int>(wide / (l.w_pieces == 1 ? 128 : 64));
             t.pieces = l.pieces, t.w_pieces = l.w_pieces, t.rows = static_cast<int>(rows);
             t.tiles = static_cast<int>(paired ? (rows + 63) / 64 : (rows + 127) / 128);
             t.scale = reinterpret_cast<const float *>(ws + scale), t.out = reinterpret_cast<float *>(ws + to);

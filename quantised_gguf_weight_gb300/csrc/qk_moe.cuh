@@ -81,7 +81,6 @@ struct RowsArgs {
 struct TileArgs {
     Plan plan;
     Weights a, b;             // as above
-    int64_t experts;
     int fmt, cols, chunks, pieces, w_pieces;      // chunks: stages of a row
     int rows, tiles;          // output columns and 128-row tiles (64 + 64 where paired)
     const float *scale;

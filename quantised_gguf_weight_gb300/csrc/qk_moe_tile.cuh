@@ -32,26 +32,28 @@ namespace moe {
 constexpr int kDeqWarp = 4;                                  // first warp that takes weights apart
 constexpr int kFlush = 4;                                    // stages whose products one accumulator takes, with fp32 accuracy
 constexpr int kEpiWarps = 8;                                 // two threads share a row's tokens
-// Groups of four warps that take weights apart.  More than two need the registers that fp32 sums, or bytes fetched a
-// stage ahead by the threads themselves (all formats but Q4_K), take.
-__host__ __device__ constexpr int tile_groups(int FMT, int PB) { return FMT == kFmtQ4K && PB == 1 ? 3 : 2; }
-__host__ __device__ constexpr int tile_epi_warp(int FMT, int PB) { return kDeqWarp + 4 * tile_groups(FMT, PB); }
-__host__ __device__ constexpr int tile_threads(int FMT, int PB) { return 32 * (tile_epi_warp(FMT, PB) + kEpiWarps); }
+// Groups of four warps that take weights apart: three, or the two that fp32 sums leave registers for.
+__host__ __device__ constexpr int tile_groups(int PB) { return PB == 1 ? 3 : 2; }
+__host__ __device__ constexpr int tile_epi_warp(int PB) { return kDeqWarp + 4 * tile_groups(PB); }
+__host__ __device__ constexpr int tile_threads(int PB) { return 32 * (tile_epi_warp(PB) + kEpiWarps); }
 constexpr int kStages = 4;                                   // of both operands
 constexpr int kMaxN = 128;                                   // tokens of a set
 // Columns of a stage: eight products for each (a wait costs the issuing warp as much as three of them).
 __host__ __device__ constexpr int tile_cols_of_stage(int PA) { return PA == 1 ? 128 : 64; }
 __host__ __device__ constexpr int tile_b_bytes(int PA, int PB) { return kMaxN / 2 * 2 * tile_cols_of_stage(PA) * PB; }
-// Q4_K's bytes of a stage: [128 rows] of half its columns' number, and of 16 for the scales.
-__host__ __device__ constexpr int tile_raw_bytes(int FMT, int PA) { return FMT == kFmtQ4K ? 128 * (tile_cols_of_stage(PA) / 2 + 16) : 0; }
+// The weights' bytes, a unit of 256 columns of each of 128 rows at a time: 16-byte chunks that hold it wherever it starts,
+// in a pitch of 4 (mod 8) words, so that eight rows' chunks lie in different banks.
+constexpr int kRawStages = 3;
+__host__ __device__ constexpr int tile_chunks(int FMT) { return FMT == kFmtQ4K ? 9 : FMT == kFmtQ80 ? 18 : 14; }
+__host__ __device__ constexpr int tile_pitch(int FMT) { return FMT == kFmtQ4K ? 144 : FMT == kFmtQ80 ? 304 : 240; }
 __host__ __device__ constexpr int tile_smem(int FMT, int PA, int PB)
 {
-    return kStages * (tile_b_bytes(PA, PB) + tile_raw_bytes(FMT, PA)) + 1024;
+    return kStages * tile_b_bytes(PA, PB) + kRawStages * 128 * tile_pitch(FMT) + 1024;
 }
 
 struct TileShared {
-    uint64_t full[kStages], empty[kStages], raw_full[kStages], raw_empty[kStages], acc_full[2], acc_empty[2], rs_full[2], rs_empty[2];
-    float row_scale[2][128];                                 // 2^s of the rows
+    uint64_t full[kStages], empty[kStages], raw_full[kRawStages], raw_empty[kRawStages], acc_full[2], acc_empty[2], rs_full[4];
+    float row_scale[4][128];                                 // 2^s of the rows of an item and of the next two
     float token_scale[kEpiWarps][64];                        // 2^-e of a warp's tokens
     uint32_t tmem;
     int abort;
@@ -155,51 +157,59 @@ __device__ __forceinline__ float row_scale_of(const uint8_t *row, int cols)
     return __uint_as_float(static_cast<uint32_t>(127 + 141 - ex) << 23);
 }
 
-// A stage's bytes of a row, in registers.
+// A stage's bytes of a row, in registers.  Q8_0, Q6_K: words from a 4-byte boundary on; `sh` is 16 where the bytes start
+// two later.
 template <int FMT, int KC>
 struct Raw {
-    static constexpr int kWords = FMT == kFmtQ4K ? KC / 8 + 4 : FMT == kFmtQ80 ? KC / 64 * 17 + 1 : 27;
-    uint32_t w[kWords];
+    static constexpr int kWords = FMT == kFmtQ4K ? KC / 8 + 4 : FMT == kFmtQ80 ? KC / 64 * 17 + 1 : 27 + 3 + 1;
+    uint32_t w[kWords], sh;
 };
 
-// The 32-bit words that hold N words from a 2-byte aligned place on (one more where it is off).
-template <int N>
-__device__ __forceinline__ void load_words2(uint32_t *w, const uint8_t *p)
+__device__ __forceinline__ uint4 tile_lds128(uint32_t p)
 {
-    const uint32_t *q = reinterpret_cast<const uint32_t *>(reinterpret_cast<uintptr_t>(p) & ~uintptr_t(3));
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(p));
+    return v;
+}
+__device__ __forceinline__ uint32_t tile_lds32(uint32_t p)
+{
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(p));
+    return v;
+}
+// N words that hold 4 (N - 1) + 2 bytes from p on.
+template <int N>
+__device__ __forceinline__ void tile_words(uint32_t *w, uint32_t p)
+{
+    const uint32_t q = p & ~3u;
 #pragma unroll
-    for (int i = 0; i < N; ++i) w[i] = __ldg(q + i);
-    w[N] = reinterpret_cast<uintptr_t>(p) & 2 ? __ldg(q + N) : 0u;
+    for (int i = 0; i < N; ++i) w[i] = tile_lds32(q + 4 * i);
 }
 
+// Stage c of the row whose unit lies at `p`.
 template <int FMT, int KC>
-__device__ __forceinline__ void load_raw(Raw<FMT, KC> &r, const uint8_t *row, int c, int cols)
+__device__ __forceinline__ void load_raw(Raw<FMT, KC> &r, uint32_t p, int c)
 {
+    const int part = c & (256 / KC - 1);
     if constexpr (FMT == kFmtQ4K) {
-        const int pair = c * (KC / 64);
-        const uint8_t *blk = row + 144 * (pair >> 2);
-        const uint4 *q = reinterpret_cast<const uint4 *>(blk + 16 + 32 * (pair & 3));
 #pragma unroll
         for (int i = 0; i < KC / 32; ++i) {
-            const uint4 v = __ldg(q + i);
+            const uint4 v = tile_lds128(p + 16 + part * (KC / 2) + 16 * i);
             r.w[4 * i] = v.x, r.w[4 * i + 1] = v.y, r.w[4 * i + 2] = v.z, r.w[4 * i + 3] = v.w;
         }
-        const uint4 h = __ldg(reinterpret_cast<const uint4 *>(blk));
+        const uint4 h = tile_lds128(p);
         r.w[KC / 8] = h.x, r.w[KC / 8 + 1] = h.y, r.w[KC / 8 + 2] = h.z, r.w[KC / 8 + 3] = h.w;
     } else if constexpr (FMT == kFmtQ80) {
-        // the words that the row's own blocks have bytes in
-        const int first = c * (KC / 32), blocks = min(KC / 32, (cols + 31) / 32 - first);
-        const uint8_t *p = row + 34 * static_cast<int64_t>(first);
-        const int off = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 2);
-        const uint32_t *q = reinterpret_cast<const uint32_t *>(p - off);
-#pragma unroll
-        for (int i = 0; i < Raw<FMT, KC>::kWords; ++i) r.w[i] = 4 * i < 34 * blocks + off ? __ldg(q + i) : 0u;
+        tile_words<Raw<FMT, KC>::kWords>(r.w, p + 34 * (KC / 32) * part);
+        r.sh = ((p + 34 * (KC / 32) * part) & 2) * 8;
     } else {
-        const int half = c * KC / 128;
-        const uint8_t *blk = row + 210 * (half >> 1);
-        load_words2<8>(r.w, blk + 64 * (half & 1));                  // low nibbles, 0..31
-        load_words2<8>(r.w + 9, blk + 64 * (half & 1) + 32);         // 32..63
-        load_words2<8>(r.w + 18, blk + 128 + 32 * (half & 1));       // high bits
+        const int half = KC == 128 ? part : part >> 1;
+        tile_words<9>(r.w, p + 64 * half);                       // low nibbles, 0..31
+        tile_words<9>(r.w + 9, p + 64 * half + 32);              // 32..63
+        tile_words<9>(r.w + 18, p + 128 + 32 * half);            // high bits
+        tile_words<3>(r.w + 27, p + 192 + 8 * half);             // scales
+        r.sh = (p & 2) * 8;
+        r.w[30] = tile_lds32((p + 208) & ~3u) >> r.sh;           // d
     }
 }
 
@@ -230,7 +240,7 @@ struct Pieces {
 
 // Values 32 k .. 32 k + 31 of a stage, times 2^s, as fp16 pairs in the order (0, 2), (1, 3) of every four columns.
 template <int FMT, int PA, int KC>
-__device__ __forceinline__ void take_apart(Pieces<PA> &o, const Raw<FMT, KC> &r, const uint8_t *row, int c, int cols, float up, int k)
+__device__ __forceinline__ void take_apart(Pieces<PA> &o, const Raw<FMT, KC> &r, int c, int cols, float up, int k)
 {
     if constexpr (FMT == kFmtQ4K) {
         const __half2 k1024 = __float2half2_rn(1024.0f);
@@ -255,8 +265,7 @@ __device__ __forceinline__ void take_apart(Pieces<PA> &o, const Raw<FMT, KC> &r,
     } else if constexpr (FMT == kFmtQ80) {
         // block k: d at byte 34 k, then the quants; none past the row's end
         const int first = c * (KC / 32), base = 17 * (k >> 1);
-        const uint32_t sh = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row + 34 * static_cast<int64_t>(first)) & 2) * 8;
-        const auto at = [&](int i) { return __funnelshift_r(r.w[i], r.w[i + 1], sh); };
+        const auto at = [&](int i) { return __funnelshift_r(r.w[i], r.w[i + 1], r.sh); };
         const __half2 bias = __float2half2_rn(1152.0f), zero = __float2half2_rn(0.0f);
         const float d = first + k < (cols + 31) / 32 ? half_bits_to_float(k & 1 ? at(base + 8) >> 16 : at(base)) * up : 0.0f;
         const __half2 dh = __float2half2_rn(d);
@@ -268,19 +277,18 @@ __device__ __forceinline__ void take_apart(Pieces<PA> &o, const Raw<FMT, KC> &r,
         }
     } else {
         // 32 columns t of the half
-        const int half = c * KC / 128, t = KC == 128 ? k : 2 * (c & 1) + k;
-        const uint8_t *blk = row + 210 * (half >> 1);
-        const float d0 = half_at(blk + 208) * up;
-        const uint32_t sh = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(blk) & 2) * 8;
+        const int t = KC == 128 ? k : 2 * (c & 1) + k;
+        const float d0 = half_bits_to_float(r.w[30]) * up;
         const __half2 bias = __float2half2_rn(1056.0f), zero = __float2half2_rn(0.0f);
+        const uint32_t scales = __funnelshift_r(r.w[27 + (t >> 1)], r.w[28 + (t >> 1)], r.sh) >> (16 * (t & 1));
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            const float d = d0 * static_cast<float>(static_cast<int8_t>(__ldg(blk + 192 + 8 * (half & 1) + 2 * t + u)));
+            const float d = d0 * static_cast<float>(static_cast<int8_t>(scales >> (8 * u)));
             const __half2 dh = __float2half2_rn(d);
 #pragma unroll
             for (int i = 4 * u; i < 4 * u + 4; ++i) {
-                const uint32_t low = __funnelshift_r(r.w[9 * (k & 1) + i], r.w[9 * (k & 1) + i + 1], sh) >> (t & 2 ? 4 : 0);
-                const uint32_t high = __funnelshift_r(r.w[18 + i], r.w[19 + i], sh) >> (2 * t);
+                const uint32_t low = __funnelshift_r(r.w[9 * (k & 1) + i], r.w[9 * (k & 1) + i + 1], r.sh) >> (t & 2 ? 4 : 0);
+                const uint32_t high = __funnelshift_r(r.w[18 + i], r.w[19 + i], r.sh) >> (2 * t);
                 const uint32_t q = (low & 0x0f0f0f0fu) | ((high & 0x03030303u) << 4);
                 o.set4(2 * i, __hsub2(tile_b2(__byte_perm(q, 0x64u, 0x4240)), bias), __hsub2(tile_b2(__byte_perm(q, 0x64u, 0x4341)), bias),
                        d, 0.0f, dh, zero);
@@ -291,16 +299,14 @@ __device__ __forceinline__ void take_apart(Pieces<PA> &o, const Raw<FMT, KC> &r,
 
 struct TileMaps {
     CUtensorMap hi, lo;              // the tokens' operands
-    CUtensorMap wa, wb, ha, hb;      // Q4_K: nibbles and scales of a's and b's rows
 };
 
 template <int FMT, int PA, int PB, bool PAIRED>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(tile_threads(FMT, PB), 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(tile_threads(PB), 1)
 tile_kernel(const __grid_constant__ TileMaps maps, const TileArgs a)
 {
-    constexpr int KC = tile_cols_of_stage(PA), kStage = tile_b_bytes(PA, PB), kRaw = tile_raw_bytes(FMT, PA);
-    constexpr int kGroups = tile_groups(FMT, PB), kEpiWarp = tile_epi_warp(FMT, PB);
-    constexpr bool kCopied = FMT == kFmtQ4K;                 // the weights' bytes come by TMA
+    constexpr int KC = tile_cols_of_stage(PA), kStage = tile_b_bytes(PA, PB), kPitch = tile_pitch(FMT), kRaw = 128 * kPitch;
+    constexpr int kGroups = tile_groups(PB), kEpiWarp = tile_epi_warp(PB), kParts = 256 / KC;      // stages of a unit
     constexpr uint32_t kACols = KC / 2 * PA, kA0 = 2 * kMaxN;         // tensor-memory columns of a stage of A, and of the first
     static_assert(kA0 + kStages * kACols == 512, "all of tensor memory");
     extern __shared__ uint8_t raw_smem[];
@@ -312,17 +318,15 @@ tile_kernel(const __grid_constant__ TileMaps maps, const TileArgs a)
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(smem_u32(&sh.full[i]), 9);             // (even block) a group's four warps of each block, and the copies
-            mbar_init(smem_u32(&sh.empty[i]), 1), mbar_init(smem_u32(&sh.raw_full[i]), 1), mbar_init(smem_u32(&sh.raw_empty[i]), 4);
+            mbar_init(smem_u32(&sh.empty[i]), 1);
         }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&sh.acc_full[i]), 1), mbar_init(smem_u32(&sh.acc_empty[i]), 2 * kEpiWarps);
-            mbar_init(smem_u32(&sh.rs_full[i]), 2), mbar_init(smem_u32(&sh.rs_empty[i]), kEpiWarps);
-        }
+        for (int i = 0; i < kRawStages; ++i) mbar_init(smem_u32(&sh.raw_full[i]), 64), mbar_init(smem_u32(&sh.raw_empty[i]), 4 * kParts);
+        for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&sh.acc_full[i]), 1), mbar_init(smem_u32(&sh.acc_empty[i]), 2 * kEpiWarps);
+        for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&sh.rs_full[i]), 4);
         sh.abort = 0;
         fence_barrier_init();
         tma_prefetch_desc(&maps.hi);
         if (PB == 2) tma_prefetch_desc(&maps.lo);
-        if (kCopied) tma_prefetch_desc(&maps.wa), tma_prefetch_desc(&maps.wb), tma_prefetch_desc(&maps.ha), tma_prefetch_desc(&maps.hb);
     }
     if (warp == 1) {
         tmem_alloc_pair(smem_u32(&sh.tmem), 512);
@@ -350,51 +354,18 @@ tile_kernel(const __grid_constant__ TileMaps maps, const TileArgs a)
 
     if (warp == 0) {
         if (lane == 0) {
-            const uint64_t keep = l2_evict_last_policy(), once = l2_evict_first_policy();
-            int n = 0, nr = 0;
+            const uint64_t keep = l2_evict_last_policy();
+            int n = 0;
             bool ok = true;
-            // the weights' bytes run ahead of the tokens by as much as their own barriers allow
-            int64_t raw_item = first;
-            int raw_c = 0;
-            const auto weights = [&]() {
-                if (!kCopied || raw_item >= items) return;
-                const int st = nr % kStages;
-                if (nr >= kStages && !mbar_test(smem_u32(&sh.raw_empty[st]), (nr / kStages - 1) & 1)) return;
-                const uint32_t bar = smem_u32(&sh.raw_full[st]), to = raw_base + st * kRaw;
-                mbar_arrive_expect_tx(bar, kRaw);
-                const int e = set_of(raw_item).expert, tile = tile_of(raw_item), pair = raw_c * (KC / 64);
-                const int r0 = static_cast<int>(e * a.a.expert_rows) + tile * (PAIRED ? 64 : 128);
-                const int r1 = PAIRED ? static_cast<int>(e * a.b.expert_rows) + tile * 64 : r0 + 64;
-                const int at = 144 * (pair >> 2);
-                tma_load_2d(to, &maps.wa, at + 16 + 32 * (pair & 3), r0, bar, once);
-                tma_load_2d(to + 64 * (KC / 2), &maps.wb, at + 16 + 32 * (pair & 3), r1, bar, once);
-                tma_load_2d(to + 128 * (KC / 2), &maps.ha, at, r0, bar, once);
-                tma_load_2d(to + 128 * (KC / 2) + 64 * 16, &maps.hb, at, r1, bar, once);
-                ++nr;
-                if (++raw_c == nk) raw_c = 0, raw_item += step;
-            };
             for (int64_t item = first; item < items && ok; item += step) {
                 const ExpertSet s = set_of(item);
                 const int cols = columns_of(s.count), boxes = (cols / 2 + kTileBoxRows - 1) / kTileBoxRows;
                 const int y = s.first + rank * (cols / 2);
                 for (int c = 0; c < nk; ++c, ++n) {
                     const int st = n % kStages;
-                    weights();
-                    if (n >= kStages) {
-                        // a bounded wait in which weights go on
-                        uint64_t since = 0;
-                        while (!mbar_test(smem_u32(&sh.empty[st]), (n / kStages - 1) & 1)) {
-                            weights();
-                            const uint64_t now = globaltimer_ns();
-                            if (since == 0) since = now;
-                            if (*abort || now - since > a.wait_ns) {
-                                if (!*abort) record_error(a.err, kErrTimeout);
-                                *abort = 1;
-                                ok = false;
-                                break;
-                            }
-                        }
-                        if (!ok) break;
+                    if (n >= kStages && !tile_wait(smem_u32(&sh.empty[st]), (n / kStages - 1) & 1, a, abort)) {
+                        ok = false;
+                        break;
                     }
                     const uint32_t full = smem_u32(&sh.full[st]), to = b_base + st * kStage;
                     if (rank == 0) mbar_arrive_expect_tx(full, 2 * boxes * kTileBoxRows * 2 * KC * PB);
@@ -409,14 +380,9 @@ tile_kernel(const __grid_constant__ TileMaps maps, const TileArgs a)
                         }
                 }
             }
-            for (const uint64_t since = globaltimer_ns(); ok && kCopied && nr < n && !*abort;) {
-                weights();
-                if (globaltimer_ns() - since > a.wait_ns) record_error(a.err, kErrTimeout), *abort = 1;
-            }
-            // every copy lands before the blocks leave: the tokens of both on the even block's barriers, and this one's weights
+            // every copy lands before the blocks leave (both blocks' are counted on the even one's barriers)
             if (rank == 0)
                 for (int t = max(0, n - kStages); t < n; ++t) mbar_wait(smem_u32(&sh.full[t % kStages]), (t / kStages) & 1, a.wait_ns);
-            for (int t = max(0, nr - kStages); t < nr; ++t) mbar_wait(smem_u32(&sh.raw_full[t % kStages]), (t / kStages) & 1, a.wait_ns);
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -456,79 +422,68 @@ tile_kernel(const __grid_constant__ TileMaps maps, const TileArgs a)
         for (int t = max(0, n - kStages); t < n; ++t) mbar_wait(smem_u32(&sh.empty[t % kStages]), (t / kStages) & 1, a.wait_ns);
         __syncwarp();
     } else if (warp < kDeqWarp) {
-        // rows' scales, an item ahead
-        int it = 0;
-        for (int64_t item = first; item < items; item += step, ++it) {
-            const int buf = it & 1;
-            const ExpertSet s = set_of(item);
-            float v[2];
-#pragma unroll
-            for (int r = 0; r < 2; ++r)
-                v[r] = row_scale_of<FMT>(tile_row<PAIRED>(a, s.expert, tile_of(item), (warp - 2) * 64 + r * 32 + lane), a.cols);
-            if (it >= 2 && !tile_wait_warp(smem_u32(&sh.rs_empty[buf]), (it / 2 - 1) & 1, a, abort)) break;
-#pragma unroll
-            for (int r = 0; r < 2; ++r) sh.row_scale[buf][(warp - 2) * 64 + r * 32 + lane] = v[r];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&sh.rs_full[buf]));
+        // the weights' bytes: 16 at a time, neighbours in neighbouring lanes
+        constexpr int UB = unit_bytes(FMT), CH = tile_chunks(FMT);
+        const int me = (warp - 2) * 32 + lane, units = (nk + kParts - 1) / kParts;
+        int n = 0;                                             // units so far
+        bool ok = true;
+        for (int64_t item = first; item < items && ok; item += step) {
+            const int expert = set_of(item).expert, tile = tile_of(item);
+            for (int u = 0; u < units; ++u, ++n) {
+                const int st = n % kRawStages;
+                if (n >= kRawStages && !tile_wait_warp(smem_u32(&sh.raw_empty[st]), (n / kRawStages - 1) & 1, a, abort)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t to = raw_base + st * kRaw;
+#pragma unroll 6
+                for (int q = me; q < 128 * CH; q += 64) {
+                    const int row = q / CH, ch = q - row * CH;
+                    const uint8_t *at = tile_row<PAIRED>(a, expert, tile, row), *from = at + static_cast<int64_t>(u) * UB;
+                    const uint8_t *last = at + a.a.row_bytes, *end = from + UB < last ? from + UB : last;
+                    from -= reinterpret_cast<uintptr_t>(from) & 15;
+                    if (from + 16 * ch < end)
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + row * kPitch + 16 * ch), "l"(from + 16 * ch)
+                                     : "memory");
+                }
+                // arrives when this thread's copies have landed
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&sh.raw_full[st])) : "memory");
+            }
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (warp < kEpiWarp) {
         // takes stages' weights apart: group h has every kGroups-th stage of the block's
         const int group = (warp - kDeqWarp) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
         int n = group, it = 0, c = group;
         int64_t item = first;
         while (c >= nk && item < items) c -= nk, ++it, item += step;
-        Raw<FMT, KC> next;
-        const uint8_t *at = nullptr;
-        if (!kCopied && item < items) {
-            // the next stage's bytes are on their way while one is taken apart
-            at = tile_row<PAIRED>(a, set_of(item).expert, tile_of(item), row);
-            load_raw<FMT, KC>(next, at, c, a.cols);
-        }
-        // this thread's row among the copied ones: gate's 64, then up's
-        const int raw_row = PAIRED ? (row >> 5) * 16 + (row & 15) + (row & 16 ? 64 : 0) : row;
+        uint32_t start = 0;                                    // low bits of the address of the thread's row
         float up = 0.0f;
         int have = -1;
         while (item < items) {
-            const int st = n % kStages;
-            Raw<FMT, KC> now;
-            const uint8_t *now_at = at;
-            const int now_c = c, now_it = it;
-            if constexpr (kCopied) {
-                if (!tile_wait_warp(smem_u32(&sh.raw_full[st]), (n / kStages) & 1, a, abort)) break;
-                const uint32_t from = raw_base + st * kRaw;
-                // chunks of 16 bytes are swapped within 64 (32) bytes by the row, as the copy's swizzle does
-                const uint32_t x = KC == 128 ? (raw_row >> 1) & 3 : (raw_row >> 2) & 1;
-#pragma unroll
-                for (int i = 0; i < KC / 32; ++i) {
-                    const uint4 v = *reinterpret_cast<const uint4 *>(raw_smem + (from - smem_u32(raw_smem)) + raw_row * (KC / 2) + ((i ^ x) * 16));
-                    now.w[4 * i] = v.x, now.w[4 * i + 1] = v.y, now.w[4 * i + 2] = v.z, now.w[4 * i + 3] = v.w;
-                }
-                const uint4 h = *reinterpret_cast<const uint4 *>(raw_smem + (from - smem_u32(raw_smem)) + 128 * (KC / 2) + raw_row * 16);
-                now.w[KC / 8] = h.x, now.w[KC / 8 + 1] = h.y, now.w[KC / 8 + 2] = h.z, now.w[KC / 8 + 3] = h.w;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&sh.raw_empty[st]));
-            } else {
-                now = next;
+            const int st = n % kStages, u = it * ((nk + kParts - 1) / kParts) + c / kParts, rs = u % kRawStages;
+            if (have != it) {
+                start = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(tile_row<PAIRED>(a, set_of(item).expert, tile_of(item), row)));
+                if (!tile_wait_warp(smem_u32(&sh.rs_full[it & 3]), (it / 4) & 1, a, abort)) break;
+                up = sh.row_scale[it & 3][row];
+                have = it;
             }
-            c += kGroups;
-            bool moved = false;
-            while (c >= nk && item < items) c -= nk, ++it, item += step, moved = true;
-            if (!kCopied && item < items) {
-                if (moved) at = tile_row<PAIRED>(a, set_of(item).expert, tile_of(item), row);
-                load_raw<FMT, KC>(next, at, c, a.cols);
-            }
-            if (have != now_it) {
-                if (!tile_wait_warp(smem_u32(&sh.rs_full[now_it & 1]), (now_it / 2) & 1, a, abort)) break;
-                up = sh.row_scale[now_it & 1][row];
-                have = now_it;
-            }
+            if (!tile_wait_warp(smem_u32(&sh.raw_full[rs]), (u / kRawStages) & 1, a, abort)) break;
+            Raw<FMT, KC> raw;
+            load_raw<FMT, KC>(raw, raw_base + rs * kRaw + row * kPitch + ((start + c / kParts * unit_bytes(FMT)) & 15), c);
+            __syncwarp();
+            // (a row's last stage arrives for those that its last unit lacks, too)
+            if (lane == 0)
+                asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(&sh.raw_empty[rs])),
+                             "r"(c + 1 == nk ? kParts - c % kParts : 1)
+                             : "memory");
             if (n >= kStages && !tile_wait_warp(smem_u32(&sh.empty[st]), (n / kStages - 1) & 1, a, abort)) break;
             tc_fence_after();
             const uint32_t to = taddr + (static_cast<uint32_t>(quarter * 32) << 16) + kA0 + st * kACols;
 #pragma unroll
             for (int k = 0; k < KC / 32; ++k) {
                 Pieces<PA> o;
-                take_apart<FMT, PA, KC>(o, now, now_at, now_c, a.cols, up, k);
+                take_apart<FMT, PA, KC>(o, raw, c, a.cols, up, k);
                 tmem_st_32x32b_x16(to + 16 * k, o.hi);
                 if constexpr (PA == 2) tmem_st_32x32b_x16(to + KC / 2 + 16 * k, o.lo);
             }
@@ -536,13 +491,23 @@ tile_kernel(const __grid_constant__ TileMaps maps, const TileArgs a)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) arrive_even(&sh.full[st]);
-            n += kGroups;
+            n += kGroups, c += kGroups;
+            while (c >= nk && item < items) c -= nk, ++it, item += step;
         }
     } else {
         const int quarter = warp & 3, row = quarter * 32 + lane, part = (warp - kEpiWarp) >> 2;
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
         int it = 0, q = 0;
         bool ok = true;
+        // the scales of item number i's rows, by the first four warps
+        const auto look_over = [&](int i) {
+            const int64_t item = first + i * step;
+            if (part != 0 || item >= items) return;
+            sh.row_scale[i & 3][row] = row_scale_of<FMT>(tile_row<PAIRED>(a, set_of(item).expert, tile_of(item), row), a.cols);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sh.rs_full[i & 3]));
+        };
+        look_over(0), look_over(1);
         for (int64_t item = first; item < items && ok; item += step, ++it) {
             const ExpertSet s = set_of(item);
             const int tile = tile_of(item);
@@ -586,7 +551,7 @@ tile_kernel(const __grid_constant__ TileMaps maps, const TileArgs a)
             const auto ready = [&]() {
                 if (!tile_wait_warp(smem_u32(&sh.acc_full[q & 1]), (q / 2) & 1, a, abort)) return ok = false;
                 tc_fence_after();
-                if (back == 0.0f) back = 1.0f / sh.row_scale[it & 1][row];      // a power of two
+                if (back == 0.0f) back = 1.0f / sh.row_scale[it & 3][row];      // a power of two
                 return true;
             };
             const auto drained = [&]() {
@@ -634,8 +599,8 @@ tile_kernel(const __grid_constant__ TileMaps maps, const TileArgs a)
                 }
                 drained();
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&sh.rs_empty[it & 1]));
+            // the slot's last item was done when this one's sums were: every thread had read its scale before
+            look_over(it + 2);
         }
     }
     tc_fence_before();
@@ -647,37 +612,26 @@ template <int FMT, int PA, int PB, bool PAIRED>
 cudaError_t tile_launch_as(const TileOperands &t, const TileArgs &a, int sms, cudaStream_t st)
 {
     const auto kern = tile_kernel<FMT, PA, PB, PAIRED>;
-    constexpr int smem = tile_smem(FMT, PA, PB), KC = tile_cols_of_stage(PA);
+    constexpr int smem = tile_smem(FMT, PA, PB);
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     TileMaps maps;
     const gemm::EncodeTiledFn enc = gemm::encode_fn();
     if (!enc) return cudaErrorNotSupported;
-    const auto encode = [&](CUtensorMap *m, bool bytes, const void *p, int64_t cols, int64_t rows, int box_cols, int box_rows,
-                            CUtensorMapSwizzle swizzle) {
-        const int64_t size = bytes ? 1 : 2;
-        const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-        const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols * size)};
-        const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows)}, one[2] = {1, 1};
-        return enc(m, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void *>(p), dims, strides,
-                   box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    // boxes of 64 columns and kTileBoxRows rows
+    const auto encode = [&](CUtensorMap *m, const void *p) {
+        const cuuint64_t dims[2] = {static_cast<cuuint64_t>(t.cols), static_cast<cuuint64_t>(t.rows)};
+        const cuuint64_t strides[1] = {static_cast<cuuint64_t>(2 * t.cols)};
+        const cuuint32_t box[2] = {64, kTileBoxRows}, one[2] = {1, 1};
+        return enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void *>(p), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
     };
-    bool ok = encode(&maps.hi, false, t.hi, t.cols, t.rows, 64, kTileBoxRows, CU_TENSOR_MAP_SWIZZLE_128B);
+    bool ok = encode(&maps.hi, t.hi);
     maps.lo = maps.hi;
-    if (PB == 2) ok = ok && encode(&maps.lo, false, t.lo, t.cols, t.rows, 64, kTileBoxRows, CU_TENSOR_MAP_SWIZZLE_128B);
-    maps.wa = maps.wb = maps.ha = maps.hb = maps.hi;
-    if (FMT == kFmtQ4K) {
-        const CUtensorMapSwizzle swizzle = KC == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B;
-        const auto rows = [&](const Weights &w) { return (a.experts - 1) * w.expert_rows + a.rows; };
-        ok = ok && encode(&maps.wa, true, a.a.w, a.a.row_bytes, rows(a.a), KC / 2, 64, swizzle) &&
-             encode(&maps.wb, true, a.b.w, a.b.row_bytes, rows(a.b), KC / 2, 64, swizzle) &&
-             encode(&maps.ha, true, a.a.w, a.a.row_bytes, rows(a.a), 16, 64, CU_TENSOR_MAP_SWIZZLE_NONE) &&
-             encode(&maps.hb, true, a.b.w, a.b.row_bytes, rows(a.b), 16, 64, CU_TENSOR_MAP_SWIZZLE_NONE);
-    }
+    if (PB == 2) ok = ok && encode(&maps.lo, t.lo);
     if (!ok) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(sms / 2 * 2)), cfg.blockDim = dim3(tile_threads(FMT, PB));
+    cfg.gridDim = dim3(static_cast<unsigned>(sms / 2 * 2)), cfg.blockDim = dim3(tile_threads(PB));
     cfg.dynamicSmemBytes = smem, cfg.stream = st;
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
