@@ -443,6 +443,8 @@ int qk_moe_ffn(const qk_expert_weights *gate, const qk_expert_weights *up, const
     if (st == QK_OK) st = check_weights(up, n_experts, F, K, &wu);
     if (st == QK_OK) st = check_weights(down, n_experts, N, F, &wd);
     if (st != QK_OK) return st;
+    // an item of the many-token form is a tile set and 256 rows of gate and up, or of down
+    if ((static_cast<int64_t>(T) * top_k / 64 + n_experts) * ((std::max(2 * F, N) + 255) / 256) > INT32_MAX) return QK_ERR_TOO_LARGE;
     if (T == 0) return QK_OK;
     if (!x || !ids || !weights || !y) return QK_ERR_NULL;
     if (!multiple(x, size_of(x_type)) || !multiple(y, size_of(y_type)) || !multiple(ids, 4) || !multiple(weights, 4))

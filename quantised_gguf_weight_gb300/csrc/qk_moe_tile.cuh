@@ -36,7 +36,7 @@ constexpr int kEpiWarps = 8;                                 // two threads shar
 __host__ __device__ constexpr int tile_groups(int PB) { return PB == 1 ? 3 : 2; }
 __host__ __device__ constexpr int tile_epi_warp(int PB) { return kDeqWarp + 4 * tile_groups(PB); }
 __host__ __device__ constexpr int tile_threads(int PB) { return 32 * (tile_epi_warp(PB) + kEpiWarps); }
-constexpr int kStages = 4;                                   // of both operands
+constexpr int kStages = 4;                                   // of the weights' operand
 constexpr int kMaxN = 128;                                   // tokens of a set
 // Columns of a stage: eight products for each (a wait costs the issuing warp as much as three of them).
 __host__ __device__ constexpr int tile_cols_of_stage(int PA) { return PA == 1 ? 128 : 64; }
@@ -46,29 +46,32 @@ __host__ __device__ constexpr int tile_b_bytes(int PA, int PB) { return kMaxN / 
 constexpr int kRawStages = 3;
 __host__ __device__ constexpr int tile_chunks(int FMT) { return FMT == kFmtQ4K ? 9 : FMT == kFmtQ80 ? 18 : 14; }
 __host__ __device__ constexpr int tile_pitch(int FMT) { return FMT == kFmtQ4K ? 144 : FMT == kFmtQ80 ? 304 : 240; }
+// Stages of the tokens' operand: as many as shared memory holds (a refill takes 3000 cycles, a stage's products 500).
+__host__ __device__ constexpr int tile_b_stages(int FMT, int PA, int PB)
+{
+    const int room = (222 * 1024 - kRawStages * 128 * tile_pitch(FMT)) / tile_b_bytes(PA, PB);
+    return room < 8 ? room : 8;
+}
 __host__ __device__ constexpr int tile_smem(int FMT, int PA, int PB)
 {
-    return kStages * tile_b_bytes(PA, PB) + kRawStages * 128 * tile_pitch(FMT) + 1024;
+    return tile_b_stages(FMT, PA, PB) * tile_b_bytes(PA, PB) + kRawStages * 128 * tile_pitch(FMT) + 1024;
 }
 
 struct TileShared {
-    uint64_t full[kStages], empty[kStages], raw_full[kRawStages], raw_empty[kRawStages], acc_full[2], acc_empty[2], rs_full[4];
+    uint64_t full[kStages], empty[kStages], b_full[8], b_empty[8], raw_full[kRawStages], raw_empty[kRawStages], acc_full[2], acc_empty[2], rs_full[4];
     float row_scale[4][128];                                 // 2^s of the rows of an item and of the next two
     float token_scale[kEpiWarps][64];                        // 2^-e of a warp's tokens
     uint32_t tmem;
     int abort;
 };
 
-// A bounded wait; one that runs out ends every other of the block.  POLL: without sleeping, and for arrivals from the
-// other block.
-template <bool POLL = false>
+// A bounded wait; one that runs out ends every other of the block.
 __device__ __forceinline__ bool tile_wait(uint32_t bar, uint32_t parity, const TileArgs &a, volatile int *abort)
 {
-    const auto test = [&]() { return POLL ? mbar_test(bar, parity) : mbar_try_wait(bar, parity); };
-    if (test()) return true;
+    if (mbar_try_wait(bar, parity)) return true;
     const uint64_t deadline = globaltimer_ns() + a.wait_ns;
     for (uint32_t i = 1; !*abort; ++i) {
-        if (test()) return true;
+        if (mbar_try_wait(bar, parity)) return true;
         if ((i & 31u) == 0 && globaltimer_ns() > deadline) {
             *abort = 1;
             record_error(a.err, kErrTimeout);
@@ -76,10 +79,9 @@ __device__ __forceinline__ bool tile_wait(uint32_t bar, uint32_t parity, const T
     }
     return false;
 }
-template <bool POLL = false>
 __device__ __forceinline__ bool tile_wait_warp(uint32_t bar, uint32_t parity, const TileArgs &a, volatile int *abort)
 {
-    return __all_sync(~0u, tile_wait<POLL>(bar, parity, a, abort));
+    return __all_sync(~0u, tile_wait(bar, parity, a, abort));
 }
 
 // One lane of the (converged) warp is elected.
@@ -305,21 +307,22 @@ template <int FMT, int PA, int PB, bool PAIRED>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(tile_threads(PB), 1)
 tile_kernel(const __grid_constant__ TileMaps maps, const TileArgs a)
 {
-    constexpr int KC = tile_cols_of_stage(PA), kStage = tile_b_bytes(PA, PB), kPitch = tile_pitch(FMT), kRaw = 128 * kPitch;
+    constexpr int KC = tile_cols_of_stage(PA), kStage = tile_b_bytes(PA, PB), kBStages = tile_b_stages(FMT, PA, PB), kPitch = tile_pitch(FMT), kRaw = 128 * kPitch;
     constexpr int kGroups = tile_groups(PB), kEpiWarp = tile_epi_warp(PB), kParts = 256 / KC;      // stages of a unit
     constexpr uint32_t kACols = KC / 2 * PA, kA0 = 2 * kMaxN;         // tensor-memory columns of a stage of A, and of the first
     static_assert(kA0 + kStages * kACols == 512, "all of tensor memory");
     extern __shared__ uint8_t raw_smem[];
     __shared__ TileShared sh;
-    const uint32_t b_base = (smem_u32(raw_smem) + 1023u) & ~1023u, raw_base = b_base + kStages * kStage;
+    const uint32_t b_base = (smem_u32(raw_smem) + 1023u) & ~1023u, raw_base = b_base + kBStages * kStage;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = static_cast<int>(cluster_ctarank());
     volatile int *abort = &sh.abort;
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(smem_u32(&sh.full[i]), 9);             // (even block) a group's four warps of each block, and the copies
+            mbar_init(smem_u32(&sh.full[i]), 8);             // (even block) a group's four warps of each block
             mbar_init(smem_u32(&sh.empty[i]), 1);
         }
+        for (int i = 0; i < kBStages; ++i) mbar_init(smem_u32(&sh.b_full[i]), 1), mbar_init(smem_u32(&sh.b_empty[i]), 1);
         for (int i = 0; i < kRawStages; ++i) mbar_init(smem_u32(&sh.raw_full[i]), 64), mbar_init(smem_u32(&sh.raw_empty[i]), 4 * kParts);
         for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&sh.acc_full[i]), 1), mbar_init(smem_u32(&sh.acc_empty[i]), 2 * kEpiWarps);
         for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&sh.rs_full[i]), 4);
@@ -340,11 +343,11 @@ tile_kernel(const __grid_constant__ TileMaps maps, const TileArgs a)
     wait_for_previous();
 
     const int pairs = (a.tiles + 1) / 2;
-    const int64_t items = static_cast<int64_t>(a.plan.head[3]) * pairs, first = blockIdx.x >> 1, step = gridDim.x >> 1;
+    const int items = a.plan.head[3] * pairs, first = blockIdx.x >> 1, step = gridDim.x >> 1;      // (the caller sees to 31 bits)
     const int nk = a.chunks;
     const int per = PB == 2 ? kFlush : nk;                     // stages an accumulator takes
-    const auto set_of = [&](int64_t item) { return a.plan.tile_sets[item / pairs]; };
-    const auto tile_of = [&](int64_t item) { return static_cast<int>(item % pairs) * 2 + rank; };
+    const auto set_of = [&](int item) { return a.plan.tile_sets[item / pairs]; };
+    const auto tile_of = [&](int item) { return item % pairs * 2 + rank; };
     const auto columns_of = [](int count) { return (count + 31) / 32 * 32; };       // of a product: a pair's are multiples of 32
     // an arrival on a barrier of the even block
     const auto arrive_even = [&](uint64_t *bar) {
@@ -352,58 +355,87 @@ tile_kernel(const __grid_constant__ TileMaps maps, const TileArgs a)
         else mbar_arrive_remote(mapa_shared(smem_u32(bar), 0));
     };
 
+    // What the warps that issue copies and products go by: they stay together and elect a lane for each, and all that
+    // steers them comes from votes, reductions and counters, so that operands are in the warp's uniform registers.  (A
+    // thread of a branch of its own, or in a loop whose end it has read from memory, takes 100 to 118 cycles a product and
+    // 250 a copy, measured; this form N / 2 and 30.)
+    // Two barriers' phases, tested side by side.
+    const auto both_ready = [&](uint32_t bar0, uint32_t parity0, uint32_t bar1, uint32_t parity1) {
+        const auto test = [&]() {
+            const bool t0 = mbar_test(bar0, parity0), t1 = mbar_test(bar1, parity1);
+            return __all_sync(~0u, t0 & t1) != 0;
+        };
+        if (test()) return true;
+        const uint64_t deadline = globaltimer_ns() + a.wait_ns;
+        for (unsigned i = 1;; ++i) {
+            if (test()) return true;
+            if ((i & 63u) == 0) {
+                const bool late = globaltimer_ns() > deadline;
+                if (late) *abort = 1, record_error(a.err, kErrTimeout);
+                if (__any_sync(~0u, late || *abort)) return false;
+            }
+        }
+    };
+    const auto ready = [&](uint32_t bar, uint32_t parity) { return both_ready(bar, parity, bar, parity); };
+    const unsigned end = __reduce_max_sync(~0u, static_cast<unsigned>(items));
+
     if (warp == 0) {
-        if (lane == 0) {
-            const uint64_t keep = l2_evict_last_policy();
-            int n = 0;
-            bool ok = true;
-            for (int64_t item = first; item < items && ok; item += step) {
-                const ExpertSet s = set_of(item);
-                const int cols = columns_of(s.count), boxes = (cols / 2 + kTileBoxRows - 1) / kTileBoxRows;
-                const int y = s.first + rank * (cols / 2);
-                for (int c = 0; c < nk; ++c, ++n) {
-                    const int st = n % kStages;
-                    if (n >= kStages && !tile_wait(smem_u32(&sh.empty[st]), (n / kStages - 1) & 1, a, abort)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t full = smem_u32(&sh.full[st]), to = b_base + st * kStage;
+        const uint64_t keep = l2_evict_last_policy();
+        unsigned n = 0;
+        bool ok = true;
+        for (unsigned item = first; item < end && ok; item += step) {
+            const ExpertSet s = set_of(item);
+            const unsigned cols = __reduce_max_sync(~0u, static_cast<unsigned>(columns_of(s.count)));
+            const unsigned boxes = (cols / 2 + kTileBoxRows - 1) / kTileBoxRows;
+            const int y = __reduce_max_sync(~0u, s.first) + rank * static_cast<int>(cols / 2);
+            for (int c = 0; c < nk; ++c, ++n) {
+                const unsigned st = n % kBStages;
+                if (n >= kBStages && !ready(smem_u32(&sh.b_empty[st]), (n / kBStages - 1) & 1)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t full = smem_u32(&sh.b_full[st]), to = b_base + st * kStage;
+                const uint32_t full0 = rank == 0 ? full : mapa_shared(full, 0);
+                if (elect_one()) {
                     if (rank == 0) mbar_arrive_expect_tx(full, 2 * boxes * kTileBoxRows * 2 * KC * PB);
-                    if (a.skip_chunk >= 0 && n == a.skip_chunk && blockIdx.x < 2) continue;     // test hook
-                    const uint32_t full0 = rank == 0 ? full : mapa_shared(full, 0);
-                    for (int b = 0; b < boxes; ++b)
+                    if (!(a.skip_chunk >= 0 && static_cast<int>(n) == a.skip_chunk && blockIdx.x < 2))       // test hook
+                        for (unsigned b = 0; b < boxes; ++b)
 #pragma unroll
-                        for (int k = 0; k < KC / 64; ++k) {
-                            const uint32_t at = to + k * (kMaxN / 2 * 128) + b * (kTileBoxRows * 128);
-                            tma_load_2d_peer(at, &maps.hi, c * KC + k * 64, y + b * kTileBoxRows, full0, keep);
-                            if (PB == 2) tma_load_2d_peer(at + kStage / 2, &maps.lo, c * KC + k * 64, y + b * kTileBoxRows, full0, keep);
-                        }
+                            for (int k = 0; k < KC / 64; ++k) {
+                                const uint32_t at = to + k * (kMaxN / 2 * 128) + b * (kTileBoxRows * 128);
+                                tma_load_2d_peer(at, &maps.hi, c * KC + k * 64, y + b * kTileBoxRows, full0, keep);
+                                if (PB == 2)
+                                    tma_load_2d_peer(at + kStage / 2, &maps.lo, c * KC + k * 64, y + b * kTileBoxRows, full0, keep);
+                            }
                 }
             }
-            // every copy lands before the blocks leave (both blocks' are counted on the even one's barriers)
-            if (rank == 0)
-                for (int t = max(0, n - kStages); t < n; ++t) mbar_wait(smem_u32(&sh.full[t % kStages]), (t / kStages) & 1, a.wait_ns);
         }
+        // every copy lands before the blocks leave (both blocks' are counted on the even one's barriers)
+        if (rank == 0)
+            for (unsigned t = n > kBStages ? n - kBStages : 0; t < n; ++t)
+                mbar_wait(smem_u32(&sh.b_full[t % kBStages]), (t / kBStages) & 1, a.wait_ns);
         __syncwarp();
     } else if (warp == 1) {
-        // The warp stays together and elects a lane for each product: a thread of a branch of its own takes 118 cycles a
-        // product whatever its size (measured), an elected one N / 2.
-        int n = 0, q = 0;                                      // stages and accumulators so far
+        unsigned n = 0, q = 0;                                 // stages and accumulators so far
         bool ok = rank == 0;
+        const uint32_t tmem = __reduce_max_sync(~0u, taddr);
         const uint64_t desc0 = smem_desc_sw128_kmajor(b_base);
-        for (int64_t item = first; item < items && ok; item += step) {
-            const uint32_t idesc = idesc_f16_f32(256, columns_of(set_of(item).count));
-            for (int c = 0; c < nk; ++c, ++n) {
-                const int st = n % kStages, buf = q & 1;
-                const bool fresh = c % per == 0, last = c + 1 == nk || (c + 1) % per == 0;
-                if ((fresh && q >= 2 && !tile_wait_warp<true>(smem_u32(&sh.acc_empty[buf]), (q / 2 - 1) & 1, a, abort)) ||
-                    !tile_wait_warp<true>(smem_u32(&sh.full[st]), (n / kStages) & 1, a, abort)) {
+        for (unsigned item = first; item < end && ok; item += step) {
+            const uint32_t idesc = idesc_f16_f32(256, columns_of(__reduce_max_sync(~0u, set_of(item).count)));
+            for (int c = 0, of = 0; c < nk; ++c, ++n) {
+                const unsigned st = n % kStages, sb = n % kBStages, buf = q & 1;
+                const bool fresh = of == 0, last = c + 1 == nk || of + 1 == per;
+                if (fresh && q >= 2 && !ready(smem_u32(&sh.acc_empty[buf]), (q / 2 - 1) & 1)) {
+                    ok = false;
+                    break;
+                }
+                if (!both_ready(smem_u32(&sh.b_full[sb]), (n / kBStages) & 1, smem_u32(&sh.full[st]), (n / kStages) & 1)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t d = taddr + buf * kMaxN, at = taddr + kA0 + st * kACols;
-                const uint64_t b = desc0 + static_cast<uint64_t>(st * (kStage >> 4));
+                const uint32_t d = tmem + buf * kMaxN, at = tmem + kA0 + st * kACols;
+                const uint64_t b = desc0 + static_cast<uint64_t>(sb * (kStage >> 4));
                 if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < KC / 16; ++k) {
@@ -413,38 +445,51 @@ tile_kernel(const __grid_constant__ TileMaps maps, const TileArgs a)
                         if constexpr (PB == 2) tc_mma_f16_tmem_a_pair(d, at + 8 * k, bk + (kStage >> 5), idesc, 1);
                     }
                     tc_commit_pair(smem_u32(&sh.empty[st]), 3);
+                    tc_commit_pair(smem_u32(&sh.b_empty[sb]), 3);
                     if (last) tc_commit_pair(smem_u32(&sh.acc_full[buf]), 3);
                 }
-                if (last) ++q;
+                of = last ? 0 : of + 1;
+                q += last;
             }
         }
         // products in flight end before tensor memory is freed; the other block sees their last arrivals as well
-        for (int t = max(0, n - kStages); t < n; ++t) mbar_wait(smem_u32(&sh.empty[t % kStages]), (t / kStages) & 1, a.wait_ns);
+        for (unsigned t = n > kBStages ? n - kBStages : 0; t < n; ++t) mbar_wait(smem_u32(&sh.b_empty[t % kBStages]), (t / kBStages) & 1, a.wait_ns);
+        if (n > 0) mbar_wait(smem_u32(&sh.empty[(n - 1) % kStages]), ((n - 1) / kStages) & 1, a.wait_ns);
         __syncwarp();
     } else if (warp < kDeqWarp) {
-        // the weights' bytes: 16 at a time, neighbours in neighbouring lanes
+        // the weights' bytes, 16 at a time: four lanes a row, eight rows an instruction, 64 rows a warp
         constexpr int UB = unit_bytes(FMT), CH = tile_chunks(FMT);
-        const int me = (warp - 2) * 32 + lane, units = (nk + kParts - 1) / kParts;
+        const int units = (nk + kParts - 1) / kParts, row0 = (warp - 2) * 64 + (lane >> 2), ch0 = lane & 3;
         int n = 0;                                             // units so far
         bool ok = true;
-        for (int64_t item = first; item < items && ok; item += step) {
+        for (int item = first; item < items && ok; item += step) {
             const int expert = set_of(item).expert, tile = tile_of(item);
+            const uint8_t *at[8];
+#pragma unroll
+            for (int o = 0; o < 8; ++o) at[o] = tile_row<PAIRED>(a, expert, tile, row0 + 8 * o);
             for (int u = 0; u < units; ++u, ++n) {
                 const int st = n % kRawStages;
                 if (n >= kRawStages && !tile_wait_warp(smem_u32(&sh.raw_empty[st]), (n / kRawStages - 1) & 1, a, abort)) {
                     ok = false;
                     break;
                 }
-                const uint32_t to = raw_base + st * kRaw;
-#pragma unroll 6
-                for (int q = me; q < 128 * CH; q += 64) {
-                    const int row = q / CH, ch = q - row * CH;
-                    const uint8_t *at = tile_row<PAIRED>(a, expert, tile, row), *from = at + static_cast<int64_t>(u) * UB;
-                    const uint8_t *last = at + a.a.row_bytes, *end = from + UB < last ? from + UB : last;
-                    from -= reinterpret_cast<uintptr_t>(from) & 15;
-                    if (from + 16 * ch < end)
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + row * kPitch + 16 * ch), "l"(from + 16 * ch)
-                                     : "memory");
+                const uint32_t to = raw_base + st * kRaw + row0 * kPitch + 16 * ch0;
+                const int64_t off = static_cast<int64_t>(u) * UB;
+                const int left = static_cast<int>(min(static_cast<int64_t>(UB), a.a.row_bytes - off));      // bytes of the unit
+#pragma unroll
+                for (int o = 0; o < 8; ++o) {
+                    const uint8_t *from = at[o] + off;
+                    int bytes = left - 16 * ch0;               // from this lane's first chunk on
+                    if constexpr (FMT != kFmtQ4K) {
+                        const int skew = static_cast<int>(reinterpret_cast<uintptr_t>(from) & 15);
+                        from -= skew, bytes += skew;
+                    }
+                    from += 16 * ch0;
+#pragma unroll
+                    for (int i = 0; i < (CH + 3) / 4; ++i)
+                        if (16 * 4 * i < bytes)
+                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + 8 * o * kPitch + 64 * i), "l"(from + 64 * i)
+                                         : "memory");
                 }
                 // arrives when this thread's copies have landed
                 asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&sh.raw_full[st])) : "memory");
@@ -455,7 +500,7 @@ tile_kernel(const __grid_constant__ TileMaps maps, const TileArgs a)
         // takes stages' weights apart: group h has every kGroups-th stage of the block's
         const int group = (warp - kDeqWarp) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
         int n = group, it = 0, c = group;
-        int64_t item = first;
+        int item = first;
         while (c >= nk && item < items) c -= nk, ++it, item += step;
         uint32_t start = 0;                                    // low bits of the address of the thread's row
         float up = 0.0f;
@@ -501,14 +546,14 @@ tile_kernel(const __grid_constant__ TileMaps maps, const TileArgs a)
         bool ok = true;
         // the scales of item number i's rows, by the first four warps
         const auto look_over = [&](int i) {
-            const int64_t item = first + i * step;
+            const int item = first + i * step;
             if (part != 0 || item >= items) return;
             sh.row_scale[i & 3][row] = row_scale_of<FMT>(tile_row<PAIRED>(a, set_of(item).expert, tile_of(item), row), a.cols);
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sh.rs_full[i & 3]));
         };
         look_over(0), look_over(1);
-        for (int64_t item = first; item < items && ok; item += step, ++it) {
+        for (int item = first; item < items && ok; item += step, ++it) {
             const ExpertSet s = set_of(item);
             const int tile = tile_of(item);
             float back = 0.0f;
