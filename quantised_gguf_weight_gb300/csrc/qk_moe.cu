@@ -14,7 +14,7 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 // Tokens an expert from which the tile form takes them (qk_moe_tile.cuh).
-constexpr int kTileFrom = 48;
+constexpr int kTileFrom = 16;
 std::atomic<int> g_skip_chunk{-1};
 
 struct PlanArgs {
@@ -218,9 +218,10 @@ __global__ void __launch_bounds__(kPackThreads) pack_kernel(const PackArgs a)
     const float up = __uint_as_float(static_cast<uint32_t>(127 + 141 - ex) << 23);
     const float back = __uint_as_float(static_cast<uint32_t>(127 - 141 + ex) << 23);
     const int64_t unit = octet_unit_bytes(a.fmt, a.pieces);
-    const int places = a.top_k ? a.top_k : 1;
+    // where blocks are few, one a place of the token's
+    const int first = gridDim.y > 1 ? blockIdx.y : 0, places = gridDim.y > 1 ? first + 1 : a.top_k ? a.top_k : 1;
     bool tiled = false;
-    for (int j = 0; j < places; ++j) {
+    for (int j = first; j < places; ++j) {
         const int p = a.top_k ? a.plan.place[r * a.top_k + j] : static_cast<int>(r);
         if (p < 0) continue;
         if (tid == 0) a.scale[p] = back;
@@ -282,7 +283,7 @@ __global__ void __launch_bounds__(kPackThreads) pack_kernel(const PackArgs a)
         v.x *= up, v.y *= up, v.z *= up, v.w *= up;
         uint2 h, l;
         pieces_of(v, h, l);
-        for (int j = 0; j < places; ++j) {
+        for (int j = first; j < places; ++j) {
             const int p = a.top_k ? a.plan.place[r * a.top_k + j] : static_cast<int>(r);
             if (p < 0 || a.plan.column[p] >= 0) continue;
             __half *to = a.tile_out + static_cast<int64_t>(p) * a.tile_cols + k;
@@ -443,8 +444,8 @@ int qk_moe_ffn(const qk_expert_weights *gate, const qk_expert_weights *up, const
     if (st == QK_OK) st = check_weights(up, n_experts, F, K, &wu);
     if (st == QK_OK) st = check_weights(down, n_experts, N, F, &wd);
     if (st != QK_OK) return st;
-    // an item of the many-token form is a tile set and 256 rows of gate and up, or of down
-    if ((static_cast<int64_t>(T) * top_k / 64 + n_experts) * ((std::max(2 * F, N) + 255) / 256) > INT32_MAX) return QK_ERR_TOO_LARGE;
+    // the kernels count items: a set of tokens, and 32 rows of gate and up, or of down
+    if ((static_cast<int64_t>(T) * top_k / 16 + n_experts) * ((std::max(2 * F, N) + 31) / 32) > INT32_MAX) return QK_ERR_TOO_LARGE;
     if (T == 0) return QK_OK;
     if (!x || !ids || !weights || !y) return QK_ERR_NULL;
     if (!multiple(x, size_of(x_type)) || !multiple(y, size_of(y_type)) || !multiple(ids, 4) || !multiple(weights, 4))
@@ -494,7 +495,8 @@ int qk_moe_ffn(const qk_expert_weights *gate, const qk_expert_weights *up, const
         // a thread block a row where rows are few, else a warp
         const int64_t n = per_row ? T : l.A;
         const bool wide = n <= 4LL * sms;
-        return wide ? launch_chained(pack_kernel<kPackThreads / 32>, dim3(static_cast<unsigned>(n)), kPackThreads, 0, s, true, k)
+        return wide ? launch_chained(pack_kernel<kPackThreads / 32>, dim3(static_cast<unsigned>(n), per_row && n * per_row <= 4LL * sms ? per_row : 1),
+                                     kPackThreads, 0, s, true, k)
                     : launch_chained(pack_kernel<1>, dim3(static_cast<unsigned>((n + kPackThreads / 32 - 1) / (kPackThreads / 32))),
                                      kPackThreads, 0, s, true, k);
     };
@@ -518,7 +520,7 @@ int qk_moe_ffn(const qk_expert_weights *gate, const qk_expert_weights *up, const
         r.plan = pa.plan, r.a = a, r.b = b, r.fmt = fmt;
         r.cols = static_cast<int>(cols), r.units = static_cast<int>((cols + kUnit - 1) / kUnit), r.pieces = l.pieces;
         r.rows = static_cast<int>(rows), r.tiles = static_cast<int>(paired ? (rows + 7) / 8 : (rows + 15) / 16);
-        r.sms = sms;
+        r.sms = sms, r.wait_ns = library_wait_limit_ns(), r.err = err;
         r.x = reinterpret_cast<const uint8_t *>(ws + ops), r.scale = reinterpret_cast<const float *>(ws + scale);
         r.out = reinterpret_cast<float *>(ws + to);
         return rows_launch(r, paired, sms, s);

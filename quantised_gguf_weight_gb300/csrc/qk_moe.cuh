@@ -25,7 +25,7 @@ namespace qk {
 namespace moe {
 
 constexpr int kMaxExperts = 1024;
-constexpr int kSetOctets = 4;
+constexpr int kSetOctets = 2;
 constexpr int kTileBoxRows = 32;                  // rows of a TMA box of a tile set's operands
 constexpr int kRowWarps = 8;                      // warps of a thread block of the few-token products
 constexpr int kUnit = 256;                        // columns of a unit of the products' loops
@@ -76,6 +76,8 @@ struct RowsArgs {
     const uint8_t *x;         // operands, octet after octet
     const float *scale;
     float *out;               // [place][rows]
+    uint64_t wait_ns;
+    int *err;
 };
 
 struct TileArgs {

@@ -13,20 +13,33 @@
 // are is free as long as both operands agree, so that a lane's values lie
 // together in the block (operands are laid out to match, qk_moe.cu).
 //
-// A warp takes a tile of 16 rows (8 gate rows and their 8 up rows, so that a
-// lane has both sums of an output), or a part of its columns where tiles are
-// few; its weights come through a ring of its own in shared memory, 16 bytes an
-// asynchronous copy, so nothing waits for other warps.
+// A warp takes two tiles of 16 rows (8 gate rows and their 8 up rows each, so
+// that a lane has both sums of an output), or a part of their columns where
+// tiles are few.  Its weights come through a ring of its own in shared memory,
+// 16 bytes an asynchronous copy, which runs on from one item to the next; the
+// tokens' operands come through a ring that the thread block's warps share, one
+// bulk copy an octet and unit.  (With operands read through L1 instead, 8 KB for
+// every 2.3 KB of weights, 64 tokens of 8 of 128 experts took 132 us for gate and
+// up.)
 #pragma once
 
+#include <type_traits>
+
 #include "qk_moe.cuh"
+#include "qk_tc.cuh"
 
 namespace qk {
 namespace moe {
 
+constexpr int kRowTiles = 2;                      // 16-row tiles of a warp
 // Shared-memory pitch of a row's unit: 16-byte chunks that hold it wherever it starts.  Q4_K's starts on one.
 __host__ __device__ constexpr int row_pitch(int fmt) { return fmt == kFmtQ4K ? 144 : fmt == kFmtQ80 ? 288 : 224; }
-__host__ __device__ constexpr int ring_stages(int fmt) { return fmt == kFmtQ4K ? 4 : fmt == kFmtQ80 ? 2 : 3; }
+__host__ __device__ constexpr int row_chunks(int fmt) { return fmt == kFmtQ4K ? 9 : fmt == kFmtQ80 ? 18 : 14; }
+__host__ __device__ constexpr int ring_stages(int fmt) { return fmt == kFmtQ4K ? 3 : 2; }
+constexpr int kOpStages = 4;                      // units of the tokens' operands
+__host__ __device__ constexpr int ring_bytes(int fmt) { return ring_stages(fmt) * kRowTiles * 16 * row_pitch(fmt); }
+__host__ __device__ constexpr int op_bytes(int fmt, int P) { return kSetOctets * static_cast<int>(octet_unit_bytes(fmt, P)); }
+__host__ __device__ constexpr int rows_smem(int fmt, int P) { return kRowWarps * ring_bytes(fmt) + kOpStages * op_bytes(fmt, P); }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src)
 {
@@ -89,285 +102,416 @@ __device__ __forceinline__ uint32_t lds32_2(uint32_t p)
     return __funnelshift_r(lds32(q), lds32(q + 4), (p & 2u) * 8);
 }
 
-// Operand words of an octet's unit: step i of piece p.
-__device__ __forceinline__ uint4 operand(const uint8_t *unit, int p, int i, int lane)
-{
-    return __ldg(reinterpret_cast<const uint4 *>(unit + p * kPieceBytes + i * 512 + lane * 16));
-}
-
-// The products of one unit (256 columns): total[n] += rows (g, g + 8) x octet n's columns.
-// st: the tile's unit in shared memory; al[2]: byte offsets of rows g and g + 8 inside their chunks.
+// The products of one unit (256 columns): total[m][n] += rows (g, g + 8) of tile m x octet n's columns.
+// st: the tiles' unit in shared memory; al[m][2]: byte offsets of rows g and g + 8 inside their chunks; x: the octets'
+// operands, step i of piece p at 512 i + 4096 p.
 template <int FMT, int P, int NT>
-__device__ __forceinline__ void unit_products(float (&total)[NT][4], uint32_t st, const uint32_t (&al)[2], int blocks,
-                                              const uint8_t *x, int64_t octet_bytes, int lane)
+__device__ __forceinline__ void unit_products(float (&total)[kRowTiles][NT][4], uint32_t st, const uint32_t (&al)[kRowTiles][2],
+                                              int blocks, uint32_t x, int lane)
 {
+    constexpr int M = kRowTiles, OB = static_cast<int>(octet_unit_bytes(FMT, P));
     const int g = lane >> 2, c = lane & 3;
-    const uint32_t row0 = st + g * row_pitch(FMT) + al[0], row1 = st + (g + 8) * row_pitch(FMT) + al[1];
+    x += lane * 16;
+    const auto row = [&](int m, int r) { return st + (16 * m + 8 * r + g) * row_pitch(FMT) + al[m][r]; };
     if constexpr (FMT == kFmtQ4K) {
-        // lane c has sub-blocks 2c and 2c + 1: 32 bytes of nibbles
-        float dd[2], dm[2];
-        __half2 sl[2], sb[2], shi[2], shb[2];     // scale of the low nibbles' sub-block, -1024 of it; high: / 16, -64
-        uint32_t m[2];
+        // lane c has sub-blocks 2c and 2c + 1: 32 bytes of nibbles.  The low and the high nibbles' products are summed apart:
+        // the tensor cores cut a sum at 2^-24 of it, so short sums are the more exact.
+        float dd[M][2], dm[M][2];
+        __half2 sl[M][2], sb[M][2], shi[M][2], shb[M][2];     // scale of the low nibbles' sub-block, -1024 of it; high: / 16, -64
+        float acc[M][NT][2][4], low[M][NT][4];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const uint4 h = lds128(r ? row1 : row0);
-            const float2 d2 = __half22float2(bits_h2(h.x));
-            dd[r] = d2.x, dm[r] = d2.y;
-            const int sh = (c & 1) * 16;
-            const uint32_t A = h.y >> sh, B = h.z >> sh, C = h.w >> sh;
-            const uint32_t sc = c < 2 ? A & 0x3f3fu : (C & 0x0f0fu) | ((A >> 2) & 0x3030u);
-            const uint32_t mm = c < 2 ? B & 0x3f3fu : ((C >> 4) & 0x0f0fu) | ((B >> 2) & 0x3030u);
-            const __half2 k1024 = __float2half2_rn(1024.0f);
-            const __half2 s0 = __hsub2(bits_h2(__byte_perm(sc, 0x64u, 0x4040)), k1024);
-            const __half2 s1 = __hsub2(bits_h2(__byte_perm(sc, 0x64u, 0x4141)), k1024);
-            sl[r] = s0, sb[r] = __hmul2(s0, __float2half2_rn(-1024.0f));
-            shi[r] = __hmul2(s1, __float2half2_rn(0.0625f)), shb[r] = __hmul2(s1, __float2half2_rn(-64.0f));
-            m[r] = h2_bits(__hmul2(__hsub2(bits_h2(__byte_perm(mm, 0x64u, 0x4140)), k1024), __float2half2_rn(32.0f)));
-        }
-        float acc[NT][4], low[NT][4];
+        for (int t = 0; t < M; ++t) {
+            uint32_t m[2];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[n][j] = low[n][j] = 0.0f;
-            const uint2 s = __ldg(reinterpret_cast<const uint2 *>(x + n * octet_bytes + P * kPieceBytes + lane * 8));
+            for (int r = 0; r < 2; ++r) {
+                const uint4 h = lds128(row(t, r));
+                const float2 d2 = __half22float2(bits_h2(h.x));
+                dd[t][r] = d2.x, dm[t][r] = d2.y;
+                const int sh = (c & 1) * 16;
+                const uint32_t A = h.y >> sh, B = h.z >> sh, C = h.w >> sh;
+                const uint32_t sc = c < 2 ? A & 0x3f3fu : (C & 0x0f0fu) | ((A >> 2) & 0x3030u);
+                const uint32_t mm = c < 2 ? B & 0x3f3fu : ((C >> 4) & 0x0f0fu) | ((B >> 2) & 0x3030u);
+                const __half2 k1024 = __float2half2_rn(1024.0f);
+                const __half2 s0 = __hsub2(bits_h2(__byte_perm(sc, 0x64u, 0x4040)), k1024);
+                const __half2 s1 = __hsub2(bits_h2(__byte_perm(sc, 0x64u, 0x4141)), k1024);
+                sl[t][r] = s0, sb[t][r] = __hmul2(s0, __float2half2_rn(-1024.0f));
+                shi[t][r] = __hmul2(s1, __float2half2_rn(0.0625f)), shb[t][r] = __hmul2(s1, __float2half2_rn(-64.0f));
+                m[r] = h2_bits(__hmul2(__hsub2(bits_h2(__byte_perm(mm, 0x64u, 0x4140)), k1024), __float2half2_rn(32.0f)));
+            }
             const uint32_t a[4] = {m[0], m[1], m[0], m[1]};
-            mma16(low[n], a, s.x, s.y);
-        }
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const uint4 w0 = lds128(row0 + 16 + 32 * c + 16 * q), w1 = lds128(row1 + 16 + 32 * c + 16 * q);
-            const uint32_t v0[4] = {w0.x, w0.y, w0.z, w0.w}, v1[4] = {w1.x, w1.y, w1.z, w1.w};
+            for (int n = 0; n < NT; ++n) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const uint32_t a[4] = {h2_bits(__hfma2(field1024<0x000f000f>(v0[k]), sl[0], sb[0])),
-                                       h2_bits(__hfma2(field1024<0x000f000f>(v1[k]), sl[1], sb[1])),
-                                       h2_bits(__hfma2(field1024<0x000f000f>(v0[k] >> 8), sl[0], sb[0])),
-                                       h2_bits(__hfma2(field1024<0x000f000f>(v1[k] >> 8), sl[1], sb[1]))};
-                const uint32_t b[4] = {h2_bits(__hfma2(field1024<0x00f000f0>(v0[k]), shi[0], shb[0])),
-                                       h2_bits(__hfma2(field1024<0x00f000f0>(v1[k]), shi[1], shb[1])),
-                                       h2_bits(__hfma2(field1024<0x00f000f0>(v0[k] >> 8), shi[0], shb[0])),
-                                       h2_bits(__hfma2(field1024<0x00f000f0>(v1[k] >> 8), shi[1], shb[1]))};
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int p = 0; p < P; ++p) {
-                        const uint4 o = operand(x + n * octet_bytes, p, 4 * q + k, lane);
-                        mma16(acc[n], a, o.x, o.y);
-                        mma16(acc[n], b, o.z, o.w);
-                    }
+                for (int j = 0; j < 4; ++j) acc[t][n][0][j] = acc[t][n][1][j] = low[t][n][j] = 0.0f;
+                const uint32_t at = x - lane * 8 + n * OB + P * kPieceBytes;
+                mma16(low[t][n], a, lds32(at), lds32(at + 4));
             }
         }
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int q = 0; q < 2; ++q) {
+            uint4 w[M][2];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                total[n][j] += dd[j >> 1] * acc[n][j] - dm[j >> 1] * low[n][j];
+            for (int t = 0; t < M; ++t)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) w[t][r] = lds128(row(t, r) + 16 + 32 * c + 16 * q);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                uint4 o[NT][P];
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int p = 0; p < P; ++p) o[n][p] = lds128(x + n * OB + p * kPieceBytes + (4 * q + k) * 512);
+#pragma unroll
+                for (int t = 0; t < M; ++t) {
+                    const uint32_t v0 = k == 0 ? w[t][0].x : k == 1 ? w[t][0].y : k == 2 ? w[t][0].z : w[t][0].w;
+                    const uint32_t v1 = k == 0 ? w[t][1].x : k == 1 ? w[t][1].y : k == 2 ? w[t][1].z : w[t][1].w;
+                    const uint32_t a[4] = {h2_bits(__hfma2(field1024<0x000f000f>(v0), sl[t][0], sb[t][0])),
+                                           h2_bits(__hfma2(field1024<0x000f000f>(v1), sl[t][1], sb[t][1])),
+                                           h2_bits(__hfma2(field1024<0x000f000f>(v0 >> 8), sl[t][0], sb[t][0])),
+                                           h2_bits(__hfma2(field1024<0x000f000f>(v1 >> 8), sl[t][1], sb[t][1]))};
+                    const uint32_t b[4] = {h2_bits(__hfma2(field1024<0x00f000f0>(v0), shi[t][0], shb[t][0])),
+                                           h2_bits(__hfma2(field1024<0x00f000f0>(v1), shi[t][1], shb[t][1])),
+                                           h2_bits(__hfma2(field1024<0x00f000f0>(v0 >> 8), shi[t][0], shb[t][0])),
+                                           h2_bits(__hfma2(field1024<0x00f000f0>(v1 >> 8), shi[t][1], shb[t][1]))};
+#pragma unroll
+                    for (int p = 0; p < P; ++p)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            mma16(acc[t][n][0], a, o[n][p].x, o[n][p].y);
+                            mma16(acc[t][n][1], b, o[n][p].z, o[n][p].w);
+                        }
+                }
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < M; ++t)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    total[t][n][j] += dd[t][j >> 1] * (acc[t][n][0][j] + acc[t][n][1][j]) - dm[t][j >> 1] * low[t][n][j];
     } else if constexpr (FMT == kFmtQ80) {
         const __half2 bias = __float2half2_rn(1152.0f);
         const auto pair = [&](uint32_t v, int sel) { return h2_bits(__hsub2(bits_h2(__byte_perm(v, 0x64u, sel)), bias)); };
 #pragma unroll 2
         for (int i = 0; i < blocks; ++i) {
-            uint32_t v[2][2];
-            float dd[2];
+            uint4 o[NT][P];
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const uint32_t blk = (r ? row1 : row0) + 34 * i;
-                dd[r] = half_bits_to_float(lds16(blk));
-                const uint32_t p = blk + 2 + 8 * c, q = p & ~3u, sh = (p & 2u) * 8;
-                const uint32_t w0 = lds32(q), w1 = lds32(q + 4), w2 = sh ? lds32(q + 8) : 0u;
-                v[r][0] = __funnelshift_r(w0, w1, sh) ^ 0x80808080u, v[r][1] = __funnelshift_r(w1, w2, sh) ^ 0x80808080u;
-            }
-            const uint32_t a[4] = {pair(v[0][0], 0x4240), pair(v[1][0], 0x4240), pair(v[0][0], 0x4341), pair(v[1][0], 0x4341)};
-            const uint32_t b[4] = {pair(v[0][1], 0x4240), pair(v[1][1], 0x4240), pair(v[0][1], 0x4341), pair(v[1][1], 0x4341)};
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                for (int p = 0; p < P; ++p) o[n][p] = lds128(x + n * OB + p * kPieceBytes + i * 512);
 #pragma unroll
-                for (int p = 0; p < P; ++p) {
-                    const uint4 o = operand(x + n * octet_bytes, p, i, lane);
-                    mma16(acc, a, o.x, o.y);
-                    mma16(acc, b, o.z, o.w);
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) total[n][j] += dd[j >> 1] * acc[j];
-            }
-        }
-    } else {
-        const __half2 bias = __float2half2_rn(1056.0f);
-        const auto pair = [&](uint32_t v, int sel) { return h2_bits(__hsub2(bits_h2(__byte_perm(v, 0x64u, sel)), bias)); };
-        const float dd[2] = {half_bits_to_float(lds16(row0 + 208)), half_bits_to_float(lds16(row1 + 208))};
-#pragma unroll 1
-        for (int hu = 0; hu < 4; ++hu) {             // half n = hu / 2, 16 positions u = hu % 2
-            uint32_t A[2], B[2], H[2];
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const uint32_t blk = (r ? row1 : row0) + 16 * (hu & 1) + 4 * c;
-                A[r] = lds32_2(blk + 64 * (hu >> 1)), B[r] = lds32_2(blk + 64 * (hu >> 1) + 32);
-                H[r] = lds32_2(blk + 128 + 32 * (hu >> 1));
-            }
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                uint32_t v[2];
-                float ds[2];
+            for (int t = 0; t < M; ++t) {
+                uint32_t v[2][2];
+                float dd[2];
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    const uint32_t lowb = ((t & 1 ? B[r] : A[r]) >> (t & 2 ? 4 : 0)) & 0x0f0f0f0fu;
-                    const uint32_t high = (t < 2 ? H[r] << (4 - 2 * t) : H[r] >> (2 * t - 4)) & 0x30303030u;
-                    v[r] = lowb | high;
-                    ds[r] = dd[r] * lds_s8((r ? row1 : row0) + 192 + 8 * (hu >> 1) + 2 * t + (hu & 1));
+                    const uint32_t blk = row(t, r) + 34 * i;
+                    dd[r] = half_bits_to_float(lds16(blk));
+                    const uint32_t p = blk + 2 + 8 * c, q = p & ~3u, sh = (p & 2u) * 8;
+                    const uint32_t w0 = lds32(q), w1 = lds32(q + 4), w2 = sh ? lds32(q + 8) : 0u;
+                    v[r][0] = __funnelshift_r(w0, w1, sh) ^ 0x80808080u, v[r][1] = __funnelshift_r(w1, w2, sh) ^ 0x80808080u;
                 }
-                const uint32_t a[4] = {pair(v[0], 0x4240), pair(v[1], 0x4240), pair(v[0], 0x4341), pair(v[1], 0x4341)};
+                const uint32_t a[4] = {pair(v[0][0], 0x4240), pair(v[1][0], 0x4240), pair(v[0][0], 0x4341), pair(v[1][0], 0x4341)};
+                const uint32_t b[4] = {pair(v[0][1], 0x4240), pair(v[1][1], 0x4240), pair(v[0][1], 0x4341), pair(v[1][1], 0x4341)};
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                     for (int p = 0; p < P; ++p) {
-                        const uint4 o = operand(x + n * octet_bytes, p, 2 * hu + (t >> 1), lane);
-                        mma16(acc, a, t & 1 ? o.z : o.x, t & 1 ? o.w : o.y);
+                        mma16(acc, a, o[n][p].x, o[n][p].y);
+                        mma16(acc, b, o[n][p].z, o[n][p].w);
                     }
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) total[n][j] += ds[j >> 1] * acc[j];
+                    for (int j = 0; j < 4; ++j) total[t][n][j] += dd[j >> 1] * acc[j];
+                }
+            }
+        }
+    } else {
+        const __half2 bias = __float2half2_rn(1056.0f);
+        const auto pair = [&](uint32_t v, int sel) { return h2_bits(__hsub2(bits_h2(__byte_perm(v, 0x64u, sel)), bias)); };
+        float dd[M][2];
+#pragma unroll
+        for (int t = 0; t < M; ++t)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) dd[t][r] = half_bits_to_float(lds16(row(t, r) + 208));
+#pragma unroll 1
+        for (int hu = 0; hu < 4; ++hu) {             // half n = hu / 2, 16 positions u = hu % 2
+            uint4 o[NT][P][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int p = 0; p < P; ++p)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) o[n][p][k] = lds128(x + n * OB + p * kPieceBytes + (2 * hu + k) * 512);
+#pragma unroll
+            for (int s = 0; s < M; ++s) {
+                uint32_t A[2], B[2], H[2];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const uint32_t blk = row(s, r) + 16 * (hu & 1) + 4 * c;
+                    A[r] = lds32_2(blk + 64 * (hu >> 1)), B[r] = lds32_2(blk + 64 * (hu >> 1) + 32);
+                    H[r] = lds32_2(blk + 128 + 32 * (hu >> 1));
+                }
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    uint32_t v[2];
+                    float ds[2];
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const uint32_t lowb = ((t & 1 ? B[r] : A[r]) >> (t & 2 ? 4 : 0)) & 0x0f0f0f0fu;
+                        const uint32_t high = (t < 2 ? H[r] << (4 - 2 * t) : H[r] >> (2 * t - 4)) & 0x30303030u;
+                        v[r] = lowb | high;
+                        ds[r] = dd[s][r] * lds_s8(row(s, r) + 192 + 8 * (hu >> 1) + 2 * t + (hu & 1));
+                    }
+                    const uint32_t a[4] = {pair(v[0], 0x4240), pair(v[1], 0x4240), pair(v[0], 0x4341), pair(v[1], 0x4341)};
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                        for (int p = 0; p < P; ++p) {
+                            const uint4 q = o[n][p][t >> 1];
+                            mma16(acc, a, t & 1 ? q.z : q.x, t & 1 ? q.w : q.y);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) total[s][n][j] += ds[j >> 1] * acc[j];
+                    }
                 }
             }
         }
     }
 }
 
-// One tile's units [u0, u1) for a set of NT octets.
-template <int FMT, int P, int NT>
-__device__ __forceinline__ void tile_products(float (&total)[NT][4], const RowsArgs &a, const uint8_t *mine,
-                                              const uint32_t (&al)[2], uint32_t ring, int u0, int u1, int octet, int lane)
+struct RowsShared {
+    uint64_t full[kOpStages], empty[kOpStages];
+    float join[kRowWarps * kRowTiles * kSetOctets * 4 * 32];
+    int abort;
+    int failed;                // a computing warp has left its units; written before the parts' barrier only
+};
+
+// A bounded wait of a whole warp; one that runs out ends every other of the block.
+__device__ __forceinline__ bool rows_wait(uint32_t bar, uint32_t parity, const RowsArgs &a, volatile int *abort)
 {
-    constexpr int S = ring_stages(FMT), UB = unit_bytes(FMT), PITCH = row_pitch(FMT), CH = PITCH / 16;
-    const int64_t ub = octet_unit_bytes(FMT, P), octet_bytes = ub * a.units;
-    const uint8_t *x = a.x + octet * octet_bytes;
-    const int r = lane >> 1, half = lane & 1;
-    const uint8_t *row_end = mine + a.a.row_bytes;
-    const uint32_t dst = ring + r * PITCH;
-    const auto fetch = [&](int u, int slot) {
-        const uint8_t *from = mine + static_cast<int64_t>(u) * UB;
-        const uint8_t *end = from + UB < row_end ? from + UB : row_end;
-        from -= reinterpret_cast<uintptr_t>(from) & 15;
-#pragma unroll
-        for (int i = 0; i < (CH + 1) / 2; ++i) {
-            const int ch = 2 * i + half;
-            if (ch < CH && from + 16 * ch < end) cp_async16(dst + slot * 16 * PITCH + 16 * ch, from + 16 * ch);
-        }
-    };
-#pragma unroll
-    for (int i = 0; i < S - 1; ++i) {
-        if (u0 + i < u1) fetch(u0 + i, i);
-        cp_async_commit();
+    bool ok = mbar_try_wait(bar, parity);
+    if (!ok) {
+        const uint64_t deadline = globaltimer_ns() + a.wait_ns;
+        for (uint32_t i = 1; !*abort && !(ok = mbar_try_wait(bar, parity)); ++i)
+            if ((i & 31u) == 0 && globaltimer_ns() > deadline) {
+                *abort = 1;
+                record_error(a.err, kErrTimeout);
+            }
     }
-    int slot = 0;
-    uint32_t at[2] = {al[0], al[1]};
-    for (int u = u0; u < u1; ++u) {
-        cp_async_wait<S - 2>();
-        __syncwarp();                // everyone's copies of this unit have landed, and the slot before it is free
-        const int next = u + S - 1, into = slot == 0 ? S - 1 : slot - 1;
-        if (next < u1) fetch(next, into);
-        cp_async_commit();
-        // a unit of Q6_K is no whole number of chunks
-        if constexpr (UB % 16 != 0) at[0] = (al[0] + u * UB) & 15, at[1] = (al[1] + u * UB) & 15;
-        const int blocks = FMT == kFmtQ80 ? min(8, (a.cols + 31) / 32 - 8 * u) : 8;
-        unit_products<FMT, P, NT>(total, ring + slot * 16 * PITCH, at, blocks, x + u * ub, octet_bytes, lane);
-        slot = slot + 1 == S ? 0 : slot + 1;
-    }
-    cp_async_wait<0>();
-    __syncwarp();
+    return __all_sync(~0u, ok);
 }
 
-template <int FMT, int P, bool PAIRED, int NT>
-__device__ __forceinline__ void set_tile(const RowsArgs &a, const ExpertSet &s, int tile, int part, int kw, uint32_t ring,
-                                         float *join, int lane, int warp)
-{
-    const int g = lane >> 2, c = lane & 3, r = lane >> 1;
-    float total[NT][4];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) total[n][j] = 0.0f;
-    if (tile < a.tiles) {
-        // rows past the last are read as the last and not written
-        const auto row_of = [&](int i) -> const uint8_t * {
-            const int row = PAIRED ? min(tile * 8 + (i & 7), a.rows - 1) : min(tile * 16 + i, a.rows - 1);
-            const Weights &w = i < 8 ? a.a : a.b;
-            return w.w + (s.expert * w.expert_rows + row) * w.row_bytes;
-        };
-        const uint32_t al[2] = {static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row_of(g)) & 15),
-                                static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row_of(g + 8)) & 15)};
-        const int u0 = a.units * part / kw, u1 = a.units * (part + 1) / kw;
-        tile_products<FMT, P, NT>(total, a, row_of(r), al, ring, u0, u1, s.octet, lane);
-    }
-    if (kw > 1) {
-        // parts of a tile, added in their order
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) join[((warp * NT + n) * 4 + j) * 32 + lane] = total[n][j];
-        __syncthreads();
-        if (part == 0)
-            for (int k = 1; k < kw; ++k)
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) total[n][j] += join[(((warp + k) * NT + n) * 4 + j) * 32 + lane];
-        __syncthreads();
-        if (part != 0) return;
-    }
-    if (tile >= a.tiles) return;
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int col = n * 8 + 2 * c + j;
-            if (col >= s.count) continue;
-            const int64_t place = s.first + col;
-            const float back = a.scale[place];
-            float *out = a.out + place * a.rows;
-            if constexpr (PAIRED) {
-                const int row = tile * 8 + g;
-                if (row < a.rows) out[row] = silu(total[n][j] * back) * (total[n][2 + j] * back);
-            } else {
-                const int row = tile * 16 + g;
-                if (row < a.rows) out[row] = total[n][j] * back;
-                if (row + 8 < a.rows) out[row + 8] = total[n][2 + j] * back;
-            }
-        }
-}
+// How a launch's sets and tiles are shared out: items of one set and `per` pairs of tiles, kw warps a pair.
+struct Share {
+    int kw, per, blocks, items;
+};
+
+// A warp's way through its items' units: item, the pair of tiles in it, the units [u, u1) left of it.
+struct Cursor {
+    int item, u, u1;
+};
 
 template <int FMT, int P, bool PAIRED>
-__global__ void __launch_bounds__(kRowWarps * 32, 2) rows_kernel(const RowsArgs a)
+__global__ void __launch_bounds__((kRowWarps + 1) * 32, 1) rows_kernel(const RowsArgs a)
 {
+    constexpr int S = ring_stages(FMT), UB = unit_bytes(FMT), PITCH = row_pitch(FMT), CH = row_chunks(FMT), M = kRowTiles;
+    constexpr int OB = static_cast<int>(octet_unit_bytes(FMT, P)), OPS = op_bytes(FMT, P), SLOT = M * 16 * PITCH;
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ float join[kRowWarps * kSetOctets * 4 * 32];
+    __shared__ RowsShared sh;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t ring = smem_u32(smem) + warp * ring_stages(FMT) * 16 * row_pitch(FMT);
+    volatile int *abort = &sh.abort;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kOpStages; ++i) mbar_init(smem_u32(&sh.full[i]), 1), mbar_init(smem_u32(&sh.empty[i]), kRowWarps);
+        sh.abort = sh.failed = 0;
+        fence_barrier_init();
+    }
+    __syncthreads();
     let_next_start();
     wait_for_previous();
-    // warps that share a tile's units: enough for every SM's 16 warps to have work where tiles are few
-    const int64_t sets = a.plan.head[0];
+    // warps that share a pair's units: enough for every SM's warps to have work where pairs are few
+    const int sets = a.plan.head[0], pairs = (a.tiles + M - 1) / M;
     int kw = 1;
-    while (kw < kRowWarps && 2 * kw <= a.units && sets * a.tiles * kw < 16 * a.sms) kw *= 2;
-    const int per = kRowWarps / kw, blocks = (a.tiles + per - 1) / per;
-    const int64_t items = sets * blocks;
-    for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
-        const ExpertSet s = a.plan.sets[i / blocks];
-        const int tile = static_cast<int>(i % blocks) * per + warp / kw, part = warp % kw;
-        if (s.count <= 8) set_tile<FMT, P, PAIRED, 1>(a, s, tile, part, kw, ring, join, lane, warp);
-        else if (s.count <= 16) set_tile<FMT, P, PAIRED, 2>(a, s, tile, part, kw, ring, join, lane, warp);
-        else set_tile<FMT, P, PAIRED, 4>(a, s, tile, part, kw, ring, join, lane, warp);
+    while (kw < kRowWarps && 2 * kw <= a.units && static_cast<int64_t>(sets) * pairs * kw < kRowWarps * a.sms) kw *= 2;
+    const int per = kRowWarps / kw, blocks = (pairs + per - 1) / per, items = sets * blocks;      // (the caller sees to 31 bits)
+    const uint32_t ops = smem_u32(smem) + kRowWarps * ring_bytes(FMT);
+
+    if (warp == kRowWarps) {
+        // the tokens' operands, every unit of every item
+        const uint64_t keep = l2_evict_last_policy();
+        int n = 0;
+        for (int item = blockIdx.x; item < items; item += gridDim.x) {
+            const ExpertSet s = a.plan.sets[item / blocks];
+            const int octets = (s.count + 7) / 8;
+            bool ok = true;
+            for (int u = 0; u < a.units && ok; ++u, ++n) {
+                const int st = n % kOpStages;
+                if (n >= kOpStages && !(ok = rows_wait(smem_u32(&sh.empty[st]), (n / kOpStages - 1) & 1, a, abort))) break;
+                if (lane == 0) {
+                    const uint32_t bar = smem_u32(&sh.full[st]);
+                    mbar_arrive_expect_tx(bar, octets * OB);
+                    for (int o = 0; o < octets; ++o)
+                        bulk_g2s(ops + st * OPS + o * OB, a.x + (static_cast<int64_t>(s.octet + o) * a.units + u) * OB, OB, bar, keep);
+                }
+                __syncwarp();
+            }
+            if (!ok) break;
+        }
+        for (int t = max(0, n - kOpStages); t < n; ++t) mbar_wait(smem_u32(&sh.full[t % kOpStages]), (t / kOpStages) & 1, a.wait_ns);
+        return;
     }
+
+    const int g = lane >> 2, c = lane & 3, part = warp % kw;
+    const uint32_t ring = smem_u32(smem) + warp * ring_bytes(FMT);
+    const int u0 = a.units * part / kw, u1 = a.units * (part + 1) / kw;
+    const auto pair_of = [&](int item) { return item % blocks * per + warp / kw; };
+    // rows past the last are read as the last and not written; row i of a pair's 32
+    const auto row_of = [&](int expert, int pair, int i) -> const uint8_t * {
+        const int tile = pair * M + (i >> 4), row = PAIRED ? min(tile * 8 + (i & 7), a.rows - 1) : min(tile * 16 + (i & 15), a.rows - 1);
+        const Weights &w = i & 8 ? a.b : a.a;
+        return w.w + (expert * w.expert_rows + row) * w.row_bytes;
+    };
+
+    // what is fetched runs S - 1 units ahead of what is computed, over the ends of items
+    Cursor f = {static_cast<int>(blockIdx.x), u0, u1};
+    const uint8_t *from[4];
+    int slot_in = 0;
+    const auto aim = [&]() {
+        if (f.item >= items) return;
+        const int expert = a.plan.sets[f.item / blocks].expert, pair = pair_of(f.item);
+#pragma unroll
+        for (int o = 0; o < 4; ++o) from[o] = row_of(expert, pair, 8 * o + (lane >> 2));
+    };
+    aim();
+    const auto fetch = [&]() {
+        if (f.item < items && pair_of(f.item) < pairs) {
+            const int64_t off = static_cast<int64_t>(f.u) * UB;
+            const int left = static_cast<int>(min(static_cast<int64_t>(UB), a.a.row_bytes - off)) - 16 * c;
+            const uint32_t to = ring + slot_in * SLOT + (lane >> 2) * PITCH + 16 * c;
+#pragma unroll
+            for (int o = 0; o < 4; ++o) {
+                const uint8_t *p = from[o] + off;
+                int bytes = left;
+                if constexpr (FMT != kFmtQ4K) {
+                    const int skew = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15);
+                    p -= skew, bytes += skew;
+                }
+                p += 16 * c;
+#pragma unroll
+                for (int i = 0; i < (CH + 3) / 4; ++i)
+                    if (64 * i < bytes) cp_async16(to + 8 * o * PITCH + 64 * i, p + 64 * i);
+            }
+        }
+        cp_async_commit();
+        slot_in = slot_in + 1 == S ? 0 : slot_in + 1;
+        if (++f.u >= f.u1 && f.item < items) f.item += gridDim.x, f.u = u0, aim();
+    };
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) fetch();
+
+    int slot = 0, n = 0;
+    const auto run = [&](auto nt, const ExpertSet &s, int pair) -> bool {
+        constexpr int NT = decltype(nt)::value;
+        float total[M][NT][4];
+#pragma unroll
+        for (int t = 0; t < M; ++t)
+#pragma unroll
+            for (int k = 0; k < NT; ++k)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) total[t][k][j] = 0.0f;
+        uint32_t start[M][2];
+#pragma unroll
+        for (int t = 0; t < M; ++t)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) start[t][r] = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row_of(s.expert, pair, 16 * t + 8 * r + g)) & 15);
+        bool ok = true;
+        for (int u = 0; u < a.units; ++u, ++n) {
+            const int st = n % kOpStages;
+            const bool mine = u >= u0 && u < u1;
+            if (mine) cp_async_wait<S - 2>();
+            if (!(ok = rows_wait(smem_u32(&sh.full[st]), (n / kOpStages) & 1, a, abort))) break;
+            if (mine) {
+                __syncwarp();                // everyone's copies of this unit have landed, and the slot before it is free
+                fetch();
+                if (pair < pairs) {
+                    uint32_t al[M][2];
+#pragma unroll
+                    for (int t = 0; t < M; ++t)
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) al[t][r] = (start[t][r] + (UB % 16 ? u * UB : 0)) & 15;
+                    const int in_row = FMT == kFmtQ80 ? min(8, (a.cols + 31) / 32 - 8 * u) : 8;
+                    unit_products<FMT, P, NT>(total, ring + slot * SLOT, al, in_row, ops + st * OPS, lane);
+                }
+                slot = slot + 1 == S ? 0 : slot + 1;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sh.empty[st]));
+        }
+        if (kw == 1 && !ok) return false;
+        if (kw > 1) {
+            // parts of a pair, added in their order; a warp that gave up comes to the barriers, too, and takes all along
+            if (!ok) *static_cast<volatile int *>(&sh.failed) = 1;
+            float *join = sh.join + warp * (M * kSetOctets * 4 * 32) + lane;
+#pragma unroll
+            for (int t = 0; t < M; ++t)
+#pragma unroll
+                for (int k = 0; k < NT; ++k)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) join[((t * NT + k) * 4 + j) * 32] = total[t][k][j];
+            named_bar_sync(1, kRowWarps * 32);
+            ok = *static_cast<volatile int *>(&sh.failed) == 0;
+            if (part == 0)
+                for (int w = 1; w < kw; ++w)
+#pragma unroll
+                    for (int t = 0; t < M; ++t)
+#pragma unroll
+                        for (int k = 0; k < NT; ++k)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) total[t][k][j] += join[w * (M * kSetOctets * 4 * 32) + ((t * NT + k) * 4 + j) * 32];
+            named_bar_sync(1, kRowWarps * 32);
+            if (part != 0 || !ok) return ok;
+        }
+        if (pair >= pairs) return true;
+#pragma unroll
+        for (int t = 0; t < M; ++t)
+#pragma unroll
+            for (int k = 0; k < NT; ++k)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int col = k * 8 + 2 * c + j;
+                    if (col >= s.count) continue;
+                    const int64_t place = s.first + col;
+                    const float back = a.scale[place];
+                    float *out = a.out + place * a.rows;
+                    if constexpr (PAIRED) {
+                        const int row = (pair * M + t) * 8 + g;
+                        if (row < a.rows) out[row] = silu(total[t][k][j] * back) * (total[t][k][2 + j] * back);
+                    } else {
+                        const int row = (pair * M + t) * 16 + g;
+                        if (row < a.rows) out[row] = total[t][k][j] * back;
+                        if (row + 8 < a.rows) out[row + 8] = total[t][k][2 + j] * back;
+                    }
+                }
+        return true;
+    };
+    for (int item = blockIdx.x; item < items; item += gridDim.x) {
+        const ExpertSet s = a.plan.sets[item / blocks];
+        const int pair = pair_of(item);
+        if (!(s.count <= 8 ? run(std::integral_constant<int, 1>{}, s, pair) : run(std::integral_constant<int, kSetOctets>{}, s, pair))) break;
+    }
+    cp_async_wait<0>();
 }
 
 template <int FMT, int P, bool PAIRED>
 cudaError_t rows_launch_as(const RowsArgs &a, int sms, cudaStream_t st)
 {
-    constexpr size_t smem = kRowWarps * ring_stages(FMT) * 16 * row_pitch(FMT);
+    constexpr size_t smem = rows_smem(FMT, P);
     const auto kern = rows_kernel<FMT, P, PAIRED>;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
-    return launch_chained(kern, dim3(2 * sms), kRowWarps * 32, smem, st, true, a);
+    return launch_chained(kern, dim3(sms), (kRowWarps + 1) * 32, smem, st, true, a);
 }
 
 template <int FMT>
