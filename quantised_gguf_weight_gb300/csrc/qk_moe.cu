@@ -116,19 +116,29 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a)
             }
         }
     }
-    const bool tiled = n >= a.tile_from;
-    // tile sets as even as 32 tokens allow, none of them empty
+    // Which form takes which experts.  Those of 16 tokens or more suit the many-token form (a launch of 512 tokens of 8
+    // of 128 experts takes 323 us; from 48 tokens 442, from 8 339).  But where they would add few sets to those of the
+    // few-token form it takes them, too, and where that one would have few of its own the other takes all: a launch that
+    // does not fill the GPU costs more than they do (64 tokens: 27 + 15 us for seven experts).
+    constexpr int kRowTokens = 8 * kSetOctets;
     const int parts = (n + a.tile_tokens - 1) / a.tile_tokens;
-    const int per = tiled ? ((n + parts - 1) / parts + 31) / 32 * 32 : 1;
-    const int rows_n = tiled ? 0 : n, tile_n = tiled ? (n + per - 1) / per : 0;
+    // tile sets as even as 32 tokens allow, none of them empty
+    const int per = n > 0 ? ((n + parts - 1) / parts + 31) / 32 * 32 : 1, tile_n = (n + per - 1) / per;
+    const bool many = n >= a.tile_from;
+    const int row_sets = (n + kRowTokens - 1) / kRowTokens;
+    int4 sum;
+    scan_before(make_int4(many ? 0 : row_sets, many ? row_sets : 0, many ? tile_n : 0, 0), warp_sums, sum);
+    __syncthreads();
+    const bool tiled = sum.y <= sum.x / 4 ? false : 2 * sum.x <= sum.z ? n > 0 : many;
+    const int rows_n = tiled ? 0 : n;
     int4 all;
-    const int4 at = scan_before(make_int4(n, (rows_n + 7) / 8, (rows_n + 8 * kSetOctets - 1) / (8 * kSetOctets), tile_n), warp_sums, all);
+    const int4 at = scan_before(make_int4(n, (rows_n + 7) / 8, tiled ? 0 : row_sets, tiled ? tile_n : 0), warp_sums, all);
     if (e < a.experts) {
         place_of[e] = at.x + before, octet_of[e] = tiled ? -1 : at.y * 8 + before;
         if (rank == 0) {
             for (int i = 0, s = at.z; i < rows_n; i += 8 * kSetOctets, ++s)
                 a.plan.sets[s] = {e, at.x + i, min(8 * kSetOctets, n - i), at.y + i / 8};
-            for (int i = 0; i < tile_n; ++i) a.plan.tile_sets[at.w + i] = {e, at.x + i * per, min(per, n - i * per), 0};
+            for (int i = 0; i < (tiled ? tile_n : 0); ++i) a.plan.tile_sets[at.w + i] = {e, at.x + i * per, min(per, n - i * per), 0};
         }
     }
     if (e == 0 && rank == 0) a.plan.head[0] = all.z, a.plan.head[1] = all.y, a.plan.head[2] = all.x, a.plan.head[3] = all.w;
@@ -356,10 +366,10 @@ Layout layout_of(int64_t T, int top_k, int64_t E, int64_t K, int64_t F, int64_t 
     // (an id may repeat within a token: such an expert goes by the few-token form, however many it has)
     l.tiled = T >= kTileFrom;
     const int64_t used = std::min(l.A, E);
-    // experts of fewer than kTileFrom tokens
-    l.octets = l.tiled ? std::min(used + l.A / 8, E * ((kTileFrom + 6) / 8)) : used + l.A / 8;
+    // with the many-token form: experts of fewer than kTileFrom tokens, or sets a quarter as many again as those
+    l.octets = l.tiled ? std::min(used + l.A / 8, 2 * E + (E / 4 + 1) * kSetOctets) : used + l.A / 8;
     l.sets = used + l.A / (8 * kSetOctets);
-    l.tile_sets = l.tiled ? l.A / 64 + std::min(E, l.A / kTileFrom) : 0;
+    l.tile_sets = l.tiled ? l.A / 64 + used : 0;
     int64_t at = 0;
     const auto take = [&](int64_t n) {
         const int64_t was = at;

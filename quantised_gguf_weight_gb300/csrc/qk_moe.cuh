@@ -27,7 +27,7 @@ namespace moe {
 constexpr int kMaxExperts = 1024;
 constexpr int kSetOctets = 2;
 constexpr int kTileBoxRows = 32;                  // rows of a TMA box of a tile set's operands
-constexpr int kRowWarps = 8;                      // warps of a thread block of the few-token products
+constexpr int kRowWarps = 16;                     // warps of a thread block of the few-token products
 constexpr int kUnit = 256;                        // columns of a unit of the products' loops
 constexpr int kPieceBytes = 8 * 32 * 16;          // an octet's unit, one piece: 8 steps of 16 bytes a lane
 constexpr int kSumBytes = 32 * 8;                 // the sums of its sub-blocks (Q4_K)

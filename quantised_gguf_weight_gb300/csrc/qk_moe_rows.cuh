@@ -31,7 +31,7 @@
 namespace qk {
 namespace moe {
 
-constexpr int kRowTiles = 2;                      // 16-row tiles of a warp
+constexpr int kRowTiles = 1;                      // 16-row tiles of a warp
 // Shared-memory pitch of a row's unit: 16-byte chunks that hold it wherever it starts.  Q4_K's starts on one.
 __host__ __device__ constexpr int row_pitch(int fmt) { return fmt == kFmtQ4K ? 144 : fmt == kFmtQ80 ? 288 : 224; }
 __host__ __device__ constexpr int row_chunks(int fmt) { return fmt == kFmtQ4K ? 9 : fmt == kFmtQ80 ? 18 : 14; }
@@ -376,13 +376,13 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, 1) rows_kernel(const Row
 
     // what is fetched runs S - 1 units ahead of what is computed, over the ends of items
     Cursor f = {static_cast<int>(blockIdx.x), u0, u1};
-    const uint8_t *from[4];
+    const uint8_t *from[2 * M];
     int slot_in = 0;
     const auto aim = [&]() {
         if (f.item >= items) return;
         const int expert = a.plan.sets[f.item / blocks].expert, pair = pair_of(f.item);
 #pragma unroll
-        for (int o = 0; o < 4; ++o) from[o] = row_of(expert, pair, 8 * o + (lane >> 2));
+        for (int o = 0; o < 2 * M; ++o) from[o] = row_of(expert, pair, 8 * o + (lane >> 2));
     };
     aim();
     const auto fetch = [&]() {
@@ -391,7 +391,7 @@ __global__ void __launch_bounds__((kRowWarps + 1) * 32, 1) rows_kernel(const Row
             const int left = static_cast<int>(min(static_cast<int64_t>(UB), a.a.row_bytes - off)) - 16 * c;
             const uint32_t to = ring + slot_in * SLOT + (lane >> 2) * PITCH + 16 * c;
 #pragma unroll
-            for (int o = 0; o < 4; ++o) {
+            for (int o = 0; o < 2 * M; ++o) {
                 const uint8_t *p = from[o] + off;
                 int bytes = left;
                 if constexpr (FMT != kFmtQ4K) {
