@@ -84,6 +84,20 @@ __device__ __forceinline__ bool tile_wait_warp(uint32_t bar, uint32_t parity, co
     return __all_sync(~0u, tile_wait(bar, parity, a, abort));
 }
 
+// A test that may sleep a while before it says no, for arrivals from the other block, too.
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // One lane of the (converged) warp is elected.
 __device__ __forceinline__ bool elect_one()
 {
@@ -215,27 +229,49 @@ __device__ __forceinline__ void load_raw(Raw<FMT, KC> &r, uint32_t p, int c)
     }
 }
 
-// fp16 pairs of 32 values: hi pieces, and lo where PA == 2.
+// a b + c and a + c in fp32, a and b the halves AT of fp16 pairs
+template <int AT>
+__device__ __forceinline__ uint16_t half_of(__half2 v)
+{
+    return static_cast<uint16_t>(AT ? tile_h2(v) >> 16 : tile_h2(v) & 0xffffu);
+}
+__device__ __forceinline__ float fma_half(uint16_t a, uint16_t b, float c)
+{
+    float r;
+    asm("fma.rn.f32.f16 %0, %1, %2, %3;" : "=f"(r) : "h"(a), "h"(b), "f"(c));
+    return r;
+}
+__device__ __forceinline__ float add_half(uint16_t a, float c)
+{
+    float r;
+    asm("add.rn.f32.f16 %0, %1, %2;" : "=f"(r) : "h"(a), "f"(c));
+    return r;
+}
+
+// fp16 pairs of 32 values: hi pieces, and lo where PA == 2, the rest to 2^-22 of the value.
 template <int PA>
 struct Pieces {
     uint32_t hi[16], lo[PA == 2 ? 16 : 1];
-    __device__ __forceinline__ void set(int i, float a, float b)
+    // whole numbers t times d (exact in fp16) less m, of which mh is the fp16
+    __device__ __forceinline__ void set(int i, __half2 t, __half2 d, float m, __half2 mh)
     {
-        const __half2 h = __floats2half2_rn(a, b);
+        const __half2 h = __hfma2(t, d, __hneg2(mh));
         hi[i] = tile_h2(h);
         if constexpr (PA == 2) {
-            const float2 f = __half22float2(h);
-            lo[i] = tile_h2(__floats2half2_rn(a - f.x, b - f.y));
+            // t d - (m + h): the sum's rounding is 2^-24 of m
+            const float a = fma_half(half_of<0>(t), half_of<0>(d), -add_half(half_of<0>(h), m));
+            const float b = fma_half(half_of<1>(t), half_of<0>(d), -add_half(half_of<1>(h), m));
+            lo[i] = tile_h2(__floats2half2_rn(a, b));
         }
     }
-    // two pairs of integers times d, plus m
-    __device__ __forceinline__ void set4(int i, __half2 a, __half2 b, float d, float m, __half2 dh, __half2 mh)
+    // whole numbers q times dh + dl: a product's rest is a fused multiply-add away
+    __device__ __forceinline__ void set(int i, __half2 q, __half2 dh, __half2 dl, bool rest)
     {
-        if constexpr (PA == 1) {
-            hi[i] = tile_h2(__hfma2(a, dh, mh)), hi[i + 1] = tile_h2(__hfma2(b, dh, mh));
-        } else {
-            const float2 x = __half22float2(a), y = __half22float2(b);
-            set(i, fmaf(x.x, d, m), fmaf(x.y, d, m)), set(i + 1, fmaf(y.x, d, m), fmaf(y.y, d, m));
+        const __half2 h = __hmul2(q, dh);
+        hi[i] = tile_h2(h);
+        if constexpr (PA == 2) {
+            const __half2 e = __hfma2(q, dh, __hneg2(h));
+            lo[i] = tile_h2(rest ? __hfma2(q, dl, e) : e);
         }
     }
 };
@@ -252,8 +288,8 @@ __device__ __forceinline__ void take_apart(Pieces<PA> &o, const Raw<FMT, KC> &r,
         const uint32_t sc = pair < 2 ? A & 0x3fu : (C & 0x0fu) | ((A >> 2) & 0x30u);
         const uint32_t mm = pair < 2 ? B & 0x3fu : ((C >> 4) & 0x0fu) | ((B >> 2) & 0x30u);
         const __half2 s0 = __hsub2(tile_b2(0x64006400u | sc | sc << 16), k1024);
-        const float d = d2.x * up, m = -d2.y * up * static_cast<float>(mm);
-        const __half2 dh = __float2half2_rn(d), mh = __float2half2_rn(m);
+        const float m = d2.y * up * static_cast<float>(mm);
+        const __half2 dh = __float2half2_rn(d2.x * up), mh = __float2half2_rn(m);
         const __half2 mul = high ? __hmul2(s0, __float2half2_rn(0.0625f)) : s0;
         const __half2 add = __hmul2(s0, __float2half2_rn(high ? -64.0f : -1024.0f));
 #pragma unroll
@@ -262,38 +298,38 @@ __device__ __forceinline__ void take_apart(Pieces<PA> &o, const Raw<FMT, KC> &r,
             // scale times quant, exact
             const __half2 a = __hfma2(high ? tile_field<0x00f000f0>(v) : tile_field<0x000f000f>(v), mul, add);
             const __half2 b = __hfma2(high ? tile_field<0x00f000f0>(v >> 8) : tile_field<0x000f000f>(v >> 8), mul, add);
-            o.set4(2 * i, a, b, d, m, dh, mh);
+            o.set(2 * i, a, dh, m, mh), o.set(2 * i + 1, b, dh, m, mh);
         }
     } else if constexpr (FMT == kFmtQ80) {
         // block k: d at byte 34 k, then the quants; none past the row's end
         const int first = c * (KC / 32), base = 17 * (k >> 1);
         const auto at = [&](int i) { return __funnelshift_r(r.w[i], r.w[i + 1], r.sh); };
-        const __half2 bias = __float2half2_rn(1152.0f), zero = __float2half2_rn(0.0f);
+        const __half2 bias = __float2half2_rn(1152.0f);
         const float d = first + k < (cols + 31) / 32 ? half_bits_to_float(k & 1 ? at(base + 8) >> 16 : at(base)) * up : 0.0f;
         const __half2 dh = __float2half2_rn(d);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const uint32_t q = (k & 1 ? at(base + 9 + i) : __funnelshift_r(at(base + i), at(base + i + 1), 16)) ^ 0x80808080u;
-            o.set4(2 * i, __hsub2(tile_b2(__byte_perm(q, 0x64u, 0x4240)), bias), __hsub2(tile_b2(__byte_perm(q, 0x64u, 0x4341)), bias),
-                   d, 0.0f, dh, zero);
+            o.set(2 * i, __hsub2(tile_b2(__byte_perm(q, 0x64u, 0x4240)), bias), dh, dh, false);
+            o.set(2 * i + 1, __hsub2(tile_b2(__byte_perm(q, 0x64u, 0x4341)), bias), dh, dh, false);
         }
     } else {
         // 32 columns t of the half
         const int t = KC == 128 ? k : 2 * (c & 1) + k;
         const float d0 = half_bits_to_float(r.w[30]) * up;
-        const __half2 bias = __float2half2_rn(1056.0f), zero = __float2half2_rn(0.0f);
+        const __half2 bias = __float2half2_rn(1056.0f);
         const uint32_t scales = __funnelshift_r(r.w[27 + (t >> 1)], r.w[28 + (t >> 1)], r.sh) >> (16 * (t & 1));
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             const float d = d0 * static_cast<float>(static_cast<int8_t>(scales >> (8 * u)));
-            const __half2 dh = __float2half2_rn(d);
+            const __half2 dh = __float2half2_rn(d), dl = __float2half2_rn(d - __low2float(dh));
 #pragma unroll
             for (int i = 4 * u; i < 4 * u + 4; ++i) {
                 const uint32_t low = __funnelshift_r(r.w[9 * (k & 1) + i], r.w[9 * (k & 1) + i + 1], r.sh) >> (t & 2 ? 4 : 0);
                 const uint32_t high = __funnelshift_r(r.w[18 + i], r.w[19 + i], r.sh) >> (2 * t);
                 const uint32_t q = (low & 0x0f0f0f0fu) | ((high & 0x03030303u) << 4);
-                o.set4(2 * i, __hsub2(tile_b2(__byte_perm(q, 0x64u, 0x4240)), bias), __hsub2(tile_b2(__byte_perm(q, 0x64u, 0x4341)), bias),
-                       d, 0.0f, dh, zero);
+                o.set(2 * i, __hsub2(tile_b2(__byte_perm(q, 0x64u, 0x4240)), bias), dh, dl, true);
+                o.set(2 * i + 1, __hsub2(tile_b2(__byte_perm(q, 0x64u, 0x4341)), bias), dh, dl, true);
             }
         }
     }
@@ -359,24 +395,18 @@ tile_kernel(const __grid_constant__ TileMaps maps, const TileArgs a)
     // steers them comes from votes, reductions and counters, so that operands are in the warp's uniform registers.  (A
     // thread of a branch of its own, or in a loop whose end it has read from memory, takes 100 to 118 cycles a product and
     // 250 a copy, measured; this form N / 2 and 30.)
-    // Two barriers' phases, tested side by side.
-    const auto both_ready = [&](uint32_t bar0, uint32_t parity0, uint32_t bar1, uint32_t parity1) {
-        const auto test = [&]() {
-            const bool t0 = mbar_test(bar0, parity0), t1 = mbar_test(bar1, parity1);
-            return __all_sync(~0u, t0 & t1) != 0;
-        };
-        if (test()) return true;
+    const auto ready = [&](uint32_t bar, uint32_t parity) {
+        if (__all_sync(~0u, mbar_try_wait_cluster(bar, parity))) return true;
         const uint64_t deadline = globaltimer_ns() + a.wait_ns;
         for (unsigned i = 1;; ++i) {
-            if (test()) return true;
-            if ((i & 63u) == 0) {
+            if (__all_sync(~0u, mbar_try_wait_cluster(bar, parity))) return true;
+            if ((i & 7u) == 0) {
                 const bool late = globaltimer_ns() > deadline;
                 if (late) *abort = 1, record_error(a.err, kErrTimeout);
                 if (__any_sync(~0u, late || *abort)) return false;
             }
         }
     };
-    const auto ready = [&](uint32_t bar, uint32_t parity) { return both_ready(bar, parity, bar, parity); };
     const unsigned end = __reduce_max_sync(~0u, static_cast<unsigned>(items));
 
     if (warp == 0) {
@@ -429,7 +459,7 @@ tile_kernel(const __grid_constant__ TileMaps maps, const TileArgs a)
                     ok = false;
                     break;
                 }
-                if (!both_ready(smem_u32(&sh.b_full[sb]), (n / kBStages) & 1, smem_u32(&sh.full[st]), (n / kStages) & 1)) {
+                if (!ready(smem_u32(&sh.b_full[sb]), (n / kBStages) & 1) || !ready(smem_u32(&sh.full[st]), (n / kStages) & 1)) {
                     ok = false;
                     break;
                 }
