@@ -573,11 +573,19 @@ size_t qk_moe_ffn_workspace_bytes(int64_t T, int top_k, int64_t n_experts, int64
  * Tokens of one adapter may lie anywhere; neighbouring ones share its reads.
  * Both products are fp32 sums of operands that are exact in 16 bits and held
  * to 22 bits in fp32 (and A x, in between).
+ *   workspace   NULL, or device scratch, 256-byte aligned, whose contents need
+ *               not be kept or set; calls that may overlap need one each.
+ *               With qk_lora_workspace_bytes() of it, many tokens take two
+ *               launches instead of one, which is faster.
  * rank <= 256; K, N <= 2^24; T <= 2^26.  T == 0 does nothing.
  */
 int qk_lora(const void *x, int64_t ldx, int x_type, int64_t T, int64_t K, const void *A, const void *B, int w_type,
             int64_t n_adapters, int rank, int64_t N, const int32_t *ids, const float *scales, const void *y,
-            int64_t ldy, void *out, int64_t ldo, int y_type, qk_stream_t stream);
+            int64_t ldy, void *out, int64_t ldo, int y_type, void *workspace, size_t workspace_bytes,
+            qk_stream_t stream);
+
+/* Workspace bytes that a qk_lora call of T tokens can make use of (0: none). */
+size_t qk_lora_workspace_bytes(int64_t T, int rank);
 
 /*
  * Bytes of one row of a tensor with K columns: ceil(K/32)*34 (Q8_0),

@@ -35,6 +35,7 @@ struct LoraArgs {
     const int32_t *ids;
     const float *scales;
     int steps;                                 // clusters that share a tile's adapters
+    float *V;                                  // many tokens: [T][ranks, padded] of scale A x
     bool vec_x, vec_y, vec_a, vec_b;
     int *err;
 };
@@ -343,6 +344,527 @@ cudaError_t launch_as(const LoraArgs &a, cudaStream_t st)
     return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
+// ---------------------------------------------------------------- many tokens
+// Two launches with V = scale A x in memory between them.  The first: a thread
+// block has 16 tokens, its warps every eighth 32 columns of x and A, straight
+// from memory into the products' registers, two turns ahead; the warps' sums are
+// added in their order.  The second: V's rows stay in a warp's registers as the
+// products' operand while it goes over its columns of B and y, one turn ahead.
+// One adapter of the tile after another, each for its own rows.
+//
+// Where x and the adapters have one 16-bit type the products are m16n8k16 in it,
+// operands as they lie in memory; V is then two fp16 pieces below its row's
+// largest, or two bf16 ones (three for fp32 outputs).  Else tf32, as above.
+
+constexpr int kTallRows = 32, kShrinkRows = 16;            // tokens of a block of the second, and of the first launch
+
+struct TileList {
+    int ids[kTallRows], list[kTallRows], n;
+};
+// The tile's ids, and its adapters in the order of their first tokens.
+__device__ __forceinline__ void list_adapters(TileList &l, const LoraArgs &a, int64_t t0, int rows)
+{
+    const int tid = threadIdx.x;
+    if (tid < kTallRows) {
+        const int id = tid < rows && t0 + tid < a.T ? a.ids[t0 + tid] : -1;
+        l.ids[tid] = id;
+        __syncwarp();
+        const unsigned same = __match_any_sync(~0u, id);
+        const bool first = id >= 0 && id < a.n_adapters && tid == __ffs(same) - 1;
+        const unsigned who = __ballot_sync(~0u, first);
+        if (first) l.list[__popc(who & ((1u << tid) - 1))] = id;
+        if (tid == 0) l.n = __popc(who);
+    }
+    __syncthreads();
+}
+
+constexpr int kBf16 = 0, kF16 = 1, kTf32 = 2;      // products' type
+
+template <int TYPE>
+__device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    if constexpr (TYPE == kF16)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Q neighbouring 16-bit values of a row as they are, 0 from element n on.
+template <int Q>
+__device__ __forceinline__ void load_raw(uint32_t (&w)[Q / 2], const void *base, int64_t row, int i, int n, bool vec)
+{
+    const uint16_t *p = static_cast<const uint16_t *>(base) + row + i;
+    if (vec && i + Q <= n) {
+        if constexpr (Q >= 8) {
+#pragma unroll
+            for (int k = 0; k < Q / 8; ++k) {
+                const uint4 f = __ldg(reinterpret_cast<const uint4 *>(p) + k);
+                w[4 * k] = f.x, w[4 * k + 1] = f.y, w[4 * k + 2] = f.z, w[4 * k + 3] = f.w;
+            }
+        } else {
+            const uint2 f = __ldg(reinterpret_cast<const uint2 *>(p));
+            w[0] = f.x, w[1] = f.y;
+        }
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < Q / 2; ++k)
+        w[k] = (i + 2 * k < n ? __ldg(p + 2 * k) : 0u) | (i + 2 * k + 1 < n ? static_cast<uint32_t>(__ldg(p + 2 * k + 1)) << 16 : 0u);
+}
+
+// What a lane has of one row's 32 columns.
+template <int TYPE, bool WIDE>
+struct Eight {
+    float f[TYPE == kTf32 ? 8 : 1];
+    uint32_t w[TYPE == kTf32 ? 1 : 4];
+    // eight values at a 16-byte boundary
+    __device__ __forceinline__ void load_whole(const char *p, bool in, bool half)
+    {
+        if constexpr (TYPE == kTf32) {
+            if (in) load_values<8, WIDE>(f, p, 0, 0, 8, true, half);
+            else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) f[k] = 0.0f;
+            }
+        } else {
+            const uint4 v = in ? __ldg(reinterpret_cast<const uint4 *>(p)) : make_uint4(0u, 0u, 0u, 0u);
+            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+        }
+    }
+    __device__ __forceinline__ void load(const void *base, int64_t row, int i, int n, bool vec, bool half, bool in)
+    {
+        if constexpr (TYPE == kTf32) {
+            if (in) load_values<8, WIDE>(f, base, row, i, n, vec, half);
+            else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) f[k] = 0.0f;
+            }
+        } else {
+            if (in) load_raw<8>(w, base, row, i, n, vec);
+            else w[0] = w[1] = w[2] = w[3] = 0u;
+        }
+    }
+};
+
+template <int NR, int TYPE, bool XW, bool WW>
+__global__ void __launch_bounds__(kThreads, TYPE == kTf32 ? 1 : 2) shrink_kernel(const LoraArgs a)
+{
+    constexpr int R8 = 8 * NR;
+    extern __shared__ __align__(16) float parts[];           // [warp][row][R8 + 4]
+    __shared__ TileList l;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kShrinkRows;
+    const int blocks = (a.rank + R8 - 1) / R8, width = blocks * R8;
+    const bool x_half = a.x_type == QK_F16, w_half = a.w_type == QK_F16;
+    moe::let_next_start();
+    moe::wait_for_previous();
+    list_adapters(l, a, t0, kShrinkRows);
+    for (int j = 0; j < l.n; ++j) {
+        const int id = l.list[j];
+        const int64_t a_row = static_cast<int64_t>(id) * a.rank;
+        const bool in[2] = {l.ids[g] == id, l.ids[8 + g] == id};
+        for (int rb = 0; rb < blocks; ++rb) {
+            float acc[NR][4];
+#pragma unroll
+            for (int n = 0; n < NR; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
+            struct Turn {
+                Eight<TYPE, XW> x[2];
+                Eight<TYPE, WW> w[NR];
+            };
+            // where this lane's values of the warp's first columns are; whole turns need no more than these and their steps
+            constexpr int XS = XW ? 4 : 2, WS = WW ? 4 : 2;
+            const char *xp = static_cast<const char *>(a.x) + ((t0 + g) * a.ldx + 8 * c) * XS;
+            const char *wp = static_cast<const char *>(a.A) + ((a_row + rb * R8 + g) * a.K + 8 * c) * WS;
+            const int64_t x_step = 8 * a.ldx * XS, w_step = 8LL * a.K * WS;
+            const bool whole = a.vec_x && a.vec_a && rb * R8 + R8 <= a.rank;
+            const auto load = [&](Turn &t, int k) {
+                if (whole && k + 32 <= a.K) {
+                    const char *q = xp + static_cast<int64_t>(k) * XS;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h, q += x_step) t.x[h].load_whole(q, in[h], x_half);
+                    q = wp + static_cast<int64_t>(k) * WS;
+#pragma unroll
+                    for (int n = 0; n < NR; ++n, q += w_step) t.w[n].load_whole(q, true, w_half);
+                    return;
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    t.x[h].load(a.x, (t0 + h * 8 + g) * a.ldx, k + 8 * c, a.K, a.vec_x, x_half, in[h] && k < a.K);
+#pragma unroll
+                for (int n = 0; n < NR; ++n) {
+                    const int r = rb * R8 + n * 8 + g;
+                    t.w[n].load(a.A, (a_row + r) * a.K, k + 8 * c, a.K, a.vec_a, w_half, r < a.rank && k < a.K);
+                }
+            };
+            const auto products = [&](const Turn &t) {
+                if constexpr (TYPE == kTf32) {
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) {
+                        const float xa[4] = {t.x[0].f[2 * s], t.x[1].f[2 * s], t.x[0].f[2 * s + 1], t.x[1].f[2 * s + 1]};
+#pragma unroll
+                        for (int n = 0; n < NR; ++n)
+                            mma_pieces<XW ? 2 : 1, WW ? 2 : 1>(acc[n], xa, t.w[n].f[2 * s], t.w[n].f[2 * s + 1]);
+                    }
+                } else {
+#pragma unroll
+                    for (int s = 0; s < 2; ++s)
+#pragma unroll
+                        for (int n = 0; n < NR; ++n)
+                            mma16<TYPE>(acc[n], t.x[0].w[2 * s], t.x[1].w[2 * s], t.x[0].w[2 * s + 1], t.x[1].w[2 * s + 1], t.w[n].w[2 * s],
+                                        t.w[n].w[2 * s + 1]);
+                }
+            };
+            if constexpr (TYPE == kTf32) {
+                for (int k = warp * 32; k < a.K; k += kWarps * 32) {
+                    Turn t;
+                    load(t, k);
+                    products(t);
+                }
+            } else {
+                Turn t[2];
+                load(t[0], warp * 32), load(t[1], (warp + kWarps) * 32);
+                for (int k = warp * 32; k < a.K; k += 2 * kWarps * 32) {
+                    products(t[0]);
+                    load(t[0], k + 2 * kWarps * 32);
+                    products(t[1]);
+                    load(t[1], k + 3 * kWarps * 32);
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < NR; ++n)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    *reinterpret_cast<float2 *>(parts + (warp * kShrinkRows + h * 8 + g) * (R8 + 4) + n * 8 + 2 * c) =
+                        make_float2(acc[n][2 * h], acc[n][2 * h + 1]);
+            __syncthreads();
+            const float scale = a.scales ? a.scales[id] : 1.0f;
+            for (int i = tid; i < kShrinkRows * R8; i += kThreads) {
+                const int row = i / R8, col = i % R8;
+                if (l.ids[row] != id) continue;
+                float s = parts[row * (R8 + 4) + col];
+#pragma unroll
+                for (int w = 1; w < kWarps; ++w) s += parts[(w * kShrinkRows + row) * (R8 + 4) + col];
+                a.V[(t0 + row) * width + rb * R8 + col] = s * scale;
+            }
+            __syncthreads();
+        }
+    }
+}
+
+__device__ __forceinline__ uint32_t pack16(float lo, float hi, bool half)
+{
+    if (half) {
+        const __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ float2 unpack16(uint32_t w, bool half)
+{
+    if (half) return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+
+// PIECES: of V, in 16 bits.
+template <int NR, int TYPE, int PIECES, bool WW>
+__global__ void __launch_bounds__(kThreads, TYPE == kTf32 ? 1 : 2) expand_kernel(const LoraArgs a)
+{
+    constexpr int R8 = 8 * NR, Q = 2 * NR;                   // ranks of a pass, and of a lane
+    __shared__ TileList l;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTallRows;
+    const int blocks = (a.rank + R8 - 1) / R8, width = blocks * R8;
+    const bool w_half = a.w_type == QK_F16, y_half = a.y_type == QK_F16, y_wide = a.y_type == QK_F32;
+    const int n_per = ((a.N + static_cast<int>(gridDim.y) - 1) / static_cast<int>(gridDim.y) + 31) / 32 * 32;
+    const int n0 = min(a.N, static_cast<int>(blockIdx.y) * n_per), n1 = min(a.N, n0 + n_per);
+    moe::let_next_start();
+    moe::wait_for_previous();
+    list_adapters(l, a, t0, kTallRows);
+    // rows without an adapter
+    for (int i = 0; i < kTallRows && t0 + i < a.T; ++i) {
+        const bool bad = l.ids[i] >= a.n_adapters;
+        if (l.ids[i] >= 0 && !bad) continue;
+        if (bad && tid == 0 && blockIdx.y == 0) record_error(a.err, kErrBadIndex);
+        if (bad || a.out != a.y)
+            for (int n = n0 + tid; n < n1; n += kThreads)
+                store_float_as(a.out, (t0 + i) * a.ldo + n, a.y_type,
+                               bad ? __int_as_float(0x7fc00000) : load_as_float(a.y, (t0 + i) * a.ldy + n, a.y_type));
+    }
+    const int m = warp & 1;                                  // the warp's 16 rows, and every fourth 16 columns
+    for (int j = 0; j < l.n; ++j) {
+        const int id = l.list[j];
+        const int64_t b_row = static_cast<int64_t>(id) * a.N, row0 = t0 + m * 16 + g;
+        const bool in[2] = {l.ids[m * 16 + g] == id, l.ids[m * 16 + 8 + g] == id};
+        if (!__any_sync(~0u, in[0] || in[1])) continue;
+        // V's rows: lane c has its Q ranks of each
+        float back[2];
+        uint32_t piece[TYPE == kTf32 ? 1 : PIECES][2][TYPE == kTf32 ? 1 : Q / 2];
+        float whole[2][TYPE == kTf32 ? Q : 1];
+        const auto take = [&](int rb) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float *from = a.V + (row0 + 8 * h) * width + rb * R8 + Q * c;
+                float v[Q];
+#pragma unroll
+                for (int k = 0; k < Q; k += 2) {
+                    const float2 f = in[h] ? *reinterpret_cast<const float2 *>(from + k) : make_float2(0.0f, 0.0f);
+                    v[k] = f.x, v[k + 1] = f.y;
+                }
+                back[h] = 1.0f;
+                if constexpr (TYPE == kTf32) {
+#pragma unroll
+                    for (int k = 0; k < Q; ++k) whole[h][k] = v[k];
+                } else {
+                    float up = 1.0f;
+                    if constexpr (TYPE == kF16) {
+                        // a power of two puts the row's largest into [2^14, 2^15)
+                        uint32_t most = 0;
+#pragma unroll
+                        for (int k = 0; k < Q; ++k) most = max(most, __float_as_uint(v[k]) & 0x7fffffffu);
+                        most = max(most, __shfl_xor_sync(~0u, most, 1)), most = max(most, __shfl_xor_sync(~0u, most, 2));
+                        const int ex = most >= 0x7f800000u || most == 0 ? 141 : max(static_cast<int>(most >> 23), 15);
+                        up = __uint_as_float(static_cast<uint32_t>(127 + 141 - ex) << 23);
+                        back[h] = __uint_as_float(static_cast<uint32_t>(127 - 141 + ex) << 23);
+                    }
+#pragma unroll
+                    for (int k = 0; k < Q; k += 2) {
+                        float x = v[k] * up, y = v[k + 1] * up;
+#pragma unroll
+                        for (int p = 0; p < PIECES; ++p) {
+                            const uint32_t w = pack16(x, y, TYPE == kF16);
+                            const float2 f = unpack16(w, TYPE == kF16);
+                            piece[p][h][k / 2] = w;
+                            x -= f.x, y -= f.y;
+                        }
+                    }
+                }
+            }
+        };
+        struct Turn {
+            float bf[2][TYPE == kTf32 ? Q : 1];
+            uint32_t bw[2][TYPE == kTf32 ? 1 : Q / 2];
+            uint4 y[2];                                      // four values: fp32, or two words of 16-bit ones
+        };
+        // this lane's places in B, y and out
+        const int b_col = 4 * (g >> 1) + (g & 1), YS = y_wide ? 4 : 2;
+        constexpr int WS = WW ? 4 : 2;
+        const char *bp = static_cast<const char *>(a.B) + ((b_row + b_col) * a.rank + Q * c) * WS;
+        const char *yp[2] = {static_cast<const char *>(a.y) + (row0 * a.ldy + 4 * c) * YS,
+                             static_cast<const char *>(a.y) + ((row0 + 8) * a.ldy + 4 * c) * YS};
+        char *op[2] = {static_cast<char *>(a.out) + (row0 * a.ldo + 4 * c) * YS, static_cast<char *>(a.out) + ((row0 + 8) * a.ldo + 4 * c) * YS};
+        const bool whole_b = a.vec_b && a.rank % R8 == 0;
+        const auto load_b = [&](Turn &t, int n, int rb) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int col = n + b_col + 2 * q;
+                if (whole_b && n + 16 <= n1) {
+                    const char *p = bp + ((static_cast<int64_t>(n) + 2 * q) * a.rank + rb * R8) * WS;
+                    if constexpr (TYPE == kTf32) load_values<Q, WW>(t.bf[q], p, 0, 0, Q, true, w_half);
+                    else load_raw<Q>(t.bw[q], p, 0, 0, Q, true);
+                } else if constexpr (TYPE == kTf32) {
+                    if (col < n1) load_values<Q, WW>(t.bf[q], a.B, (b_row + col) * a.rank, rb * R8 + Q * c, a.rank, a.vec_b, w_half);
+                    else {
+#pragma unroll
+                        for (int i = 0; i < Q; ++i) t.bf[q][i] = 0.0f;
+                    }
+                } else {
+                    if (col < n1) load_raw<Q>(t.bw[q], a.B, (b_row + col) * a.rank, rb * R8 + Q * c, a.rank, a.vec_b);
+                    else {
+#pragma unroll
+                        for (int i = 0; i < Q / 2; ++i) t.bw[q][i] = 0u;
+                    }
+                }
+            }
+        };
+        const auto load_y = [&](Turn &t, int n) {
+            if (!a.vec_y || n + 4 * c + 4 > n1) return;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (!in[h]) continue;
+                if (y_wide) t.y[h] = *reinterpret_cast<const uint4 *>(yp[h] + 4LL * n);
+                else {
+                    const uint2 w = *reinterpret_cast<const uint2 *>(yp[h] + 2LL * n);
+                    t.y[h].x = w.x, t.y[h].y = w.y;
+                }
+            }
+        };
+        if (blocks == 1) take(0);
+        // whole turns of 32 columns, a lane's eight neighbours of each row: product `nt` has columns 8 c + 2 nt and the next
+        int done = n0;                                       // columns before it are done
+        if constexpr (TYPE != kTf32) {
+            const int turns = blocks == 1 && whole_b && a.vec_y ? (n1 - n0) / 32 : 0;
+            done += 32 * turns;
+            const int64_t row_bytes = 2LL * a.rank, y_bytes = 32 * YS, first = n0 + 32 * (warp >> 1);
+            const char *b = static_cast<const char *>(a.B) + (b_row + first + 8 * (g >> 1) + (g & 1)) * row_bytes + 2 * Q * c;
+            const char *y[2] = {yp[0] + (first + 4 * c) * YS, yp[1] + (first + 4 * c) * YS};
+            char *o[2] = {op[0] + (first + 4 * c) * YS, op[1] + (first + 4 * c) * YS};
+            uint4 next[2][2];
+            const auto fetch_y = [&]() {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (!in[h]) continue;
+                    next[h][0] = *reinterpret_cast<const uint4 *>(y[h]);
+                    if (y_wide) next[h][1] = *(reinterpret_cast<const uint4 *>(y[h]) + 1);
+                }
+            };
+            int i = warp >> 1;
+            if (i < turns) fetch_y();
+            for (; i < turns; i += kWarps / 2) {
+                uint32_t w[4][Q / 2];
+#pragma unroll
+                for (int nt = 0; nt < 4; ++nt) load_raw<Q>(w[nt], b + 2 * nt * row_bytes, 0, 0, Q, true);
+                uint4 now[2][2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) now[h][0] = next[h][0], now[h][1] = next[h][1], y[h] += kWarps / 2 * y_bytes;
+                if (i + kWarps / 2 < turns) fetch_y();
+                b += kWarps / 2 * 32 * row_bytes;
+                float sum[4][4];
+#pragma unroll
+                for (int nt = 0; nt < 4; ++nt) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) sum[nt][k] = 0.0f;
+#pragma unroll
+                    for (int p = PIECES - 1; p >= 0; --p)
+#pragma unroll
+                        for (int s = 0; s < NR / 2; ++s)
+                            mma16<TYPE>(sum[nt], piece[p][0][2 * s], piece[p][1][2 * s], piece[p][0][2 * s + 1], piece[p][1][2 * s + 1],
+                                        w[nt][2 * s], w[nt][2 * s + 1]);
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float d[8];
+#pragma unroll
+                    for (int nt = 0; nt < 4; ++nt) d[2 * nt] = sum[nt][2 * h] * back[h], d[2 * nt + 1] = sum[nt][2 * h + 1] * back[h];
+                    if (in[h]) {
+                        const uint32_t v[8] = {now[h][0].x, now[h][0].y, now[h][0].z, now[h][0].w, now[h][1].x, now[h][1].y, now[h][1].z, now[h][1].w};
+                        if (y_wide) {
+#pragma unroll
+                            for (int k = 0; k < 2; ++k)
+                                *(reinterpret_cast<float4 *>(o[h]) + k) =
+                                    make_float4(__uint_as_float(v[4 * k]) + d[4 * k], __uint_as_float(v[4 * k + 1]) + d[4 * k + 1],
+                                                __uint_as_float(v[4 * k + 2]) + d[4 * k + 2], __uint_as_float(v[4 * k + 3]) + d[4 * k + 3]);
+                        } else {
+                            uint32_t r[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const float2 f = unpack16(v[k], y_half);
+                                r[k] = pack16(f.x + d[2 * k], f.y + d[2 * k + 1], y_half);
+                            }
+                            *reinterpret_cast<uint4 *>(o[h]) = make_uint4(r[0], r[1], r[2], r[3]);
+                        }
+                    }
+                    o[h] += kWarps / 2 * y_bytes;
+                }
+            }
+        }
+        Turn next;
+        constexpr int kStep = kWarps / 2 * 16;
+        int n = done + (warp >> 1) * 16;
+        if (n < n1) load_b(next, n, 0), load_y(next, n);
+        for (; n < n1; n += kStep) {
+            Turn t = next;
+            if (n + kStep < n1) load_b(next, n + kStep, 0), load_y(next, n + kStep);
+            float acc[2][4];
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[q][i] = 0.0f;
+            for (int rb = 0; rb < blocks; ++rb) {
+                if (blocks > 1) {
+                    take(rb);
+                    if (rb > 0) load_b(t, n, rb);
+                }
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    if constexpr (TYPE == kTf32) {
+#pragma unroll
+                        for (int s = 0; s < NR; ++s) {
+                            const float va[4] = {whole[0][2 * s], whole[1][2 * s], whole[0][2 * s + 1], whole[1][2 * s + 1]};
+                            mma_pieces<2, WW ? 2 : 1>(sum, va, t.bf[q][2 * s], t.bf[q][2 * s + 1]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int p = PIECES - 1; p >= 0; --p)
+#pragma unroll
+                            for (int s = 0; s < NR / 2; ++s)
+                                mma16<TYPE>(sum, piece[p][0][2 * s], piece[p][1][2 * s], piece[p][0][2 * s + 1], piece[p][1][2 * s + 1],
+                                            t.bw[q][2 * s], t.bw[q][2 * s + 1]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[q][i] += sum[i] * back[i >> 1];
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (!in[h]) continue;
+                const int col = n + 4 * c;
+                const float d[4] = {acc[0][2 * h], acc[0][2 * h + 1], acc[1][2 * h], acc[1][2 * h + 1]};
+                if (a.vec_y && col + 4 <= n1) {
+                    const uint4 w = t.y[h];
+                    if (y_wide) {
+                        *reinterpret_cast<float4 *>(op[h] + 4LL * n) = make_float4(
+                            __uint_as_float(w.x) + d[0], __uint_as_float(w.y) + d[1], __uint_as_float(w.z) + d[2], __uint_as_float(w.w) + d[3]);
+                    } else {
+                        const float2 f0 = unpack16(w.x, y_half), f1 = unpack16(w.y, y_half);
+                        *reinterpret_cast<uint2 *>(op[h] + 2LL * n) =
+                            make_uint2(pack16(f0.x + d[0], f0.y + d[1], y_half), pack16(f1.x + d[2], f1.y + d[3], y_half));
+                    }
+                } else {
+                    const int64_t row = row0 + 8 * h;
+                    for (int i = 0; i < 4 && col + i < n1; ++i)
+                        store_float_as(a.out, row * a.ldo + col + i, a.y_type, load_as_float(a.y, row * a.ldy + col + i, a.y_type) + d[i]);
+                }
+            }
+        }
+    }
+}
+
+template <int NR, int TYPE, int PIECES, bool XW, bool WW>
+cudaError_t launch_tall_as(const LoraArgs &a, int sms, cudaStream_t st)
+{
+    constexpr int R8 = 8 * NR;
+    const int smem = static_cast<int>(sizeof(float)) * kWarps * kShrinkRows * (R8 + 4);
+    const auto shrink = shrink_kernel<NR, TYPE, XW, WW>;
+    cudaError_t e = cudaFuncSetAttribute(shrink, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const unsigned tiles = static_cast<unsigned>((a.T + kTallRows - 1) / kTallRows);
+    e = moe::launch_chained(shrink, dim3(static_cast<unsigned>((a.T + kShrinkRows - 1) / kShrinkRows)), kThreads, smem, st, library_programmatic(), a);
+    if (e != cudaSuccess) return e;
+    // columns are cut so that the two blocks an SM holds have work, a few turns each
+    const unsigned cuts = static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>((a.N + 127) / 128, 4LL * sms / tiles)));
+    return moe::launch_chained(expand_kernel<NR, TYPE, PIECES, WW>, dim3(tiles, cuts), kThreads, 0, st, true, a);
+}
+
+template <int NR>
+cudaError_t launch_tall_types(const LoraArgs &a, int sms, cudaStream_t st)
+{
+    if (a.x_type == QK_BF16 && a.w_type == QK_BF16)
+        return a.y_type == QK_F32 ? launch_tall_as<NR, kBf16, 3, false, false>(a, sms, st) : launch_tall_as<NR, kBf16, 2, false, false>(a, sms, st);
+    if (a.x_type == QK_F16 && a.w_type == QK_F16) return launch_tall_as<NR, kF16, 2, false, false>(a, sms, st);
+    if (a.x_type == QK_F32)
+        return a.w_type == QK_F32 ? launch_tall_as<NR, kTf32, 2, true, true>(a, sms, st) : launch_tall_as<NR, kTf32, 2, true, false>(a, sms, st);
+    return a.w_type == QK_F32 ? launch_tall_as<NR, kTf32, 2, false, true>(a, sms, st) : launch_tall_as<NR, kTf32, 2, false, false>(a, sms, st);
+}
+
+int tall_blocks(int rank) { return rank <= 16 ? 2 : rank <= 32 ? 4 : 8; }      // 8-rank tiles of a pass
+
+cudaError_t launch_tall(const LoraArgs &a, int sms, cudaStream_t st)
+{
+    switch (tall_blocks(a.rank)) {
+    case 2: return launch_tall_types<2>(a, sms, st);
+    case 4: return launch_tall_types<4>(a, sms, st);
+    default: return launch_tall_types<8>(a, sms, st);
+    }
+}
+
 template <int MT, int NR>
 cudaError_t launch_types(const LoraArgs &a, cudaStream_t st)
 {
@@ -369,9 +891,25 @@ int size_of(int t) { return t == QK_F32 ? 4 : 2; }
 
 using namespace qk;
 
+namespace {
+// Tokens from which the two-launch form takes a call that has a workspace.
+constexpr int64_t kTallFrom = 256;
+size_t lora_bytes(int64_t T, int rank)
+{
+    const int r8 = 8 * tall_blocks(rank);
+    return static_cast<size_t>(T) * ((rank + r8 - 1) / r8 * r8) * sizeof(float);
+}
+}  // namespace
+
+extern "C" size_t qk_lora_workspace_bytes(int64_t T, int rank)
+{
+    return T < kTallFrom || T > (1 << 26) || rank <= 0 || rank > kMaxRank ? 0 : lora_bytes(T, rank);
+}
+
 extern "C" int qk_lora(const void *x, int64_t ldx, int x_type, int64_t T, int64_t K, const void *A, const void *B, int w_type,
                        int64_t n_adapters, int rank, int64_t N, const int32_t *ids, const float *scales, const void *y,
-                       int64_t ldy, void *out, int64_t ldo, int y_type, qk_stream_t stream)
+                       int64_t ldy, void *out, int64_t ldo, int y_type, void *workspace,
+                       size_t workspace_bytes, qk_stream_t stream)
 {
     if (!type_ok(x_type) || !type_ok(w_type) || !type_ok(y_type)) return QK_ERR_TYPE;
     if (T < 0 || K <= 0 || N <= 0 || n_adapters <= 0 || rank <= 0) return QK_ERR_BAD_DIM;
@@ -389,21 +927,26 @@ extern "C" int qk_lora(const void *x, int64_t ldx, int x_type, int64_t T, int64_
     a.x = x, a.y = y, a.A = A, a.B = B, a.out = out, a.ldx = ldx, a.ldy = ldy, a.ldo = ldo, a.T = T;
     a.n_adapters = n_adapters, a.x_type = x_type, a.y_type = y_type, a.w_type = w_type;
     a.K = static_cast<int>(K), a.N = static_cast<int>(N), a.rank = rank, a.ids = ids, a.scales = scales;
-    // rows that start on 16 bytes (y: four values)
+    // rows that start on 16 bytes
     const auto rows_ok = [](const void *p, int64_t ld, int size, int n) { return multiple(p, n * size) && ld % n == 0; };
     a.vec_x = rows_ok(x, ldx, size_of(x_type), 16 / size_of(x_type));
     a.vec_a = rows_ok(A, K, size_of(w_type), 16 / size_of(w_type));
     a.vec_b = rows_ok(B, rank, size_of(w_type), 16 / size_of(w_type));
-    a.vec_y = rows_ok(y, ldy, size_of(y_type), 4) && rows_ok(out, ldo, size_of(y_type), 4);
+    a.vec_y = rows_ok(y, ldy, size_of(y_type), 16 / size_of(y_type)) && rows_ok(out, ldo, size_of(y_type), 16 / size_of(y_type));
     a.err = library_error_word();
     int sms = 0, smem = 0;
     if (!a.err || !device_limits(&sms, &smem)) return QK_ERR_CUDA;
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (workspace && !multiple(workspace, 256)) return QK_ERR_WORKSPACE;
+    if (T >= kTallFrom && workspace && workspace_bytes >= lora_bytes(T, rank)) {
+        a.V = static_cast<float *>(workspace);
+        return launch_tall(a, sms, st) == cudaSuccess ? QK_OK : QK_ERR_CUDA;
+    }
     // few tokens may each have an adapter of their own: as many clusters a tile as the GPU holds, up to its tokens
     const bool tall = T > 16LL * sms / kCluster;
     const int rows = tall ? 32 : 16;
     const int64_t tiles = (T + rows - 1) / rows;
     a.steps = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({rows, n_adapters, T, 4LL * sms / (kCluster * tiles)})));
-    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const cudaError_t e = tall ? launch_rank<2>(a, st) : launch_rank<1>(a, st);
     return e == cudaSuccess ? QK_OK : QK_ERR_CUDA;
 }

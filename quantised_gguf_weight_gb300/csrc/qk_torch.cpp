@@ -381,11 +381,11 @@ PyObject *moe_ffn(PyObject *, PyObject *const *a, Py_ssize_t n)
     END_HANDLE_TH_ERRORS
 }
 
-// lora(x, y, A, B, ids, scales, out, stream)
+// lora(x, y, A, B, ids, scales, out, workspace, stream)
 PyObject *lora(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
     HANDLE_TH_ERRORS
-    count_args(n, 8);
+    count_args(n, 9);
     const int dev = c10::cuda::current_device();
     const at::Tensor &xt = tensor_of(a[0], "x", dev), &yt = tensor_of(a[1], "y", dev);
     const at::Tensor &At = tensor_of(a[2], "A", dev), &Bt = tensor_of(a[3], "B", dev);
@@ -399,16 +399,22 @@ PyObject *lora(PyObject *, PyObject *const *a, Py_ssize_t n)
     TORCH_CHECK_VALUE(y.n == x.n, "x has ", x.n, " rows, y ", y.n);
     at::Tensor made;
     const bool given = a[6] != Py_None;
-    if (!given) made = new_rows(x.n, Bt.size(1), yt, yt.scalar_type(), a[7]);
+    if (!given) made = new_rows(x.n, Bt.size(1), yt, yt.scalar_type(), a[8]);
     const Rows o = rows_of(given ? tensor_of(a[6], "out", dev) : made, Bt.size(1), "out");
     TORCH_CHECK_VALUE(o.type == y.type, "out and y must have one element type");
     TORCH_CHECK_VALUE(o.n >= y.n, "out has ", o.n, " rows, y ", y.n);
     const int32_t *ids = vector_of<const int32_t>(a[4], x.n, at::kInt, "ids", dev);
     TORCH_CHECK_VALUE(ids || x.n == 0, "ids must be a CUDA tensor");
+    at::Tensor scratch;
+    const size_t need = qk_lora_workspace_bytes(x.n, static_cast<int>(At.size(1)));
+    if (a[7] != Py_None) scratch = tensor_of(a[7], "workspace", dev);
+    else if (need) scratch = new_rows(1, static_cast<int64_t>(need), xt, at::kByte, a[8]);
+    TORCH_CHECK_VALUE(!scratch.defined() || scratch.is_contiguous(), "workspace must be contiguous");
     const int status = qk_lora(x.p, x.ld, x.type, x.n, At.size(2), At.data_ptr(), Bt.data_ptr(), w_type, At.size(0),
                                static_cast<int>(At.size(1)), Bt.size(1), ids,
                                vector_of<const float>(a[5], At.size(0), at::kFloat, "scales", dev), y.p, y.ld, o.p, o.ld, y.type,
-                               stream_of(a[7]));
+                               scratch.defined() ? scratch.data_ptr() : nullptr, scratch.defined() ? scratch.nbytes() : 0,
+                               stream_of(a[8]));
     return done(status, given ? a[6] : nullptr, made);
     END_HANDLE_TH_ERRORS
 }

@@ -38,7 +38,7 @@ EXPORTS = ["qmatvec_q8_0", "qmatvec_q4_k", "qmatvec_q6_k", "qmatvec_swiglu_q8_0"
            "qk_status_string", "qk_device_error", "qk_set_wait_limit_ns", "qk_set_programmatic_launch",
            "qk_set_strict_blocks", "qk_version", "qk_rope_table", "qk_norm_rope", "qk_kv_append_q4",
            "qk_kv_read_q4", "qk_attn_q4", "qk_attn_q4_workspace_bytes", "qk_moe_route", "qk_moe_ffn",
-           "qk_moe_ffn_workspace_bytes", "qk_lora"]
+           "qk_moe_ffn_workspace_bytes", "qk_lora", "qk_lora_workspace_bytes"]
 
 
 class _KVCacheQ4(ctypes.Structure):
@@ -135,7 +135,9 @@ def load(path: str | None = None):
         lib.qk_moe_ffn.argtypes = [P, P, P, I64, I64, I64, I64, P, I64, I, I64, P, P, I, P, I64, I, P, ctypes.c_size_t, P]
         lib.qk_moe_ffn_workspace_bytes.argtypes = [I64, I, I64, I64, I64, I64]
         lib.qk_moe_ffn_workspace_bytes.restype = ctypes.c_size_t
-        lib.qk_lora.argtypes = [P, I64, I, I64, I64, P, P, I, I64, I, I64, P, P, P, I64, P, I64, I, P]
+        lib.qk_lora.argtypes = [P, I64, I, I64, I64, P, P, I, I64, I, I64, P, P, P, I64, P, I64, I, P, ctypes.c_size_t, P]
+        lib.qk_lora_workspace_bytes.argtypes = [I64, I]
+        lib.qk_lora_workspace_bytes.restype = ctypes.c_size_t
         for name in ("qk_rope_table", "qk_norm_rope", "qk_kv_append_q4", "qk_kv_read_q4", "qk_attn_q4", "qk_moe_route",
                      "qk_moe_ffn", "qk_lora"):
             getattr(lib, name).restype = I
@@ -571,11 +573,13 @@ def moe_ffn(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, gate: Exp
 
 
 def lora(x: torch.Tensor, y: torch.Tensor, A: torch.Tensor, B: torch.Tensor, ids: torch.Tensor,
-         scales: torch.Tensor | None = None, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+         scales: torch.Tensor | None = None, out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+         stream=None) -> torch.Tensor:
     """y[t] + scales[a] * B[a] (A[a] x[t]), a = ids[t] (int32; negative: y[t]), for rows x [T][K], y [T][N] and adapters
-    A [adapters][rank][K], B [adapters][N][rank] of one type.  out may be y."""
-    return _result((_ext or _binding()).lora(x, y, A, B, ids, scales, out, None if stream is None else _stream(stream)),
-                   "qk_lora")
+    A [adapters][rank][K], B [adapters][N][rank] of one type.  out may be y.  `workspace` (uint8, of
+    qk_lora_workspace_bytes) is allocated here through torch when not given."""
+    return _result((_ext or _binding()).lora(x, y, A, B, ids, scales, out, workspace,
+                                             None if stream is None else _stream(stream)), "qk_lora")
 
 
 def debug_gemm_skip_chunk(chunk: int) -> int:

@@ -88,7 +88,7 @@ def test_workspace_of_nothing(qk):
 def test_lora_statuses(qk):
     call = caller(qk.load().qk_lora,
                   dict(x=FAKE, ldx=0, x_type=0, T=3, K=64, A=FAKE, B=FAKE, w_type=1, n=2, rank=8, N=64, ids=FAKE, scales=None, y=FAKE,
-                       ldy=0, out=2 * FAKE, ldo=0, y_type=0, stream=None))
+                       ldy=0, out=2 * FAKE, ldo=0, y_type=0, ws=None, bytes=0, stream=None))
     for n in ("x", "A", "B", "ids", "y", "out"):
         assert call(**{n: None}) == 1, n
     for kw in (dict(T=-1), dict(K=0), dict(N=0), dict(n=0), dict(rank=0), dict(ldx=63), dict(ldy=63), dict(ldo=63), dict(out=FAKE, ldo=80)):
@@ -98,6 +98,8 @@ def test_lora_statuses(qk):
     assert call(rank=257) == 8 and call(T=1 << 40) == 8 and call(K=1 << 25) == 8 and call(N=1 << 25) == 8
     assert call(x_type=3) == 10 and call(w_type=-1) == 10 and call(y_type=7) == 10
     assert call(T=0, x=None) == 0
+    f = qk.load().qk_lora_workspace_bytes
+    assert f(0, 8) == f(1, 8) == f(4096, 0) == f(4096, 257) == 0 and f(4096, 64) == 4096 * 64 * 4 and f(4096, 65) == 4096 * 128 * 4
 
 
 def test_binding_refuses_host_tensors(qk):
