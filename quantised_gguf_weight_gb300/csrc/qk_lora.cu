@@ -696,77 +696,9 @@ __global__ void __launch_bounds__(kThreads, TYPE == kTf32 ? 1 : 2) expand_kernel
             }
         };
         if (blocks == 1) take(0);
-        // whole turns of 32 columns, a lane's eight neighbours of each row: product `nt` has columns 8 c + 2 nt and the next
-        int done = n0;                                       // columns before it are done
-        if constexpr (TYPE != kTf32) {
-            const int turns = blocks == 1 && whole_b && a.vec_y ? (n1 - n0) / 32 : 0;
-            done += 32 * turns;
-            const int64_t row_bytes = 2LL * a.rank, y_bytes = 32 * YS, first = n0 + 32 * (warp >> 1);
-            const char *b = static_cast<const char *>(a.B) + (b_row + first + 8 * (g >> 1) + (g & 1)) * row_bytes + 2 * Q * c;
-            const char *y[2] = {yp[0] + (first + 4 * c) * YS, yp[1] + (first + 4 * c) * YS};
-            char *o[2] = {op[0] + (first + 4 * c) * YS, op[1] + (first + 4 * c) * YS};
-            uint4 next[2][2];
-            const auto fetch_y = [&]() {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (!in[h]) continue;
-                    next[h][0] = *reinterpret_cast<const uint4 *>(y[h]);
-                    if (y_wide) next[h][1] = *(reinterpret_cast<const uint4 *>(y[h]) + 1);
-                }
-            };
-            int i = warp >> 1;
-            if (i < turns) fetch_y();
-            for (; i < turns; i += kWarps / 2) {
-                uint32_t w[4][Q / 2];
-#pragma unroll
-                for (int nt = 0; nt < 4; ++nt) load_raw<Q>(w[nt], b + 2 * nt * row_bytes, 0, 0, Q, true);
-                uint4 now[2][2];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) now[h][0] = next[h][0], now[h][1] = next[h][1], y[h] += kWarps / 2 * y_bytes;
-                if (i + kWarps / 2 < turns) fetch_y();
-                b += kWarps / 2 * 32 * row_bytes;
-                float sum[4][4];
-#pragma unroll
-                for (int nt = 0; nt < 4; ++nt) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) sum[nt][k] = 0.0f;
-#pragma unroll
-                    for (int p = PIECES - 1; p >= 0; --p)
-#pragma unroll
-                        for (int s = 0; s < NR / 2; ++s)
-                            mma16<TYPE>(sum[nt], piece[p][0][2 * s], piece[p][1][2 * s], piece[p][0][2 * s + 1], piece[p][1][2 * s + 1],
-                                        w[nt][2 * s], w[nt][2 * s + 1]);
-                }
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float d[8];
-#pragma unroll
-                    for (int nt = 0; nt < 4; ++nt) d[2 * nt] = sum[nt][2 * h] * back[h], d[2 * nt + 1] = sum[nt][2 * h + 1] * back[h];
-                    if (in[h]) {
-                        const uint32_t v[8] = {now[h][0].x, now[h][0].y, now[h][0].z, now[h][0].w, now[h][1].x, now[h][1].y, now[h][1].z, now[h][1].w};
-                        if (y_wide) {
-#pragma unroll
-                            for (int k = 0; k < 2; ++k)
-                                *(reinterpret_cast<float4 *>(o[h]) + k) =
-                                    make_float4(__uint_as_float(v[4 * k]) + d[4 * k], __uint_as_float(v[4 * k + 1]) + d[4 * k + 1],
-                                                __uint_as_float(v[4 * k + 2]) + d[4 * k + 2], __uint_as_float(v[4 * k + 3]) + d[4 * k + 3]);
-                        } else {
-                            uint32_t r[4];
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const float2 f = unpack16(v[k], y_half);
-                                r[k] = pack16(f.x + d[2 * k], f.y + d[2 * k + 1], y_half);
-                            }
-                            *reinterpret_cast<uint4 *>(o[h]) = make_uint4(r[0], r[1], r[2], r[3]);
-                        }
-                    }
-                    o[h] += kWarps / 2 * y_bytes;
-                }
-            }
-        }
         Turn next;
         constexpr int kStep = kWarps / 2 * 16;
-        int n = done + (warp >> 1) * 16;
+        int n = n0 + (warp >> 1) * 16;
         if (n < n1) load_b(next, n, 0), load_y(next, n);
         for (; n < n1; n += kStep) {
             Turn t = next;
@@ -827,6 +759,326 @@ __global__ void __launch_bounds__(kThreads, TYPE == kTf32 ? 1 : 2) expand_kernel
     }
 }
 
+__device__ __forceinline__ void lora_copy16(uint32_t dst, const void *src, bool on)
+{
+    if (on) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ uint4 lora_lds(uint32_t p)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(p));
+    return v;
+}
+
+// The same for 16-bit operands of one type in whole vectors (rows of x, A, B, y and out on 16 bytes, K, N and the rank
+// multiples of 8), which leaves every 16 bytes either inside their row or outside, and so no other path.  A warp's
+// operands come through a ring of its own, two turns ahead.
+constexpr int kTurns = 3;                                    // of a warp on their way or at work
+
+template <int NR>
+__host__ __device__ constexpr int shrink_turn_bytes() { return (kTallRows + 8 * NR) * 64; }
+
+template <int NR, int TYPE>
+__global__ void __launch_bounds__(kThreads, 1) shrink16_kernel(const LoraArgs a)
+{
+    constexpr int R8 = 8 * NR, TURN = shrink_turn_bytes<NR>();
+    extern __shared__ __align__(16) uint8_t ring[];
+    __shared__ TileList l;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTallRows;
+    const uint32_t mine = smem_u32(ring) + warp * kTurns * TURN;
+    float *parts = reinterpret_cast<float *>(ring);          // afterwards: [warp][row][R8 + 4]
+    const int width = (a.rank + R8 - 1) / R8 * R8;
+    moe::let_next_start();
+    moe::wait_for_previous();
+    list_adapters(l, a, t0, kTallRows);
+    for (int j = 0; j < l.n; ++j) {
+        const int id = l.list[j];
+        const float scale = a.scales ? a.scales[id] : 1.0f;
+        // a lane copies 16 bytes of every eighth row
+        unsigned rows = 0;
+#pragma unroll
+        for (int i = 0; i < kTallRows / 8; ++i) rows |= (l.ids[8 * i + g] == id) << i;
+        const uint16_t *x0 = static_cast<const uint16_t *>(a.x) + (t0 + g) * a.ldx + 8 * c;
+        for (int rb = 0; rb * R8 < a.rank; ++rb) {
+            const uint16_t *w0 = static_cast<const uint16_t *>(a.A) + (static_cast<int64_t>(id) * a.rank + rb * R8 + g) * a.K + 8 * c;
+            const int tiles = min(NR, (a.rank - rb * R8) / 8);
+            const int64_t x_step = 8 * a.ldx, w_step = 8LL * a.K;
+            const auto fetch = [&](int k, int slot) {
+                if (k + 8 * c < a.K) {
+                    uint32_t to = mine + slot * TURN + g * 64 + 16 * c;
+                    const uint16_t *q = x0 + k;
+#pragma unroll
+                    for (int i = 0; i < kTallRows / 8; ++i, q += x_step) lora_copy16(to + i * 512, q, (rows >> i) & 1u);
+                    to += kTallRows * 64, q = w0 + k;
+#pragma unroll
+                    for (int i = 0; i < NR; ++i, q += w_step) lora_copy16(to + i * 512, q, i < tiles);
+                }
+                asm volatile("cp.async.commit_group;" ::: "memory");
+            };
+            constexpr int kTurn = kWarps * 32;
+            int k = warp * 32;
+#pragma unroll
+            for (int i = 0; i < kTurns - 1; ++i) fetch(k + i * kTurn, i);
+            float acc[2][NR][4];
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int n = 0; n < NR; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.0f;
+            const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+            for (int slot = 0; k < a.K; k += kTurn) {
+                asm volatile("cp.async.wait_group %0;" ::"n"(kTurns - 2) : "memory");
+                __syncwarp();                                // this turn has landed, and the slot before it is free
+                fetch(k + (kTurns - 1) * kTurn, slot == 0 ? kTurns - 1 : slot - 1);
+                const uint32_t at = mine + slot * TURN + g * 64 + 16 * c;
+                const bool has = k + 8 * c < a.K;
+                uint4 x[2][2];
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) x[m][h] = has && (rows >> (2 * m + h)) & 1u ? lora_lds(at + (2 * m + h) * 512) : zero;
+#pragma unroll
+                for (int n = 0; n < NR; ++n) {
+                    const uint4 w = has && n < tiles ? lora_lds(at + kTallRows * 64 + n * 512) : zero;
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
+                        mma16<TYPE>(acc[m][n], x[m][0].x, x[m][1].x, x[m][0].y, x[m][1].y, w.x, w.y);
+                        mma16<TYPE>(acc[m][n], x[m][0].z, x[m][1].z, x[m][0].w, x[m][1].w, w.z, w.w);
+                    }
+                }
+                slot = slot + 1 == kTurns ? 0 : slot + 1;
+            }
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+            __syncthreads();
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int n = 0; n < NR; ++n)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        *reinterpret_cast<float2 *>(parts + (warp * kTallRows + m * 16 + h * 8 + g) * (R8 + 4) + n * 8 + 2 * c) =
+                            make_float2(acc[m][n][2 * h], acc[m][n][2 * h + 1]);
+            __syncthreads();
+            for (int i = tid * 4; i < kTallRows * R8; i += kThreads * 4) {
+                const int r = i / R8, col = i % R8;
+                float4 s = *reinterpret_cast<const float4 *>(parts + r * (R8 + 4) + col);
+#pragma unroll
+                for (int v = 1; v < kWarps; ++v) {
+                    const float4 p = *reinterpret_cast<const float4 *>(parts + (v * kTallRows + r) * (R8 + 4) + col);
+                    s.x += p.x, s.y += p.y, s.z += p.z, s.w += p.w;
+                }
+                if (l.ids[r] == id)
+                    *reinterpret_cast<float4 *>(a.V + (t0 + r) * width + rb * R8 + col) =
+                        make_float4(s.x * scale, s.y * scale, s.z * scale, s.w * scale);
+            }
+            __syncthreads();
+        }
+    }
+}
+
+// A warp's turn is 32 columns: B's 32 rows, in a pitch that keeps two rows' 16 bytes apart, and the tile's 32 rows of y.
+__host__ __device__ constexpr int expand_turn_bytes(int NR, int ys) { return 32 * (16 * NR + 16) + 32 * 32 * ys; }
+
+// Ranks up to 8 NR in one pass.
+template <int NR, int TYPE, int PIECES, bool YW>
+__global__ void __launch_bounds__(kThreads, 1) expand16_kernel(const LoraArgs a)
+{
+    constexpr int Q = 2 * NR, PITCH = 16 * NR + 16, YS = YW ? 4 : 2, TURN = expand_turn_bytes(NR, YS), YP = 32 * YS;
+    constexpr int BL = NR, YL = YP / 16;                     // 16-byte pieces of a row of B (2 NR bytes a lane of 8), and of y
+    extern __shared__ __align__(16) uint8_t ring[];
+    __shared__ TileList l;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTallRows;
+    const bool y_half = a.y_type == QK_F16;
+    const int turns_all = (a.N + 31) / 32, per = (turns_all + static_cast<int>(gridDim.y) - 1) / static_cast<int>(gridDim.y);
+    const int first = min(turns_all, static_cast<int>(blockIdx.y) * per), last = min(turns_all, first + per);
+    const uint32_t mine = smem_u32(ring) + warp * kTurns * TURN;
+    moe::let_next_start();
+    moe::wait_for_previous();
+    list_adapters(l, a, t0, kTallRows);
+    // rows without an adapter
+    unsigned none = __ballot_sync(~0u, t0 + lane < a.T && (l.ids[lane] < 0 || l.ids[lane] >= a.n_adapters));
+    for (; none; none &= none - 1) {
+        const int i = __ffs(none) - 1;
+        const bool bad = l.ids[i] >= 0;
+        if (bad && tid == 0 && blockIdx.y == 0) record_error(a.err, kErrBadIndex);
+        if (bad || a.out != a.y)
+            for (int n = 32 * first + tid; n < min(a.N, 32 * last); n += kThreads)
+                store_float_as(a.out, (t0 + i) * a.ldo + n, a.y_type,
+                               bad ? __int_as_float(0x7fc00000) : load_as_float(a.y, (t0 + i) * a.ldy + n, a.y_type));
+    }
+    for (int j = 0; j < l.n; ++j) {
+        const int id = l.list[j];
+        // a lane copies 16 bytes of every (32 / BL)th row of B, and of every (32 / YL)th of y
+        const int b_row = lane / BL, b_ch = lane % BL, y_row = lane / YL, y_ch = lane % YL;
+        const bool b_on = 8 * b_ch < a.rank;
+        unsigned rows = 0;
+#pragma unroll
+        for (int i = 0; i < YL; ++i) rows |= (l.ids[i * (32 / YL) + y_row] == id) << i;
+        int from = first + warp;                             // the turn that is fetched next
+        const uint16_t *B = static_cast<const uint16_t *>(a.B) + (static_cast<int64_t>(id) * a.N + 32 * from + b_row) * a.rank + 8 * b_ch;
+        const char *Y = static_cast<const char *>(a.y) + ((t0 + y_row) * a.ldy + 32 * from) * YS + 16 * y_ch;
+        const int64_t b_step = (32 / BL) * static_cast<int64_t>(a.rank), y_step = (32 / YL) * a.ldy * YS;
+        const auto fetch = [&](int slot) {
+            if (from < last) {
+                const uint32_t to = mine + slot * TURN;
+                const uint16_t *b = B;
+#pragma unroll
+                for (int i = 0; i < BL; ++i, b += b_step)
+                    lora_copy16(to + (i * (32 / BL) + b_row) * PITCH + 16 * b_ch, b, b_on && 32 * from + i * (32 / BL) + b_row < a.N);
+                const char *y = Y;
+                const bool y_on = 32 * from + y_ch * (16 / YS) < a.N;
+#pragma unroll
+                for (int i = 0; i < YL; ++i, y += y_step)
+                    lora_copy16(to + 32 * PITCH + (i * (32 / YL) + y_row) * YP + 16 * y_ch, y, y_on && (rows >> i) & 1u);
+                from += kWarps, B += kWarps * 32 * static_cast<int64_t>(a.rank), Y += kWarps * 32 * YS;
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        if (a.rank < 8 * NR) {
+            // ranks past the last hold zeros for good
+            for (int i = lane; i < kTurns * 32 * NR; i += 32) {
+                const int ch = i % NR, row = i / NR % 32, slot = i / NR / 32;
+                if (8 * ch >= a.rank)
+                    *reinterpret_cast<uint4 *>(ring + warp * kTurns * TURN + slot * TURN + row * PITCH + 16 * ch) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            __syncwarp();
+        }
+#pragma unroll
+        for (int i = 0; i < kTurns - 1; ++i) fetch(i);
+        bool in[2][2];
+        float back[2][2];
+        uint32_t piece[PIECES][2][2][Q / 2];
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                in[m][h] = l.ids[m * 16 + h * 8 + g] == id;
+                const float *from = a.V + (t0 + m * 16 + h * 8 + g) * (8 * NR) + Q * c;
+                float v[Q], up = 1.0f;
+#pragma unroll
+                for (int k = 0; k < Q; k += 4) {
+                    const float4 f = in[m][h] ? *reinterpret_cast<const float4 *>(from + k) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    v[k] = f.x, v[k + 1] = f.y, v[k + 2] = f.z, v[k + 3] = f.w;
+                }
+                back[m][h] = 1.0f;
+                if constexpr (TYPE == kF16) {
+                    // a power of two puts the row's largest into [2^14, 2^15)
+                    uint32_t most = 0;
+#pragma unroll
+                    for (int k = 0; k < Q; ++k) most = max(most, __float_as_uint(v[k]) & 0x7fffffffu);
+                    most = max(most, __shfl_xor_sync(~0u, most, 1)), most = max(most, __shfl_xor_sync(~0u, most, 2));
+                    const int ex = most >= 0x7f800000u || most == 0 ? 141 : max(static_cast<int>(most >> 23), 15);
+                    up = __uint_as_float(static_cast<uint32_t>(127 + 141 - ex) << 23);
+                    back[m][h] = __uint_as_float(static_cast<uint32_t>(127 - 141 + ex) << 23);
+                }
+#pragma unroll
+                for (int k = 0; k < Q; k += 2) {
+                    float x = v[k] * up, y = v[k + 1] * up;
+#pragma unroll
+                    for (int p = 0; p < PIECES; ++p) {
+                        const uint32_t w = pack16(x, y, TYPE == kF16);
+                        const float2 f = unpack16(w, TYPE == kF16);
+                        piece[p][m][h][k / 2] = w;
+                        x -= f.x, y -= f.y;
+                    }
+                }
+            }
+        int slot = 0;
+        for (int turn = first + warp; turn < last; turn += kWarps) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kTurns - 2) : "memory");
+            __syncwarp();                                    // this turn has landed, and the slot before it is free
+            fetch(slot == 0 ? kTurns - 1 : slot - 1);
+            const uint32_t at = mine + slot * TURN;
+            float sum[2][4][4];
+#pragma unroll
+            for (int nt = 0; nt < 4; ++nt) {
+                uint32_t w[Q / 2];
+                const uint32_t from = at + (8 * (g >> 1) + 2 * nt + (g & 1)) * PITCH + 2 * Q * c;
+                if constexpr (Q >= 8) {
+#pragma unroll
+                    for (int k = 0; k < Q / 8; ++k) {
+                        const uint4 v = lora_lds(from + 16 * k);
+                        w[4 * k] = v.x, w[4 * k + 1] = v.y, w[4 * k + 2] = v.z, w[4 * k + 3] = v.w;
+                    }
+                } else {
+                    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(from));
+                }
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) sum[m][nt][k] = 0.0f;
+#pragma unroll
+                    for (int p = PIECES - 1; p >= 0; --p)
+#pragma unroll
+                        for (int s = 0; s < NR / 2; ++s)
+                            mma16<TYPE>(sum[m][nt], piece[p][m][0][2 * s], piece[p][m][1][2 * s], piece[p][m][0][2 * s + 1],
+                                        piece[p][m][1][2 * s + 1], w[2 * s], w[2 * s + 1]);
+                }
+            }
+            const int col = turn * 32 + 8 * c;
+            char *out0 = static_cast<char *>(a.out) + ((t0 + g) * a.ldo + col) * YS;
+            const int64_t o_step = 8 * a.ldo * YS;
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int row = m * 16 + h * 8 + g;
+                    float d[8];
+#pragma unroll
+                    for (int nt = 0; nt < 4; ++nt) d[2 * nt] = sum[m][nt][2 * h], d[2 * nt + 1] = sum[m][nt][2 * h + 1];
+                    if constexpr (TYPE == kF16) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) d[k] *= back[m][h];
+                    }
+                    char *out = out0 + (2 * m + h) * o_step;
+                    const bool on = in[m][h] && col < a.N;
+                    if constexpr (YW) {
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const uint4 v = lora_lds(at + 32 * PITCH + row * YP + 32 * c + 16 * k);
+                            if (on)
+                                *(reinterpret_cast<float4 *>(out) + k) = make_float4(__uint_as_float(v.x) + d[4 * k], __uint_as_float(v.y) + d[4 * k + 1],
+                                                                                     __uint_as_float(v.z) + d[4 * k + 2], __uint_as_float(v.w) + d[4 * k + 3]);
+                        }
+                    } else {
+                        const uint4 v = lora_lds(at + 32 * PITCH + row * YP + 16 * c);
+                        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+                        uint32_t r[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float2 f = unpack16(u[k], y_half);
+                            r[k] = pack16(f.x + d[2 * k], f.y + d[2 * k + 1], y_half);
+                        }
+                        if (on) *reinterpret_cast<uint4 *>(out) = make_uint4(r[0], r[1], r[2], r[3]);
+                    }
+                }
+            slot = slot + 1 == kTurns ? 0 : slot + 1;
+        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncwarp();
+    }
+}
+
+template <int NR, int TYPE, int PIECES, bool YW>
+cudaError_t launch_tall16(const LoraArgs &a, int sms, cudaStream_t st)
+{
+    constexpr int sums = static_cast<int>(sizeof(float)) * kWarps * kTallRows * (8 * NR + 4), turns = kWarps * kTurns * shrink_turn_bytes<NR>();
+    constexpr int smem = sums > turns ? sums : turns, ring = kWarps * kTurns * expand_turn_bytes(NR, YW ? 4 : 2);
+    cudaError_t e = cudaFuncSetAttribute(shrink16_kernel<NR, TYPE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(expand16_kernel<NR, TYPE, PIECES, YW>, cudaFuncAttributeMaxDynamicSharedMemorySize, ring);
+    if (e != cudaSuccess) return e;
+    e = moe::launch_chained(shrink16_kernel<NR, TYPE>, dim3(static_cast<unsigned>((a.T + kTallRows - 1) / kTallRows)), kThreads, smem, st,
+                            library_programmatic(), a);
+    if (e != cudaSuccess) return e;
+    const unsigned tiles = static_cast<unsigned>((a.T + kTallRows - 1) / kTallRows);
+    // columns are cut where tiles do not fill the GPU, down to a turn a warp
+    const unsigned cuts = static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>((a.N + 32 * kWarps - 1) / (32 * kWarps), sms / tiles)));
+    return moe::launch_chained(expand16_kernel<NR, TYPE, PIECES, YW>, dim3(tiles, cuts), kThreads, ring, st, true, a);
+}
+
 template <int NR, int TYPE, int PIECES, bool XW, bool WW>
 cudaError_t launch_tall_as(const LoraArgs &a, int sms, cudaStream_t st)
 {
@@ -846,6 +1098,11 @@ cudaError_t launch_tall_as(const LoraArgs &a, int sms, cudaStream_t st)
 template <int NR>
 cudaError_t launch_tall_types(const LoraArgs &a, int sms, cudaStream_t st)
 {
+    if (a.x_type == a.w_type && a.x_type != QK_F32 && a.vec_x && a.vec_a && a.vec_b && a.vec_y && a.N % 8 == 0 && a.rank <= 8 * NR) {
+        const bool wide = a.y_type == QK_F32;
+        if (a.x_type == QK_F16) return wide ? launch_tall16<NR, kF16, 2, true>(a, sms, st) : launch_tall16<NR, kF16, 2, false>(a, sms, st);
+        return wide ? launch_tall16<NR, kBf16, 3, true>(a, sms, st) : launch_tall16<NR, kBf16, 2, false>(a, sms, st);
+    }
     if (a.x_type == QK_BF16 && a.w_type == QK_BF16)
         return a.y_type == QK_F32 ? launch_tall_as<NR, kBf16, 3, false, false>(a, sms, st) : launch_tall_as<NR, kBf16, 2, false, false>(a, sms, st);
     if (a.x_type == QK_F16 && a.w_type == QK_F16) return launch_tall_as<NR, kF16, 2, false, false>(a, sms, st);
