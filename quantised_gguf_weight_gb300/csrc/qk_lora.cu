@@ -805,8 +805,12 @@ __global__ void __launch_bounds__(kThreads, 1) shrink16_kernel(const LoraArgs a)
             const int tiles = min(NR, (a.rank - rb * R8) / 8);
             const int64_t x_step = 8 * a.ldx, w_step = 8LL * a.K;
             const auto fetch = [&](int k, int slot) {
-                if (k + 8 * c < a.K) {
-                    uint32_t to = mine + slot * TURN + g * 64 + 16 * c;
+                uint32_t to = mine + slot * TURN + g * 64 + 16 * c;
+                if (k < a.K && k + 8 * c >= a.K) {
+                    // past the rows' end: zeros
+#pragma unroll
+                    for (int i = 0; i < kTallRows / 8 + NR; ++i) asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(to + i * 512), "r"(0) : "memory");
+                } else if (k < a.K) {
                     const uint16_t *q = x0 + k;
 #pragma unroll
                     for (int i = 0; i < kTallRows / 8; ++i, q += x_step) lora_copy16(to + i * 512, q, (rows >> i) & 1u);
@@ -833,21 +837,25 @@ __global__ void __launch_bounds__(kThreads, 1) shrink16_kernel(const LoraArgs a)
                 __syncwarp();                                // this turn has landed, and the slot before it is free
                 fetch(k + (kTurns - 1) * kTurn, slot == 0 ? kTurns - 1 : slot - 1);
                 const uint32_t at = mine + slot * TURN + g * 64 + 16 * c;
-                const bool has = k + 8 * c < a.K;
-                uint4 x[2][2];
+                // (rows of other tokens hold what they held; ranks past the last are dropped below)
+                uint4 x[2][2], w[NR];
 #pragma unroll
                 for (int m = 0; m < 2; ++m)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) x[m][h] = has && (rows >> (2 * m + h)) & 1u ? lora_lds(at + (2 * m + h) * 512) : zero;
-#pragma unroll
-                for (int n = 0; n < NR; ++n) {
-                    const uint4 w = has && n < tiles ? lora_lds(at + kTallRows * 64 + n * 512) : zero;
-#pragma unroll
-                    for (int m = 0; m < 2; ++m) {
-                        mma16<TYPE>(acc[m][n], x[m][0].x, x[m][1].x, x[m][0].y, x[m][1].y, w.x, w.y);
-                        mma16<TYPE>(acc[m][n], x[m][0].z, x[m][1].z, x[m][0].w, x[m][1].w, w.z, w.w);
+                    for (int h = 0; h < 2; ++h) {
+                        x[m][h] = lora_lds(at + (2 * m + h) * 512);
+                        if (!((rows >> (2 * m + h)) & 1u)) x[m][h] = zero;
                     }
-                }
+#pragma unroll
+                for (int n = 0; n < NR; ++n) w[n] = lora_lds(at + kTallRows * 64 + n * 512);
+#pragma unroll
+                for (int n = 0; n < NR; ++n)
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) mma16<TYPE>(acc[m][n], x[m][0].x, x[m][1].x, x[m][0].y, x[m][1].y, w[n].x, w[n].y);
+#pragma unroll
+                for (int n = 0; n < NR; ++n)
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) mma16<TYPE>(acc[m][n], x[m][0].z, x[m][1].z, x[m][0].w, x[m][1].w, w[n].z, w[n].w);
                 slot = slot + 1 == kTurns ? 0 : slot + 1;
             }
             asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -871,7 +879,7 @@ __global__ void __launch_bounds__(kThreads, 1) shrink16_kernel(const LoraArgs a)
                 }
                 if (l.ids[r] == id)
                     *reinterpret_cast<float4 *>(a.V + (t0 + r) * width + rb * R8 + col) =
-                        make_float4(s.x * scale, s.y * scale, s.z * scale, s.w * scale);
+                        rb * R8 + col < a.rank ? make_float4(s.x * scale, s.y * scale, s.z * scale, s.w * scale) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             }
             __syncthreads();
         }
@@ -993,31 +1001,35 @@ __global__ void __launch_bounds__(kThreads, 1) expand16_kernel(const LoraArgs a)
             fetch(slot == 0 ? kTurns - 1 : slot - 1);
             const uint32_t at = mine + slot * TURN;
             float sum[2][4][4];
+            uint32_t w[4][Q / 2];
 #pragma unroll
             for (int nt = 0; nt < 4; ++nt) {
-                uint32_t w[Q / 2];
                 const uint32_t from = at + (8 * (g >> 1) + 2 * nt + (g & 1)) * PITCH + 2 * Q * c;
                 if constexpr (Q >= 8) {
 #pragma unroll
                     for (int k = 0; k < Q / 8; ++k) {
                         const uint4 v = lora_lds(from + 16 * k);
-                        w[4 * k] = v.x, w[4 * k + 1] = v.y, w[4 * k + 2] = v.z, w[4 * k + 3] = v.w;
+                        w[nt][4 * k] = v.x, w[nt][4 * k + 1] = v.y, w[nt][4 * k + 2] = v.z, w[nt][4 * k + 3] = v.w;
                     }
                 } else {
-                    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(from));
+                    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[nt][0]), "=r"(w[nt][1]) : "r"(from));
                 }
 #pragma unroll
-                for (int m = 0; m < 2; ++m) {
+                for (int m = 0; m < 2; ++m)
 #pragma unroll
                     for (int k = 0; k < 4; ++k) sum[m][nt][k] = 0.0f;
-#pragma unroll
-                    for (int p = PIECES - 1; p >= 0; --p)
-#pragma unroll
-                        for (int s = 0; s < NR / 2; ++s)
-                            mma16<TYPE>(sum[m][nt], piece[p][m][0][2 * s], piece[p][m][1][2 * s], piece[p][m][0][2 * s + 1],
-                                        piece[p][m][1][2 * s + 1], w[2 * s], w[2 * s + 1]);
-                }
             }
+            // eight sums in turn: a product waits for the one before it in its own
+#pragma unroll
+            for (int p = PIECES - 1; p >= 0; --p)
+#pragma unroll
+                for (int s = 0; s < NR / 2; ++s)
+#pragma unroll
+                    for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+                        for (int m = 0; m < 2; ++m)
+                            mma16<TYPE>(sum[m][nt], piece[p][m][0][2 * s], piece[p][m][1][2 * s], piece[p][m][0][2 * s + 1],
+                                        piece[p][m][1][2 * s + 1], w[nt][2 * s], w[nt][2 * s + 1]);
             const int col = turn * 32 + 8 * c;
             char *out0 = static_cast<char *>(a.out) + ((t0 + g) * a.ldo + col) * YS;
             const int64_t o_step = 8 * a.ldo * YS;
