@@ -115,6 +115,21 @@ __device__ __forceinline__ void mma_pieces(float (&d)[4], const float (&a)[4], f
     if constexpr (PB == 2) mma8(d, ah, tf32_of(b0 - __uint_as_float(h0)), tf32_of(b1 - __uint_as_float(h1)));
 }
 
+__device__ __forceinline__ uint32_t pack16(float lo, float hi, bool half)
+{
+    if (half) {
+        const __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ float2 unpack16(uint32_t w, bool half)
+{
+    if (half) return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+
 __device__ __forceinline__ float4 read_remote(uint32_t addr)
 {
     float4 v;
@@ -162,18 +177,21 @@ __global__ void __launch_bounds__(kThreads) lora_kernel(const LoraArgs a)
     const int n_per = ((a.N + kCluster - 1) / kCluster + 15) / 16 * 16, n0 = min(a.N, rank * n_per), n1 = min(a.N, n0 + n_per);
     const bool x_half = a.x_type == QK_F16, w_half = a.w_type == QK_F16;
 
-    if (step == 0) {                                         // rows without an adapter
-        const bool moves = a.out != a.y;
-        for (int i = 0; i < ROWS; ++i) {
-            const int64_t t = t0 + i;
-            if (t >= a.T) break;
-            const bool bad = ids[i] >= a.n_adapters;
-            if (ids[i] >= 0 && !bad) continue;
-            if (bad && tid == 0 && rank == 0) record_error(a.err, kErrBadIndex);
-            if (bad || moves)
-                for (int n = n0 + tid; n < n1; n += kThreads)
-                    store_float_as(a.out, t * a.ldo + n, a.y_type,
-                                   bad ? __int_as_float(0x7fc00000) : load_as_float(a.y, t * a.ldy + n, a.y_type));
+    if (step == 0) {
+        // rows without an adapter
+        for (int base = 0; base < ROWS; base += 32) {
+            const int r = base + lane;
+            unsigned none = __ballot_sync(~0u, r < ROWS && t0 + r < a.T && (ids[r < ROWS ? r : 0] < 0 || ids[r < ROWS ? r : 0] >= a.n_adapters));
+            for (; none; none &= none - 1) {
+                const int i = base + __ffs(none) - 1;
+                const int64_t t = t0 + i;
+                const bool bad = ids[i] >= 0;
+                if (bad && tid == 0 && rank == 0) record_error(a.err, kErrBadIndex);
+                if (bad || a.out != a.y)
+                    for (int n = n0 + tid; n < n1; n += kThreads)
+                        store_float_as(a.out, t * a.ldo + n, a.y_type,
+                                       bad ? __int_as_float(0x7fc00000) : load_as_float(a.y, t * a.ldy + n, a.y_type));
+            }
         }
     }
 
@@ -188,36 +206,57 @@ __global__ void __launch_bounds__(kThreads) lora_kernel(const LoraArgs a)
                 for (int n = 0; n < NR; ++n)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.0f;
-            for (int k = k0 + warp * 32; k < k1; k += kWarps * 32) {
-                float xv[MT][2][8];
+            struct Turn {
+                float x[MT][2][8], w[NR][8];
+            };
+            const auto load = [&](Turn &t, int k) {
 #pragma unroll
                 for (int m = 0; m < MT; ++m)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const int row = m * 16 + h * 8 + g;
-                        const bool in = ids[row] == id;
-                        if (in) load_values<8, XW>(xv[m][h], a.x, (t0 + row) * a.ldx, k + 8 * c, a.K, a.vec_x, x_half);
+                        if (ids[row] == id) load_values<8, XW>(t.x[m][h], a.x, (t0 + row) * a.ldx, k + 8 * c, a.K, a.vec_x, x_half);
                         else {
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) xv[m][h][i] = 0.0f;
+                            for (int i = 0; i < 8; ++i) t.x[m][h][i] = 0.0f;
                         }
                     }
 #pragma unroll
                 for (int n = 0; n < NR; ++n) {
                     const int r = rb * R8 + n * 8 + g;
-                    float av[8];
-                    if (r < a.rank) load_values<8, WW>(av, a.A, (a_row + r) * a.K, k + 8 * c, a.K, a.vec_a, w_half);
+                    if (r < a.rank) load_values<8, WW>(t.w[n], a.A, (a_row + r) * a.K, k + 8 * c, a.K, a.vec_a, w_half);
                     else {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) av[i] = 0.0f;
+                        for (int i = 0; i < 8; ++i) t.w[n][i] = 0.0f;
                     }
+                }
+            };
+            const auto products = [&](const Turn &t) {
 #pragma unroll
-                    for (int s = 0; s < 4; ++s)
+                for (int s = 0; s < 4; ++s)
+#pragma unroll
+                    for (int n = 0; n < NR; ++n)
 #pragma unroll
                         for (int m = 0; m < MT; ++m) {
-                            const float xa[4] = {xv[m][0][2 * s], xv[m][1][2 * s], xv[m][0][2 * s + 1], xv[m][1][2 * s + 1]};
-                            mma_pieces<XW ? 2 : 1, WW ? 2 : 1>(acc[m][n], xa, av[2 * s], av[2 * s + 1]);
+                            const float xa[4] = {t.x[m][0][2 * s], t.x[m][1][2 * s], t.x[m][0][2 * s + 1], t.x[m][1][2 * s + 1]};
+                            mma_pieces<XW ? 2 : 1, WW ? 2 : 1>(acc[m][n], xa, t.w[n][2 * s], t.w[n][2 * s + 1]);
                         }
+            };
+            // a turn ahead where registers allow
+            if constexpr (MT * 2 + NR <= 6) {
+                int k = k0 + warp * 32;
+                Turn next;
+                if (k < k1) load(next, k);
+                for (; k < k1; k += kWarps * 32) {
+                    const Turn t = next;
+                    if (k + kWarps * 32 < k1) load(next, k + kWarps * 32);
+                    products(t);
+                }
+            } else {
+                for (int k = k0 + warp * 32; k < k1; k += kWarps * 32) {
+                    Turn t;
+                    load(t, k);
+                    products(t);
                 }
             }
 #pragma unroll
@@ -555,21 +594,6 @@ __global__ void __launch_bounds__(kThreads, TYPE == kTf32 ? 1 : 2) shrink_kernel
             __syncthreads();
         }
     }
-}
-
-__device__ __forceinline__ uint32_t pack16(float lo, float hi, bool half)
-{
-    if (half) {
-        const __half2 h = __floats2half2_rn(lo, hi);
-        return *reinterpret_cast<const uint32_t *>(&h);
-    }
-    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-__device__ __forceinline__ float2 unpack16(uint32_t w, bool half)
-{
-    if (half) return __half22float2(*reinterpret_cast<const __half2 *>(&w));
-    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 
 // PIECES: of V, in 16 bits.

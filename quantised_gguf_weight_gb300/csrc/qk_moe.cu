@@ -4,7 +4,6 @@
 #include <algorithm>
 #include <atomic>
 
-#include "qk_kv4.cuh"
 #include "qk_moe.cuh"
 #include "qk_tc.cuh"
 
@@ -157,26 +156,6 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a)
         }
     });
     if (blocks > 1) cluster_sync();             // the counts are read to the end
-}
-
-// Four neighbouring values of a row, 0 past its end.
-__device__ __forceinline__ float4 four(const void *x, int64_t row, int k, int cols, int type, bool vec)
-{
-    if (vec && k + 4 <= cols) {
-        if (type == QK_F32) return *reinterpret_cast<const float4 *>(static_cast<const float *>(x) + row + k);
-        const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(x) + row + k);
-        if (type == QK_F16) {
-            const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&w.x));
-            const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&w.y));
-            return make_float4(a.x, a.y, b.x, b.y);
-        }
-        return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
-                           __uint_as_float(w.y & 0xffff0000u));
-    }
-    float v[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = k + i < cols ? load_as_float(x, row + k + i, type) : 0.0f;
-    return make_float4(v[0], v[1], v[2], v[3]);
 }
 
 __device__ __forceinline__ uint32_t pack2h(float a, float b)
@@ -347,6 +326,7 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(const SumArgs a)
 struct Layout {
     int64_t A, octets, sets, tile_sets;
     int pieces, w_pieces, tile_tokens;
+    bool few;                 // few assignments: only h is used
     bool tiled;               // some expert may have enough tokens for the tile form
     int64_t head, assignment, place, column, set, tile_set, x_scale, h_scale, x, x_tile, h, h_ops, h_tile, parts, bytes;
 };
@@ -364,6 +344,12 @@ Layout layout_of(int64_t T, int top_k, int64_t E, int64_t K, int64_t F, int64_t 
     l.w_pieces = x_type == QK_BF16 && y_type == QK_BF16 ? 1 : 2;
     l.tile_tokens = 128;
     // (an id may repeat within a token: such an expert goes by the few-token form, however many it has)
+    l.few = l.A <= kMaxFew && K <= kMaxFewCols && F <= kMaxFewCols;
+    if (l.few) {
+        // groups of 16 values and their sum, whole runs of 256
+        l.bytes = up256(l.A * ((F + 255) / 256 * 256) / 16 * 20 * 4);
+        return l;
+    }
     l.tiled = T >= kTileFrom;
     const int64_t used = std::min(l.A, E);
     // with the many-token form: experts of fewer than kTileFrom tokens, or sets a quarter as many again as those
@@ -411,10 +397,10 @@ int check_weights(const qk_expert_weights *w, int64_t E, int64_t rows, int64_t c
     return QK_OK;
 }
 
-cudaError_t rows_launch(const RowsArgs &a, bool paired, int sms, cudaStream_t st)
+template <class F>
+F *by_format(int fmt, F *q4k, F *q80, F *q6k)
 {
-    return a.fmt == kFmtQ4K ? rows_launch_q4k(a, paired, sms, st)
-                            : a.fmt == kFmtQ80 ? rows_launch_q80(a, paired, sms, st) : rows_launch_q6k(a, paired, sms, st);
+    return fmt == kFmtQ4K ? q4k : fmt == kFmtQ80 ? q80 : q6k;
 }
 
 }  // namespace
@@ -467,6 +453,19 @@ int qk_moe_ffn(const qk_expert_weights *gate, const qk_expert_weights *up, const
     if (!err || !device_limits(&sms, &smem)) return QK_ERR_CUDA;
     char *ws = static_cast<char *>(workspace);
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+
+    if (l.few) {
+        FewArgs f{};
+        f.ids = ids, f.experts = static_cast<int>(n_experts), f.top_k = top_k, f.err = err;
+        f.a = wg, f.b = wu, f.cols = static_cast<int>(K), f.rows = static_cast<int>(F);
+        f.x = x, f.ldx = ldx, f.x_type = x_type, f.vec = multiple(x, 4 * size_of(x_type)) && ldx % 4 == 0;
+        f.h = reinterpret_cast<float *>(ws + l.h);
+        f.weights = weights, f.y = y, f.ldy = ldy, f.y_type = y_type;
+        cudaError_t e = by_format(gate->format, few_gate_q4k, few_gate_q80, few_gate_q6k)(f, l.A, down->format, library_programmatic(), s);
+        f.a = wd, f.cols = static_cast<int>(F), f.rows = static_cast<int>(N);
+        if (e == cudaSuccess) e = by_format(down->format, few_down_q4k, few_down_q80, few_down_q6k)(f, T, s);
+        return e == cudaSuccess ? QK_OK : QK_ERR_CUDA;
+    }
 
     PlanArgs pa{};
     pa.ids = ids, pa.n = static_cast<int>(l.A), pa.experts = static_cast<int>(n_experts), pa.err = err;
@@ -521,9 +520,7 @@ int qk_moe_ffn(const qk_expert_weights *gate, const qk_expert_weights *up, const
             t.tiles = static_cast<int>(paired ? (rows + 63) / 64 : (rows + 127) / 128);
             t.scale = reinterpret_cast<const float *>(ws + scale), t.out = reinterpret_cast<float *>(ws + to);
             t.skip_chunk = g_skip_chunk.load(), t.wait_ns = library_wait_limit_ns(), t.err = err;
-            const cudaError_t e = fmt == kFmtQ4K ? tile_launch_q4k(o, t, paired, sms, s)
-                                : fmt == kFmtQ80 ? tile_launch_q80(o, t, paired, sms, s)
-                                                 : tile_launch_q6k(o, t, paired, sms, s);
+            const cudaError_t e = by_format(fmt, tile_launch_q4k, tile_launch_q80, tile_launch_q6k)(o, t, paired, sms, s);
             if (e != cudaSuccess) return e;
         }
         RowsArgs r{};
@@ -533,7 +530,7 @@ int qk_moe_ffn(const qk_expert_weights *gate, const qk_expert_weights *up, const
         r.sms = sms, r.wait_ns = library_wait_limit_ns(), r.err = err;
         r.x = reinterpret_cast<const uint8_t *>(ws + ops), r.scale = reinterpret_cast<const float *>(ws + scale);
         r.out = reinterpret_cast<float *>(ws + to);
-        return rows_launch(r, paired, sms, s);
+        return by_format(fmt, rows_launch_q4k, rows_launch_q80, rows_launch_q6k)(r, paired, sms, s);
     };
     e = pack(x, ldx, x_type, top_k, K, gate->format, l.x, l.x_tile, l.x_scale);
     if (e == cudaSuccess) e = products(wg, wu, gate->format, K, F, true, l.x, l.x_tile, l.x_scale, l.h);

@@ -20,6 +20,7 @@
 
 #include "qk_device.cuh"
 #include "qk_internal.h"
+#include "qk_kv4.cuh"
 
 namespace qk {
 namespace moe {
@@ -28,6 +29,11 @@ constexpr int kMaxExperts = 1024;
 constexpr int kSetOctets = 2;
 constexpr int kTileBoxRows = 32;                  // rows of a TMA box of a tile set's operands
 constexpr int kRowWarps = 16;                     // warps of a thread block of the few-token products
+// Assignments up to which no plan is made (qk_moe_few.cuh), which reads an expert again for each of its tokens.  8 of
+// 128 experts of 768 x 2048, Q4_K and Q6_K: one token 30 us, with the plan 50; three 63 and 68; four 76 and 72; where 8
+// experts have all tokens three take 52 and 50.
+constexpr int kMaxFew = 24;
+constexpr int kMaxFewCols = 8192;                 // a row of x has to fit into shared memory
 constexpr int kUnit = 256;                        // columns of a unit of the products' loops
 constexpr int kPieceBytes = 8 * 32 * 16;          // an octet's unit, one piece: 8 steps of 16 bytes a lane
 constexpr int kSumBytes = 32 * 8;                 // the sums of its sub-blocks (Q4_K)
@@ -92,6 +98,24 @@ struct TileArgs {
     int *err;
 };
 
+// The two launches of few assignments.
+struct FewArgs {
+    const int32_t *ids;
+    int experts, top_k;
+    Weights a, b;             // gate and up; or down
+    int cols, rows;
+    const void *x;
+    int64_t ldx;
+    int x_type;
+    bool vec;                 // rows of x start on four values
+    float *h;                 // [assignment], groups of 16
+    const float *weights;
+    void *y;
+    int64_t ldy;
+    int y_type;
+    int *err;
+};
+
 // The tokens' operands: rows [rows][cols] of fp16 pieces.
 struct TileOperands {
     const void *hi, *lo;
@@ -108,12 +132,38 @@ __host__ __device__ inline int64_t row_bytes_of(int fmt, int64_t K)
     return fmt == kFmtQ80 ? (K + 31) / 32 * 34 : (K + 255) / 256 * unit_bytes(fmt);
 }
 
+cudaError_t few_gate_q4k(const FewArgs &a, int64_t A, int down, bool chained, cudaStream_t st);
+cudaError_t few_down_q4k(const FewArgs &a, int64_t T, cudaStream_t st);
+cudaError_t few_gate_q80(const FewArgs &a, int64_t A, int down, bool chained, cudaStream_t st);
+cudaError_t few_down_q80(const FewArgs &a, int64_t T, cudaStream_t st);
+cudaError_t few_gate_q6k(const FewArgs &a, int64_t A, int down, bool chained, cudaStream_t st);
+cudaError_t few_down_q6k(const FewArgs &a, int64_t T, cudaStream_t st);
 cudaError_t rows_launch_q4k(const RowsArgs &a, bool paired, int sms, cudaStream_t st);
 cudaError_t rows_launch_q80(const RowsArgs &a, bool paired, int sms, cudaStream_t st);
 cudaError_t rows_launch_q6k(const RowsArgs &a, bool paired, int sms, cudaStream_t st);
 cudaError_t tile_launch_q4k(const TileOperands &t, const TileArgs &a, bool paired, int sms, cudaStream_t st);
 cudaError_t tile_launch_q80(const TileOperands &t, const TileArgs &a, bool paired, int sms, cudaStream_t st);
 cudaError_t tile_launch_q6k(const TileOperands &t, const TileArgs &a, bool paired, int sms, cudaStream_t st);
+
+// Four neighbouring values of a row, 0 past its end.
+__device__ __forceinline__ float4 four(const void *x, int64_t row, int k, int cols, int type, bool vec)
+{
+    if (vec && k + 4 <= cols) {
+        if (type == QK_F32) return *reinterpret_cast<const float4 *>(static_cast<const float *>(x) + row + k);
+        const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(x) + row + k);
+        if (type == QK_F16) {
+            const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&w.x));
+            const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&w.y));
+            return make_float4(a.x, a.y, b.x, b.y);
+        }
+        return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
+                           __uint_as_float(w.y & 0xffff0000u));
+    }
+    float v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = k + i < cols ? load_as_float(x, row + k + i, type) : 0.0f;
+    return make_float4(v[0], v[1], v[2], v[3]);
+}
 
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
