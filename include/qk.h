@@ -575,8 +575,9 @@ size_t qk_moe_ffn_workspace_bytes(int64_t T, int top_k, int64_t n_experts, int64
  * to 22 bits in fp32 (and A x, in between).
  *   workspace   NULL, or device scratch, 256-byte aligned, whose contents need
  *               not be kept or set; calls that may overlap need one each.
- *               With qk_lora_workspace_bytes() of it, many tokens take two
- *               launches instead of one, which is faster.
+ *               With qk_lora_workspace_bytes() of it, calls of many tokens,
+ *               of 16-bit operands or of high ranks take two launches instead
+ *               of one, which is faster.
  * rank <= 256; K, N <= 2^24; T <= 2^26.  T == 0 does nothing.
  */
 int qk_lora(const void *x, int64_t ldx, int x_type, int64_t T, int64_t K, const void *A, const void *B, int w_type,

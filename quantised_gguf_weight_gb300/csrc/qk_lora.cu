@@ -502,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, TYPE == kTf32 ? 1 : 2) shrink_kernel
     moe::let_next_start();
     moe::wait_for_previous();
     list_adapters(l, a, t0, kShrinkRows);
-    for (int j = 0; j < l.n; ++j) {
+    for (int j = blockIdx.y; j < l.n; j += gridDim.y) {
         const int id = l.list[j];
         const int64_t a_row = static_cast<int64_t>(id) * a.rank;
         const bool in[2] = {l.ids[g] == id, l.ids[8 + g] == id};
@@ -543,12 +543,17 @@ __global__ void __launch_bounds__(kThreads, TYPE == kTf32 ? 1 : 2) shrink_kernel
             };
             const auto products = [&](const Turn &t) {
                 if constexpr (TYPE == kTf32) {
+                    // a turn's products are summed apart: the tensor cores cut a sum at 2^-24 of it, always towards zero
 #pragma unroll
-                    for (int s = 0; s < 4; ++s) {
-                        const float xa[4] = {t.x[0].f[2 * s], t.x[1].f[2 * s], t.x[0].f[2 * s + 1], t.x[1].f[2 * s + 1]};
+                    for (int n = 0; n < NR; ++n) {
+                        float sum[4] = {};
 #pragma unroll
-                        for (int n = 0; n < NR; ++n)
-                            mma_pieces<XW ? 2 : 1, WW ? 2 : 1>(acc[n], xa, t.w[n].f[2 * s], t.w[n].f[2 * s + 1]);
+                        for (int s = 0; s < 4; ++s) {
+                            const float xa[4] = {t.x[0].f[2 * s], t.x[1].f[2 * s], t.x[0].f[2 * s + 1], t.x[1].f[2 * s + 1]};
+                            mma_pieces<XW ? 2 : 1, WW ? 2 : 1>(sum, xa, t.w[n].f[2 * s], t.w[n].f[2 * s + 1]);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) acc[n][i] += sum[i];
                     }
                 } else {
 #pragma unroll
@@ -612,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, TYPE == kTf32 ? 1 : 2) expand_kernel
     moe::wait_for_previous();
     list_adapters(l, a, t0, kTallRows);
     // rows without an adapter
-    for (int i = 0; i < kTallRows && t0 + i < a.T; ++i) {
+    for (int i = 0; blockIdx.z == 0 && i < kTallRows && t0 + i < a.T; ++i) {
         const bool bad = l.ids[i] >= a.n_adapters;
         if (l.ids[i] >= 0 && !bad) continue;
         if (bad && tid == 0 && blockIdx.y == 0) record_error(a.err, kErrBadIndex);
@@ -622,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, TYPE == kTf32 ? 1 : 2) expand_kernel
                                bad ? __int_as_float(0x7fc00000) : load_as_float(a.y, (t0 + i) * a.ldy + n, a.y_type));
     }
     const int m = warp & 1;                                  // the warp's 16 rows, and every fourth 16 columns
-    for (int j = 0; j < l.n; ++j) {
+    for (int j = blockIdx.z; j < l.n; j += gridDim.z) {
         const int id = l.list[j];
         const int64_t b_row = static_cast<int64_t>(id) * a.N, row0 = t0 + m * 16 + g;
         const bool in[2] = {l.ids[m * 16 + g] == id, l.ids[m * 16 + 8 + g] == id};
@@ -799,19 +804,20 @@ __device__ __forceinline__ uint4 lora_lds(uint32_t p)
 // operands come through a ring of its own, two turns ahead.
 constexpr int kTurns = 3;                                    // of a warp on their way or at work
 
-template <int NR>
-__host__ __device__ constexpr int shrink_turn_bytes() { return (kTallRows + 8 * NR) * 64; }
+__host__ __device__ constexpr int shrink_turn_bytes(int NR, bool XW) { return kTallRows * (XW ? 128 : 64) + 8 * NR * 64; }
 
-template <int NR, int TYPE>
+// TYPE: that of x and A; kTf32 where x is fp32 (XW) or the other 16-bit type.
+template <int NR, int TYPE, bool XW>
 __global__ void __launch_bounds__(kThreads, 1) shrink16_kernel(const LoraArgs a)
 {
-    constexpr int R8 = 8 * NR, TURN = shrink_turn_bytes<NR>();
+    constexpr int R8 = 8 * NR, XP = XW ? 128 : 64, XC = XP / 16, TURN = shrink_turn_bytes(NR, XW);
     extern __shared__ __align__(16) uint8_t ring[];
     __shared__ TileList l;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
     const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTallRows;
     const uint32_t mine = smem_u32(ring) + warp * kTurns * TURN;
     float *parts = reinterpret_cast<float *>(ring);          // afterwards: [warp][row][R8 + 4]
+    const bool x_half = a.x_type == QK_F16, w_half = a.w_type == QK_F16;
     const int width = (a.rank + R8 - 1) / R8 * R8;
     moe::let_next_start();
     moe::wait_for_previous();
@@ -819,28 +825,41 @@ __global__ void __launch_bounds__(kThreads, 1) shrink16_kernel(const LoraArgs a)
     for (int j = blockIdx.y; j < l.n; j += gridDim.y) {
         const int id = l.list[j];
         const float scale = a.scales ? a.scales[id] : 1.0f;
-        // a lane copies 16 bytes of every eighth row
-        unsigned rows = 0;
+        // a lane copies 16 bytes of every eighth row of A, and of every (32 / XC)th of x; and reads every eighth
+        const int x_row = lane / XC, x_ch = lane % XC;
+        unsigned rows = 0, copied = 0;
 #pragma unroll
         for (int i = 0; i < kTallRows / 8; ++i) rows |= (l.ids[8 * i + g] == id) << i;
-        const uint16_t *x0 = static_cast<const uint16_t *>(a.x) + (t0 + g) * a.ldx + 8 * c;
+#pragma unroll
+        for (int i = 0; i < XC; ++i) copied |= (l.ids[i * (32 / XC) + x_row] == id) << i;
+        const char *x0 = static_cast<const char *>(a.x) + (t0 + x_row) * a.ldx * (XW ? 4 : 2) + 16 * x_ch;
+        // (of fp32, the 16-byte pieces of odd rows lie exchanged: no bank conflicts when two rows are read at once)
+        const uint32_t x_to = x_row * XP + 16 * (XW ? x_ch ^ (x_row & 1) : x_ch);
         for (int rb = 0; rb * R8 < a.rank; ++rb) {
             const uint16_t *w0 = static_cast<const uint16_t *>(a.A) + (static_cast<int64_t>(id) * a.rank + rb * R8 + g) * a.K + 8 * c;
             const int tiles = min(NR, (a.rank - rb * R8) / 8);
-            const int64_t x_step = 8 * a.ldx, w_step = 8LL * a.K;
+            const int64_t x_step = (32 / XC) * a.ldx * (XW ? 4 : 2), w_step = 8LL * a.K;
             const auto fetch = [&](int k, int slot) {
-                uint32_t to = mine + slot * TURN + g * 64 + 16 * c;
-                if (k < a.K && k + 8 * c >= a.K) {
+                if (k < a.K) {
                     // past the rows' end: zeros
+                    uint32_t to = mine + slot * TURN + x_to;
+                    if (k + x_ch * (XW ? 4 : 8) < a.K) {
+                        const char *q = x0 + static_cast<int64_t>(k) * (XW ? 4 : 2);
 #pragma unroll
-                    for (int i = 0; i < kTallRows / 8 + NR; ++i) asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(to + i * 512), "r"(0) : "memory");
-                } else if (k < a.K) {
-                    const uint16_t *q = x0 + k;
+                        for (int i = 0; i < XC; ++i, q += x_step) lora_copy16(to + i * 512, q, (copied >> i) & 1u);
+                    } else {
 #pragma unroll
-                    for (int i = 0; i < kTallRows / 8; ++i, q += x_step) lora_copy16(to + i * 512, q, (rows >> i) & 1u);
-                    to += kTallRows * 64, q = w0 + k;
+                        for (int i = 0; i < XC; ++i) asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(to + i * 512), "r"(0) : "memory");
+                    }
+                    to = mine + slot * TURN + kTallRows * XP + g * 64 + 16 * c;
+                    if (k + 8 * c < a.K) {
+                        const uint16_t *q = w0 + k;
 #pragma unroll
-                    for (int i = 0; i < NR; ++i, q += w_step) lora_copy16(to + i * 512, q, i < tiles);
+                        for (int i = 0; i < NR; ++i, q += w_step) lora_copy16(to + i * 512, q, i < tiles);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < NR; ++i) asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(to + i * 512), "r"(0) : "memory");
+                    }
                 }
                 asm volatile("cp.async.commit_group;" ::: "memory");
             };
@@ -860,26 +879,68 @@ __global__ void __launch_bounds__(kThreads, 1) shrink16_kernel(const LoraArgs a)
                 asm volatile("cp.async.wait_group %0;" ::"n"(kTurns - 2) : "memory");
                 __syncwarp();                                // this turn has landed, and the slot before it is free
                 fetch(k + (kTurns - 1) * kTurn, slot == 0 ? kTurns - 1 : slot - 1);
-                const uint32_t at = mine + slot * TURN + g * 64 + 16 * c;
+                const uint32_t at = mine + slot * TURN;
                 // (rows of other tokens hold what they held; ranks past the last are dropped below)
-                uint4 x[2][2], w[NR];
+                uint4 x[2][2][XW ? 2 : 1], w[NR];
 #pragma unroll
                 for (int m = 0; m < 2; ++m)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        x[m][h] = lora_lds(at + (2 * m + h) * 512);
-                        if (!((rows >> (2 * m + h)) & 1u)) x[m][h] = zero;
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int q = 0; q < (XW ? 2 : 1); ++q) {
+                            x[m][h][q] = lora_lds(at + (16 * m + 8 * h + g) * XP + 16 * (XW ? (2 * c + q) ^ (g & 1) : c));
+                            if (!((rows >> (2 * m + h)) & 1u)) x[m][h][q] = zero;
+                        }
+#pragma unroll
+                for (int n = 0; n < NR; ++n) w[n] = lora_lds(at + kTallRows * XP + n * 512 + g * 64 + 16 * c);
+                if constexpr (TYPE != kTf32) {
+#pragma unroll
+                    for (int n = 0; n < NR; ++n)
+#pragma unroll
+                        for (int m = 0; m < 2; ++m) {
+                            const uint4 p = x[m][0][0], q = x[m][1][0];
+                            mma16<TYPE>(acc[m][n], p.x, q.x, p.y, q.y, w[n].x, w[n].y);
+                        }
+#pragma unroll
+                    for (int n = 0; n < NR; ++n)
+#pragma unroll
+                        for (int m = 0; m < 2; ++m) {
+                            const uint4 p = x[m][0][0], q = x[m][1][0];
+                            mma16<TYPE>(acc[m][n], p.z, q.z, p.w, q.w, w[n].z, w[n].w);
+                        }
+                } else {
+                    // (summed apart by turns, as above)
+                    float2 v[4][2][2];                       // a lane's columns 2s and 2s + 1
+#pragma unroll
+                    for (int s = 0; s < 4; ++s)
+#pragma unroll
+                        for (int m = 0; m < 2; ++m)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const uint4 p = x[m][h][XW ? s / 2 : 0];
+                                if constexpr (XW)
+                                    v[s][m][h] = s % 2 ? make_float2(__uint_as_float(p.z), __uint_as_float(p.w)) : make_float2(__uint_as_float(p.x), __uint_as_float(p.y));
+                                else
+                                    v[s][m][h] = unpack16(s == 0 ? p.x : s == 1 ? p.y : s == 2 ? p.z : p.w, x_half);
+                            }
+#pragma unroll
+                    for (int n = 0; n < NR; ++n) {
+                        float sum[2][4] = {};
+#pragma unroll
+                        for (int s = 0; s < 4; ++s) {
+                            const float2 b = unpack16(s == 0 ? w[n].x : s == 1 ? w[n].y : s == 2 ? w[n].z : w[n].w, w_half);
+#pragma unroll
+                            for (int m = 0; m < 2; ++m) {
+                                const float p[4] = {v[s][m][0].x, v[s][m][1].x, v[s][m][0].y, v[s][m][1].y};
+                                mma_pieces<XW ? 2 : 1, 1>(sum[m], p, b.x, b.y);
+                            }
+                        }
+#pragma unroll
+                        for (int m = 0; m < 2; ++m)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) acc[m][n][i] += sum[m][i];
                     }
-#pragma unroll
-                for (int n = 0; n < NR; ++n) w[n] = lora_lds(at + kTallRows * 64 + n * 512);
-#pragma unroll
-                for (int n = 0; n < NR; ++n)
-#pragma unroll
-                    for (int m = 0; m < 2; ++m) mma16<TYPE>(acc[m][n], x[m][0].x, x[m][1].x, x[m][0].y, x[m][1].y, w[n].x, w[n].y);
-#pragma unroll
-                for (int n = 0; n < NR; ++n)
-#pragma unroll
-                    for (int m = 0; m < 2; ++m) mma16<TYPE>(acc[m][n], x[m][0].z, x[m][1].z, x[m][0].w, x[m][1].w, w[n].z, w[n].w);
+                }
                 slot = slot + 1 == kTurns ? 0 : slot + 1;
             }
             asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -1098,56 +1159,73 @@ __global__ void __launch_bounds__(kThreads, 1) expand16_kernel(const LoraArgs a)
     }
 }
 
-template <int NR, int TYPE, int PIECES, bool YW>
-cudaError_t launch_tall16(const LoraArgs &a, int sms, cudaStream_t st)
+// 16-bit adapters in whole vectors, ranks of one pass.
+bool ring_ok(const LoraArgs &a)
 {
-    constexpr int sums = static_cast<int>(sizeof(float)) * kWarps * kTallRows * (8 * NR + 4), turns = kWarps * kTurns * shrink_turn_bytes<NR>();
-    constexpr int smem = sums > turns ? sums : turns, ring = kWarps * kTurns * expand_turn_bytes(NR, YW ? 4 : 2);
-    cudaError_t e = cudaFuncSetAttribute(shrink16_kernel<NR, TYPE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(expand16_kernel<NR, TYPE, PIECES, YW>, cudaFuncAttributeMaxDynamicSharedMemorySize, ring);
+    return a.w_type != QK_F32 && a.vec_x && a.vec_a && a.vec_b && a.vec_y && a.N % 8 == 0 && a.rank <= kBlockRank;
+}
+
+// A tile's adapters are shared out over blocks, at least two: with one, a tile at the border of two requests takes twice
+// as long as the others, and the launch with it (4096 tokens of 7 requests: 35 and 55 us).
+unsigned share_of(const LoraArgs &a, unsigned tiles, int sms)
+{
+    return std::min(static_cast<unsigned>(std::min<int64_t>(kTallRows, a.n_adapters)), std::max(2u, 4u * sms / tiles));
+}
+
+// TYPE: of the adapters.
+template <int NR, int TYPE, int PIECES, bool YW>
+cudaError_t launch_ring(const LoraArgs &a, int sms, cudaStream_t st)
+{
+    const bool wide = a.x_type == QK_F32;
+    const auto shrink = a.x_type == a.w_type ? shrink16_kernel<NR, TYPE, false> : wide ? shrink16_kernel<NR, kTf32, true> : shrink16_kernel<NR, kTf32, false>;
+    const auto expand = expand16_kernel<NR, TYPE, PIECES, YW>;
+    constexpr int sums = static_cast<int>(sizeof(float)) * kWarps * kTallRows * (8 * NR + 4);
+    const int smem = std::max(sums, kWarps * kTurns * shrink_turn_bytes(NR, wide)), ring = kWarps * kTurns * expand_turn_bytes(NR, YW ? 4 : 2);
+    cudaError_t e = cudaFuncSetAttribute(shrink, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(expand, cudaFuncAttributeMaxDynamicSharedMemorySize, ring);
     if (e != cudaSuccess) return e;
-    const unsigned tiles = static_cast<unsigned>((a.T + kTallRows - 1) / kTallRows);
-    // A tile's adapters are shared out over blocks, at least two: with one, a tile at the border of two requests takes
-    // twice as long as the others, and the launch with it (4096 tokens of 7 requests: 35 and 55 us).
-    const unsigned most = static_cast<unsigned>(std::min<int64_t>(kTallRows, a.n_adapters));
-    const unsigned share = std::min(most, std::max(2u, 4u * sms / tiles));
-    e = moe::launch_chained(shrink16_kernel<NR, TYPE>, dim3(tiles, share), kThreads, smem, st, library_programmatic(), a);
+    const unsigned tiles = static_cast<unsigned>((a.T + kTallRows - 1) / kTallRows), share = share_of(a, tiles, sms);
+    e = moe::launch_chained(shrink, dim3(tiles, share), kThreads, smem, st, library_programmatic(), a);
     if (e != cudaSuccess) return e;
     // columns are cut where tiles do not fill the GPU, down to a turn a warp
     const unsigned cuts = static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>((a.N + 32 * kWarps - 1) / (32 * kWarps), sms / tiles)));
-    return moe::launch_chained(expand16_kernel<NR, TYPE, PIECES, YW>, dim3(tiles, cuts, share), kThreads, ring, st, true, a);
+    return moe::launch_chained(expand, dim3(tiles, cuts, share), kThreads, ring, st, true, a);
 }
 
-template <int NR, int TYPE, int PIECES, bool XW, bool WW>
+// SHRINK, EXPAND: the launches' types.
+template <int NR, int SHRINK, int EXPAND, int PIECES, bool XW, bool WW>
 cudaError_t launch_tall_as(const LoraArgs &a, int sms, cudaStream_t st)
 {
     constexpr int R8 = 8 * NR;
     const int smem = static_cast<int>(sizeof(float)) * kWarps * kShrinkRows * (R8 + 4);
-    const auto shrink = shrink_kernel<NR, TYPE, XW, WW>;
+    const auto shrink = shrink_kernel<NR, SHRINK, XW, WW>;
     cudaError_t e = cudaFuncSetAttribute(shrink, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const unsigned tiles = static_cast<unsigned>((a.T + kTallRows - 1) / kTallRows);
-    e = moe::launch_chained(shrink, dim3(static_cast<unsigned>((a.T + kShrinkRows - 1) / kShrinkRows)), kThreads, smem, st, library_programmatic(), a);
+    const unsigned share = share_of(a, tiles, sms);
+    e = moe::launch_chained(shrink, dim3(static_cast<unsigned>((a.T + kShrinkRows - 1) / kShrinkRows), share), kThreads, smem, st, library_programmatic(), a);
     if (e != cudaSuccess) return e;
     // columns are cut so that the two blocks an SM holds have work, a few turns each
     const unsigned cuts = static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>((a.N + 127) / 128, 4LL * sms / tiles)));
-    return moe::launch_chained(expand_kernel<NR, TYPE, PIECES, WW>, dim3(tiles, cuts), kThreads, 0, st, true, a);
+    return moe::launch_chained(expand_kernel<NR, EXPAND, PIECES, WW>, dim3(tiles, cuts, share), kThreads, 0, st, true, a);
+}
+
+template <int NR, int TYPE, int PIECES, bool YW>
+cudaError_t launch_w16(const LoraArgs &a, int sms, cudaStream_t st)
+{
+    if (ring_ok(a)) return launch_ring<NR, TYPE, PIECES, YW>(a, sms, st);
+    if (a.x_type == a.w_type) return launch_tall_as<NR, TYPE, TYPE, PIECES, false, false>(a, sms, st);
+    return a.x_type == QK_F32 ? launch_tall_as<NR, kTf32, TYPE, PIECES, true, false>(a, sms, st)
+                              : launch_tall_as<NR, kTf32, TYPE, PIECES, false, false>(a, sms, st);
 }
 
 template <int NR>
 cudaError_t launch_tall_types(const LoraArgs &a, int sms, cudaStream_t st)
 {
-    if (a.x_type == a.w_type && a.x_type != QK_F32 && a.vec_x && a.vec_a && a.vec_b && a.vec_y && a.N % 8 == 0 && a.rank <= 8 * NR) {
-        const bool wide = a.y_type == QK_F32;
-        if (a.x_type == QK_F16) return wide ? launch_tall16<NR, kF16, 2, true>(a, sms, st) : launch_tall16<NR, kF16, 2, false>(a, sms, st);
-        return wide ? launch_tall16<NR, kBf16, 3, true>(a, sms, st) : launch_tall16<NR, kBf16, 2, false>(a, sms, st);
-    }
-    if (a.x_type == QK_BF16 && a.w_type == QK_BF16)
-        return a.y_type == QK_F32 ? launch_tall_as<NR, kBf16, 3, false, false>(a, sms, st) : launch_tall_as<NR, kBf16, 2, false, false>(a, sms, st);
-    if (a.x_type == QK_F16 && a.w_type == QK_F16) return launch_tall_as<NR, kF16, 2, false, false>(a, sms, st);
-    if (a.x_type == QK_F32)
-        return a.w_type == QK_F32 ? launch_tall_as<NR, kTf32, 2, true, true>(a, sms, st) : launch_tall_as<NR, kTf32, 2, true, false>(a, sms, st);
-    return a.w_type == QK_F32 ? launch_tall_as<NR, kTf32, 2, false, true>(a, sms, st) : launch_tall_as<NR, kTf32, 2, false, false>(a, sms, st);
+    // 16-bit adapters: the same products in the same order by rings or through registers, so that bits depend on no alignment
+    if (a.w_type == QK_F16) return a.y_type == QK_F32 ? launch_w16<NR, kF16, 2, true>(a, sms, st) : launch_w16<NR, kF16, 2, false>(a, sms, st);
+    if (a.w_type == QK_BF16) return a.y_type == QK_F32 ? launch_w16<NR, kBf16, 3, true>(a, sms, st) : launch_w16<NR, kBf16, 2, false>(a, sms, st);
+    return a.x_type == QK_F32 ? launch_tall_as<NR, kTf32, kTf32, 2, true, true>(a, sms, st) : launch_tall_as<NR, kTf32, kTf32, 2, false, true>(a, sms, st);
 }
 
 int tall_blocks(int rank) { return rank <= 16 ? 2 : rank <= 32 ? 4 : 8; }      // 8-rank tiles of a pass
@@ -1188,8 +1266,15 @@ int size_of(int t) { return t == QK_F32 ? 4 : 2; }
 using namespace qk;
 
 namespace {
-// Tokens from which the two-launch form takes a call that has a workspace.
-constexpr int64_t kTallFrom = 256;
+// Which calls with a workspace take the two-launch form.  K = N = 4096, 16-bit operands of rank 16: one token 16.5 us and
+// 20.6 in one launch, 64 tokens of 48 adapters 25.7 and 34.9; with fp32 activations 21.7 and 18.6, 37.0 and 34.9, but of
+// rank 64 62.6 and 123 (4 adapters: 42 and 33).  Adapters in fp32 and ranks past one pass: many tokens only.
+bool two_launches(int64_t T, int rank, int x_type, int w_type)
+{
+    if (T >= 256) return true;
+    if (w_type == QK_F32 || rank > kBlockRank) return false;
+    return x_type != QK_F32 || (T >= 16 && rank > 32);
+}
 size_t lora_bytes(int64_t T, int rank)
 {
     const int r8 = 8 * tall_blocks(rank);
@@ -1199,7 +1284,7 @@ size_t lora_bytes(int64_t T, int rank)
 
 extern "C" size_t qk_lora_workspace_bytes(int64_t T, int rank)
 {
-    return T < kTallFrom || T > (1 << 26) || rank <= 0 || rank > kMaxRank ? 0 : lora_bytes(T, rank);
+    return T <= 0 || T > (1 << 26) || rank <= 0 || rank > kMaxRank ? 0 : lora_bytes(T, rank);
 }
 
 extern "C" int qk_lora(const void *x, int64_t ldx, int x_type, int64_t T, int64_t K, const void *A, const void *B, int w_type,
@@ -1234,7 +1319,7 @@ extern "C" int qk_lora(const void *x, int64_t ldx, int x_type, int64_t T, int64_
     if (!a.err || !device_limits(&sms, &smem)) return QK_ERR_CUDA;
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (workspace && !multiple(workspace, 256)) return QK_ERR_WORKSPACE;
-    if (T >= kTallFrom && workspace && workspace_bytes >= lora_bytes(T, rank)) {
+    if (two_launches(T, rank, x_type, w_type) && workspace && workspace_bytes >= lora_bytes(T, rank)) {
         a.V = static_cast<float *>(workspace);
         return launch_tall(a, sms, st) == cudaSuccess ? QK_OK : QK_ERR_CUDA;
     }

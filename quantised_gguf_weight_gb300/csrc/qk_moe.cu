@@ -471,7 +471,7 @@ int qk_moe_ffn(const qk_expert_weights *gate, const qk_expert_weights *up, const
     pa.ids = ids, pa.n = static_cast<int>(l.A), pa.experts = static_cast<int>(n_experts), pa.err = err;
     // 8 thread blocks where one would go over its ids more than four times (32768 ids: 82 us in one, see the kernel)
     constexpr int kWarps = kPlanThreads / 32;
-    const int plan_blocks = l.A > 4 * 32 * kWarps ? 8 : 1;
+    const int plan_blocks = l.A > 32 * kWarps ? 8 : 1;
     pa.per_warp = static_cast<int>((l.A + 32LL * kWarps * plan_blocks - 1) / (32LL * kWarps * plan_blocks) * 32);
     pa.plan = {reinterpret_cast<int *>(ws + l.head), reinterpret_cast<int *>(ws + l.assignment),
                reinterpret_cast<int *>(ws + l.place), reinterpret_cast<int *>(ws + l.column),

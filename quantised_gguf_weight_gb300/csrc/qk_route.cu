@@ -150,8 +150,27 @@ __device__ __forceinline__ bool choose(const RouteArgs &a, const float (&z)[V], 
         const int e = lane * V + v;
         key[v] = e < a.E && (a.groups == 1 || (kept >> (e / each)) & 1u) ? key_of(c[v]) : Key(0);
     }
+    if (by_logits) {
+        // the key is the logit
+        for (int j = 0; j < a.top_k; ++j) {
+            Key best = key[0];
+#pragma unroll
+            for (int v = 1; v < V; ++v) best = key[v] > best ? key[v] : best;
+            const Key top = warp_max(best);
+            const int winner = __ffs(__ballot_sync(~0u, best == top)) - 1;
+            int at = V - 1;
+#pragma unroll
+            for (int v = V - 2; v >= 0; --v) at = key[v] == top ? v : at;
+            const int e = __shfl_sync(~0u, lane * V + at, winner);
+            if (lane == j) index = e, logit = static_cast<float>(value_of(top));
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (lane * V + v == e) key[v] = 0;
+        }
+        return true;
+    }
     // one more than top_k, where there is one, shows whether the last is apart from what follows
-    const int rounds = kWide || by_logits || a.top_k >= (a.groups > 1 ? a.top_groups * each : a.E) ? a.top_k : a.top_k + 1;
+    const int rounds = kWide || a.top_k >= (a.groups > 1 ? a.top_groups * each : a.E) ? a.top_k : a.top_k + 1;
     R last_c = 0, last_err = 0;
     float last_z = 0, last_b = 0;
     for (int j = 0; j < rounds; ++j) {
@@ -173,7 +192,7 @@ __device__ __forceinline__ bool choose(const RouteArgs &a, const float (&z)[V], 
         const int e = __shfl_sync(~0u, lane * V + at, winner);
         zw = __shfl_sync(~0u, zw, winner);
         if (lane == j && j < a.top_k) index = e, logit = zw;
-        if (!kWide && !by_logits) {
+        if (!kWide) {
             ew = __shfl_sync(~0u, ew, winner);
             const R cw = value_of(top);
             if (j > 0 && !(last_c - cw > last_err + ew)) {

@@ -99,7 +99,7 @@ def test_lora_statuses(qk):
     assert call(x_type=3) == 10 and call(w_type=-1) == 10 and call(y_type=7) == 10
     assert call(T=0, x=None) == 0
     f = qk.load().qk_lora_workspace_bytes
-    assert f(0, 8) == f(1, 8) == f(4096, 0) == f(4096, 257) == 0 and f(4096, 64) == 4096 * 64 * 4 and f(4096, 65) == 4096 * 128 * 4
+    assert f(0, 8) == f(4096, 0) == f(4096, 257) == 0 and f(4096, 64) == 4096 * 64 * 4 and f(4096, 65) == 4096 * 128 * 4 and f(1, 8) == 64
 
 
 def test_binding_refuses_host_tensors(qk):
