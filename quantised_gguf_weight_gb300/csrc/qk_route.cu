@@ -152,6 +152,25 @@ __device__ __forceinline__ bool choose(const RouteArgs &a, const float (&z)[V], 
     }
     if (by_logits) {
         // the key is the logit
+        if (!kWide && a.type != QK_F32) {
+            // 16-bit logits have 19 bits of key at most: the index goes with them, lower ones first
+            uint32_t both[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) both[v] = key[v] ? (static_cast<uint32_t>(key[v]) >> 13 << 11) + (kMaxExperts - (lane * V + v)) : 0u;
+            for (int j = 0; j < a.top_k; ++j) {
+                uint32_t best = both[0];
+#pragma unroll
+                for (int v = 1; v < V; ++v) best = max(best, both[v]);
+                const uint32_t top = __reduce_max_sync(~0u, best);
+                if (lane == j) {
+                    const uint32_t k = top >> 11 << 13;
+                    index = kMaxExperts - (top & 2047u), logit = __uint_as_float(k >> 31 ? k & 0x7fffffffu : ~(k | 0x1fffu));
+                }
+#pragma unroll
+                for (int v = 0; v < V; ++v) both[v] = both[v] == top ? 0u : both[v];
+            }
+            return true;
+        }
         for (int j = 0; j < a.top_k; ++j) {
             Key best = key[0];
 #pragma unroll
