@@ -187,6 +187,15 @@ __global__ void __launch_bounds__(kPackThreads) pack_kernel(const PackArgs a)
     const int64_t r = static_cast<int64_t>(blockIdx.x) * (kPackThreads / kThreads) + threadIdx.x / kThreads;
     if (r >= (a.top_k ? a.tokens : a.plan.head[2])) return;         // (whole rows: all of a block's threads, or of a warp)
     const int64_t row = r * a.ld;
+    // where blocks are few, one a place of the token's; a lane looks up one of up to 32 at once
+    const int lane = threadIdx.x & 31;
+    const int first = gridDim.y > 1 ? blockIdx.y : 0, places = gridDim.y > 1 ? first + 1 : a.top_k ? a.top_k : 1;
+    int p = -1, column = 0;
+    const auto look = [&](int j) {
+        p = j >= places ? -1 : a.top_k ? a.plan.place[r * a.top_k + j] : static_cast<int>(r);
+        column = p >= 0 ? a.plan.column[p] : 0;
+    };
+    look(first + lane);
     uint32_t most = 0;          // magnitudes order as their bits do
 #pragma unroll 4
     for (int k = tid * 4; k < a.cols; k += kThreads * 4) {
@@ -207,77 +216,78 @@ __global__ void __launch_bounds__(kPackThreads) pack_kernel(const PackArgs a)
     const float up = __uint_as_float(static_cast<uint32_t>(127 + 141 - ex) << 23);
     const float back = __uint_as_float(static_cast<uint32_t>(127 - 141 + ex) << 23);
     const int64_t unit = octet_unit_bytes(a.fmt, a.pieces);
-    // where blocks are few, one a place of the token's
-    const int first = gridDim.y > 1 ? blockIdx.y : 0, places = gridDim.y > 1 ? first + 1 : a.top_k ? a.top_k : 1;
-    bool tiled = false;
-    for (int j = first; j < places; ++j) {
-        const int p = a.top_k ? a.plan.place[r * a.top_k + j] : static_cast<int>(r);
-        if (p < 0) continue;
-        if (tid == 0) a.scale[p] = back;
-        const int column = a.plan.column[p];
-        if (column < 0) {
-            tiled = true;
-            continue;
-        }
-        // thread (unit, c, i) makes the 16 bytes that lane (column, c) of step i reads
-        uint8_t *out = a.out + (column >> 3) * unit * a.units;
-        const int col = column & 7;
-        for (int q = tid; q < a.units * 32; q += kThreads) {
-            const int u = q >> 5, c = (q >> 3) & 3, i = q & 7;
-            const int k = u * kUnit;
-            int k0, k1;
-            if (a.fmt == kFmtQ4K) k0 = k + 64 * c + 4 * i, k1 = k0 + 32;                     // sub-blocks 2c and 2c + 1
-            else if (a.fmt == kFmtQ80) k0 = k + 32 * i + 8 * c, k1 = k0 + 4;                 // block i
-            else k0 = k + 128 * (i >> 2) + 64 * (i & 1) + 16 * ((i >> 1) & 1) + 4 * c, k1 = k0 + 32;    // sub-blocks t, t + 1
-            float4 v0 = four(a.x, row, k0, a.cols, a.type, a.vec), v1 = four(a.x, row, k1, a.cols, a.type, a.vec);
-            v0.x *= up, v0.y *= up, v0.z *= up, v0.w *= up;
-            v1.x *= up, v1.y *= up, v1.z *= up, v1.w *= up;
-            uint2 h0, l0, h1, l1;
-            pieces_of(v0, h0, l0), pieces_of(v1, h1, l1);
-            uint8_t *at = out + u * unit;
-            const int lane = col * 4 + c;
-            *reinterpret_cast<uint4 *>(at + i * 512 + lane * 16) = make_uint4(h0.x, h0.y, h1.x, h1.y);
-            if (a.pieces == 2)
-                *reinterpret_cast<uint4 *>(at + kPieceBytes + i * 512 + lane * 16) = make_uint4(l0.x, l0.y, l1.x, l1.y);
-            if (a.fmt == kFmtQ4K) {
-                // sums of the values as the pieces hold them, over the 8 threads of a sub-block; 2^-5 of them in two pieces
-                const auto held = [&](uint2 h, uint2 l) {
-                    const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&h.x));
-                    const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&h.y));
-                    float s = (x.x + x.y) + (y.x + y.y);
-                    if (a.pieces == 2) {
-                        const float2 z = __half22float2(*reinterpret_cast<const __half2 *>(&l.x));
-                        const float2 w = __half22float2(*reinterpret_cast<const __half2 *>(&l.y));
-                        s += (z.x + z.y) + (w.x + w.y);
+    for (int j0 = first; j0 < places; j0 += 32) {
+        if (j0 > first) look(j0 + lane);
+        if (tid < 32 && p >= 0) a.scale[p] = back;
+        const unsigned to_rows = __ballot_sync(~0u, p >= 0 && column >= 0), to_tiles = __ballot_sync(~0u, p >= 0 && column < 0);
+        for (unsigned who = to_rows; who; who &= who - 1) {
+            const int at_column = __shfl_sync(~0u, column, __ffs(who) - 1);
+            // thread (unit, c, i) makes the 16 bytes that lane (column, c) of step i reads
+            uint8_t *out = a.out + (at_column >> 3) * unit * a.units;
+            const int col = at_column & 7;
+            for (int q = tid; q < a.units * 32; q += kThreads) {
+                const int u = q >> 5, c = (q >> 3) & 3, i = q & 7;
+                const int k = u * kUnit;
+                int k0, k1;
+                if (a.fmt == kFmtQ4K) k0 = k + 64 * c + 4 * i, k1 = k0 + 32;                     // sub-blocks 2c and 2c + 1
+                else if (a.fmt == kFmtQ80) k0 = k + 32 * i + 8 * c, k1 = k0 + 4;                 // block i
+                else k0 = k + 128 * (i >> 2) + 64 * (i & 1) + 16 * ((i >> 1) & 1) + 4 * c, k1 = k0 + 32;    // sub-blocks t, t + 1
+                float4 v0 = four(a.x, row, k0, a.cols, a.type, a.vec), v1 = four(a.x, row, k1, a.cols, a.type, a.vec);
+                v0.x *= up, v0.y *= up, v0.z *= up, v0.w *= up;
+                v1.x *= up, v1.y *= up, v1.z *= up, v1.w *= up;
+                uint2 h0, l0, h1, l1;
+                pieces_of(v0, h0, l0), pieces_of(v1, h1, l1);
+                uint8_t *at = out + u * unit;
+                const int slot = col * 4 + c;
+                *reinterpret_cast<uint4 *>(at + i * 512 + slot * 16) = make_uint4(h0.x, h0.y, h1.x, h1.y);
+                if (a.pieces == 2)
+                    *reinterpret_cast<uint4 *>(at + kPieceBytes + i * 512 + slot * 16) = make_uint4(l0.x, l0.y, l1.x, l1.y);
+                if (a.fmt == kFmtQ4K) {
+                    // sums of the values as the pieces hold them, over the 8 threads of a sub-block; 2^-5 of them in two pieces
+                    const auto held = [&](uint2 h, uint2 l) {
+                        const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&h.x));
+                        const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&h.y));
+                        float s = (x.x + x.y) + (y.x + y.y);
+                        if (a.pieces == 2) {
+                            const float2 z = __half22float2(*reinterpret_cast<const __half2 *>(&l.x));
+                            const float2 w = __half22float2(*reinterpret_cast<const __half2 *>(&l.y));
+                            s += (z.x + z.y) + (w.x + w.y);
+                        }
+                        return s;
+                    };
+                    float s0 = held(h0, l0), s1 = held(h1, l1);
+    #pragma unroll
+                    for (int d = 1; d < 8; d *= 2) s0 += __shfl_xor_sync(~0u, s0, d), s1 += __shfl_xor_sync(~0u, s1, d);
+                    s0 *= 0.03125f, s1 *= 0.03125f;
+                    if (i == 0) {
+                        const uint32_t hi = pack2h(s0, s1);
+                        const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+                        *reinterpret_cast<uint2 *>(at + a.pieces * kPieceBytes + slot * 8) =
+                            make_uint2(hi, pack2h(s0 - h.x, s1 - h.y));
                     }
-                    return s;
-                };
-                float s0 = held(h0, l0), s1 = held(h1, l1);
-#pragma unroll
-                for (int d = 1; d < 8; d *= 2) s0 += __shfl_xor_sync(~0u, s0, d), s1 += __shfl_xor_sync(~0u, s1, d);
-                s0 *= 0.03125f, s1 *= 0.03125f;
-                if (i == 0) {
-                    const uint32_t hi = pack2h(s0, s1);
-                    const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
-                    *reinterpret_cast<uint2 *>(at + a.pieces * kPieceBytes + lane * 8) =
-                        make_uint2(hi, pack2h(s0 - h.x, s1 - h.y));
                 }
             }
         }
-    }
-    if (!tiled) return;
-    // rows of tile sets, in the order in which their weights are taken apart: (0, 2, 1, 3) of every four
-    for (int k = tid * 4; k < a.tile_cols; k += kThreads * 4) {
-        float4 v = four(a.x, row, k, a.cols, a.type, a.vec);
-        v.x *= up, v.y *= up, v.z *= up, v.w *= up;
-        uint2 h, l;
-        pieces_of(v, h, l);
-        for (int j = first; j < places; ++j) {
-            const int p = a.top_k ? a.plan.place[r * a.top_k + j] : static_cast<int>(r);
-            if (p < 0 || a.plan.column[p] >= 0) continue;
-            __half *to = a.tile_out + static_cast<int64_t>(p) * a.tile_cols + k;
-            *reinterpret_cast<uint2 *>(to) = h;
-            if (a.pieces == 2) *reinterpret_cast<uint2 *>(to + a.tile_lo) = l;
+        if (!to_tiles) continue;
+        // rows of tile sets, in the order in which their weights are taken apart: (0, 2, 1, 3) of every four
+        for (int base = 0; base < a.tile_cols; base += kThreads * 8) {
+            const int k = base + tid * 8;
+            uint4 hi, lo;
+            if (k < a.tile_cols) {
+                float4 v = four(a.x, row, k, a.cols, a.type, a.vec), w = four(a.x, row, k + 4, a.cols, a.type, a.vec);
+                v.x *= up, v.y *= up, v.z *= up, v.w *= up;
+                w.x *= up, w.y *= up, w.z *= up, w.w *= up;
+                uint2 h0, l0, h1, l1;
+                pieces_of(v, h0, l0), pieces_of(w, h1, l1);
+                hi = make_uint4(h0.x, h0.y, h1.x, h1.y), lo = make_uint4(l0.x, l0.y, l1.x, l1.y);
+            }
+            for (unsigned who = to_tiles; who; who &= who - 1) {
+                __half *to = a.tile_out + static_cast<int64_t>(__shfl_sync(~0u, p, __ffs(who) - 1)) * a.tile_cols + k;
+                if (k < a.tile_cols) {
+                    *reinterpret_cast<uint4 *>(to) = hi;
+                    if (a.pieces == 2) *reinterpret_cast<uint4 *>(to + a.tile_lo) = lo;
+                }
+            }
         }
     }
 }
@@ -303,20 +313,28 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(const SumArgs a)
     if (n >= a.N) return;
     const bool vec = a.N % 4 == 0;
     float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int j = 0; j < a.top_k; ++j) {
-        const int p = a.plan.place[t * a.top_k + j];
-        if (p == -1) continue;
-        const float w = p < 0 ? __int_as_float(0x7fc00000) : a.weights[t * a.top_k + j];
-        const float *part = a.parts + static_cast<int64_t>(p < 0 ? 0 : p) * a.N + n;
-        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (p >= 0 && vec) {
-            const float4 f = *reinterpret_cast<const float4 *>(part);
-            v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
-        } else if (p >= 0) {
-            for (int i = 0; i < 4; ++i) v[i] = n + i < a.N ? part[i] : 0.0f;
+    constexpr int kAhead = 8;                   // parts on their way at once
+    for (int j0 = 0; j0 < a.top_k; j0 += kAhead) {
+        int p[kAhead];
+        float w[kAhead], v[kAhead][4];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) p[i] = j0 + i < a.top_k ? a.plan.place[t * a.top_k + j0 + i] : -1;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            w[i] = p[i] >= 0 ? a.weights[t * a.top_k + j0 + i] : p[i] == -1 ? 0.0f : __int_as_float(0x7fc00000);
+            const float *part = a.parts + static_cast<int64_t>(p[i]) * a.N + n;
+            v[i][0] = v[i][1] = v[i][2] = v[i][3] = 0.0f;
+            if (p[i] >= 0 && vec) {
+                const float4 f = *reinterpret_cast<const float4 *>(part);
+                v[i][0] = f.x, v[i][1] = f.y, v[i][2] = f.z, v[i][3] = f.w;
+            } else if (p[i] >= 0) {
+                for (int k = 0; k < 4; ++k) v[i][k] = n + k < a.N ? part[k] : 0.0f;
+            }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] += w * v[i];
+        for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) y[k] += w[i] * v[i][k];
     }
     for (int i = 0; i < 4 && n + i < a.N; ++i) store_float_as(a.y, t * a.ldy + n + i, a.type, y[i]);
 }
