@@ -46,12 +46,13 @@ def route(z, top_k, score, bias, groups, top_groups, group_top, renorm, scale):
     return ids, weights
 
 
-def ffn(x, ids, weights, gate, up, down, x_type, y_type):
+def ffn(x, ids, weights, gate, up, down, x_type, y_type, dw=None):
     """y and its bound for decoded weights gate, up [E][F][K], down [E][N][F] (f64) and rows x as the call has them.
 
     Bound: a sum of products in 32 bits is within 1e-5 of the products' magnitudes (as the GEMVs' bound), silu's slope is
     below 1.1 and its evaluation within 2e-6; h is held to 2^-22 (2^-11 with 16-bit x and y) of itself, or to 2^-39
-    (2^-26) of its row's largest; the output is rounded once."""
+    (2^-26) of its row's largest; the output is rounded once.  dw: what the weights themselves may be off by, arrays like
+    gate, up and down (rounded_weights)."""
     T, k = ids.shape
     N = down.shape[1]
     exact = x_type == "f32" or y_type == "f32"
@@ -67,12 +68,16 @@ def ffn(x, ids, weights, gate, up, down, x_type, y_type):
             dx = rel * np.abs(x[t]) + low * np.abs(x[t]).max() if exact else low * np.abs(x[t]).max() * np.ones_like(x[t])
             dg = 1e-5 * np.abs(gate[e]) @ np.abs(x[t]) + np.abs(gate[e]) @ dx
             du = 1e-5 * np.abs(up[e]) @ np.abs(x[t]) + np.abs(up[e]) @ dx
+            if dw is not None:
+                dg, du = dg + dw[0][e] @ (np.abs(x[t]) + dx), du + dw[1][e] @ (np.abs(x[t]) + dx)
             h = silu(g) * u
             dh = 1.1 * dg * np.abs(u) + (np.abs(silu(g)) + 1.1 * dg) * du + 2e-6 * np.abs(h)
             dh += rel * (np.abs(h) + dh) + low * np.abs(h).max()
             w = float(weights[t, j])
             y[t] += w * (down[e] @ h)
             bound[t] += abs(w) * (np.abs(down[e]) @ (dh + 1e-5 * np.abs(h)))
+            if dw is not None:
+                bound[t] += abs(w) * (dw[2][e] @ (np.abs(h) + dh))
     bound += 1e-6 * np.abs(y)
     return y, bound + HALF_STEP[y_type] * (np.abs(y) + bound) + SUBNORMAL[y_type] + 1e-30
 
@@ -97,6 +102,28 @@ def expert_weights(fmt, E, rows, K, seed):
     from quantised_gguf_weight_gb300 import synth
     b = synth.weights(fmt, E * rows, K, seed=seed)
     return b, orc.decode(fmt, b, K, n_rows_total=E * rows).reshape(E, rows, K)
+
+
+def rounded_weights(fmt, b, w):
+    """What weights of bytes b, decoded w [E][rows][K], may be off by where they are rounded to fp16 after a power of two
+    that puts the largest that a row's scales allow into [2^14, 2^15), as bf16 rows and outputs let them.
+
+    A rounding is 2^-11 of the value at most, or 2^-25 (half the smallest fp16), 2^-39 of the row's largest.  Q8_0: d is
+    exact, d q rounded once.  Q6_K: d sc is rounded, and its product with q: twice.  Q4_K: d and sc q are exact, the minimum
+    is rounded, and the sum: 2^-11 of |w| and of |dmin| 63.  The second order is below a 2^-10th of these."""
+    E, rows, K = w.shape
+    most = {"q8_0": 128, "q6_k": 4096, "q4_k": 945}[fmt]
+    if fmt == "q8_0":
+        d = np.abs(b.reshape(E, rows, -1, 34)[..., :2].copy().view(np.float16)[..., 0].astype(np.float64))
+        dw, largest = 2.0 ** -11 * np.abs(w), most * d.max(2)
+    elif fmt == "q6_k":
+        d = np.abs(b.reshape(E, rows, -1, 210)[..., 208:].copy().view(np.float16)[..., 0].astype(np.float64))
+        dw, largest = 2.0 ** -10 * np.abs(w), most * d.max(2)
+    else:
+        d = np.abs(b.reshape(E, rows, -1, 144)[..., :4].copy().view(np.float16).astype(np.float64))
+        m = np.repeat(63 * d[..., 1], 256, axis=2)[..., :K]
+        dw, largest = 2.0 ** -11 * (np.abs(w) + m), (most * d[..., 0] + 63 * d[..., 1]).max(2)
+    return (1 + 2.0 ** -10) * dw + 2.0 ** -38 * largest[..., None]
 
 
 def as_rows(x, dtype):
