@@ -532,8 +532,10 @@ typedef struct {
  * The experts' feed-forward products of T tokens:
  *   y[t] = sum_{j < top_k} weights[t][j] * down_e h,
  *   h = silu(gate_e x[t]) * (up_e x[t]),   e = ids[t][j],
- * gate and up [F][K] (one format), down [N][F], each expert's weights read
- * once for up to 32 of its tokens.  ids may be in any order and repeat; a
+ * gate and up [F][K] (one format), down [N][F].  An expert's weights are
+ * read once for up to 128 of its tokens (16 of them where it has fewer than
+ * 16; for each where a call has 24 assignments or fewer).  ids may be in any
+ * order and repeat; a
  * negative id adds nothing (a token with none left gets 0).  An id past the
  * last makes the token's row NaN and qk_device_error() reports
  * QK_ERR_BAD_INDEX.
@@ -543,10 +545,12 @@ typedef struct {
  *   workspace   device scratch, 256-byte aligned, of at least
  *               qk_moe_ffn_workspace_bytes() bytes; its contents need not be
  *               kept or set.  Calls that may overlap need one each.
- * Accuracy: the weights' quants and scales are exact.  With fp32 x or y every
- * activation (x, and h) is held to 2^-22 of itself or 2^-39 of its row's
- * largest; else to 2^-11 or 2^-28 (fp16's, so bf16 values are exact above
- * that).  Sums are fp32.
+ * Accuracy: with fp32 x or y every activation (x, and h) is held to 2^-22 of
+ * itself or 2^-39 of its row's largest; else to 2^-11 or 2^-28 (fp16's, so
+ * bf16 values are exact above that).  Weights are exact, or held to 2^-21
+ * where an expert has 16 tokens or more; with bf16 x and y they are then
+ * rounded to fp16, by 2^-11 of them and of what they are made of (scale times
+ * quant, and minimum).  Sums are fp32.
  * A NaN or an infinity in a row of x makes that token's y not finite, and no other's.
  * n_experts <= 1024; K, F, N <= 2^24; T * top_k <= 2^28.  T == 0 does nothing.
  */

@@ -1,11 +1,17 @@
 // qk_lora.cu -- low-rank adapters of many requests beside a shared projection:
 //   out[t] = y[t] + scale[a] * B[a] (A[a] x[t]),  a = ids[t].
 //
-// A cluster of thread blocks takes a tile of neighbouring tokens and one adapter
-// after another of those that the tile has: each block forms its columns' part
-// of V = A x (rank values a token), the blocks add the parts through distributed
-// shared memory, always in their order, and each adds its columns of B V to y.
-// So x, y and out pass once, and one launch does both products.
+// Two forms.  In one launch a cluster of thread blocks takes a tile of
+// neighbouring tokens and one adapter after another of those that the tile has:
+// each block forms its columns' part of V = A x (rank values a token), the blocks
+// add the parts through distributed shared memory, always in their order, and
+// each adds its columns of B V to y.  In two launches V lies in memory between
+// them (below); two_launches() says which calls take which.
+//
+// Few tokens are bound by latency: one token beside 4096 x 6144, rank 16, 12.3 us,
+// 64 of 48 adapters 22.5 (8 MB of adapters, 2.3 us at the memory's rate; of the
+// 512 blocks 304 are resident at once.  Clusters of 4, which all would be, took
+// 20.5, but 255 tokens of 4 adapters 58 us for 24).
 //
 // The products are m16n8k8 in tf32, which holds 16-bit adapters and activations
 // exactly; fp32 operands, and V, are two tf32 pieces (22 bits).  A lane's values
@@ -385,15 +391,22 @@ cudaError_t launch_as(const LoraArgs &a, cudaStream_t st)
 
 // ---------------------------------------------------------------- many tokens
 // Two launches with V = scale A x in memory between them.  The first: a thread
-// block has 16 tokens, its warps every eighth 32 columns of x and A, straight
-// from memory into the products' registers, two turns ahead; the warps' sums are
-// added in their order.  The second: V's rows stay in a warp's registers as the
-// products' operand while it goes over its columns of B and y, one turn ahead.
-// One adapter of the tile after another, each for its own rows.
+// block has a tile of tokens, its warps every eighth 32 columns of x and A; the
+// warps' sums are added in their order.  The second: V's rows stay in a warp's
+// registers as the products' operand while it goes over its columns of B and y.
+// A tile's adapters are shared out over blocks, each for its own rows.
 //
 // Where x and the adapters have one 16-bit type the products are m16n8k16 in it,
-// operands as they lie in memory; V is then two fp16 pieces below its row's
-// largest, or two bf16 ones (three for fp32 outputs).  Else tf32, as above.
+// operands as they lie in memory; else the first launch's are tf32, as above.
+// In the second 16-bit adapters meet V as two fp16 pieces below its row's
+// largest, or two bf16 ones (three for fp32 outputs), fp32 ones as tf32.
+//
+// The kernels here load straight into the products' registers and take any
+// alignment; the ones with rings further down do the same products in the same
+// order.  4096 bf16 tokens of 7 requests beside 4096 x 6144, rank 64: 24 and 36
+// us, 57 together, for 140 MB (21 us at the memory's rate; the tensor cores are
+// 16% and 31% busy).  A turn's copies are what both wait for: a block has 8 warps
+// at two turns of 6 KB each.
 
 constexpr int kTallRows = 32, kShrinkRows = 16;            // tokens of a block of the second, and of the first launch
 
@@ -799,7 +812,7 @@ __device__ __forceinline__ uint4 lora_lds(uint32_t p)
     return v;
 }
 
-// The same for 16-bit operands of one type in whole vectors (rows of x, A, B, y and out on 16 bytes, K, N and the rank
+// The same for 16-bit adapters, and activations of any type, in whole vectors (rows of x, A, B, y and out on 16 bytes, K, N and the rank
 // multiples of 8), which leaves every 16 bytes either inside their row or outside, and so no other path.  A warp's
 // operands come through a ring of its own, two turns ahead.
 constexpr int kTurns = 3;                                    // of a warp on their way or at work

@@ -487,7 +487,7 @@ int qk_moe_ffn(const qk_expert_weights *gate, const qk_expert_weights *up, const
 
     PlanArgs pa{};
     pa.ids = ids, pa.n = static_cast<int>(l.A), pa.experts = static_cast<int>(n_experts), pa.err = err;
-    // 8 thread blocks where one would go over its ids more than four times (32768 ids: 82 us in one, see the kernel)
+    // 8 thread blocks where one would go over its ids more than once (4096 ids: 15 us in one and 12 in 8; 32768: 82 and 16)
     constexpr int kWarps = kPlanThreads / 32;
     const int plan_blocks = l.A > 32 * kWarps ? 8 : 1;
     pa.per_warp = static_cast<int>((l.A + 32LL * kWarps * plan_blocks - 1) / (32LL * kWarps * plan_blocks) * 32);

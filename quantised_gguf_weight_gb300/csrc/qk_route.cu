@@ -11,7 +11,12 @@
 // order is exact.  Else scores are compared, first in 32 bits with a bound on
 // their error; a token in which that leaves two neighbours of the order, or a
 // group at the edge, undecided is done again in 64 bits (about 1 in 500 tokens
-// of 256 experts).  So the choice is that of the formulas, not of a rounding.
+// of 256 experts; a launch that has one takes 5 us longer).  So the choice is
+// that of the formulas, not of a rounding.
+//
+// Measured: one token 6.2 us, which is a launch; 512 tokens of 256 experts in
+// groups 8.2 or 13.0; 16384 tokens of 128 experts in bf16 12.7 us, bound by
+// instructions (0.65 a cycle and scheduler), 4.3 MB read.
 #include <cmath>
 
 #include "qk_kv4.cuh"
