@@ -196,12 +196,28 @@ __global__ void __launch_bounds__(kPackThreads) pack_kernel(const PackArgs a)
         column = p >= 0 ? a.plan.column[p] : 0;
     };
     look(first + lane);
+    // short rows stay in registers: eight neighbouring values of every 256 (kThreads of them)
+    constexpr int kHeld = WARPS == 1 ? 4 : 1;
+    const bool hold = a.cols <= kHeld * kThreads * 8;
+    float4 held[kHeld][2];
     uint32_t most = 0;          // magnitudes order as their bits do
-#pragma unroll 4
-    for (int k = tid * 4; k < a.cols; k += kThreads * 4) {
-        const float4 v = four(a.x, row, k, a.cols, a.type, a.vec);
+    const auto look_at = [&](const float4 v) {
         most = max(max(most, max(__float_as_uint(v.x) & 0x7fffffffu, __float_as_uint(v.y) & 0x7fffffffu)),
                    max(__float_as_uint(v.z) & 0x7fffffffu, __float_as_uint(v.w) & 0x7fffffffu));
+    };
+    if (hold) {
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int k = (i * kThreads + tid) * 8 + 4 * q;
+                held[i][q] = k < a.cols ? four(a.x, row, k, a.cols, a.type, a.vec) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            }
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) look_at(held[i][0]), look_at(held[i][1]);
+    } else {
+#pragma unroll 4
+        for (int k = tid * 4; k < a.cols; k += kThreads * 4) look_at(four(a.x, row, k, a.cols, a.type, a.vec));
     }
     most = __reduce_max_sync(~0u, most);
     if constexpr (WARPS > 1) {
@@ -270,23 +286,26 @@ __global__ void __launch_bounds__(kPackThreads) pack_kernel(const PackArgs a)
         }
         if (!to_tiles) continue;
         // rows of tile sets, in the order in which their weights are taken apart: (0, 2, 1, 3) of every four
-        for (int base = 0; base < a.tile_cols; base += kThreads * 8) {
-            const int k = base + tid * 8;
-            uint4 hi, lo;
-            if (k < a.tile_cols) {
-                float4 v = four(a.x, row, k, a.cols, a.type, a.vec), w = four(a.x, row, k + 4, a.cols, a.type, a.vec);
-                v.x *= up, v.y *= up, v.z *= up, v.w *= up;
-                w.x *= up, w.y *= up, w.z *= up, w.w *= up;
-                uint2 h0, l0, h1, l1;
-                pieces_of(v, h0, l0), pieces_of(w, h1, l1);
-                hi = make_uint4(h0.x, h0.y, h1.x, h1.y), lo = make_uint4(l0.x, l0.y, l1.x, l1.y);
-            }
+        const auto store = [&](int k, float4 v, float4 w) {
+            v.x *= up, v.y *= up, v.z *= up, v.w *= up;
+            w.x *= up, w.y *= up, w.z *= up, w.w *= up;
+            uint2 h0, l0, h1, l1;
+            pieces_of(v, h0, l0), pieces_of(w, h1, l1);
             for (unsigned who = to_tiles; who; who &= who - 1) {
                 __half *to = a.tile_out + static_cast<int64_t>(__shfl_sync(~0u, p, __ffs(who) - 1)) * a.tile_cols + k;
                 if (k < a.tile_cols) {
-                    *reinterpret_cast<uint4 *>(to) = hi;
-                    if (a.pieces == 2) *reinterpret_cast<uint4 *>(to + a.tile_lo) = lo;
+                    *reinterpret_cast<uint4 *>(to) = make_uint4(h0.x, h0.y, h1.x, h1.y);
+                    if (a.pieces == 2) *reinterpret_cast<uint4 *>(to + a.tile_lo) = make_uint4(l0.x, l0.y, l1.x, l1.y);
                 }
+            }
+        };
+        if (hold) {
+#pragma unroll
+            for (int i = 0; i < kHeld; ++i) store((i * kThreads + tid) * 8, held[i][0], held[i][1]);
+        } else {
+            for (int k = tid * 8; k - tid * 8 < a.tile_cols; k += kThreads * 8) {
+                const bool in = k < a.tile_cols;
+                store(k, four(a.x, row, in ? k : 0, a.cols, a.type, a.vec), four(a.x, row, in ? k + 4 : 0, a.cols, a.type, a.vec));
             }
         }
     }
