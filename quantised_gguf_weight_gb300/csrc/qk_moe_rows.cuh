@@ -26,7 +26,7 @@
 // 2048 in Q8_0: 104 us, 2.7 TB/s, and 61.  What bounds it is the way from shared
 // memory into the products: a scheduler issues 0.44 to 0.54 instructions a cycle
 // and its warps wait most for the queue of shared-memory loads (Q8_0: eight for a
-// row pair's 32 columns, of blocks of 34 bytes that no wider load fits).
+// row pair's 32 columns, in blocks of 34 bytes).
 #pragma once
 
 #include <type_traits>
