@@ -40,7 +40,7 @@ struct LoraArgs {
     int x_type, y_type, w_type, K, N, rank;
     const int32_t *ids;
     const float *scales;
-    int steps;                                 // clusters that share a tile's adapters
+    int steps, cuts;                           // clusters that share a tile's adapters, and their columns of y
     float *V;                                  // many tokens: [T][ranks, padded] of scale A x
     bool vec_x, vec_y, vec_a, vec_b;
     int *err;
@@ -157,8 +157,8 @@ __global__ void __launch_bounds__(kThreads) lora_kernel(const LoraArgs a)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
     const int rank = static_cast<int>(cluster_ctarank());
     const int64_t cluster = blockIdx.x / kCluster;
-    const int64_t t0 = cluster / a.steps * ROWS;
-    const int step = static_cast<int>(cluster % a.steps);
+    const int cut = static_cast<int>(cluster % a.cuts), step = static_cast<int>(cluster / a.cuts % a.steps);
+    const int64_t t0 = cluster / a.cuts / a.steps * ROWS;
     moe::let_next_start();
     moe::wait_for_previous();
     if (tid == 0) n_list = 0;
@@ -180,7 +180,8 @@ __global__ void __launch_bounds__(kThreads) lora_kernel(const LoraArgs a)
     const int n_adapters = n_list;
     // columns of this block: of x, and of y
     const int k_per = ((a.K + kCluster - 1) / kCluster + 31) / 32 * 32, k0 = min(a.K, rank * k_per), k1 = min(a.K, k0 + k_per);
-    const int n_per = ((a.N + kCluster - 1) / kCluster + 15) / 16 * 16, n0 = min(a.N, rank * n_per), n1 = min(a.N, n0 + n_per);
+    const int parts_n = kCluster * a.cuts, n_per = ((a.N + parts_n - 1) / parts_n + 15) / 16 * 16;
+    const int n0 = min(a.N, (cut * kCluster + rank) * n_per), n1 = min(a.N, n0 + n_per);
     const bool x_half = a.x_type == QK_F16, w_half = a.w_type == QK_F16;
 
     if (step == 0) {
@@ -378,7 +379,7 @@ cudaError_t launch_as(const LoraArgs &a, cudaStream_t st)
     if (e != cudaSuccess) return e;
     const int64_t tiles = (a.T + ROWS - 1) / ROWS;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(tiles * a.steps * kCluster)), cfg.blockDim = dim3(kThreads);
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles * a.steps * a.cuts * kCluster)), cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem, cfg.stream = st;
     cudaLaunchAttribute at[2]{};
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -1341,6 +1342,9 @@ extern "C" int qk_lora(const void *x, int64_t ldx, int x_type, int64_t T, int64_
     const int rows = tall ? 32 : 16;
     const int64_t tiles = (T + rows - 1) / rows;
     a.steps = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({rows, n_adapters, T, 4LL * sms / (kCluster * tiles)})));
+    // what is left of the GPU takes a part of the columns each, down to a turn a warp, and forms A x for itself
+    a.cuts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((a.N + 16 * kWarps * kCluster - 1) / (16 * kWarps * kCluster),
+                                                                      (rank <= 16 ? 2 : 1) * sms / (kCluster * tiles * a.steps))));
     const cudaError_t e = tall ? launch_rank<2>(a, st) : launch_rank<1>(a, st);
     return e == cudaSuccess ? QK_OK : QK_ERR_CUDA;
 }
