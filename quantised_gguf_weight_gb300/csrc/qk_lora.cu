@@ -8,8 +8,8 @@
 // each adds its columns of B V to y.  In two launches V lies in memory between
 // them (below); two_launches() says which calls take which.
 //
-// Few tokens are bound by latency: one token beside 4096 x 6144, rank 16, 12.3 us,
-// 64 of 48 adapters 22.5 (8 MB of adapters, 2.3 us at the memory's rate; of the
+// Few tokens are bound by latency: one token beside 4096 x 6144, rank 16, 8.2 us
+// (12.3 before clusters shared its columns), 64 of 48 adapters 22.5 (8 MB of adapters, 2.3 us at the memory's rate; of the
 // 512 blocks 304 are resident at once.  Clusters of 4, which all would be, took
 // 20.5, but 255 tokens of 4 adapters 58 us for 24).
 //
@@ -1280,14 +1280,15 @@ int size_of(int t) { return t == QK_F32 ? 4 : 2; }
 using namespace qk;
 
 namespace {
-// Which calls with a workspace take the two-launch form.  K = N = 4096, 16-bit operands of rank 16: one token 16.5 us and
-// 20.6 in one launch, 64 tokens of 48 adapters 25.7 and 34.9; with fp32 activations 21.7 and 18.6, 37.0 and 34.9, but of
-// rank 64 62.6 and 123 (4 adapters: 42 and 33).  Adapters in fp32 and ranks past one pass: many tokens only.
+// Which calls with a workspace take the two-launch form.  K = N = 4096, bf16 and rank 16: one token 16.5 us, 15.5 in one
+// launch; 23 of 23 adapters 19.6 and 21.7; 64 of 48 25.8 and 34; rank 64, one token 23.7 and 25.8.  With fp32 activations
+// of rank 16 64 tokens take 37.0 and 34, but of rank 64 62.6 and 123 (of 4 adapters 42 and 33).  Adapters in fp32 and
+// ranks past one pass: many tokens only.
 bool two_launches(int64_t T, int rank, int x_type, int w_type)
 {
     if (T >= 256) return true;
     if (w_type == QK_F32 || rank > kBlockRank) return false;
-    return x_type != QK_F32 || (T >= 16 && rank > 32);
+    return x_type != QK_F32 ? T > 16 || rank > 16 : T >= 16 && rank > 32;
 }
 size_t lora_bytes(int64_t T, int rank)
 {
