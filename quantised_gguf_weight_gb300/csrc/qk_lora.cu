@@ -1180,10 +1180,12 @@ bool ring_ok(const LoraArgs &a)
 }
 
 // A tile's adapters are shared out over blocks, at least two: with one, a tile at the border of two requests takes twice
-// as long as the others, and the launch with it (4096 tokens of 7 requests: 35 and 55 us).
-unsigned share_of(const LoraArgs &a, unsigned tiles, int sms)
+// as long as the others, and the launch with it (4096 tokens of 7 requests: 35 and 55 us).  But a block that finds no
+// adapter for itself costs its start, so that the launch's blocks are two rounds of the GPU at most (493 tokens of 34
+// requests, rank 64: 39 us, 52 with all 32 that a tile's tokens can have).
+unsigned share_of(const LoraArgs &a, unsigned blocks, int sms)
 {
-    return std::min(static_cast<unsigned>(std::min<int64_t>(kTallRows, a.n_adapters)), std::max(2u, 4u * sms / tiles));
+    return std::min(static_cast<unsigned>(std::min<int64_t>(kTallRows, a.n_adapters)), std::max(2u, 2u * sms / blocks));
 }
 
 // TYPE: of the adapters.
@@ -1198,12 +1200,12 @@ cudaError_t launch_ring(const LoraArgs &a, int sms, cudaStream_t st)
     cudaError_t e = cudaFuncSetAttribute(shrink, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(expand, cudaFuncAttributeMaxDynamicSharedMemorySize, ring);
     if (e != cudaSuccess) return e;
-    const unsigned tiles = static_cast<unsigned>((a.T + kTallRows - 1) / kTallRows), share = share_of(a, tiles, sms);
-    e = moe::launch_chained(shrink, dim3(tiles, share), kThreads, smem, st, library_programmatic(), a);
+    const unsigned tiles = static_cast<unsigned>((a.T + kTallRows - 1) / kTallRows);
+    e = moe::launch_chained(shrink, dim3(tiles, share_of(a, tiles, sms)), kThreads, smem, st, library_programmatic(), a);
     if (e != cudaSuccess) return e;
     // columns are cut where tiles do not fill the GPU, down to a turn a warp
     const unsigned cuts = static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>((a.N + 32 * kWarps - 1) / (32 * kWarps), sms / tiles)));
-    return moe::launch_chained(expand, dim3(tiles, cuts, share), kThreads, ring, st, true, a);
+    return moe::launch_chained(expand, dim3(tiles, cuts, share_of(a, tiles * cuts, sms)), kThreads, ring, st, true, a);
 }
 
 // SHRINK, EXPAND: the launches' types.
@@ -1216,12 +1218,12 @@ cudaError_t launch_tall_as(const LoraArgs &a, int sms, cudaStream_t st)
     cudaError_t e = cudaFuncSetAttribute(shrink, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const unsigned tiles = static_cast<unsigned>((a.T + kTallRows - 1) / kTallRows);
-    const unsigned share = share_of(a, tiles, sms);
-    e = moe::launch_chained(shrink, dim3(static_cast<unsigned>((a.T + kShrinkRows - 1) / kShrinkRows), share), kThreads, smem, st, library_programmatic(), a);
+    const unsigned halves = static_cast<unsigned>((a.T + kShrinkRows - 1) / kShrinkRows);
+    e = moe::launch_chained(shrink, dim3(halves, share_of(a, halves, sms)), kThreads, smem, st, library_programmatic(), a);
     if (e != cudaSuccess) return e;
-    // columns are cut so that the two blocks an SM holds have work, a few turns each
-    const unsigned cuts = static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>((a.N + 127) / 128, 4LL * sms / tiles)));
-    return moe::launch_chained(expand_kernel<NR, EXPAND, PIECES, WW>, dim3(tiles, cuts, share), kThreads, 0, st, true, a);
+    // columns are cut where tiles do not fill the GPU, down to two turns
+    const unsigned cuts = static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>((a.N + 127) / 128, sms / tiles)));
+    return moe::launch_chained(expand_kernel<NR, EXPAND, PIECES, WW>, dim3(tiles, cuts, share_of(a, tiles * cuts, sms)), kThreads, 0, st, true, a);
 }
 
 template <int NR, int TYPE, int PIECES, bool YW>
@@ -1281,8 +1283,8 @@ using namespace qk;
 
 namespace {
 // Which calls with a workspace take the two-launch form.  K = N = 4096, bf16 and rank 16: one token 16.5 us, 15.5 in one
-// launch; 23 of 23 adapters 19.6 and 21.7; 64 of 48 25.8 and 34; rank 64, one token 23.7 and 25.8.  With fp32 activations
-// of rank 16 64 tokens take 37.0 and 34, but of rank 64 62.6 and 123 (of 4 adapters 42 and 33).  Adapters in fp32 and
+// launch; 23 of 23 adapters 19.6 and 21.7; 64 of 48 22.7 and 34; rank 64, one token 23.7 and 25.8.  With fp32 activations
+// of rank 16 64 tokens take 37.0 and 34, but of rank 64 58.5 and 123 (of 4 adapters 45 and 33).  Adapters in fp32 and
 // ranks past one pass: many tokens only.
 bool two_launches(int64_t T, int rank, int x_type, int w_type)
 {
