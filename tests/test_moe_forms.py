@@ -198,3 +198,60 @@ def test_adapters_streams_and_graphs(qk):
             x.copy_(x.flip(0)), ids.copy_((ids + 2) % 7 - 1)
             graph.replay()
             assert torch.equal(bits(out), bits(qk.lora(x, y0, A, B, ids, scales=s)))
+
+
+def test_two_streams_at_once(qk):
+    """Calls that run beside one another, each with its workspace."""
+    sides = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for T in (2, 40, 200):
+        cs = [Case(qk, T, 8, 2, 512, 96, 64, "q4_k", "q8_0", xt, seed=i) for i, xt in enumerate(("f32", "bf16"))]
+        ls = [LoraCase(qk, T, 5, 16, 512, 96, xt, "bf16", seed=i) for i, xt in enumerate(("f32", "bf16"))]
+        want = [[bits(c.call()) for c in cs], [bits(c.call()) for c in ls]]
+        ws = [qk.moe_ffn_workspace(T, 2, 8, 512, 96, 64) for _ in sides]
+        torch.cuda.synchronize()
+        got = [([], []), ([], [])]
+        for _ in range(8):
+            for i, side in enumerate(sides):
+                got[0][i].append(cs[i].call(workspace=ws[i], stream=side)), got[1][i].append(ls[i].call(stream=side))
+        torch.cuda.synchronize()
+        for o in range(2):
+            for i in range(2):
+                assert all(torch.equal(bits(y), want[o][i]) for y in got[o][i])
+    assert qk.device_error() == 0
+
+
+def test_rows_far_apart(qk):
+    """Rows of x whose offsets pass 32 bits."""
+    T, ld = 20, (1 << 27) + 8
+    big = torch.empty(T * ld, dtype=torch.bfloat16, device="cuda")
+    for k in (1, 2):                                            # 20 assignments, and 40
+        c = Case(qk, T, 4, k, 256, 64, 48, "q4_k", "q8_0", "bf16", seed=k)
+        x = big.as_strided((T, 256), (ld, 1))
+        x.copy_(c.x)
+        assert torch.equal(bits(c.call(x=x)), bits(c.call()))
+        l = LoraCase(qk, T, 4, 8 * k * k, 256, 48, "bf16", "bf16", seed=k)
+        x.copy_(l.x)
+        assert torch.equal(bits(l.call(x=x)), bits(l.call()))
+        x = big.as_strided((T, 64), (ld, 1))
+        z = torch.randn(T, 64).bfloat16().cuda()
+        x.copy_(z)
+        assert all(torch.equal(a, b) for a, b in zip(qk.moe_route(x, 4), qk.moe_route(z, 4)))
+    assert qk.device_error() == 0
+
+
+def test_experts_behind_32_bits(qk):
+    """The last experts of a tensor of 4.6 GB, in each form."""
+    E, F, K, N, last = 1024, 2048, 2048, 32, 8
+    c = Case(qk, 30, last, 1, K, F, N, "q8_0", "q8_0", "f32", seed=1)
+    need = F * (K // 32 * 34)
+    w = torch.zeros(E * need, dtype=torch.uint8, device="cuda")
+    d = torch.zeros(E * N * (F // 32 * 34), dtype=torch.uint8, device="cuda")
+    w[-last * need:], d[-c.b["down"].w.numel():] = c.b["gate"].w.reshape(-1), c.b["down"].w.reshape(-1)
+    c.b["up"] = c.b["gate"]
+    far = [qk.ExpertWeights("q8_0", t) for t in (w, w, d)]
+    for ids in ([7], [6] * 30, [i % 8 for i in range(30)]):      # one assignment, 30 tokens an expert, four
+        x, ids = c.x[:len(ids)].cuda(), torch.tensor(ids, dtype=torch.int32).cuda()[:, None]
+        p = torch.from_numpy(c.p[:len(ids)]).cuda()
+        near = qk.moe_ffn(x, ids, p, c.b["gate"], c.b["up"], c.b["down"], last, F, N)
+        assert torch.equal(bits(qk.moe_ffn(x, ids + E - last, p, *far, E, F, N)), bits(near))
+    assert qk.device_error() == 0
