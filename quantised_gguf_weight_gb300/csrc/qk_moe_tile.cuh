@@ -600,6 +600,7 @@ tile_kernel(const __grid_constant__ TileMaps maps, const TileArgs a)
             // a warp's 64 tokens from c_first on
             const int c_first = part * 64;
             float *ts = sh.token_scale[warp - kEpiWarp];
+            __syncwarp();                                      // every lane has read the last item's
 #pragma unroll
             for (int j = lane; j < 64; j += 32) ts[j] = c_first + j < s.count ? a.scale[s.first + c_first + j] : 0.0f;
             __syncwarp();
