@@ -89,8 +89,10 @@ __device__ __forceinline__ bool choose(const RouteArgs &a, const float (&z)[V], 
     using Key = typename KeyOf<R>::type;
     constexpr bool kWide = sizeof(R) == 8;
     const bool by_logits = a.by_logits;
-    // a score's error in 32 bits: of itself, and of its sum with the bias
-    const R of_score = kWide ? R(0) : (a.sigmoid ? R(4e-7) : R(4e-6)), of_sum = kWide ? R(0) : R(1.2e-7);
+    // A score's error in 32 bits, of itself: an exponential's 2^-23, the sum 1 + e^-z and the division 2^-24 each; softmax:
+    // the argument's 2^-18 (differences of 64 to 128), sums of up to 37 terms one after the other, 2^-24 each.  Scores below
+    // the normal numbers have few bits or none.  And the error of its sum with the bias, twice the rounding's 2^-24.
+    const R of_score = a.sigmoid ? R(4e-7) : R(7e-6), of_sum = R(1.2e-7), least = R(1e-37);
     R c[V], err[V];
     R total = 0;
     if (!by_logits && !a.sigmoid) {
@@ -111,24 +113,35 @@ __device__ __forceinline__ bool choose(const RouteArgs &a, const float (&z)[V], 
             c[v] = R(z[v]);
         } else {
             c[v] = a.sigmoid ? R(1) / (R(1) + exp_of(-R(z[v]))) : (total > R(0) ? c[v] / total : R(0));
-            err[v] = c[v] * of_score;
+            if (!kWide) err[v] = c[v] * of_score + least;
             if (a.bias && e < a.E) c[v] += R(__ldg(a.bias + e));
-            err[v] += (c[v] < R(0) ? -c[v] : c[v]) * of_sum;
+            if (!kWide) err[v] = isinf(c[v]) ? R(0) : err[v] + fabsf(static_cast<float>(c[v])) * of_sum;
         }
     }
     bool open = false;
     unsigned kept = ~0u;
     if (a.groups > 1) {
+        // A group's value lies between the sum of its best lower ends and that of its best upper ends, whatever is added up
+        // in it (biases may cancel); without errors both are the value.
+        const bool bounds = !kWide && !by_logits;
+        R *errs = shared + a.E;                  // (32 bits: as many bytes as 64 bits have)
 #pragma unroll
         for (int v = 0; v < V; ++v)
-            if (lane * V + v < a.E) shared[lane * V + v] = c[v];
+            if (lane * V + v < a.E) {
+                shared[lane * V + v] = c[v];
+                if (bounds) errs[lane * V + v] = err[v];
+            }
         __syncwarp();
-        R first = -INFINITY, second = -INFINITY;
+        R first = -INFINITY, second = -INFINITY, low_first = -INFINITY, low_second = -INFINITY;
+        const auto take = [](R &best, R &next, R s) {
+            next = s > best ? best : (s > next ? s : next);
+            best = s > best ? s : best;
+        };
         if (lane < a.groups)
-            for (int i = 0; i < each; ++i) {
-                const R s = shared[lane * each + (i + lane) % each];      // lanes start apart: fewer bank conflicts
-                second = s > first ? first : (s > second ? s : second);
-                first = s > first ? s : first;
+            for (int i = 0, at = lane % each; i < each; ++i, at = at + 1 == each ? 0 : at + 1) {      // lanes start apart: fewer bank conflicts
+                const R s = shared[lane * each + at], e = bounds ? errs[lane * each + at] : R(0);
+                take(first, second, kWide ? s : s + e);
+                if (bounds) take(low_first, low_second, s - e);
             }
         __syncwarp();
         const R sum = a.group_top == 2 ? first + second : first;
@@ -140,13 +153,12 @@ __device__ __forceinline__ bool choose(const RouteArgs &a, const float (&z)[V], 
         }
         const bool keep = lane < a.groups && better < a.top_groups;
         kept = __ballot_sync(~0u, keep);
-        if (!kWide && !by_logits && a.top_groups < a.groups) {
-            // the worst that is kept and the best that is not
-            const Key low = static_cast<Key>(~warp_max(keep ? static_cast<Key>(~mine) : Key(0)));
-            const Key high = warp_max(!keep && lane < a.groups ? mine : Key(0));
-            const R gap = value_of(low) - value_of(high);
-            const R size = fabsf(static_cast<float>(value_of(low)));
-            open = !(gap > R(2) * (R(2) * of_score + of_sum * size));
+        if (bounds) {
+            // the worst that is kept and the best that is not, whose sums are rounded themselves
+            const R low = a.group_top == 2 ? low_first + low_second : low_first;
+            const R worst = value_of(static_cast<Key>(~warp_max(keep ? static_cast<Key>(~key_of(low)) : Key(0))));
+            const R best = value_of(warp_max(!keep && lane < a.groups ? mine : Key(0)));
+            open = best > R(-INFINITY) && !(worst - best > of_sum * (fabsf(static_cast<float>(worst)) + fabsf(static_cast<float>(best))));
         }
     }
     Key key[V];
