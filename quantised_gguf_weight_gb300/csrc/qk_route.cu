@@ -205,11 +205,9 @@ __device__ __forceinline__ bool choose(const RouteArgs &a, const float (&z)[V], 
         }
         return true;
     }
-    // one more than top_k, where there is one, shows whether the last is apart from what follows
-    const int rounds = kWide || a.top_k >= (a.groups > 1 ? a.top_groups * each : a.E) ? a.top_k : a.top_k + 1;
     R last_c = 0, last_err = 0;
     float last_z = 0, last_b = 0;
-    for (int j = 0; j < rounds; ++j) {
+    for (int j = 0; j < a.top_k; ++j) {
         Key best = 0;
         int at = 0;
 #pragma unroll
@@ -227,7 +225,7 @@ __device__ __forceinline__ bool choose(const RouteArgs &a, const float (&z)[V], 
             }
         const int e = __shfl_sync(~0u, lane * V + at, winner);
         zw = __shfl_sync(~0u, zw, winner);
-        if (lane == j && j < a.top_k) index = e, logit = zw;
+        if (lane == j) index = e, logit = zw;
         if (!kWide) {
             ew = __shfl_sync(~0u, ew, winner);
             const R cw = value_of(top);
@@ -240,6 +238,14 @@ __device__ __forceinline__ bool choose(const RouteArgs &a, const float (&z)[V], 
             last_c = cw, last_err = ew, last_z = zw;
             if (a.bias) last_b = __ldg(a.bias + e);
         }
+    }
+    if (!kWide) {
+        // every one that is left has to be apart from the last, not only the next: its error may be larger
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (key[v] && !(last_c - c[v] > last_err + err[v]))
+                open |= z[v] != last_z || (a.bias && __ldg(a.bias + lane * V + v) != last_b);
+        open = __any_sync(~0u, open);
     }
     return !open;
 }

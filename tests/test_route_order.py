@@ -46,6 +46,37 @@ def test_groups_whose_biases_cancel(qk, big):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_an_expert_behind_the_next_one(qk, score):
+    """The choice is undecided between the last that is chosen and one that 32 bits put two places behind it: a large score
+    that its bias takes back to the others' size, beside small ones that are exact."""
+    rng = np.random.default_rng(2)
+    rows = []
+    for _ in range(4000):
+        top = F(rng.uniform(1.5, 4))
+        z = np.array([top, -15.0, -15.015, -18, -18, -18, -18, -18], F)
+        p = sigmoid(z)
+        if score == "softmax":
+            z[1:3] += top
+            z[3] = top - F(rng.uniform(0.8, 2))          # (its bias takes it out)
+            p = np.exp(z.astype(np.float64)) / np.exp(z.astype(np.float64)).sum()
+        below = p[0] - float(F(p[0]))
+        # exact: first, by a little; in 32 bits: behind both others
+        b = -(p[0] - p[1] - 5e-9)
+        b0 = F(b)
+        c = p[0] + float(b0)
+        if below > 1e-8 and c > p[1] + 2e-9 and float(F(F(p[0]) + b0)) < p[2] - 2e-9:
+            rows.append((z, b0))
+        if len(rows) == 12:
+            break
+    assert len(rows) == 12
+    for z, b0 in rows:
+        bias = np.zeros(8)
+        bias[0], bias[3] = b0, -10
+        check(qk, z[None], 1, score, bias, renorm=False)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("low", [-np.inf, float(np.finfo(F).min), -1e4])
 def test_experts_that_a_bias_masks(qk, score, low):
     rng = np.random.default_rng(3)
