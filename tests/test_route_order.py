@@ -1,4 +1,5 @@
-"""Routing where 32 bits mislead: the choice is the formulas'.  Inputs are picked on the CPU for what 32 bits make of them."""
+"""Routing where 32 bits mislead: the choice is the formulas', and weights are within 1e-6 of themselves.  Inputs are picked on
+the CPU for what 32 bits make of them."""
 import numpy as np
 import pytest
 import torch
@@ -98,3 +99,17 @@ def test_scores_below_the_normal_numbers(qk):
     check(qk, z, 2, "sigmoid", None, 8, 2, 2)
     z[:, 0] = 0                                   # softmax: the others lie that far below
     check(qk, z, 4, "softmax", None, 8, 2, 2)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("E", [64, 512, 1024])
+def test_weights_of_logits_far_apart(qk, renorm, E):
+    """Chosen logits 20 to 80 below the largest, whose differences 32 bits round."""
+    rng = np.random.default_rng(5)
+    z = F(rng.uniform(-150, -100, (60, E)))
+    for i in range(7):
+        z[:, i] = F(10.1 + rng.random(60) - 12 * i)
+    check(qk, z, 7, "softmax", renorm=renorm)
+    check(qk, F(rng.uniform(-3, 3, (60, E))), 7, "softmax", renorm=renorm)
+    check(qk, z - 60, 7, "sigmoid", renorm=True)
