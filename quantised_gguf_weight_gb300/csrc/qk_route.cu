@@ -76,6 +76,10 @@ __device__ __forceinline__ R warp_sum(R v)
 }
 __device__ __forceinline__ float exp_of(float v) { return expf(v); }
 __device__ __forceinline__ double exp_of(double v) { return exp(v); }
+__device__ __forceinline__ float most_of(float a, float b) { return fmaxf(a, b); }
+__device__ __forceinline__ double most_of(double a, double b) { return a > b ? a : b; }
+__device__ __forceinline__ float least_of(float a, float b) { return fminf(a, b); }
+__device__ __forceinline__ double least_of(double a, double b) { return a > b ? b : a; }
 // e^(a - b) for a <= b: the difference with what its rounding leaves (an argument of 80 rounded by itself is 4e-6 of the result)
 __device__ __forceinline__ float exp_less(float a, float b)
 {
@@ -145,25 +149,31 @@ __device__ __forceinline__ bool choose(const RouteArgs &a, const float (&z)[V], 
         // A group's value lies between the sum of its best lower ends and that of its best upper ends, whatever is added up
         // in it (biases may cancel); without errors both are the value.
         const bool bounds = !kWide && !by_logits;
-        R *errs = shared + a.E;                  // (32 bits: as many bytes as 64 bits have)
+        float2 *ends = reinterpret_cast<float2 *>(shared);       // (32 bits: as many bytes as 64 bits have)
 #pragma unroll
         for (int v = 0; v < V; ++v)
             if (lane * V + v < a.E) {
-                shared[lane * V + v] = c[v];
-                if (bounds) errs[lane * V + v] = err[v];
+                if (bounds) ends[lane * V + v] = make_float2(c[v] + err[v], c[v] - err[v]);
+                else shared[lane * V + v] = c[v];
             }
         __syncwarp();
         R first = -INFINITY, second = -INFINITY, low_first = -INFINITY, low_second = -INFINITY;
         const auto take = [](R &best, R &next, R s) {
-            next = s > best ? best : (s > next ? s : next);
-            best = s > best ? s : best;
+            next = most_of(next, least_of(best, s));
+            best = most_of(best, s);
         };
-        if (lane < a.groups)
-            for (int i = 0, at = lane % each; i < each; ++i, at = at + 1 == each ? 0 : at + 1) {      // lanes start apart: fewer bank conflicts
-                const R s = shared[lane * each + at], e = bounds ? errs[lane * each + at] : R(0);
-                take(first, second, kWide ? s : s + e);
-                if (bounds) take(low_first, low_second, s - e);
+        // (lanes start apart: fewer bank conflicts)
+        int at = lane % each;
+        if (lane < a.groups && bounds) {
+#pragma unroll 2
+            for (int i = 0; i < each; ++i, at = at + 1 == each ? 0 : at + 1) {
+                const float2 s = ends[lane * each + at];
+                take(first, second, s.x), take(low_first, low_second, s.y);
             }
+        } else if (lane < a.groups) {
+#pragma unroll 2
+            for (int i = 0; i < each; ++i, at = at + 1 == each ? 0 : at + 1) take(first, second, shared[lane * each + at]);
+        }
         __syncwarp();
         const R sum = a.group_top == 2 ? first + second : first;
         const Key mine = lane < a.groups ? key_of(sum) : Key(0);
