@@ -456,7 +456,9 @@ size_t qk_moe_ffn_workspace_bytes(int64_t T, int top_k, int64_t n_experts, int64
 {
     if (T <= 0 || top_k <= 0 || n_experts <= 0 || K <= 0 || F <= 0 || N <= 0) return 0;
     if (T > INT32_MAX / top_k || K > INT32_MAX || F > INT32_MAX || N > INT32_MAX) return 0;
-    return static_cast<size_t>(layout_of(T, top_k, n_experts, K, F, N, kFmtQ4K, kFmtQ4K, QK_F32, QK_F32).bytes);
+    const auto bytes = [&](int64_t t) { return layout_of(t, top_k, n_experts, K, F, N, kFmtQ4K, kFmtQ4K, QK_F32, QK_F32).bytes; };
+    // with more ids a token than experts the most tokens that go without the many-token form can need more than a few more do
+    return static_cast<size_t>(std::max(bytes(T), bytes(std::min<int64_t>(T, kTileFrom - 1))));
 }
 
 int qk_moe_ffn(const qk_expert_weights *gate, const qk_expert_weights *up, const qk_expert_weights *down, int64_t n_experts,

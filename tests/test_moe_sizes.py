@@ -1,0 +1,16 @@
+"""Sizes of workspaces, and calls whose arguments were taken wrongly (no GPU)."""
+import random
+
+from tests.test_moe_abi import FAKE, caller, qk  # noqa: F401
+
+
+def test_a_workspace_serves_smaller_calls(qk):
+    """A buffer for some sizes is enough for every call of at most these, ids that repeat in a token among them."""
+    f = qk.load().qk_moe_ffn_workspace_bytes
+    assert f(16, 8, 1, 64, 32, 64) >= f(15, 8, 1, 64, 32, 64)
+    rng = random.Random(1)
+    for _ in range(20000):
+        big = [rng.choice([1, 3, 15, 16, 17, 24, 25, 40, 1000]), rng.choice([1, 2, 8, 25, 64]), rng.choice([1, 2, 8, 64, 1024]),
+               *(rng.choice([1, 64, 128, 129, 256, 300, 1000, 8192, 8193, 9000]) for _ in range(3))]
+        small = [v if rng.random() < 0.4 else rng.randint(1, v) for v in big]
+        assert f(*small) <= f(*big), (small, big)
