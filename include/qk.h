@@ -559,7 +559,7 @@ int qk_moe_ffn(const qk_expert_weights *gate, const qk_expert_weights *up, const
                const int32_t *ids, const float *weights, int top_k, void *y, int64_t ldy, int y_type, void *workspace,
                size_t workspace_bytes, qk_stream_t stream);
 
-/* Workspace bytes of qk_moe_ffn calls of up to these sizes, whatever the formats and types. */
+/* Workspace bytes of qk_moe_ffn calls of up to these sizes, whatever the formats and types (0: no call has them). */
 size_t qk_moe_ffn_workspace_bytes(int64_t T, int top_k, int64_t n_experts, int64_t K, int64_t F, int64_t N);
 
 /*

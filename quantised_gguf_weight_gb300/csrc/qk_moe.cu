@@ -419,6 +419,11 @@ bool type_ok(int t) { return t == QK_F32 || t == QK_F16 || t == QK_BF16; }
 bool format_ok(int f) { return f == kFmtQ80 || f == kFmtQ4K || f == kFmtQ6K; }
 int size_of(int t) { return t == QK_F32 ? 4 : 2; }
 
+bool sizes_too_large(int64_t T, int top_k, int64_t E, int64_t K, int64_t F, int64_t N)
+{
+    return E > kMaxExperts || K > (1 << 24) || F > (1 << 24) || N > (1 << 24) || T > (1 << 28) / top_k;
+}
+
 // An expert tensor's rows of `cols` columns, `rows` of each expert (a qk_status).
 int check_weights(const qk_expert_weights *w, int64_t E, int64_t rows, int64_t cols, Weights *out)
 {
@@ -455,7 +460,7 @@ int qk_debug_moe_skip_chunk(int chunk) { return g_skip_chunk.exchange(chunk); }
 size_t qk_moe_ffn_workspace_bytes(int64_t T, int top_k, int64_t n_experts, int64_t K, int64_t F, int64_t N)
 {
     if (T <= 0 || top_k <= 0 || n_experts <= 0 || K <= 0 || F <= 0 || N <= 0) return 0;
-    if (T > INT32_MAX / top_k || K > INT32_MAX || F > INT32_MAX || N > INT32_MAX) return 0;
+    if (sizes_too_large(T, top_k, n_experts, K, F, N)) return 0;
     const auto bytes = [&](int64_t t) { return layout_of(t, top_k, n_experts, K, F, N, kFmtQ4K, kFmtQ4K, QK_F32, QK_F32).bytes; };
     // with more ids a token than experts the most tokens that go without the many-token form can need more than a few more do
     return static_cast<size_t>(std::max(bytes(T), bytes(std::min<int64_t>(T, kTileFrom - 1))));
@@ -472,8 +477,7 @@ int qk_moe_ffn(const qk_expert_weights *gate, const qk_expert_weights *up, const
     if (ldx == 0) ldx = K;
     if (ldy == 0) ldy = N;
     if (ldx < K || ldy < N) return QK_ERR_BAD_DIM;
-    if (n_experts > kMaxExperts || K > (1 << 24) || F > (1 << 24) || N > (1 << 24) || T > (1 << 28) / top_k)
-        return QK_ERR_TOO_LARGE;
+    if (sizes_too_large(T, top_k, n_experts, K, F, N)) return QK_ERR_TOO_LARGE;
     Weights wg, wu, wd;
     int st = check_weights(gate, n_experts, F, K, &wg);
     if (st == QK_OK) st = check_weights(up, n_experts, F, K, &wu);

@@ -14,3 +14,13 @@ def test_a_workspace_serves_smaller_calls(qk):
                *(rng.choice([1, 64, 128, 129, 256, 300, 1000, 8192, 8193, 9000]) for _ in range(3))]
         small = [v if rng.random() < 0.4 else rng.randint(1, v) for v in big]
         assert f(*small) <= f(*big), (small, big)
+
+
+def test_workspace_sizes_that_no_call_has(qk):
+    """Sizes that a call refuses as too large have no workspace; the largest that it takes have one beyond 2^32."""
+    f = qk.load().qk_moe_ffn_workspace_bytes
+    for a in ((1 << 28, 2, 8, 256, 64, 256), (2, 2, 1025, 256, 64, 256), (2, 2, 8, (1 << 24) + 1, 64, 256),
+              (2, 2, 8, 256, (1 << 24) + 1, 256), (2, 2, 8, 256, 64, (1 << 24) + 1),
+              ((1 << 31) - 1, 1, 8, (1 << 31) - 1, (1 << 31) - 1, (1 << 31) - 1)):
+        assert f(*a) == 0, a
+    assert f(1 << 28, 1, 1024, 1 << 24, 1 << 24, 1 << 24) > 1 << 52
