@@ -572,8 +572,8 @@ size_t qk_moe_ffn_workspace_bytes(int64_t T, int top_k, int64_t n_experts, int64
  *               last makes the row NaN (QK_ERR_BAD_INDEX from qk_device_error()).
  *   scales      device fp32 [n_adapters], or NULL: 1.
  *   y, out      device rows of N elements of y_type, ldy / ldo apart (0:
- *               packed); out may be y (with the same stride) and must not
- *               overlap x.
+ *               packed); out may be y (with the same stride, if there is more
+ *               than one row) and must not overlap x.
  * Tokens of one adapter may lie anywhere; neighbouring ones share its reads.
  * Both products are fp32 sums of operands that are exact in 16 bits and held
  * to 22 bits in fp32 (and A x, in between).

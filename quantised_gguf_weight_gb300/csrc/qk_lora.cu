@@ -1314,7 +1314,7 @@ extern "C" int qk_lora(const void *x, int64_t ldx, int x_type, int64_t T, int64_
     if (ldx == 0) ldx = K;
     if (ldy == 0) ldy = N;
     if (ldo == 0) ldo = N;
-    if (ldx < K || ldy < N || ldo < N || (out && out == y && ldo != ldy)) return QK_ERR_BAD_DIM;
+    if (ldx < K || ldy < N || ldo < N || (out && out == y && T > 1 && ldo != ldy)) return QK_ERR_BAD_DIM;
     if (rank > kMaxRank || K > (1 << 24) || N > (1 << 24) || T > (1 << 26) || n_adapters > INT32_MAX) return QK_ERR_TOO_LARGE;
     if (T == 0) return QK_OK;
     if (!x || !A || !B || !ids || !y || !out) return QK_ERR_NULL;

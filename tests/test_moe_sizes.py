@@ -24,3 +24,12 @@ def test_workspace_sizes_that_no_call_has(qk):
               ((1 << 31) - 1, 1, 8, (1 << 31) - 1, (1 << 31) - 1, (1 << 31) - 1)):
         assert f(*a) == 0, a
     assert f(1 << 28, 1, 1024, 1 << 24, 1 << 24, 1 << 24) > 1 << 52
+
+
+def test_one_row_in_place_has_no_stride(qk):
+    """A single token's row may be given with any distance to the next."""
+    call = caller(qk.load().qk_lora,
+                  dict(x=FAKE, ldx=0, x_type=0, T=1, K=64, A=FAKE, B=FAKE, w_type=1, n=2, rank=8, N=64, ids=None, scales=None, y=FAKE,
+                       ldy=0, out=FAKE, ldo=80, y_type=0, ws=None, bytes=0, stream=None))
+    assert call() == 1 and call(ldo=0) == 1           # only the ids are missing
+    assert call(T=2) == 2 and call(ldo=63) == 2
