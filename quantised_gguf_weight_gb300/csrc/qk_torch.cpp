@@ -122,6 +122,13 @@ float float_of(PyObject *o)
     return static_cast<float>(v);
 }
 
+bool bool_of(PyObject *o)
+{
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) throw python_error();
+    return v != 0;
+}
+
 // None: the current stream of the current device; else a stream's handle.
 qk_stream_t stream_of(PyObject *o)
 {
@@ -170,7 +177,7 @@ PyObject *norm_rope(PyObject *, PyObject *const *a, Py_ssize_t n)
     const Table t = table_of(a[5], a[4], x.n, D, dev);
     const int status = qk_norm_rope(x.p, x.ld, x.type, nq, nk, D, vector_of<const float>(a[6], D, at::kFloat, "q_weight", dev),
                                     vector_of<const float>(a[7], D, at::kFloat, "k_weight", dev), float_of(a[8]), t.p,
-                                    t.n_pos, t.rot, PyObject_IsTrue(a[9]), t.positions, x.n, y.p, y.ld, y.type,
+                                    t.n_pos, t.rot, bool_of(a[9]), t.positions, x.n, y.p, y.ld, y.type,
                                     stream_of(a[11]));
     return done(status, given ? a[10] : nullptr, made);
     END_HANDLE_TH_ERRORS
@@ -209,7 +216,7 @@ PyObject *kv_append_q4(PyObject *, PyObject *const *a, Py_ssize_t n)
     const int status = qk_kv_append_q4(&c, q.p, q.ld, heads, k.p, k.ld, v.p, v.ld, k.type,
                                        vector_of<const float>(a[7], D, at::kFloat, "q_weight", dev),
                                        vector_of<const float>(a[8], D, at::kFloat, "k_weight", dev), float_of(a[9]), t.p,
-                                       t.n_pos, t.rot, PyObject_IsTrue(a[10]), t.positions, slots, k.n, qo.p, qo.ld,
+                                       t.n_pos, t.rot, bool_of(a[10]), t.positions, slots, k.n, qo.p, qo.ld,
                                        qo.type, stream_of(a[12]));
     return done(status, given ? a[11] : (has_q ? nullptr : Py_None), made);
     END_HANDLE_TH_ERRORS
@@ -308,7 +315,7 @@ PyObject *moe_route(PyObject *, PyObject *const *a, Py_ssize_t n)
     float *wp = pairs_of<float>(weights, l.n, k, at::kFloat, "weights");
     const int status = qk_moe_route(l.p, l.ld, l.type, l.n, static_cast<int>(E), k, int32_of(a[2], "score"),
                                     vector_of<const float>(a[3], E, at::kFloat, "bias", dev), int32_of(a[4], "n_groups"),
-                                    int32_of(a[5], "top_groups"), int32_of(a[6], "group_top"), PyObject_IsTrue(a[7]),
+                                    int32_of(a[5], "top_groups"), int32_of(a[6], "group_top"), bool_of(a[7]),
                                     float_of(a[8]), ip, wp, stream_of(a[11]));
     if (status != QK_OK) return PyLong_FromLong(status);
     PyObject *pair = PyTuple_New(2);

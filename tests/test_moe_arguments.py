@@ -1,8 +1,29 @@
-"""Arguments of routing, experts and adapters that the binding has to refuse or take as they are meant."""
+"""Arguments that the binding has to refuse or take as they are meant."""
 import pytest
 import torch
 
 pytestmark = pytest.mark.gpu
+
+
+def test_renorm_without_a_truth_value(qk):
+    """An error in asking for it is raised as it is, before anything is launched."""
+    z = torch.randn(3, 16).cuda()
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        qk.moe_route(z, 2, renorm=torch.tensor([1, 2]))
+    ids, w = qk.moe_route(z, 2, renorm=torch.tensor([0]))
+    assert torch.equal(w, qk.moe_route(z, 2, renorm=False)[1]) and qk.device_error() == 0
+
+
+def test_interleaved_without_a_truth_value(qk):
+    """The same of the rotation's order of pairs."""
+    x, pos, slots = torch.randn(2, 64).cuda(), torch.zeros(2, dtype=torch.int32).cuda(), torch.arange(2).cuda()
+    table, cache = qk.rope_table(4, 64), qk.kv_cache_q4(1, 1, 16, 64)
+    was = cache.clone()
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        qk.norm_rope(x, 1, 0, 64, pos, table, interleaved=torch.tensor([0, 1]))
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        qk.kv_append_q4(cache, None, x, x, pos, slots, table, interleaved=torch.tensor([0, 1]))
+    assert torch.equal(cache, was) and qk.device_error() == 0
 
 
 def test_one_row_in_place(qk):
