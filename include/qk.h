@@ -576,7 +576,8 @@ size_t qk_moe_ffn_workspace_bytes(int64_t T, int top_k, int64_t n_experts, int64
  *               than one row) and must not overlap x.
  * Tokens of one adapter may lie anywhere; neighbouring ones share its reads.
  * Both products are fp32 sums of operands that are exact in 16 bits and held
- * to 22 bits in fp32 (and A x, in between).
+ * to 22 bits in fp32.  So is A x in between, but to 2^-17 of itself with bf16
+ * adapters and outputs.
  *   workspace   NULL, or device scratch, 256-byte aligned, whose contents need
  *               not be kept or set; calls that may overlap need one each.
  *               With qk_lora_workspace_bytes() of it, calls of many tokens,

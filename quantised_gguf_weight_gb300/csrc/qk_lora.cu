@@ -400,7 +400,9 @@ cudaError_t launch_as(const LoraArgs &a, cudaStream_t st)
 // Where x and the adapters have one 16-bit type the products are m16n8k16 in it,
 // operands as they lie in memory; else the first launch's are tf32, as above.
 // In the second 16-bit adapters meet V as two fp16 pieces below its row's
-// largest, or two bf16 ones (three for fp32 outputs), fp32 ones as tf32.
+// largest, or three bf16 ones, fp32 ones as two of tf32: 22 bits or more.  Beside
+// bf16 outputs bf16 adapters meet two, 2^-17 of V, eight bits below the outputs'
+// own rounding (with three, 4096 tokens of rank 64 take 61 us in a graph for 55).
 //
 // The kernels here load straight into the products' registers and take any
 // alignment; the ones with rings further down do the same products in the same
@@ -1240,7 +1242,10 @@ cudaError_t launch_tall_types(const LoraArgs &a, int sms, cudaStream_t st)
 {
     // 16-bit adapters: the same products in the same order by rings or through registers, so that bits depend on no alignment
     if (a.w_type == QK_F16) return a.y_type == QK_F32 ? launch_w16<NR, kF16, 2, true>(a, sms, st) : launch_w16<NR, kF16, 2, false>(a, sms, st);
-    if (a.w_type == QK_BF16) return a.y_type == QK_F32 ? launch_w16<NR, kBf16, 3, true>(a, sms, st) : launch_w16<NR, kBf16, 2, false>(a, sms, st);
+    if (a.w_type == QK_BF16)
+        return a.y_type == QK_F32   ? launch_w16<NR, kBf16, 3, true>(a, sms, st)
+               : a.y_type == QK_F16 ? launch_w16<NR, kBf16, 3, false>(a, sms, st)
+                                    : launch_w16<NR, kBf16, 2, false>(a, sms, st);
     return a.x_type == QK_F32 ? launch_tall_as<NR, kTf32, kTf32, 2, true, true>(a, sms, st) : launch_tall_as<NR, kTf32, kTf32, 2, false, true>(a, sms, st);
 }
 
