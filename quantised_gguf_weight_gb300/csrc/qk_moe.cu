@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a)
             for (int i = 0; i < (tiled ? tile_n : 0); ++i) a.plan.tile_sets[at.w + i] = {e, at.x + i * per, min(per, n - i * per), 0};
         }
     }
-    if (e == 0 && rank == 0) a.plan.head[0] = all.z, a.plan.head[1] = all.y, a.plan.head[2] = all.x, a.plan.head[3] = all.w;
+    if (e == 0 && rank == 0) a.plan.head[0] = all.z, a.plan.head[1] = all.w, a.plan.head[2] = all.x;
     __syncthreads();
     over_run([&](int64_t i, int id, bool live, unsigned same) {
         const int taken = live ? mine[id] : 0;
@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a)
             const int k = taken + __popc(same & ((1u << lane) - 1));       // its number among this block's of the expert
             if (lane == __ffs(same) - 1) mine[id] = taken + __popc(same);
             const int p = place_of[id] + k;
-            a.plan.assignment[p] = static_cast<int>(i), a.plan.place[i] = p;
+            a.plan.place[i] = p;
             a.plan.column[p] = octet_of[id] < 0 ? -1 : octet_of[id] + k;
         } else if (i < last) {
             a.plan.place[i] = id < 0 ? -1 : -2;
@@ -365,7 +365,7 @@ struct Layout {
     int pieces, w_pieces, tile_tokens;
     bool few;                 // few assignments: only h is used
     bool tiled;               // some expert may have enough tokens for the tile form
-    int64_t head, assignment, place, column, set, tile_set, x_scale, h_scale, x, x_tile, h, h_ops, h_tile, parts, bytes;
+    int64_t head, place, column, set, tile_set, x_scale, h_scale, x, x_tile, h, h_ops, h_tile, parts, bytes;
 };
 int64_t tile_cols(int64_t cols) { return (cols + 127) / 128 * 128; }
 
@@ -400,10 +400,9 @@ Layout layout_of(int64_t T, int top_k, int64_t E, int64_t K, int64_t F, int64_t 
         return was;
     };
     const auto operands = [&](int fmt, int64_t cols) {
-        // a set's missing octets are read, too
-        return (l.octets + kSetOctets - 1) * ((cols + kUnit - 1) / kUnit) * octet_unit_bytes(fmt, l.pieces);
+        return l.octets * ((cols + kUnit - 1) / kUnit) * octet_unit_bytes(fmt, l.pieces);
     };
-    l.head = take(64), l.assignment = take(4 * l.A), l.place = take(4 * l.A), l.column = take(4 * l.A);
+    l.head = take(64), l.place = take(4 * l.A), l.column = take(4 * l.A);
     l.set = take(l.sets * sizeof(ExpertSet)), l.tile_set = take(l.tile_sets * sizeof(ExpertSet));
     const auto rows = [&](int64_t cols) { return l.tiled ? 2 * l.pieces * l.A * tile_cols(cols) : 0; };
     l.x_scale = take(4 * l.A), l.h_scale = take(4 * l.A);
@@ -516,8 +515,7 @@ int qk_moe_ffn(const qk_expert_weights *gate, const qk_expert_weights *up, const
     constexpr int kWarps = kPlanThreads / 32;
     const int plan_blocks = l.A > 32 * kWarps ? 8 : 1;
     pa.per_warp = static_cast<int>((l.A + 32LL * kWarps * plan_blocks - 1) / (32LL * kWarps * plan_blocks) * 32);
-    pa.plan = {reinterpret_cast<int *>(ws + l.head), reinterpret_cast<int *>(ws + l.assignment),
-               reinterpret_cast<int *>(ws + l.place), reinterpret_cast<int *>(ws + l.column),
+    pa.plan = {reinterpret_cast<int *>(ws + l.head), reinterpret_cast<int *>(ws + l.place), reinterpret_cast<int *>(ws + l.column),
                reinterpret_cast<ExpertSet *>(ws + l.set), reinterpret_cast<ExpertSet *>(ws + l.tile_set)};
     pa.tile_from = l.tiled ? kTileFrom : INT32_MAX, pa.tile_tokens = l.tile_tokens;
     const size_t counts = sizeof(int) * kWarps * pa.experts;
@@ -558,7 +556,7 @@ int qk_moe_ffn(const qk_expert_weights *gate, const qk_expert_weights *up, const
             const int64_t wide = tile_cols(cols);
             const TileOperands o = {ws + tile_ops, ws + tile_ops + 2 * l.A * wide, l.A, wide};
             TileArgs t{};
-            t.plan = pa.plan, t.a = a, t.b = b, t.fmt = fmt, t.cols = static_cast<int>(cols), t.chunks = static_cast<int>(wide / (l.w_pieces == 1 ? 128 : 64));
+            t.plan = pa.plan, t.a = a, t.b = b, t.cols = static_cast<int>(cols), t.chunks = static_cast<int>(wide / (l.w_pieces == 1 ? 128 : 64));
             t.pieces = l.pieces, t.w_pieces = l.w_pieces, t.rows = static_cast<int>(rows);
             t.tiles = static_cast<int>(paired ? (rows + 63) / 64 : (rows + 127) / 128);
             t.scale = reinterpret_cast<const float *>(ws + scale), t.out = reinterpret_cast<float *>(ws + to);
@@ -567,7 +565,7 @@ int qk_moe_ffn(const qk_expert_weights *gate, const qk_expert_weights *up, const
             if (e != cudaSuccess) return e;
         }
         RowsArgs r{};
-        r.plan = pa.plan, r.a = a, r.b = b, r.fmt = fmt;
+        r.plan = pa.plan, r.a = a, r.b = b;
         r.cols = static_cast<int>(cols), r.units = static_cast<int>((cols + kUnit - 1) / kUnit), r.pieces = l.pieces;
         r.rows = static_cast<int>(rows), r.tiles = static_cast<int>(paired ? (rows + 7) / 8 : (rows + 15) / 16);
         r.sms = sms, r.wait_ns = library_wait_limit_ns(), r.err = err;

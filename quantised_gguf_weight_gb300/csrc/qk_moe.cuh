@@ -43,8 +43,7 @@ struct ExpertSet {
 };
 
 struct Plan {
-    int *head;                // [0] sets, [1] octets, [2] live places, [3] tile sets
-    int *assignment;          // [A] assignment at a place
+    int *head;                // [0] sets, [1] tile sets, [2] live places
     int *place;               // [A] place of an assignment; -1 none, -2 an id out of range
     int *column;              // [A] octet * 8 + column of a place; -1: of a tile set
     ExpertSet *sets;
@@ -76,7 +75,7 @@ struct PackArgs {
 struct RowsArgs {
     Plan plan;
     Weights a, b;             // gate and up; or down twice
-    int fmt, cols, units, pieces;
+    int cols, units, pieces;
     int rows, tiles;          // output columns and 16-row tiles (8 + 8 where gate and up are paired)
     int sms;
     const uint8_t *x;         // operands, octet after octet
@@ -89,7 +88,7 @@ struct RowsArgs {
 struct TileArgs {
     Plan plan;
     Weights a, b;             // as above
-    int fmt, cols, chunks, pieces, w_pieces;      // chunks: stages of a row
+    int cols, chunks, pieces, w_pieces;      // chunks: stages of a row
     int rows, tiles;          // output columns and 128-row tiles (64 + 64 where paired)
     const float *scale;
     float *out;

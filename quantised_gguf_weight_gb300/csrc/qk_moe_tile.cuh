@@ -389,7 +389,7 @@ tile_kernel(const __grid_constant__ TileMaps maps, const TileArgs a)
     wait_for_previous();
 
     const int pairs = (a.tiles + 1) / 2;
-    const int items = a.plan.head[3] * pairs, first = blockIdx.x >> 1, step = gridDim.x >> 1;      // (the caller sees to 31 bits)
+    const int items = a.plan.head[1] * pairs, first = blockIdx.x >> 1, step = gridDim.x >> 1;      // (the caller sees to 31 bits)
     const int nk = a.chunks;
     const int per = PB == 2 ? kFlush : nk;                     // stages an accumulator takes
     const auto set_of = [&](int item) { return a.plan.tile_sets[item / pairs]; };
