@@ -533,24 +533,28 @@ typedef struct {
  *   y[t] = sum_{j < top_k} weights[t][j] * down_e h,
  *   h = silu(gate_e x[t]) * (up_e x[t]),   e = ids[t][j],
  * gate and up [F][K] (one format), down [N][F].  An expert's weights are
- * read once for up to 128 of its tokens (16 of them where it has fewer than
- * 16; for each where a call has 24 assignments or fewer).  ids may be in any
- * order and repeat; a
- * negative id adds nothing (a token with none left gets 0).  An id past the
- * last makes the token's row NaN and qk_device_error() reports
- * QK_ERR_BAD_INDEX.
+ * read once for up to 128 of its tokens, or for 16 where the batch has few such
+ * experts; for each of its tokens where a call has 24 assignments or fewer and
+ * K and F are 8192 at most.  ids may be in any order and repeat; a negative id
+ * adds nothing (a token with none left gets 0).  An id past the last makes the
+ * token's row NaN and qk_device_error() reports QK_ERR_BAD_INDEX.
  *   x, y        device rows of K and N elements of x_type / y_type, ldx / ldy
  *               apart (0: packed), aligned to their element.
  *   ids, weights  device int32 and fp32 [T][top_k].
  *   workspace   device scratch, 256-byte aligned, of at least
  *               qk_moe_ffn_workspace_bytes() bytes; its contents need not be
  *               kept or set.  Calls that may overlap need one each.
- * Accuracy: with fp32 x or y every activation (x, and h) is held to 2^-22 of
- * itself or 2^-39 of its row's largest; else to 2^-11 or 2^-28 (fp16's, so
- * bf16 values are exact above that).  Weights are exact, or held to 2^-21
- * where an expert has 16 tokens or more; with bf16 x and y they are then
- * rounded to fp16, by 2^-11 of them and of what they are made of (scale times
- * quant, and minimum).  Sums are fp32.
+ * Accuracy: sums are fp32.  Activations (x, and h) are held to 2^-22 of
+ * themselves or 2^-39 of their row's largest with fp32 x or y; else to 2^-11 or
+ * 2^-39 (one fp16 below a power of two of the row's own, so bf16 values are
+ * exact above 2^-28 of it); in calls of up to 24 assignments (as above) in fp32,
+ * whatever the types, to 2^-138.  Weights are exact in calls of fewer than 16
+ * tokens.  In others those of an expert with 16 tokens or more, and of any other
+ * where the counts of the whole batch make it cheaper, are held to 2^-22 of
+ * themselves and 2^-24 of what they are made of (scale times quant, and
+ * minimum), or 2^-29 of the largest that their row's scales allow; with bf16 x
+ * and y to 2^-11 of themselves and of what they are made of, or that 2^-29.  A
+ * token's low bits can so differ with the batch it is in.
  * A NaN or an infinity in a row of x makes that token's y not finite, and no other's.
  * n_experts <= 1024; K, F, N <= 2^24; T * top_k <= 2^28.  T == 0 does nothing.
  */
