@@ -572,12 +572,18 @@ def moe_ffn(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, gate: Exp
         y, workspace, None if stream is None else _stream(stream)), "qk_moe_ffn")
 
 
+def lora_workspace(T: int, rank: int, device=None) -> torch.Tensor:
+    """Scratch for lora calls of up to T tokens and ranks (one for each stream that calls)."""
+    n = load().qk_lora_workspace_bytes(T, rank)
+    return torch.empty(max(256, n), dtype=torch.uint8, device=device or "cuda")
+
+
 def lora(x: torch.Tensor, y: torch.Tensor, A: torch.Tensor, B: torch.Tensor, ids: torch.Tensor,
          scales: torch.Tensor | None = None, out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
          stream=None) -> torch.Tensor:
     """y[t] + scales[a] * B[a] (A[a] x[t]), a = ids[t] (int32; negative: y[t]), for rows x [T][K], y [T][N] and adapters
-    A [adapters][rank][K], B [adapters][N][rank] of one type.  out may be y.  `workspace` (uint8, of
-    qk_lora_workspace_bytes) is allocated here through torch when not given."""
+    A [adapters][rank][K], B [adapters][N][rank] of one type.  out may be y.  `workspace`
+    (lora_workspace) is allocated here through torch when not given."""
     return _result((_ext or _binding()).lora(x, y, A, B, ids, scales, out, workspace,
                                              None if stream is None else _stream(stream)), "qk_lora")
 

@@ -34,3 +34,15 @@ def test_one_row_in_place(qk):
     y, behind = buf[:1, :48].clone(), buf[1:].clone()
     qk.lora(x, buf[:1, :48], A, B, ids, out=buf[:, :48])
     assert torch.equal(buf[:1, :48], qk.lora(x, y, A, B, ids)) and torch.equal(buf[1:], behind)
+
+
+def test_adapters_with_a_workspace_of_ones_own(qk):
+    """A buffer for more, and with anything in it, gives the bits that one made by the call gives."""
+    for T, rank, dtype in ((1, 64, torch.float16), (40, 16, torch.bfloat16), (300, 100, torch.float32)):
+        x, y = torch.randn(T, 96).to(dtype).cuda(), torch.randn(T, 40).to(dtype).cuda()
+        A, B = torch.randn(3, rank, 96).to(dtype).cuda(), torch.randn(3, 40, rank).to(dtype).cuda()
+        ids = (torch.arange(T) % 4 - 1).int().cuda()
+        ws = qk.lora_workspace(2 * T, rank)
+        ws.fill_(0xff)
+        assert torch.equal(qk.lora(x, y, A, B, ids, workspace=ws), qk.lora(x, y, A, B, ids))
+    assert qk.device_error() == 0

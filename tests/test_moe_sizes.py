@@ -33,3 +33,11 @@ def test_one_row_in_place_has_no_stride(qk):
                        ldy=0, out=FAKE, ldo=80, y_type=0, ws=None, bytes=0, stream=None))
     assert call() == 1 and call(ldo=0) == 1           # only the ids are missing
     assert call(T=2) == 2 and call(ldo=63) == 2
+
+
+def test_adapters_workspace(qk):
+    """A buffer for some tokens and ranks serves fewer of either."""
+    sizes = [[qk.lora_workspace(T, r, "cpu").numel() for r in range(1, 257)] for T in (1, 2, 15, 16, 300, 4096)]
+    assert all(a <= b for row in sizes for a, b in zip(row, row[1:]))
+    assert all(a <= b for m, n in zip(sizes, sizes[1:]) for a, b in zip(m, n))
+    assert sizes[5][63] == 4096 * 64 * 4 and qk.lora_workspace(0, 8, "cpu").numel() == 256
