@@ -42,11 +42,15 @@ def far_apart(c, name, fmt, rows, up):
 @pytest.mark.parametrize("fmt,up", [("q8_0", 14), ("q4_k", 12), ("q6_k", 12)])
 @pytest.mark.parametrize("T,k,E", [(2, 1, 2), (14, 3, 3), (48, 1, 2)])
 @pytest.mark.parametrize("xt", ["f32", "f16", "bf16"])
-def test_blocks_far_apart(qk, fmt, up, T, k, E, xt):
-    """No token has anything in the columns of the large blocks: the small ones are all of gate and up."""
+@pytest.mark.parametrize("one", [False, True])
+def test_blocks_far_apart(qk, fmt, up, T, k, E, xt, one):
+    """No token has anything in the columns of the large blocks: the small ones are all of gate and up.  one: each token has
+    one column, so that gate and up are single weights and the bound all but theirs."""
     c = Case(qk, T, E, k, 512, 40, 64, fmt, "q8_0", xt, seed=T)
     ids = np.stack([np.arange(k) + (0 if k == E else t % (E - k + 1)) for t in range(T)]).astype(np.int32)
     c.ids, c.xv = ids, c.xv * (np.arange(512) >= 256)
+    if one:
+        c.xv *= np.arange(512) == 256 + 5 * np.arange(T)[:, None]
     c.x = torch.from_numpy(c.xv).to(mo.TORCH[xt])
     dw = [far_apart(c, n, fmt, 40, up) for n in ("gate", "up")]
     y = c.call()
