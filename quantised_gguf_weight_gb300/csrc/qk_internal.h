@@ -1,9 +1,11 @@
 // qk_internal.h -- declarations shared by the library's translation units.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <mutex>
 
 #include "../../include/qk.h"
 
@@ -56,6 +58,31 @@ EncodeTiledFn encode_fn();
 }  // namespace gemm
 // SM count and shared memory per block (opt-in) of the current device.
 bool device_limits(int *sms, int *smem_optin);
+
+// The dynamic shared memory that one kernel may have, for each device: raised where a launch needs more and never lowered, so
+// that host threads may launch the kernel with different sizes at once.
+class SharedGrant {
+public:
+    template <class Kern>
+    cudaError_t at_least(Kern kern, int smem)
+    {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        if (dev < 0 || dev >= kDevices) return cudaErrorInvalidDevice;
+        if (granted_[dev].load(std::memory_order_acquire) >= smem) return cudaSuccess;
+        const std::lock_guard<std::mutex> lock(raise_);
+        if (granted_[dev].load(std::memory_order_relaxed) >= smem) return cudaSuccess;
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e == cudaSuccess) granted_[dev].store(smem, std::memory_order_release);
+        return e;
+    }
+
+private:
+    static constexpr int kDevices = 64;
+    std::atomic<int> granted_[kDevices]{};
+    std::mutex raise_;
+};
 
 // The device error word of the current device and the bound of device waits.
 int *library_error_word();

@@ -375,7 +375,8 @@ cudaError_t launch_as(const LoraArgs &a, cudaStream_t st)
     const int width = (a.rank + R8 - 1) / R8 * R8;
     const size_t smem = sizeof(float) * (kWarps * ROWS * R8 + ROWS * width + ROWS * (width + 4));
     const auto kern = lora_kernel<MT, NR, XW, WW>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    static SharedGrant granted;                              // (the size goes with the rank)
+    cudaError_t e = granted.at_least(kern, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     const int64_t tiles = (a.T + ROWS - 1) / ROWS;
     cudaLaunchConfig_t cfg{};
