@@ -1561,16 +1561,9 @@ template <int FMT, int B, bool WIDE = false, int MODE = kModeAny>
 cudaError_t gemv_launch_one(const GemvArgs &a, int grid, int smem, cudaStream_t st, bool pdl)
 {
     auto kern = gemv_kernel<FMT, B, WIDE, MODE>;
-    static int granted[64];
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    static SharedGrant granted;
+    cudaError_t e = granted.at_least(kern, smem);
     if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (__atomic_load_n(&granted[dev], __ATOMIC_ACQUIRE) < smem) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return e;
-        __atomic_store_n(&granted[dev], smem, __ATOMIC_RELEASE);
-    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(32 * (gemv_warps(FMT, B, WIDE) + 1));

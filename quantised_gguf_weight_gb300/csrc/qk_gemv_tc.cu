@@ -823,16 +823,9 @@ cudaError_t gemv_tc_launch_ks(const CUtensorMap &tm0, const CUtensorMap &tm1, co
                               int smem, cudaStream_t st, bool pdl)
 {
     auto kern = gemv_tc_kernel<FMT, B, KS>;
-    static int granted[64];
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    static SharedGrant granted;
+    cudaError_t e = granted.at_least(kern, smem);
     if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (__atomic_load_n(&granted[dev], __ATOMIC_ACQUIRE) < smem) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return e;
-        __atomic_store_n(&granted[dev], smem, __ATOMIC_RELEASE);
-    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(kTcThreads);
