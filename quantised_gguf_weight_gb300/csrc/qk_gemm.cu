@@ -749,17 +749,14 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t
 
 EncodeTiledFn encode_fn()
 {
-    static EncodeTiledFn fn = nullptr;
-    static bool tried = false;
-    if (!tried) {
-        tried = true;
+    // (threads that come while the first looks it up wait for it)
+    static const EncodeTiledFn fn = [] {
         void *p = nullptr;
         cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
-    }
+        const bool found = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+                           q == cudaDriverEntryPointSuccess;
+        return found ? reinterpret_cast<EncodeTiledFn>(p) : nullptr;
+    }();
     return fn;
 }
 
@@ -777,15 +774,9 @@ cudaError_t launch_mode(const CUtensorMap &tm_x, const CUtensorMap &tm_w, const 
 {
     using namespace gemm;
     constexpr int smem = Shape<FMT, MODE>::smem;
-    static int granted[64];
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    static SharedGrant granted;
+    cudaError_t e = granted.at_least(gemm_q4k_kernel<FMT, MODE>, smem);
     if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < 64 && granted[dev] == 0) {
-        e = cudaFuncSetAttribute(gemm_q4k_kernel<FMT, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return e;
-        granted[dev] = 1;
-    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
     cfg.blockDim = dim3(kThreads);
