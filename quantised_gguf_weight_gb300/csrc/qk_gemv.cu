@@ -19,16 +19,19 @@ struct DevInfo {
 
 DevInfo dev_info()
 {
-    static DevInfo cache[64];
+    // (the SM count is stored last: a thread that finds it finds the rest)
+    static std::atomic<int> sms[64], smem_optin[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return DevInfo{};
-    DevInfo &di = cache[dev];
+    DevInfo di;
+    di.sms = sms[dev].load(std::memory_order_acquire);
     if (di.sms == 0) {
-        int sms = 0, smem = 0;
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-        cudaDeviceGetAttribute(&smem, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
-        di.smem_optin = smem;
-        di.sms = sms;
+        cudaDeviceGetAttribute(&di.sms, cudaDevAttrMultiProcessorCount, dev);
+        cudaDeviceGetAttribute(&di.smem_optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+        smem_optin[dev].store(di.smem_optin, std::memory_order_relaxed);
+        sms[dev].store(di.sms, std::memory_order_release);
+    } else {
+        di.smem_optin = smem_optin[dev].load(std::memory_order_relaxed);
     }
     return di;
 }
