@@ -539,7 +539,9 @@ typedef struct {
  * adds nothing (a token with none left gets 0).  An id past the last makes the
  * token's row NaN and qk_device_error() reports QK_ERR_BAD_INDEX.
  *   x, y        device rows of K and N elements of x_type / y_type, ldx / ldy
- *               apart (0: packed), aligned to their element.
+ *               apart (0: packed), aligned to their element.  y may overlap x,
+ *               whose rows are all read before one of y is written, and nothing
+ *               else.
  *   ids, weights  device int32 and fp32 [T][top_k].
  *   workspace   device scratch, 256-byte aligned, of at least
  *               qk_moe_ffn_workspace_bytes() bytes; its contents need not be

@@ -46,3 +46,20 @@ def test_adapters_with_a_workspace_of_ones_own(qk):
         ws.fill_(0xff)
         assert torch.equal(qk.lora(x, y, A, B, ids, workspace=ws), qk.lora(x, y, A, B, ids))
     assert qk.device_error() == 0
+
+
+@pytest.mark.parametrize("T", [1, 12, 40, 300])
+def test_experts_in_place(qk, T):
+    """y is x, or rows that lie across x's, in calls of every form."""
+    from tests.test_moe_ffn import Case, bits
+    for xt in ("f32", "bf16"):
+        c = Case(qk, T, 9, 3, 256, 64, 256, "q4_k", "q8_0", xt, seed=T)
+        want = c.call()
+        x = c.x.cuda()
+        assert c.call(x=x, y=x).data_ptr() == x.data_ptr() and torch.equal(bits(x), bits(want))
+        buf = torch.zeros(T + 1, 256, dtype=c.x.dtype, device="cuda")
+        buf[:T] = c.x.cuda()
+        y = buf.reshape(-1)[128:128 + T * 256].reshape(T, 256)
+        c.call(x=buf[:T], y=y)
+        assert torch.equal(bits(y), bits(want))
+    assert qk.device_error() == 0
