@@ -9,9 +9,10 @@
 // them (below); two_launches() says which calls take which.
 //
 // Few tokens are bound by latency: one token beside 4096 x 6144, rank 16, 8.2 us
-// (12.3 before clusters shared its columns), 64 of 48 adapters 22.5 (8 MB of adapters, 2.3 us at the memory's rate; of the
-// 512 blocks 304 are resident at once.  Clusters of 4, which all would be, took
-// 20.5, but 255 tokens of 4 adapters 58 us for 24).
+// (6.3 in a graph; 12.3 before clusters shared its columns), 64 of 48 adapters
+// 22.6 (8 MB of adapters, 2.3 us at the memory's rate; of the 512 blocks 304 are
+// resident at once.  Clusters of 4, which all would be, took 20.5 for 22.5, but
+// 255 tokens of 4 adapters 58 us for 24).
 //
 // The products are m16n8k8 in tf32, which holds 16-bit adapters and activations
 // exactly; fp32 operands, and V, are two tf32 pieces (22 bits).  A lane's values
@@ -409,8 +410,9 @@ cudaError_t launch_as(const LoraArgs &a, cudaStream_t st)
 // alignment; the ones with rings further down do the same products in the same
 // order.  4096 bf16 tokens of 7 requests beside 4096 x 6144, rank 64: 24 and 36
 // us, 57 together, for 140 MB (21 us at the memory's rate; the tensor cores are
-// 16% and 31% busy).  A turn's copies are what both wait for: a block has 8 warps
-// at two turns of 6 KB each.
+// 16% and 31% busy).  Every 32 tokens read A and B again, 167 MB more from L2, and
+// the first launch is one round of 128 working blocks, whose start and whose sum
+// over eight warps overlap with nothing.
 
 constexpr int kTallRows = 32, kShrinkRows = 16;            // tokens of a block of the second, and of the first launch
 
@@ -1185,7 +1187,9 @@ bool ring_ok(const LoraArgs &a)
 // A tile's adapters are shared out over blocks, at least two: with one, a tile at the border of two requests takes twice
 // as long as the others, and the launch with it (4096 tokens of 7 requests: 35 and 55 us).  But a block that finds no
 // adapter for itself costs its start, so that the launch's blocks are two rounds of the GPU at most (493 tokens of 34
-// requests, rank 64: 39 us, 52 with all 32 that a tile's tokens can have).
+// requests, rank 64: 39 us, 52 with all 32 that a tile's tokens can have).  Many tokens whose neighbours differ pay for it:
+// each adapter of a tile is a pass of a block (4096 tokens of 7 requests one after another 57 us, alternating over 8 adapters
+// 329, over 64 1207).
 unsigned share_of(const LoraArgs &a, unsigned blocks, int sms)
 {
     return std::min(static_cast<unsigned>(std::min<int64_t>(kTallRows, a.n_adapters)), std::max(2u, 2u * sms / blocks));
@@ -1288,10 +1292,12 @@ int size_of(int t) { return t == QK_F32 ? 4 : 2; }
 using namespace qk;
 
 namespace {
-// Which calls with a workspace take the two-launch form.  K = N = 4096, bf16 and rank 16: one token 16.5 us, 15.5 in one
-// launch; 23 of 23 adapters 19.6 and 21.7; 64 of 48 22.7 and 34; rank 64, one token 23.7 and 25.8.  With fp32 activations
-// of rank 16 64 tokens take 37.0 and 34, but of rank 64 58.5 and 123 (of 4 adapters 45 and 33).  Adapters in fp32 and
-// ranks past one pass: many tokens only.
+// Which calls with a workspace take the two-launch form.  K = N = 4096, bf16 adapters, calls one after another in a graph (what
+// they read is in L2), two launches and one.  bf16 activations of rank 16: one token 7.8 us and 6.3, 23 of 23 adapters 9.8 and
+// 10.5, 64 of 48 13.0 and 20.6 (of 4 11.1 and 9.4); rank 64: one token 17.0 and 11.8, 23 22.1 and 32.4, 64 30.7 and 79.8.  fp32
+// activations of rank 16: 64 of 48 25.4 and 20.6; of rank 64 52.9 and 81.2 (of 4 38.1 and 18.3).  Which adapters a call has is
+// not known here; with caches emptied between calls one token of rank 64 took 23.7 and 25.8.  Adapters in fp32 and ranks past
+// one pass: many tokens only.
 bool two_launches(int64_t T, int rank, int x_type, int w_type)
 {
     if (T >= 256) return true;

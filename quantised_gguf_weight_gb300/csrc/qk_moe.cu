@@ -115,8 +115,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a)
             }
         }
     }
-    // Which form takes which experts.  Those of 16 tokens or more suit the many-token form (a launch of 512 tokens of 8
-    // of 128 experts takes 323 us; from 48 tokens 442, from 8 339).  But where they would add few sets to those of the
+    // Which form takes which experts.  Those of 16 tokens or more suit the many-token form (512 tokens of 8 of 128 experts
+    // take 291 us in a graph, as from 8 tokens; from 48 349).  But where they would add few sets to those of the
     // few-token form it takes them, too, and where that one would have few of its own the other takes all: a launch that
     // does not fill the GPU costs more than they do (64 tokens: 27 + 15 us for seven experts).
     constexpr int kRowTokens = 8 * kSetOctets;

@@ -30,8 +30,8 @@ constexpr int kSetOctets = 2;
 constexpr int kTileBoxRows = 32;                  // rows of a TMA box of a tile set's operands
 constexpr int kRowWarps = 16;                     // warps of a thread block of the few-token products
 // Assignments up to which no plan is made (qk_moe_few.cuh), which reads an expert again for each of its tokens.  8 of
-// 128 experts of 768 x 2048, Q4_K and Q6_K: one token 30 us, with the plan 50; three 63 and 68; four 76 and 72; where 8
-// experts have all tokens three take 52 and 50.
+// 128 experts of 768 x 2048, Q4_K and Q6_K, calls one after another in a graph: one token 19.3 us, with the plan 38.2; three
+// 50.2 and 59.6; four 63.6 and 66.9, five 82.2 and 68.4; where 8 experts have all tokens three take 48.6 and 40.1.
 constexpr int kMaxFew = 24;
 constexpr int kMaxFewCols = 8192;                 // a row of x has to fit into shared memory
 constexpr int kUnit = 256;                        // columns of a unit of the products' loops

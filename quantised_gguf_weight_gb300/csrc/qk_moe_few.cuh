@@ -18,9 +18,12 @@
 // With so few assignments a call is bound by the time from one dependent load to
 // the next and by its launches, so the second launch starts while the first runs
 // and fetches its first weights before it waits for h.  One token of 8 of 128
-// experts of 768 x 2048, Q4_K and Q6_K: 22.5 us (24 MB of weights, 3.6 us at the
-// memory's rate), where the plan and its launches took 45.  Rows of a warp: 2 and
-// 2 of gate and up, 4 of down (8 of down: 23.7 us, and 64 tokens 120 for 114).
+// experts of 768 x 2048, Q4_K and Q6_K, calls one after another in a graph: 19.3
+// us (24 MB of weights, 3.6 us at the memory's rate), where the plan and its
+// launches take 38.2.  What bounds the first launch besides: each of its 384
+// thread blocks lays out all of x for 32 rows, 37 KB of weights, and a lane has two
+// units of a row to overlap.  Rows of a warp: 2 and 2 of gate and up, 4 of down (8
+// of down: 1.2 us more a token).
 #pragma once
 
 #include "qk_moe.cuh"

@@ -10,16 +10,17 @@
 // that count as their best expert), the logits themselves are compared and the
 // order is exact.  Else scores are compared, first in 32 bits with a bound on
 // their error; a token in which that leaves two neighbours of the order, or a
-// group at the edge, undecided is done again in 64 bits (about 1 in 500 tokens
-// of 256 experts; a launch that has one takes 5 us longer).  So the choice is
-// that of the formulas, not of a rounding.
+// group at the edge, undecided is done again in 64 bits (about 1 in 2000 tokens
+// of 256 experts in groups; a launch that has one takes 14 us longer).  So the
+// choice is that of the formulas, not of a rounding.
 //
 // A weight is off by at most 18 x 2^-24 of itself: two exponentials 2^-23 each, their arguments' rests 2^-24 each, ten
 // additions, the division and the scale.
 //
-// Measured: one token 6.2 us, which is a launch; 512 tokens of 256 experts in
-// groups 8.2 or 13.0; 16384 tokens of 128 experts in bf16 12.7 us, bound by
-// instructions (0.65 a cycle and scheduler), 4.3 MB read.
+// Measured, calls one after another in a graph: one token 2.9 us, which is a
+// launch; 512 tokens of 256 experts in groups 6.6, or 20.7 where a token is done
+// again; 16384 tokens of 128 experts in bf16 11.4 us, bound by instructions (0.66
+// a cycle and scheduler), 4.3 MB read.
 #include <cmath>
 
 #include "qk_kv4.cuh"
