@@ -498,7 +498,7 @@ typedef enum { QK_SOFTMAX = 0, QK_SIGMOID = 1 } qk_score;
  * The choice is that of the exact formulas: neighbours that 32-bit scores
  * leave undecided are compared in 64 bits; without a bias (and with
  * group_top 1, where groups count) the logits are compared.  Weights are
- * within 1.1e-6 of themselves, or 2^-126 times scale.
+ * within 1.2e-6 of themselves, or 2^-126 times scale.
  * A logit of -infinity has score 0.  A token none of whose chosen experts has
  * a score gets weights of 0.  A token with a NaN among its logits or the
  * biases, or (softmax) a logit of +infinity, gets ids 0..top_k-1 and NaN

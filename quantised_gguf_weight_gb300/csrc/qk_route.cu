@@ -14,8 +14,9 @@
 // of 256 experts in groups; a launch that has one takes 14 us longer).  So the
 // choice is that of the formulas, not of a rounding.
 //
-// A weight is off by at most 18 x 2^-24 of itself: two exponentials 2^-23 each, their arguments' rests 2^-24 each, ten
-// additions, the division and the scale.
+// A weight is off by at most 19 x 2^-24 of itself: softmax over all experts, two exponentials 2^-23 each, their arguments'
+// rests 2^-24 each, ten additions, the division and the scale; sigmoid over its sum, six for each score, five additions, the
+// division and the scale.
 //
 // Measured, calls one after another in a graph: one token 2.9 us, which is a
 // launch; 512 tokens of 256 experts in groups 6.6, or 20.7 where a token is done
@@ -340,7 +341,8 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a)
         // weights from the chosen logits: divided by their sum they need no other, and cannot all underflow
         const float most = value_of(warp_max(key_of(mine ? logit : -INFINITY)));
         if (a.sigmoid) {
-            w = a.renorm && most < -30.0f ? exp_less(logit, most) : 1.0f / (1.0f + expf(-logit));
+            // below zero as e^z / (1 + e^z), which divided by their sum may all be times e^-most: none is lost that is left in it
+            w = logit < 0.0f ? exp_less(logit, a.renorm ? fminf(most, 0.0f) : 0.0f) / (1.0f + expf(logit)) : 1.0f / (1.0f + expf(-logit));
         } else if (a.renorm) {
             w = exp_less(logit, most);
         } else {

@@ -87,6 +87,10 @@ def test_experts_that_a_bias_masks(qk, score, low):
     check(qk, z, 8, score, bias)
     check(qk, z, 8, score, bias, 8, 3, 2)
     check(qk, z, 8, score, bias, 8, 3, 1)
+    few = bias[:12].copy()
+    few[::2] = low                                # and chosen all the same, where nothing else is left
+    check(qk, z[:, :12], 12, score, few)
+    check(qk, z[:, :12], 5, score, few, 6, 3, 2)
     bias[:16] = low                               # whole groups, too
     check(qk, z, 8, score, bias, 8, 5, 2)
 
@@ -113,3 +117,16 @@ def test_weights_of_logits_far_apart(qk, renorm, E):
     check(qk, z, 7, "softmax", renorm=renorm)
     check(qk, F(rng.uniform(-3, 3, (60, E))), 7, "softmax", renorm=renorm)
     check(qk, z - 60, 7, "sigmoid", renorm=True)
+
+
+@pytest.mark.gpu
+def test_small_sigmoids_beside_larger_ones(qk):
+    """Scores below 32 bits' range that are within it over their sum."""
+    rng = np.random.default_rng(6)
+    z = F(rng.uniform(-95, -84, (200, 8)))
+    z[:, 0] = F(rng.uniform(-28, -8, 200))
+    check(qk, z, 8, "sigmoid")
+    z[:, 1] = F(rng.uniform(-12, 12, 200))
+    check(qk, z, 8, "sigmoid")
+    check(qk, z, 8, "sigmoid", renorm=False)
+    check(qk, F(rng.uniform(-60, 60, (200, 8))), 8, "sigmoid")
