@@ -546,17 +546,18 @@ typedef struct {
  *   workspace   device scratch, 256-byte aligned, of at least
  *               qk_moe_ffn_workspace_bytes() bytes; its contents need not be
  *               kept or set.  Calls that may overlap need one each.
- * Accuracy: sums are fp32.  Activations (x, and h) are held to 2^-22 of
- * themselves or 2^-39 of their row's largest with fp32 x or y; else to 2^-11 or
- * 2^-39 (one fp16 below a power of two of the row's own, so bf16 values are
- * exact above 2^-28 of it); in calls of up to 24 assignments (as above) in fp32,
- * whatever the types, to 2^-138.  Weights are exact in calls of fewer than 16
- * tokens.  In others those of an expert with 16 tokens or more, and of any other
- * where the counts of the whole batch make it cheaper, are held to 2^-22 of
- * themselves and 2^-24 of what they are made of (scale times quant, and
- * minimum), or 2^-29 of the largest that their row's scales allow; with bf16 x
- * and y to 2^-11 of themselves and of what they are made of, or that 2^-29.  A
- * token's low bits can so differ with the batch it is in.
+ * Accuracy: sums are fp32 (Q4_K's two each, of scales times quants and of
+ * minima).  Activations (x, and h) are held to 2^-22 of themselves or 2^-39 of
+ * their row's largest with fp32 x or y; else to 2^-11 or 2^-39 (one fp16 below a
+ * power of two of the row's own, so bf16 values are exact above 2^-28 of it); in
+ * calls of up to 24 assignments (as above) in fp32, whatever the types, to
+ * 2^-138.  Weights are exact in calls of fewer than 16 tokens.  In others those
+ * of an expert with 16 tokens or more, and of any other where the counts of the
+ * whole batch make it cheaper, are held to 2^-22 of themselves and 2^-24 of what
+ * they are made of (scale times quant, and minimum), or 2^-29 of the largest that
+ * their row's scales allow; with bf16 x and y to 2^-11 of themselves and of what
+ * they are made of, or that 2^-29.  A token's low bits can so differ with the
+ * batch it is in.
  * A NaN or an infinity in a row of x makes that token's y not finite, and no other's.
  * n_experts <= 1024; K, F, N <= 2^24; T * top_k <= 2^28.  T == 0 does nothing.
  */
